@@ -77,6 +77,9 @@ typedef enum {
 #define VW4_DEV_BOUNDS         0x20u /* checks build only: an index that came from data was
                                         out of range (a library bug): a memory access it
                                         addressed was skipped; a token id is still written */
+#define VW4_DEV_BAD_PAGE       0x40u /* a cache page id outside [0, num_pages), or a length
+                                        beyond the block table: those tokens read as zero
+                                        keys and values, and are not written            */
 
 /* A block-quantized weight matrix [N][K] (see the format notes above). */
 typedef struct vw4_weight {
@@ -103,6 +106,7 @@ typedef struct vw4_sampling {
 #define VW4_OP_MOE        2
 #define VW4_OP_REJECTION  3
 #define VW4_OP_REJECTION_TOPK 4
+#define VW4_OP_ATTN       5
 
 /*
  * verify_gemm_w4 -- the verification pass's skinny matmul.
@@ -445,11 +449,188 @@ VW4_API vw4_status vw4_rejection_row_records(const void* workspace_dev, size_t w
                                              int Kd, int V, vw4_row_record* records_dev,
                                              void* stream);
 
+/* Cache types of vw4_kv_cache. */
+#define VW4_KV_BF16 1
+#define VW4_KV_E4M3 2
+
+/*
+ * A paged key-value cache.  Token j of sequence b lives in page
+ * block_table[b][j / page_size] at position j % page_size; element d of key
+ * head h is k[page * page_stride + (j % page_size) * token_stride +
+ * h * head_stride + d] (strides in elements, the same for K and V), so that
+ * both the token-major and the head-major page layouts, and pages that hold K
+ * and V next to each other, are described without a copy.
+ *
+ * dtype       VW4_KV_BF16, or VW4_KV_E4M3: an e4m3 byte times the head's scale.
+ * page_size   a power of two, 8..65536.
+ * D           64, 128 or 256; Hkv 1..256.
+ * max_blocks  columns of the block table that may be read; the cache length of
+ *             a sequence is at most max_blocks * page_size (<= 2^30).
+ * k_dev, v_dev  16-byte aligned; every stride a multiple of 16 bytes.
+ * block_table_dev  int32 [B][table_stride], table_stride >= max_blocks.
+ *             Entries beyond a sequence's length are not read.
+ * k_scale_dev, v_scale_dev  fp32 [Hkv], e4m3 only; NULL = 1.
+ */
+typedef struct vw4_kv_cache {
+    int32_t dtype, page_size, num_pages, Hkv, D, max_blocks;
+    int64_t page_stride, token_stride, head_stride, table_stride;
+    void* k_dev;
+    void* v_dev;
+    const int32_t* block_table_dev;
+    const float* k_scale_dev;
+    const float* v_scale_dev;
+} vw4_kv_cache;
+
+/*
+ * verify_rope_append -- the verify rows' queries, keys and values from the
+ * packed qkv GEMM to where the attention reads them.
+ *
+ * Defined by: "Faster Gemma 4 on MLX with multi-token prediction" (the verify
+ * pass runs the target model over the draft rows: its layers' queries, keys
+ * and values, with the cache extended by the rows); the formulas are the
+ * usual RMS norm and rotary embedding.
+ *
+ * Row b * R + i of x holds the query heads, then the key heads, then the value
+ * heads of the token at position pos = seq_lens[b] - R + i:
+ *   y = q_norm or k_norm given ? x / sqrt(mean(x^2) + eps) * norm : x
+ *   the first `rot` dimensions of a query or key head turn by the angle
+ *   pos * inv_freq[j] in the planes (j, j + rot/2), or (2j, 2j + 1) when
+ *   adjacent = 1:  (a, c) -> (a cos - c sin, c cos + a sin)
+ *   queries -> q_dev as bf16; keys and values -> the token's cache slot, as
+ *   bf16, or as e4m3 of value / scale (nearest, at most 448 in magnitude).
+ * The angle is computed in 64 bits and reduced before it is rounded.
+ *
+ * x_dev, ldx  fp32 (x_bf16 = 0) or bf16 (1) [B*R][ldx], ldx >= (Hq+2 Hkv) D.
+ * inv_freq_dev  fp64 [rot/2] (NULL when rot = 0); rot even, 0..D.
+ * q_norm_dev, k_norm_dev  fp32 [D] or NULL (no norm).
+ * q_dev, ldq  bf16 [B*R][ldq], ldq >= Hq D.
+ * seq_lens_dev  int32 [B]: tokens in the cache, these R rows included.  A row
+ *             at a negative position writes its query alone.
+ * B 1..16384, R 1..16, Hq a multiple of Hkv, at most 256.
+ * Errors: VW4_ERR_INVALID_ARG, VW4_ERR_UNSUPPORTED (D, page_size),
+ * VW4_ERR_ALIGN (x, q, norms and caches must be 16-byte aligned, their strides
+ * multiples of 16 bytes).  A page id outside [0, num_pages), or a position
+ * beyond the block table, sets VW4_DEV_BAD_PAGE and nothing is written there.
+ */
+typedef struct vw4_append {
+    vw4_kv_cache kv;
+    const void* x_dev;
+    const double* inv_freq_dev;
+    const float* q_norm_dev;
+    const float* k_norm_dev;
+    void* q_dev;
+    const int32_t* seq_lens_dev;
+    int64_t ldx, ldq;
+    int32_t x_bf16, B, R, Hq, rot, adjacent;
+    float eps;
+} vw4_append;
+VW4_API vw4_status verify_rope_append(const vw4_append* a, void* stream);
+
+/*
+ * verify_attn -- attention of the verify rows over the paged cache.
+ *
+ * Defined by: the Qiita article PART 2 section 2-3 (a verify pass is a batch
+ * of one's own future tokens: its rows attend to the cache and to the rows
+ * before them); R = 1 is plain decoding.
+ *
+ * Row i < R of sequence b is at position p = seq_lens[b] - R + i, and sees key
+ * j iff j <= p and (window = 0 or j > p - window or j < sinks):
+ *   s_j = scale * q . k_j,   out = sum_j exp(s_j) v_j / sum_j exp(s_j),
+ *   lse = log sum_j exp(s_j)
+ * for every query head, whose key head is its index / (Hq / Hkv).  A row that
+ * sees no key (a position below 0) gets zeros and lse = -infinity.  A key that
+ * a row does not see does not touch it, whatever the cache holds there
+ * (infinities and NaN included).
+ *
+ * q_dev, ldq  bf16 [B*R][ldq], ldq >= Hq D.
+ * out_dev, ldo  bf16 [B*R][ldo].
+ * lse_dev     fp32 [B*R][Hq], or NULL.
+ * seq_lens_dev  int32 [B]: tokens in the cache, the R rows included.
+ * B 1..16384, R 1..16, Hq a multiple of Hkv, at most 256; window >= 0, sinks >= 0 (0 unless
+ * window > 0); scale > 0 and finite.
+ * Precision: scores, softmax statistics and sums in fp32; the weights enter
+ * the value product as bf16 (e4m3 caches: as f16), the queries of an e4m3
+ * cache as f16 under an exact power of two per row.
+ * Errors as verify_rope_append; VW4_ERR_WORKSPACE when the workspace is
+ * smaller than vw4_workspace_bytes(VW4_OP_ATTN, B, R * (Hq / Hkv), D) or not
+ * given (256-byte aligned).
+ */
+typedef struct vw4_attn {
+    vw4_kv_cache kv;
+    const void* q_dev;
+    void* out_dev;
+    float* lse_dev;
+    const int32_t* seq_lens_dev;
+    int64_t ldq, ldo;
+    int32_t B, R, Hq, window, sinks;
+    float scale;
+} vw4_attn;
+VW4_API vw4_status verify_attn(const vw4_attn* a, void* workspace_dev, size_t ws_bytes,
+                               void* stream);
+
+/*
+ * process_logits -- the sampler's first stage on the verify logits: penalties
+ * for repeated tokens, sparse biases and grammar masks.
+ *
+ * Defined by: Ollama's mtp.go commit log, paragraph "rework the MLX sampler"
+ * (the pipeline's stages ahead of top-k, on the verify rows, whose history
+ * grows by one draft per row).
+ *
+ * For row i < R of sequence b (R = Kd + 1; drafts 0..i-1 count as output):
+ *   known(v): v among the first hist_len[b] history ids or those drafts
+ *   c(v):     its count among history ids prompt_len[b].. and those drafts
+ *   y = known ? (x > 0 ? x / repetition[b] : x * repetition[b]) : x
+ *   y = c > 0 ? y - frequency[b] * c - presence[b] : y
+ *   y = y + bias (of repeated bias ids the last entry holds)
+ *   out = the mask allows v ? y : -infinity
+ * and block_max as verify_gemm_w4_blockmax writes it, of the outputs (what
+ * accept_rejection_blockmax takes).
+ *
+ * x_dev, ldx  fp32 [B*R][ldx]; out_dev, ldo  fp32 [B*R][ldo], may be x_dev
+ *             (then ldo = ldx).
+ * block_max_dev  fp32 [B*R][ceil(V/16)], or NULL.
+ * drafts_dev  int32 [B][R-1] (NULL when R = 1).
+ * history_dev int32 [B][hist_stride] (NULL: none), hist_max columns;
+ * hist_len_dev  int32 [B] (NULL: hist_max); prompt_len_dev int32 [B] (NULL: 0).
+ * repetition_dev (> 0), presence_dev, frequency_dev  fp32 [B], NULL = 1, 0, 0.
+ * bias_ids_dev, bias_vals_dev  int32 / fp32 [B][bias_stride] (NULL: none),
+ *             bias_max columns; bias_len_dev int32 [B] (NULL: bias_max).
+ * mask_dev    uint32 [mask_rows][mask_stride], bit v % 32 of word v / 32 set =
+ *             allowed (NULL: all allowed); mask_index_dev int32 [B*R] gives the
+ *             mask row of a row, outside [0, mask_rows) = all allowed (NULL: row
+ *             b * R + i).
+ * B 1..16384, R 1..16, 1 <= V <= 2^24.
+ * Errors: VW4_ERR_INVALID_ARG, VW4_ERR_ALIGN (4-byte alignment).  Ids outside
+ * [0, V) are skipped and set VW4_DEV_BAD_LIST_ID (history, bias) or
+ * VW4_DEV_BAD_DRAFT_ID.
+ */
+typedef struct vw4_logits {
+    const float* x_dev;
+    float* out_dev;
+    float* block_max_dev;
+    const int32_t* drafts_dev;
+    const int32_t* history_dev;
+    const int32_t* hist_len_dev;
+    const int32_t* prompt_len_dev;
+    const float* repetition_dev;
+    const float* presence_dev;
+    const float* frequency_dev;
+    const int32_t* bias_ids_dev;
+    const float* bias_vals_dev;
+    const int32_t* bias_len_dev;
+    const uint32_t* mask_dev;
+    const int32_t* mask_index_dev;
+    int64_t ldx, ldo, hist_stride, bias_stride, mask_stride;
+    int32_t B, R, V, hist_max, bias_max, mask_rows;
+} vw4_logits;
+VW4_API vw4_status process_logits(const vw4_logits* a, void* stream);
+
 /* Workspace bytes needed by an operation:
  *   VW4_OP_GEMM:      (M, N, K)
  *   VW4_OP_MOE:       (M*topk, N, K)   -- pass the number of routed pairs first
  *   VW4_OP_REJECTION: (B, Kd, V)
  *   VW4_OP_REJECTION_TOPK: (B, Kd, Kt)
+ *   VW4_OP_ATTN:      (B, R * (Hq / Hkv), D)
  * Returns 0 for an unknown op or invalid sizes. */
 VW4_API size_t vw4_workspace_bytes(int op, int a, int b, int c);
 

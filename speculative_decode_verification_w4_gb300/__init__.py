@@ -8,7 +8,7 @@ call raises.
 
 Entry points (same names as the C ABI):
   verify_gemm_w4, verify_moe_w4, accept_greedy, accept_rejection,
-  accept_rejection_topk,
+  accept_rejection_topk, verify_rope_append, verify_attn, process_logits,
   vw4_workspace_bytes, vw4_get_device_status, vw4_q4_0_from_blocks,
   vw4_set_wait_limit_ns.
 """
@@ -33,6 +33,9 @@ OP_GEMM = 1
 OP_MOE = 2
 OP_REJECTION = 3
 OP_REJECTION_TOPK = 4
+OP_ATTN = 5
+KV_BF16 = 1
+KV_E4M3 = 2
 
 DEV_BAD_DRAFT_ID = 0x1
 DEV_BAD_EXPERT_ID = 0x2
@@ -40,6 +43,7 @@ DEV_WAIT_TIMEOUT = 0x4
 DEV_ZERO_RESIDUAL = 0x8
 DEV_BAD_LIST_ID = 0x10
 DEV_BOUNDS = 0x20          # checks build only: an in-kernel bounds check failed
+DEV_BAD_PAGE = 0x40
 BUILD_CHECKS = 0x1         # vw4_build_flags(): the checks build
 
 STATUS_NAMES = {0: "VW4_OK", 1: "VW4_ERR_INVALID_ARG", 2: "VW4_ERR_UNSUPPORTED",
@@ -55,7 +59,7 @@ EXPORTS = ("verify_gemm_w4", "verify_moe_w4", "accept_greedy", "accept_rejection
            "vw4_depth_ctl_observe", "vw4_depth_ctl_expected", "vw4_depth_ctl_choose",
            "accept_rejection_topk", "vw4_rejection_row_records",
            "vw4_test_inject_stall", "verify_gemm_w4_blockmax", "accept_rejection_blockmax",
-           "vw4_build_flags")
+           "vw4_build_flags", "verify_rope_append", "verify_attn", "process_logits")
 
 
 class VW4Error(RuntimeError):
@@ -85,6 +89,42 @@ class Weight(ctypes.Structure):
 class Sampling(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_float), ("top_p", ctypes.c_float),
                 ("top_k", ctypes.c_int32), ("min_p", ctypes.c_float)]
+
+
+def _fields(ptrs_first, *rest):
+    return [(n, t) for names, t in (ptrs_first, *rest) for n in names.split()]
+
+
+class KVDesc(ctypes.Structure):
+    """vw4_kv_cache (see vw4.h)."""
+    _fields_ = _fields(("dtype page_size num_pages Hkv D max_blocks", ctypes.c_int32),
+                       ("page_stride token_stride head_stride table_stride", ctypes.c_int64),
+                       ("k_dev v_dev block_table_dev k_scale_dev v_scale_dev", ctypes.c_void_p))
+
+
+class AppendArgs(ctypes.Structure):
+    """vw4_append (see vw4.h)."""
+    _fields_ = [("kv", KVDesc)] + _fields(
+        ("x_dev inv_freq_dev q_norm_dev k_norm_dev q_dev seq_lens_dev", ctypes.c_void_p),
+        ("ldx ldq", ctypes.c_int64), ("x_bf16 B R Hq rot adjacent", ctypes.c_int32),
+        ("eps", ctypes.c_float))
+
+
+class AttnArgs(ctypes.Structure):
+    """vw4_attn (see vw4.h)."""
+    _fields_ = [("kv", KVDesc)] + _fields(
+        ("q_dev out_dev lse_dev seq_lens_dev", ctypes.c_void_p), ("ldq ldo", ctypes.c_int64),
+        ("B R Hq window sinks", ctypes.c_int32), ("scale", ctypes.c_float))
+
+
+class LogitsArgs(ctypes.Structure):
+    """vw4_logits (see vw4.h)."""
+    _fields_ = _fields(
+        ("x_dev out_dev block_max_dev drafts_dev history_dev hist_len_dev prompt_len_dev "
+         "repetition_dev presence_dev frequency_dev bias_ids_dev bias_vals_dev bias_len_dev "
+         "mask_dev mask_index_dev", ctypes.c_void_p),
+        ("ldx ldo hist_stride bias_stride mask_stride", ctypes.c_int64),
+        ("B R V hist_max bias_max mask_rows", ctypes.c_int32))
 
 
 _lib = None
@@ -136,6 +176,9 @@ def load_library(path: str = LIB_PATH):
                                             ctypes.c_size_t, P]),
             "accept_rejection_blockmax": (I, [P, P, P, P, P, I, I, I, ctypes.POINTER(Sampling),
                                               U64, U64, P, P, P, ctypes.c_size_t, P]),
+            "verify_rope_append": (I, [ctypes.POINTER(AppendArgs), P]),
+            "verify_attn": (I, [ctypes.POINTER(AttnArgs), P, ctypes.c_size_t, P]),
+            "process_logits": (I, [ctypes.POINTER(LogitsArgs), P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
@@ -474,6 +517,232 @@ def accept_rejection_topk(target_ids: torch.Tensor, target_vals: torch.Tensor,
         _ptr(ws), ws.numel(), _stream(stream))
     _check(code, "accept_rejection_topk")
     return tokens, length
+
+
+class KVCache:
+    """A paged cache bound to its vw4_kv_cache descriptor (see vw4.h): k, v are
+    [pages, page_size, Hkv, D] tensors (views of any page layout whose last
+    dimension is contiguous), bf16 or float8_e4m3fn; block_table int32
+    [B, max_blocks]; k_scale, v_scale fp32 [Hkv] of an e4m3 cache."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
+                 k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None):
+        kinds = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3}
+        if k.dtype not in kinds or v.dtype != k.dtype:
+            raise ValueError("k and v must both be bfloat16 or both float8_e4m3fn")
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must be [pages, page_size, Hkv, D] of equal strides, the "
+                             "last dimension contiguous")
+        if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
+                (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+            raise ValueError("block_table must be int32 [B, max_blocks] with contiguous rows")
+        pages, page, hkv, d = k.shape
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None and (t.dtype != torch.float32 or t.shape != (hkv,)
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name} must be contiguous float32 [Hkv]")
+        self.k, self.v, self.block_table = k, v, block_table
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.B, self.Hkv, self.D, self.page_size = block_table.shape[0], hkv, d, page
+        # a dimension of one element is never stepped over: its stride may be anything
+        self.desc = KVDesc(kinds[k.dtype], page, pages, hkv, d, block_table.shape[1],
+                           k.stride(0) if pages > 1 else 0, k.stride(1) if page > 1 else 0,
+                           k.stride(2) if hkv > 1 else 0,
+                           max(block_table.stride(0), block_table.shape[1]),
+                           *(_addr(t) for t in (k, v, block_table, k_scale, v_scale)))
+
+
+def _addr(t):
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return t.data_ptr()
+
+
+def _need(t, dtype, shape, what):
+    """t as an optional contiguous tensor of that type and shape."""
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)
+                          or not t.is_contiguous()):
+        raise ValueError(f"{what} must be contiguous {dtype} {list(shape)}")
+    return t
+
+
+def _rows(t, dtype, shape, what):
+    """The row stride of a [B, R, *inner] tensor whose rows are contiguous and evenly spaced."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {dtype} {list(shape)}")
+    inner = 1
+    for n, st in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
+        if n > 1 and st != inner:
+            raise ValueError(f"{what}: the rows must be contiguous")
+        inner *= n
+    B, R = t.shape[:2]
+    ld = t.stride(1) if R > 1 else (t.stride(0) if B > 1 else inner)
+    if B > 1 and t.stride(0) != R * ld:
+        raise ValueError(f"{what}: the rows must be evenly spaced")
+    return ld
+
+
+class _Prepared:
+    """One call bound to its tensors: the argument block is filled once, a call
+    is a single ctypes call on the stream of construction (like PreparedGemm).
+    The tensors are kept alive and read anew by every call."""
+
+    def _bind(self, name, args, keep, stream, workspace=None):
+        self._name, self._args, self._keep = name, args, keep
+        self._fn, self._ref = getattr(load_library(), name), ctypes.byref(args)
+        s = (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+        self._tail = (s,) if workspace is None else (workspace.data_ptr(), workspace.numel(), s)
+        self._ws = workspace
+
+    def __call__(self):
+        code = self._fn(self._ref, *self._tail)
+        if code:
+            _check(code, self._name)
+
+
+class PreparedAppend(_Prepared):
+    """verify_rope_append bound to its tensors."""
+
+    def __init__(self, x: torch.Tensor, cache: KVCache, seq_lens: torch.Tensor, R: int, Hq: int,
+                 inv_freq: torch.Tensor | None = None, adjacent: bool = False,
+                 q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None,
+                 eps: float = 1e-6, q_out: torch.Tensor | None = None, stream=None):
+        B, D = cache.B, cache.D
+        if x.dtype not in (torch.float32, torch.bfloat16) or x.dim() != 2 or \
+                x.shape != (B * R, (Hq + 2 * cache.Hkv) * D) or x.stride(1) != 1:
+            raise ValueError("x must be float32 or bfloat16 [B*R, (Hq + 2 Hkv) * D] with "
+                             "contiguous rows")
+        if q_out is None:
+            q_out = torch.empty((B, R, Hq, D), dtype=torch.bfloat16, device=x.device)
+        ldq = _rows(q_out, torch.bfloat16, (B, R, Hq, D), "q_out")
+        _need(seq_lens, torch.int32, (B,), "seq_lens")
+        rot = 0
+        if inv_freq is not None:
+            rot = 2 * inv_freq.numel()
+            _need(inv_freq, torch.float64, (rot // 2,), "inv_freq")
+        for n, t in (("q_norm", q_norm), ("k_norm", k_norm)):
+            _need(t, torch.float32, (D,), n)
+        self.q_out = q_out
+        ldx = x.stride(0) if x.shape[0] > 1 else x.shape[1]
+        args = AppendArgs(cache.desc, _addr(x), _addr(inv_freq) if rot else None, _addr(q_norm),
+                          _addr(k_norm), _addr(q_out), _addr(seq_lens), ldx, ldq,
+                          int(x.dtype == torch.bfloat16), B, R, Hq, rot, int(adjacent), eps)
+        self._bind("verify_rope_append", args,
+                   (x, cache, seq_lens, inv_freq, q_norm, k_norm, q_out), stream)
+
+
+def verify_rope_append(x, cache, seq_lens, R, Hq, **kw):
+    """Packed qkv rows x [B*R, (Hq + 2 Hkv) * D] (fp32 or bf16) -> rotated
+    queries bf16 [B, R, Hq, D] (returned), keys and values into the cache slots
+    of positions seq_lens[b] - R + i; see vw4.h.  Keywords: inv_freq fp64
+    [rot/2], adjacent, q_norm, k_norm fp32 [D], eps, q_out, stream."""
+    p = PreparedAppend(x, cache, seq_lens, R, Hq, **kw)
+    p()
+    return p.q_out
+
+
+class PreparedAttn(_Prepared):
+    """verify_attn bound to its tensors and a workspace."""
+
+    def __init__(self, q: torch.Tensor, cache: KVCache, seq_lens: torch.Tensor,
+                 scale: float | None = None, window: int = 0, sinks: int = 0,
+                 out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                 workspace=None, stream=None):
+        if q.dim() != 4:
+            raise ValueError("q must be [B, R, Hq, D]")
+        B, R, Hq, D = q.shape
+        if B != cache.B or D != cache.D:
+            raise ValueError("q must be [B, R, Hq, D] of the cache's batch and head size")
+        ldq = _rows(q, torch.bfloat16, (B, R, Hq, D), "q")
+        if out is None:
+            out = torch.empty((B, R, Hq, D), dtype=torch.bfloat16, device=q.device)
+        ldo = _rows(out, torch.bfloat16, (B, R, Hq, D), "out")
+        _need(lse, torch.float32, (B, R, Hq), "lse")
+        _need(seq_lens, torch.int32, (B,), "seq_lens")
+        self.out, self.lse = out, lse
+        args = AttnArgs(cache.desc, _addr(q), _addr(out), _addr(lse), _addr(seq_lens), ldq, ldo, B,
+                        R, Hq, int(window), int(sinks), float(D ** -0.5 if scale is None else scale))
+        need = vw4_workspace_bytes(OP_ATTN, B, R * max(1, Hq // cache.Hkv), D)
+        if workspace is None:
+            workspace = Workspace(q.device)
+        ws = _workspace(workspace, need, q.device)
+        self._bind("verify_attn", args, (q, cache, seq_lens, out, lse), stream, ws)
+
+
+def verify_attn(q, cache, seq_lens, scale=None, window=0, sinks=0, out=None, lse=None,
+                workspace=None, stream=None):
+    """Attention of the verify rows q bf16 [B, R, Hq, D] (R = 1: plain decoding)
+    over the paged cache -> out bf16 [B, R, Hq, D]; scale defaults to
+    1/sqrt(D); lse: optional fp32 [B, R, Hq]; see vw4.h."""
+    need = vw4_workspace_bytes(OP_ATTN, q.shape[0], q.shape[1] * max(1, q.shape[2] // cache.Hkv),
+                               q.shape[3])
+    p = PreparedAttn(q, cache, seq_lens, scale, window, sinks, out, lse,
+                     _workspace(workspace, need, q.device), stream)
+    p()
+    return p.out
+
+
+class PreparedLogits(_Prepared):
+    """process_logits bound to its tensors."""
+
+    def __init__(self, logits: torch.Tensor, drafts: torch.Tensor | None = None,
+                 history: torch.Tensor | None = None, hist_len: torch.Tensor | None = None,
+                 prompt_len: torch.Tensor | None = None, repetition: torch.Tensor | None = None,
+                 presence: torch.Tensor | None = None, frequency: torch.Tensor | None = None,
+                 bias_ids: torch.Tensor | None = None, bias_vals: torch.Tensor | None = None,
+                 bias_len: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                 mask_index: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 block_max: torch.Tensor | None = None, stream=None):
+        if logits.dim() != 3:
+            raise ValueError("logits must be [B, R, V]")
+        B, R, V = logits.shape
+        ldx = _rows(logits, torch.float32, (B, R, V), "logits")
+        if out is None:
+            out = torch.empty((B, R, V), dtype=torch.float32, device=logits.device)
+        ldo = _rows(out, torch.float32, (B, R, V), "out")
+        _need(block_max, torch.float32, (B, R, (V + 15) // 16), "block_max")
+        if R > 1 and drafts is None:
+            raise ValueError("drafts int32 [B, R - 1] are needed")
+        _need(drafts, torch.int32, (B, R - 1), "drafts")
+        for n, t in (("hist_len", hist_len), ("prompt_len", prompt_len), ("bias_len", bias_len)):
+            _need(t, torch.int32, (B,), n)
+        for n, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
+            _need(t, torch.float32, (B,), n)
+        for n, t, dt in (("history", history, torch.int32), ("bias_ids", bias_ids, torch.int32),
+                         ("bias_vals", bias_vals, torch.float32)):
+            if t is not None:
+                _need(t, dt, (B, t.shape[-1]), n)
+        if (bias_ids is None) != (bias_vals is None) or \
+                (bias_ids is not None and bias_ids.shape != bias_vals.shape):
+            raise ValueError("bias_ids and bias_vals come together, of one shape")
+        if mask is not None:
+            W = (V + 31) // 32
+            if mask.dtype != torch.int32 or mask.shape[-1] != W or not mask.is_contiguous():
+                raise ValueError("mask must be contiguous int32 [rows, ceil(V / 32)]")
+            if mask_index is None and mask.numel() != B * R * W:
+                raise ValueError("mask must have a row for every logits row, or mask_index")
+            _need(mask_index, torch.int32, (B, R), "mask_index")
+        self.out, self.block_max = out, block_max
+        keep = (logits, out, block_max, drafts, history, hist_len, prompt_len, repetition,
+                presence, frequency, bias_ids, bias_vals, bias_len, mask, mask_index)
+        H = 0 if history is None else history.shape[1]
+        nb = 0 if bias_ids is None else bias_ids.shape[1]
+        W = (V + 31) // 32
+        args = LogitsArgs(*(_addr(t) if t is None or t.numel() else None for t in keep), ldx, ldo,
+                          H, nb, W, B, R, V, H, nb, 0 if mask is None else mask.numel() // W)
+        self._bind("process_logits", args, keep, stream)
+
+
+def process_logits(logits, drafts=None, **kw):
+    """Penalties, biases and grammar masks on verify logits fp32 [B, R, V], row i
+    with drafts[:, :i] (int32 [B, R - 1]) in its history -> processed logits
+    (a new tensor, or `out`, which may be `logits`); keywords as
+    PreparedLogits; see vw4.h."""
+    p = PreparedLogits(logits, drafts, **kw)
+    p()
+    return p.out
 
 
 # vw4_row_record (see vw4.h): 32 bytes per row

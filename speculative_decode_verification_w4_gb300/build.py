@@ -21,7 +21,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libvw4.so")
 BUILD_CHECKS = os.path.join(HERE, "_build_checks")
 LIB_CHECKS = os.path.join(HERE, "libvw4_checks.so")
-SOURCES = ["api.cu", "gemm_w4.cu", "accept.cu", "rejection.cu", "controller.cpp"]
+SOURCES = ["api.cu", "gemm_w4.cu", "accept.cu", "rejection.cu", "controller.cpp", "step_api.cu",
+           "attn.cu", "attn_d64.cu", "attn_d128.cu", "attn_d256.cu", "rope_append.cu", "logits.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler",
          "-fvisibility=hidden", "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

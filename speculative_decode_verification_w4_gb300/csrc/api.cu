@@ -158,6 +158,18 @@ vw4_status check_weight(const vw4_weight* W) {
 int padded_k(int K) { return (K + kStageK - 1) / kStageK * kStageK; }
 
 }  // namespace
+
+int current_device(int* sms, uint32_t** status) {
+    DeviceInfo* d = nullptr;
+    const vw4_status st = device_info(&d);
+    if (st != VW4_OK) return st;
+    *sms = d->sms;
+    *status = d->status;
+    return VW4_OK;
+}
+
+int report_cuda(cudaError_t e, const char* where) { return cuda_fail(e, where); }
+
 }  // namespace vw4
 
 using namespace vw4;
@@ -210,6 +222,12 @@ VW4_API size_t vw4_workspace_bytes(int op, int a, int b, int c) {
     if (op == VW4_OP_REJECTION_TOPK) {
         if (a < 1 || b < 0 || b > 8 || c < 1 || c > 1024) return 0;
         return rejection_topk_workspace_bytes(a, b, c);
+    }
+    if (op == VW4_OP_ATTN) {
+        if (a < 1 || a > kMaxSeqs || b < 1 || b > kMaxVerifyRows * kMaxHeads ||
+            (c != 64 && c != 128 && c != 256))
+            return 0;
+        return attn_workspace_bytes(a, b, c);
     }
     return 0;
 }

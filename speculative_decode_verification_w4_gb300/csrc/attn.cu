@@ -1,0 +1,125 @@
+// attn.cu -- attention of the verify rows: choice of the kernel, workspace,
+// and the kernel that joins the partial rows of items split over CTAs.
+#include "attn.cuh"
+
+namespace vw4 {
+
+// Query rows of a block: the smallest shape that holds them all.  More rows
+// than the largest shape are cut into blocks of it, each reading the keys
+// again (from L2: the blocks of a key head are neighbours in the schedule).
+int attn_rows(int rows, int D) {
+    if (rows <= 16) return 16;
+    if (rows <= 32) return 32;
+    if (rows <= 64 || D == 256) return 64;
+    return 128;
+}
+
+static int attn_grid_cap(int D) { return D == 256 ? kAttnMaxGrid256 : kAttnMaxGrid64; }
+
+static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
+
+size_t attn_workspace_bytes(int B, int rows, int D) {
+    const size_t base = align256((static_cast<size_t>(B) + 1) * sizeof(long long));
+    return base + align256(2u * static_cast<size_t>(attn_grid_cap(D)) * attn_rows(rows, D) *
+                           (D + 2) * sizeof(float));
+}
+
+constexpr int kJoinThreads = 128;
+
+// Joins the partials of split items, in the order of their tiles, and writes
+// the rows of sequences without keys.  One block takes `chunk` rows of an
+// item, one warp a row; each lane owns D / 32 columns.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParams p, int rows,
+                                                                 int grid, int tk, int chunk) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int item = blockIdx.x, b = item / p.groups, g = item - b * p.groups;
+    const int rb = g % p.row_blocks, h = g / p.row_blocks;
+    const long long T = p.base[p.B];
+    const int nt = attn_seq(p.seq_lens[b], p.max_blocks * p.page_size, p.R, p.window, p.sinks, tk).nt;
+    const long long u = p.base[b] + static_cast<long long>(g) * nt;
+    const int G = attn_ctas(T, grid);
+    int c0 = 0, c1 = 0;
+    if (nt > 0) {
+        c0 = attn_owner(T, G, u);
+        c1 = attn_owner(T, G, u + nt - 1);
+        if (c0 == c1) return;  // written by the attention kernel
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float vs = p.v_scale ? __ldg(p.v_scale + h) : 1.f;
+    constexpr int E = D / 32;
+    for (int r = blockIdx.y * chunk + warp; r < (static_cast<int>(blockIdx.y) + 1) * chunk && r < rows;
+         r += kJoinThreads / 32) {
+        const int row = rb * rows + r;
+        if (row >= p.R * p.G) return;
+        const int i = row / p.G, hq = h * p.G + row - i * p.G;
+        const long long orow = static_cast<long long>(b) * p.R + i;
+        float M = -INFINITY, L = 0.f, acc[E] = {};
+        if (nt > 0) {
+            // the partials' maxima first (lanes in parallel), then their rows
+            const size_t slot = static_cast<size_t>(rows) * (D + 2);
+            for (int c = c0 + lane; c <= c1; c += 32) {
+                const float* q = p.partial + static_cast<size_t>(c == c0 ? 2 * c + 1 : 2 * c) * slot;
+                M = fmaxf(M, q[rows * D + r]);
+            }
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) {
+                const float* q = p.partial + static_cast<size_t>(c == c0 ? 2 * c + 1 : 2 * c) * slot;
+                const float w = M == -INFINITY ? 1.f : ex2(q[rows * D + r] - M);
+                L += q[rows * (D + 1) + r] * w;
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float2 v = *reinterpret_cast<const float2*>(q + r * D + lane * 2 + e * 32);
+                    acc[e] = fmaf(v.x, w, acc[e]);
+                    acc[e + 1] = fmaf(v.y, w, acc[e + 1]);
+                }
+            }
+        }
+        const float f = L == 0.f ? 0.f : vs / L;
+        __nv_bfloat16* out = p.out + orow * p.ldo + static_cast<long long>(hq) * D;
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t*>(out + lane * 2 + e * 32) =
+                pack2<false>(acc[e] * f, acc[e + 1] * f);
+        if (lane == 0 && p.lse)
+            p.lse[orow * p.Hq + hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    }
+}
+
+cudaError_t launch_attn(AttnParams p, int D, bool f8, int sms, void* ws, cudaStream_t s) {
+    const int total = p.R * p.G, rows = attn_rows(total, D), tk = f8 ? 128 : 64;
+    p.row_blocks = (total + rows - 1) / rows;
+    p.groups = p.Hkv * p.row_blocks;
+    p.base = static_cast<long long*>(ws);
+    p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                         align256((static_cast<size_t>(p.B) + 1) * sizeof(long long)));
+    // at most one CTA per tile that the table could hold
+    const long long cap = static_cast<long long>(p.max_blocks) * p.page_size;
+    const long long units = static_cast<long long>(p.B) * p.groups * ((cap + tk - 1) / tk);
+    int grid = attn_grid_cap(D);
+    if (units < grid) grid = static_cast<int>(units < 1 ? 1 : units);
+    cudaError_t e = D == 64    ? launch_attn_d64(p, f8, rows, &grid, sms, s)
+                    : D == 128 ? launch_attn_d128(p, f8, rows, &grid, sms, s)
+                               : launch_attn_d256(p, f8, rows, &grid, sms, s);
+    if (e != cudaSuccess) return e;
+    // about eight blocks an SM; a warp takes a row at a time
+    const int items = p.B * p.groups, used = total < rows ? total : rows;
+    int chunk = static_cast<int>((static_cast<long long>(items) * used + 8 * sms - 1) / (8 * sms));
+    chunk = chunk < 4 ? 4 : (chunk > used ? used : chunk);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(items, (used + chunk - 1) / chunk);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto* join = D == 64 ? attn_join_kernel<64> : (D == 128 ? attn_join_kernel<128> : attn_join_kernel<256>);
+    return cudaLaunchKernelEx(&cfg, join, p, rows, grid, tk, chunk);
+}
+
+}  // namespace vw4

@@ -1,0 +1,186 @@
+// logits.cu -- the sampler's first stage on the verify logits: penalties for
+// repeated tokens, sparse biases and grammar masks, with the block maxima that
+// the sampled accept reads.
+//
+//   known(v) = v among prompt, output and the row's earlier drafts;
+//   c(v)     = its count among output and the row's earlier drafts
+//   y = known ? (x > 0 ? x / r : x r) : x;   y -= f c + q [c > 0];   y += bias
+//   out = allowed ? y : -infinity
+//
+// One pass over the logits: a block owns a chunk of the vocabulary of one
+// sequence and keeps its counts in shared memory, so the rows of a verify
+// batch share one scan of the token history, and row i + 1 adds one draft to
+// the counts of row i.  The bytes bound it (8 a logit); the scan re-reads the
+// history once per chunk, from L2.
+#include "attn.cuh"
+
+namespace vw4 {
+
+constexpr int kLogitThreads = 256;
+constexpr int kLogitChunk = 4096;               // vocabulary entries of a block
+constexpr uint32_t kKnown = 0x80000000u;        // count word: in the prompt
+constexpr uint32_t kLogitBadDraft = 0x1u;
+
+// VEC consecutive logits a thread and step
+template <int VEC>
+__global__ void __launch_bounds__(kLogitThreads) logits_kernel(const LogitsParams p, int row_step) {
+    constexpr int N = kLogitChunk / (kLogitThreads * VEC);  // steps of a row
+    __shared__ uint32_t s_cnt[kLogitChunk];
+    __shared__ int s_bias[kLogitChunk];                     // bias entry + 1 (0: none)
+    __shared__ uint32_t s_hit[kLogitChunk / 32];            // entries with a count or a bias
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, b = blockIdx.y;
+    const int c0 = blockIdx.x * kLogitChunk;
+    const int row0 = blockIdx.z * row_step, row1 = min(p.R, row0 + row_step);
+    for (int k = tid; k < kLogitChunk; k += kLogitThreads) {
+        s_cnt[k] = 0u;
+        s_bias[k] = 0;
+    }
+    for (int k = tid; k < kLogitChunk / 32; k += kLogitThreads) s_hit[k] = 0u;
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    auto hit = [&](int at) { atomicOr(&s_hit[at >> 5], 1u << (at & 31)); };
+    const bool flagger = blockIdx.x == 0 && blockIdx.z == 0;
+    bool bad = false;
+    if (p.history) {
+        const int n = p.hist_len ? max(0, min(p.hist_max, p.hist_len[b])) : p.hist_max;
+        const int np = p.prompt_len ? p.prompt_len[b] : 0;
+        const int32_t* ids = p.history + static_cast<long long>(b) * p.hist_stride;
+#pragma unroll 4
+        for (int t = tid; t < n; t += kLogitThreads) {
+            const int v = __ldg(ids + t), at = v - c0;
+            if (v >= c0 && v < p.V && at < kLogitChunk) {
+                if (t < np) atomicOr(&s_cnt[at], kKnown);
+                else atomicAdd(&s_cnt[at], 1u);
+                hit(at);
+            }
+            bad |= v < 0 || v >= p.V;
+        }
+    }
+    if (p.bias_ids) {
+        const int n = p.bias_len ? max(0, min(p.bias_max, p.bias_len[b])) : p.bias_max;
+        const int32_t* ids = p.bias_ids + static_cast<long long>(b) * p.bias_stride;
+        for (int t = tid; t < n; t += kLogitThreads) {
+            const int v = __ldg(ids + t), at = v - c0;
+            if (v >= c0 && v < p.V && at < kLogitChunk) {
+                atomicMax(&s_bias[at], t + 1);  // of repeated ids the last entry holds
+                hit(at);
+            }
+            bad |= v < 0 || v >= p.V;
+        }
+    }
+    if (flagger && bad) atomicOr(p.status, kStatusBadListId);
+    auto add_draft = [&](int i) {
+        const int v = p.drafts[static_cast<long long>(b) * (p.R - 1) + i];
+        if (v >= c0 && v < p.V && v - c0 < kLogitChunk) {
+            atomicAdd(&s_cnt[v - c0], 1u);
+            hit(v - c0);
+        }
+    };
+    if (tid < row0) add_draft(tid);  // the drafts before this block's first row
+    if (flagger && tid < p.R - 1) {
+        const int v = p.drafts[static_cast<long long>(b) * (p.R - 1) + tid];
+        if (v < 0 || v >= p.V) atomicOr(p.status, kLogitBadDraft);
+    }
+
+    const float rep = p.repetition ? __ldg(p.repetition + b) : 1.f;
+    const float pre = p.presence ? __ldg(p.presence + b) : 0.f;
+    const float fre = p.frequency ? __ldg(p.frequency + b) : 0.f;
+    const float* bias = p.bias_ids ? p.bias_vals + static_cast<long long>(b) * p.bias_stride : nullptr;
+
+    float x[N][VEC];
+    uint32_t allow[N];  // VEC bits a step
+    auto fetch = [&](int i) {
+        const long long row = static_cast<long long>(b) * p.R + i;
+        const uint32_t* mk = nullptr;
+        if (p.mask) {
+            const long long mr = p.mask_index ? p.mask_index[row] : row;
+            if (mr >= 0 && mr < p.mask_rows) mk = p.mask + mr * p.mask_stride;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int v = c0 + (k * kLogitThreads + tid) * VEC;
+            constexpr uint32_t full = (1u << VEC) - 1u;
+            allow[k] = v >= p.V ? 0u : (mk ? (__ldg(mk + (v >> 5)) >> (v & 31)) & full : full);
+        }
+        const float* src = p.x + row * p.ldx;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int v = c0 + (k * kLogitThreads + tid) * VEC;
+            if (allow[k]) {  // masked logits are not read
+                if (VEC == 4) *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(src + v);
+                else x[k][0] = src[v];
+            }
+        }
+    };
+
+    for (int i = row0; i < row1; ++i) {
+        fetch(i);
+        __syncthreads();  // the counts of this row are complete
+        const long long row = static_cast<long long>(b) * p.R + i;
+        float* dst = p.out + row * p.ldo;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int at = (k * kLogitThreads + tid) * VEC, v = c0 + at;
+            uint32_t hits = (s_hit[at >> 5] >> (at & 31)) & allow[k];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float y = -INFINITY;
+                if ((allow[k] >> e) & 1u) {
+                    y = x[k][e];
+                    if ((hits >> e) & 1u) {
+                        const uint32_t c = s_cnt[at + e];
+                        const int be = s_bias[at + e];
+                        if (c) y = y > 0.f ? __fdiv_rn(y, rep) : y * rep;
+                        const float n = static_cast<float>(c & ~kKnown);
+                        if (n > 0.f) y = y - fre * n - pre;
+                        if (be) y += __ldg(bias + be - 1);
+                    }
+                }
+                x[k][e] = y;
+                mx = fmaxf(mx, y);
+            }
+            if (v < p.V) {
+                if (VEC == 4) *reinterpret_cast<float4*>(dst + v) = *reinterpret_cast<float4*>(x[k]);
+                else dst[v] = x[k][0];
+            }
+            if (p.bmax) {
+#pragma unroll
+                for (int o = 1; o < 16 / VEC; o <<= 1)
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                if (v < p.V && (at & 15) == 0)
+                    p.bmax[row * ((p.V + 15) / 16) + (v >> 4)] = mx;
+            }
+        }
+        if (i + 1 < row1) {
+            __syncthreads();  // every thread has read the counts of row i
+            if (tid == 0) add_draft(i);
+        }
+    }
+}
+
+cudaError_t launch_logits(const LogitsParams& p, int sms, cudaStream_t s) {
+    const int chunks = (p.V + kLogitChunk - 1) / kLogitChunk;
+    // few sequences: the rows are split over blocks too (each scans the history again)
+    const long long blocks = static_cast<long long>(chunks) * p.B;
+    int split = static_cast<int>((4LL * sms + blocks - 1) / blocks);
+    if (split > p.R) split = p.R;
+    const int step = (p.R + split - 1) / split;
+    const auto a16 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
+    const bool vec = p.V % 4 == 0 && p.ldx % 4 == 0 && p.ldo % 4 == 0 && a16(p.x) && a16(p.out);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(chunks, p.B, (p.R + step - 1) / step);
+    cfg.blockDim = dim3(kLogitThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return vec ? cudaLaunchKernelEx(&cfg, logits_kernel<4>, p, step)
+               : cudaLaunchKernelEx(&cfg, logits_kernel<1>, p, step);
+}
+
+}  // namespace vw4

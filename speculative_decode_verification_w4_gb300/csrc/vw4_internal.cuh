@@ -2,6 +2,7 @@
 // shared by the kernels and the C-ABI layer.  Not part of the public ABI.
 #pragma once
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <atomic>
@@ -45,6 +46,8 @@ __device__ __forceinline__ bool check(bool ok, uint32_t* status) {
 constexpr int kMaxRows = 8;        // rows of one mma n-tile; verify rows per MoE segment
 constexpr int kMaxVerifyRows = 16; // dense verify rows per call: two n-tiles
 constexpr int kMaxSeg = 128;       // routed (token, expert) pairs per call: 16 tokens x top-8
+constexpr int kMaxSeqs = 16384;    // sequences of an attention, append or logits call
+constexpr int kMaxHeads = 256;     // query heads of an attention or append call
 constexpr int kTileRows = 128;     // weight rows per tile
 constexpr int kStageK = 256;       // k elements per pipeline stage
 constexpr int kMinUnitsPerCta = 4; // tile-aligned split-K: at least this many stages per part
@@ -199,6 +202,94 @@ cudaError_t launch_accept_rejection(const float* target, const float* draft,
                                     unsigned long long wait_ns, cudaStream_t s,
                                     const float* target_bmax = nullptr,
                                     const float* draft_bmax = nullptr);
+
+// What the entry points outside api.cu need of it: the current device's SM
+// count and status word, and the text of a failed CUDA call (both return a
+// vw4_status).
+int current_device(int* sms, uint32_t** status);
+int report_cuda(cudaError_t e, const char* where);
+
+// ---- attention of the verify rows over a paged cache (attn*.cu)
+constexpr uint32_t kStatusBadPage = 0x40u;
+constexpr uint32_t kStatusBadListId = 0x10u;
+struct AttnParams {
+    const __nv_bfloat16* q;
+    const void* k;
+    const void* v;
+    const int32_t* table;
+    const int32_t* seq_lens;
+    const float* k_scale;   // [Hkv] or null (e4m3 caches)
+    const float* v_scale;
+    __nv_bfloat16* out;
+    float* lse;             // or null
+    float* partial;         // [2 grid][rows][D] unnormalized rows, then m [rows], l [rows]
+    long long* base;        // [B + 1]: units before each sequence, all units
+    uint32_t* status;
+    long long ldq, ldo, table_stride, page_stride, token_stride, head_stride;
+    float scale;
+    int B, R, Hq, Hkv, G;   // G: query heads of a key head
+    int window, sinks;
+    int page_size, page_shift, max_blocks, num_pages;
+    int row_blocks, groups;  // query-row blocks of a key head; Hkv * row_blocks
+};
+constexpr int kAttnMaxGrid64 = 608, kAttnMaxGrid256 = 304;
+int attn_rows(int rows, int D);        // rows of a block of the kernel chosen for that many rows
+size_t attn_workspace_bytes(int B, int rows, int D);
+cudaError_t launch_attn(AttnParams p, int D, bool f8, int sms, void* ws, cudaStream_t s);
+cudaError_t launch_attn_d64(const AttnParams& p, bool f8, int rows, int* grid, int sms,
+                            cudaStream_t s);
+cudaError_t launch_attn_d128(const AttnParams& p, bool f8, int rows, int* grid, int sms,
+                             cudaStream_t s);
+cudaError_t launch_attn_d256(const AttnParams& p, bool f8, int rows, int* grid, int sms,
+                             cudaStream_t s);
+
+// ---- head norm, rotation and cache append (rope_append.cu)
+struct AppendParams {
+    const void* x;
+    int x_bf16;
+    long long ldx;
+    const double* inv_freq;  // [rot / 2]
+    const float* q_norm;     // [D] or null
+    const float* k_norm;
+    float eps;
+    int rot, adjacent;
+    __nv_bfloat16* q;
+    long long ldq;
+    const int32_t* seq_lens;
+    const int32_t* table;
+    void* k;
+    void* v;
+    const float* k_scale;
+    const float* v_scale;
+    uint32_t* status;
+    long long table_stride, page_stride, token_stride, head_stride;
+    int B, R, Hq, Hkv, D;
+    int page_size, page_shift, max_blocks, num_pages;
+};
+cudaError_t launch_append(const AppendParams& p, bool f8, int sms, cudaStream_t s);
+
+// ---- penalties, biases and masks on the verify logits (logits.cu)
+struct LogitsParams {
+    const float* x;
+    float* out;
+    float* bmax;                // or null
+    const int32_t* drafts;
+    const int32_t* history;
+    const int32_t* hist_len;
+    const int32_t* prompt_len;
+    const float* repetition;
+    const float* presence;
+    const float* frequency;
+    const int32_t* bias_ids;
+    const float* bias_vals;
+    const int32_t* bias_len;
+    const uint32_t* mask;
+    const int32_t* mask_index;
+    uint32_t* status;
+    long long ldx, ldo, hist_stride, bias_stride, mask_stride;
+    int B, R, V, hist_max, bias_max, mask_rows;
+};
+cudaError_t launch_logits(const LogitsParams& p, int sms, cudaStream_t s);
 
 // Copies the first `rows` row records of a rejection workspace (test hook).
 cudaError_t copy_rejection_row_records(const void* ws, long long rows, void* out,
