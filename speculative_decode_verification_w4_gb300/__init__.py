@@ -546,7 +546,7 @@ class KVCache:
         self.B, self.Hkv, self.D, self.page_size = block_table.shape[0], hkv, d, page
         # a dimension of one element is never stepped over: its stride may be anything
         self.desc = KVDesc(kinds[k.dtype], page, pages, hkv, d, block_table.shape[1],
-                           k.stride(0) if pages > 1 else 0, k.stride(1) if page > 1 else 0,
+                           k.stride(0) if pages > 1 else 0, k.stride(1) if page > 1 else hkv * d,
                            k.stride(2) if hkv > 1 else 0,
                            max(block_table.stride(0), block_table.shape[1]),
                            *(_addr(t) for t in (k, v, block_table, k_scale, v_scale)))

@@ -170,6 +170,65 @@ int current_device(int* sms, uint32_t** status) {
 
 int report_cuda(cudaError_t e, const char* where) { return cuda_fail(e, where); }
 
+unsigned long long wait_limit_ns() { return g_wait_ns; }
+
+int encode_map(CUtensorMap* map, bool bf16, int n, const void* base, const uint64_t* dims,
+               const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw) {
+    struct Key {
+        const void* base;
+        uint64_t d[4], s[4];
+        uint32_t b[4];
+        int n, bf16, sw;
+    };
+    constexpr int kSlots = 64;
+    static Key keys[kSlots];
+    static CUtensorMap maps[kSlots];
+    static int next = 0;
+    static std::mutex mu;
+    Key key;
+    memset(&key, 0, sizeof key);
+    key.base = base;
+    key.n = n;
+    key.bf16 = bf16;
+    key.sw = static_cast<int>(sw);
+    const uint64_t es = bf16 ? 2 : 1;
+    for (int i = 0; i < n; ++i) {
+        key.d[i] = dims[i];
+        key.s[i] = i > 0 ? strides[i - 1] * es : es;
+        key.b[i] = box[i];
+    }
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        for (int i = 0; i < kSlots; ++i)
+            if (memcmp(&keys[i], &key, sizeof key) == 0) {
+                *map = maps[i];
+                return VW4_OK;
+            }
+    }
+    cuuint64_t d[4], st[3];
+    cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+    for (int i = 0; i < n; ++i) {
+        d[i] = key.d[i];
+        b[i] = key.b[i];
+        if (i > 0) st[i - 1] = key.s[i];
+    }
+    const CUresult r =
+        g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, n,
+                 const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        char buf[128];
+        snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+        g_last_error = buf;
+        return VW4_ERR_CUDA;
+    }
+    std::lock_guard<std::mutex> lk(mu);
+    keys[next] = key;
+    maps[next] = *map;
+    next = (next + 1) % kSlots;
+    return VW4_OK;
+}
+
 }  // namespace vw4
 
 using namespace vw4;

@@ -4,14 +4,14 @@
 
 namespace vw4 {
 
-// Query rows of a block: the smallest shape that holds them all.  More rows
-// than the largest shape are cut into blocks of it, each reading the keys
-// again (from L2: the blocks of a key head are neighbours in the schedule).
-int attn_rows(int rows, int D) {
-    if (rows <= 16) return 16;
-    if (rows <= 32) return 32;
-    if (rows <= 64 || D == 256) return 64;
-    return 128;
+// Query rows of a block: the smallest kernel shape that holds a key head's
+// rows; more than 128 are cut into blocks, each reading the keys again (from
+// L2: the blocks of a key head are neighbours in the schedule).
+static int attn_rows(int rows) { return rows <= 16 ? 16 : (rows <= 64 ? 64 : 128); }
+// keys of a tile of the kernel for blocks of that many rows
+static int attn_tile(int rows, int D, bool f8) {
+    if (rows == 16) return f8 ? 128 : 64;
+    return D == 256 ? 64 : 128;
 }
 
 static int attn_grid_cap(int D) { return D == 256 ? kAttnMaxGrid256 : kAttnMaxGrid64; }
@@ -20,8 +20,8 @@ static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 size_t attn_workspace_bytes(int B, int rows, int D) {
     const size_t base = align256((static_cast<size_t>(B) + 1) * sizeof(long long));
-    return base + align256(2u * static_cast<size_t>(attn_grid_cap(D)) * attn_rows(rows, D) *
-                           (D + 2) * sizeof(float));
+    return base + align256(2u * static_cast<size_t>(attn_grid_cap(D)) * attn_rows(rows) * (D + 2) *
+                           sizeof(float));
 }
 
 constexpr int kJoinThreads = 128;
@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int item = blockIdx.x, b = item / p.groups, g = item - b * p.groups;
-    const int rb = g % p.row_blocks, h = g / p.row_blocks;
+    const int h = g / p.row_blocks;
     const long long T = p.base[p.B];
     const int nt = attn_seq(p.seq_lens[b], p.max_blocks * p.page_size, p.R, p.window, p.sinks, tk).nt;
     const long long u = p.base[b] + static_cast<long long>(g) * nt;
@@ -51,10 +51,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
     constexpr int E = D / 32;
     for (int r = blockIdx.y * chunk + warp; r < (static_cast<int>(blockIdx.y) + 1) * chunk && r < rows;
          r += kJoinThreads / 32) {
-        const int row = rb * rows + r;
-        if (row >= p.R * p.G) return;
-        const int i = row / p.G, hq = h * p.G + row - i * p.G;
-        const long long orow = static_cast<long long>(b) * p.R + i;
+        const AttnRow row = attn_row(p, g, r);
+        if (!row.live) continue;
+        const long long orow = static_cast<long long>(b) * p.R + row.i;
         float M = -INFINITY, L = 0.f, acc[E] = {};
         if (nt > 0) {
             // the partials' maxima first (lanes in parallel), then their rows
@@ -79,34 +78,53 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
             }
         }
         const float f = L == 0.f ? 0.f : vs / L;
-        __nv_bfloat16* out = p.out + orow * p.ldo + static_cast<long long>(hq) * D;
+        __nv_bfloat16* out = p.out + orow * p.ldo + static_cast<long long>(row.hq) * D;
 #pragma unroll
         for (int e = 0; e < E; e += 2)
             *reinterpret_cast<uint32_t*>(out + lane * 2 + e * 32) =
                 pack2<false>(acc[e] * f, acc[e + 1] * f);
         if (lane == 0 && p.lse)
-            p.lse[orow * p.Hq + hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+            p.lse[orow * p.Hq + row.hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
     }
 }
 
-cudaError_t launch_attn(AttnParams p, int D, bool f8, int sms, void* ws, cudaStream_t s) {
-    const int total = p.R * p.G, rows = attn_rows(total, D), tk = f8 ? 128 : 64;
-    p.row_blocks = (total + rows - 1) / rows;
+AttnPlan attn_plan(AttnParams& p, int D, bool f8, void* ws) {
+    AttnPlan plan;
+    const int total = p.R * p.G;
+    plan.rows = attn_rows(total);
+    plan.tk = attn_tile(plan.rows, D, f8);
+    p.gb = p.G < plan.rows ? p.G : plan.rows;
+    p.tb = plan.rows / p.gb < p.R ? plan.rows / p.gb : p.R;
+    p.blocks_g = (p.G + p.gb - 1) / p.gb;
+    p.row_blocks = p.blocks_g * ((p.R + p.tb - 1) / p.tb);
     p.groups = p.Hkv * p.row_blocks;
     p.base = static_cast<long long*>(ws);
     p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
                                          align256((static_cast<size_t>(p.B) + 1) * sizeof(long long)));
     // at most one CTA per tile that the table could hold
     const long long cap = static_cast<long long>(p.max_blocks) * p.page_size;
-    const long long units = static_cast<long long>(p.B) * p.groups * ((cap + tk - 1) / tk);
-    int grid = attn_grid_cap(D);
-    if (units < grid) grid = static_cast<int>(units < 1 ? 1 : units);
-    cudaError_t e = D == 64    ? launch_attn_d64(p, f8, rows, &grid, sms, s)
-                    : D == 128 ? launch_attn_d128(p, f8, rows, &grid, sms, s)
-                               : launch_attn_d256(p, f8, rows, &grid, sms, s);
+    const long long units = static_cast<long long>(p.B) * p.groups * ((cap + plan.tk - 1) / plan.tk);
+    plan.grid = attn_grid_cap(D);
+    if (units < plan.grid) plan.grid = static_cast<int>(units < 1 ? 1 : units);
+    plan.box_rows = p.page_size < plan.tk ? p.page_size : plan.tk;
+    const int key = D * (f8 ? 1 : 2);
+    const bool raw = f8 && plan.rows > 16;  // converted on the way: whole keys, unswizzled
+    plan.box_bytes = raw || key < 128 ? key : 128;
+    plan.swizzle = raw ? CU_TENSOR_MAP_SWIZZLE_NONE
+                       : (key == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+    return plan;
+}
+
+cudaError_t launch_attn(const AttnParams& p, const AttnMaps& maps, AttnPlan plan, int D, bool f8,
+                        int sms, cudaStream_t s) {
+    const int rows = plan.rows, tk = plan.tk;
+    int grid = plan.grid;
+    cudaError_t e = D == 64    ? launch_attn_d64(p, maps, f8, rows, &grid, sms, s)
+                    : D == 128 ? launch_attn_d128(p, maps, f8, rows, &grid, sms, s)
+                               : launch_attn_d256(p, maps, f8, rows, &grid, sms, s);
     if (e != cudaSuccess) return e;
     // about eight blocks an SM; a warp takes a row at a time
-    const int items = p.B * p.groups, used = total < rows ? total : rows;
+    const int items = p.B * p.groups, used = p.tb * p.gb;
     int chunk = static_cast<int>((static_cast<long long>(items) * used + 8 * sms - 1) / (8 * sms));
     chunk = chunk < 4 ? 4 : (chunk > used ? used : chunk);
     cudaLaunchConfig_t cfg{};

@@ -1,6 +1,8 @@
 // attn.cuh -- attention of the verify rows over a paged key-value cache: the
-// work schedule, and the kernel as a template over the head size, the cache
-// type and the warp layout (instantiated per head size in attn_d*.cu).
+// work schedule, the page loads, and the kernel for up to 16 query rows of a
+// key head (plain decoding and narrow verify batches) as a template over the
+// head size and the cache type, instantiated per head size in attn_d*.cu.
+// More rows: attn_tc.cuh.
 //
 // Mathematics.  Sequence b's R new tokens sit at positions p_i = len - R + i.
 // The R * G query rows (G query heads to a key head) that read the same keys
@@ -72,18 +74,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 #ifdef __CUDACC__
 // ------------------------------------------------------------ primitives
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;"); }
-// all but the newest `newer` groups of this thread have landed
-__device__ __forceinline__ void cp_async_wait(int newer) {
-    if (newer >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
-    else if (newer == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (newer == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
@@ -122,83 +112,67 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t b) {
     return r;
 }
 
-// ---------------------------------------------------------------- layout
-// TK keys of K and of V are one ring stage.  Rows of RB bytes are kept in
-// 16-byte chunks whose index is exclusive-ored with the row, so that the 8
-// rows of a matrix load fall into different banks.
-template <int D, bool F8, int WR, int WK>
-struct AttnShape {
-    static constexpr int kWarps = WR * WK;
-    static constexpr int kThreads = kWarps * 32;
-    static constexpr int kTK = F8 ? 128 : 64;
-    static constexpr int kRows = 16 * WR;            // query rows of an item
-    static constexpr int kRB = D * (F8 ? 1 : 2);     // bytes of a key
-    static constexpr int kCH = kRB / 16;             // 16-byte chunks of a key
-    static constexpr int kTile = kTK * kRB;          // 128 D bytes
-    static constexpr int kStage = 2 * kTile;         // K then V
-    static constexpr int kQ = kRows * D * 2;         // bf16 queries (f16 for an e4m3 cache)
-    static constexpr int kKW = kTK / WK;             // keys of a tile per warp
-    static constexpr int kSB = kKW < 32 ? kKW : 32;  // keys per softmax step
-    static constexpr int kStages =
-        D == 256 ? (WR >= 4 ? 2 : 3) : (D == 128 && WR < 8 ? (WR == 4 ? 2 : 3) : 4);
-    static constexpr int kOffQ = kStages * kStage;
-    static constexpr int kOffML = kOffQ + 2 * kQ;              // float m, l [WK][rows]
-    static constexpr int kOffRS = kOffML + 2 * WK * kRows * 4;  // float row scale [2][rows]
-    static constexpr int kOffDesc = kOffRS + 2 * kRows * 4;
-    static constexpr int kSmem = kOffDesc + kStages * 64 + 64;
-    static_assert(WK == 1 || WK * kRows * D * 4 <= kStage, "the merge uses a consumed stage");
-    static_assert(kSmem <= 227 * 1024, "shared memory");
-};
 
-__device__ __forceinline__ uint32_t swz(int row, int chunk, int rb) {
-    // 64-byte rows: two rows share a 128-byte line
-    const int x = rb == 64 ? ((row >> 1) & 3) : (row & 7);
-    return static_cast<uint32_t>(row * rb + ((chunk ^ x) << 4));
+// ------------------------------------------------------- units and pages
+constexpr int kUnitFirst = 1;  // first / last tile of this CTA's part of an item
+constexpr int kUnitLast = 2;
+constexpr int kUnitEdge = 4;   // some row does not see some key of the tile
+
+struct AttnUnit {  // what a tile is, from the producer to the other warps
+    int b, g, start, len;
+    int p0, flags;
+    int slot;  // partial slot of the item's part, or -1: written directly
+    int seg;   // part number within the CTA
+};
+constexpr int kUnitRing = 16;
+
+// the rows of block rb of key head h: row r is verify index i, query head hq
+struct AttnRow {
+    int i, hq;
+    bool live;
+};
+__device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int g, int r) {
+    const int h = g / p.row_blocks, rb = g - h * p.row_blocks;
+    const int bt = rb / p.blocks_g, bg = rb - bt * p.blocks_g;
+    const int t = r / p.gb, q = r - t * p.gb;
+    AttnRow a;
+    a.i = bt * p.tb + t;
+    const int gq = bg * p.gb + q;
+    a.hq = h * p.G + gq;
+    a.live = t < p.tb && a.i < p.R && gq < p.G;
+    return a;
 }
-
-struct AttnTile {  // what a ring stage holds
-    int b, g, start;      // sequence, (key head, row block), first key
-    int len, p0;
-    int seg;              // segment of this CTA's units (query slot: seg & 1)
-    int flags;
-    int slot;             // partial slot, or -1: written directly
-};
-constexpr int kTileFirst = 1, kTileLast = 2;
 
 __device__ __forceinline__ bool key_seen(int j, int p, int window, int sinks) {
     return j <= p && (window == 0 || j > p - window || j < sinks);
 }
+// seen by some row of the sequence / by every row (j < len)
+__device__ __forceinline__ bool key_some(int j, int len, int p0, int window, int sinks) {
+    return j < len && (window == 0 || j > p0 - window || j < sinks);
+}
+__device__ __forceinline__ bool key_all(int j, int len, int p0, int window, int sinks) {
+    return j <= p0 && (window == 0 || j > len - 1 - window || j < sinks);
+}
 
-// ---------------------------------------------------------------- kernel
-template <int D, bool F8, int WR, int WK, int MINB>
-__global__ void __launch_bounds__(AttnShape<D, F8, WR, WK>::kThreads, MINB)
-    attn_kernel(const AttnParams p) {
-    using S = AttnShape<D, F8, WR, WK>;
-    constexpr int NT = S::kThreads, TK = S::kTK;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ long long s_scan[S::kWarps];
+// Where this CTA's units begin, by a scan over the sequences' unit counts; CTA
+// 0 leaves the scan for the join kernel.  All threads of the block call it.
+struct AttnSpan {
+    long long u0, u1, base;  // units; those before sequence b
+    int b;
+};
+template <int NT>
+__device__ __forceinline__ AttnSpan attn_span(const AttnParams& p, int cap, int tk) {
+    __shared__ long long s_scan[NT / 32];
     __shared__ long long s_base;
     __shared__ int s_b;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int wr = warp % WR, wk = warp / WR;
-    const uint32_t sm = smem_u32(smem);
-    float* s_m = reinterpret_cast<float*>(smem + S::kOffML);
-    float* s_l = s_m + WK * S::kRows;
-    float* s_rs = reinterpret_cast<float*>(smem + S::kOffRS);
-    AttnTile* s_desc = reinterpret_cast<AttnTile*>(smem + S::kOffDesc);
-
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    // where this CTA's units begin: a scan over the sequences' unit counts
-    const int cap = p.max_blocks * p.page_size;
     const int per = (p.B + NT - 1) / NT;
     long long mine = 0;
     for (int k = 0; k < per; ++k) {
         const int b = tid * per + k;
         if (b < p.B)
             mine += static_cast<long long>(
-                        attn_seq(p.seq_lens[b], cap, p.R, p.window, p.sinks, TK).nt) * p.groups;
+                        attn_seq(p.seq_lens[b], cap, p.R, p.window, p.sinks, tk).nt) * p.groups;
     }
     long long incl = mine;
 #pragma unroll
@@ -208,172 +182,287 @@ __global__ void __launch_bounds__(AttnShape<D, F8, WR, WK>::kThreads, MINB)
     }
     if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
-    long long T = 0, before = 0;
+    long long T = 0, at = incl - mine;  // units before this thread's sequences
 #pragma unroll
-    for (int w = 0; w < S::kWarps; ++w) {
-        if (w < warp) before += s_scan[w];
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) at += s_scan[w];
         T += s_scan[w];
     }
     const int G = attn_ctas(T, static_cast<int>(gridDim.x)), cta = static_cast<int>(blockIdx.x);
-    const long long u0 = cta < G ? attn_unit(T, G, cta) : T;
-    const long long u1 = cta < G ? attn_unit(T, G, cta + 1) : T;
-    {
-        long long at = before + incl - mine;  // units before this thread's sequences
-        if (blockIdx.x == 0 || (u0 >= at && u0 < at + mine)) {
-            for (int k = 0; k < per; ++k) {
-                const int b = tid * per + k;
-                if (b >= p.B) break;
-                const long long n =
-                    static_cast<long long>(
-                        attn_seq(p.seq_lens[b], cap, p.R, p.window, p.sinks, TK).nt) * p.groups;
-                if (blockIdx.x == 0) p.base[b] = at;  // for the combine kernel
-                if (u0 >= at && u0 < at + n) {
-                    s_b = b;
-                    s_base = at;
-                }
-                at += n;
+    AttnSpan r;
+    r.u0 = cta < G ? attn_unit(T, G, cta) : T;
+    r.u1 = cta < G ? attn_unit(T, G, cta + 1) : T;
+    if (cta == 0 || (r.u0 >= at && r.u0 < at + mine)) {
+        for (int k = 0; k < per; ++k) {
+            const int b = tid * per + k;
+            if (b >= p.B) break;
+            const long long n = static_cast<long long>(
+                attn_seq(p.seq_lens[b], cap, p.R, p.window, p.sinks, tk).nt) * p.groups;
+            if (cta == 0) p.base[b] = at;
+            if (r.u0 >= at && r.u0 < at + n) {
+                s_b = b;
+                s_base = at;
             }
+            at += n;
         }
-        if (blockIdx.x == 0 && tid == 0) p.base[p.B] = T;
     }
+    if (cta == 0 && tid == 0) p.base[p.B] = T;
     __syncthreads();
-    if (u0 >= u1) return;
+    r.b = s_b;
+    r.base = s_base;
+    return r;
+}
 
-    // ---- load cursor (the same in every thread)
-    int lb = s_b, lg, lt;
-    AttnSeq ls = attn_seq(p.seq_lens[lb], cap, p.R, p.window, p.sinks, TK);
-    if (p.seq_lens[lb] > cap && tid == 0) atomicOr(p.status, kStatusBadPage);
-    {
-        const long long r = u0 - s_base;
-        lg = static_cast<int>(r / ls.nt);
-        lt = static_cast<int>(r - static_cast<long long>(lg) * ls.nt);
-    }
-    const int n_units = static_cast<int>(u1 - u0);
-    int loaded = 0, l_seg = -1;
-    const int ps_shift = p.page_shift;
-    // lane l keeps the page of keys start + 8 l .. + 7 of the next tile to load
-    auto fetch_pages = [&]() {
-        const int t = lt < ls.ns ? lt : lt + ls.skip;
-        const int j = t * TK + lane * 8;
-        int pg = -1;
-        if (lane < TK / 8 && j < ls.len) {
-            pg = __ldg(p.table + static_cast<long long>(lb) * p.table_stride + (j >> ps_shift));
-            // pages that no row sees may hold any id; key_seen decides below
-            if (pg < 0 || pg >= p.num_pages) pg = -1;
-        }
-        return pg;
-    };
-    int pages = fetch_pages();
-
-    auto issue = [&]() {
-        const int st = loaded % S::kStages;
-        const int t = lt < ls.ns ? lt : lt + ls.skip;
-        const int start = t * TK;
-        const int rb = lg % p.row_blocks, h = lg / p.row_blocks;
-        const bool first = loaded == 0 || lt == 0;
-        const bool last = loaded == n_units - 1 || lt == ls.nt - 1;
-        if (first) ++l_seg;
-        if (tid == 0) {
-            AttnTile d;
-            d.b = lb;
-            d.g = lg;
-            d.start = start;
-            d.len = ls.len;
-            d.p0 = ls.p0;
-            d.seg = l_seg;
-            d.flags = (first ? kTileFirst : 0) | (last ? kTileLast : 0);
-            // a segment that does not begin with the item's first tile is the CTA's first;
-            // one that does not end with its last tile is the CTA's last
-            const bool cut_front = loaded - lt < 0;  // tile 0 lies before this CTA's units
-            const bool cut_back = lt != ls.nt - 1;   // (read for the last tile of the segment)
-            d.slot = cut_front ? 2 * cta : (cut_back ? 2 * cta + 1 : -1);
-            s_desc[st] = d;
-        }
-        const uint8_t* kb = static_cast<const uint8_t*>(p.k);
-        const uint8_t* vb = static_cast<const uint8_t*>(p.v);
-        const uint32_t dst = sm + st * S::kStage;
-        bool bad = false;
-#pragma unroll 4
-        for (int i = 0; i < TK * S::kCH / NT; ++i) {
-            const int c = tid + i * NT;
-            const int row = c / S::kCH, col = c % S::kCH;
-            const int pg = __shfl_sync(0xffffffffu, pages, row >> 3);
-            const int j = start + row;
-            // keys that no row sees are zeros, whatever the cache holds there
-            bool ok = j < ls.len && (p.window == 0 || j > ls.p0 - p.window || j < p.sinks);
-            if (ok && pg < 0) {
-                bad = true;
-                ok = false;
-            }
-            const long long off =
-                ok ? (static_cast<long long>(pg) * p.page_stride +
-                      static_cast<long long>(j & (p.page_size - 1)) * p.token_stride +
-                      static_cast<long long>(h) * p.head_stride) * (F8 ? 1 : 2) + col * 16
-                   : 0;
-            const uint32_t a = dst + swz(row, col, S::kRB);
-            cp_async16(a, kb + off, ok ? 16 : 0);
-            cp_async16(a + S::kTile, vb + off, ok ? 16 : 0);
-        }
-        if (bad) atomicOr(p.status, kStatusBadPage);
-        if (first) {
-            const uint32_t qd = sm + S::kOffQ + (l_seg & 1) * S::kQ;
-            constexpr int QC = D / 8;
-            for (int c = tid; c < S::kRows * QC; c += NT) {
-                const int r = c / QC, col = c % QC;
-                const int row = rb * S::kRows + r;  // i * G + query head of the group
-                const bool ok = row < p.R * p.G;
-                const int i = ok ? row / p.G : 0, gq = ok ? row - i * p.G : 0;
-                const __nv_bfloat16* src = p.q + (static_cast<long long>(lb) * p.R + i) * p.ldq +
-                                           (h * p.G + gq) * D + col * 8;
-                cp_async16(qd + swz(r, col, D * 2), src, ok ? 16 : 0);
-            }
-        }
-        cp_async_commit();
-        ++loaded;
-        if (loaded < n_units) {
-            if (++lt == ls.nt) {
-                lt = 0;
-                if (++lg == p.groups) {
-                    lg = 0;
-                    do {
-                        ++lb;
-                        ls = attn_seq(p.seq_lens[lb], cap, p.R, p.window, p.sinks, TK);
-                    } while (ls.nt == 0);
-                    if (p.seq_lens[lb] > cap && tid == 0) atomicOr(p.status, kStatusBadPage);
+// The producer warp's walk over the CTA's units.  Every lane holds the walk;
+// lane l also holds the page of the l-th box of the current tile.
+template <int TK>
+struct AttnWalk {
+    int b, g, t, u, n, seg, cap;
+    AttnSeq s;
+    int box_rows, boxes;  // tokens of a page box, boxes of a tile
+    int page;             // -1: no box to load; num_pages: a bad page (reads as zeros)
+    __device__ __forceinline__ int start() const { return (t < s.ns ? t : t + s.skip) * TK; }
+    __device__ __forceinline__ void fetch(const AttnParams& p, int lane) {
+        const int lo = start() + lane * box_rows;
+        page = -1;
+        if (lane < boxes && lo < s.len) {
+            const int hi = min(lo + box_rows, s.len) - 1;
+            if (p.window == 0 || hi > s.p0 - p.window || lo < p.sinks) {
+                page = __ldg(p.table + static_cast<long long>(b) * p.table_stride +
+                             (lo >> p.page_shift));
+                if (page < 0 || page >= p.num_pages) {
+                    page = p.num_pages;
+                    atomicOr(p.status, kStatusBadPage);
                 }
             }
-            pages = fetch_pages();
         }
+    }
+    __device__ __forceinline__ void enter(const AttnParams& p, int lane) {
+        const int raw = p.seq_lens[b];
+        s = attn_seq(raw, cap, p.R, p.window, p.sinks, TK);
+        if (raw > cap && lane == 0) atomicOr(p.status, kStatusBadPage);
+    }
+    __device__ __forceinline__ void begin(const AttnParams& p, const AttnSpan& w, int cap_, int lane) {
+        cap = cap_;
+        b = w.b;
+        u = 0;
+        n = static_cast<int>(w.u1 - w.u0);
+        seg = 0;
+        box_rows = p.page_size < TK ? p.page_size : TK;
+        boxes = TK / box_rows;
+        enter(p, lane);
+        const long long r = w.u0 - w.base;
+        g = static_cast<int>(r / s.nt);
+        t = static_cast<int>(r - static_cast<long long>(g) * s.nt);
+        fetch(p, lane);
+    }
+    __device__ __forceinline__ AttnUnit unit(const AttnParams& p) const {
+        AttnUnit d;
+        d.b = b;
+        d.g = g;
+        d.start = start();
+        d.len = s.len;
+        d.p0 = s.p0;
+        const bool edge = d.start + TK > s.p0 + 1 ||
+                          (p.window > 0 && d.start <= s.len - 1 - p.window && d.start + TK > p.sinks);
+        d.flags = (u == 0 || t == 0 ? kUnitFirst : 0) |
+                  (u == n - 1 || t == s.nt - 1 ? kUnitLast : 0) | (edge ? kUnitEdge : 0);
+        // a part that does not begin with the item's first tile is the CTA's first; one
+        // that does not end with its last tile (read for a part's last unit) is the last
+        const int cta = static_cast<int>(blockIdx.x);
+        d.slot = u - t < 0 ? 2 * cta : (t != s.nt - 1 ? 2 * cta + 1 : -1);
+        d.seg = seg;
+        return d;
+    }
+    // to the next unit (not past the last)
+    __device__ __forceinline__ void next(const AttnParams& p, int lane) {
+        ++u;
+        if (++t == s.nt) {
+            t = 0;
+            ++seg;
+            if (++g == p.groups) {
+                g = 0;
+                do {
+                    ++b;
+                    enter(p, lane);
+                } while (s.nt == 0);
+            }
+        }
+        fetch(p, lane);
+    }
+    // Bytes of the current tile's boxes of K (or V): NBLK blocks of BOXB bytes of a key.
+    template <int NBLK, int BOXB>
+    __device__ __forceinline__ uint32_t bytes() const {
+        return __popc(__ballot_sync(0xffffffffu, page >= 0)) *
+               static_cast<uint32_t>(box_rows * NBLK * BOXB);
+    }
+    // Loads them: block k at dst + k * TK * BOXB, a row of BOXB bytes a key.
+    template <int NBLK, int BOXB, int ESZ>
+    __device__ __forceinline__ void load(const AttnParams& p, const CUtensorMap* map, uint32_t dst,
+                                         uint64_t* bar, int lane) const {
+        const int token = start() & (p.page_size - 1);  // 0 unless a page holds several tiles
+        if (page >= 0) {
+#pragma unroll
+            for (int k = 0; k < NBLK; ++k)
+                tma_load_4d(dst + k * (TK * BOXB) + lane * box_rows * BOXB, map, k * (BOXB / ESZ),
+                            g / p.row_blocks, token, page, bar);
+        }
+        __syncwarp();
+    }
+};
+
+// The queries of an item's row block: a box of tb tokens x gb heads x 64
+// dimensions a block, so that row r is token r / gb, head r % gb.
+__device__ __forceinline__ uint32_t attn_q_bytes(const AttnParams& p, int D) {
+    return static_cast<uint32_t>(p.tb * p.gb * D * 2);
+}
+template <int D>
+__device__ __forceinline__ void attn_load_q(const AttnParams& p, const CUtensorMap* map, uint32_t dst,
+                                            int block, const AttnUnit& d, uint64_t* bar) {
+    const int h = d.g / p.row_blocks, rb = d.g - h * p.row_blocks;
+    const int bt = rb / p.blocks_g, bg = rb - bt * p.blocks_g;
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+        tma_load_3d(dst + k * block, map, k * 64, h * p.G + bg * p.gb, d.b * p.R + bt * p.tb, bar);
+}
+
+// ------------------------------------------------------- up to 16 query rows
+// Four warps share the 16 rows and take a quarter of a tile's keys each, so
+// every key and value byte is read from shared memory once; a fifth warp loads
+// (TMA, a box per page and 128 bytes of a key) into a ring.  The warps' running
+// maxima, sums and outputs are joined at the end of an item's part.
+template <int D, bool F8>
+struct AttnShape {
+    static constexpr int kWarps = 4;
+    static constexpr int kThreads = (kWarps + 1) * 32;
+    static constexpr int kTK = F8 ? 128 : 64;
+    static constexpr int kRows = 16;
+    static constexpr int kRB = D * (F8 ? 1 : 2);         // bytes of a key
+    static constexpr int kBoxB = kRB < 128 ? kRB : 128;  // of them in a box
+    static constexpr int kNBlk = kRB / kBoxB;
+    static constexpr int kCPB = kBoxB / 16;
+    static constexpr int kBlk = kTK * kBoxB;
+    static constexpr int kTile = kTK * kRB;              // 128 D bytes
+    static constexpr int kStage = 2 * kTile;             // K then V
+    static constexpr int kQ = kRows * D * 2;
+    static constexpr int kQBlk = kRows * 128;
+    static constexpr int kKW = kTK / kWarps;             // keys of a tile per warp
+    static constexpr int kStages = D == 256 ? 3 : (D == 128 ? 3 : 4);
+    static constexpr int kOffQ = kStages * kStage;
+    static constexpr int kOffML = kOffQ + 2 * kQ;                  // float m, l [4][16]
+    static constexpr int kOffRS = kOffML + 2 * kWarps * kRows * 4;  // float row scale [2][16]
+    static constexpr int kSmem = kOffRS + 2 * kRows * 4 + 1024;
+    static_assert(kWarps * kRows * D * 4 <= kStage, "the join of the warps uses a consumed stage");
+    static_assert(kSmem <= 225 * 1024, "shared memory");
+    __device__ static __forceinline__ uint32_t at(int row, int chunk) {  // chunk of 16 bytes of a key
+        const int x = kBoxB == 64 ? (row >> 1) & 3 : row & 7;
+        return static_cast<uint32_t>(chunk / kCPB * kBlk + row * kBoxB + (((chunk % kCPB) ^ x) << 4));
+    }
+    __device__ static __forceinline__ uint32_t q_at(int row, int chunk) {  // 16 bytes of a query
+        return static_cast<uint32_t>((chunk >> 3) * kQBlk + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+    }
+};
+
+template <int D, bool F8, int MINB>
+__global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
+    attn_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps) {
+    using S = AttnShape<D, F8>;
+    constexpr int TK = S::kTK, NST = S::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ __align__(8) uint64_t b_full[NST], b_empty[NST], b_qe[2], b_sync;
+    __shared__ AttnUnit s_unit[kUnitRing];
+    __shared__ volatile int s_abort;
+    const int tid = threadIdx.x, lane = tid & 31, wk = tid >> 5;
+    const uint32_t sm = smem_u32(smem);
+    float* s_m = reinterpret_cast<float*>(smem + S::kOffML);
+    float* s_l = s_m + S::kWarps * S::kRows;
+    float* s_rs = reinterpret_cast<float*>(smem + S::kOffRS);
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 0) {
+        for (int k = 0; k < NST; ++k) {
+            mbar_init(&b_full[k], 1);
+            mbar_init(&b_empty[k], S::kWarps);
+        }
+        mbar_init(&b_qe[0], S::kWarps);
+        mbar_init(&b_qe[1], S::kWarps);
+        mbar_init(&b_sync, S::kWarps);
+        fence_barrier_init();
+        s_abort = 0;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int cap = p.max_blocks * p.page_size;
+    const AttnSpan span = attn_span<S::kThreads>(p, cap, TK);
+    const int n_units = static_cast<int>(span.u1 - span.u0);
+    if (n_units == 0) return;
+    // the same answer in every lane: what follows is executed by whole warps
+    auto wait = [&](uint64_t* bar, int phase) {
+        const bool ok = mbar_wait_bounded(bar, phase & 1, p.wait_ns, &s_abort);
+        if (!ok) {
+            s_abort = 1;
+            atomicOr(p.status, kStatusWaitTimeout);
+        }
+        return __all_sync(0xffffffffu, ok) != 0;
     };
+
+    if (wk == S::kWarps) {
+        // -------------------------------------------------------- producer
+        AttnWalk<TK> w;
+        w.begin(p, span, cap, lane);
+        int u = 0;
+        for (; u < n_units; ++u) {
+            const int st = u % NST;
+            const AttnUnit d = w.unit(p);
+            if (u >= NST && !wait(&b_empty[st], u / NST - 1)) break;
+            const bool first = d.flags & kUnitFirst;
+            if (first && d.seg >= 2 && !wait(&b_qe[d.seg & 1], (d.seg >> 1) - 1)) break;
+            const uint32_t kv = 2 * w.template bytes<S::kNBlk, S::kBoxB>();
+            if (lane == 0) {
+                s_unit[u % kUnitRing] = d;
+                mbar_arrive_expect_tx(&b_full[st], kv + (first ? attn_q_bytes(p, D) : 0u));
+                if (first)
+                    attn_load_q<D>(p, &maps.q, sm + S::kOffQ + (d.seg & 1) * S::kQ, S::kQBlk, d,
+                                   &b_full[st]);
+            }
+            __syncwarp();
+            const uint32_t dst = sm + st * S::kStage;
+            w.template load<S::kNBlk, S::kBoxB, F8 ? 1 : 2>(p, &maps.k, dst, &b_full[st], lane);
+            w.template load<S::kNBlk, S::kBoxB, F8 ? 1 : 2>(p, &maps.v, dst + S::kTile, &b_full[st],
+                                                            lane);
+            if (u + 1 < n_units) w.next(p, lane);
+        }
+        // copies in flight land before the block ends
+        if (u < n_units) {
+            for (int k = u > NST ? u - NST : 0; k < u; ++k)
+                mbar_wait_bounded(&b_full[k % NST], (k / NST) & 1, p.wait_ns, nullptr);
+        }
+        return;
+    }
 
     // ---- compute state
     float o[D / 8][4];
     float m[2], l[2], c2[2];
-    int pr[2];   // positions of this thread's two rows (-1: no such row)
-    int vi[2];   // their verify indexes
-    const int r0 = wr * 16 + (lane >> 2);
-    const int t4 = lane & 3;
+    int pr[2];   // positions of this thread's two rows (below 0: sees nothing)
+    AttnRow ar[2];
+    const int r0 = lane >> 2, t4 = lane & 3;
     // ldmatrix lane addresses: (row, chunk) of the 8x8 matrices, see each use
     const int lm = lane >> 3, lr = lane & 7;
+    int syncs = 0;
+    auto warps_sync = [&] {  // the four warps (a wait with a limit, like every other)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_sync);
+        return wait(&b_sync, syncs++);
+    };
 
     for (int done = 0; done < n_units; ++done) {
-        // every warp is past the tile whose stage the loads below overwrite
-        __syncthreads();
-        while (loaded < n_units && loaded < done + S::kStages) {
-            // two query slots: a segment's queries replace those of the segment before
-            // the last loaded one, which must be finished
-            if (loaded > done && lt == 0 && l_seg >= 1 && s_desc[done % S::kStages].seg < l_seg)
-                break;
-            issue();
-        }
-        cp_async_wait(loaded - done - 1);
-        __syncthreads();
-        const int st = done % S::kStages;
-        const AttnTile td = s_desc[st];
-        const int rb = td.g % p.row_blocks, h = td.g / p.row_blocks;
+        const int st = done % NST;
+        if (!wait(&b_full[st], done / NST)) break;
+        const AttnUnit td = s_unit[done % kUnitRing];
+        const int h = td.g / p.row_blocks;
         const int qslot = td.seg & 1;
         const uint32_t qs = sm + S::kOffQ + qslot * S::kQ;
-        if (td.flags & kTileFirst) {
+        if (td.flags & kUnitFirst) {
 #pragma unroll
             for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
             const float ks = F8 && p.k_scale ? __ldg(p.k_scale + h) : 1.f;
@@ -382,7 +471,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, WR, WK>::kThreads, MINB)
                 // row's largest magnitude into [2^14, 2^15): exact for every value down
                 // to 2^-31 of it (bf16 has 8 significant bits, f16 11 and subnormals).
                 // Within 16 dimensions the order is that of the byte loads of K below.
-                for (int r = warp; r < S::kRows; r += S::kWarps) {
+                for (int r = wk; r < S::kRows; r += S::kWarps) {
                     uint32_t* row = reinterpret_cast<uint32_t*>(smem + S::kOffQ + qslot * S::kQ);
                     float v[D / 32];
                     uint32_t x[D / 64];
@@ -390,7 +479,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, WR, WK>::kThreads, MINB)
 #pragma unroll
                     for (int k = 0; k < D / 64; ++k) {
                         const int e = lane + 32 * k;  // pair of dimensions 2e, 2e + 1
-                        x[k] = row[(swz(r, e >> 2, D * 2) >> 2) + (e & 3)];
+                        x[k] = row[(S::q_at(r, e >> 2) >> 2) + (e & 3)];
                         v[2 * k] = __uint_as_float(x[k] << 16);
                         v[2 * k + 1] = __uint_as_float(x[k] & 0xffff0000u);
                         mx = fmaxf(mx, fmaxf(fabsf(v[2 * k]), fabsf(v[2 * k + 1])));
@@ -411,46 +500,55 @@ __global__ void __launch_bounds__(AttnShape<D, F8, WR, WK>::kThreads, MINB)
                         const int e = lane + 32 * k;
                         // pair (4t, 4t+1) -> stored pair t, (4t+2, 4t+3) -> stored pair t + 4
                         const int w = e & 7, s = (e & ~7) + (w >> 1) + (w & 1) * 4;
-                        row[(swz(r, s >> 2, D * 2) >> 2) + (s & 3)] =
+                        row[(S::q_at(r, s >> 2) >> 2) + (s & 3)] =
                             pack2<true>(v[2 * k] * up, v[2 * k + 1] * up);
                     }
                 }
-                __syncthreads();
+                fence_async_smem();  // (a later load will write there)
+                if (!warps_sync()) break;
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 m[k] = -INFINITY;
                 l[k] = 0.f;
-                const int row = rb * S::kRows + r0 + 8 * k;
-                vi[k] = row / p.G;
-                pr[k] = row < p.R * p.G ? td.p0 + vi[k] : -1;
+                ar[k] = attn_row(p, td.g, r0 + 8 * k);
+                pr[k] = ar[k].live ? td.p0 + ar[k].i : -1;
                 c2[k] = p.scale * kLog2e * ks;
                 if (F8) c2[k] *= s_rs[qslot * S::kRows + r0 + 8 * k];
             }
         }
-        // keys that some row of the sequence does not see
-        const bool edge = td.start + TK > td.p0 + 1 ||
-                          (p.window > 0 && td.start <= td.len - 1 - p.window &&
-                           td.start + TK > p.sinks);
+        const bool edge = td.flags & kUnitEdge;
         const uint32_t kS = sm + st * S::kStage, vS = kS + S::kTile;
-
+        if (edge) {
+            // values that no row sees are made zeros, whatever the cache holds there (0
+            // times an infinity would not be 0); each warp cleans its own keys
 #pragma unroll 1
-        for (int sb = 0; sb < S::kKW; sb += S::kSB) {
-            const int k0 = wk * S::kKW + sb;   // first key of the step within the tile
-            if (td.start + k0 >= td.len) break;  // (uniform) nothing of the sequence left
-            float s[S::kSB / 8][4];
+            for (int c = lane; c < S::kKW * (S::kRB / 16); c += 32) {
+                const int row = wk * S::kKW + c / (S::kRB / 16);
+                if (!key_some(td.start + row, td.len, td.p0, p.window, p.sinks))
+                    *reinterpret_cast<uint4*>(smem + st * S::kStage + S::kTile +
+                                              S::at(row, c % (S::kRB / 16))) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+            __syncwarp();
+        }
+
+        const int k0 = wk * S::kKW;            // this warp's first key of the tile
+        const int j0 = td.start + k0, j1 = min(j0 + S::kKW, td.len) - 1;
+        // (the same for the warp) some row sees some of them
+        if (j1 >= j0 && (p.window == 0 || j1 > td.p0 - p.window || j0 < p.sinks)) {
+            float s[S::kKW / 8][4];
 #pragma unroll
-            for (int n = 0; n < S::kSB / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            for (int n = 0; n < S::kKW / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
             if (!F8) {
 #pragma unroll 4
                 for (int ks = 0; ks < D / 16; ++ks) {
                     uint32_t a[4];
-                    ldsm4(a, qs + swz(wr * 16 + lr + (lm & 1) * 8, ks * 2 + (lm >> 1), D * 2));
+                    ldsm4(a, qs + S::q_at(lr + (lm & 1) * 8, ks * 2 + (lm >> 1)));
 #pragma unroll
-                    for (int n = 0; n < S::kSB / 16; ++n) {
+                    for (int n = 0; n < S::kKW / 16; ++n) {
                         uint32_t bk[4];
-                        ldsm4(bk, kS + swz(k0 + n * 16 + lr + (lm >> 1) * 8, ks * 2 + (lm & 1),
-                                           S::kRB));
+                        ldsm4(bk, kS + S::at(k0 + n * 16 + lr + (lm >> 1) * 8, ks * 2 + (lm & 1)));
                         mma16816<false>(s[2 * n], a, bk[0], bk[1]);
                         mma16816<false>(s[2 * n + 1], a, bk[2], bk[3]);
                     }
@@ -461,14 +559,13 @@ __global__ void __launch_bounds__(AttnShape<D, F8, WR, WK>::kThreads, MINB)
 #pragma unroll 2
                 for (int ks = 0; ks < D / 32; ++ks) {
                     uint32_t a[2][4];
-                    ldsm4(a[0], qs + swz(wr * 16 + lr + (lm & 1) * 8, ks * 4 + (lm >> 1), D * 2));
+                    ldsm4(a[0], qs + S::q_at(lr + (lm & 1) * 8, ks * 4 + (lm >> 1)));
                     ldsm4(a[1],
-                          qs + swz(wr * 16 + lr + (lm & 1) * 8, ks * 4 + 2 + (lm >> 1), D * 2));
+                          qs + S::q_at(lr + (lm & 1) * 8, ks * 4 + 2 + (lm >> 1)));
 #pragma unroll
-                    for (int n = 0; n < S::kSB / 16; ++n) {
+                    for (int n = 0; n < S::kKW / 16; ++n) {
                         uint32_t bk[4];
-                        ldsm4(bk, kS + swz(k0 + n * 16 + lr + (lm >> 1) * 8, ks * 2 + (lm & 1),
-                                           S::kRB));
+                        ldsm4(bk, kS + S::at(k0 + n * 16 + lr + (lm >> 1) * 8, ks * 2 + (lm & 1)));
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             mma16816<true>(s[2 * n], a[e], e4m3x2_f16x2(bk[e]),
@@ -481,7 +578,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, WR, WK>::kThreads, MINB)
             }
             if (edge) {
 #pragma unroll
-                for (int n = 0; n < S::kSB / 8; ++n)
+                for (int n = 0; n < S::kKW / 8; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int j = td.start + k0 + n * 8 + t4 * 2 + (e & 1);
@@ -495,7 +592,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, WR, WK>::kThreads, MINB)
             for (int k = 0; k < 2; ++k) {
                 float mx = -INFINITY;
 #pragma unroll
-                for (int n = 0; n < S::kSB / 8; ++n)
+                for (int n = 0; n < S::kKW / 8; ++n)
                     mx = fmaxf(mx, fmaxf(s[n][2 * k], s[n][2 * k + 1]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -506,7 +603,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, WR, WK>::kThreads, MINB)
                 const float mc = mn == -INFINITY ? 0.f : mn * c2[k];
                 float sum = 0.f;
 #pragma unroll
-                for (int n = 0; n < S::kSB / 8; ++n) {
+                for (int n = 0; n < S::kKW / 8; ++n) {
                     s[n][2 * k] = ex2(fmaf(s[n][2 * k], c2[k], -mc));
                     s[n][2 * k + 1] = ex2(fmaf(s[n][2 * k + 1], c2[k], -mc));
                     sum += s[n][2 * k] + s[n][2 * k + 1];
@@ -529,11 +626,11 @@ __global__ void __launch_bounds__(AttnShape<D, F8, WR, WK>::kThreads, MINB)
                 // bv: operand registers of two 8-column blocks, keys (2t, 2t+1) and + 8 each
                 const int row = k0 + n * 16 + lr + (lm & 1) * 8;
                 if (!F8) {
-                    ldsm4t(bv, vS + swz(row, db * 2 + (lm >> 1), S::kRB));
+                    ldsm4t(bv, vS + S::at(row, db * 2 + (lm >> 1)));
                     return;
                 }
                 uint32_t x[4];
-                ldsm4t(x, vS + swz(row, db * 2 + (lm >> 1), S::kRB));
+                ldsm4t(x, vS + S::at(row, db * 2 + (lm >> 1)));
                 // x: 2 keys x 2 dimensions a register; even and odd dimensions apart
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {  // dimensions 32 db + 16 q ..
@@ -549,7 +646,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, WR, WK>::kThreads, MINB)
             bool odd = false;  // an infinity or NaN among keys that some rows do not see
             if (edge) {
 #pragma unroll 1
-                for (int n = 0; n < S::kSB / 16; ++n)
+                for (int n = 0; n < S::kKW / 16; ++n)
 #pragma unroll 1
                     for (int db = 0; db < DB; ++db) {
                         uint32_t bv[VR];
@@ -562,7 +659,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, WR, WK>::kThreads, MINB)
             }
             if (!odd) {
 #pragma unroll
-                for (int n = 0; n < S::kSB / 16; ++n) {
+                for (int n = 0; n < S::kKW / 16; ++n) {
                     const uint32_t a[4] = {pack2<F8>(s[2 * n][0], s[2 * n][1]),
                                            pack2<F8>(s[2 * n][2], s[2 * n][3]),
                                            pack2<F8>(s[2 * n + 1][0], s[2 * n + 1][1]),
@@ -579,13 +676,13 @@ __global__ void __launch_bounds__(AttnShape<D, F8, WR, WK>::kThreads, MINB)
             } else {
                 // 0 times infinity must not reach a row that does not see the key: one
                 // product per verify index, its unseen values set to zero
-                const int i_lo = (rb * S::kRows + wr * 16) / p.G;
-                const int i_hi = min(p.R - 1, (rb * S::kRows + wr * 16 + 15) / p.G);
+                const int i_lo = attn_row(p, td.g, 0).i;
+                const int i_hi = min(p.R, i_lo + p.tb) - 1;
 #pragma unroll 1
                 for (int i = i_lo; i <= i_hi; ++i)
 #pragma unroll
-                    for (int n = 0; n < S::kSB / 16; ++n) {
-                        const bool a0 = vi[0] == i, a1 = vi[1] == i;
+                    for (int n = 0; n < S::kKW / 16; ++n) {
+                        const bool a0 = ar[0].live && ar[0].i == i, a1 = ar[1].live && ar[1].i == i;
                         const uint32_t a[4] = {
                             a0 ? pack2<F8>(s[2 * n][0], s[2 * n][1]) : 0u,
                             a1 ? pack2<F8>(s[2 * n][2], s[2 * n][3]) : 0u,
@@ -619,183 +716,158 @@ __global__ void __launch_bounds__(AttnShape<D, F8, WR, WK>::kThreads, MINB)
             }
         }
 
-        if (!(td.flags & kTileLast)) continue;
-        // ---- end of the segment: join the warps' key slices, write out
+        if (!(td.flags & kUnitLast)) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b_empty[st]);
+            continue;
+        }
+        // ---- end of the item's part: join the warps' keys, write out
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
             l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
         }
+        if (lane == 0) mbar_arrive(&b_qe[td.seg & 1]);
         const float vs = F8 && p.v_scale ? __ldg(p.v_scale + h) : 1.f;
         float* po = nullptr;   // partial rows [rows][D], then m [rows], l [rows]
         if (td.slot >= 0) po = p.partial + static_cast<long long>(td.slot) * S::kRows * (D + 2);
-        if (WK == 1) {
+        if (t4 == 0) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const int r = r0 + 8 * k, row = rb * S::kRows + r;
-                if (row >= p.R * p.G) continue;
-                const float mc = m[k] == -INFINITY ? -INFINITY : m[k] * c2[k];
-                const float f = td.slot >= 0 ? 1.f : (l[k] == 0.f ? 0.f : vs / l[k]);
-                const long long orow = static_cast<long long>(td.b) * p.R + vi[k];
-                const int hq = h * p.G + row - vi[k] * p.G;
-                __nv_bfloat16* out = p.out + orow * p.ldo + static_cast<long long>(hq) * D;
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    // column of element e of block n
-                    const int col = F8 ? (n >> 1) * 16 + t4 * 4 + (n & 1) : n * 8 + t4 * 2;
-                    const float x = o[n][2 * k] * f, y = o[n][2 * k + 1] * f;
-                    if (F8) {
-                        if (n & 1) continue;
-                        const float x1 = o[n + 1][2 * k] * f, y1 = o[n + 1][2 * k + 1] * f;
-                        if (td.slot >= 0)
-                            *reinterpret_cast<float4*>(po + r * D + col) = make_float4(x, x1, y, y1);
-                        else
-                            *reinterpret_cast<uint2*>(out + col) =
-                                make_uint2(pack2<false>(x, x1), pack2<false>(y, y1));
-                    } else if (td.slot >= 0) {
-                        *reinterpret_cast<float2*>(po + r * D + col) = make_float2(x, y);
-                    } else {
-                        *reinterpret_cast<uint32_t*>(out + col) = pack2<false>(x, y);
-                    }
-                }
-                if (t4 == 0) {
-                    if (td.slot >= 0) {
-                        po[S::kRows * D + r] = mc;
-                        po[S::kRows * (D + 1) + r] = l[k];
-                    } else if (p.lse) {
-                        p.lse[orow * p.Hq + hq] =
-                            l[k] == 0.f ? -INFINITY : (mc + log2f(l[k])) * kLn2;
-                    }
-                }
+                s_m[wk * S::kRows + r0 + 8 * k] = m[k] == -INFINITY ? -INFINITY : m[k] * c2[k];
+                s_l[wk * S::kRows + r0 + 8 * k] = l[k];
             }
-        } else {
-            if (t4 == 0) {
+        }
+        if (!warps_sync()) break;  // also: every warp is done with this stage
+        float* buf = reinterpret_cast<float*>(smem + st * S::kStage);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    s_m[wk * S::kRows + r0 + 8 * k] = m[k] == -INFINITY ? -INFINITY : m[k] * c2[k];
-                    s_l[wk * S::kRows + r0 + 8 * k] = l[k];
-                }
-            }
-            __syncthreads();  // also: every warp is done with this stage
-            float* buf = reinterpret_cast<float*>(smem + st * S::kStage);
+        for (int k = 0; k < 2; ++k) {
+            const int r = r0 + 8 * k;
+            float M = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int r = r0 + 8 * k;
-                float M = -INFINITY;
+            for (int w = 0; w < S::kWarps; ++w) M = fmaxf(M, s_m[w * S::kRows + r]);
+            const float f = M == -INFINITY ? 1.f : ex2(s_m[wk * S::kRows + r] - M);
+            float* row = buf + (wk * S::kRows + r) * D;
 #pragma unroll
-                for (int w = 0; w < WK; ++w) M = fmaxf(M, s_m[w * S::kRows + r]);
-                const float f = M == -INFINITY ? 1.f : ex2(s_m[wk * S::kRows + r] - M);
-                float* row = buf + (wk * S::kRows + r) * D;
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    if (F8) {
-                        if (n & 1) continue;
-                        const int col = ((n >> 1) * 16 + t4 * 4) ^ ((r & 1) << 4);
-                        *reinterpret_cast<float4*>(row + col) =
-                            make_float4(o[n][2 * k] * f, o[n + 1][2 * k] * f,
-                                        o[n][2 * k + 1] * f, o[n + 1][2 * k + 1] * f);
-                    } else {
-                        const int col = (n * 8 + t4 * 2) ^ ((r & 3) << 3);
-                        *reinterpret_cast<float2*>(row + col) =
-                            make_float2(o[n][2 * k] * f, o[n][2 * k + 1] * f);
-                    }
-                }
-            }
-            __syncthreads();
-            for (int c = tid; c < S::kRows * (D / 8); c += NT) {
-                const int r = c / (D / 8), blk = c % (D / 8);
-                const int row = rb * S::kRows + r;
-                if (row >= p.R * p.G) break;  // later chunks are of later rows
-                float M = -INFINITY, L = 0.f;
-#pragma unroll
-                for (int w = 0; w < WK; ++w) M = fmaxf(M, s_m[w * S::kRows + r]);
-#pragma unroll
-                for (int w = 0; w < WK; ++w)
-                    L += s_l[w * S::kRows + r] *
-                         (M == -INFINITY ? 1.f : ex2(s_m[w * S::kRows + r] - M));
-                float x[8] = {};
-                const int col = F8 ? (blk * 8) ^ ((r & 1) << 4) : (blk * 8) ^ ((r & 3) << 3);
-#pragma unroll
-                for (int w = 0; w < WK; ++w) {
-                    const float4* src =
-                        reinterpret_cast<const float4*>(buf + (w * S::kRows + r) * D + col);
-                    const float4 u = src[0], v = src[1];
-                    x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
-                    x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
-                }
-                const int i = row / p.G, hq = h * p.G + row - i * p.G;
-                const long long orow = static_cast<long long>(td.b) * p.R + i;
-                if (td.slot >= 0) {
-                    float4* dst = reinterpret_cast<float4*>(po + r * D + blk * 8);
-                    dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-                    dst[1] = make_float4(x[4], x[5], x[6], x[7]);
-                    if (blk == 0) {
-                        po[S::kRows * D + r] = M;
-                        po[S::kRows * (D + 1) + r] = L;
-                    }
+            for (int n = 0; n < D / 8; ++n) {
+                if (F8) {
+                    if (n & 1) continue;
+                    const int col = ((n >> 1) * 16 + t4 * 4) ^ ((r & 1) << 4);
+                    *reinterpret_cast<float4*>(row + col) =
+                        make_float4(o[n][2 * k] * f, o[n + 1][2 * k] * f, o[n][2 * k + 1] * f,
+                                    o[n + 1][2 * k + 1] * f);
                 } else {
-                    const float f = L == 0.f ? 0.f : vs / L;
-                    __nv_bfloat16* out = p.out + orow * p.ldo + static_cast<long long>(hq) * D;
-                    *reinterpret_cast<uint4*>(out + blk * 8) =
-                        make_uint4(pack2<false>(x[0] * f, x[1] * f), pack2<false>(x[2] * f, x[3] * f),
-                                   pack2<false>(x[4] * f, x[5] * f), pack2<false>(x[6] * f, x[7] * f));
-                    if (blk == 0 && p.lse)
-                        p.lse[orow * p.Hq + hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+                    const int col = (n * 8 + t4 * 2) ^ ((r & 3) << 3);
+                    *reinterpret_cast<float2*>(row + col) =
+                        make_float2(o[n][2 * k] * f, o[n][2 * k + 1] * f);
                 }
             }
         }
+        if (!warps_sync()) break;
+        for (int c = tid; c < S::kRows * (D / 8); c += S::kWarps * 32) {
+            const int r = c / (D / 8), blk = c % (D / 8);
+            const AttnRow row = attn_row(p, td.g, r);
+            if (!row.live) continue;
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < S::kWarps; ++w) M = fmaxf(M, s_m[w * S::kRows + r]);
+#pragma unroll
+            for (int w = 0; w < S::kWarps; ++w)
+                L += s_l[w * S::kRows + r] * (M == -INFINITY ? 1.f : ex2(s_m[w * S::kRows + r] - M));
+            float x[8] = {};
+            const int col = F8 ? (blk * 8) ^ ((r & 1) << 4) : (blk * 8) ^ ((r & 3) << 3);
+#pragma unroll
+            for (int w = 0; w < S::kWarps; ++w) {
+                const float4* src = reinterpret_cast<const float4*>(buf + (w * S::kRows + r) * D + col);
+                const float4 u = src[0], v = src[1];
+                x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
+                x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
+            }
+            const long long orow = static_cast<long long>(td.b) * p.R + row.i;
+            if (td.slot >= 0) {
+                float4* dst = reinterpret_cast<float4*>(po + r * D + blk * 8);
+                dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+                dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+                if (blk == 0) {
+                    po[S::kRows * D + r] = M;
+                    po[S::kRows * (D + 1) + r] = L;
+                }
+            } else {
+                const float f = L == 0.f ? 0.f : vs / L;
+                __nv_bfloat16* out = p.out + orow * p.ldo + static_cast<long long>(row.hq) * D;
+                *reinterpret_cast<uint4*>(out + blk * 8) =
+                    make_uint4(pack2<false>(x[0] * f, x[1] * f), pack2<false>(x[2] * f, x[3] * f),
+                               pack2<false>(x[4] * f, x[5] * f), pack2<false>(x[6] * f, x[7] * f));
+                if (blk == 0 && p.lse)
+                    p.lse[orow * p.Hq + row.hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+            }
+        }
+        fence_async_smem();  // the stage was written here; the next load writes it again
+        if (!warps_sync()) break;  // (also before s_m and s_l are written again)
+        if (lane == 0) mbar_arrive(&b_empty[st]);
     }
 }
 
 // The kernel's attributes and occupancy, once per device, and its launch on
 // min(*grid, resident CTAs) CTAs (written back to *grid).
-template <int D, bool F8, int WR, int WK, int MINB>
-cudaError_t attn_launch(const AttnParams& p, int* grid, int sms, cudaStream_t s) {
-    using S = AttnShape<D, F8, WR, WK>;
-    static std::atomic<unsigned long long> once{0};
-    static std::atomic<int> occ{0};
-    cudaError_t e = set_attribute_per_device(once, [] {
-        cudaError_t r = cudaFuncSetAttribute(attn_kernel<D, F8, WR, WK, MINB>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-        int n = 0;
-        if (r == cudaSuccess)
-            r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                &n, attn_kernel<D, F8, WR, WK, MINB>, S::kThreads, S::kSmem);
-        if (r == cudaSuccess) occ.store(n);
-        return r;
-    });
+template <class K>
+cudaError_t attn_launch(K kernel, int threads, int smem, std::atomic<unsigned long long>& once,
+                        std::atomic<int>& occ, const AttnParams& p, const AttnMaps& maps, int* grid,
+                        int sms, cudaStream_t s) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const int resident = sms * (occ.load() > 0 ? occ.load() : 1);
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (!bit || !(once.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        int n = 0;
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+        if (e != cudaSuccess) return e;
+        occ.store(n < 1 ? 1 : n);
+        once.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    const int resident = sms * occ.load();
     if (*grid > resident) *grid = resident;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(*grid);
-    cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_kernel<D, F8, WR, WK, MINB>, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p, maps);
 }
+}  // namespace vw4
+
+#include "attn_tc.cuh"
+
+namespace vw4 {
 
 template <int D, bool F8>
-cudaError_t attn_dispatch_rows(const AttnParams& p, int rows, int* grid, int sms, cudaStream_t s) {
-    switch (rows) {
-        case 16: return attn_launch<D, F8, 1, 4, D == 256 ? 1 : (D == 128 ? 2 : 3)>(p, grid, sms, s);
-        case 32: return attn_launch<D, F8, 2, 2, D == 256 ? 1 : (D == 128 ? 2 : 3)>(p, grid, sms, s);
-        case 64: return attn_launch<D, F8, 4, 1, D == 256 ? 1 : 2>(p, grid, sms, s);
-    }
-    if constexpr (D < 256) return attn_launch<D, F8, 8, 1, D == 64 ? 2 : 1>(p, grid, sms, s);
-    return cudaErrorInvalidValue;
+cudaError_t attn_dispatch_rows(const AttnParams& p, const AttnMaps& maps, int rows, int* grid, int sms,
+                               cudaStream_t s) {
+    static std::atomic<unsigned long long> once[3];
+    static std::atomic<int> occ[3];
+    constexpr int kMinBlocks = D == 256 ? 1 : (D == 128 ? 2 : 3);
+    if (rows == 16)
+        return attn_launch(attn_kernel<D, F8, kMinBlocks>, AttnShape<D, F8>::kThreads,
+                           AttnShape<D, F8>::kSmem, once[0], occ[0], p, maps, grid, sms, s);
+    if (rows == 64)
+        return attn_launch(attn_tc_kernel<D, F8, 64>, AttnTcShape<D, F8, 64>::kThreads,
+                           AttnTcShape<D, F8, 64>::kSmem, once[1], occ[1], p, maps, grid, sms, s);
+    return attn_launch(attn_tc_kernel<D, F8, 128>, AttnTcShape<D, F8, 128>::kThreads,
+                       AttnTcShape<D, F8, 128>::kSmem, once[2], occ[2], p, maps, grid, sms, s);
 }
 
 template <int D>
-cudaError_t attn_dispatch(const AttnParams& p, bool f8, int rows, int* grid, int sms,
-                          cudaStream_t s) {
-    return f8 ? attn_dispatch_rows<D, true>(p, rows, grid, sms, s)
-              : attn_dispatch_rows<D, false>(p, rows, grid, sms, s);
+cudaError_t attn_dispatch(const AttnParams& p, const AttnMaps& maps, bool f8, int rows, int* grid,
+                          int sms, cudaStream_t s) {
+    return f8 ? attn_dispatch_rows<D, true>(p, maps, rows, grid, sms, s)
+              : attn_dispatch_rows<D, false>(p, maps, rows, grid, sms, s);
 }
 #endif  // __CUDACC__
 

@@ -1,9 +1,9 @@
-// attn_d64.cu -- the attention kernels of head size 64 (see attn.cuh).
+// attn_d64.cu -- the attention kernels of head size 64 (see attn.cuh, attn_tc.cuh).
 #include "attn.cuh"
 
 namespace vw4 {
-cudaError_t launch_attn_d64(const AttnParams& p, bool f8, int rows, int* grid, int sms,
-                            cudaStream_t s) {
-    return attn_dispatch<64>(p, f8, rows, grid, sms, s);
+cudaError_t launch_attn_d64(const AttnParams& p, const AttnMaps& maps, bool f8, int rows, int* grid,
+                            int sms, cudaStream_t s) {
+    return attn_dispatch<64>(p, maps, f8, rows, grid, sms, s);
 }
 }  // namespace vw4

@@ -28,6 +28,9 @@ vw4_status check_cache(const vw4_kv_cache& c, int B, int R, int Hq) {
         return VW4_ERR_INVALID_ARG;
     if (c.page_size < 1 || c.page_stride < 0 || c.token_stride < 0 || c.head_stride < 0)
         return VW4_ERR_INVALID_ARG;
+    if (c.token_stride == 0 || (c.num_pages > 1 && c.page_stride == 0) ||
+        (c.Hkv > 1 && c.head_stride == 0))
+        return VW4_ERR_INVALID_ARG;
     if (c.D != 64 && c.D != 128 && c.D != 256) return VW4_ERR_UNSUPPORTED;
     if (c.page_size < 8 || c.page_size > 65536 || (c.page_size & (c.page_size - 1)))
         return VW4_ERR_UNSUPPORTED;
@@ -138,6 +141,7 @@ VW4_API vw4_status verify_attn(const vw4_attn* a, void* workspace_dev, size_t ws
     p.out = static_cast<__nv_bfloat16*>(a->out_dev);
     p.lse = a->lse_dev;
     p.status = status;
+    p.wait_ns = wait_limit_ns();
     p.ldq = a->ldq;
     p.ldo = a->ldo;
     p.table_stride = c.table_stride;
@@ -157,8 +161,32 @@ VW4_API vw4_status verify_attn(const vw4_attn* a, void* workspace_dev, size_t ws
     p.page_shift = shift_of(c.page_size);
     p.max_blocks = c.max_blocks;
     p.num_pages = c.num_pages;
-    const cudaError_t e = launch_attn(p, c.D, c.dtype == VW4_KV_E4M3, sms, workspace_dev,
-                                      static_cast<cudaStream_t>(stream));
+    const bool f8 = c.dtype == VW4_KV_E4M3;
+    const AttnPlan plan = attn_plan(p, c.D, f8, workspace_dev);
+    AttnMaps maps;
+    {
+        // strides of dimensions of one element are never used, but must be valid
+        const uint64_t step = f8 ? 16 : 8;
+        const auto valid = [step](int64_t v) { return v > 0 ? static_cast<uint64_t>(v) : step; };
+        const uint64_t dims[4] = {static_cast<uint64_t>(c.D), static_cast<uint64_t>(c.Hkv),
+                                  static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(c.num_pages)};
+        const uint64_t strides[3] = {valid(c.head_stride), valid(c.token_stride), valid(c.page_stride)};
+        const uint32_t box[4] = {static_cast<uint32_t>(plan.box_bytes / (f8 ? 1 : 2)), 1u,
+                                 static_cast<uint32_t>(plan.box_rows), 1u};
+        st = static_cast<vw4_status>(encode_map(&maps.k, !f8, 4, c.k_dev, dims, strides, box, plan.swizzle));
+        if (st != VW4_OK) return st;
+        st = static_cast<vw4_status>(encode_map(&maps.v, !f8, 4, c.v_dev, dims, strides, box, plan.swizzle));
+        if (st != VW4_OK) return st;
+        const uint64_t qd[3] = {static_cast<uint64_t>(c.D), static_cast<uint64_t>(a->Hq),
+                                static_cast<uint64_t>(a->B) * a->R};
+        const uint64_t qs[2] = {static_cast<uint64_t>(c.D), static_cast<uint64_t>(a->ldq)};
+        const uint32_t qb[3] = {64u, static_cast<uint32_t>(p.gb), static_cast<uint32_t>(p.tb)};
+        st = static_cast<vw4_status>(
+            encode_map(&maps.q, true, 3, a->q_dev, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B));
+        if (st != VW4_OK) return st;
+    }
+    const cudaError_t e =
+        launch_attn(p, maps, plan, c.D, f8, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return static_cast<vw4_status>(report_cuda(e, "verify_attn launch"));
     return VW4_OK;
 }

@@ -204,13 +204,15 @@ cudaError_t launch_accept_rejection(const float* target, const float* draft,
                                     const float* draft_bmax = nullptr);
 
 // What the entry points outside api.cu need of it: the current device's SM
-// count and status word, and the text of a failed CUDA call (both return a
-// vw4_status).
+// count and status word, the text of a failed CUDA call (both return a
+// vw4_status), and the limit of a pipeline wait.
 int current_device(int* sms, uint32_t** status);
 int report_cuda(cudaError_t e, const char* where);
+unsigned long long wait_limit_ns();
 
 // ---- attention of the verify rows over a paged cache (attn*.cu)
 constexpr uint32_t kStatusBadPage = 0x40u;
+constexpr uint32_t kStatusWaitTimeout = 0x4u;
 constexpr uint32_t kStatusBadListId = 0x10u;
 struct AttnParams {
     const __nv_bfloat16* q;
@@ -225,23 +227,42 @@ struct AttnParams {
     float* partial;         // [2 grid][rows][D] unnormalized rows, then m [rows], l [rows]
     long long* base;        // [B + 1]: units before each sequence, all units
     uint32_t* status;
+    unsigned long long wait_ns;  // limit of a pipeline wait
     long long ldq, ldo, table_stride, page_stride, token_stride, head_stride;
     float scale;
     int B, R, Hq, Hkv, G;   // G: query heads of a key head
     int window, sinks;
     int page_size, page_shift, max_blocks, num_pages;
-    int row_blocks, groups;  // query-row blocks of a key head; Hkv * row_blocks
+    // the query rows of a key head in blocks of tb verify indexes x gb heads:
+    // blocks_g of them along the heads, row_blocks in all; groups = Hkv * row_blocks
+    int tb, gb, blocks_g, row_blocks, groups;
+};
+// TMA maps of the cache (dimension, head, token of the page, page) and of the
+// queries (dimension, head, row).
+struct AttnMaps {
+    CUtensorMap k, v, q;
 };
 constexpr int kAttnMaxGrid64 = 608, kAttnMaxGrid256 = 304;
-int attn_rows(int rows, int D);        // rows of a block of the kernel chosen for that many rows
 size_t attn_workspace_bytes(int B, int rows, int D);
-cudaError_t launch_attn(AttnParams p, int D, bool f8, int sms, void* ws, cudaStream_t s);
-cudaError_t launch_attn_d64(const AttnParams& p, bool f8, int rows, int* grid, int sms,
-                            cudaStream_t s);
-cudaError_t launch_attn_d128(const AttnParams& p, bool f8, int rows, int* grid, int sms,
-                             cudaStream_t s);
-cudaError_t launch_attn_d256(const AttnParams& p, bool f8, int rows, int* grid, int sms,
-                             cudaStream_t s);
+// Plans a call: block shape, grid bound and workspace pointers in p.
+struct AttnPlan {
+    int rows, tk, grid;
+    int box_rows, box_bytes;   // of K and V: tokens, bytes of a key
+    CUtensorMapSwizzle swizzle;
+};
+AttnPlan attn_plan(AttnParams& p, int D, bool f8, void* ws);
+cudaError_t launch_attn(const AttnParams& p, const AttnMaps& maps, AttnPlan plan, int D, bool f8,
+                        int sms, cudaStream_t s);
+cudaError_t launch_attn_d64(const AttnParams& p, const AttnMaps& maps, bool f8, int rows, int* grid,
+                            int sms, cudaStream_t s);
+cudaError_t launch_attn_d128(const AttnParams& p, const AttnMaps& maps, bool f8, int rows, int* grid,
+                             int sms, cudaStream_t s);
+cudaError_t launch_attn_d256(const AttnParams& p, const AttnMaps& maps, bool f8, int rows, int* grid,
+                             int sms, cudaStream_t s);
+// A tensor map of n dimensions (element type u8 or bf16, sizes and strides in
+// elements of the type, strides of dimensions 1..), cached by its contents.
+int encode_map(CUtensorMap* map, bool bf16, int n, const void* base, const uint64_t* dims,
+               const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw);
 
 // ---- head norm, rotation and cache append (rope_append.cu)
 struct AppendParams {
