@@ -28,7 +28,9 @@ constexpr int kJoinThreads = 128;
 
 // Joins the partials of split items, in the order of their tiles, and writes
 // the rows of sequences without keys.  One block takes `chunk` rows of an
-// item, one warp a row; each lane owns D / 32 columns.
+// item, one warp a row.  The lanes weigh up to 32 partials at once and then
+// own D / 32 columns each; the first partials' rows are on their way while the
+// weights are computed (the kernel is a chain of load latencies).
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParams p, int rows,
                                                                  int grid, int tk, int chunk) {
@@ -36,11 +38,11 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int item = blockIdx.x, b = item / p.groups, g = item - b * p.groups;
     const int h = g / p.row_blocks;
-    const long long T = p.base[p.B];
+    const long long T = p.base[p.B], base = p.base[b];
     const int nt = attn_seq(p.seq_lens[b], p.max_blocks * p.page_size, p.R, p.window, p.sinks, tk).nt;
-    const long long u = p.base[b] + static_cast<long long>(g) * nt;
+    const long long u = base + static_cast<long long>(g) * nt;
     const int G = attn_ctas(T, grid);
-    int c0 = 0, c1 = 0;
+    int c0 = 0, c1 = -1;
     if (nt > 0) {
         c0 = attn_owner(T, G, u);
         c1 = attn_owner(T, G, u + nt - 1);
@@ -48,36 +50,64 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float vs = p.v_scale ? __ldg(p.v_scale + h) : 1.f;
-    constexpr int E = D / 32;
-    for (int r = blockIdx.y * chunk + warp; r < (static_cast<int>(blockIdx.y) + 1) * chunk && r < rows;
-         r += kJoinThreads / 32) {
+    constexpr int E = D / 32, U = 8;
+    const size_t slot = static_cast<size_t>(rows) * (D + 2);
+    auto part = [&](int c) { return p.partial + static_cast<size_t>(c == c0 ? 2 * c + 1 : 2 * c) * slot; };
+    const int r1 = min((static_cast<int>(blockIdx.y) + 1) * chunk, rows);
+    for (int r = blockIdx.y * chunk + warp; r < r1; r += kJoinThreads / 32) {
         const AttnRow row = attn_row(p, g, r);
         if (!row.live) continue;
-        const long long orow = static_cast<long long>(b) * p.R + row.i;
         float M = -INFINITY, L = 0.f, acc[E] = {};
-        if (nt > 0) {
-            // the partials' maxima first (lanes in parallel), then their rows
-            const size_t slot = static_cast<size_t>(rows) * (D + 2);
-            for (int c = c0 + lane; c <= c1; c += 32) {
-                const float* q = p.partial + static_cast<size_t>(c == c0 ? 2 * c + 1 : 2 * c) * slot;
-                M = fmaxf(M, q[rows * D + r]);
+        for (int cb = c0; cb <= c1; cb += 32) {
+            const int n = min(32, c1 - cb + 1);
+            float v[U][E];
+            auto fetch = [&](int k0) {
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    if (k0 + k < n) {
+                        const float* q = part(cb + k0 + k) + r * D + lane * 2;
+#pragma unroll
+                        for (int e = 0; e < E; e += 2) {
+                            const float2 t = *reinterpret_cast<const float2*>(q + e * 32);
+                            v[k][e] = t.x;
+                            v[k][e + 1] = t.y;
+                        }
+                    }
+            };
+            fetch(0);
+            float m = -INFINITY, l = 0.f;
+            if (lane < n) {
+                const float* q = part(cb + lane);
+                m = q[rows * D + r];
+                l = q[rows * (D + 1) + r];
             }
+            float mx = m;
 #pragma unroll
-            for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) {
-                const float* q = p.partial + static_cast<size_t>(c == c0 ? 2 * c + 1 : 2 * c) * slot;
-                const float w = M == -INFINITY ? 1.f : ex2(q[rows * D + r] - M);
-                L += q[rows * (D + 1) + r] * w;
+            for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+            mx = fmaxf(mx, M);
+            const float old = mx == M ? 1.f : ex2(M - mx);  // (M = -infinity: 0)
+            M = mx;
+            const float w = lane < n ? (M == -INFINITY ? 1.f : ex2(m - M)) : 0.f;
+            float sum = l * w;
 #pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const float2 v = *reinterpret_cast<const float2*>(q + r * D + lane * 2 + e * 32);
-                    acc[e] = fmaf(v.x, w, acc[e]);
-                    acc[e + 1] = fmaf(v.y, w, acc[e + 1]);
+            for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+            L = L * old + sum;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= old;
+            for (int k0 = 0; k0 < n; k0 += U) {
+                if (k0 > 0) fetch(k0);
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+                    if (k0 + k < n) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) acc[e] = fmaf(v[k][e], wk, acc[e]);
+                    }
                 }
             }
         }
         const float f = L == 0.f ? 0.f : vs / L;
+        const long long orow = static_cast<long long>(b) * p.R + row.i;
         __nv_bfloat16* out = p.out + orow * p.ldo + static_cast<long long>(row.hq) * D;
 #pragma unroll
         for (int e = 0; e < E; e += 2)

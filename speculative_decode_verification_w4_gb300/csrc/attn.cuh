@@ -380,6 +380,11 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
     float* s_rs = reinterpret_cast<float*>(smem + S::kOffRS);
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 128) {
+        tma_prefetch_desc(&maps.k);
+        tma_prefetch_desc(&maps.v);
+        tma_prefetch_desc(&maps.q);
+    }
     if (tid == 0) {
         for (int k = 0; k < NST; ++k) {
             mbar_init(&b_full[k], 1);

@@ -4,17 +4,18 @@
 //
 // One CTA per SM, warps with roles.  A producer warp loads K and V tiles (TMA)
 // into a ring of half stages (K, V, K, V, ...) in the 128-byte swizzled layout
-// the tensor cores read; one thread issues S = Q K^T (both operands in shared
-// memory) and O += P V (P in tensor memory, V contiguous along N); the softmax
-// warps own one query row a thread, so the softmax has no shuffles and S and P
-// never pass through shared memory.  S has two buffers: Q K^T of the next tile
-// runs under the softmax of this one; P overwrites the front of its S.
+// the tensor cores read; one thread issues S = Q K^T and O += P V, whichever
+// has its operands first, with Q and P in tensor memory (a product of 64 or
+// 128 keys that also read Q from shared memory was bound by those reads); the
+// softmax warps own one query row a thread, so the softmax has no shuffles and
+// S and P never pass through shared memory.  S has two buffers: Q K^T of the
+// next tile runs under the softmax of this one; P overwrites the front of its S.
 //
-// The last role differs by the cache's type.  bf16: four warps pass each V tile
-// on; at the edges (keys that not every row sees) they clean it first.  e4m3:
-// tiles arrive raw in a ring of their own and eight warps turn them into f16
-// (exact), the queries into f16 under a power of two per row; both cleaned the
-// same way.
+// The last role brings an item's queries into tensor memory and differs by the
+// cache's type.  bf16: four warps pass each V tile on; at the edges (keys that
+// not every row sees) they clean it first.  e4m3: tiles arrive raw in a ring of
+// their own, four warps turn K and four V into f16 (exact), cleaned the same
+// way, and the queries into f16 under a power of two per row.
 //
 // The running maximum that the exponents use follows the true one lazily: O is
 // rescaled only when a row's maximum grew by more than 2^8 (its weights are
@@ -30,23 +31,19 @@ struct AttnTcShape {
     static constexpr int kTK = D == 256 ? 64 : 128;  // keys of a tile
     static constexpr int kHalf = kTK * D * 2;        // K or V of a tile, 16-bit operands
     static constexpr int kBlk = kTK * 128;           // 64 dimensions of it
-    static constexpr int kQ = ROWS * D * 2;
-    static constexpr int kQBlk = ROWS * 128;
-    static constexpr int kNQ = D == 256 && ROWS == 128 ? 1 : 2;
     static constexpr int kRaw = kTK * D;             // e4m3 half before conversion
-    static constexpr int kNR = !F8 ? 0 : (D == 64 ? 8 : 4);
-    static constexpr int kNS = F8 ? (D == 64 ? 4 : 3)
-                                  : (D == 64 ? 8 : (D == 128 && ROWS == 64 ? 6 : 5));
+    static constexpr int kNR = !F8 ? 0 : (D == 64 ? 8 : 5);
+    static constexpr int kNS = F8 ? 4 : (D == 64 ? 8 : 6);
     static constexpr int kAuxWarps = F8 ? 8 : 4;     // converters, or cleaners
     static constexpr int kThreads = (6 + kAuxWarps) * 32;
-    static constexpr int kOffSlots = kNQ * kQ;
-    static constexpr int kOffRaw = kOffSlots + kNS * kHalf;
-    static constexpr int kSmem = kOffRaw + kNR * kRaw + 1024;  // and alignment
-    // the products read 128 rows of Q whatever ROWS is: what follows must be there
-    static_assert(kOffRaw >= (kNQ - 1) * kQ + (D / 64 - 1) * kQBlk + 128 * 128, "Q reads");
+    static constexpr int kOffRaw = kNS * kHalf;
+    static constexpr int kOffStage = kOffRaw + kNR * kRaw;  // 4 KB a softmax warp, for the output
+    static constexpr int kSmem = kOffStage + 4 * 4096 + 1024;  // and alignment
     static_assert(kSmem + 2048 <= 227 * 1024 && kSmem > 114 * 1024, "one CTA per SM");
-    static constexpr uint32_t kColO = 0, kColS = D;  // tensor memory columns
-    static_assert(D + 2 * kTK <= 512, "tensor memory");
+    // tensor memory columns: O, two S, the queries (two 16-bit values a column)
+    static constexpr uint32_t kColO = 0, kColS = D, kColQ = D + 2 * kTK;
+    static constexpr int kNQ = D == 256 ? 1 : 2;
+    static_assert(D + 2 * kTK + kNQ * D / 2 <= 512, "tensor memory");
     __device__ static __forceinline__ uint32_t at(int row, int chunk) {  // 16 bytes of an operand row
         return static_cast<uint32_t>((chunk >> 3) * kBlk + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
     }
@@ -74,31 +71,37 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     // loaded (bf16) or converted (e4m3) halves, their release, cleaned V halves (bf16)
     __shared__ __align__(8) uint64_t b_full[NS], b_empty[NS], b_clean[NS];
     __shared__ __align__(8) uint64_t b_raw[NR], b_raw_empty[NR];
-    __shared__ __align__(8) uint64_t b_s[2], b_p[2], b_pv, b_q[2], b_qc[2], b_qe[2], b_o, b_end;
-    __shared__ float s_rs[F8 ? 2 : 1][F8 ? ROWS : 1];  // 1 / row scale of f16 queries
+    __shared__ __align__(8) uint64_t b_s[2], b_p[2], b_pv, b_q[2], b_qe[2], b_part[8], b_o, b_end;
+    // log2 of the row scales of f16 queries, by part: the queries of part n + 4 wait for
+    // the last products of part n + 2 or later, whose scores wait for reads of part n
+    __shared__ int8_t s_rs[F8 ? 4 : 1][F8 ? ROWS : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row_warps = (p.tb * p.gb + 31) / 32;     // softmax warps with rows
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 160) {
+        tma_prefetch_desc(&maps.k);
+        tma_prefetch_desc(&maps.v);
+    }
     if (warp == 4) {
         tmem_alloc<512>(&s_tmem);
         if (lane == 0) {
             for (int k = 0; k < NS; ++k) {
-                mbar_init(&b_full[k], F8 ? S::kAuxWarps : 1);
+                mbar_init(&b_full[k], F8 ? 4 : 1);
                 mbar_init(&b_empty[k], 1);
-                mbar_init(&b_clean[k], S::kAuxWarps);
+                mbar_init(&b_clean[k], 4);
             }
             for (int k = 0; k < NR; ++k) {
                 mbar_init(&b_raw[k], 1);
-                mbar_init(&b_raw_empty[k], S::kAuxWarps);
+                mbar_init(&b_raw_empty[k], 4);
             }
             for (int k = 0; k < 2; ++k) {
                 mbar_init(&b_s[k], 1);
                 mbar_init(&b_p[k], row_warps);
-                mbar_init(&b_q[k], 1);
-                mbar_init(&b_qc[k], S::kAuxWarps);
+                mbar_init(&b_q[k], row_warps);
                 mbar_init(&b_qe[k], 1);
             }
+            for (int k = 0; k < 8; ++k) mbar_init(&b_part[k], 1);
             mbar_init(&b_pv, 1);
             mbar_init(&b_o, row_warps);
             mbar_init(&b_end, 1);
@@ -125,6 +128,74 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         return __all_sync(0xffffffffu, wait(bar, phase)) != 0;
     };
 
+    // An item's queries into tensor memory: one row a thread of four warps.  For an
+    // e4m3 cache they become f16 under a power of two per row that puts the row's
+    // largest magnitude into [2^14, 2^15): exact for every value down to 2^-31 of it
+    // (bf16 has 8 significant bits, f16 11 and subnormals).
+    auto queries = [&](const AttnUnit& d, int qw) {
+        const int qs = d.seg % S::kNQ, r = qw * 32 + lane;
+        const AttnRow row = attn_row(p, d.g, r);
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + (static_cast<long long>(d.b) * p.R + row.i) * p.ldq + static_cast<long long>(row.hq) * D);
+        uint4 v[D == 256 ? 16 : D / 8];  // half a row of 256, else a row
+        constexpr int NV = D == 256 ? 16 : D / 8;
+        float up = 1.f;
+        auto get = [&](int from) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                v[k] = row.live ? __ldg(src + from + k) : make_uint4(0, 0, 0, 0);
+        };
+        if (F8) {
+            uint32_t mx = 0;  // largest magnitude, as bits
+#pragma unroll 1
+            for (int from = 0; from < D / 8; from += NV) {
+                get(from);
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx = max(mx, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+                }
+            }
+            const int ex = static_cast<int>(mx >> 7);
+            int sh = ex == 0 || ex == 255 ? 0 : 127 + 14 - ex;
+            sh = max(-126, min(126, sh));
+            up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+            if (r < ROWS)
+                s_rs[F8 ? d.seg & 3 : 0][F8 ? r : 0] = static_cast<int8_t>(sh);
+        } else {
+            get(0);
+        }
+        if (d.seg >= S::kNQ && !warp_wait(&b_qe[qs], d.seg / S::kNQ - 1)) return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int from = 0; from < D / 8; from += NV) {
+            if (F8 || from > 0) get(from);
+#pragma unroll
+            for (int c = 0; c < NV; c += 8) {
+                uint32_t y[32];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint4 t = v[c + k];
+                    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[4 * k + e] = F8 ? pack2<true>(__uint_as_float(w[e] << 16) * up,
+                                                        __uint_as_float(w[e] & 0xffff0000u) * up)
+                                          : w[e];
+                }
+                tmem_st32(tmem + (static_cast<uint32_t>(qw * 32) << 16) + S::kColQ + qs * (D / 2) +
+                              (from + c) * 4, y);
+            }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_q[qs]);
+        return true;
+    };
+
     if (n_units > 0 && warp == 5) {
         // -------------------------------------------------------- producer
         constexpr int NB = F8 ? 1 : D / 64, BOXB = F8 ? D : 128;  // boxes across a key
@@ -135,22 +206,13 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         w.begin(p, span, cap, lane);
         int hl = 0;  // halves loaded
         bool ok = true;
-        int q_loads = 0;
         for (int u = 0; u < n_units; ++u) {
             const AttnUnit d = w.unit(p);
             const uint32_t bytes = w.template bytes<NB, BOXB>();
-            if (d.flags & kUnitFirst) {
-                const int qs = d.seg % S::kNQ;
-                ok = d.seg < S::kNQ || warp_wait(&b_qe[qs], d.seg / S::kNQ - 1);
-                if (!ok) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&b_q[qs], attn_q_bytes(p, D));
-                    attn_load_q<D>(p, &maps.q, sm + qs * S::kQ, S::kQBlk, d, &b_q[qs]);
-                }
-                ++q_loads;
-                __syncwarp();
+            if (lane == 0) {
+                s_unit[u % kUnitRing] = d;
+                if (d.flags & kUnitFirst) mbar_arrive(&b_part[d.seg & 7]);  // its queries may be read
             }
-            if (lane == 0) s_unit[u % kUnitRing] = d;
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 const int st = hl % NL;
@@ -160,7 +222,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 __syncwarp();
                 w.template load<NB, BOXB, F8 ? 1 : 2>(
                     p, half ? &maps.v : &maps.k,
-                    sm + (F8 ? S::kOffRaw + st * S::kRaw : S::kOffSlots + st * S::kHalf), &full[st], lane);
+                    sm + (F8 ? S::kOffRaw + st * S::kRaw : st * S::kHalf), &full[st], lane);
                 ++hl;
             }
             if (!ok) break;
@@ -169,19 +231,32 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         if (!ok) {  // copies in flight land before the block ends
             for (int k = hl > NL ? hl - NL : 0; k < hl; ++k)
                 mbar_wait_bounded(&full[k % NL], (k / NL) & 1, p.wait_ns, nullptr);
-            for (int k = q_loads > S::kNQ ? q_loads - S::kNQ : 0; k < q_loads; ++k)
-                mbar_wait_bounded(&b_q[k % S::kNQ], (k / S::kNQ) & 1, p.wait_ns, nullptr);
         }
     } else if (n_units > 0 && warp >= 6) {
         // ----------------------------------------- cleaners or converters
-        const int at = tid - 192;
-        constexpr int N = S::kAuxWarps * 32;
+        // Four warps a group; group 0 also brings the queries (its warps reach all
+        // lanes of tensor memory: 32 (warp % 4) ..).  e4m3: group 0 has K, group 1 V.
+        constexpr int N = 128;
+        const int group = (warp - 6) >> 2, at = (tid - 192) & 127, half = F8 ? group : 1;
+        const int qw = warp & 3;
+        bool first = true;
+        int parts = 0;
         for (int u = 0; u < n_units; ++u) {
+            const int hh = 2 * u + half, st = hh % NS, sr = hh % NR;
+            if (first) {
+                if (group == 0 && qw < row_warps) {
+                    if (!warp_wait(&b_part[parts & 7], parts >> 3)) break;
+                    const AttnUnit d = s_unit[u % kUnitRing];
+                    if (!queries(d, qw)) break;
+                }
+                ++parts;
+            }
+            if (!warp_wait(F8 ? &b_raw[sr] : &b_full[st], F8 ? hh / NR : hh / NS)) break;
+            const AttnUnit d = s_unit[u % kUnitRing];
+            first = d.flags & kUnitLast;  // (of the next unit)
+            const bool clean = half == 1 && (d.flags & kUnitEdge);
             if (!F8) {
-                const int hv = 2 * u + 1, st = hv % NS;
-                if (!warp_wait(&b_full[st], hv / NS)) break;
-                const AttnUnit d = s_unit[u % kUnitRing];
-                if (d.flags & kUnitEdge) {
+                if (clean) {
                     // Values that no row sees become zeros; infinities and NaN of values
                     // that only some rows see too (0 times them must not reach the other
                     // rows): the end of the part gives them to the rows that see them.
@@ -190,8 +265,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                     for (int c = at; c < TK * (D / 8); c += N) {
                         const int row = c / (D / 8), j = d.start + row;
                         if (key_all(j, d.len, d.p0, p.window, p.sinks)) continue;
-                        uint4* q = reinterpret_cast<uint4*>(smem + S::kOffSlots + st * S::kHalf +
-                                                            S::at(row, c % (D / 8)));
+                        uint4* q = reinterpret_cast<uint4*>(smem + st * S::kHalf + S::at(row, c % (D / 8)));
                         if (!key_some(j, d.len, d.p0, p.window, p.sinks)) {
                             *q = make_uint4(0, 0, 0, 0);
                             continue;
@@ -212,62 +286,10 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b_clean[st]);
-                continue;
-            }
-            bool ok = true;
-#pragma unroll 1
-            for (int half = 0; half < 2 && ok; ++half) {
-                const int hh = 2 * u + half, st = hh % NS, sr = hh % NR;
-                ok = warp_wait(&b_raw[sr], hh / NR);
-                if (!ok) break;
-                const AttnUnit d = s_unit[u % kUnitRing];
-                if (half == 0 && (d.flags & kUnitFirst)) {
-                    // The queries become f16 under a power of two per row that puts the
-                    // row's largest magnitude into [2^14, 2^15): exact for every value
-                    // down to 2^-31 of it.
-                    const int qs = d.seg % S::kNQ;
-                    ok = warp_wait(&b_q[qs], d.seg / S::kNQ);
-                    if (!ok) break;
-                    for (int r = warp - 6; r < p.tb * p.gb; r += S::kAuxWarps) {
-                        uint32_t x[D / 64];
-                        float mx = 0.f;
-#pragma unroll
-                        for (int k = 0; k < D / 64; ++k) {
-                            // 64 dimensions: word `lane` of the 128-byte row of block k
-                            const uint32_t o = qs * S::kQ + k * S::kQBlk + r * 128 +
-                                               (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-                            x[k] = *reinterpret_cast<const uint32_t*>(smem + o);
-                            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[k] << 16)),
-                                                 fabsf(__uint_as_float(x[k] & 0xffff0000u))));
-                        }
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1)
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
-                        int sh = ex == 0 || ex == 255 ? 0 : 127 + 14 - ex;
-                        sh = max(-126, min(126, sh));
-                        const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-                        if (lane == 0)
-                            s_rs[F8 ? qs : 0][F8 ? r : 0] =
-                                __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-#pragma unroll
-                        for (int k = 0; k < D / 64; ++k) {
-                            const uint32_t o = qs * S::kQ + k * S::kQBlk + r * 128 +
-                                               (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-                            *reinterpret_cast<uint32_t*>(smem + o) =
-                                pack2<true>(__uint_as_float(x[k] << 16) * up,
-                                            __uint_as_float(x[k] & 0xffff0000u) * up);
-                        }
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&b_qc[qs]);
-                }
-                ok = hh < NS || warp_wait(&b_empty[st], hh / NS - 1);
-                if (!ok) break;
+            } else {
+                if (hh >= NS && !warp_wait(&b_empty[st], hh / NS - 1)) break;
                 const uint8_t* src = smem + S::kOffRaw + sr * S::kRaw;
-                uint8_t* dst = smem + S::kOffSlots + st * S::kHalf;
-                const bool clean = half == 1 && (d.flags & kUnitEdge);
+                uint8_t* dst = smem + st * S::kHalf;
                 bool odd = false;
                 constexpr int CH = D / 16;
 #pragma unroll 4
@@ -311,54 +333,70 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                     mbar_arrive(&b_raw_empty[sr]);
                 }
             }
-            if (!ok) break;
         }
     } else if (n_units > 0 && warp == 4) {
         // ----------------------------------------------- the tensor cores
         if (lane == 0) {
             constexpr uint32_t iS = tc_idesc(!F8, 128, TK, false), iO = tc_idesc(!F8, 128, D, true);
-            int fl[2] = {0, 0}, seg = 0;
-            auto scores = [&](int u) {
-                const int hk = 2 * u;
-                if (!wait(&b_full[hk % NS], hk / NS)) return false;
-                const AttnUnit* d = &s_unit[u % kUnitRing];
-                fl[u & 1] = d->flags;
-                seg = d->seg;
-                const int qs = seg % S::kNQ;
-                if ((d->flags & kUnitFirst) && !wait(F8 ? &b_qc[qs] : &b_q[qs], seg / S::kNQ))
-                    return false;
-                tc_fence_after();
-                const uint32_t q = sm + qs * S::kQ;
-                const uint32_t k = sm + S::kOffSlots + (hk % NS) * S::kHalf;
+            int fl[2] = {0, 0}, parts = 0;
+            int qk = 0, pv = 0;   // next tile of either product
+            bool k_in = false;    // the next K tile has arrived (its unit is known)
+            uint64_t t0 = 0;
+            while (pv < n_units) {
+                // S of tile qk takes the buffer of tile qk - 2, whose P has been read
+                if (qk < n_units && qk <= pv + 1) {
+                    const int hk = 2 * qk;
+                    k_in = k_in || mbar_test(&b_full[hk % NS], (hk / NS) & 1);
+                    const AttnUnit* d = &s_unit[qk % kUnitRing];
+                    const int seg = k_in ? d->seg : 0, qs = seg % S::kNQ;
+                    if (k_in && (!(d->flags & kUnitFirst) || mbar_test(&b_q[qs], (seg / S::kNQ) & 1))) {
+                        tc_fence_after();
+                        const uint32_t k = sm + (hk % NS) * S::kHalf;
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    tc_mma_ss(tmem + S::kColS + (u & 1) * TK,
-                              tc_desc(q + (ks >> 2) * S::kQBlk + (ks & 3) * 32, 16, 1024),
-                              tc_desc(k + (ks >> 2) * S::kBlk + (ks & 3) * 32, 16, 1024), iS, ks > 0);
-                tc_commit(&b_s[u & 1]);
-                tc_commit(&b_empty[hk % NS]);
-                if (d->flags & kUnitLast) tc_commit(&b_qe[qs]);
-                return true;
-            };
-            bool ok = scores(0);
-            int parts = -1;
-            for (int u = 0; u < n_units && ok; ++u) {
-                const bool first = fl[u & 1] & kUnitFirst;
-                if (u + 1 < n_units) ok = scores(u + 1);
-                if (first && ++parts > 0) ok = ok && wait(&b_o, parts - 1);  // O has been read
-                const int hv = 2 * u + 1;
-                ok = ok && wait(&b_p[u & 1], u >> 1) &&
-                     wait(F8 ? &b_full[hv % NS] : &b_clean[hv % NS],
-                          F8 ? hv / NS : attn_v_phase(hv, NS));
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t v = sm + S::kOffSlots + (hv % NS) * S::kHalf;
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            tc_mma_ts(tmem + S::kColS + (qk & 1) * TK,
+                                      tmem + S::kColQ + qs * (D / 2) + ks * 8,
+                                      tc_desc(k + (ks >> 2) * S::kBlk + (ks & 3) * 32, 16, 1024), iS,
+                                      ks > 0);
+                        tc_commit(&b_s[qk & 1]);
+                        tc_commit(&b_empty[hk % NS]);
+                        if (d->flags & kUnitLast) tc_commit(&b_qe[qs]);
+                        fl[qk & 1] = d->flags;
+                        ++qk;
+                        k_in = false;
+                        t0 = 0;
+                        continue;
+                    }
+                }
+                if (pv < qk) {
+                    const int hv = 2 * pv + 1;
+                    const bool first = fl[pv & 1] & kUnitFirst;
+                    if (mbar_test(&b_p[pv & 1], (pv >> 1) & 1) &&
+                        mbar_test(F8 ? &b_full[hv % NS] : &b_clean[hv % NS],
+                                  (F8 ? hv / NS : attn_v_phase(hv, NS)) & 1) &&
+                        (!first || parts == 0 || mbar_test(&b_o, (parts - 1) & 1))) {  // O was read
+                        tc_fence_after();
+                        const uint32_t v = sm + (hv % NS) * S::kHalf;
 #pragma unroll
-                for (int ks = 0; ks < TK / 16; ++ks)
-                    tc_mma_ts(tmem + S::kColO, tmem + S::kColS + (u & 1) * TK + ks * 8,
-                              tc_desc(v + ks * 2048, S::kBlk, 1024), iO, !(first && ks == 0));
-                tc_commit(&b_empty[hv % NS]);
-                tc_commit(&b_pv);
+                        for (int ks = 0; ks < TK / 16; ++ks)
+                            tc_mma_ts(tmem + S::kColO, tmem + S::kColS + (pv & 1) * TK + ks * 8,
+                                      tc_desc(v + ks * 2048, S::kBlk, 1024), iO, !(first && ks == 0));
+                        tc_commit(&b_empty[hv % NS]);
+                        tc_commit(&b_pv);
+                        parts += first;
+                        ++pv;
+                        t0 = 0;
+                        continue;
+                    }
+                }
+                if (s_abort) break;
+                const uint64_t now = globaltimer_ns();
+                if (t0 == 0) t0 = now;
+                if (now - t0 > p.wait_ns) {
+                    s_abort = 1;
+                    atomicOr(p.status, kStatusWaitTimeout);
+                    break;
+                }
             }
             // everything issued is complete before the tensor memory is given back
             tc_commit(&b_end);
@@ -386,7 +424,8 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 c2 = p.scale * kLog2e;
                 if (F8) {
                     if (p.k_scale) c2 *= __ldg(p.k_scale + h);
-                    c2 *= s_rs[F8 ? td.seg % S::kNQ : 0][F8 ? min(r, ROWS - 1) : 0];
+                    c2 *= __uint_as_float(
+                        static_cast<uint32_t>(127 - s_rs[F8 ? td.seg & 3 : 0][F8 ? min(r, ROWS - 1) : 0]) << 23);
                 }
                 l = 0.f;
             }
@@ -396,9 +435,18 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             auto masked = [&](int c) {  // 64 columns of the row from column c
                 tmem_ld64(x, tS + c);
                 if (edge) {
+                    // seen: k <= hi and (k > lo or k < sk)
+                    const int hi = pr - td.start - c;
+                    if (p.window == 0) {
 #pragma unroll
-                    for (int k = 0; k < 64; ++k)
-                        if (!key_seen(td.start + c + k, pr, p.window, p.sinks)) x[k] = 0xff800000u;
+                        for (int k = 0; k < 64; ++k)
+                            if (k > hi) x[k] = 0xff800000u;
+                    } else {
+                        const int lo = hi - p.window, sk = p.sinks - td.start - c;
+#pragma unroll
+                        for (int k = 0; k < 64; ++k)
+                            if (k > hi || (k <= lo && k >= sk)) x[k] = 0xff800000u;
+                    }
                 }
             };
 #pragma unroll
@@ -465,8 +513,17 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             const float vs = F8 && p.v_scale ? __ldg(p.v_scale + h) : 1.f;
             const float f = td.slot >= 0 ? 1.f : (l == 0.f ? 0.f : vs / l);
             const long long orow = static_cast<long long>(td.b) * p.R + row.i;
-            __nv_bfloat16* out = p.out + orow * p.ldo + static_cast<long long>(row.hq) * D;
-            float* po = p.partial + static_cast<long long>(td.slot < 0 ? 0 : td.slot) * ROWS * (D + 2);
+            // The rows leave through 4 KB of shared memory a warp, 128 bytes of each of
+            // the 32 rows at a time (fp32 partial: 32 columns, bf16: 64), so that eight
+            // lanes write one row's line.
+            const long long dst_row =
+                td.slot >= 0 ? (static_cast<long long>(td.slot) * ROWS * (D + 2) + static_cast<long long>(r) * D) * 4
+                             : (orow * p.ldo + static_cast<long long>(row.hq) * D) * 2;
+            uint8_t* dst_base = td.slot >= 0 ? reinterpret_cast<uint8_t*>(p.partial)
+                                             : reinterpret_cast<uint8_t*>(p.out);
+            const int my_row = live ? 1 : 0;
+            uint8_t* stage = smem + S::kOffStage + warp * 4096;
+            const int width = td.slot >= 0 ? 32 : 64;  // columns a line
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t y[32];
@@ -503,27 +560,42 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                         give(max(0, td.p0 - p.window + 1), min(td.p0, td.len - 1 - p.window));
                     give(max(0, td.p0 + 1), td.len - 1);
                 }
-                if (live && td.slot >= 0) {
+                if (td.slot >= 0) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-                        *reinterpret_cast<uint4*>(po + r * D + c + k) =
-                            make_uint4(y[k], y[k + 1], y[k + 2], y[k + 3]);
-                } else if (live) {
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                            make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                } else {
+                    const int k0 = c & 32 ? 4 : 0;
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
+                    for (int k = 0; k < 4; ++k) {
                         uint32_t w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            w[e] = pack2<false>(__uint_as_float(y[k + 2 * e]) * f,
-                                                __uint_as_float(y[k + 2 * e + 1]) * f);
-                        *reinterpret_cast<uint4*>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                            w[e] = pack2<false>(__uint_as_float(y[8 * k + 2 * e]) * f,
+                                                __uint_as_float(y[8 * k + 2 * e + 1]) * f);
+                        *reinterpret_cast<uint4*>(stage + lane * 128 + (((k0 + k) ^ (lane & 7)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
                     }
+                    if (k0 == 0) continue;  // the other half of the lines is to come
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int rr = k * 4 + (lane >> 3);
+                    const long long to = __shfl_sync(0xffffffffu, dst_row, rr);
+                    const int on = __shfl_sync(0xffffffffu, my_row, rr);
+                    if (on)
+                        *reinterpret_cast<uint4*>(dst_base + to + (c / width) * 128 + (lane & 7) * 16) =
+                            *reinterpret_cast<const uint4*>(stage + rr * 128 +
+                                                            (((lane & 7) ^ (rr & 7)) << 4));
                 }
             }
             __syncwarp();
             tc_fence_before();
             if (live) {
                 if (td.slot >= 0) {
+                    float* po = p.partial + static_cast<long long>(td.slot) * ROWS * (D + 2);
                     po[ROWS * D + r] = mm;
                     po[ROWS * (D + 1) + r] = l;
                 } else if (p.lse) {
