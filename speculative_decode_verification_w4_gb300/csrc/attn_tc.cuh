@@ -506,7 +506,9 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             if (!(td.flags & kUnitLast)) continue;
 
             // ---- end of the segment
-            if (!warp_wait(&b_pv, u)) break;
+            // A wait names a phase by its parity, so the one before it must be known to be
+            // over: S of tile u was committed after the product of tile u - 2.
+            if ((u > 0 && !warp_wait(&b_pv, u - 1)) || !warp_wait(&b_pv, u)) break;
             tc_fence_after();
             const bool live = row.live, odd = s_odd[td.seg & 7] == td.seg + 1;
             const float mm = m == -INFINITY ? -INFINITY : mc;

@@ -96,18 +96,21 @@ def attention64(q, k, v, n, scale, window, sinks, kv):
         sel = torch.nonzero(vis[i])[:, 0]
         if len(sel) == 0:
             continue
-        ki, vi = k[sel].repeat_interleave(G, 1), v[sel].repeat_interleave(G, 1)
-        s = torch.einsum("hd,thd->ht", q[i], ki) * scale
-        mag = torch.einsum("hd,thd->ht", q[i].abs(), ki.abs()).amax(1) * scale
+        ki, vi = k[sel], v[sel]
+
+        def heads(x, y, eq):  # per key head, its G query heads
+            return torch.einsum(eq, x.reshape(Hkv, G, -1), y).reshape(Hq, -1)
+        s = heads(q[i], ki, "kgd,tkd->kgt") * scale
+        mag = heads(q[i].abs(), ki.abs(), "kgd,tkd->kgt").amax(1) * scale
         m = s.amax(1, keepdim=True)
         p = (s - m).exp()
         z = p.sum(1, keepdim=True)
-        o = torch.einsum("ht,thd->hd", p / z, vi)
-        a = torch.einsum("ht,thd->hd", p / z, vi.abs())
+        o = heads(p / z, vi, "kgt,tkd->kgd")
+        a = heads(p / z, vi.abs(), "kgt,tkd->kgd")
         delta = 2 * D * 2.0 ** -24 * mag + 2.0 ** -22 * (2 * s.abs().amax(1) + 1)
         out[i], lse[i] = o, (m + z.log())[:, 0]
         tol[i] = (2 ** -8 * o.abs() + wp * a + 2 * delta[:, None] * a
-                  + tiny * vi.abs().sum(0) / z + 1e-30)
+                  + tiny * vi.abs().sum(0).repeat_interleave(G, 0) / z + 1e-30)
         tol_lse[i] = delta + 2.0 ** -22 * (1 + lse[i].abs())
     return out, lse, tol, tol_lse
 

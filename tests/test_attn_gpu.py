@@ -64,6 +64,22 @@ def test_window_and_sinks(R, window, sinks, kv):
     run_case(window, [1, 4, 65, 199, 700, 1500], R, 6, 2, 128, 16, kv, window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("R,G,D,page", [(8, 6, 256, 64), (16, 8, 256, 16), (16, 8, 128, 32),
+                                        (4, 6, 128, 128), (9, 3, 64, 8), (16, 8, 64, 256),
+                                        (1, 4, 256, 16), (2, 8, 64, 64)])
+def test_many_tiles_per_block(R, G, D, page, kv):
+    """Several tiles of one item in every thread block, and several items in one."""
+    run_case(60, [41000], R, G, 1, D, page, kv)
+    run_case(61, [300 + 37 * b for b in range(40)], R, 2 * G, 2, D, page, kv)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("R,G,D", [(4, 6, 256), (16, 6, 128), (7, 3, 64), (1, 6, 128)])
+def test_many_windows_per_block(R, G, D, kv):
+    run_case(62, [700 + 61 * b for b in range(40)], R, 2 * G, 2, D, 16, kv, window=500, sinks=5)
+
+
 def test_many_sequences():
     lens = [(37 * b) % 301 for b in range(300)]
     run_case(5, lens, 2, 4, 2, 64, 16, "bf16")
