@@ -9,10 +9,7 @@ namespace vw4 {
 // L2: the blocks of a key head are neighbours in the schedule).
 static int attn_rows(int rows) { return rows <= 16 ? 16 : (rows <= 64 ? 64 : 128); }
 // keys of a tile of the kernel for blocks of that many rows
-static int attn_tile(int rows, int D, bool f8) {
-    if (rows == 16) return f8 ? 128 : 64;
-    return D == 256 ? 64 : 128;
-}
+static int attn_tile(int rows, bool f8) { return rows == 16 && !f8 ? 64 : 128; }
 
 static int attn_grid_cap(int D) { return D == 256 ? kAttnMaxGrid256 : kAttnMaxGrid64; }
 
@@ -122,7 +119,7 @@ AttnPlan attn_plan(AttnParams& p, int D, bool f8, void* ws) {
     AttnPlan plan;
     const int total = p.R * p.G;
     plan.rows = attn_rows(total);
-    plan.tk = attn_tile(plan.rows, D, f8);
+    plan.tk = attn_tile(plan.rows, f8);
     p.gb = p.G < plan.rows ? p.G : plan.rows;
     p.tb = plan.rows / p.gb < p.R ? plan.rows / p.gb : p.R;
     p.blocks_g = (p.G + p.gb - 1) / p.gb;
@@ -136,12 +133,12 @@ AttnPlan attn_plan(AttnParams& p, int D, bool f8, void* ws) {
     const long long units = static_cast<long long>(p.B) * p.groups * ((cap + plan.tk - 1) / plan.tk);
     plan.grid = attn_grid_cap(D);
     if (units < plan.grid) plan.grid = static_cast<int>(units < 1 ? 1 : units);
-    plan.box_rows = p.page_size < plan.tk ? p.page_size : plan.tk;
+    // a box lies inside a page and inside a ring piece of the kernel
+    const int piece = plan.rows > 16 && D == 256 && !f8 ? 64 : plan.tk;
+    p.box_rows = p.page_size < piece ? p.page_size : piece;
     const int key = D * (f8 ? 1 : 2);
-    const bool raw = f8 && plan.rows > 16;  // converted on the way: whole keys, unswizzled
-    plan.box_bytes = raw || key < 128 ? key : 128;
-    plan.swizzle = raw ? CU_TENSOR_MAP_SWIZZLE_NONE
-                       : (key == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+    plan.box_bytes = key < 128 ? key : 128;
+    plan.swizzle = key == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     return plan;
 }
 

@@ -113,6 +113,23 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t b) {
 }
 
 
+// four f16 values (two pairs) as e4m3 bytes hi + lo: hi the nearest, lo the nearest to
+// the rest, which f16 holds exactly
+__device__ __forceinline__ void e4m3_terms(uint32_t ab, uint32_t cd, uint32_t& hi, uint32_t& lo) {
+    uint16_t h0, h1, l0, l1;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h0) : "r"(ab));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h1) : "r"(cd));
+    uint32_t r0, r1;
+    asm("{\n\t.reg .b32 t;\n\tcvt.rn.f16x2.e4m3x2 t, %1;\n\tsub.rn.f16x2 %0, %2, t;\n\t}"
+        : "=r"(r0) : "h"(h0), "r"(ab));
+    asm("{\n\t.reg .b32 t;\n\tcvt.rn.f16x2.e4m3x2 t, %1;\n\tsub.rn.f16x2 %0, %2, t;\n\t}"
+        : "=r"(r1) : "h"(h1), "r"(cd));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l0) : "r"(r0));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l1) : "r"(r1));
+    hi = h0 | (static_cast<uint32_t>(h1) << 16);
+    lo = l0 | (static_cast<uint32_t>(l1) << 16);
+}
+
 // ------------------------------------------------------- units and pages
 constexpr int kUnitFirst = 1;  // first / last tile of this CTA's part of an item
 constexpr int kUnitLast = 2;
@@ -248,7 +265,7 @@ struct AttnWalk {
         u = 0;
         n = static_cast<int>(w.u1 - w.u0);
         seg = 0;
-        box_rows = p.page_size < TK ? p.page_size : TK;
+        box_rows = p.box_rows;
         boxes = TK / box_rows;
         enter(p, lane);
         const long long r = w.u0 - w.base;
@@ -290,22 +307,25 @@ struct AttnWalk {
         }
         fetch(p, lane);
     }
-    // Bytes of the current tile's boxes of K (or V): NBLK blocks of BOXB bytes of a key.
-    template <int NBLK, int BOXB>
-    __device__ __forceinline__ uint32_t bytes() const {
-        return __popc(__ballot_sync(0xffffffffu, page >= 0)) *
-               static_cast<uint32_t>(box_rows * NBLK * BOXB);
+    // A part of the current tile of K or V: keys FROM .. FROM + KEYS, BLKS blocks of BOXB
+    // bytes of a key from block BLK on.  Its bytes (the boxes that some row sees), and
+    // its load: block k at dst + k * KEYS * BOXB, a row of BOXB bytes a key.
+    template <int FROM, int KEYS, int BLKS, int BOXB>
+    __device__ __forceinline__ uint32_t bytes(int lane) const {
+        const int key = lane * box_rows;
+        return __popc(__ballot_sync(0xffffffffu, page >= 0 && key >= FROM && key < FROM + KEYS)) *
+               static_cast<uint32_t>(box_rows * BLKS * BOXB);
     }
-    // Loads them: block k at dst + k * TK * BOXB, a row of BOXB bytes a key.
-    template <int NBLK, int BOXB, int ESZ>
+    template <int FROM, int KEYS, int BLK, int BLKS, int BOXB, int ESZ>
     __device__ __forceinline__ void load(const AttnParams& p, const CUtensorMap* map, uint32_t dst,
                                          uint64_t* bar, int lane) const {
-        const int token = start() & (p.page_size - 1);  // 0 unless a page holds several tiles
-        if (page >= 0) {
+        const int key = lane * box_rows;
+        if (page >= 0 && key >= FROM && key < FROM + KEYS) {
+            const int token = (start() + key) & (p.page_size - 1);
 #pragma unroll
-            for (int k = 0; k < NBLK; ++k)
-                tma_load_4d(dst + k * (TK * BOXB) + lane * box_rows * BOXB, map, k * (BOXB / ESZ),
-                            g / p.row_blocks, token, page, bar);
+            for (int k = 0; k < BLKS; ++k)
+                tma_load_4d(dst + k * (KEYS * BOXB) + (key - FROM) * BOXB, map,
+                            (BLK + k) * (BOXB / ESZ), g / p.row_blocks, token, page, bar);
         }
         __syncwarp();
     }
@@ -422,7 +442,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
             if (u >= NST && !wait(&b_empty[st], u / NST - 1)) break;
             const bool first = d.flags & kUnitFirst;
             if (first && d.seg >= 2 && !wait(&b_qe[d.seg & 1], (d.seg >> 1) - 1)) break;
-            const uint32_t kv = 2 * w.template bytes<S::kNBlk, S::kBoxB>();
+            const uint32_t kv = 2 * w.template bytes<0, TK, S::kNBlk, S::kBoxB>(lane);
             if (lane == 0) {
                 s_unit[u % kUnitRing] = d;
                 mbar_arrive_expect_tx(&b_full[st], kv + (first ? attn_q_bytes(p, D) : 0u));
@@ -432,9 +452,9 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
             }
             __syncwarp();
             const uint32_t dst = sm + st * S::kStage;
-            w.template load<S::kNBlk, S::kBoxB, F8 ? 1 : 2>(p, &maps.k, dst, &b_full[st], lane);
-            w.template load<S::kNBlk, S::kBoxB, F8 ? 1 : 2>(p, &maps.v, dst + S::kTile, &b_full[st],
-                                                            lane);
+            w.template load<0, TK, 0, S::kNBlk, S::kBoxB, F8 ? 1 : 2>(p, &maps.k, dst, &b_full[st], lane);
+            w.template load<0, TK, 0, S::kNBlk, S::kBoxB, F8 ? 1 : 2>(p, &maps.v, dst + S::kTile,
+                                                                      &b_full[st], lane);
             if (u + 1 < n_units) w.next(p, lane);
         }
         // copies in flight land before the block ends

@@ -2,24 +2,33 @@
 // 5th-generation tensor cores: the same units, partials and results as
 // attn_kernel (attn.cuh).
 //
-// One CTA per SM, warps with roles.  A producer warp loads K and V tiles (TMA)
-// into a ring of half stages (K, V, K, V, ...) in the 128-byte swizzled layout
-// the tensor cores read; one thread issues S = Q K^T and O += P V, whichever
-// has its operands first, with Q and P in tensor memory (a product of 64 or
-// 128 keys that also read Q from shared memory was bound by those reads); the
-// softmax warps own one query row a thread, so the softmax has no shuffles and
-// S and P never pass through shared memory.  S has two buffers: Q K^T of the
-// next tile runs under the softmax of this one; P overwrites the front of its S.
+// One CTA per SM, warps with roles.  A producer warp loads tiles of 128 keys
+// (TMA) into a ring of pieces in the swizzled layout the tensor cores read (K
+// whole and V whole; bf16 at head size 256: K by halves of its dimensions, V by
+// halves of its keys, 32 KB each).  One thread issues S = Q K^T and O += P V
+// piece by piece, whichever has its operands first.  The softmax warps own one
+// query row a thread, so the softmax has no shuffles, and S and P never pass
+// through shared memory.  S has two buffers: Q K^T of the next tile runs under
+// the softmax of this one; P overwrites the front of its S.  Q lies in tensor
+// memory where O (D columns), two S (256) and two Q fit its 512 columns, else
+// (head size 256) in shared memory: tiles of 64 keys would make room, but the
+// products of 64 columns run at half the rate of those of 128.  Four warps bring
+// an item's queries to their place and pass each V piece on, cleaned where not
+// every row sees every key.
 //
-// The last role brings an item's queries into tensor memory and differs by the
-// cache's type.  bf16: four warps pass each V tile on; at the edges (keys that
-// not every row sees) they clean it first.  e4m3: tiles arrive raw in a ring of
-// their own, four warps turn K and four V into f16 (exact), cleaned the same
-// way, and the queries into f16 under a power of two per row.
+// e4m3 caches are multiplied as they are (kind::f8f6f4); the other operand is a
+// sum of two e4m3 terms.  A query row, scaled by a power of two that puts its
+// largest magnitude into [2^7, 2^8), is hi + lo with hi its nearest e4m3 value and
+// lo that of the rest: 4 + 4 significant bits, so exact for a bf16 value down to
+// 2^-10 of the largest and off by at most 2^-17 of the largest below.  The weights
+// are taken as 2^8 P = hi + lo: off by at most 2^-9 of their value, or 2^-18.
+// (Turning the tiles into f16 on the way instead, with eight more warps, was bound
+// by that step.)
 //
 // The running maximum that the exponents use follows the true one lazily: O is
-// rescaled only when a row's maximum grew by more than 2^8 (its weights are
-// then at most 2^8, harmless in bf16, f16 and the fp32 sum).
+// rescaled only when a row's maximum grew by more than 2^8 (its weights are then
+// at most 2^8, harmless in bf16 and the fp32 sum), e4m3: by more than 2^0.75
+// (2^8.75 is below 448).
 #pragma once
 #include "attn.cuh"
 
@@ -28,52 +37,67 @@ namespace vw4 {
 
 template <int D, bool F8, int ROWS>
 struct AttnTcShape {
-    static constexpr int kTK = D == 256 ? 64 : 128;  // keys of a tile
-    static constexpr int kHalf = kTK * D * 2;        // K or V of a tile, 16-bit operands
-    static constexpr int kBlk = kTK * 128;           // 64 dimensions of it
-    static constexpr int kRaw = kTK * D;             // e4m3 half before conversion
-    static constexpr int kNR = !F8 ? 0 : (D == 64 ? 8 : 5);
-    static constexpr int kNS = F8 ? 4 : (D == 64 ? 8 : 6);
-    static constexpr int kAuxWarps = F8 ? 8 : 4;     // converters, or cleaners
+    static constexpr int kTK = 128;                  // keys of a tile
+    static constexpr int kES = F8 ? 1 : 2;           // bytes of an element
+    static constexpr int kNP = D == 256 && !F8 ? 2 : 1;  // pieces of K, and of V
+    static constexpr int kPieces = 2 * kNP;          // of a tile
+    static constexpr int kPiece = kTK * D * kES / kNP;
+    static constexpr int kVKeys = kTK / kNP;         // keys of a V piece
+    static constexpr int kBoxB = D * kES < 128 ? D * kES : 128;  // bytes of a key in a box
+    static constexpr int kKBlks = D * kES / kNP / kBoxB;  // blocks of kBoxB bytes of a K piece
+    static constexpr int kVBlks = D * kES / kBoxB;
+    static constexpr int kKBlk = kTK * kBoxB, kVBlk = kVKeys * kBoxB;
+    static constexpr int kSteps = kBoxB / 32;        // k steps (32 bytes) of a block
+    static constexpr int kKeysPerStep = 32 / kES;    // of O += P V
+    static constexpr int kTerms = F8 ? 2 : 1;        // of Q, and of P
+    static constexpr bool kQSmem = D == 256;
+    static constexpr int kQRow = D * kES;            // bytes of a term of a query row
+    static constexpr int kQBlk = ROWS * kBoxB;
+    static constexpr int kQ = kQSmem ? ROWS * D * 2 : 0;
+    static constexpr int kNQ = kQSmem ? 1 : 2;       // query buffers
+    static constexpr int kNS = F8 ? (D == 64 ? 12 : (D == 128 ? 8 : (ROWS == 64 ? 5 : 4)))
+                                  : (D == 64 ? 8 : (D == 128 ? 6 : (ROWS == 64 ? 5 : 4)));
+    static constexpr int kAuxWarps = 4;
     static constexpr int kThreads = (6 + kAuxWarps) * 32;
-    static constexpr int kOffRaw = kNS * kHalf;
-    static constexpr int kOffStage = kOffRaw + kNR * kRaw;  // 4 KB a softmax warp, for the output
-    static constexpr int kSmem = kOffStage + 4 * 4096 + 1024;  // and alignment
-    static_assert(kSmem + 2048 <= 227 * 1024 && kSmem > 114 * 1024, "one CTA per SM");
+    static constexpr int kOffRing = kQ;
+    static constexpr int kOffStage = kOffRing + kNS * kPiece;  // 4 KB a softmax warp, for the output
+    static constexpr int kUsed = kOffStage + 4 * 4096 + 1024;  // and alignment
+    static constexpr int kSmem = kUsed < 115 * 1024 ? 115 * 1024 : kUsed;  // one CTA per SM
+    static_assert(kSmem + 2048 <= 227 * 1024, "shared memory");
+    // the products read 128 rows of Q whatever ROWS is: what follows must be there
+    static_assert(!kQSmem || kOffStage >= (kTerms * kQRow / kBoxB - 1) * kQBlk + 128 * kBoxB, "Q reads");
     // tensor memory columns: O, two S, the queries (two 16-bit values a column)
     static constexpr uint32_t kColO = 0, kColS = D, kColQ = D + 2 * kTK;
-    static constexpr int kNQ = D == 256 ? 1 : 2;
-    static_assert(D + 2 * kTK + kNQ * D / 2 <= 512, "tensor memory");
-    __device__ static __forceinline__ uint32_t at(int row, int chunk) {  // 16 bytes of an operand row
-        return static_cast<uint32_t>((chunk >> 3) * kBlk + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+    static_assert(D + 2 * kTK + (kQSmem ? 0 : kNQ * D / 2) <= 512, "tensor memory");
+    // 16 bytes of a row of a piece or of Q: blocks of blk bytes, rows of kBoxB in them
+    __device__ static __forceinline__ uint32_t at(int blk, int row, int chunk) {
+        constexpr int CPB = kBoxB / 16;
+        const int x = kBoxB == 64 ? (row >> 1) & 3 : row & 7;
+        return static_cast<uint32_t>(chunk / CPB * blk + row * kBoxB + (((chunk % CPB) ^ x) << 4));
     }
+    __device__ static __forceinline__ uint64_t desc(uint32_t addr, uint32_t lbo) {
+        return tc_desc<kBoxB>(addr, lbo, 8 * kBoxB);
+    }
+    static constexpr float kLazy = F8 ? 0.75f : 8.f;  // (log2) see above
+    static constexpr float kShift = F8 ? 8.f : 0.f;   // log2 of what P is multiplied by
 };
-
-constexpr float kLazy = 8.f;
-
-// The V halves are the odd ones: of a ring of ns slots, an even ns gives a slot
-// only halves of one kind (every ns-th half), an odd ns one V in two rounds.
-__host__ __device__ constexpr int attn_v_phase(int h, int ns) {
-    return ns % 2 == 0 ? h / ns : h / (2 * ns);
-}
 
 template <int D, bool F8, int ROWS>
 __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     attn_tc_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps) {
     using S = AttnTcShape<D, F8, ROWS>;
-    constexpr int TK = S::kTK, NS = S::kNS, NR = F8 ? S::kNR : 1;
+    constexpr int TK = S::kTK, NS = S::kNS, NP = S::kNP, PT = S::kPieces;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ volatile int s_odd[8];  // seg + 1: the part's values lost infinities or NaN
     __shared__ AttnUnit s_unit[kUnitRing];
-    // loaded (bf16) or converted (e4m3) halves, their release, cleaned V halves (bf16)
-    __shared__ __align__(8) uint64_t b_full[NS], b_empty[NS], b_clean[NS];
-    __shared__ __align__(8) uint64_t b_raw[NR], b_raw_empty[NR];
+    // loaded pieces, their release; V pieces passed on
+    __shared__ __align__(8) uint64_t b_full[NS], b_empty[NS], b_clean[8];
     __shared__ __align__(8) uint64_t b_s[2], b_p[2], b_pv, b_q[2], b_qe[2], b_part[8], b_o, b_end;
-    // log2 of the row scales of f16 queries, by part: the queries of part n + 4 wait for
-    // the last products of part n + 2 or later, whose scores wait for reads of part n
+    // log2 of the row scales of e4m3 queries, by part: those of part n + 4 are written
+    // after the last scores of part n + 2, which wait for the softmax of part n
     __shared__ int8_t s_rs[F8 ? 4 : 1][F8 ? ROWS : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row_warps = (p.tb * p.gb + 31) / 32;     // softmax warps with rows
@@ -87,13 +111,8 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         tmem_alloc<512>(&s_tmem);
         if (lane == 0) {
             for (int k = 0; k < NS; ++k) {
-                mbar_init(&b_full[k], F8 ? 4 : 1);
+                mbar_init(&b_full[k], 1);
                 mbar_init(&b_empty[k], 1);
-                mbar_init(&b_clean[k], 4);
-            }
-            for (int k = 0; k < NR; ++k) {
-                mbar_init(&b_raw[k], 1);
-                mbar_init(&b_raw_empty[k], 4);
             }
             for (int k = 0; k < 2; ++k) {
                 mbar_init(&b_s[k], 1);
@@ -101,7 +120,10 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 mbar_init(&b_q[k], row_warps);
                 mbar_init(&b_qe[k], 1);
             }
-            for (int k = 0; k < 8; ++k) mbar_init(&b_part[k], 1);
+            for (int k = 0; k < 8; ++k) {
+                mbar_init(&b_part[k], 1);
+                mbar_init(&b_clean[k], 4);
+            }
             mbar_init(&b_pv, 1);
             mbar_init(&b_o, row_warps);
             mbar_init(&b_end, 1);
@@ -128,17 +150,14 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         return __all_sync(0xffffffffu, wait(bar, phase)) != 0;
     };
 
-    // An item's queries into tensor memory: one row a thread of four warps.  For an
-    // e4m3 cache they become f16 under a power of two per row that puts the row's
-    // largest magnitude into [2^14, 2^15): exact for every value down to 2^-31 of it
-    // (bf16 has 8 significant bits, f16 11 and subnormals).
+    // An item's queries to their place: one row a thread of four warps.
     auto queries = [&](const AttnUnit& d, int qw) {
         const int qs = d.seg % S::kNQ, r = qw * 32 + lane;
         const AttnRow row = attn_row(p, d.g, r);
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q + (static_cast<long long>(d.b) * p.R + row.i) * p.ldq + static_cast<long long>(row.hq) * D);
-        uint4 v[D == 256 ? 16 : D / 8];  // half a row of 256, else a row
-        constexpr int NV = D == 256 ? 16 : D / 8;
+        constexpr int NV = D == 256 ? 16 : D / 8;  // half a row of 256, else a row
+        uint4 v[NV];
         float up = 1.f;
         auto get = [&](int from) {
 #pragma unroll
@@ -159,38 +178,67 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 }
             }
             const int ex = static_cast<int>(mx >> 7);
-            int sh = ex == 0 || ex == 255 ? 0 : 127 + 14 - ex;
+            int sh = ex == 0 || ex == 255 ? 0 : 127 + 7 - ex;  // to [2^7, 2^8)
             sh = max(-126, min(126, sh));
-            up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-            if (r < ROWS)
-                s_rs[F8 ? d.seg & 3 : 0][F8 ? r : 0] = static_cast<int8_t>(sh);
+            // (a row with an infinity or NaN is made NaN: e4m3 has no infinity)
+            up = ex == 255 ? NAN : __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+            if (r < ROWS) s_rs[F8 ? d.seg & 3 : 0][F8 ? r : 0] = static_cast<int8_t>(sh);
         } else {
             get(0);
         }
         if (d.seg >= S::kNQ && !warp_wait(&b_qe[qs], d.seg / S::kNQ - 1)) return false;
         tc_fence_after();
+        const uint32_t tq = tmem + (static_cast<uint32_t>(qw * 32) << 16) + S::kColQ + qs * (D / 2);
 #pragma unroll 1
         for (int from = 0; from < D / 8; from += NV) {
             if (F8 || from > 0) get(from);
 #pragma unroll
-            for (int c = 0; c < NV; c += 8) {
+            for (int c = 0; c < NV; c += 8) {  // 64 dimensions
                 uint32_t y[32];
+                if (F8) {  // hi: y[0 .. 15], lo: y[16 .. 31]
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint4 t = v[c + k];
-                    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t w[4] = {v[c + k].x, v[c + k].y, v[c + k].z, v[c + k].w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        y[4 * k + e] = F8 ? pack2<true>(__uint_as_float(w[e] << 16) * up,
-                                                        __uint_as_float(w[e] & 0xffff0000u) * up)
-                                          : w[e];
+                        for (int e = 0; e < 4; e += 2)
+                            e4m3_terms(pack2<true>(__uint_as_float(w[e] << 16) * up,
+                                                   __uint_as_float(w[e] & 0xffff0000u) * up),
+                                       pack2<true>(__uint_as_float(w[e + 1] << 16) * up,
+                                                   __uint_as_float(w[e + 1] & 0xffff0000u) * up),
+                                       y[2 * k + e / 2], y[16 + 2 * k + e / 2]);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        y[4 * k] = v[c + k].x;
+                        y[4 * k + 1] = v[c + k].y;
+                        y[4 * k + 2] = v[c + k].z;
+                        y[4 * k + 3] = v[c + k].w;
+                    }
                 }
-                tmem_st32(tmem + (static_cast<uint32_t>(qw * 32) << 16) + S::kColQ + qs * (D / 2) +
-                              (from + c) * 4, y);
+                if (S::kQSmem) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        // e4m3: four chunks of 16 dimensions of either term
+                        const int chunk = F8 ? (k >> 2) * (D / 16) + (from + c) / 2 + (k & 3) : from + c + k;
+                        if (r < ROWS)
+                            *reinterpret_cast<uint4*>(smem + S::at(S::kQBlk, r, chunk)) =
+                                make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                    }
+                } else if (F8) {
+                    tmem_st16(tq + (from + c) * 2, y);
+                    tmem_st16(tq + D / 4 + (from + c) * 2, y + 16);
+                } else {
+                    tmem_st32(tq + (from + c) * 4, y);
+                }
             }
         }
-        tmem_st_wait();
-        tc_fence_before();
+        if (S::kQSmem) {
+            fence_async_smem();
+        } else {
+            tmem_st_wait();
+            tc_fence_before();
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&b_q[qs]);
         return true;
@@ -198,74 +246,82 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
 
     if (n_units > 0 && warp == 5) {
         // -------------------------------------------------------- producer
-        constexpr int NB = F8 ? 1 : D / 64, BOXB = F8 ? D : 128;  // boxes across a key
-        constexpr int NL = F8 ? NR : NS;                          // ring that is loaded
-        uint64_t* full = F8 ? b_raw : b_full;
-        uint64_t* empty = F8 ? b_raw_empty : b_empty;
+        constexpr int ESZ = S::kES, BOXB = S::kBoxB, KB = S::kKBlks, VB = S::kVBlks;
         AttnWalk<TK> w;
         w.begin(p, span, cap, lane);
-        int hl = 0;  // halves loaded
+        int hl = 0;  // pieces loaded
         bool ok = true;
+        // the next piece's place, once it is free; its bytes are announced
+        auto place = [&](uint32_t bytes) {
+            const int st = hl % NS;
+            ok = hl < NS || warp_wait(&b_empty[st], hl / NS - 1);
+            if (ok && lane == 0) mbar_arrive_expect_tx(&b_full[st], bytes);
+            __syncwarp();
+            return sm + S::kOffRing + st * S::kPiece;
+        };
         for (int u = 0; u < n_units; ++u) {
             const AttnUnit d = w.unit(p);
-            const uint32_t bytes = w.template bytes<NB, BOXB>();
             if (lane == 0) {
                 s_unit[u % kUnitRing] = d;
                 if (d.flags & kUnitFirst) mbar_arrive(&b_part[d.seg & 7]);  // its queries may be read
             }
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                const int st = hl % NL;
-                ok = hl < NL || warp_wait(&empty[st], hl / NL - 1);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
-                __syncwarp();
-                w.template load<NB, BOXB, F8 ? 1 : 2>(
-                    p, half ? &maps.v : &maps.k,
-                    sm + (F8 ? S::kOffRaw + st * S::kRaw : st * S::kHalf), &full[st], lane);
-                ++hl;
-            }
+            uint32_t dst = place(w.template bytes<0, TK, KB, BOXB>(lane));
             if (!ok) break;
+            w.template load<0, TK, 0, KB, BOXB, ESZ>(p, &maps.k, dst, &b_full[hl++ % NS], lane);
+            if (NP == 2) {
+                dst = place(w.template bytes<0, TK, KB, BOXB>(lane));
+                if (!ok) break;
+                w.template load<0, TK, KB, KB, BOXB, ESZ>(p, &maps.k, dst, &b_full[hl++ % NS], lane);
+            }
+            dst = place(w.template bytes<0, S::kVKeys, VB, BOXB>(lane));
+            if (!ok) break;
+            w.template load<0, S::kVKeys, 0, VB, BOXB, ESZ>(p, &maps.v, dst, &b_full[hl++ % NS], lane);
+            if (NP == 2) {
+                dst = place(w.template bytes<S::kVKeys, S::kVKeys, VB, BOXB>(lane));
+                if (!ok) break;
+                w.template load<S::kVKeys, S::kVKeys, 0, VB, BOXB, ESZ>(p, &maps.v, dst,
+                                                                       &b_full[hl++ % NS], lane);
+            }
             if (u + 1 < n_units) w.next(p, lane);
         }
         if (!ok) {  // copies in flight land before the block ends
-            for (int k = hl > NL ? hl - NL : 0; k < hl; ++k)
-                mbar_wait_bounded(&full[k % NL], (k / NL) & 1, p.wait_ns, nullptr);
+            for (int k = hl > NS ? hl - NS : 0; k < hl; ++k)
+                mbar_wait_bounded(&b_full[k % NS], (k / NS) & 1, p.wait_ns, nullptr);
         }
     } else if (n_units > 0 && warp >= 6) {
-        // ----------------------------------------- cleaners or converters
-        // Four warps a group; group 0 also brings the queries (its warps reach all
-        // lanes of tensor memory: 32 (warp % 4) ..).  e4m3: group 0 has K, group 1 V.
-        constexpr int N = 128;
-        const int group = (warp - 6) >> 2, at = (tid - 192) & 127, half = F8 ? group : 1;
-        const int qw = warp & 3;
-        bool first = true;
+        // ------------------------------------- queries in, V pieces passed on
+        const int at = tid - 192, qw = warp & 3;  // (a warp reaches lanes 32 (warp % 4) ..)
+        bool first = true, ok = true;
         int parts = 0;
-        for (int u = 0; u < n_units; ++u) {
-            const int hh = 2 * u + half, st = hh % NS, sr = hh % NR;
-            if (first) {
-                if (group == 0 && qw < row_warps) {
-                    if (!warp_wait(&b_part[parts & 7], parts >> 3)) break;
-                    const AttnUnit d = s_unit[u % kUnitRing];
-                    if (!queries(d, qw)) break;
-                }
-                ++parts;
+        for (int u = 0; u < n_units && ok; ++u) {
+            if (first && qw < row_warps) {
+                ok = warp_wait(&b_part[parts & 7], parts >> 3);
+                if (!ok) break;
+                const AttnUnit d = s_unit[u % kUnitRing];
+                ok = queries(d, qw);
+                if (!ok) break;
             }
-            if (!warp_wait(F8 ? &b_raw[sr] : &b_full[st], F8 ? hh / NR : hh / NS)) break;
-            const AttnUnit d = s_unit[u % kUnitRing];
-            first = d.flags & kUnitLast;  // (of the next unit)
-            const bool clean = half == 1 && (d.flags & kUnitEdge);
-            if (!F8) {
-                if (clean) {
+            parts += first;
+#pragma unroll 1
+            for (int i = 0; i < NP; ++i) {
+                const int pc = u * PT + NP + i, st = pc % NS;
+                ok = warp_wait(&b_full[st], pc / NS);
+                if (!ok) break;
+                const AttnUnit d = s_unit[u % kUnitRing];
+                first = d.flags & kUnitLast;  // (of the next unit)
+                if (d.flags & kUnitEdge) {
                     // Values that no row sees become zeros; infinities and NaN of values
                     // that only some rows see too (0 times them must not reach the other
                     // rows): the end of the part gives them to the rows that see them.
+                    const int key0 = d.start + i * S::kVKeys;
+                    constexpr int CH = D * S::kES / 16;
                     bool odd = false;
 #pragma unroll 1
-                    for (int c = at; c < TK * (D / 8); c += N) {
-                        const int row = c / (D / 8), j = d.start + row;
+                    for (int c = at; c < S::kVKeys * CH; c += S::kAuxWarps * 32) {
+                        const int row = c / CH, j = key0 + row;
                         if (key_all(j, d.len, d.p0, p.window, p.sinks)) continue;
-                        uint4* q = reinterpret_cast<uint4*>(smem + st * S::kHalf + S::at(row, c % (D / 8)));
+                        uint4* q = reinterpret_cast<uint4*>(smem + S::kOffRing + st * S::kPiece +
+                                                            S::at(S::kVBlk, row, c % CH));
                         if (!key_some(j, d.len, d.p0, p.window, p.sinks)) {
                             *q = make_uint4(0, 0, 0, 0);
                             continue;
@@ -275,8 +331,14 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                         bool hit = false;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xffff0000u, hit = true;
-                            if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xffffu, hit = true;
+                            if (F8) {
+#pragma unroll
+                                for (int k = 0; k < 32; k += 8)
+                                    if (((w[e] >> k) & 0x7Fu) == 0x7Fu) w[e] &= ~(0xFFu << k), hit = true;
+                            } else {
+                                if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xffff0000u, hit = true;
+                                if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xffffu, hit = true;
+                            }
                         }
                         if (hit) *q = make_uint4(w[0], w[1], w[2], w[3]);
                         odd |= hit;
@@ -285,53 +347,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                     fence_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&b_clean[st]);
-            } else {
-                if (hh >= NS && !warp_wait(&b_empty[st], hh / NS - 1)) break;
-                const uint8_t* src = smem + S::kOffRaw + sr * S::kRaw;
-                uint8_t* dst = smem + st * S::kHalf;
-                bool odd = false;
-                constexpr int CH = D / 16;
-#pragma unroll 4
-                for (int i = 0; i < TK * CH / N; ++i) {
-                    const int c = at + i * N, row = c / CH, ch = c % CH;
-                    const uint4 v = *reinterpret_cast<const uint4*>(src + c * 16);
-                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    if (clean) {  // (as above)
-                        const int j = d.start + row;
-                        if (!key_some(j, d.len, d.p0, p.window, p.sinks)) {
-                            w[0] = w[1] = w[2] = w[3] = 0u;
-                        } else if (!key_all(j, d.len, d.p0, p.window, p.sinks)) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                                for (int q = 0; q < 32; q += 8)
-                                    if (((w[e] >> q) & 0x7Fu) == 0x7Fu) {
-                                        w[e] &= ~(0xFFu << q);
-                                        odd = true;
-                                    }
-                        }
-                    }
-                    uint32_t f[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        f[2 * e] = e4m3x2_f16x2(w[e]);
-                        f[2 * e + 1] = e4m3x2_f16x2(w[e] >> 16);
-                    }
-                    // lanes of neighbouring 64-dimension blocks write their two chunks in
-                    // opposite order: eight lanes then cover all banks
-                    const int flip = (ch >> 2) & 1;
-                    uint4 a = make_uint4(f[0], f[1], f[2], f[3]), b = make_uint4(f[4], f[5], f[6], f[7]);
-                    *reinterpret_cast<uint4*>(dst + S::at(row, 2 * ch + flip)) = flip ? b : a;
-                    *reinterpret_cast<uint4*>(dst + S::at(row, 2 * ch + 1 - flip)) = flip ? a : b;
-                }
-                if (odd) s_odd[d.seg & 7] = d.seg + 1;
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&b_full[st]);
-                    mbar_arrive(&b_raw_empty[sr]);
-                }
+                if (lane == 0) mbar_arrive(&b_clean[(u * NP + i) & 7]);
             }
         }
     } else if (n_units > 0 && warp == 4) {
@@ -339,52 +355,74 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         if (lane == 0) {
             constexpr uint32_t iS = tc_idesc(!F8, 128, TK, false), iO = tc_idesc(!F8, 128, D, true);
             int fl[2] = {0, 0}, parts = 0;
-            int qk = 0, pv = 0;   // next tile of either product
-            bool k_in = false;    // the next K tile has arrived (its unit is known)
+            int qk = 0, kp = 0, pv = 0, vp = 0;  // next tile and piece of either product
             uint64_t t0 = 0;
             while (pv < n_units) {
                 // S of tile qk takes the buffer of tile qk - 2, whose P has been read
                 if (qk < n_units && qk <= pv + 1) {
-                    const int hk = 2 * qk;
-                    k_in = k_in || mbar_test(&b_full[hk % NS], (hk / NS) & 1);
-                    const AttnUnit* d = &s_unit[qk % kUnitRing];
-                    const int seg = k_in ? d->seg : 0, qs = seg % S::kNQ;
-                    if (k_in && (!(d->flags & kUnitFirst) || mbar_test(&b_q[qs], (seg / S::kNQ) & 1))) {
-                        tc_fence_after();
-                        const uint32_t k = sm + (hk % NS) * S::kHalf;
+                    const int pc = qk * PT + kp, st = pc % NS;
+                    if (mbar_test(&b_full[st], (pc / NS) & 1)) {
+                        const AttnUnit* d = &s_unit[qk % kUnitRing];
+                        const int flags = d->flags, seg = d->seg, qs = seg % S::kNQ;
+                        if (kp > 0 || !(flags & kUnitFirst) || mbar_test(&b_q[qs], (seg / S::kNQ) & 1)) {
+                            tc_fence_after();
+                            const uint32_t k = sm + S::kOffRing + st * S::kPiece;
+                            const uint32_t dS = tmem + S::kColS + (qk & 1) * TK;
+                            constexpr int KS = S::kKBlks * S::kSteps;  // k steps of the piece
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            tc_mma_ts(tmem + S::kColS + (qk & 1) * TK,
-                                      tmem + S::kColQ + qs * (D / 2) + ks * 8,
-                                      tc_desc(k + (ks >> 2) * S::kBlk + (ks & 3) * 32, 16, 1024), iS,
-                                      ks > 0);
-                        tc_commit(&b_s[qk & 1]);
-                        tc_commit(&b_empty[hk % NS]);
-                        if (d->flags & kUnitLast) tc_commit(&b_qe[qs]);
-                        fl[qk & 1] = d->flags;
-                        ++qk;
-                        k_in = false;
-                        t0 = 0;
-                        continue;
+                            for (int t = 0; t < S::kTerms; ++t)
+#pragma unroll
+                                for (int ks = 0; ks < KS; ++ks) {
+                                    const uint64_t kd = S::desc(
+                                        k + (ks / S::kSteps) * S::kKBlk + (ks % S::kSteps) * 32, 16);
+                                    const int kq = t * (S::kQRow / 32) + kp * KS + ks;  // k step of Q
+                                    const bool add = t > 0 || kp > 0 || ks > 0;
+                                    if (S::kQSmem)
+                                        tc_mma_ss<F8>(dS,
+                                                      S::desc(sm + (kq / S::kSteps) * S::kQBlk +
+                                                                  (kq % S::kSteps) * 32, 16),
+                                                      kd, iS, add);
+                                    else
+                                        tc_mma_ts<F8>(dS, tmem + S::kColQ + qs * (D / 2) + kq * 8, kd, iS, add);
+                                }
+                            tc_commit(&b_empty[st]);
+                            if (++kp == NP) {
+                                tc_commit(&b_s[qk & 1]);
+                                if (flags & kUnitLast) tc_commit(&b_qe[qs]);
+                                fl[qk & 1] = flags;
+                                kp = 0;
+                                ++qk;
+                            }
+                            t0 = 0;
+                            continue;
+                        }
                     }
                 }
                 if (pv < qk) {
-                    const int hv = 2 * pv + 1;
+                    const int pc = pv * PT + NP + vp, st = pc % NS, vs = pv * NP + vp;
                     const bool first = fl[pv & 1] & kUnitFirst;
-                    if (mbar_test(&b_p[pv & 1], (pv >> 1) & 1) &&
-                        mbar_test(F8 ? &b_full[hv % NS] : &b_clean[hv % NS],
-                                  (F8 ? hv / NS : attn_v_phase(hv, NS)) & 1) &&
-                        (!first || parts == 0 || mbar_test(&b_o, (parts - 1) & 1))) {  // O was read
+                    if (mbar_test(&b_clean[vs & 7], (vs >> 3) & 1) &&
+                        (vp > 0 || (mbar_test(&b_p[pv & 1], (pv >> 1) & 1) &&
+                                    (!first || parts == 0 || mbar_test(&b_o, (parts - 1) & 1))))) {
                         tc_fence_after();
-                        const uint32_t v = sm + (hv % NS) * S::kHalf;
+                        const uint32_t v = sm + S::kOffRing + st * S::kPiece;
+                        constexpr int KS = S::kVKeys / S::kKeysPerStep;
 #pragma unroll
-                        for (int ks = 0; ks < TK / 16; ++ks)
-                            tc_mma_ts(tmem + S::kColO, tmem + S::kColS + (pv & 1) * TK + ks * 8,
-                                      tc_desc(v + ks * 2048, S::kBlk, 1024), iO, !(first && ks == 0));
-                        tc_commit(&b_empty[hv % NS]);
-                        tc_commit(&b_pv);
-                        parts += first;
-                        ++pv;
+                        for (int t = 0; t < S::kTerms; ++t)
+#pragma unroll
+                            for (int ks = 0; ks < KS; ++ks)
+                                tc_mma_ts<F8>(tmem + S::kColO,
+                                              tmem + S::kColS + (pv & 1) * TK +
+                                                  (t * (TK / S::kKeysPerStep) + vp * KS + ks) * 8,
+                                              S::desc(v + ks * (S::kKeysPerStep * S::kBoxB), S::kVBlk), iO,
+                                              !(first && t == 0 && vp == 0 && ks == 0));
+                        tc_commit(&b_empty[st]);
+                        if (++vp == NP) {
+                            tc_commit(&b_pv);
+                            parts += first;
+                            vp = 0;
+                            ++pv;
+                        }
                         t0 = 0;
                         continue;
                     }
@@ -460,7 +498,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             float corr = 1.f;
             if (first) {
                 m = mx;
-            } else if ((mx - m) * c2 > kLazy) {
+            } else if ((mx - m) * c2 > S::kLazy) {
                 // (m = -infinity: O and l are zeros still)
                 if (m != -INFINITY) {
                     corr = ex2((m - mx) * c2);
@@ -482,21 +520,36 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                     tmem_st32(tO + c, y);
                 }
             }
-            const float mc = m == -INFINITY ? 0.f : m * c2;
+            const float mc = m == -INFINITY ? 0.f : m * c2 - S::kShift;
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll
             for (int c = 0; c < TK; c += 64) {
                 if (c > 0) masked(c);
                 uint32_t y[32];
+                if (F8) {  // hi: y[0 .. 15], lo: y[16 .. 31]
 #pragma unroll
-                for (int k = 0; k < 64; k += 2) {
-                    const float a = ex2(fmaf(__uint_as_float(x[k]), c2, -mc));
-                    const float b = ex2(fmaf(__uint_as_float(x[k + 1]), c2, -mc));
-                    s0 += a;
-                    s1 += b;
-                    y[k / 2] = pack2<F8>(a, b);
+                    for (int k = 0; k < 64; k += 4) {
+                        float e[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) e[q] = ex2(fmaf(__uint_as_float(x[k + q]), c2, -mc));
+                        s0 += e[0] + e[1];
+                        s1 += e[2] + e[3];
+                        e4m3_terms(pack2<true>(e[0], e[1]), pack2<true>(e[2], e[3]), y[k / 4],
+                                   y[16 + k / 4]);
+                    }
+                    tmem_st16(tS + c / 4, y);
+                    tmem_st16(tS + TK / 4 + c / 4, y + 16);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 64; k += 2) {
+                        const float a = ex2(fmaf(__uint_as_float(x[k]), c2, -mc));
+                        const float b = ex2(fmaf(__uint_as_float(x[k + 1]), c2, -mc));
+                        s0 += a;
+                        s1 += b;
+                        y[k / 2] = pack2<false>(a, b);
+                    }
+                    tmem_st32(tS + c / 2, y);
                 }
-                tmem_st32(tS + c / 2, y);
             }
             l += s0 + s1;
             tmem_st_wait();
@@ -523,7 +576,11 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                              : (orow * p.ldo + static_cast<long long>(row.hq) * D) * 2;
             uint8_t* dst_base = td.slot >= 0 ? reinterpret_cast<uint8_t*>(p.partial)
                                              : reinterpret_cast<uint8_t*>(p.out);
-            const int my_row = live ? 1 : 0;
+            // the rows that this lane writes, as offsets in 16 bytes (rows start on 16)
+            const uint32_t mine = live ? static_cast<uint32_t>(dst_row >> 4) : 0xffffffffu;
+            uint32_t to[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) to[k] = __shfl_sync(0xffffffffu, mine, k * 4 + (lane >> 3));
             uint8_t* stage = smem + S::kOffStage + warp * 4096;
             const int width = td.slot >= 0 ? 32 : 64;  // columns a line
 #pragma unroll 1
@@ -585,10 +642,9 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const int rr = k * 4 + (lane >> 3);
-                    const long long to = __shfl_sync(0xffffffffu, dst_row, rr);
-                    const int on = __shfl_sync(0xffffffffu, my_row, rr);
-                    if (on)
-                        *reinterpret_cast<uint4*>(dst_base + to + (c / width) * 128 + (lane & 7) * 16) =
+                    if (to[k] != 0xffffffffu)
+                        *reinterpret_cast<uint4*>(dst_base + (static_cast<long long>(to[k]) << 4) +
+                                                  (c / width) * 128 + (lane & 7) * 16) =
                             *reinterpret_cast<const uint4*>(stage + rr * 128 +
                                                             (((lane & 7) ^ (rr & 7)) << 4));
                 }

@@ -186,26 +186,54 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
                      smem_u32(bar))
                  : "memory");
 }
-// Shared-memory operand in 128-byte swizzled atoms of 8 rows (1024 bytes).
-// sbo: bytes between 8-row groups; lbo: bytes between 64-element blocks along
-// the contiguous dimension (read for operands contiguous along M or N only).
+// Shared-memory operand in atoms of 8 rows of ROWB bytes (128 or 64, swizzled
+// over that width).  sbo: bytes between 8-row groups; lbo: bytes between blocks of
+// ROWB bytes along the contiguous dimension (read for operands contiguous along M
+// or N only).
+template <int ROWB>
 __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    static_assert(ROWB == 128 || ROWB == 64, "128- or 64-byte swizzle");
     return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-           (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
+           (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | ((ROWB == 128 ? 2ull : 4ull) << 61);
 }
-// 16-bit operands (both f16 or both bf16), f32 accumulators, M x N tile
+// M x N tile of f32 accumulators; A and B both bf16 (kind::f16) or both e4m3
+// (kind::f8f6f4)
 __host__ __device__ constexpr uint32_t tc_idesc(bool bf16, int M, int N, bool b_n_major) {
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_n_major ? 1u << 16 : 0u) |
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// A from tensor memory (two 16-bit values a column)
+template <bool F8>
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          bool add) {
+    if (F8)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+            : "memory");
+}
+// A from tensor memory (32 bits of a row of A a column)
+template <bool F8>
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                           bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
-        : "memory");
+    if (F8)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+            : "memory");
 }
 // 32 columns of this thread's lane; the values are there when it returns
 __device__ __forceinline__ void tmem_ld32(uint32_t* r, uint32_t a) {
@@ -260,6 +288,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
 }
 // makes this thread's shared-memory writes visible to the tensor cores
 __device__ __forceinline__ void fence_async_smem() {

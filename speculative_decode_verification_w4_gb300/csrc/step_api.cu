@@ -172,7 +172,7 @@ VW4_API vw4_status verify_attn(const vw4_attn* a, void* workspace_dev, size_t ws
                                   static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(c.num_pages)};
         const uint64_t strides[3] = {valid(c.head_stride), valid(c.token_stride), valid(c.page_stride)};
         const uint32_t box[4] = {static_cast<uint32_t>(plan.box_bytes / (f8 ? 1 : 2)), 1u,
-                                 static_cast<uint32_t>(plan.box_rows), 1u};
+                                 static_cast<uint32_t>(p.box_rows), 1u};
         st = static_cast<vw4_status>(encode_map(&maps.k, !f8, 4, c.k_dev, dims, strides, box, plan.swizzle));
         if (st != VW4_OK) return st;
         st = static_cast<vw4_status>(encode_map(&maps.v, !f8, 4, c.v_dev, dims, strides, box, plan.swizzle));

@@ -233,6 +233,7 @@ struct AttnParams {
     int B, R, Hq, Hkv, G;   // G: query heads of a key head
     int window, sinks;
     int page_size, page_shift, max_blocks, num_pages;
+    int box_rows;           // tokens of a TMA box
     // the query rows of a key head in blocks of tb verify indexes x gb heads:
     // blocks_g of them along the heads, row_blocks in all; groups = Hkv * row_blocks
     int tb, gb, blocks_g, row_blocks, groups;
@@ -247,7 +248,7 @@ size_t attn_workspace_bytes(int B, int rows, int D);
 // Plans a call: block shape, grid bound and workspace pointers in p.
 struct AttnPlan {
     int rows, tk, grid;
-    int box_rows, box_bytes;   // of K and V: tokens, bytes of a key
+    int box_bytes;             // bytes of a key in a box of K or V
     CUtensorMapSwizzle swizzle;
 };
 AttnPlan attn_plan(AttnParams& p, int D, bool f8, void* ws);

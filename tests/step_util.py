@@ -79,9 +79,11 @@ def attention64(q, k, v, n, scale, window, sinks, kv):
     how far a kernel may be from them.
 
     The tolerance counts the roundings: half a step of bf16 on the output; the
-    weights' half step (bf16 2^-8, f16 2^-11, and f16's 2^-25 below its normal
-    range) on sum(p |v|); the scores' fp32 error delta = 2 D 2^-24 scale
-    sum|q k|, plus 2^-22 of the exponent, on every weight."""
+    weights' half step on sum(p |v|): bf16 2^-8; e4m3 caches with up to 16 rows
+    a key head f16, 2^-11 and 2^-25 below its normal range; with more rows two
+    e4m3 terms of 2^8 p, 2^-9 + 2^-12 and 2^-18; the scores' fp32 error delta =
+    2 D 2^-24 scale sum|q k|, plus 2^-22 of the exponent, on every weight; the
+    queries' two e4m3 terms, 2^-17 of the row's largest, on every score."""
     R, Hq, D = q.shape
     Hkv = k.shape[1] if n else 1
     out = torch.zeros(R, Hq, D, dtype=torch.float64)
@@ -91,7 +93,10 @@ def attention64(q, k, v, n, scale, window, sinks, kv):
         return out, lse, tol, tol_lse
     G = Hq // Hkv
     vis = seen(n, R, window, sinks)
+    terms = kv == "e4m3" and R * G > 16
     wp, tiny = (2 ** -8, 0.0) if kv == "bf16" else (2 ** -11, 2 ** -25)
+    if terms:
+        wp, tiny = 2 ** -9 + 2 ** -12, 2 ** -18
     for i in range(R):
         sel = torch.nonzero(vis[i])[:, 0]
         if len(sel) == 0:
@@ -108,6 +113,9 @@ def attention64(q, k, v, n, scale, window, sinks, kv):
         o = heads(p / z, vi, "kgt,tkd->kgd")
         a = heads(p / z, vi.abs(), "kgt,tkd->kgd")
         delta = 2 * D * 2.0 ** -24 * mag + 2.0 ** -22 * (2 * s.abs().amax(1) + 1)
+        if terms:
+            k1 = ki.abs().sum(2).amax(0).repeat_interleave(G)  # largest sum|k| of the key head
+            delta = delta + 2.0 ** -17 * q[i].abs().amax(1) * k1 * scale
         out[i], lse[i] = o, (m + z.log())[:, 0]
         tol[i] = (2 ** -8 * o.abs() + wp * a + 2 * delta[:, None] * a
                   + tiny * vi.abs().sum(0).repeat_interleave(G, 0) / z + 1e-30)
