@@ -93,9 +93,12 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     __shared__ volatile int s_abort;
     __shared__ volatile int s_odd[8];  // seg + 1: the part's values lost infinities or NaN
     __shared__ AttnUnit s_unit[kUnitRing];
-    // loaded pieces, their release; V pieces passed on
+    // A wait names a phase by its parity: when it begins, the phase before has to be over
+    // and the one after not.  So products and scores have two barriers each, taken in
+    // turn: S of tile u is committed after the product of tile u - 2.
+    // Loaded pieces, their release; V pieces passed on:
     __shared__ __align__(8) uint64_t b_full[NS], b_empty[NS], b_clean[8];
-    __shared__ __align__(8) uint64_t b_s[2], b_p[2], b_pv, b_q[2], b_qe[2], b_part[8], b_o, b_end;
+    __shared__ __align__(8) uint64_t b_s[2], b_p[2], b_pv[2], b_q[2], b_qe[2], b_part[8], b_o, b_end;
     // log2 of the row scales of e4m3 queries, by part: those of part n + 4 are written
     // after the last scores of part n + 2, which wait for the softmax of part n
     __shared__ int8_t s_rs[F8 ? 4 : 1][F8 ? ROWS : 1];
@@ -116,6 +119,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             }
             for (int k = 0; k < 2; ++k) {
                 mbar_init(&b_s[k], 1);
+                mbar_init(&b_pv[k], 1);
                 mbar_init(&b_p[k], row_warps);
                 mbar_init(&b_q[k], row_warps);
                 mbar_init(&b_qe[k], 1);
@@ -124,7 +128,6 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 mbar_init(&b_part[k], 1);
                 mbar_init(&b_clean[k], 4);
             }
-            mbar_init(&b_pv, 1);
             mbar_init(&b_o, row_warps);
             mbar_init(&b_end, 1);
             fence_barrier_init();
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                                               !(first && t == 0 && vp == 0 && ks == 0));
                         tc_commit(&b_empty[st]);
                         if (++vp == NP) {
-                            tc_commit(&b_pv);
+                            tc_commit(&b_pv[pv & 1]);
                             parts += first;
                             vp = 0;
                             ++pv;
@@ -508,7 +511,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 m = mx;
             }
             if (__any_sync(0xffffffffu, grow)) {
-                if (!warp_wait(&b_pv, u - 1)) break;
+                if (!warp_wait(&b_pv[(u - 1) & 1], (u - 1) >> 1)) break;
                 tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
@@ -559,9 +562,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             if (!(td.flags & kUnitLast)) continue;
 
             // ---- end of the segment
-            // A wait names a phase by its parity, so the one before it must be known to be
-            // over: S of tile u was committed after the product of tile u - 2.
-            if ((u > 0 && !warp_wait(&b_pv, u - 1)) || !warp_wait(&b_pv, u)) break;
+            if (!warp_wait(&b_pv[u & 1], u >> 1)) break;
             tc_fence_after();
             const bool live = row.live, odd = s_odd[td.seg & 7] == td.seg + 1;
             const float mm = m == -INFINITY ? -INFINITY : mc;

@@ -80,6 +80,30 @@ def test_many_windows_per_block(R, G, D, kv):
     run_case(62, [700 + 61 * b for b in range(40)], R, 2 * G, 2, D, 16, kv, window=500, sinks=5)
 
 
+@pytest.mark.parametrize("D,R,G,kv", [(128, 16, 8, "bf16"), (256, 8, 6, "bf16"), (256, 4, 6, "e4m3"),
+                                      (64, 9, 8, "e4m3"), (128, 1, 4, "e4m3")])
+def test_calls_one_after_another(D, R, G, kv):
+    """Two calls in turn, 300 times with nothing waiting between: the same bits as
+    alone, and no wait ran out."""
+    calls, outs, alone = [], [], []
+    for k, lens in enumerate(([9000 + 77 * b for b in range(8)], [500 + 7 * b for b in range(30)])):
+        c, _, _ = make_cache(70 + k, lens, 32, 2, D, kv)
+        g = torch.Generator().manual_seed(k)
+        q = torch.randn(len(lens), R, 2 * G, D, generator=g).to(torch.bfloat16).cuda()
+        out = torch.empty_like(q)
+        calls.append(vw4.PreparedAttn(q, c, torch.tensor(lens, dtype=torch.int32, device="cuda"), out=out))
+        calls[-1]()
+        torch.cuda.synchronize()
+        outs.append(out)
+        alone.append(out.clone())
+    for _ in range(300):
+        for c in calls:
+            c()
+    status()
+    for a, b in zip(outs, alone):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
 def test_many_sequences():
     lens = [(37 * b) % 301 for b in range(300)]
     run_case(5, lens, 2, 4, 2, 64, 16, "bf16")
