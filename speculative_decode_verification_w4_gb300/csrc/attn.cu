@@ -5,9 +5,12 @@
 namespace vw4 {
 
 // Query rows of a block: the smallest kernel shape that holds a key head's
-// rows; more than 128 are cut into blocks, each reading the keys again (from
-// L2: the blocks of a key head are neighbours in the schedule).
-static int attn_rows(int rows) { return rows <= 16 ? 16 : (rows <= 64 ? 64 : 128); }
+// rows; more than 128 (64: e4m3 at head size 256, whose f16 ring leaves no room
+// for more queries) are cut into blocks, each reading the keys again (from L2: the
+// blocks of a key head are neighbours in the schedule).
+static int attn_rows(int rows, int D, bool f8) {
+    return rows <= 16 ? 16 : (rows <= 64 || (D == 256 && f8) ? 64 : 128);
+}
 // keys of a tile of the kernel for blocks of that many rows
 static int attn_tile(int rows, bool f8) { return rows == 16 && !f8 ? 64 : 128; }
 
@@ -17,7 +20,7 @@ static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 size_t attn_workspace_bytes(int B, int rows, int D) {
     const size_t base = align256((static_cast<size_t>(B) + 1) * sizeof(long long));
-    return base + align256(2u * static_cast<size_t>(attn_grid_cap(D)) * attn_rows(rows) * (D + 2) *
+    return base + align256(2u * static_cast<size_t>(attn_grid_cap(D)) * attn_rows(rows, D, false) * (D + 2) *
                            sizeof(float));
 }
 
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
 AttnPlan attn_plan(AttnParams& p, int D, bool f8, void* ws) {
     AttnPlan plan;
     const int total = p.R * p.G;
-    plan.rows = attn_rows(total);
+    plan.rows = attn_rows(total, D, f8);
     plan.tk = attn_tile(plan.rows, f8);
     p.gb = p.G < plan.rows ? p.G : plan.rows;
     p.tb = plan.rows / p.gb < p.R ? plan.rows / p.gb : p.R;
@@ -134,7 +137,7 @@ AttnPlan attn_plan(AttnParams& p, int D, bool f8, void* ws) {
     plan.grid = attn_grid_cap(D);
     if (units < plan.grid) plan.grid = static_cast<int>(units < 1 ? 1 : units);
     // a box lies inside a page and inside a ring piece of the kernel
-    const int piece = plan.rows > 16 && D == 256 && !f8 ? 64 : plan.tk;
+    const int piece = plan.rows > 16 && D == 256 ? 64 : plan.tk;
     p.box_rows = p.page_size < piece ? p.page_size : piece;
     const int key = D * (f8 ? 1 : 2);
     plan.box_bytes = key < 128 ? key : 128;

@@ -884,8 +884,10 @@ cudaError_t attn_dispatch_rows(const AttnParams& p, const AttnMaps& maps, int ro
     if (rows == 64)
         return attn_launch(attn_tc_kernel<D, F8, 64>, AttnTcShape<D, F8, 64>::kThreads,
                            AttnTcShape<D, F8, 64>::kSmem, once[1], occ[1], p, maps, grid, sms, s);
-    return attn_launch(attn_tc_kernel<D, F8, 128>, AttnTcShape<D, F8, 128>::kThreads,
-                       AttnTcShape<D, F8, 128>::kSmem, once[2], occ[2], p, maps, grid, sms, s);
+    if constexpr (!(F8 && D == 256))
+        return attn_launch(attn_tc_kernel<D, F8, 128>, AttnTcShape<D, F8, 128>::kThreads,
+                           AttnTcShape<D, F8, 128>::kSmem, once[2], occ[2], p, maps, grid, sms, s);
+    return cudaErrorInvalidValue;
 }
 
 template <int D>

@@ -3,32 +3,32 @@
 // attn_kernel (attn.cuh).
 //
 // One CTA per SM, warps with roles.  A producer warp loads tiles of 128 keys
-// (TMA) into a ring of pieces in the swizzled layout the tensor cores read (K
-// whole and V whole; bf16 at head size 256: K by halves of its dimensions, V by
-// halves of its keys, 32 KB each).  One thread issues S = Q K^T and O += P V
-// piece by piece, whichever has its operands first.  The softmax warps own one
-// query row a thread, so the softmax has no shuffles, and S and P never pass
-// through shared memory.  S has two buffers: Q K^T of the next tile runs under
-// the softmax of this one; P overwrites the front of its S.  Q lies in tensor
-// memory where O (D columns), two S (256) and two Q fit its 512 columns, else
-// (head size 256) in shared memory: tiles of 64 keys would make room, but the
-// products of 64 columns run at half the rate of those of 128.  Four warps bring
-// an item's queries to their place and pass each V piece on, cleaned where not
-// every row sees every key.
+// (TMA) into two rings in the swizzled layout the tensor cores read, one of K
+// pieces and one of V pieces (a piece is the whole tile, or at head size 256 and
+// bf16 half of K's dimensions; at head size 256 half of V's keys).  One thread
+// issues S = Q K^T and O += P V piece by piece, whichever has its operands first.
+// The softmax warps own one query row a thread, so the softmax has no shuffles,
+// and S and P never pass through shared memory.  S has two buffers: Q K^T of the
+// next tile runs under the softmax of this one; P overwrites the front of its S.
+// Q lies in tensor memory where O (D columns), two S (256) and two Q fit its 512
+// columns, else (head size 256) in shared memory: tiles of 64 keys would make
+// room, but the products of 64 columns run at half the rate of those of 128.
 //
-// e4m3 caches are multiplied as they are (kind::f8f6f4); the other operand is a
-// sum of two e4m3 terms.  A query row, scaled by a power of two that puts its
-// largest magnitude into [2^7, 2^8), is hi + lo with hi its nearest e4m3 value and
-// lo that of the rest: 4 + 4 significant bits, so exact for a bf16 value down to
-// 2^-10 of the largest and off by at most 2^-17 of the largest below.  The weights
-// are taken as 2^8 P = hi + lo: off by at most 2^-9 of their value, or 2^-18.
-// (Turning the tiles into f16 on the way instead, with eight more warps, was bound
-// by that step.)
+// The last role brings an item's queries to their place and passes V on, cleaned
+// where not every row sees every key: four warps for bf16; for e4m3 eight, which
+// turn it into f16 (exact) in a third ring.
+//
+// e4m3 keys are multiplied as they are (kind::f8f6f4); a query row, scaled by a
+// power of two that puts its largest magnitude into [2^7, 2^8), is the sum of two
+// e4m3 terms, its nearest value and that of the rest: 4 + 4 significant bits, so
+// exact for a bf16 value down to 2^-10 of the largest and off by at most 2^-17 of
+// the largest below.  For the weights two such terms would not do: a long tail of
+// small weights under one large one lies below their range.  So P is f16 and V
+// becomes f16; converting K as well was bound by that step.
 //
 // The running maximum that the exponents use follows the true one lazily: O is
 // rescaled only when a row's maximum grew by more than 2^8 (its weights are then
-// at most 2^8, harmless in bf16 and the fp32 sum), e4m3: by more than 2^0.75
-// (2^8.75 is below 448).
+// at most 2^8, harmless in bf16, f16 and the fp32 sum).
 #pragma once
 #include "attn.cuh"
 
@@ -38,29 +38,38 @@ namespace vw4 {
 template <int D, bool F8, int ROWS>
 struct AttnTcShape {
     static constexpr int kTK = 128;                  // keys of a tile
-    static constexpr int kES = F8 ? 1 : 2;           // bytes of an element
-    static constexpr int kNP = D == 256 && !F8 ? 2 : 1;  // pieces of K, and of V
-    static constexpr int kPieces = 2 * kNP;          // of a tile
-    static constexpr int kPiece = kTK * D * kES / kNP;
-    static constexpr int kVKeys = kTK / kNP;         // keys of a V piece
+    static constexpr int kES = F8 ? 1 : 2;           // bytes of an element in memory
     static constexpr int kBoxB = D * kES < 128 ? D * kES : 128;  // bytes of a key in a box
-    static constexpr int kKBlks = D * kES / kNP / kBoxB;  // blocks of kBoxB bytes of a K piece
-    static constexpr int kVBlks = D * kES / kBoxB;
-    static constexpr int kKBlk = kTK * kBoxB, kVBlk = kVKeys * kBoxB;
+    // K: pieces of kKBlks blocks of kBoxB bytes of a key
+    static constexpr int kKP = D == 256 && !F8 ? 2 : 1;
+    static constexpr int kKBlks = D * kES / kKP / kBoxB;
+    static constexpr int kKBlk = kTK * kBoxB;
+    static constexpr int kKPiece = kKBlks * kKBlk;
     static constexpr int kSteps = kBoxB / 32;        // k steps (32 bytes) of a block
-    static constexpr int kKeysPerStep = 32 / kES;    // of O += P V
-    static constexpr int kTerms = F8 ? 2 : 1;        // of Q, and of P
+    static constexpr int kTerms = F8 ? 2 : 1;        // of Q
+    // V: pieces of kVKeys keys, as loaded and as multiplied (16-bit, blocks of 64 dimensions)
+    static constexpr int kVP = D == 256 ? 2 : 1;
+    static constexpr int kVKeys = kTK / kVP;
+    static constexpr int kVBlks = D * kES / kBoxB;
+    static constexpr int kVLoad = kVKeys * D * kES;
+    static constexpr int kVPiece = kVKeys * D * 2;
+    static constexpr int kVBlk = kVKeys * 128;
     static constexpr bool kQSmem = D == 256;
     static constexpr int kQRow = D * kES;            // bytes of a term of a query row
     static constexpr int kQBlk = ROWS * kBoxB;
     static constexpr int kQ = kQSmem ? ROWS * D * 2 : 0;
     static constexpr int kNQ = kQSmem ? 1 : 2;       // query buffers
-    static constexpr int kNS = F8 ? (D == 64 ? 12 : (D == 128 ? 8 : (ROWS == 64 ? 5 : 4)))
-                                  : (D == 64 ? 8 : (D == 128 ? 6 : (ROWS == 64 ? 5 : 4)));
-    static constexpr int kAuxWarps = 4;
-    static constexpr int kThreads = (6 + kAuxWarps) * 32;
-    static constexpr int kOffRing = kQ;
-    static constexpr int kOffStage = kOffRing + kNS * kPiece;  // 4 KB a softmax warp, for the output
+    static_assert(!(F8 && D == 256 && ROWS > 64), "blocks of 64 rows");
+    static constexpr int kNK = F8 ? (D == 64 ? 6 : (D == 128 ? 4 : 2)) : (D == 64 ? 4 : (D == 128 ? 3 : 2));
+    static constexpr int kNV = F8 ? (D == 64 ? 6 : (D == 128 ? 4 : 3))
+                                  : (D == 64 ? 4 : (D == 128 || ROWS == 64 ? 3 : 2));
+    static constexpr int kNF = !F8 ? 0 : (D == 64 ? 4 : 2);  // f16 pieces
+    static constexpr int kVWarps = F8 ? 8 : 4;       // that pass V on
+    static constexpr int kThreads = (6 + kVWarps) * 32;
+    static constexpr int kOffK = kQ;
+    static constexpr int kOffV = kOffK + kNK * kKPiece;
+    static constexpr int kOffF = kOffV + kNV * kVLoad;
+    static constexpr int kOffStage = kOffF + kNF * kVPiece;    // 4 KB a softmax warp, for the output
     static constexpr int kUsed = kOffStage + 4 * 4096 + 1024;  // and alignment
     static constexpr int kSmem = kUsed < 115 * 1024 ? 115 * 1024 : kUsed;  // one CTA per SM
     static_assert(kSmem + 2048 <= 227 * 1024, "shared memory");
@@ -69,24 +78,23 @@ struct AttnTcShape {
     // tensor memory columns: O, two S, the queries (two 16-bit values a column)
     static constexpr uint32_t kColO = 0, kColS = D, kColQ = D + 2 * kTK;
     static_assert(D + 2 * kTK + (kQSmem ? 0 : kNQ * D / 2) <= 512, "tensor memory");
-    // 16 bytes of a row of a piece or of Q: blocks of blk bytes, rows of kBoxB in them
+    // 16 bytes of a row: blocks of blk bytes, rows of BOXB bytes in them
+    template <int BOXB>
     __device__ static __forceinline__ uint32_t at(int blk, int row, int chunk) {
-        constexpr int CPB = kBoxB / 16;
-        const int x = kBoxB == 64 ? (row >> 1) & 3 : row & 7;
-        return static_cast<uint32_t>(chunk / CPB * blk + row * kBoxB + (((chunk % CPB) ^ x) << 4));
+        constexpr int CPB = BOXB / 16;
+        const int x = BOXB == 64 ? (row >> 1) & 3 : row & 7;
+        return static_cast<uint32_t>(chunk / CPB * blk + row * BOXB + (((chunk % CPB) ^ x) << 4));
     }
-    __device__ static __forceinline__ uint64_t desc(uint32_t addr, uint32_t lbo) {
-        return tc_desc<kBoxB>(addr, lbo, 8 * kBoxB);
-    }
-    static constexpr float kLazy = F8 ? 0.75f : 8.f;  // (log2) see above
-    static constexpr float kShift = F8 ? 8.f : 0.f;   // log2 of what P is multiplied by
 };
+
+constexpr float kLazy = 8.f;  // (log2) see above
 
 template <int D, bool F8, int ROWS>
 __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     attn_tc_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps) {
     using S = AttnTcShape<D, F8, ROWS>;
-    constexpr int TK = S::kTK, NS = S::kNS, NP = S::kNP, PT = S::kPieces;
+    constexpr int TK = S::kTK, NK = S::kNK, NV = S::kNV, NF = F8 ? S::kNF : 1;
+    constexpr int KP = S::kKP, VP = S::kVP;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ uint32_t s_tmem;
@@ -96,8 +104,8 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     // A wait names a phase by its parity: when it begins, the phase before has to be over
     // and the one after not.  So products and scores have two barriers each, taken in
     // turn: S of tile u is committed after the product of tile u - 2.
-    // Loaded pieces, their release; V pieces passed on:
-    __shared__ __align__(8) uint64_t b_full[NS], b_empty[NS], b_clean[8];
+    // Loaded pieces and their release; V pieces passed on (bf16) or as f16 and released.
+    __shared__ __align__(8) uint64_t b_k[NK], b_ke[NK], b_v[NV], b_ve[NV], b_clean[8], b_fe[NF];
     __shared__ __align__(8) uint64_t b_s[2], b_p[2], b_pv[2], b_q[2], b_qe[2], b_part[8], b_o, b_end;
     // log2 of the row scales of e4m3 queries, by part: those of part n + 4 are written
     // after the last scores of part n + 2, which wait for the softmax of part n
@@ -113,10 +121,15 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     if (warp == 4) {
         tmem_alloc<512>(&s_tmem);
         if (lane == 0) {
-            for (int k = 0; k < NS; ++k) {
-                mbar_init(&b_full[k], 1);
-                mbar_init(&b_empty[k], 1);
+            for (int k = 0; k < NK; ++k) {
+                mbar_init(&b_k[k], 1);
+                mbar_init(&b_ke[k], 1);
             }
+            for (int k = 0; k < NV; ++k) {
+                mbar_init(&b_v[k], 1);
+                mbar_init(&b_ve[k], F8 ? S::kVWarps : 1);
+            }
+            for (int k = 0; k < NF; ++k) mbar_init(&b_fe[k], 1);
             for (int k = 0; k < 2; ++k) {
                 mbar_init(&b_s[k], 1);
                 mbar_init(&b_pv[k], 1);
@@ -126,7 +139,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             }
             for (int k = 0; k < 8; ++k) {
                 mbar_init(&b_part[k], 1);
-                mbar_init(&b_clean[k], 4);
+                mbar_init(&b_clean[k], S::kVWarps);
             }
             mbar_init(&b_o, row_warps);
             mbar_init(&b_end, 1);
@@ -225,7 +238,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                         // e4m3: four chunks of 16 dimensions of either term
                         const int chunk = F8 ? (k >> 2) * (D / 16) + (from + c) / 2 + (k & 3) : from + c + k;
                         if (r < ROWS)
-                            *reinterpret_cast<uint4*>(smem + S::at(S::kQBlk, r, chunk)) =
+                            *reinterpret_cast<uint4*>(smem + S::template at<S::kBoxB>(S::kQBlk, r, chunk)) =
                                 make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
                     }
                 } else if (F8) {
@@ -252,15 +265,14 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         constexpr int ESZ = S::kES, BOXB = S::kBoxB, KB = S::kKBlks, VB = S::kVBlks;
         AttnWalk<TK> w;
         w.begin(p, span, cap, lane);
-        int hl = 0;  // pieces loaded
+        int nk = 0, nv = 0;  // pieces loaded
         bool ok = true;
         // the next piece's place, once it is free; its bytes are announced
-        auto place = [&](uint32_t bytes) {
-            const int st = hl % NS;
-            ok = hl < NS || warp_wait(&b_empty[st], hl / NS - 1);
-            if (ok && lane == 0) mbar_arrive_expect_tx(&b_full[st], bytes);
+        auto place = [&](uint64_t* full, uint64_t* empty, int n, int ring, uint32_t bytes) {
+            ok = n < ring || warp_wait(&empty[n % ring], n / ring - 1);
+            if (ok && lane == 0) mbar_arrive_expect_tx(&full[n % ring], bytes);
             __syncwarp();
-            return sm + S::kOffRing + st * S::kPiece;
+            return ok;
         };
         for (int u = 0; u < n_units; ++u) {
             const AttnUnit d = w.unit(p);
@@ -268,36 +280,44 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 s_unit[u % kUnitRing] = d;
                 if (d.flags & kUnitFirst) mbar_arrive(&b_part[d.seg & 7]);  // its queries may be read
             }
-            uint32_t dst = place(w.template bytes<0, TK, KB, BOXB>(lane));
-            if (!ok) break;
-            w.template load<0, TK, 0, KB, BOXB, ESZ>(p, &maps.k, dst, &b_full[hl++ % NS], lane);
-            if (NP == 2) {
-                dst = place(w.template bytes<0, TK, KB, BOXB>(lane));
-                if (!ok) break;
-                w.template load<0, TK, KB, KB, BOXB, ESZ>(p, &maps.k, dst, &b_full[hl++ % NS], lane);
+            if (!place(b_k, b_ke, nk, NK, w.template bytes<0, TK, KB, BOXB>(lane))) break;
+            w.template load<0, TK, 0, KB, BOXB, ESZ>(p, &maps.k, sm + S::kOffK + nk % NK * S::kKPiece,
+                                                     &b_k[nk % NK], lane);
+            ++nk;
+            if (KP == 2) {
+                if (!place(b_k, b_ke, nk, NK, w.template bytes<0, TK, KB, BOXB>(lane))) break;
+                w.template load<0, TK, KB, KB, BOXB, ESZ>(
+                    p, &maps.k, sm + S::kOffK + nk % NK * S::kKPiece, &b_k[nk % NK], lane);
+                ++nk;
             }
-            dst = place(w.template bytes<0, S::kVKeys, VB, BOXB>(lane));
-            if (!ok) break;
-            w.template load<0, S::kVKeys, 0, VB, BOXB, ESZ>(p, &maps.v, dst, &b_full[hl++ % NS], lane);
-            if (NP == 2) {
-                dst = place(w.template bytes<S::kVKeys, S::kVKeys, VB, BOXB>(lane));
-                if (!ok) break;
-                w.template load<S::kVKeys, S::kVKeys, 0, VB, BOXB, ESZ>(p, &maps.v, dst,
-                                                                       &b_full[hl++ % NS], lane);
+            if (!place(b_v, b_ve, nv, NV, w.template bytes<0, S::kVKeys, VB, BOXB>(lane))) break;
+            w.template load<0, S::kVKeys, 0, VB, BOXB, ESZ>(
+                p, &maps.v, sm + S::kOffV + nv % NV * S::kVLoad, &b_v[nv % NV], lane);
+            ++nv;
+            if (VP == 2) {
+                if (!place(b_v, b_ve, nv, NV, w.template bytes<S::kVKeys, S::kVKeys, VB, BOXB>(lane)))
+                    break;
+                w.template load<S::kVKeys, S::kVKeys, 0, VB, BOXB, ESZ>(
+                    p, &maps.v, sm + S::kOffV + nv % NV * S::kVLoad, &b_v[nv % NV], lane);
+                ++nv;
             }
             if (u + 1 < n_units) w.next(p, lane);
         }
         if (!ok) {  // copies in flight land before the block ends
-            for (int k = hl > NS ? hl - NS : 0; k < hl; ++k)
-                mbar_wait_bounded(&b_full[k % NS], (k / NS) & 1, p.wait_ns, nullptr);
+            for (int k = nk > NK ? nk - NK : 0; k < nk; ++k)
+                mbar_wait_bounded(&b_k[k % NK], (k / NK) & 1, p.wait_ns, nullptr);
+            for (int k = nv > NV ? nv - NV : 0; k < nv; ++k)
+                mbar_wait_bounded(&b_v[k % NV], (k / NV) & 1, p.wait_ns, nullptr);
         }
     } else if (n_units > 0 && warp >= 6) {
-        // ------------------------------------- queries in, V pieces passed on
-        const int at = tid - 192, qw = warp & 3;  // (a warp reaches lanes 32 (warp % 4) ..)
+        // ------------------- queries in (the first four warps), V pieces passed on
+        constexpr int N = S::kVWarps * 32;
+        const int at = tid - 192;
+        const int qw = warp & 3;  // (a warp reaches lanes 32 (warp % 4) .. of tensor memory)
         bool first = true, ok = true;
         int parts = 0;
         for (int u = 0; u < n_units && ok; ++u) {
-            if (first && qw < row_warps) {
+            if (first && at < 128 && qw < row_warps) {
                 ok = warp_wait(&b_part[parts & 7], parts >> 3);
                 if (!ok) break;
                 const AttnUnit d = s_unit[u % kUnitRing];
@@ -306,90 +326,139 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             }
             parts += first;
 #pragma unroll 1
-            for (int i = 0; i < NP; ++i) {
-                const int pc = u * PT + NP + i, st = pc % NS;
-                ok = warp_wait(&b_full[st], pc / NS);
+            for (int i = 0; i < VP; ++i) {
+                const int pc = u * VP + i, st = pc % NV;
+                ok = warp_wait(&b_v[st], pc / NV);
                 if (!ok) break;
                 const AttnUnit d = s_unit[u % kUnitRing];
                 first = d.flags & kUnitLast;  // (of the next unit)
-                if (d.flags & kUnitEdge) {
-                    // Values that no row sees become zeros; infinities and NaN of values
-                    // that only some rows see too (0 times them must not reach the other
-                    // rows): the end of the part gives them to the rows that see them.
-                    const int key0 = d.start + i * S::kVKeys;
-                    constexpr int CH = D * S::kES / 16;
-                    bool odd = false;
+                // Values that no row sees become zeros; infinities and NaN of values that
+                // only some rows see too (0 times them must not reach the other rows): the
+                // end of the part gives them to the rows that see them.
+                const bool edge = d.flags & kUnitEdge;
+                const int key0 = d.start + i * S::kVKeys;
+                uint8_t* src = smem + S::kOffV + st * S::kVLoad;
+                constexpr int CH = D * S::kES / 16;
+                bool odd = false;
+                if (!F8) {
+                    if (edge) {
 #pragma unroll 1
-                    for (int c = at; c < S::kVKeys * CH; c += S::kAuxWarps * 32) {
-                        const int row = c / CH, j = key0 + row;
-                        if (key_all(j, d.len, d.p0, p.window, p.sinks)) continue;
-                        uint4* q = reinterpret_cast<uint4*>(smem + S::kOffRing + st * S::kPiece +
-                                                            S::at(S::kVBlk, row, c % CH));
-                        if (!key_some(j, d.len, d.p0, p.window, p.sinks)) {
-                            *q = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        const uint4 v = *q;
-                        uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                        bool hit = false;
+                        for (int c = at; c < S::kVKeys * CH; c += N) {
+                            const int row = c / CH, j = key0 + row;
+                            if (key_all(j, d.len, d.p0, p.window, p.sinks)) continue;
+                            uint4* q = reinterpret_cast<uint4*>(
+                                src + S::template at<S::kBoxB>(S::kVKeys * S::kBoxB, row, c % CH));
+                            if (!key_some(j, d.len, d.p0, p.window, p.sinks)) {
+                                *q = make_uint4(0, 0, 0, 0);
+                                continue;
+                            }
+                            const uint4 v = *q;
+                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            bool hit = false;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (F8) {
-#pragma unroll
-                                for (int k = 0; k < 32; k += 8)
-                                    if (((w[e] >> k) & 0x7Fu) == 0x7Fu) w[e] &= ~(0xFFu << k), hit = true;
-                            } else {
+                            for (int e = 0; e < 4; ++e) {
                                 if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xffff0000u, hit = true;
                                 if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xffffu, hit = true;
                             }
+                            if (hit) *q = make_uint4(w[0], w[1], w[2], w[3]);
+                            odd |= hit;
                         }
-                        if (hit) *q = make_uint4(w[0], w[1], w[2], w[3]);
-                        odd |= hit;
+                        if (odd) s_odd[d.seg & 7] = d.seg + 1;
+                        fence_async_smem();
                     }
-                    if (odd) s_odd[d.seg & 7] = d.seg + 1;
-                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b_clean[pc & 7]);
+                    continue;
                 }
+                ok = pc < NF || warp_wait(&b_fe[pc % NF], pc / NF - 1);
+                if (!ok) break;
+                uint8_t* dst = smem + S::kOffF + pc % NF * S::kVPiece;
+#pragma unroll 4
+                for (int k = 0; k < S::kVKeys * CH / N; ++k) {
+                    const int c = at + k * N, row = c / CH, ch = c % CH;  // 16 dimensions of a key
+                    const uint4 v = *reinterpret_cast<const uint4*>(
+                        src + S::template at<S::kBoxB>(S::kVKeys * S::kBoxB, row, ch));
+                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    if (edge) {
+                        const int j = key0 + row;
+                        if (!key_some(j, d.len, d.p0, p.window, p.sinks)) {
+                            w[0] = w[1] = w[2] = w[3] = 0u;
+                        } else if (!key_all(j, d.len, d.p0, p.window, p.sinks)) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                                for (int q = 0; q < 32; q += 8)
+                                    if (((w[e] >> q) & 0x7Fu) == 0x7Fu) {
+                                        w[e] &= ~(0xFFu << q);
+                                        odd = true;
+                                    }
+                        }
+                    }
+                    uint32_t f[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        f[2 * e] = e4m3x2_f16x2(w[e]);
+                        f[2 * e + 1] = e4m3x2_f16x2(w[e] >> 16);
+                    }
+                    // lanes of neighbouring 64-dimension blocks write their two chunks in
+                    // opposite order: eight lanes then cover all banks
+                    const int flip = (ch >> 2) & 1;
+                    const uint4 a = make_uint4(f[0], f[1], f[2], f[3]);
+                    const uint4 b = make_uint4(f[4], f[5], f[6], f[7]);
+                    *reinterpret_cast<uint4*>(dst + S::template at<128>(S::kVBlk, row, 2 * ch + flip)) =
+                        flip ? b : a;
+                    *reinterpret_cast<uint4*>(dst + S::template at<128>(S::kVBlk, row, 2 * ch + 1 - flip)) =
+                        flip ? a : b;
+                }
+                if (odd) s_odd[d.seg & 7] = d.seg + 1;
+                fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&b_clean[(u * NP + i) & 7]);
+                if (lane == 0) {
+                    mbar_arrive(&b_clean[pc & 7]);
+                    mbar_arrive(&b_ve[st]);
+                }
             }
         }
     } else if (n_units > 0 && warp == 4) {
         // ----------------------------------------------- the tensor cores
         if (lane == 0) {
-            constexpr uint32_t iS = tc_idesc(!F8, 128, TK, false), iO = tc_idesc(!F8, 128, D, true);
+            constexpr uint32_t iS = tc_idesc(!F8, 128, TK, false);  // bf16, or e4m3
+            constexpr uint32_t iO = tc_idesc(!F8, 128, D, true);    // bf16, or f16
             int fl[2] = {0, 0}, parts = 0;
             int qk = 0, kp = 0, pv = 0, vp = 0;  // next tile and piece of either product
             uint64_t t0 = 0;
             while (pv < n_units) {
                 // S of tile qk takes the buffer of tile qk - 2, whose P has been read
                 if (qk < n_units && qk <= pv + 1) {
-                    const int pc = qk * PT + kp, st = pc % NS;
-                    if (mbar_test(&b_full[st], (pc / NS) & 1)) {
+                    const int pc = qk * KP + kp, st = pc % NK;
+                    if (mbar_test(&b_k[st], (pc / NK) & 1)) {
                         const AttnUnit* d = &s_unit[qk % kUnitRing];
                         const int flags = d->flags, seg = d->seg, qs = seg % S::kNQ;
                         if (kp > 0 || !(flags & kUnitFirst) || mbar_test(&b_q[qs], (seg / S::kNQ) & 1)) {
                             tc_fence_after();
-                            const uint32_t k = sm + S::kOffRing + st * S::kPiece;
+                            const uint32_t k = sm + S::kOffK + st * S::kKPiece;
                             const uint32_t dS = tmem + S::kColS + (qk & 1) * TK;
                             constexpr int KS = S::kKBlks * S::kSteps;  // k steps of the piece
 #pragma unroll
                             for (int t = 0; t < S::kTerms; ++t)
 #pragma unroll
                                 for (int ks = 0; ks < KS; ++ks) {
-                                    const uint64_t kd = S::desc(
-                                        k + (ks / S::kSteps) * S::kKBlk + (ks % S::kSteps) * 32, 16);
+                                    const uint64_t kd = tc_desc<S::kBoxB>(
+                                        k + (ks / S::kSteps) * S::kKBlk + (ks % S::kSteps) * 32, 16,
+                                        8 * S::kBoxB);
                                     const int kq = t * (S::kQRow / 32) + kp * KS + ks;  // k step of Q
                                     const bool add = t > 0 || kp > 0 || ks > 0;
                                     if (S::kQSmem)
                                         tc_mma_ss<F8>(dS,
-                                                      S::desc(sm + (kq / S::kSteps) * S::kQBlk +
-                                                                  (kq % S::kSteps) * 32, 16),
+                                                      tc_desc<S::kBoxB>(sm + (kq / S::kSteps) * S::kQBlk +
+                                                                            (kq % S::kSteps) * 32,
+                                                                        16, 8 * S::kBoxB),
                                                       kd, iS, add);
                                     else
                                         tc_mma_ts<F8>(dS, tmem + S::kColQ + qs * (D / 2) + kq * 8, kd, iS, add);
                                 }
-                            tc_commit(&b_empty[st]);
-                            if (++kp == NP) {
+                            tc_commit(&b_ke[st]);
+                            if (++kp == KP) {
                                 tc_commit(&b_s[qk & 1]);
                                 if (flags & kUnitLast) tc_commit(&b_qe[qs]);
                                 fl[qk & 1] = flags;
@@ -402,25 +471,22 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                     }
                 }
                 if (pv < qk) {
-                    const int pc = pv * PT + NP + vp, st = pc % NS, vs = pv * NP + vp;
+                    const int pc = pv * VP + vp;
                     const bool first = fl[pv & 1] & kUnitFirst;
-                    if (mbar_test(&b_clean[vs & 7], (vs >> 3) & 1) &&
+                    if (mbar_test(&b_clean[pc & 7], (pc >> 3) & 1) &&
                         (vp > 0 || (mbar_test(&b_p[pv & 1], (pv >> 1) & 1) &&
                                     (!first || parts == 0 || mbar_test(&b_o, (parts - 1) & 1))))) {
                         tc_fence_after();
-                        const uint32_t v = sm + S::kOffRing + st * S::kPiece;
-                        constexpr int KS = S::kVKeys / S::kKeysPerStep;
+                        const uint32_t v = sm + (F8 ? S::kOffF + pc % NF * S::kVPiece
+                                                    : S::kOffV + pc % NV * S::kVLoad);
 #pragma unroll
-                        for (int t = 0; t < S::kTerms; ++t)
-#pragma unroll
-                            for (int ks = 0; ks < KS; ++ks)
-                                tc_mma_ts<F8>(tmem + S::kColO,
-                                              tmem + S::kColS + (pv & 1) * TK +
-                                                  (t * (TK / S::kKeysPerStep) + vp * KS + ks) * 8,
-                                              S::desc(v + ks * (S::kKeysPerStep * S::kBoxB), S::kVBlk), iO,
-                                              !(first && t == 0 && vp == 0 && ks == 0));
-                        tc_commit(&b_empty[st]);
-                        if (++vp == NP) {
+                        for (int ks = 0; ks < S::kVKeys / 16; ++ks)
+                            tc_mma_ts<false>(tmem + S::kColO,
+                                             tmem + S::kColS + (pv & 1) * TK + (vp * (S::kVKeys / 16) + ks) * 8,
+                                             tc_desc<128>(v + ks * 2048, S::kVBlk, 1024), iO,
+                                             !(first && vp == 0 && ks == 0));
+                        tc_commit(F8 ? &b_fe[pc % NF] : &b_ve[pc % NV]);
+                        if (++vp == VP) {
                             tc_commit(&b_pv[pv & 1]);
                             parts += first;
                             vp = 0;
@@ -501,7 +567,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             float corr = 1.f;
             if (first) {
                 m = mx;
-            } else if ((mx - m) * c2 > S::kLazy) {
+            } else if ((mx - m) * c2 > kLazy) {
                 // (m = -infinity: O and l are zeros still)
                 if (m != -INFINITY) {
                     corr = ex2((m - mx) * c2);
@@ -523,36 +589,21 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                     tmem_st32(tO + c, y);
                 }
             }
-            const float mc = m == -INFINITY ? 0.f : m * c2 - S::kShift;
+            const float mc = m == -INFINITY ? 0.f : m * c2;
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll
             for (int c = 0; c < TK; c += 64) {
                 if (c > 0) masked(c);
                 uint32_t y[32];
-                if (F8) {  // hi: y[0 .. 15], lo: y[16 .. 31]
 #pragma unroll
-                    for (int k = 0; k < 64; k += 4) {
-                        float e[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) e[q] = ex2(fmaf(__uint_as_float(x[k + q]), c2, -mc));
-                        s0 += e[0] + e[1];
-                        s1 += e[2] + e[3];
-                        e4m3_terms(pack2<true>(e[0], e[1]), pack2<true>(e[2], e[3]), y[k / 4],
-                                   y[16 + k / 4]);
-                    }
-                    tmem_st16(tS + c / 4, y);
-                    tmem_st16(tS + TK / 4 + c / 4, y + 16);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 64; k += 2) {
-                        const float a = ex2(fmaf(__uint_as_float(x[k]), c2, -mc));
-                        const float b = ex2(fmaf(__uint_as_float(x[k + 1]), c2, -mc));
-                        s0 += a;
-                        s1 += b;
-                        y[k / 2] = pack2<false>(a, b);
-                    }
-                    tmem_st32(tS + c / 2, y);
+                for (int k = 0; k < 64; k += 2) {
+                    const float a = ex2(fmaf(__uint_as_float(x[k]), c2, -mc));
+                    const float b = ex2(fmaf(__uint_as_float(x[k + 1]), c2, -mc));
+                    s0 += a;
+                    s1 += b;
+                    y[k / 2] = pack2<F8>(a, b);
                 }
+                tmem_st32(tS + c / 2, y);
             }
             l += s0 + s1;
             tmem_st_wait();

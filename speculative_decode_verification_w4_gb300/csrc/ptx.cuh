@@ -196,8 +196,8 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_
     return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
            (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | ((ROWB == 128 ? 2ull : 4ull) << 61);
 }
-// M x N tile of f32 accumulators; A and B both bf16 (kind::f16) or both e4m3
-// (kind::f8f6f4)
+// M x N tile of f32 accumulators; A and B both bf16, or else both f16 (kind::f16) or
+// both e4m3 (kind::f8f6f4)
 __host__ __device__ constexpr uint32_t tc_idesc(bool bf16, int M, int N, bool b_n_major) {
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_n_major ? 1u << 16 : 0u) |
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);

@@ -79,11 +79,11 @@ def attention64(q, k, v, n, scale, window, sinks, kv):
     how far a kernel may be from them.
 
     The tolerance counts the roundings: half a step of bf16 on the output; the
-    weights' half step on sum(p |v|): bf16 2^-8; e4m3 caches with up to 16 rows
-    a key head f16, 2^-11 and 2^-25 below its normal range; with more rows two
-    e4m3 terms of 2^8 p, 2^-9 + 2^-12 and 2^-18; the scores' fp32 error delta =
-    2 D 2^-24 scale sum|q k|, plus 2^-22 of the exponent, on every weight; the
-    queries' two e4m3 terms, 2^-17 of the row's largest, on every score."""
+    weights' half step on sum(p |v|): bf16 2^-8; e4m3 caches f16, 2^-11, and
+    2^-25 below its normal range; the scores' fp32 error delta = 2 D 2^-24 scale
+    sum|q k|, plus 2^-22 of the exponent, on every weight; e4m3 caches with more
+    than 16 rows a key head: the queries' two e4m3 terms, 2^-17 of the row's
+    largest, on every score."""
     R, Hq, D = q.shape
     Hkv = k.shape[1] if n else 1
     out = torch.zeros(R, Hq, D, dtype=torch.float64)
@@ -95,8 +95,6 @@ def attention64(q, k, v, n, scale, window, sinks, kv):
     vis = seen(n, R, window, sinks)
     terms = kv == "e4m3" and R * G > 16
     wp, tiny = (2 ** -8, 0.0) if kv == "bf16" else (2 ** -11, 2 ** -25)
-    if terms:
-        wp, tiny = 2 ** -9 + 2 ** -12, 2 ** -18
     for i in range(R):
         sel = torch.nonzero(vis[i])[:, 0]
         if len(sel) == 0:

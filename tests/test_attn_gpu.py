@@ -109,6 +109,24 @@ def test_many_sequences():
     run_case(5, lens, 2, 4, 2, 64, 16, "bf16")
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("R,Hq,D", [(1, 4, 128), (8, 6, 256), (16, 4, 64)])
+def test_long_tail_under_one_large_weight(R, Hq, D, kv):
+    """One token takes most of the weight, and thousands of small ones the rest."""
+    n = 6000
+    c, k64, v64 = make_cache(25, [n], 16, 1, D, kv)
+    q = torch.full((1, R, Hq, D), 0.25, dtype=torch.bfloat16)
+    big = 9.0 / (0.25 * D * D ** -0.5)          # score 9: weight e^9 over 6000 of about 1
+    unit = 1.0 if kv == "bf16" else float(c.k_scale[0])
+    c.k[int(c.block_table[0, 3]), 5, 0] = torch.full((D,), big / unit, device="cuda").to(c.k.dtype)
+    k64[0][53, 0] = (torch.full((D,), big / unit).to(c.k.dtype).float().double() * unit)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out = vw4.verify_attn(q.cuda(), c, lens)
+    status()
+    o, _, t, _ = attention64(q[0].double(), k64[0], v64[0], n, D ** -0.5, 0, 0, kv)
+    check_close(out[0], o, t, "out")
+
+
 def test_small_and_large_scores():
     run_case(6, [500], 4, 4, 1, 128, 16, "bf16", gain=40.0)
     run_case(7, [500], 4, 4, 1, 128, 16, "e4m3", gain=1e-6)
