@@ -65,7 +65,7 @@ struct AttnTcShape {
                                   : (D == 64 ? 4 : (D == 128 || ROWS == 64 ? 3 : 2));
     static constexpr int kNF = !F8 ? 0 : (D == 64 ? 4 : 2);  // f16 pieces
     static constexpr int kVWarps = F8 ? 8 : 4;       // that pass V on
-    static constexpr int kThreads = (6 + kVWarps) * 32;
+    static constexpr int kThreads = (8 + kVWarps) * 32;  // warps 4 and 5 have no work
     static constexpr int kOffK = kQ;
     static constexpr int kOffV = kOffK + kNK * kKPiece;
     static constexpr int kOffF = kOffV + kNV * kVLoad;
@@ -88,6 +88,11 @@ struct AttnTcShape {
 };
 
 constexpr float kLazy = 8.f;  // (log2) see above
+
+// Warps: 0 .. 3 softmax, 8 .. pass V on.  The loading warp and the one that issues
+// the products (it polls) share schedulers with the softmax warps that only the
+// largest blocks use.
+constexpr int kTcLoad = 6, kTcMma = 7, kTcPass = 8;
 
 template <int D, bool F8, int ROWS>
 __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
@@ -114,11 +119,11 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     const int row_warps = (p.tb * p.gb + 31) / 32;     // softmax warps with rows
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (tid == 160) {
+    if (tid == kTcLoad * 32) {
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
     }
-    if (warp == 4) {
+    if (warp == kTcMma) {
         tmem_alloc<512>(&s_tmem);
         if (lane == 0) {
             for (int k = 0; k < NK; ++k) {
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 mbar_init(&b_s[k], 1);
                 mbar_init(&b_pv[k], 1);
                 mbar_init(&b_p[k], row_warps);
-                mbar_init(&b_q[k], row_warps);
+                mbar_init(&b_q[k], S::kQSmem ? S::kVWarps : row_warps);
                 mbar_init(&b_qe[k], 1);
             }
             for (int k = 0; k < 8; ++k) {
@@ -166,101 +171,124 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         return __all_sync(0xffffffffu, wait(bar, phase)) != 0;
     };
 
-    // An item's queries to their place: one row a thread of four warps.
-    auto queries = [&](const AttnUnit& d, int qw) {
-        const int qs = d.seg % S::kNQ, r = qw * 32 + lane;
-        const AttnRow row = attn_row(p, d.g, r);
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (static_cast<long long>(d.b) * p.R + row.i) * p.ldq + static_cast<long long>(row.hq) * D);
-        constexpr int NV = D == 256 ? 16 : D / 8;  // half a row of 256, else a row
-        uint4 v[NV];
-        float up = 1.f;
-        auto get = [&](int from) {
+    // An item's queries to their place.  e4m3: as two terms (see above); a row with an
+    // infinity or NaN is made NaN, for e4m3 has no infinity.
+    auto q_scale = [&](uint32_t largest, const AttnUnit& d, int r, bool keep) {
+        const int ex = static_cast<int>(largest >> 7);  // of the largest magnitude, bf16 bits
+        int sh = ex == 0 || ex == 255 ? 0 : 127 + 7 - ex;  // to [2^7, 2^8)
+        sh = max(-126, min(126, sh));
+        if (keep) s_rs[F8 ? d.seg & 3 : 0][F8 ? r : 0] = static_cast<int8_t>(sh);
+        return ex == 255 ? NAN : __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+    };
+    auto largest_of = [](uint32_t mx, const uint4& v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-                v[k] = row.live ? __ldg(src + from + k) : make_uint4(0, 0, 0, 0);
+        for (int e = 0; e < 4; ++e) mx = max(mx, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        return mx;
+    };
+    // 8 bf16 values as 8 bytes of either term
+    auto two_terms = [](const uint4& v, float up, uint32_t* hi, uint32_t* lo) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; e += 2)
+            e4m3_terms(pack2<true>(__uint_as_float(w[e] << 16) * up,
+                                   __uint_as_float(w[e] & 0xffff0000u) * up),
+                       pack2<true>(__uint_as_float(w[e + 1] << 16) * up,
+                                   __uint_as_float(w[e + 1] & 0xffff0000u) * up),
+                       hi[e / 2], lo[e / 2]);
+    };
+    auto queries = [&](const AttnUnit& d, int vw) {
+        const int qs = d.seg % S::kNQ;
+        auto source = [&](const AttnRow& row) {
+            return reinterpret_cast<const uint4*>(p.q +
+                                                  (static_cast<long long>(d.b) * p.R + row.i) * p.ldq +
+                                                  static_cast<long long>(row.hq) * D);
         };
-        if (F8) {
-            uint32_t mx = 0;  // largest magnitude, as bits
-#pragma unroll 1
-            for (int from = 0; from < D / 8; from += NV) {
-                get(from);
+        const bool reused = d.seg >= S::kNQ;
+        if constexpr (S::kQSmem) {
+            // a warp a row, a lane 8 dimensions; the first rows are on their way while the
+            // last products of the part before are waited for
+            constexpr int W = S::kVWarps, AHEAD = 4;
+            const int rows = p.tb * p.gb;
+            uint4 v[AHEAD];
+            for (int r0 = vw; r0 < rows; r0 += W * AHEAD) {
 #pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                for (int k = 0; k < AHEAD; ++k) {
+                    const int r = r0 + k * W;
+                    const AttnRow row = attn_row(p, d.g, r);
+                    v[k] = r < rows && row.live ? __ldg(source(row) + lane) : make_uint4(0, 0, 0, 0);
+                }
+                if (r0 == vw && reused && !warp_wait(&b_qe[qs], d.seg / S::kNQ - 1)) return false;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx = max(mx, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+                for (int k = 0; k < AHEAD; ++k) {
+                    const int r = r0 + k * W;
+                    if (r >= rows) break;
+                    if (F8) {
+                        const uint32_t mx = __reduce_max_sync(0xffffffffu, largest_of(0u, v[k]));
+                        uint32_t hi[2], lo[2];
+                        two_terms(v[k], q_scale(mx, d, r, lane == 0), hi, lo);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+                            *reinterpret_cast<uint2*>(
+                                smem + S::template at<S::kBoxB>(S::kQBlk, r, t * (D / 16) + lane / 2) +
+                                (lane & 1) * 8) = t ? make_uint2(lo[0], lo[1]) : make_uint2(hi[0], hi[1]);
+                    } else {
+                        *reinterpret_cast<uint4*>(smem + S::template at<S::kBoxB>(S::kQBlk, r, lane)) = v[k];
+                    }
                 }
             }
-            const int ex = static_cast<int>(mx >> 7);
-            int sh = ex == 0 || ex == 255 ? 0 : 127 + 7 - ex;  // to [2^7, 2^8)
-            sh = max(-126, min(126, sh));
-            // (a row with an infinity or NaN is made NaN: e4m3 has no infinity)
-            up = ex == 255 ? NAN : __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-            if (r < ROWS) s_rs[F8 ? d.seg & 3 : 0][F8 ? r : 0] = static_cast<int8_t>(sh);
-        } else {
-            get(0);
-        }
-        if (d.seg >= S::kNQ && !warp_wait(&b_qe[qs], d.seg / S::kNQ - 1)) return false;
-        tc_fence_after();
-        const uint32_t tq = tmem + (static_cast<uint32_t>(qw * 32) << 16) + S::kColQ + qs * (D / 2);
-#pragma unroll 1
-        for (int from = 0; from < D / 8; from += NV) {
-            if (F8 || from > 0) get(from);
+            if (vw >= rows && reused && !warp_wait(&b_qe[qs], d.seg / S::kNQ - 1)) return false;
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b_q[qs]);
+        } else if (vw < 4 && (warp & 3) < row_warps) {
+            // a row a thread (a warp reaches lanes 32 (warp % 4) .. of tensor memory)
+            const int r = (warp & 3) * 32 + lane;
+            const AttnRow row = attn_row(p, d.g, r);
+            const uint4* src = source(row);
+            uint4 v[D / 8];
 #pragma unroll
-            for (int c = 0; c < NV; c += 8) {  // 64 dimensions
+            for (int k = 0; k < D / 8; ++k) v[k] = row.live ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+            float up = 1.f;
+            if (F8) {
+                uint32_t mx = 0;
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) mx = largest_of(mx, v[k]);
+                up = q_scale(mx, d, r, r < ROWS);
+            }
+            if (reused && !warp_wait(&b_qe[qs], d.seg / S::kNQ - 1)) return false;
+            tc_fence_after();
+            const uint32_t tq = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + S::kColQ + qs * (D / 2);
+#pragma unroll
+            for (int c = 0; c < D / 8; c += 8) {  // 64 dimensions
                 uint32_t y[32];
-                if (F8) {  // hi: y[0 .. 15], lo: y[16 .. 31]
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t w[4] = {v[c + k].x, v[c + k].y, v[c + k].z, v[c + k].w};
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2)
-                            e4m3_terms(pack2<true>(__uint_as_float(w[e] << 16) * up,
-                                                   __uint_as_float(w[e] & 0xffff0000u) * up),
-                                       pack2<true>(__uint_as_float(w[e + 1] << 16) * up,
-                                                   __uint_as_float(w[e + 1] & 0xffff0000u) * up),
-                                       y[2 * k + e / 2], y[16 + 2 * k + e / 2]);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 8; ++k) {
+                    if (F8) {  // hi: y[0 .. 15], lo: y[16 .. 31]
+                        two_terms(v[c + k], up, y + 2 * k, y + 16 + 2 * k);
+                    } else {
                         y[4 * k] = v[c + k].x;
                         y[4 * k + 1] = v[c + k].y;
                         y[4 * k + 2] = v[c + k].z;
                         y[4 * k + 3] = v[c + k].w;
                     }
                 }
-                if (S::kQSmem) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        // e4m3: four chunks of 16 dimensions of either term
-                        const int chunk = F8 ? (k >> 2) * (D / 16) + (from + c) / 2 + (k & 3) : from + c + k;
-                        if (r < ROWS)
-                            *reinterpret_cast<uint4*>(smem + S::template at<S::kBoxB>(S::kQBlk, r, chunk)) =
-                                make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-                    }
-                } else if (F8) {
-                    tmem_st16(tq + (from + c) * 2, y);
-                    tmem_st16(tq + D / 4 + (from + c) * 2, y + 16);
+                if (F8) {
+                    tmem_st16(tq + c * 2, y);
+                    tmem_st16(tq + D / 4 + c * 2, y + 16);
                 } else {
-                    tmem_st32(tq + (from + c) * 4, y);
+                    tmem_st32(tq + c * 4, y);
                 }
             }
-        }
-        if (S::kQSmem) {
-            fence_async_smem();
-        } else {
             tmem_st_wait();
             tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b_q[qs]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b_q[qs]);
         return true;
     };
 
-    if (n_units > 0 && warp == 5) {
+    if (n_units > 0 && warp == kTcLoad) {
         // -------------------------------------------------------- producer
         constexpr int ESZ = S::kES, BOXB = S::kBoxB, KB = S::kKBlks, VB = S::kVBlks;
         AttnWalk<TK> w;
@@ -309,19 +337,18 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             for (int k = nv > NV ? nv - NV : 0; k < nv; ++k)
                 mbar_wait_bounded(&b_v[k % NV], (k / NV) & 1, p.wait_ns, nullptr);
         }
-    } else if (n_units > 0 && warp >= 6) {
-        // ------------------- queries in (the first four warps), V pieces passed on
+    } else if (n_units > 0 && warp >= kTcPass) {
+        // ----------------------------------------- queries in, V pieces passed on
         constexpr int N = S::kVWarps * 32;
-        const int at = tid - 192;
-        const int qw = warp & 3;  // (a warp reaches lanes 32 (warp % 4) .. of tensor memory)
+        const int at = tid - kTcPass * 32;
         bool first = true, ok = true;
         int parts = 0;
         for (int u = 0; u < n_units && ok; ++u) {
-            if (first && at < 128 && qw < row_warps) {
+            if (first) {
                 ok = warp_wait(&b_part[parts & 7], parts >> 3);
                 if (!ok) break;
                 const AttnUnit d = s_unit[u % kUnitRing];
-                ok = queries(d, qw);
+                ok = queries(d, warp - kTcPass);
                 if (!ok) break;
             }
             parts += first;
@@ -419,7 +446,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 }
             }
         }
-    } else if (n_units > 0 && warp == 4) {
+    } else if (n_units > 0 && warp == kTcMma) {
         // ----------------------------------------------- the tensor cores
         if (lane == 0) {
             constexpr uint32_t iS = tc_idesc(!F8, 128, TK, false);  // bf16, or e4m3
@@ -497,6 +524,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                     }
                 }
                 if (s_abort) break;
+                __nanosleep(20);
                 const uint64_t now = globaltimer_ns();
                 if (t0 == 0) t0 = now;
                 if (now - t0 > p.wait_ns) {
@@ -542,18 +570,18 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             auto masked = [&](int c) {  // 64 columns of the row from column c
                 tmem_ld64(x, tS + c);
                 if (edge) {
-                    // seen: k <= hi and (k > lo or k < sk)
+                    // seen: k <= hi and (k > lo or k < sk), as bits
                     const int hi = pr - td.start - c;
-                    if (p.window == 0) {
+                    auto below = [](int n) {  // bits 0 .. n - 1
+                        return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull);
+                    };
+                    unsigned long long seen = below(hi + 1);
+                    if (p.window > 0)
+                        seen &= ~below(hi - p.window + 1) | below(p.sinks - td.start - c);
+                    const uint32_t s_lo = static_cast<uint32_t>(seen), s_hi = static_cast<uint32_t>(seen >> 32);
 #pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            if (k > hi) x[k] = 0xff800000u;
-                    } else {
-                        const int lo = hi - p.window, sk = p.sinks - td.start - c;
-#pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            if (k > hi || (k <= lo && k >= sk)) x[k] = 0xff800000u;
-                    }
+                    for (int k = 0; k < 64; ++k)
+                        if (!((k < 32 ? s_lo >> k : s_hi >> (k - 32)) & 1u)) x[k] = 0xff800000u;
                 }
             };
 #pragma unroll
@@ -718,7 +746,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 4) {
+    if (warp == kTcMma) {
         tc_fence_after();
         tmem_dealloc<512>(tmem);
     }
