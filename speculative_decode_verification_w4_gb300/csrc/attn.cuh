@@ -349,12 +349,12 @@ __device__ __forceinline__ void attn_load_q(const AttnParams& p, const CUtensorM
 // ------------------------------------------------------- up to 16 query rows
 // Four warps share the 16 rows and take a quarter of a tile's keys each, so
 // every key and value byte is read from shared memory once; a fifth warp loads
-// (TMA, a box per page and 128 bytes of a key) into a ring.  The warps' running
+// K and a sixth V (TMA, a box per page and 128 bytes of a key) into a ring.  The warps' running
 // maxima, sums and outputs are joined at the end of an item's part.
 template <int D, bool F8>
 struct AttnShape {
     static constexpr int kWarps = 4;
-    static constexpr int kThreads = (kWarps + 1) * 32;
+    static constexpr int kThreads = (kWarps + 2) * 32;
     static constexpr int kTK = F8 ? 128 : 64;
     static constexpr int kRows = 16;
     static constexpr int kRB = D * (F8 ? 1 : 2);         // bytes of a key
@@ -367,7 +367,7 @@ struct AttnShape {
     static constexpr int kQ = kRows * D * 2;
     static constexpr int kQBlk = kRows * 128;
     static constexpr int kKW = kTK / kWarps;             // keys of a tile per warp
-    static constexpr int kStages = D == 256 ? 3 : (D == 128 ? 3 : 4);
+    static constexpr int kStages = D == 64 ? 6 : 3;
     static constexpr int kOffQ = kStages * kStage;
     static constexpr int kOffML = kOffQ + 2 * kQ;                  // float m, l [4][16]
     static constexpr int kOffRS = kOffML + 2 * kWarps * kRows * 4;  // float row scale [2][16]
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
     }
     if (tid == 0) {
         for (int k = 0; k < NST; ++k) {
-            mbar_init(&b_full[k], 1);
+            mbar_init(&b_full[k], 2);
             mbar_init(&b_empty[k], S::kWarps);
         }
         mbar_init(&b_qe[0], S::kWarps);
@@ -431,8 +431,9 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
         return __all_sync(0xffffffffu, ok) != 0;
     };
 
-    if (wk == S::kWarps) {
-        // -------------------------------------------------------- producer
+    if (wk >= S::kWarps) {
+        // ------------------------------------------------------- producers
+        const bool keys = wk == S::kWarps;  // else values
         AttnWalk<TK> w;
         w.begin(p, span, cap, lane);
         int u = 0;
@@ -440,21 +441,20 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
             const int st = u % NST;
             const AttnUnit d = w.unit(p);
             if (u >= NST && !wait(&b_empty[st], u / NST - 1)) break;
-            const bool first = d.flags & kUnitFirst;
-            if (first && d.seg >= 2 && !wait(&b_qe[d.seg & 1], (d.seg >> 1) - 1)) break;
-            const uint32_t kv = 2 * w.template bytes<0, TK, S::kNBlk, S::kBoxB>(lane);
+            const bool q = keys && (d.flags & kUnitFirst);
+            if (q && d.seg >= 2 && !wait(&b_qe[d.seg & 1], (d.seg >> 1) - 1)) break;
+            const uint32_t bytes = w.template bytes<0, TK, S::kNBlk, S::kBoxB>(lane);
             if (lane == 0) {
-                s_unit[u % kUnitRing] = d;
-                mbar_arrive_expect_tx(&b_full[st], kv + (first ? attn_q_bytes(p, D) : 0u));
-                if (first)
+                if (keys) s_unit[u % kUnitRing] = d;
+                mbar_arrive_expect_tx(&b_full[st], bytes + (q ? attn_q_bytes(p, D) : 0u));
+                if (q)
                     attn_load_q<D>(p, &maps.q, sm + S::kOffQ + (d.seg & 1) * S::kQ, S::kQBlk, d,
                                    &b_full[st]);
             }
             __syncwarp();
-            const uint32_t dst = sm + st * S::kStage;
-            w.template load<0, TK, 0, S::kNBlk, S::kBoxB, F8 ? 1 : 2>(p, &maps.k, dst, &b_full[st], lane);
-            w.template load<0, TK, 0, S::kNBlk, S::kBoxB, F8 ? 1 : 2>(p, &maps.v, dst + S::kTile,
-                                                                      &b_full[st], lane);
+            w.template load<0, TK, 0, S::kNBlk, S::kBoxB, F8 ? 1 : 2>(
+                p, keys ? &maps.k : &maps.v, sm + st * S::kStage + (keys ? 0 : S::kTile), &b_full[st],
+                lane);
             if (u + 1 < n_units) w.next(p, lane);
         }
         // copies in flight land before the block ends
@@ -877,7 +877,7 @@ cudaError_t attn_dispatch_rows(const AttnParams& p, const AttnMaps& maps, int ro
                                cudaStream_t s) {
     static std::atomic<unsigned long long> once[3];
     static std::atomic<int> occ[3];
-    constexpr int kMinBlocks = D == 256 ? 1 : (D == 128 ? 2 : 3);
+    constexpr int kMinBlocks = D == 256 ? 1 : 2;
     if (rows == 16)
         return attn_launch(attn_kernel<D, F8, kMinBlocks>, AttnShape<D, F8>::kThreads,
                            AttnShape<D, F8>::kSmem, once[0], occ[0], p, maps, grid, sms, s);

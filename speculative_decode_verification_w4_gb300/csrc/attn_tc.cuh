@@ -30,6 +30,8 @@
 // rescaled only when a row's maximum grew by more than 2^8 (its weights are then
 // at most 2^8, harmless in bf16, f16 and the fp32 sum).
 #pragma once
+#include <type_traits>
+
 #include "attn.cuh"
 
 namespace vw4 {
@@ -65,7 +67,7 @@ struct AttnTcShape {
                                   : (D == 64 ? 4 : (D == 128 || ROWS == 64 ? 3 : 2));
     static constexpr int kNF = !F8 ? 0 : (D == 64 ? 4 : 2);  // f16 pieces
     static constexpr int kVWarps = F8 ? 8 : 4;       // that pass V on
-    static constexpr int kThreads = (8 + kVWarps) * 32;  // warps 4 and 5 have no work
+    static constexpr int kThreads = (8 + kVWarps) * 32;  // warp 4 has no work
     static constexpr int kOffK = kQ;
     static constexpr int kOffV = kOffK + kNK * kKPiece;
     static constexpr int kOffF = kOffV + kNV * kVLoad;
@@ -89,10 +91,11 @@ struct AttnTcShape {
 
 constexpr float kLazy = 8.f;  // (log2) see above
 
-// Warps: 0 .. 3 softmax, 8 .. pass V on.  The loading warp and the one that issues
-// the products (it polls) share schedulers with the softmax warps that only the
-// largest blocks use.
-constexpr int kTcLoad = 6, kTcMma = 7, kTcPass = 8;
+// Warps: 0 .. 3 softmax, 8 .. pass V on.  The loading warps (one each for K and V: a box
+// costs its warp some 60 ns, and a tile of 16-token pages has 32) and the one that
+// issues the products (it polls) share schedulers with the softmax warps that only
+// the largest blocks use.
+constexpr int kTcLoadV = 5, kTcLoadK = 6, kTcMma = 7, kTcPass = 8;
 
 template <int D, bool F8, int ROWS>
 __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ volatile int s_odd[8];  // seg + 1: the part's values lost infinities or NaN
-    __shared__ AttnUnit s_unit[kUnitRing];
+    __shared__ AttnUnit s_unit[kUnitRing], s_vunit[kUnitRing];  // by the K and the V warp
     // A wait names a phase by its parity: when it begins, the phase before has to be over
     // and the one after not.  So products and scores have two barriers each, taken in
     // turn: S of tile u is committed after the product of tile u - 2.
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     const int row_warps = (p.tb * p.gb + 31) / 32;     // softmax warps with rows
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (tid == kTcLoad * 32) {
+    if (tid == kTcLoadK * 32) {
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
     }
@@ -288,55 +291,62 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         return true;
     };
 
-    if (n_units > 0 && warp == kTcLoad) {
-        // -------------------------------------------------------- producer
+    if (n_units > 0 && (warp == kTcLoadK || warp == kTcLoadV)) {
+        // -------------------------------------------------------- producers
+        const bool keys = warp == kTcLoadK;
         constexpr int ESZ = S::kES, BOXB = S::kBoxB, KB = S::kKBlks, VB = S::kVBlks;
+        uint64_t* full = keys ? b_k : b_v;
+        uint64_t* empty = keys ? b_ke : b_ve;
+        const int ring = keys ? NK : NV;
         AttnWalk<TK> w;
         w.begin(p, span, cap, lane);
-        int nk = 0, nv = 0;  // pieces loaded
+        int n = 0, st = 0, round = 0;  // pieces loaded; the next one's place
         bool ok = true;
-        // the next piece's place, once it is free; its bytes are announced
-        auto place = [&](uint64_t* full, uint64_t* empty, int n, int ring, uint32_t bytes) {
-            ok = n < ring || warp_wait(&empty[n % ring], n / ring - 1);
-            if (ok && lane == 0) mbar_arrive_expect_tx(&full[n % ring], bytes);
+        // waits for the place and announces the bytes that come
+        auto place = [&](uint32_t bytes) {
+            ok = round == 0 || warp_wait(&empty[st], round - 1);
+            if (ok && lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
             __syncwarp();
             return ok;
         };
+        auto loaded = [&] {
+            ++n;
+            if (++st == ring) st = 0, ++round;
+        };
         for (int u = 0; u < n_units; ++u) {
-            const AttnUnit d = w.unit(p);
             if (lane == 0) {
-                s_unit[u % kUnitRing] = d;
-                if (d.flags & kUnitFirst) mbar_arrive(&b_part[d.seg & 7]);  // its queries may be read
+                const AttnUnit d = w.unit(p);
+                (keys ? s_unit : s_vunit)[u % kUnitRing] = d;
+                if (keys && (d.flags & kUnitFirst)) mbar_arrive(&b_part[d.seg & 7]);
             }
-            if (!place(b_k, b_ke, nk, NK, w.template bytes<0, TK, KB, BOXB>(lane))) break;
-            w.template load<0, TK, 0, KB, BOXB, ESZ>(p, &maps.k, sm + S::kOffK + nk % NK * S::kKPiece,
-                                                     &b_k[nk % NK], lane);
-            ++nk;
-            if (KP == 2) {
-                if (!place(b_k, b_ke, nk, NK, w.template bytes<0, TK, KB, BOXB>(lane))) break;
-                w.template load<0, TK, KB, KB, BOXB, ESZ>(
-                    p, &maps.k, sm + S::kOffK + nk % NK * S::kKPiece, &b_k[nk % NK], lane);
-                ++nk;
-            }
-            if (!place(b_v, b_ve, nv, NV, w.template bytes<0, S::kVKeys, VB, BOXB>(lane))) break;
-            w.template load<0, S::kVKeys, 0, VB, BOXB, ESZ>(
-                p, &maps.v, sm + S::kOffV + nv % NV * S::kVLoad, &b_v[nv % NV], lane);
-            ++nv;
-            if (VP == 2) {
-                if (!place(b_v, b_ve, nv, NV, w.template bytes<S::kVKeys, S::kVKeys, VB, BOXB>(lane)))
-                    break;
-                w.template load<S::kVKeys, S::kVKeys, 0, VB, BOXB, ESZ>(
-                    p, &maps.v, sm + S::kOffV + nv % NV * S::kVLoad, &b_v[nv % NV], lane);
-                ++nv;
+            if (keys) {
+                if (!place(w.template bytes<0, TK, KB, BOXB>(lane))) break;
+                w.template load<0, TK, 0, KB, BOXB, ESZ>(p, &maps.k, sm + S::kOffK + st * S::kKPiece,
+                                                         &full[st], lane);
+                loaded();
+                if (KP == 2) {
+                    if (!place(w.template bytes<0, TK, KB, BOXB>(lane))) break;
+                    w.template load<0, TK, KB, KB, BOXB, ESZ>(
+                        p, &maps.k, sm + S::kOffK + st * S::kKPiece, &full[st], lane);
+                    loaded();
+                }
+            } else {
+                if (!place(w.template bytes<0, S::kVKeys, VB, BOXB>(lane))) break;
+                w.template load<0, S::kVKeys, 0, VB, BOXB, ESZ>(
+                    p, &maps.v, sm + S::kOffV + st * S::kVLoad, &full[st], lane);
+                loaded();
+                if (VP == 2) {
+                    if (!place(w.template bytes<S::kVKeys, S::kVKeys, VB, BOXB>(lane))) break;
+                    w.template load<S::kVKeys, S::kVKeys, 0, VB, BOXB, ESZ>(
+                        p, &maps.v, sm + S::kOffV + st * S::kVLoad, &full[st], lane);
+                    loaded();
+                }
             }
             if (u + 1 < n_units) w.next(p, lane);
         }
-        if (!ok) {  // copies in flight land before the block ends
-            for (int k = nk > NK ? nk - NK : 0; k < nk; ++k)
-                mbar_wait_bounded(&b_k[k % NK], (k / NK) & 1, p.wait_ns, nullptr);
-            for (int k = nv > NV ? nv - NV : 0; k < nv; ++k)
-                mbar_wait_bounded(&b_v[k % NV], (k / NV) & 1, p.wait_ns, nullptr);
-        }
+        if (!ok)  // copies in flight land before the block ends
+            for (int k = n > ring ? n - ring : 0; k < n; ++k)
+                mbar_wait_bounded(&full[k % ring], (k / ring) & 1, p.wait_ns, nullptr);
     } else if (n_units > 0 && warp >= kTcPass) {
         // ----------------------------------------- queries in, V pieces passed on
         constexpr int N = S::kVWarps * 32;
@@ -357,7 +367,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 const int pc = u * VP + i, st = pc % NV;
                 ok = warp_wait(&b_v[st], pc / NV);
                 if (!ok) break;
-                const AttnUnit d = s_unit[u % kUnitRing];
+                const AttnUnit d = s_vunit[u % kUnitRing];
                 first = d.flags & kUnitLast;  // (of the next unit)
                 // Values that no row sees become zeros; infinities and NaN of values that
                 // only some rows see too (0 times them must not reach the other rows): the
@@ -400,20 +410,19 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 ok = pc < NF || warp_wait(&b_fe[pc % NF], pc / NF - 1);
                 if (!ok) break;
                 uint8_t* dst = smem + S::kOffF + pc % NF * S::kVPiece;
-#pragma unroll 4
-                for (int k = 0; k < S::kVKeys * CH / N; ++k) {
-                    const int c = at + k * N, row = c / CH, ch = c % CH;  // 16 dimensions of a key
+                auto pass = [&](int c, auto cleaning) {
+                    const int row = c / CH, ch = c % CH;  // 16 dimensions of a key
                     const uint4 v = *reinterpret_cast<const uint4*>(
                         src + S::template at<S::kBoxB>(S::kVKeys * S::kBoxB, row, ch));
                     uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    if (edge) {
+                    if (cleaning) {
                         const int j = key0 + row;
                         if (!key_some(j, d.len, d.p0, p.window, p.sinks)) {
                             w[0] = w[1] = w[2] = w[3] = 0u;
                         } else if (!key_all(j, d.len, d.p0, p.window, p.sinks)) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-#pragma unroll
+#pragma unroll 1
                                 for (int q = 0; q < 32; q += 8)
                                     if (((w[e] >> q) & 0x7Fu) == 0x7Fu) {
                                         w[e] &= ~(0xFFu << q);
@@ -436,6 +445,13 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                         flip ? b : a;
                     *reinterpret_cast<uint4*>(dst + S::template at<128>(S::kVBlk, row, 2 * ch + 1 - flip)) =
                         flip ? a : b;
+                };
+                if (edge) {
+#pragma unroll 1
+                    for (int c = at; c < S::kVKeys * CH; c += N) pass(c, std::true_type{});
+                } else {
+#pragma unroll 2
+                    for (int c = at; c < S::kVKeys * CH; c += N) pass(c, std::false_type{});
                 }
                 if (odd) s_odd[d.seg & 7] = d.seg + 1;
                 fence_async_smem();
@@ -565,37 +581,42 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 l = 0.f;
             }
             const uint32_t tS = tmem + lanes + S::kColS + (u & 1) * TK;
-            uint32_t x[64];
+            // The row is walked 32 columns at a time, twice, by rolled loops: the roles share
+            // the instruction caches, and unrolled over 128 columns this one alone
+            // overflowed them (a fifth of all warp stalls waited for instructions).
+            uint32_t x[32];
             float mx = -INFINITY;
-            auto masked = [&](int c) {  // 64 columns of the row from column c
-                tmem_ld64(x, tS + c);
+            auto columns = [&](int c) {  // 32 columns of the row from column c
+                tmem_ld32(x, tS + c);
                 if (edge) {
                     // seen: k <= hi and (k > lo or k < sk), as bits
                     const int hi = pr - td.start - c;
                     auto below = [](int n) {  // bits 0 .. n - 1
-                        return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull);
+                        return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
                     };
-                    unsigned long long seen = below(hi + 1);
-                    if (p.window > 0)
-                        seen &= ~below(hi - p.window + 1) | below(p.sinks - td.start - c);
-                    const uint32_t s_lo = static_cast<uint32_t>(seen), s_hi = static_cast<uint32_t>(seen >> 32);
+                    uint32_t seen = below(hi + 1);
+                    if (p.window > 0) seen &= ~below(hi - p.window + 1) | below(p.sinks - td.start - c);
 #pragma unroll
-                    for (int k = 0; k < 64; ++k)
-                        if (!((k < 32 ? s_lo >> k : s_hi >> (k - 32)) & 1u)) x[k] = 0xff800000u;
+                    for (int k = 0; k < 32; ++k)
+                        if (!((seen >> k) & 1u)) x[k] = 0xff800000u;
                 }
             };
+#pragma unroll 1
+            for (int c = 0; c < TK; c += 32) {
+                columns(c);
+                float m1 = -INFINITY;
 #pragma unroll
-            for (int c = TK - 64; c >= 0; c -= 64) {
-                masked(c);
-#pragma unroll
-                for (int k = 0; k < 64; k += 2)
-                    mx = fmaxf(mx, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+                for (int k = 0; k < 32; k += 2) {
+                    mx = fmaxf(mx, __uint_as_float(x[k]));
+                    m1 = fmaxf(m1, __uint_as_float(x[k + 1]));
+                }
+                mx = fmaxf(mx, m1);
             }
             bool grow = false;
             float corr = 1.f;
             if (first) {
                 m = mx;
-            } else if ((mx - m) * c2 > kLazy) {
+            } else if (row.live && (mx - m) * c2 > kLazy) {  // (the other rows hold anything)
                 // (m = -infinity: O and l are zeros still)
                 if (m != -INFINITY) {
                     corr = ex2((m - mx) * c2);
@@ -619,19 +640,20 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             }
             const float mc = m == -INFINITY ? 0.f : m * c2;
             float s0 = 0.f, s1 = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < TK; c += 32) {
+                // (P's columns c / 2 .. + 15 hold scores that have been read)
+                columns(c);
+                uint32_t y[16];
 #pragma unroll
-            for (int c = 0; c < TK; c += 64) {
-                if (c > 0) masked(c);
-                uint32_t y[32];
-#pragma unroll
-                for (int k = 0; k < 64; k += 2) {
+                for (int k = 0; k < 32; k += 2) {
                     const float a = ex2(fmaf(__uint_as_float(x[k]), c2, -mc));
                     const float b = ex2(fmaf(__uint_as_float(x[k + 1]), c2, -mc));
                     s0 += a;
                     s1 += b;
                     y[k / 2] = pack2<F8>(a, b);
                 }
-                tmem_st32(tS + c / 2, y);
+                tmem_st16(tS + c / 2, y);
             }
             l += s0 + s1;
             tmem_st_wait();
