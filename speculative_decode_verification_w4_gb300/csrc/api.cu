@@ -176,8 +176,8 @@ int encode_map(CUtensorMap* map, bool bf16, int n, const void* base, const uint6
                const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw) {
     struct Key {
         const void* base;
-        uint64_t d[4], s[4];
-        uint32_t b[4];
+        uint64_t d[5], s[5];
+        uint32_t b[5];
         int n, bf16, sw;
     };
     constexpr int kSlots = 64;
@@ -205,8 +205,8 @@ int encode_map(CUtensorMap* map, bool bf16, int n, const void* base, const uint6
                 return VW4_OK;
             }
     }
-    cuuint64_t d[4], st[3];
-    cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], one[5] = {1, 1, 1, 1, 1};
     for (int i = 0; i < n; ++i) {
         d[i] = key.d[i];
         b[i] = key.b[i];

@@ -141,6 +141,17 @@ AttnPlan attn_plan(AttnParams& p, int D, bool f8, void* ws) {
     p.box_rows = p.page_size < piece ? p.page_size : piece;
     const int key = D * (f8 ? 1 : 2);
     plan.box_bytes = key < 128 ? key : 128;
+    plan.v_blocks = key / plan.box_bytes;
+    plan.k_blocks = plan.rows > 16 && D == 256 && !f8 ? 2 : plan.v_blocks;  // of a piece
+    const long long group = 8 * p.token_stride;  // elements
+    if (p.head_stride == D || p.Hkv == 1) {
+        p.fold = kFoldBlocks;
+    } else if (p.head_stride % group == 0) {
+        p.fold = kFoldGroups;
+        p.fold_step = static_cast<int>(p.head_stride / group);
+    } else {
+        p.fold = kFoldNone;
+    }
     plan.swizzle = key == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     return plan;
 }

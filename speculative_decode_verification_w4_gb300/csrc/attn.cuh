@@ -230,29 +230,64 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnParams& p, int cap, int 
     return r;
 }
 
-// The producer warp's walk over the CTA's units.  Every lane holds the walk;
+// A tile to load: every lane holds it, and the page of the lane's box.
+struct AttnTile {
+    int start, h, box_rows;
+    int page;  // -1: no box to load
+    // A part of the tile of K or V: keys FROM .. FROM + KEYS, BLKS blocks of BOXB
+    // bytes of a key from block BLK of ALL on.  In shared memory it is atoms of 8 keys x
+    // BOXB bytes, the blocks of 8 keys next to each other.  Its bytes (the boxes that
+    // some row sees), and its load, one box a page where the layout of the cache lets
+    // the head be a coordinate of the blocks (heads next to each other) or of the
+    // groups of 8 tokens (heads above tokens); a box an atom else.
+    template <int FROM, int KEYS, int BLKS, int BOXB>
+    __device__ __forceinline__ uint32_t bytes(int lane) const {
+        const int key = lane * box_rows;
+        return __popc(__ballot_sync(0xffffffffu, page >= 0 && key >= FROM && key < FROM + KEYS)) *
+               static_cast<uint32_t>(box_rows * BLKS * BOXB);
+    }
+    template <int FROM, int KEYS, int BLK, int BLKS, int ALL, int BOXB, int ESZ>
+    __device__ __forceinline__ void load(const AttnParams& p, const CUtensorMap* map, uint32_t dst,
+                                         uint64_t* bar, int lane) const {
+        const int key = lane * box_rows;
+        if (page >= 0 && key >= FROM && key < FROM + KEYS) {
+            const int token = (start + key) & (p.page_size - 1);
+            dst += (key - FROM) * (BLKS * BOXB);
+            if (p.fold != kFoldNone) {
+                tma_load_5d(dst, map, 0, 0, p.fold == kFoldBlocks ? h * ALL + BLK : BLK,
+                            (p.fold == kFoldGroups ? h * p.fold_step : 0) + (token >> 3), page, bar);
+            } else {
+#pragma unroll 1
+                for (int t = 0; t < box_rows; t += 8)
+#pragma unroll 1
+                    for (int k = 0; k < BLKS; ++k)
+                        tma_load_4d(dst + (t * BLKS + k * 8) * BOXB, map, (BLK + k) * (BOXB / ESZ), h,
+                                    token + t, page, bar);
+            }
+        }
+        __syncwarp();
+    }
+};
+
+// The producer warps' walk over the CTA's units.  Every lane holds the walk;
 // lane l also holds the page of the l-th box of the current tile.
 template <int TK>
 struct AttnWalk {
     int b, g, t, u, n, seg, cap;
     AttnSeq s;
     int box_rows, boxes;  // tokens of a page box, boxes of a tile
-    int page;             // -1: no box to load; num_pages: a bad page (reads as zeros)
+    int page;             // of this lane's box, as read (on its way until it is used)
+    bool want;            // some row sees a key of that box
     __device__ __forceinline__ int start() const { return (t < s.ns ? t : t + s.skip) * TK; }
     __device__ __forceinline__ void fetch(const AttnParams& p, int lane) {
         const int lo = start() + lane * box_rows;
-        page = -1;
+        want = false;
         if (lane < boxes && lo < s.len) {
             const int hi = min(lo + box_rows, s.len) - 1;
-            if (p.window == 0 || hi > s.p0 - p.window || lo < p.sinks) {
-                page = __ldg(p.table + static_cast<long long>(b) * p.table_stride +
-                             (lo >> p.page_shift));
-                if (page < 0 || page >= p.num_pages) {
-                    page = p.num_pages;
-                    atomicOr(p.status, kStatusBadPage);
-                }
-            }
+            want = p.window == 0 || hi > s.p0 - p.window || lo < p.sinks;
         }
+        if (want)
+            page = __ldg(p.table + static_cast<long long>(b) * p.table_stride + (lo >> p.page_shift));
     }
     __device__ __forceinline__ void enter(const AttnParams& p, int lane) {
         const int raw = p.seq_lens[b];
@@ -307,27 +342,20 @@ struct AttnWalk {
         }
         fetch(p, lane);
     }
-    // A part of the current tile of K or V: keys FROM .. FROM + KEYS, BLKS blocks of BOXB
-    // bytes of a key from block BLK on.  Its bytes (the boxes that some row sees), and
-    // its load: block k at dst + k * KEYS * BOXB, a row of BOXB bytes a key.
-    template <int FROM, int KEYS, int BLKS, int BOXB>
-    __device__ __forceinline__ uint32_t bytes(int lane) const {
-        const int key = lane * box_rows;
-        return __popc(__ballot_sync(0xffffffffu, page >= 0 && key >= FROM && key < FROM + KEYS)) *
-               static_cast<uint32_t>(box_rows * BLKS * BOXB);
-    }
-    template <int FROM, int KEYS, int BLK, int BLKS, int BOXB, int ESZ>
-    __device__ __forceinline__ void load(const AttnParams& p, const CUtensorMap* map, uint32_t dst,
-                                         uint64_t* bar, int lane) const {
-        const int key = lane * box_rows;
-        if (page >= 0 && key >= FROM && key < FROM + KEYS) {
-            const int token = (start() + key) & (p.page_size - 1);
-#pragma unroll
-            for (int k = 0; k < BLKS; ++k)
-                tma_load_4d(dst + k * (KEYS * BOXB) + (key - FROM) * BOXB, map,
-                            (BLK + k) * (BOXB / ESZ), g / p.row_blocks, token, page, bar);
+    // The current tile, for its loads after the walk has moved on (so that the next
+    // tile's pages are on their way meanwhile).  A page outside the cache becomes
+    // num_pages, which reads as zeros.
+    __device__ __forceinline__ AttnTile tile(const AttnParams& p) const {
+        AttnTile t;
+        t.start = start();
+        t.h = g / p.row_blocks;
+        t.box_rows = box_rows;
+        t.page = want ? page : -1;
+        if (want && (page < 0 || page >= p.num_pages)) {
+            t.page = p.num_pages;
+            atomicOr(p.status, kStatusBadPage);
         }
-        __syncwarp();
+        return t;
     }
 };
 
@@ -361,7 +389,6 @@ struct AttnShape {
     static constexpr int kBoxB = kRB < 128 ? kRB : 128;  // of them in a box
     static constexpr int kNBlk = kRB / kBoxB;
     static constexpr int kCPB = kBoxB / 16;
-    static constexpr int kBlk = kTK * kBoxB;
     static constexpr int kTile = kTK * kRB;              // 128 D bytes
     static constexpr int kStage = 2 * kTile;             // K then V
     static constexpr int kQ = kRows * D * 2;
@@ -376,7 +403,8 @@ struct AttnShape {
     static_assert(kSmem <= 225 * 1024, "shared memory");
     __device__ static __forceinline__ uint32_t at(int row, int chunk) {  // chunk of 16 bytes of a key
         const int x = kBoxB == 64 ? (row >> 1) & 3 : row & 7;
-        return static_cast<uint32_t>(chunk / kCPB * kBlk + row * kBoxB + (((chunk % kCPB) ^ x) << 4));
+        return static_cast<uint32_t>(((row >> 3) * kNBlk + chunk / kCPB) * (8 * kBoxB) +
+                                     (row & 7) * kBoxB + (((chunk % kCPB) ^ x) << 4));
     }
     __device__ static __forceinline__ uint32_t q_at(int row, int chunk) {  // 16 bytes of a query
         return static_cast<uint32_t>((chunk >> 3) * kQBlk + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
@@ -440,10 +468,12 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
         for (; u < n_units; ++u) {
             const int st = u % NST;
             const AttnUnit d = w.unit(p);
+            const AttnTile t = w.tile(p);
+            if (u + 1 < n_units) w.next(p, lane);
             if (u >= NST && !wait(&b_empty[st], u / NST - 1)) break;
             const bool q = keys && (d.flags & kUnitFirst);
             if (q && d.seg >= 2 && !wait(&b_qe[d.seg & 1], (d.seg >> 1) - 1)) break;
-            const uint32_t bytes = w.template bytes<0, TK, S::kNBlk, S::kBoxB>(lane);
+            const uint32_t bytes = t.template bytes<0, TK, S::kNBlk, S::kBoxB>(lane);
             if (lane == 0) {
                 if (keys) s_unit[u % kUnitRing] = d;
                 mbar_arrive_expect_tx(&b_full[st], bytes + (q ? attn_q_bytes(p, D) : 0u));
@@ -452,10 +482,9 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
                                    &b_full[st]);
             }
             __syncwarp();
-            w.template load<0, TK, 0, S::kNBlk, S::kBoxB, F8 ? 1 : 2>(
+            t.template load<0, TK, 0, S::kNBlk, S::kNBlk, S::kBoxB, F8 ? 1 : 2>(
                 p, keys ? &maps.k : &maps.v, sm + st * S::kStage + (keys ? 0 : S::kTile), &b_full[st],
                 lane);
-            if (u + 1 < n_units) w.next(p, lane);
         }
         // copies in flight land before the block ends
         if (u < n_units) {

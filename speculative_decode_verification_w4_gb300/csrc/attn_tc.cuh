@@ -45,8 +45,8 @@ struct AttnTcShape {
     // K: pieces of kKBlks blocks of kBoxB bytes of a key
     static constexpr int kKP = D == 256 && !F8 ? 2 : 1;
     static constexpr int kKBlks = D * kES / kKP / kBoxB;
-    static constexpr int kKBlk = kTK * kBoxB;
-    static constexpr int kKPiece = kKBlks * kKBlk;
+    static constexpr int kAtom = 8 * kBoxB;          // 8 keys of a block
+    static constexpr int kKPiece = kTK / 8 * kKBlks * kAtom;
     static constexpr int kSteps = kBoxB / 32;        // k steps (32 bytes) of a block
     static constexpr int kTerms = F8 ? 2 : 1;        // of Q
     // V: pieces of kVKeys keys, as loaded and as multiplied (16-bit, blocks of 64 dimensions)
@@ -80,6 +80,11 @@ struct AttnTcShape {
     // tensor memory columns: O, two S, the queries (two 16-bit values a column)
     static constexpr uint32_t kColO = 0, kColS = D, kColQ = D + 2 * kTK;
     static_assert(D + 2 * kTK + (kQSmem ? 0 : kNQ * D / 2) <= 512, "tensor memory");
+    // 16 bytes of a key of a V piece as it is loaded
+    __device__ static __forceinline__ uint32_t v_at(int row, int chunk) {
+        return static_cast<uint32_t>((row >> 3) * kVBlks * kAtom) +
+               at<kBoxB>(kAtom, row & 7, chunk);
+    }
     // 16 bytes of a row: blocks of blk bytes, rows of BOXB bytes in them
     template <int BOXB>
     __device__ static __forceinline__ uint32_t at(int blk, int row, int chunk) {
@@ -319,30 +324,31 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 (keys ? s_unit : s_vunit)[u % kUnitRing] = d;
                 if (keys && (d.flags & kUnitFirst)) mbar_arrive(&b_part[d.seg & 7]);
             }
+            const AttnTile t = w.tile(p);
+            if (u + 1 < n_units) w.next(p, lane);
             if (keys) {
-                if (!place(w.template bytes<0, TK, KB, BOXB>(lane))) break;
-                w.template load<0, TK, 0, KB, BOXB, ESZ>(p, &maps.k, sm + S::kOffK + st * S::kKPiece,
+                if (!place(t.template bytes<0, TK, KB, BOXB>(lane))) break;
+                t.template load<0, TK, 0, KB, VB, BOXB, ESZ>(p, &maps.k, sm + S::kOffK + st * S::kKPiece,
                                                          &full[st], lane);
                 loaded();
                 if (KP == 2) {
-                    if (!place(w.template bytes<0, TK, KB, BOXB>(lane))) break;
-                    w.template load<0, TK, KB, KB, BOXB, ESZ>(
+                    if (!place(t.template bytes<0, TK, KB, BOXB>(lane))) break;
+                    t.template load<0, TK, KB, KB, VB, BOXB, ESZ>(
                         p, &maps.k, sm + S::kOffK + st * S::kKPiece, &full[st], lane);
                     loaded();
                 }
             } else {
-                if (!place(w.template bytes<0, S::kVKeys, VB, BOXB>(lane))) break;
-                w.template load<0, S::kVKeys, 0, VB, BOXB, ESZ>(
+                if (!place(t.template bytes<0, S::kVKeys, VB, BOXB>(lane))) break;
+                t.template load<0, S::kVKeys, 0, VB, VB, BOXB, ESZ>(
                     p, &maps.v, sm + S::kOffV + st * S::kVLoad, &full[st], lane);
                 loaded();
                 if (VP == 2) {
-                    if (!place(w.template bytes<S::kVKeys, S::kVKeys, VB, BOXB>(lane))) break;
-                    w.template load<S::kVKeys, S::kVKeys, 0, VB, BOXB, ESZ>(
+                    if (!place(t.template bytes<S::kVKeys, S::kVKeys, VB, BOXB>(lane))) break;
+                    t.template load<S::kVKeys, S::kVKeys, 0, VB, VB, BOXB, ESZ>(
                         p, &maps.v, sm + S::kOffV + st * S::kVLoad, &full[st], lane);
                     loaded();
                 }
             }
-            if (u + 1 < n_units) w.next(p, lane);
         }
         if (!ok)  // copies in flight land before the block ends
             for (int k = n > ring ? n - ring : 0; k < n; ++k)
@@ -384,7 +390,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                             const int row = c / CH, j = key0 + row;
                             if (key_all(j, d.len, d.p0, p.window, p.sinks)) continue;
                             uint4* q = reinterpret_cast<uint4*>(
-                                src + S::template at<S::kBoxB>(S::kVKeys * S::kBoxB, row, c % CH));
+                                src + S::v_at(row, c % CH));
                             if (!key_some(j, d.len, d.p0, p.window, p.sinks)) {
                                 *q = make_uint4(0, 0, 0, 0);
                                 continue;
@@ -413,7 +419,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 auto pass = [&](int c, auto cleaning) {
                     const int row = c / CH, ch = c % CH;  // 16 dimensions of a key
                     const uint4 v = *reinterpret_cast<const uint4*>(
-                        src + S::template at<S::kBoxB>(S::kVKeys * S::kBoxB, row, ch));
+                        src + S::v_at(row, ch));
                     uint32_t w[4] = {v.x, v.y, v.z, v.w};
                     if (cleaning) {
                         const int j = key0 + row;
@@ -487,8 +493,8 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
 #pragma unroll
                                 for (int ks = 0; ks < KS; ++ks) {
                                     const uint64_t kd = tc_desc<S::kBoxB>(
-                                        k + (ks / S::kSteps) * S::kKBlk + (ks % S::kSteps) * 32, 16,
-                                        8 * S::kBoxB);
+                                        k + (ks / S::kSteps) * S::kAtom + (ks % S::kSteps) * 32, 16,
+                                        S::kKBlks * S::kAtom);
                                     const int kq = t * (S::kQRow / 32) + kp * KS + ks;  // k step of Q
                                     const bool add = t > 0 || kp > 0 || ks > 0;
                                     if (S::kQSmem)
@@ -526,7 +532,10 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                         for (int ks = 0; ks < S::kVKeys / 16; ++ks)
                             tc_mma_ts<false>(tmem + S::kColO,
                                              tmem + S::kColS + (pv & 1) * TK + (vp * (S::kVKeys / 16) + ks) * 8,
-                                             tc_desc<128>(v + ks * 2048, S::kVBlk, 1024), iO,
+                                             F8 ? tc_desc<128>(v + ks * 2048, S::kVBlk, 1024)
+                                                : tc_desc<128>(v + ks * (2 * S::kVBlks * S::kAtom), S::kAtom,
+                                                               S::kVBlks * S::kAtom),
+                                             iO,
                                              !(first && vp == 0 && ks == 0));
                         tc_commit(F8 ? &b_fe[pc % NF] : &b_ve[pc % NV]);
                         if (++vp == VP) {

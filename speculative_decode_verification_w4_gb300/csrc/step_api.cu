@@ -168,15 +168,26 @@ VW4_API vw4_status verify_attn(const vw4_attn* a, void* workspace_dev, size_t ws
         // strides of dimensions of one element are never used, but must be valid
         const uint64_t step = f8 ? 16 : 8;
         const auto valid = [step](int64_t v) { return v > 0 ? static_cast<uint64_t>(v) : step; };
-        const uint64_t dims[4] = {static_cast<uint64_t>(c.D), static_cast<uint64_t>(c.Hkv),
-                                  static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(c.num_pages)};
-        const uint64_t strides[3] = {valid(c.head_stride), valid(c.token_stride), valid(c.page_stride)};
-        const uint32_t box[4] = {static_cast<uint32_t>(plan.box_bytes / (f8 ? 1 : 2)), 1u,
-                                 static_cast<uint32_t>(p.box_rows), 1u};
-        st = static_cast<vw4_status>(encode_map(&maps.k, !f8, 4, c.k_dev, dims, strides, box, plan.swizzle));
-        if (st != VW4_OK) return st;
-        st = static_cast<vw4_status>(encode_map(&maps.v, !f8, 4, c.v_dev, dims, strides, box, plan.swizzle));
-        if (st != VW4_OK) return st;
+        const uint64_t Hkv = static_cast<uint64_t>(c.Hkv), pages = static_cast<uint64_t>(c.num_pages);
+        const uint64_t page = static_cast<uint64_t>(c.page_size), block = plan.box_bytes / (f8 ? 1 : 2);
+        const uint64_t all = static_cast<uint64_t>(c.D) / block, token = valid(c.token_stride);
+        const uint64_t groups = p.fold == kFoldGroups ? (Hkv - 1) * p.fold_step + page / 8 : page / 8;
+        const uint64_t dims5[5] = {block, 8, p.fold == kFoldBlocks ? Hkv * all : all, groups, pages};
+        const uint64_t strides5[4] = {token, block, 8 * token, valid(c.page_stride)};
+        const uint64_t dims4[4] = {static_cast<uint64_t>(c.D), Hkv, page, pages};
+        const uint64_t strides4[3] = {valid(c.head_stride), token, valid(c.page_stride)};
+        for (int v = 0; v < 2; ++v) {
+            const uint32_t box5[5] = {static_cast<uint32_t>(block), 8u,
+                                      static_cast<uint32_t>(v ? plan.v_blocks : plan.k_blocks),
+                                      static_cast<uint32_t>(p.box_rows / 8), 1u};
+            const uint32_t box4[4] = {static_cast<uint32_t>(block), 1u, 8u, 1u};
+            CUtensorMap* m = v ? &maps.v : &maps.k;
+            const void* base = v ? c.v_dev : c.k_dev;
+            st = static_cast<vw4_status>(
+                p.fold != kFoldNone ? encode_map(m, !f8, 5, base, dims5, strides5, box5, plan.swizzle)
+                                    : encode_map(m, !f8, 4, base, dims4, strides4, box4, plan.swizzle));
+            if (st != VW4_OK) return st;
+        }
         const uint64_t qd[3] = {static_cast<uint64_t>(c.D), static_cast<uint64_t>(a->Hq),
                                 static_cast<uint64_t>(a->B) * a->R};
         const uint64_t qs[2] = {static_cast<uint64_t>(c.D), static_cast<uint64_t>(a->ldq)};

@@ -234,12 +234,15 @@ struct AttnParams {
     int window, sinks;
     int page_size, page_shift, max_blocks, num_pages;
     int box_rows;           // tokens of a TMA box
+    int fold, fold_step;    // how a box finds its head (AttnWalk::load); groups per head
     // the query rows of a key head in blocks of tb verify indexes x gb heads:
     // blocks_g of them along the heads, row_blocks in all; groups = Hkv * row_blocks
     int tb, gb, blocks_g, row_blocks, groups;
 };
-// TMA maps of the cache (dimension, head, token of the page, page) and of the
-// queries (dimension, head, row).
+constexpr int kFoldNone = 0, kFoldBlocks = 1, kFoldGroups = 2;
+// TMA maps of the cache (dimensions of a block, 8 tokens, block, 8-token group, page;
+// unfolded: dimension, head, token of the page, page) and of the queries (dimension,
+// head, row).
 struct AttnMaps {
     CUtensorMap k, v, q;
 };
@@ -248,7 +251,8 @@ size_t attn_workspace_bytes(int B, int rows, int D);
 // Plans a call: block shape, grid bound and workspace pointers in p.
 struct AttnPlan {
     int rows, tk, grid;
-    int box_bytes;             // bytes of a key in a box of K or V
+    int box_bytes;             // bytes of a key in a block of a box of K or V
+    int k_blocks, v_blocks;    // blocks of a box
     CUtensorMapSwizzle swizzle;
 };
 AttnPlan attn_plan(AttnParams& p, int D, bool f8, void* ws);

@@ -48,6 +48,28 @@ def test_pages(page, order, kv):
     run_case(page, [5, 300, 1025], 3, 8, 4, 128, page, kv, order)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page,order", [(8, "nhd"), (8, "hnd"), (128, "hnd"), (256, "nhd")])
+def test_pages_many_rows(page, order, D, kv):
+    run_case(page + 1, [5, 300, 1025], 9, 8, 4, D, page, kv, order)
+
+
+@pytest.mark.parametrize("R", [2, 9])
+@pytest.mark.parametrize("D,kv", [(64, "e4m3"), (128, "bf16"), (256, "bf16"), (256, "e4m3")])
+def test_head_stride_of_its_own(D, kv, R):
+    """Heads spaced apart by neither a head nor whole groups of tokens."""
+    lens, page, Hkv = [200, 77], 16, 3
+    c, k64, v64 = make_cache(33, lens, page, Hkv, D, kv)
+    stores = []
+    for t in (c.k, c.v):
+        wide = torch.zeros(t.shape[0], page, Hkv, D + 32, device="cuda").to(t.dtype)
+        wide[..., :D] = t
+        stores.append(wide[..., :D])
+    cache = vw4.KVCache(stores[0], stores[1], c.block_table, c.k_scale, c.v_scale)
+    run_case(33, lens, R, 6, Hkv, D, page, kv, cache=(cache, k64, v64))
+
+
 @pytest.mark.parametrize("D,kv", [(64, "bf16"), (128, "e4m3"), (256, "bf16"), (256, "e4m3")])
 @pytest.mark.parametrize("R", [1, 8])
 def test_long_split(R, D, kv):
