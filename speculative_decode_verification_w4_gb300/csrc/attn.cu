@@ -137,7 +137,10 @@ AttnPlan attn_plan(AttnParams& p, int D, bool f8, void* ws) {
     plan.grid = attn_grid_cap(D);
     if (units < plan.grid) plan.grid = static_cast<int>(units < 1 ? 1 : units);
     // a box lies inside a page and inside a ring piece of the kernel
-    const int piece = plan.rows > 16 && D == 256 ? 64 : plan.tk;
+    const int piece = plan.rows == 16 ? plan.tk
+                      : D == 256      ? (f8 ? 32 : 64)
+                      : D == 128 && f8 ? 64
+                                       : 128;
     p.box_rows = p.page_size < piece ? p.page_size : piece;
     const int key = D * (f8 ? 1 : 2);
     plan.box_bytes = key < 128 ? key : 128;

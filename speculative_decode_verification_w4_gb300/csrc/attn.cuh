@@ -234,34 +234,34 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnParams& p, int cap, int 
 struct AttnTile {
     int start, h, box_rows;
     int page;  // -1: no box to load
-    // A part of the tile of K or V: keys FROM .. FROM + KEYS, BLKS blocks of BOXB
-    // bytes of a key from block BLK of ALL on.  In shared memory it is atoms of 8 keys x
+    // A part of the tile of K or V: keys from .. from + KEYS, BLKS blocks of BOXB
+    // bytes of a key from block blk of ALL on.  In shared memory it is atoms of 8 keys x
     // BOXB bytes, the blocks of 8 keys next to each other.  Its bytes (the boxes that
     // some row sees), and its load, one box a page where the layout of the cache lets
     // the head be a coordinate of the blocks (heads next to each other) or of the
     // groups of 8 tokens (heads above tokens); a box an atom else.
-    template <int FROM, int KEYS, int BLKS, int BOXB>
-    __device__ __forceinline__ uint32_t bytes(int lane) const {
+    template <int KEYS, int BLKS, int BOXB>
+    __device__ __forceinline__ uint32_t bytes(int from, int lane) const {
         const int key = lane * box_rows;
-        return __popc(__ballot_sync(0xffffffffu, page >= 0 && key >= FROM && key < FROM + KEYS)) *
+        return __popc(__ballot_sync(0xffffffffu, page >= 0 && key >= from && key < from + KEYS)) *
                static_cast<uint32_t>(box_rows * BLKS * BOXB);
     }
-    template <int FROM, int KEYS, int BLK, int BLKS, int ALL, int BOXB, int ESZ>
+    template <int KEYS, int BLKS, int ALL, int BOXB, int ESZ>
     __device__ __forceinline__ void load(const AttnParams& p, const CUtensorMap* map, uint32_t dst,
-                                         uint64_t* bar, int lane) const {
+                                         uint64_t* bar, int from, int blk, int lane) const {
         const int key = lane * box_rows;
-        if (page >= 0 && key >= FROM && key < FROM + KEYS) {
+        if (page >= 0 && key >= from && key < from + KEYS) {
             const int token = (start + key) & (p.page_size - 1);
-            dst += (key - FROM) * (BLKS * BOXB);
+            dst += (key - from) * (BLKS * BOXB);
             if (p.fold != kFoldNone) {
-                tma_load_5d(dst, map, 0, 0, p.fold == kFoldBlocks ? h * ALL + BLK : BLK,
+                tma_load_5d(dst, map, 0, 0, p.fold == kFoldBlocks ? h * ALL + blk : blk,
                             (p.fold == kFoldGroups ? h * p.fold_step : 0) + (token >> 3), page, bar);
             } else {
 #pragma unroll 1
                 for (int t = 0; t < box_rows; t += 8)
 #pragma unroll 1
                     for (int k = 0; k < BLKS; ++k)
-                        tma_load_4d(dst + (t * BLKS + k * 8) * BOXB, map, (BLK + k) * (BOXB / ESZ), h,
+                        tma_load_4d(dst + (t * BLKS + k * 8) * BOXB, map, (blk + k) * (BOXB / ESZ), h,
                                     token + t, page, bar);
             }
         }
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
             if (u >= NST && !wait(&b_empty[st], u / NST - 1)) break;
             const bool q = keys && (d.flags & kUnitFirst);
             if (q && d.seg >= 2 && !wait(&b_qe[d.seg & 1], (d.seg >> 1) - 1)) break;
-            const uint32_t bytes = t.template bytes<0, TK, S::kNBlk, S::kBoxB>(lane);
+            const uint32_t bytes = t.template bytes<TK, S::kNBlk, S::kBoxB>(0, lane);
             if (lane == 0) {
                 if (keys) s_unit[u % kUnitRing] = d;
                 mbar_arrive_expect_tx(&b_full[st], bytes + (q ? attn_q_bytes(p, D) : 0u));
@@ -482,9 +482,9 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
                                    &b_full[st]);
             }
             __syncwarp();
-            t.template load<0, TK, 0, S::kNBlk, S::kNBlk, S::kBoxB, F8 ? 1 : 2>(
+            t.template load<TK, S::kNBlk, S::kNBlk, S::kBoxB, F8 ? 1 : 2>(
                 p, keys ? &maps.k : &maps.v, sm + st * S::kStage + (keys ? 0 : S::kTile), &b_full[st],
-                lane);
+                0, 0, lane);
         }
         // copies in flight land before the block ends
         if (u < n_units) {

@@ -5,7 +5,7 @@
 // One CTA per SM, warps with roles.  A producer warp loads tiles of 128 keys
 // (TMA) into two rings in the swizzled layout the tensor cores read, one of K
 // pieces and one of V pieces (a piece is the whole tile, or at head size 256 and
-// bf16 half of K's dimensions; at head size 256 half of V's keys).  One thread
+// bf16 half of K's dimensions; of V 32, 64 or all 128 keys).  One thread
 // issues S = Q K^T and O += P V piece by piece, whichever has its operands first.
 // The softmax warps own one query row a thread, so the softmax has no shuffles,
 // and S and P never pass through shared memory.  S has two buffers: Q K^T of the
@@ -50,7 +50,7 @@ struct AttnTcShape {
     static constexpr int kSteps = kBoxB / 32;        // k steps (32 bytes) of a block
     static constexpr int kTerms = F8 ? 2 : 1;        // of Q
     // V: pieces of kVKeys keys, as loaded and as multiplied (16-bit, blocks of 64 dimensions)
-    static constexpr int kVP = D == 256 ? 2 : 1;
+    static constexpr int kVP = D < 256 ? (F8 && D == 128 ? 2 : 1) : (F8 ? 4 : 2);
     static constexpr int kVKeys = kTK / kVP;
     static constexpr int kVBlks = D * kES / kBoxB;
     static constexpr int kVLoad = kVKeys * D * kES;
@@ -63,9 +63,9 @@ struct AttnTcShape {
     static constexpr int kNQ = kQSmem ? 1 : 2;       // query buffers
     static_assert(!(F8 && D == 256 && ROWS > 64), "blocks of 64 rows");
     static constexpr int kNK = F8 ? (D == 64 ? 6 : (D == 128 ? 4 : 2)) : (D == 64 ? 4 : (D == 128 ? 3 : 2));
-    static constexpr int kNV = F8 ? (D == 64 ? 6 : (D == 128 ? 4 : 3))
+    static constexpr int kNV = F8 ? (D == 64 ? 6 : (D == 128 ? 8 : 6))
                                   : (D == 64 ? 4 : (D == 128 || ROWS == 64 ? 3 : 2));
-    static constexpr int kNF = !F8 ? 0 : (D == 64 ? 4 : 2);  // f16 pieces
+    static constexpr int kNF = !F8 ? 0 : (D == 128 ? 3 : 4);  // f16 pieces
     static constexpr int kVWarps = F8 ? 8 : 4;       // that pass V on
     static constexpr int kThreads = (8 + kVWarps) * 32;  // warp 4 has no work
     static constexpr int kOffK = kQ;
@@ -314,10 +314,6 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             __syncwarp();
             return ok;
         };
-        auto loaded = [&] {
-            ++n;
-            if (++st == ring) st = 0, ++round;
-        };
         for (int u = 0; u < n_units; ++u) {
             if (lane == 0) {
                 const AttnUnit d = w.unit(p);
@@ -326,29 +322,22 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             }
             const AttnTile t = w.tile(p);
             if (u + 1 < n_units) w.next(p, lane);
-            if (keys) {
-                if (!place(t.template bytes<0, TK, KB, BOXB>(lane))) break;
-                t.template load<0, TK, 0, KB, VB, BOXB, ESZ>(p, &maps.k, sm + S::kOffK + st * S::kKPiece,
-                                                         &full[st], lane);
-                loaded();
-                if (KP == 2) {
-                    if (!place(t.template bytes<0, TK, KB, BOXB>(lane))) break;
-                    t.template load<0, TK, KB, KB, VB, BOXB, ESZ>(
-                        p, &maps.k, sm + S::kOffK + st * S::kKPiece, &full[st], lane);
-                    loaded();
-                }
-            } else {
-                if (!place(t.template bytes<0, S::kVKeys, VB, BOXB>(lane))) break;
-                t.template load<0, S::kVKeys, 0, VB, VB, BOXB, ESZ>(
-                    p, &maps.v, sm + S::kOffV + st * S::kVLoad, &full[st], lane);
-                loaded();
-                if (VP == 2) {
-                    if (!place(t.template bytes<S::kVKeys, S::kVKeys, VB, BOXB>(lane))) break;
-                    t.template load<S::kVKeys, S::kVKeys, 0, VB, VB, BOXB, ESZ>(
-                        p, &maps.v, sm + S::kOffV + st * S::kVLoad, &full[st], lane);
-                    loaded();
-                }
+#pragma unroll 1
+            for (int i = 0; i < (keys ? KP : VP) && ok; ++i) {
+                const int from = keys ? 0 : i * S::kVKeys, blk = keys ? i * KB : 0;
+                if (!place(keys ? t.template bytes<TK, KB, BOXB>(0, lane)
+                                : t.template bytes<S::kVKeys, VB, BOXB>(from, lane)))
+                    break;
+                if (keys)
+                    t.template load<TK, KB, VB, BOXB, ESZ>(p, &maps.k, sm + S::kOffK + st * S::kKPiece,
+                                                           &full[st], from, blk, lane);
+                else
+                    t.template load<S::kVKeys, VB, VB, BOXB, ESZ>(
+                        p, &maps.v, sm + S::kOffV + st * S::kVLoad, &full[st], from, blk, lane);
+                ++n;
+                if (++st == ring) st = 0, ++round;
             }
+            if (!ok) break;
         }
         if (!ok)  // copies in flight land before the block ends
             for (int k = n > ring ? n - ring : 0; k < n; ++k)
