@@ -14,9 +14,10 @@
 // columns, else (head size 256) in shared memory: tiles of 64 keys would make
 // room, but the products of 64 columns run at half the rate of those of 128.
 //
-// The last role brings an item's queries to their place and passes V on, cleaned
-// where not every row sees every key: four warps for bf16; for e4m3 eight, which
-// turn it into f16 (exact) in a third ring.
+// Four warps bring an item's queries to their place, and four pass V on, cleaned
+// where not every row sees every key: together for bf16 (most tiles need nothing),
+// for e4m3 a piece each, turned into f16 (exact) in a third ring: a piece is more
+// latency than work, so several go on at once.
 //
 // e4m3 keys are multiplied as they are (kind::f8f6f4); a query row, scaled by a
 // power of two that puts its largest magnitude into [2^7, 2^8), is the sum of two
@@ -65,16 +66,15 @@ struct AttnTcShape {
     static constexpr int kNK = F8 ? (D == 64 ? 6 : (D == 128 ? 4 : 2)) : (D == 64 ? 4 : (D == 128 ? 3 : 2));
     static constexpr int kNV = F8 ? (D == 64 ? 6 : (D == 128 ? 8 : 6))
                                   : (D == 64 ? 4 : (D == 128 || ROWS == 64 ? 3 : 2));
-    static constexpr int kNF = !F8 ? 0 : (D == 128 ? 3 : 4);  // f16 pieces
-    static constexpr int kVWarps = F8 ? 8 : 4;       // that pass V on
-    static constexpr int kThreads = (8 + kVWarps) * 32;  // warp 4 has no work
+    static constexpr int kNF = !F8 ? 0 : 4;  // f16 pieces
+    static constexpr int kThreads = 16 * 32;         // (warp 4 has no work)
     static constexpr int kOffK = kQ;
     static constexpr int kOffV = kOffK + kNK * kKPiece;
     static constexpr int kOffF = kOffV + kNV * kVLoad;
     static constexpr int kOffStage = kOffF + kNF * kVPiece;    // 4 KB a softmax warp, for the output
-    static constexpr int kUsed = kOffStage + 4 * 4096 + 1024;  // and alignment
+    static constexpr int kUsed = kOffStage + ROWS / 32 * 4096 + 1024;  // and alignment
     static constexpr int kSmem = kUsed < 115 * 1024 ? 115 * 1024 : kUsed;  // one CTA per SM
-    static_assert(kSmem + 2048 <= 227 * 1024, "shared memory");
+    static_assert(kSmem + 3072 <= 227 * 1024, "shared memory");
     // the products read 128 rows of Q whatever ROWS is: what follows must be there
     static_assert(!kQSmem || kOffStage >= (kTerms * kQRow / kBoxB - 1) * kQBlk + 128 * kBoxB, "Q reads");
     // tensor memory columns: O, two S, the queries (two 16-bit values a column)
@@ -96,11 +96,11 @@ struct AttnTcShape {
 
 constexpr float kLazy = 8.f;  // (log2) see above
 
-// Warps: 0 .. 3 softmax, 8 .. pass V on.  The loading warps (one each for K and V: a box
+// Warps: 0 .. 3 softmax, 8 .. 11 queries, 12 .. 15 pass V on.  The loading warps (one each for K and V: a box
 // costs its warp some 60 ns, and a tile of 16-token pages has 32) and the one that
 // issues the products (it polls) share schedulers with the softmax warps that only
 // the largest blocks use.
-constexpr int kTcLoadV = 5, kTcLoadK = 6, kTcMma = 7, kTcPass = 8;
+constexpr int kTcLoadV = 5, kTcLoadK = 6, kTcMma = 7, kTcQ = 8, kTcPass = 12;
 
 template <int D, bool F8, int ROWS>
 __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
@@ -114,6 +114,8 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     __shared__ volatile int s_abort;
     __shared__ volatile int s_odd[8];  // seg + 1: the part's values lost infinities or NaN
     __shared__ AttnUnit s_unit[kUnitRing], s_vunit[kUnitRing];  // by the K and the V warp
+    __shared__ AttnUnit s_part[8];     // first units of the parts
+    __shared__ volatile int s_parts;   // how many parts, once it is known
     // A wait names a phase by its parity: when it begins, the phase before has to be over
     // and the one after not.  So products and scores have two barriers each, taken in
     // turn: S of tile u is committed after the product of tile u - 2.
@@ -140,24 +142,25 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             }
             for (int k = 0; k < NV; ++k) {
                 mbar_init(&b_v[k], 1);
-                mbar_init(&b_ve[k], F8 ? S::kVWarps : 1);
+                mbar_init(&b_ve[k], 1);
             }
             for (int k = 0; k < NF; ++k) mbar_init(&b_fe[k], 1);
             for (int k = 0; k < 2; ++k) {
                 mbar_init(&b_s[k], 1);
                 mbar_init(&b_pv[k], 1);
                 mbar_init(&b_p[k], row_warps);
-                mbar_init(&b_q[k], S::kQSmem ? S::kVWarps : row_warps);
+                mbar_init(&b_q[k], S::kQSmem ? 4 : row_warps);
                 mbar_init(&b_qe[k], 1);
             }
             for (int k = 0; k < 8; ++k) {
                 mbar_init(&b_part[k], 1);
-                mbar_init(&b_clean[k], S::kVWarps);
+                mbar_init(&b_clean[k], F8 ? 1 : 4);
             }
             mbar_init(&b_o, row_warps);
             mbar_init(&b_end, 1);
             fence_barrier_init();
             s_abort = 0;
+            s_parts = 1 << 30;
             for (int k = 0; k < 8; ++k) s_odd[k] = 0;
         }
         tc_fence_before();
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         if constexpr (S::kQSmem) {
             // a warp a row, a lane 8 dimensions; the first rows are on their way while the
             // last products of the part before are waited for
-            constexpr int W = S::kVWarps, AHEAD = 4;
+            constexpr int W = 4, AHEAD = 8;
             const int rows = p.tb * p.gb;
             uint4 v[AHEAD];
             for (int r0 = vw; r0 < rows; r0 += W * AHEAD) {
@@ -249,9 +252,9 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b_q[qs]);
-        } else if (vw < 4 && (warp & 3) < row_warps) {
+        } else if (vw < row_warps) {
             // a row a thread (a warp reaches lanes 32 (warp % 4) .. of tensor memory)
-            const int r = (warp & 3) * 32 + lane;
+            const int r = vw * 32 + lane;
             const AttnRow row = attn_row(p, d.g, r);
             const uint4* src = source(row);
             uint4 v[D / 8];
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             }
             if (reused && !warp_wait(&b_qe[qs], d.seg / S::kNQ - 1)) return false;
             tc_fence_after();
-            const uint32_t tq = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + S::kColQ + qs * (D / 2);
+            const uint32_t tq = tmem + (static_cast<uint32_t>(vw * 32) << 16) + S::kColQ + qs * (D / 2);
 #pragma unroll
             for (int c = 0; c < D / 8; c += 8) {  // 64 dimensions
                 uint32_t y[32];
@@ -318,7 +321,14 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             if (lane == 0) {
                 const AttnUnit d = w.unit(p);
                 (keys ? s_unit : s_vunit)[u % kUnitRing] = d;
-                if (keys && (d.flags & kUnitFirst)) mbar_arrive(&b_part[d.seg & 7]);
+                if (keys && (d.flags & kUnitFirst)) {
+                    s_part[d.seg & 7] = d;
+                    mbar_arrive(&b_part[d.seg & 7]);  // its queries may be read
+                }
+                if (keys && u == n_units - 1) {
+                    s_parts = d.seg + 1;
+                    mbar_arrive(&b_part[(d.seg + 1) & 7]);
+                }
             }
             const AttnTile t = w.tile(p);
             if (u + 1 < n_units) w.next(p, lane);
@@ -342,119 +352,107 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         if (!ok)  // copies in flight land before the block ends
             for (int k = n > ring ? n - ring : 0; k < n; ++k)
                 mbar_wait_bounded(&full[k % ring], (k / ring) & 1, p.wait_ns, nullptr);
+    } else if (n_units > 0 && warp >= kTcQ && warp < kTcPass) {
+        // --------------------------------------------------------- queries
+        for (int k = 0;; ++k) {
+            if (!warp_wait(&b_part[k & 7], k >> 3) || k >= s_parts) break;
+            const AttnUnit d = s_part[k & 7];
+            if (!queries(d, warp - kTcQ)) break;
+        }
     } else if (n_units > 0 && warp >= kTcPass) {
-        // ----------------------------------------- queries in, V pieces passed on
-        constexpr int N = S::kVWarps * 32;
+        // ---------------------------------------------------- V pieces passed on
         const int at = tid - kTcPass * 32;
-        bool first = true, ok = true;
-        int parts = 0;
-        for (int u = 0; u < n_units && ok; ++u) {
-            if (first) {
-                ok = warp_wait(&b_part[parts & 7], parts >> 3);
-                if (!ok) break;
-                const AttnUnit d = s_unit[u % kUnitRing];
-                ok = queries(d, warp - kTcPass);
-                if (!ok) break;
-            }
-            parts += first;
-#pragma unroll 1
-            for (int i = 0; i < VP; ++i) {
-                const int pc = u * VP + i, st = pc % NV;
-                ok = warp_wait(&b_v[st], pc / NV);
-                if (!ok) break;
-                const AttnUnit d = s_vunit[u % kUnitRing];
-                first = d.flags & kUnitLast;  // (of the next unit)
-                // Values that no row sees become zeros; infinities and NaN of values that
-                // only some rows see too (0 times them must not reach the other rows): the
-                // end of the part gives them to the rows that see them.
-                const bool edge = d.flags & kUnitEdge;
-                const int key0 = d.start + i * S::kVKeys;
-                uint8_t* src = smem + S::kOffV + st * S::kVLoad;
-                constexpr int CH = D * S::kES / 16;
-                bool odd = false;
-                if (!F8) {
-                    if (edge) {
-#pragma unroll 1
-                        for (int c = at; c < S::kVKeys * CH; c += N) {
-                            const int row = c / CH, j = key0 + row;
-                            if (key_all(j, d.len, d.p0, p.window, p.sinks)) continue;
-                            uint4* q = reinterpret_cast<uint4*>(
-                                src + S::v_at(row, c % CH));
-                            if (!key_some(j, d.len, d.p0, p.window, p.sinks)) {
-                                *q = make_uint4(0, 0, 0, 0);
-                                continue;
-                            }
-                            const uint4 v = *q;
-                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                            bool hit = false;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xffff0000u, hit = true;
-                                if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xffffu, hit = true;
-                            }
-                            if (hit) *q = make_uint4(w[0], w[1], w[2], w[3]);
-                            odd |= hit;
-                        }
-                        if (odd) s_odd[d.seg & 7] = d.seg + 1;
-                        fence_async_smem();
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&b_clean[pc & 7]);
-                    continue;
-                }
-                ok = pc < NF || warp_wait(&b_fe[pc % NF], pc / NF - 1);
-                if (!ok) break;
-                uint8_t* dst = smem + S::kOffF + pc % NF * S::kVPiece;
-                auto pass = [&](int c, auto cleaning) {
-                    const int row = c / CH, ch = c % CH;  // 16 dimensions of a key
-                    const uint4 v = *reinterpret_cast<const uint4*>(
-                        src + S::v_at(row, ch));
-                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    if (cleaning) {
-                        const int j = key0 + row;
-                        if (!key_some(j, d.len, d.p0, p.window, p.sinks)) {
-                            w[0] = w[1] = w[2] = w[3] = 0u;
-                        } else if (!key_all(j, d.len, d.p0, p.window, p.sinks)) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-#pragma unroll 1
-                                for (int q = 0; q < 32; q += 8)
-                                    if (((w[e] >> q) & 0x7Fu) == 0x7Fu) {
-                                        w[e] &= ~(0xFFu << q);
-                                        odd = true;
-                                    }
-                        }
-                    }
-                    uint32_t f[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        f[2 * e] = e4m3x2_f16x2(w[e]);
-                        f[2 * e + 1] = e4m3x2_f16x2(w[e] >> 16);
-                    }
-                    // lanes of neighbouring 64-dimension blocks write their two chunks in
-                    // opposite order: eight lanes then cover all banks
-                    const int flip = (ch >> 2) & 1;
-                    const uint4 a = make_uint4(f[0], f[1], f[2], f[3]);
-                    const uint4 b = make_uint4(f[4], f[5], f[6], f[7]);
-                    *reinterpret_cast<uint4*>(dst + S::template at<128>(S::kVBlk, row, 2 * ch + flip)) =
-                        flip ? b : a;
-                    *reinterpret_cast<uint4*>(dst + S::template at<128>(S::kVBlk, row, 2 * ch + 1 - flip)) =
-                        flip ? a : b;
-                };
+        constexpr int CH = D * S::kES / 16;
+        for (int pc = F8 ? warp - kTcPass : 0; pc < n_units * VP; pc += F8 ? 4 : 1) {
+            const int u = pc / VP, st = pc % NV;
+            if (!warp_wait(&b_v[st], pc / NV)) break;
+            const AttnUnit d = s_vunit[u % kUnitRing];
+            // Values that no row sees become zeros; infinities and NaN of values that only
+            // some rows see too (0 times them must not reach the other rows): the end of
+            // the part gives them to the rows that see them.
+            const bool edge = d.flags & kUnitEdge;
+            const int key0 = d.start + (pc % VP) * S::kVKeys;
+            uint8_t* src = smem + S::kOffV + st * S::kVLoad;
+            bool odd = false;
+            if (!F8) {
                 if (edge) {
 #pragma unroll 1
-                    for (int c = at; c < S::kVKeys * CH; c += N) pass(c, std::true_type{});
-                } else {
-#pragma unroll 2
-                    for (int c = at; c < S::kVKeys * CH; c += N) pass(c, std::false_type{});
+                    for (int c = at; c < S::kVKeys * CH; c += 128) {
+                        const int row = c / CH, j = key0 + row;
+                        if (key_all(j, d.len, d.p0, p.window, p.sinks)) continue;
+                        uint4* q = reinterpret_cast<uint4*>(src + S::v_at(row, c % CH));
+                        if (!key_some(j, d.len, d.p0, p.window, p.sinks)) {
+                            *q = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        const uint4 v = *q;
+                        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        bool hit = false;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xffff0000u, hit = true;
+                            if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xffffu, hit = true;
+                        }
+                        if (hit) *q = make_uint4(w[0], w[1], w[2], w[3]);
+                        odd |= hit;
+                    }
+                    if (odd) s_odd[d.seg & 7] = d.seg + 1;
+                    fence_async_smem();
                 }
-                if (odd) s_odd[d.seg & 7] = d.seg + 1;
-                fence_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&b_clean[pc & 7]);
-                    mbar_arrive(&b_ve[st]);
+                if (lane == 0) mbar_arrive(&b_clean[pc & 7]);
+                continue;
+            }
+            if (pc >= NF && !warp_wait(&b_fe[pc % NF], pc / NF - 1)) break;
+            uint8_t* dst = smem + S::kOffF + pc % NF * S::kVPiece;
+            auto pass = [&](int c, auto cleaning) {
+                const int row = c / CH, ch = c % CH;  // 16 dimensions of a key
+                const uint4 v = *reinterpret_cast<const uint4*>(src + S::v_at(row, ch));
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                if (decltype(cleaning)::value) {
+                    const int j = key0 + row;
+                    if (!key_some(j, d.len, d.p0, p.window, p.sinks)) {
+                        w[0] = w[1] = w[2] = w[3] = 0u;
+                    } else if (!key_all(j, d.len, d.p0, p.window, p.sinks)) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+#pragma unroll 1
+                            for (int q = 0; q < 32; q += 8)
+                                if (((w[e] >> q) & 0x7Fu) == 0x7Fu) {
+                                    w[e] &= ~(0xFFu << q);
+                                    odd = true;
+                                }
+                    }
                 }
+                uint32_t f[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[2 * e] = e4m3x2_f16x2(w[e]);
+                    f[2 * e + 1] = e4m3x2_f16x2(w[e] >> 16);
+                }
+                // lanes of neighbouring 64-dimension blocks write their two chunks in
+                // opposite order: eight lanes then cover all banks
+                const int flip = (ch >> 2) & 1;
+                const uint4 a = make_uint4(f[0], f[1], f[2], f[3]);
+                const uint4 b = make_uint4(f[4], f[5], f[6], f[7]);
+                *reinterpret_cast<uint4*>(dst + S::template at<128>(S::kVBlk, row, 2 * ch + flip)) =
+                    flip ? b : a;
+                *reinterpret_cast<uint4*>(dst + S::template at<128>(S::kVBlk, row, 2 * ch + 1 - flip)) =
+                    flip ? a : b;
+            };
+            if (edge) {
+#pragma unroll 1
+                for (int c = lane; c < S::kVKeys * CH; c += 32) pass(c, std::true_type{});
+            } else {
+#pragma unroll 4
+                for (int c = lane; c < S::kVKeys * CH; c += 32) pass(c, std::false_type{});
+            }
+            if (odd) s_odd[d.seg & 7] = d.seg + 1;
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&b_clean[pc & 7]);
+                mbar_arrive(&b_ve[st]);
             }
         }
     } else if (n_units > 0 && warp == kTcMma) {
