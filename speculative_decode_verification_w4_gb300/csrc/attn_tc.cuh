@@ -31,8 +31,6 @@
 // rescaled only when a row's maximum grew by more than 2^8 (its weights are then
 // at most 2^8, harmless in bf16, f16 and the fp32 sum).
 #pragma once
-#include <type_traits>
-
 #include "attn.cuh"
 
 namespace vw4 {
@@ -405,12 +403,22 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             }
             if (pc >= NF && !warp_wait(&b_fe[pc % NF], pc / NF - 1)) break;
             uint8_t* dst = smem + S::kOffF + pc % NF * S::kVPiece;
-            auto pass = [&](int c, auto cleaning) {
-                const int row = c / CH, ch = c % CH;  // 16 dimensions of a key
-                const uint4 v = *reinterpret_cast<const uint4*>(src + S::v_at(row, ch));
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                if (decltype(cleaning)::value) {
-                    const int j = key0 + row;
+            auto write = [&](const uint32_t* w, uint8_t* lo, uint8_t* hi) {  // 16 dimensions
+                uint32_t f[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[2 * e] = e4m3x2_f16x2(w[e]);
+                    f[2 * e + 1] = e4m3x2_f16x2(w[e] >> 16);
+                }
+                *reinterpret_cast<uint4*>(lo) = make_uint4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<uint4*>(hi) = make_uint4(f[4], f[5], f[6], f[7]);
+            };
+            if (edge) {
+#pragma unroll 1
+                for (int c = lane; c < S::kVKeys * CH; c += 32) {
+                    const int row = c / CH, ch = c % CH, j = key0 + row;
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + S::v_at(row, ch));
+                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
                     if (!key_some(j, d.len, d.p0, p.window, p.sinks)) {
                         w[0] = w[1] = w[2] = w[3] = 0u;
                     } else if (!key_all(j, d.len, d.p0, p.window, p.sinks)) {
@@ -423,29 +431,37 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                                     odd = true;
                                 }
                     }
+                    write(w, dst + S::template at<128>(S::kVBlk, row, 2 * ch),
+                          dst + S::template at<128>(S::kVBlk, row, 2 * ch + 1));
                 }
-                uint32_t f[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    f[2 * e] = e4m3x2_f16x2(w[e]);
-                    f[2 * e + 1] = e4m3x2_f16x2(w[e] >> 16);
-                }
-                // lanes of neighbouring 64-dimension blocks write their two chunks in
-                // opposite order: eight lanes then cover all banks
-                const int flip = (ch >> 2) & 1;
-                const uint4 a = make_uint4(f[0], f[1], f[2], f[3]);
-                const uint4 b = make_uint4(f[4], f[5], f[6], f[7]);
-                *reinterpret_cast<uint4*>(dst + S::template at<128>(S::kVBlk, row, 2 * ch + flip)) =
-                    flip ? b : a;
-                *reinterpret_cast<uint4*>(dst + S::template at<128>(S::kVBlk, row, 2 * ch + 1 - flip)) =
-                    flip ? a : b;
-            };
-            if (edge) {
-#pragma unroll 1
-                for (int c = lane; c < S::kVKeys * CH; c += 32) pass(c, std::true_type{});
             } else {
-#pragma unroll 4
-                for (int c = lane; c < S::kVKeys * CH; c += 32) pass(c, std::false_type{});
+                // Eight neighbouring lanes take four chunks of rows r and r + 5 of a group of
+                // eight: loads and stores then fall into different banks.  The offsets within
+                // a group are the lane's own, so the loop is loads, conversions and stores.
+                constexpr int P = CH / 4;  // passes of a warp over a group of eight rows
+                uint32_t from[P], lo[P], hi[P];
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    const int idx = (lane >> 3) + 4 * k;         // 4 chunks of a pair of rows
+                    const int ch = idx % P * 4 + (lane & 3);
+                    const int row = (idx / P * 2 + (lane & 4 ? 5 : 0)) & 7;
+                    from[k] = S::v_at(row, ch);
+                    lo[k] = S::template at<128>(S::kVBlk, row, 2 * ch);
+                    hi[k] = S::template at<128>(S::kVBlk, row, 2 * ch + 1);
+                }
+#pragma unroll 1
+                for (int g = 0; g < S::kVKeys / 8; ++g) {
+                    const uint8_t* sg = src + g * (S::kVBlks * S::kAtom);
+                    uint8_t* dg = dst + g * 1024;
+                    uint4 v[P];
+#pragma unroll
+                    for (int k = 0; k < P; ++k) v[k] = *reinterpret_cast<const uint4*>(sg + from[k]);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                        write(w, dg + lo[k], dg + hi[k]);
+                    }
+                }
             }
             if (odd) s_odd[d.seg & 7] = d.seg + 1;
             fence_async_smem();
