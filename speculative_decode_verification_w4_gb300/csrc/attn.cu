@@ -145,7 +145,7 @@ AttnPlan attn_plan(AttnParams& p, int D, bool f8, void* ws) {
     const int key = D * (f8 ? 1 : 2);
     plan.box_bytes = key < 128 ? key : 128;
     plan.v_blocks = key / plan.box_bytes;
-    plan.k_blocks = plan.rows > 16 && D == 256 && !f8 ? 2 : plan.v_blocks;  // of a piece
+    plan.k_blocks = plan.rows > 16 && D == 256 ? plan.v_blocks / 2 : plan.v_blocks;  // of a piece
     const long long group = 8 * p.token_stride;  // elements
     if (p.head_stride == D || p.Hkv == 1) {
         p.fold = kFoldBlocks;

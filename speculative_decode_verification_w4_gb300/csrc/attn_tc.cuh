@@ -4,8 +4,8 @@
 //
 // One CTA per SM, warps with roles.  A producer warp loads tiles of 128 keys
 // (TMA) into two rings in the swizzled layout the tensor cores read, one of K
-// pieces and one of V pieces (a piece is the whole tile, or at head size 256 and
-// bf16 half of K's dimensions; of V 32, 64 or all 128 keys).  One thread
+// pieces and one of V pieces (a piece is the whole tile, or at head size 256
+// half of K's dimensions; of V 32, 64 or all 128 keys).  One thread
 // issues S = Q K^T and O += P V piece by piece, whichever has its operands first.
 // The softmax warps own one query row a thread, so the softmax has no shuffles,
 // and S and P never pass through shared memory.  S has two buffers: Q K^T of the
@@ -14,7 +14,8 @@
 // columns, else (head size 256) in shared memory: tiles of 64 keys would make
 // room, but the products of 64 columns run at half the rate of those of 128.
 //
-// Four warps bring an item's queries to their place, and four pass V on, cleaned
+// Four warps bring an item's queries to their place and write the rows of the item
+// before, while the softmax warps are on with the next; four pass V on, cleaned
 // where not every row sees every key: together for bf16 (most tiles need nothing),
 // for e4m3 a piece each, turned into f16 (exact) in a third ring: a piece is more
 // latency than work, so several go on at once.
@@ -42,7 +43,7 @@ struct AttnTcShape {
     static constexpr int kES = F8 ? 1 : 2;           // bytes of an element in memory
     static constexpr int kBoxB = D * kES < 128 ? D * kES : 128;  // bytes of a key in a box
     // K: pieces of kKBlks blocks of kBoxB bytes of a key
-    static constexpr int kKP = D == 256 && !F8 ? 2 : 1;
+    static constexpr int kKP = D == 256 ? 2 : 1;
     static constexpr int kKBlks = D * kES / kKP / kBoxB;
     static constexpr int kAtom = 8 * kBoxB;          // 8 keys of a block
     static constexpr int kKPiece = kTK / 8 * kKBlks * kAtom;
@@ -61,10 +62,10 @@ struct AttnTcShape {
     static constexpr int kQ = kQSmem ? ROWS * D * 2 : 0;
     static constexpr int kNQ = kQSmem ? 1 : 2;       // query buffers
     static_assert(!(F8 && D == 256 && ROWS > 64), "blocks of 64 rows");
-    static constexpr int kNK = F8 ? (D == 64 ? 6 : (D == 128 ? 4 : 2)) : (D == 64 ? 4 : (D == 128 ? 3 : 2));
-    static constexpr int kNV = F8 ? (D == 64 ? 6 : (D == 128 ? 8 : 6))
+    static constexpr int kNK = F8 ? (D == 64 ? 6 : (D == 128 ? 4 : 3)) : (D == 64 ? 4 : (D == 128 ? 3 : 2));
+    static constexpr int kNV = F8 ? (D == 64 ? 6 : (D == 128 ? 6 : 4))
                                   : (D == 64 ? 4 : (D == 128 || ROWS == 64 ? 3 : 2));
-    static constexpr int kNF = !F8 ? 0 : 4;  // f16 pieces
+    static constexpr int kNF = !F8 ? 0 : (D == 64 ? 4 : (D == 128 ? 5 : 6));  // f16 pieces
     static constexpr int kThreads = 16 * 32;         // (warp 4 has no work)
     static constexpr int kOffK = kQ;
     static constexpr int kOffV = kOffK + kNK * kKPiece;
@@ -113,13 +114,16 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     __shared__ volatile int s_odd[8];  // seg + 1: the part's values lost infinities or NaN
     __shared__ AttnUnit s_unit[kUnitRing], s_vunit[kUnitRing];  // by the K and the V warp
     __shared__ AttnUnit s_part[8];     // first units of the parts
+    __shared__ AttnUnit s_end[2];      // a part's last unit (its start: the first unit's)
+    __shared__ int s_end_u[2], s_end_start[2];  // its number, its first key
+    __shared__ float2 s_ml[2][ROWS];   // maximum and sum of a part's rows
     __shared__ volatile int s_parts;   // how many parts, once it is known
     // A wait names a phase by its parity: when it begins, the phase before has to be over
     // and the one after not.  So products and scores have two barriers each, taken in
     // turn: S of tile u is committed after the product of tile u - 2.
     // Loaded pieces and their release; V pieces passed on (bf16) or as f16 and released.
     __shared__ __align__(8) uint64_t b_k[NK], b_ke[NK], b_v[NV], b_ve[NV], b_clean[8], b_fe[NF];
-    __shared__ __align__(8) uint64_t b_s[2], b_p[2], b_pv[2], b_q[2], b_qe[2], b_part[8], b_o, b_end;
+    __shared__ __align__(8) uint64_t b_s[2], b_p[2], b_pv[2], b_q[2], b_qe[2], b_part[8], b_ml[2], b_o, b_end;
     // log2 of the row scales of e4m3 queries, by part: those of part n + 4 are written
     // after the last scores of part n + 2, which wait for the softmax of part n
     __shared__ int8_t s_rs[F8 ? 4 : 1][F8 ? ROWS : 1];
@@ -146,6 +150,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             for (int k = 0; k < 2; ++k) {
                 mbar_init(&b_s[k], 1);
                 mbar_init(&b_pv[k], 1);
+                mbar_init(&b_ml[k], row_warps);
                 mbar_init(&b_p[k], row_warps);
                 mbar_init(&b_q[k], S::kQSmem ? 4 : row_warps);
                 mbar_init(&b_qe[k], 1);
@@ -297,6 +302,122 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         return true;
     };
 
+    // A part's rows from tensor memory to the output, or to its partial.
+    auto finish = [&](int part, int vw) {
+        const int r = vw * 32 + lane;  // row of the block = lane of tensor memory
+        const uint32_t tO = tmem + (static_cast<uint32_t>(vw * 32) << 16) + S::kColO;
+        if (!warp_wait(&b_ml[part & 1], part >> 1)) return false;
+        const AttnUnit td = s_end[part & 1];
+        const int u = s_end_u[part & 1], h = td.g / p.row_blocks;
+        const AttnRow row = attn_row(p, td.g, r);
+        const int pr = row.live ? td.p0 + row.i : -1;
+        const float2 ml = s_ml[part & 1][min(r, ROWS - 1)];
+        const float mm = ml.x, l = ml.y;
+        // S of tile u was committed after the product of tile u - 2 (see the barriers)
+        if (!warp_wait(&b_pv[u & 1], u >> 1)) return false;
+        tc_fence_after();
+        const int last_key = s_end_start[part & 1] + TK - 1;
+        const bool live = row.live, odd = s_odd[part & 7] == part + 1;
+        const float vs = F8 && p.v_scale ? __ldg(p.v_scale + h) : 1.f;
+        const float f = td.slot >= 0 ? 1.f : (l == 0.f ? 0.f : vs / l);
+        const long long orow = static_cast<long long>(td.b) * p.R + row.i;
+        // The rows leave through 4 KB of shared memory a warp, 128 bytes of each of
+        // the 32 rows at a time (fp32 partial: 32 columns, bf16: 64), so that eight
+        // lanes write one row's line.
+        const long long dst_row =
+            td.slot >= 0 ? (static_cast<long long>(td.slot) * ROWS * (D + 2) + static_cast<long long>(r) * D) * 4
+                         : (orow * p.ldo + static_cast<long long>(row.hq) * D) * 2;
+        uint8_t* dst_base = td.slot >= 0 ? reinterpret_cast<uint8_t*>(p.partial)
+                                         : reinterpret_cast<uint8_t*>(p.out);
+        // the rows that this lane writes, as offsets in 16 bytes (rows start on 16)
+        const uint32_t mine = live ? static_cast<uint32_t>(dst_row >> 4) : 0xffffffffu;
+        uint32_t to[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) to[k] = __shfl_sync(0xffffffffu, mine, k * 4 + (lane >> 3));
+        uint8_t* stage = smem + S::kOffStage + vw * 4096;
+        const int width = td.slot >= 0 ? 32 : 64;  // columns a line
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            uint32_t y[32];
+            __syncwarp();
+            tmem_ld32(y, tO + c);
+            if (odd && live) {
+                // infinities and NaN of values that this row sees and others do not
+                auto give = [&](int j0, int j1) {
+#pragma unroll 1
+                    for (int j = max(j0, td.start); j <= min(j1, last_key); ++j) {
+                        const int pg = p.table[static_cast<long long>(td.b) * p.table_stride +
+                                               (j >> p.page_shift)];
+                        if (pg < 0 || pg >= p.num_pages || !key_seen(j, pr, p.window, p.sinks))
+                            continue;
+                        const long long at = static_cast<long long>(pg) * p.page_stride +
+                                             static_cast<long long>(j & (p.page_size - 1)) *
+                                                 p.token_stride +
+                                             static_cast<long long>(h) * p.head_stride + c;
+                        // (loops: rare, and y keeps constant indexes)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            float vv;
+                            if (F8)
+                                vv = (static_cast<const uint8_t*>(p.v)[at + k] & 0x7F) == 0x7F ? NAN : 0.f;
+                            else
+                                vv = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v)[at + k]);
+                            if (!isfinite(vv))
+                                y[k] = __float_as_uint(__uint_as_float(y[k]) + vv);
+                        }
+                    }
+                };
+                // the ends of the rows' windows, then the verify rows themselves
+                if (p.window > 0)
+                    give(max(0, td.p0 - p.window + 1), min(td.p0, td.len - 1 - p.window));
+                give(max(0, td.p0 + 1), td.len - 1);
+            }
+            if (td.slot >= 0) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                        make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+            } else {
+                const int k0 = c & 32 ? 4 : 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = pack2<false>(__uint_as_float(y[8 * k + 2 * e]) * f,
+                                            __uint_as_float(y[8 * k + 2 * e + 1]) * f);
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + (((k0 + k) ^ (lane & 7)) << 4)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                if (k0 == 0) continue;  // the other half of the lines is to come
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int rr = k * 4 + (lane >> 3);
+                if (to[k] != 0xffffffffu)
+                    *reinterpret_cast<uint4*>(dst_base + (static_cast<long long>(to[k]) << 4) +
+                                              (c / width) * 128 + (lane & 7) * 16) =
+                        *reinterpret_cast<const uint4*>(stage + rr * 128 +
+                                                        (((lane & 7) ^ (rr & 7)) << 4));
+            }
+        }
+        __syncwarp();
+        tc_fence_before();
+        if (live) {
+            if (td.slot >= 0) {
+                float* po = p.partial + static_cast<long long>(td.slot) * ROWS * (D + 2);
+                po[ROWS * D + r] = mm;
+                po[ROWS * (D + 1) + r] = l;
+            } else if (p.lse) {
+                p.lse[orow * p.Hq + row.hq] = l == 0.f ? -INFINITY : (mm + log2f(l)) * kLn2;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_o);
+        return true;
+    };
+
     if (n_units > 0 && (warp == kTcLoadK || warp == kTcLoadV)) {
         // -------------------------------------------------------- producers
         const bool keys = warp == kTcLoadK;
@@ -351,11 +472,17 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             for (int k = n > ring ? n - ring : 0; k < n; ++k)
                 mbar_wait_bounded(&full[k % ring], (k / ring) & 1, p.wait_ns, nullptr);
     } else if (n_units > 0 && warp >= kTcQ && warp < kTcPass) {
-        // --------------------------------------------------------- queries
+        // ------------------------------------------- queries in, finished rows out
+        const int vw = warp - kTcQ;
         for (int k = 0;; ++k) {
-            if (!warp_wait(&b_part[k & 7], k >> 3) || k >= s_parts) break;
-            const AttnUnit d = s_part[k & 7];
-            if (!queries(d, warp - kTcQ)) break;
+            if (!warp_wait(&b_part[k & 7], k >> 3)) break;
+            const bool more = k < s_parts;
+            if (more) {
+                const AttnUnit d = s_part[k & 7];
+                if (!queries(d, vw)) break;
+            }
+            if (k > 0 && vw < row_warps && !finish(k - 1, vw)) break;
+            if (!more) break;
         }
     } else if (n_units > 0 && warp >= kTcPass) {
         // ---------------------------------------------------- V pieces passed on
@@ -674,108 +801,17 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             if (lane == 0) mbar_arrive(&b_p[u & 1]);
             if (!(td.flags & kUnitLast)) continue;
 
-            // ---- end of the segment
-            if (!warp_wait(&b_pv[u & 1], u >> 1)) break;
-            tc_fence_after();
-            const bool live = row.live, odd = s_odd[td.seg & 7] == td.seg + 1;
-            const float mm = m == -INFINITY ? -INFINITY : mc;
-            const float vs = F8 && p.v_scale ? __ldg(p.v_scale + h) : 1.f;
-            const float f = td.slot >= 0 ? 1.f : (l == 0.f ? 0.f : vs / l);
-            const long long orow = static_cast<long long>(td.b) * p.R + row.i;
-            // The rows leave through 4 KB of shared memory a warp, 128 bytes of each of
-            // the 32 rows at a time (fp32 partial: 32 columns, bf16: 64), so that eight
-            // lanes write one row's line.
-            const long long dst_row =
-                td.slot >= 0 ? (static_cast<long long>(td.slot) * ROWS * (D + 2) + static_cast<long long>(r) * D) * 4
-                             : (orow * p.ldo + static_cast<long long>(row.hq) * D) * 2;
-            uint8_t* dst_base = td.slot >= 0 ? reinterpret_cast<uint8_t*>(p.partial)
-                                             : reinterpret_cast<uint8_t*>(p.out);
-            // the rows that this lane writes, as offsets in 16 bytes (rows start on 16)
-            const uint32_t mine = live ? static_cast<uint32_t>(dst_row >> 4) : 0xffffffffu;
-            uint32_t to[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) to[k] = __shfl_sync(0xffffffffu, mine, k * 4 + (lane >> 3));
-            uint8_t* stage = smem + S::kOffStage + warp * 4096;
-            const int width = td.slot >= 0 ? 32 : 64;  // columns a line
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t y[32];
-                __syncwarp();
-                tmem_ld32(y, tO + c);
-                if (odd && live) {
-                    // infinities and NaN of values that this row sees and others do not
-                    auto give = [&](int j0, int j1) {
-#pragma unroll 1
-                        for (int j = max(j0, seg_start); j <= min(j1, td.start + TK - 1); ++j) {
-                            const int pg = p.table[static_cast<long long>(td.b) * p.table_stride +
-                                                   (j >> p.page_shift)];
-                            if (pg < 0 || pg >= p.num_pages || !key_seen(j, pr, p.window, p.sinks))
-                                continue;
-                            const long long at = static_cast<long long>(pg) * p.page_stride +
-                                                 static_cast<long long>(j & (p.page_size - 1)) *
-                                                     p.token_stride +
-                                                 static_cast<long long>(h) * p.head_stride + c;
-                            // (loops: rare, and y keeps constant indexes)
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                float vv;
-                                if (F8)
-                                    vv = (static_cast<const uint8_t*>(p.v)[at + k] & 0x7F) == 0x7F ? NAN : 0.f;
-                                else
-                                    vv = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v)[at + k]);
-                                if (!isfinite(vv))
-                                    y[k] = __float_as_uint(__uint_as_float(y[k]) + vv);
-                            }
-                        }
-                    };
-                    // the ends of the rows' windows, then the verify rows themselves
-                    if (p.window > 0)
-                        give(max(0, td.p0 - p.window + 1), min(td.p0, td.len - 1 - p.window));
-                    give(max(0, td.p0 + 1), td.len - 1);
-                }
-                if (td.slot >= 0) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-                            make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-                } else {
-                    const int k0 = c & 32 ? 4 : 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack2<false>(__uint_as_float(y[8 * k + 2 * e]) * f,
-                                                __uint_as_float(y[8 * k + 2 * e + 1]) * f);
-                        *reinterpret_cast<uint4*>(stage + lane * 128 + (((k0 + k) ^ (lane & 7)) << 4)) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                    if (k0 == 0) continue;  // the other half of the lines is to come
-                }
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int rr = k * 4 + (lane >> 3);
-                    if (to[k] != 0xffffffffu)
-                        *reinterpret_cast<uint4*>(dst_base + (static_cast<long long>(to[k]) << 4) +
-                                                  (c / width) * 128 + (lane & 7) * 16) =
-                            *reinterpret_cast<const uint4*>(stage + rr * 128 +
-                                                            (((lane & 7) ^ (rr & 7)) << 4));
-                }
+            // ---- end of the part: its rows are written by the query warps
+            if (r < ROWS) s_ml[td.seg & 1][r] = make_float2(m == -INFINITY ? -INFINITY : mc, l);
+            if (tid == 0) {
+                AttnUnit d = td;
+                d.start = seg_start;
+                s_end[td.seg & 1] = d;
+                s_end_u[td.seg & 1] = u;
+                s_end_start[td.seg & 1] = td.start;
             }
             __syncwarp();
-            tc_fence_before();
-            if (live) {
-                if (td.slot >= 0) {
-                    float* po = p.partial + static_cast<long long>(td.slot) * ROWS * (D + 2);
-                    po[ROWS * D + r] = mm;
-                    po[ROWS * (D + 1) + r] = l;
-                } else if (p.lse) {
-                    p.lse[orow * p.Hq + row.hq] = l == 0.f ? -INFINITY : (mm + log2f(l)) * kLn2;
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&b_o);
+            if (lane == 0) mbar_arrive(&b_ml[td.seg & 1]);
         }
     }
     tc_fence_before();
