@@ -605,6 +605,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             constexpr uint32_t iO = tc_idesc(!F8, 128, D, true);    // bf16, or f16
             int fl[2] = {0, 0}, parts = 0;
             int qk = 0, kp = 0, pv = 0, vp = 0;  // next tile and piece of either product
+            bool p_in = false;  // P of tile pv is there, and O free for it
             uint64_t t0 = 0;
             while (pv < n_units) {
                 // S of tile qk takes the buffer of tile qk - 2, whose P has been read
@@ -650,11 +651,13 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                     }
                 }
                 if (pv < qk) {
-                    const int pc = pv * VP + vp;
                     const bool first = fl[pv & 1] & kUnitFirst;
-                    if (mbar_test(&b_clean[pc & 7], (pc >> 3) & 1) &&
-                        (vp > 0 || (mbar_test(&b_p[pv & 1], (pv >> 1) & 1) &&
-                                    (!first || parts == 0 || mbar_test(&b_o, (parts - 1) & 1))))) {
+                    p_in = p_in || (mbar_test(&b_p[pv & 1], (pv >> 1) & 1) &&
+                                    (!first || parts == 0 || mbar_test(&b_o, (parts - 1) & 1)));
+                    bool went = false;
+                    while (p_in && vp < VP) {
+                        const int pc = pv * VP + vp;
+                        if (!mbar_test(&b_clean[pc & 7], (pc >> 3) & 1)) break;
                         tc_fence_after();
                         const uint32_t v = sm + (F8 ? S::kOffF + pc % NF * S::kVPiece
                                                     : S::kOffV + pc % NV * S::kVLoad);
@@ -665,15 +668,19 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                                              F8 ? tc_desc<128>(v + ks * 2048, S::kVBlk, 1024)
                                                 : tc_desc<128>(v + ks * (2 * S::kVBlks * S::kAtom), S::kAtom,
                                                                S::kVBlks * S::kAtom),
-                                             iO,
-                                             !(first && vp == 0 && ks == 0));
+                                             iO, !(first && vp == 0 && ks == 0));
                         tc_commit(F8 ? &b_fe[pc % NF] : &b_ve[pc % NV]);
-                        if (++vp == VP) {
-                            tc_commit(&b_pv[pv & 1]);
-                            parts += first;
-                            vp = 0;
-                            ++pv;
-                        }
+                        ++vp;
+                        went = true;
+                    }
+                    if (vp == VP) {
+                        tc_commit(&b_pv[pv & 1]);
+                        parts += first;
+                        vp = 0;
+                        p_in = false;
+                        ++pv;
+                    }
+                    if (went) {
                         t0 = 0;
                         continue;
                     }
