@@ -21,24 +21,61 @@ constexpr int kLogitChunk = 4096;               // vocabulary entries of a block
 constexpr uint32_t kKnown = 0x80000000u;        // count word: in the prompt
 constexpr uint32_t kLogitBadDraft = 0x1u;
 
-// VEC consecutive logits a thread and step
+// VEC consecutive logits a thread and step.  A row's logits are on their way while
+// the history is scanned, or while the row before is finished; its mask words a row
+// earlier still, for they decide which logits are read.
 template <int VEC>
-__global__ void __launch_bounds__(kLogitThreads) logits_kernel(const LogitsParams p, int row_step) {
+__global__ void __launch_bounds__(kLogitThreads, 5) logits_kernel(const LogitsParams p, int row_step) {
     constexpr int N = kLogitChunk / (kLogitThreads * VEC);  // steps of a row
-    __shared__ uint32_t s_cnt[kLogitChunk];
-    __shared__ int s_bias[kLogitChunk];                     // bias entry + 1 (0: none)
+    __shared__ __align__(16) uint32_t s_cnt[kLogitChunk];
+    __shared__ __align__(16) uint32_t s_bias[kLogitChunk];  // bias entry + 1 (0: none)
     __shared__ uint32_t s_hit[kLogitChunk / 32];            // entries with a count or a bias
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, b = blockIdx.y;
     const int c0 = blockIdx.x * kLogitChunk;
     const int row0 = blockIdx.z * row_step, row1 = min(p.R, row0 + row_step);
-    for (int k = tid; k < kLogitChunk; k += kLogitThreads) {
-        s_cnt[k] = 0u;
-        s_bias[k] = 0;
+    for (int k = tid; k < kLogitChunk / 4; k += kLogitThreads) {
+        reinterpret_cast<uint4*>(s_cnt)[k] = make_uint4(0, 0, 0, 0);
+        if (p.bias_ids) reinterpret_cast<uint4*>(s_bias)[k] = make_uint4(0, 0, 0, 0);
     }
     for (int k = tid; k < kLogitChunk / 32; k += kLogitThreads) s_hit[k] = 0u;
-    __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    constexpr uint32_t kFull = VEC == 4 ? 0xfu : 1u;
+    auto place = [&](int k) { return c0 + (k * kLogitThreads + tid) * VEC; };
+    // mask words of a row (all ones without a mask)
+    uint32_t words[N];
+    auto masks = [&](int i) {
+        const long long row = static_cast<long long>(b) * p.R + i;
+        const uint32_t* mk = nullptr;
+        if (p.mask) {
+            const long long mr = p.mask_index ? p.mask_index[row] : row;
+            if (mr >= 0 && mr < p.mask_rows) mk = p.mask + mr * p.mask_stride;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            words[k] = mk && place(k) < p.V ? __ldg(mk + (place(k) >> 5)) : ~0u;
+    };
+    // a row's allowed logits (the masked ones are not read); step k's bits of `allow`
+    float x[N][VEC];
+    uint32_t allow = 0;
+    auto fetch = [&](int i) {
+        const float* src = p.x + (static_cast<long long>(b) * p.R + i) * p.ldx;
+        allow = 0;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int v = place(k);
+            const uint32_t a = v < p.V ? (words[k] >> (v & 31)) & kFull : 0u;
+            allow |= a << (k * VEC);
+            if (a) {
+                if (VEC == 4) *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(src + v);
+                else x[k][0] = src[v];
+            }
+        }
+    };
+    masks(row0);
+    fetch(row0);
+    __syncthreads();  // the tables are clear
 
     auto hit = [&](int at) { atomicOr(&s_hit[at >> 5], 1u << (at & 31)); };
     const bool flagger = blockIdx.x == 0 && blockIdx.z == 0;
@@ -47,24 +84,38 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(const LogitsParam
         const int n = p.hist_len ? max(0, min(p.hist_max, p.hist_len[b])) : p.hist_max;
         const int np = p.prompt_len ? p.prompt_len[b] : 0;
         const int32_t* ids = p.history + static_cast<long long>(b) * p.hist_stride;
-#pragma unroll 4
-        for (int t = tid; t < n; t += kLogitThreads) {
-            const int v = __ldg(ids + t), at = v - c0;
-            if (v >= c0 && v < p.V && at < kLogitChunk) {
+        auto count = [&](int t, int v) {
+            const int at = v - c0;
+            if (v >= c0 && at < kLogitChunk && v < p.V) {
                 if (t < np) atomicOr(&s_cnt[at], kKnown);
                 else atomicAdd(&s_cnt[at], 1u);
                 hit(at);
             }
             bad |= v < 0 || v >= p.V;
+        };
+        // four ids a load from the first whole 16 bytes on
+        const int head = min(n, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(ids) & 15u)) & 15u) / 4);
+        if (tid < head) count(tid, __ldg(ids + tid));
+        const int quads = (n - head) / 4;
+#pragma unroll 2
+        for (int q = tid; q < quads; q += kLogitThreads) {
+            const int t = head + 4 * q;
+            const int4 v = __ldg(reinterpret_cast<const int4*>(ids + t));
+            count(t, v.x);
+            count(t + 1, v.y);
+            count(t + 2, v.z);
+            count(t + 3, v.w);
         }
+        const int t = head + 4 * quads + tid;
+        if (t < n) count(t, __ldg(ids + t));
     }
     if (p.bias_ids) {
         const int n = p.bias_len ? max(0, min(p.bias_max, p.bias_len[b])) : p.bias_max;
         const int32_t* ids = p.bias_ids + static_cast<long long>(b) * p.bias_stride;
         for (int t = tid; t < n; t += kLogitThreads) {
             const int v = __ldg(ids + t), at = v - c0;
-            if (v >= c0 && v < p.V && at < kLogitChunk) {
-                atomicMax(&s_bias[at], t + 1);  // of repeated ids the last entry holds
+            if (v >= c0 && at < kLogitChunk && v < p.V) {
+                atomicMax(&s_bias[at], static_cast<uint32_t>(t) + 1u);  // the last entry holds
                 hit(at);
             }
             bad |= v < 0 || v >= p.V;
@@ -83,60 +134,36 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(const LogitsParam
         const int v = p.drafts[static_cast<long long>(b) * (p.R - 1) + tid];
         if (v < 0 || v >= p.V) atomicOr(p.status, kLogitBadDraft);
     }
-
     const float rep = p.repetition ? __ldg(p.repetition + b) : 1.f;
     const float pre = p.presence ? __ldg(p.presence + b) : 0.f;
     const float fre = p.frequency ? __ldg(p.frequency + b) : 0.f;
     const float* bias = p.bias_ids ? p.bias_vals + static_cast<long long>(b) * p.bias_stride : nullptr;
 
-    float x[N][VEC];
-    uint32_t allow[N];  // VEC bits a step
-    auto fetch = [&](int i) {
-        const long long row = static_cast<long long>(b) * p.R + i;
-        const uint32_t* mk = nullptr;
-        if (p.mask) {
-            const long long mr = p.mask_index ? p.mask_index[row] : row;
-            if (mr >= 0 && mr < p.mask_rows) mk = p.mask + mr * p.mask_stride;
-        }
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int v = c0 + (k * kLogitThreads + tid) * VEC;
-            constexpr uint32_t full = (1u << VEC) - 1u;
-            allow[k] = v >= p.V ? 0u : (mk ? (__ldg(mk + (v >> 5)) >> (v & 31)) & full : full);
-        }
-        const float* src = p.x + row * p.ldx;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int v = c0 + (k * kLogitThreads + tid) * VEC;
-            if (allow[k]) {  // masked logits are not read
-                if (VEC == 4) *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(src + v);
-                else x[k][0] = src[v];
-            }
-        }
-    };
-
     for (int i = row0; i < row1; ++i) {
-        fetch(i);
         __syncthreads();  // the counts of this row are complete
+        if (i + 1 < row1) masks(i + 1);
         const long long row = static_cast<long long>(b) * p.R + i;
         float* dst = p.out + row * p.ldo;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const int at = (k * kLogitThreads + tid) * VEC, v = c0 + at;
-            uint32_t hits = (s_hit[at >> 5] >> (at & 31)) & allow[k];
+            const int v = place(k), at = v - c0;
+            const uint32_t a = (allow >> (k * VEC)) & kFull;
+            const uint32_t hits = (s_hit[at >> 5] >> (at & 31)) & a;
             float mx = -INFINITY;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 float y = -INFINITY;
-                if ((allow[k] >> e) & 1u) {
+                if ((a >> e) & 1u) {
                     y = x[k][e];
                     if ((hits >> e) & 1u) {
                         const uint32_t c = s_cnt[at + e];
-                        const int be = s_bias[at + e];
                         if (c) y = y > 0.f ? __fdiv_rn(y, rep) : y * rep;
                         const float n = static_cast<float>(c & ~kKnown);
                         if (n > 0.f) y = y - fre * n - pre;
-                        if (be) y += __ldg(bias + be - 1);
+                        if (bias) {
+                            const uint32_t be = s_bias[at + e];
+                            if (be) y += __ldg(bias + be - 1);
+                        }
                     }
                 }
                 x[k][e] = y;
@@ -155,6 +182,7 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(const LogitsParam
             }
         }
         if (i + 1 < row1) {
+            fetch(i + 1);
             __syncthreads();  // every thread has read the counts of row i
             if (tid == 0) add_draft(i);
         }
