@@ -9,9 +9,10 @@
 //
 // One pass over the logits: a block owns a chunk of the vocabulary of one
 // sequence and keeps its counts in shared memory, so the rows of a verify
-// batch share one scan of the token history, and row i + 1 adds one draft to
-// the counts of row i.  The bytes bound it (8 a logit); the scan re-reads the
-// history once per chunk, from L2.
+// batch share one scan of the token history; the few drafts before a row are
+// compared only where an entry is marked.  So the rows need no barrier between
+// them.  The bytes bound it (8 a logit); the scan re-reads the history once per
+// chunk, from L2.
 #include "attn.cuh"
 
 namespace vw4 {
@@ -25,11 +26,12 @@ constexpr uint32_t kLogitBadDraft = 0x1u;
 // the history is scanned, or while the row before is finished; its mask words a row
 // earlier still, for they decide which logits are read.
 template <int VEC>
-__global__ void __launch_bounds__(kLogitThreads, 5) logits_kernel(const LogitsParams p, int row_step) {
+__global__ void __launch_bounds__(kLogitThreads, VEC == 4 ? 4 : 3) logits_kernel(const LogitsParams p, int row_step) {
     constexpr int N = kLogitChunk / (kLogitThreads * VEC);  // steps of a row
     __shared__ __align__(16) uint32_t s_cnt[kLogitChunk];
     __shared__ __align__(16) uint32_t s_bias[kLogitChunk];  // bias entry + 1 (0: none)
-    __shared__ uint32_t s_hit[kLogitChunk / 32];            // entries with a count or a bias
+    __shared__ uint32_t s_hit[kLogitChunk / 32];            // entries with a count, a draft or a bias
+    __shared__ int s_draft[kMaxVerifyRows];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, b = blockIdx.y;
     const int c0 = blockIdx.x * kLogitChunk;
@@ -122,25 +124,19 @@ __global__ void __launch_bounds__(kLogitThreads, 5) logits_kernel(const LogitsPa
         }
     }
     if (flagger && bad) atomicOr(p.status, kStatusBadListId);
-    auto add_draft = [&](int i) {
-        const int v = p.drafts[static_cast<long long>(b) * (p.R - 1) + i];
-        if (v >= c0 && v < p.V && v - c0 < kLogitChunk) {
-            atomicAdd(&s_cnt[v - c0], 1u);
-            hit(v - c0);
-        }
-    };
-    if (tid < row0) add_draft(tid);  // the drafts before this block's first row
-    if (flagger && tid < p.R - 1) {
+    if (tid < p.R - 1) {
         const int v = p.drafts[static_cast<long long>(b) * (p.R - 1) + tid];
-        if (v < 0 || v >= p.V) atomicOr(p.status, kLogitBadDraft);
+        s_draft[tid] = v;
+        if (v >= c0 && v < p.V && v - c0 < kLogitChunk) hit(v - c0);
+        if (flagger && (v < 0 || v >= p.V)) atomicOr(p.status, kLogitBadDraft);
     }
     const float rep = p.repetition ? __ldg(p.repetition + b) : 1.f;
     const float pre = p.presence ? __ldg(p.presence + b) : 0.f;
     const float fre = p.frequency ? __ldg(p.frequency + b) : 0.f;
     const float* bias = p.bias_ids ? p.bias_vals + static_cast<long long>(b) * p.bias_stride : nullptr;
 
+    __syncthreads();  // the tables are complete
     for (int i = row0; i < row1; ++i) {
-        __syncthreads();  // the counts of this row are complete
         if (i + 1 < row1) masks(i + 1);
         const long long row = static_cast<long long>(b) * p.R + i;
         float* dst = p.out + row * p.ldo;
@@ -156,7 +152,9 @@ __global__ void __launch_bounds__(kLogitThreads, 5) logits_kernel(const LogitsPa
                 if ((a >> e) & 1u) {
                     y = x[k][e];
                     if ((hits >> e) & 1u) {
-                        const uint32_t c = s_cnt[at + e];
+                        uint32_t c = s_cnt[at + e];
+#pragma unroll 1
+                        for (int j = 0; j < i; ++j) c += s_draft[j] == v + e ? 1u : 0u;
                         if (c) y = y > 0.f ? __fdiv_rn(y, rep) : y * rep;
                         const float n = static_cast<float>(c & ~kKnown);
                         if (n > 0.f) y = y - fre * n - pre;
@@ -181,11 +179,7 @@ __global__ void __launch_bounds__(kLogitThreads, 5) logits_kernel(const LogitsPa
                     p.bmax[row * ((p.V + 15) / 16) + (v >> 4)] = mx;
             }
         }
-        if (i + 1 < row1) {
-            fetch(i + 1);
-            __syncthreads();  // every thread has read the counts of row i
-            if (tid == 0) add_draft(i);
-        }
+        if (i + 1 < row1) fetch(i + 1);
     }
 }
 
