@@ -43,6 +43,23 @@ __global__ void __launch_bounds__(kLogitThreads, VEC == 4 ? 4 : 3) logits_kernel
     for (int k = tid; k < kLogitChunk / 32; k += kLogitThreads) s_hit[k] = 0u;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
+    // everything small that is needed later, asked for at once: a short call is a chain
+    // of load latencies
+    const int n_hist = p.history ? (p.hist_len ? max(0, min(p.hist_max, __ldg(p.hist_len + b))) : p.hist_max) : 0;
+    const int n_prompt = p.prompt_len ? __ldg(p.prompt_len + b) : 0;
+    const int n_bias = p.bias_ids ? (p.bias_len ? max(0, min(p.bias_max, __ldg(p.bias_len + b))) : p.bias_max) : 0;
+    const int draft = tid < p.R - 1 ? __ldg(p.drafts + static_cast<long long>(b) * (p.R - 1) + tid) : -1;
+    const float rep = p.repetition ? __ldg(p.repetition + b) : 1.f;
+    const float pre = p.presence ? __ldg(p.presence + b) : 0.f;
+    const float fre = p.frequency ? __ldg(p.frequency + b) : 0.f;
+    const int32_t* bias_ids = p.bias_ids ? p.bias_ids + static_cast<long long>(b) * p.bias_stride : nullptr;
+    const int bias_id = tid < p.bias_max ? __ldg(bias_ids + tid) : -1;
+    // the first ids of the history, whether or not its length reaches them
+    const int32_t* ids = p.history ? p.history + static_cast<long long>(b) * p.hist_stride : nullptr;
+    const int head = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(ids) & 15u)) & 15u) / 4;
+    const int4 id4 = head + 4 * tid + 3 < p.hist_max
+                         ? __ldg(reinterpret_cast<const int4*>(ids + head) + tid)
+                         : make_int4(-1, -1, -1, -1);
     constexpr uint32_t kFull = VEC == 4 ? 0xfu : 1u;
     auto place = [&](int k) { return c0 + (k * kLogitThreads + tid) * VEC; };
     // mask words of a row (all ones without a mask)
@@ -82,57 +99,45 @@ __global__ void __launch_bounds__(kLogitThreads, VEC == 4 ? 4 : 3) logits_kernel
     auto hit = [&](int at) { atomicOr(&s_hit[at >> 5], 1u << (at & 31)); };
     const bool flagger = blockIdx.x == 0 && blockIdx.z == 0;
     bool bad = false;
-    if (p.history) {
-        const int n = p.hist_len ? max(0, min(p.hist_max, p.hist_len[b])) : p.hist_max;
-        const int np = p.prompt_len ? p.prompt_len[b] : 0;
-        const int32_t* ids = p.history + static_cast<long long>(b) * p.hist_stride;
-        auto count = [&](int t, int v) {
-            const int at = v - c0;
-            if (v >= c0 && at < kLogitChunk && v < p.V) {
-                if (t < np) atomicOr(&s_cnt[at], kKnown);
-                else atomicAdd(&s_cnt[at], 1u);
-                hit(at);
-            }
-            bad |= v < 0 || v >= p.V;
-        };
-        // four ids a load from the first whole 16 bytes on
-        const int head = min(n, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(ids) & 15u)) & 15u) / 4);
-        if (tid < head) count(tid, __ldg(ids + tid));
-        const int quads = (n - head) / 4;
-#pragma unroll 2
-        for (int q = tid; q < quads; q += kLogitThreads) {
-            const int t = head + 4 * q;
-            const int4 v = __ldg(reinterpret_cast<const int4*>(ids + t));
-            count(t, v.x);
-            count(t + 1, v.y);
-            count(t + 2, v.z);
-            count(t + 3, v.w);
+    auto count = [&](int t, int v) {
+        const int at = v - c0;
+        if (v >= c0 && at < kLogitChunk && v < p.V) {
+            if (t < n_prompt) atomicOr(&s_cnt[at], kKnown);
+            else atomicAdd(&s_cnt[at], 1u);
+            hit(at);
         }
-        const int t = head + 4 * quads + tid;
-        if (t < n) count(t, __ldg(ids + t));
+        bad |= v < 0 || v >= p.V;
+    };
+    // four ids a load from the first whole 16 bytes on
+    if (tid < min(head, n_hist)) count(tid, __ldg(ids + tid));
+    const int quads = max(0, n_hist - head) / 4;
+    int4 v4 = id4;
+#pragma unroll 1
+    for (int q = tid; q < quads; q += kLogitThreads) {
+        const int t = head + 4 * q;
+        int4 next = v4;
+        if (q + kLogitThreads < quads) next = __ldg(reinterpret_cast<const int4*>(ids + head) + q + kLogitThreads);
+        count(t, v4.x);
+        count(t + 1, v4.y);
+        count(t + 2, v4.z);
+        count(t + 3, v4.w);
+        v4 = next;
     }
-    if (p.bias_ids) {
-        const int n = p.bias_len ? max(0, min(p.bias_max, p.bias_len[b])) : p.bias_max;
-        const int32_t* ids = p.bias_ids + static_cast<long long>(b) * p.bias_stride;
-        for (int t = tid; t < n; t += kLogitThreads) {
-            const int v = __ldg(ids + t), at = v - c0;
-            if (v >= c0 && at < kLogitChunk && v < p.V) {
-                atomicMax(&s_bias[at], static_cast<uint32_t>(t) + 1u);  // the last entry holds
-                hit(at);
-            }
-            bad |= v < 0 || v >= p.V;
+    if (head + 4 * quads + tid < n_hist) count(head + 4 * quads + tid, __ldg(ids + head + 4 * quads + tid));
+    for (int t = tid; t < n_bias; t += kLogitThreads) {
+        const int v = t == tid ? bias_id : __ldg(bias_ids + t), at = v - c0;
+        if (v >= c0 && at < kLogitChunk && v < p.V) {
+            atomicMax(&s_bias[at], static_cast<uint32_t>(t) + 1u);  // the last entry holds
+            hit(at);
         }
+        bad |= v < 0 || v >= p.V;
     }
     if (flagger && bad) atomicOr(p.status, kStatusBadListId);
     if (tid < p.R - 1) {
-        const int v = p.drafts[static_cast<long long>(b) * (p.R - 1) + tid];
-        s_draft[tid] = v;
-        if (v >= c0 && v < p.V && v - c0 < kLogitChunk) hit(v - c0);
-        if (flagger && (v < 0 || v >= p.V)) atomicOr(p.status, kLogitBadDraft);
+        s_draft[tid] = draft;
+        if (draft >= c0 && draft < p.V && draft - c0 < kLogitChunk) hit(draft - c0);
+        if (flagger && (draft < 0 || draft >= p.V)) atomicOr(p.status, kLogitBadDraft);
     }
-    const float rep = p.repetition ? __ldg(p.repetition + b) : 1.f;
-    const float pre = p.presence ? __ldg(p.presence + b) : 0.f;
-    const float fre = p.frequency ? __ldg(p.frequency + b) : 0.f;
     const float* bias = p.bias_ids ? p.bias_vals + static_cast<long long>(b) * p.bias_stride : nullptr;
 
     __syncthreads();  // the tables are complete
