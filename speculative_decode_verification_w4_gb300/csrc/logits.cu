@@ -20,6 +20,7 @@ namespace vw4 {
 constexpr int kLogitThreads = 256;
 constexpr int kLogitChunk = 4096;               // vocabulary entries of a block
 constexpr uint32_t kKnown = 0x80000000u;        // count word: in the prompt
+constexpr uint32_t kDrafted = 0x40000000u;      // count word: a draft of the sequence
 constexpr uint32_t kLogitBadDraft = 0x1u;
 
 // VEC consecutive logits a thread and step.  A row's logits are on their way while
@@ -135,7 +136,10 @@ __global__ void __launch_bounds__(kLogitThreads, VEC == 4 ? 4 : 3) logits_kernel
     if (flagger && bad) atomicOr(p.status, kStatusBadListId);
     if (tid < p.R - 1) {
         s_draft[tid] = draft;
-        if (draft >= c0 && draft < p.V && draft - c0 < kLogitChunk) hit(draft - c0);
+        if (draft >= c0 && draft < p.V && draft - c0 < kLogitChunk) {
+            atomicOr(&s_cnt[draft - c0], kDrafted);
+            hit(draft - c0);
+        }
         if (flagger && (draft < 0 || draft >= p.V)) atomicOr(p.status, kLogitBadDraft);
     }
     const float* bias = p.bias_ids ? p.bias_vals + static_cast<long long>(b) * p.bias_stride : nullptr;
@@ -158,8 +162,11 @@ __global__ void __launch_bounds__(kLogitThreads, VEC == 4 ? 4 : 3) logits_kernel
                     y = x[k][e];
                     if ((hits >> e) & 1u) {
                         uint32_t c = s_cnt[at + e];
+                        if (c & kDrafted) {
+                            c &= ~kDrafted;
 #pragma unroll 1
-                        for (int j = 0; j < i; ++j) c += s_draft[j] == v + e ? 1u : 0u;
+                            for (int j = 0; j < i; ++j) c += s_draft[j] == v + e ? 1u : 0u;
+                        }
                         if (c) y = y > 0.f ? __fdiv_rn(y, rep) : y * rep;
                         const float n = static_cast<float>(c & ~kKnown);
                         if (n > 0.f) y = y - fre * n - pre;
