@@ -600,13 +600,14 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         }
     } else if (n_units > 0 && warp == kTcMma) {
         // ----------------------------------------------- the tensor cores
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t iS = tc_idesc(!F8, 128, TK, false);  // bf16, or e4m3
             constexpr uint32_t iO = tc_idesc(!F8, 128, D, true);    // bf16, or f16
             int fl[2] = {0, 0}, parts = 0;
             int qk = 0, kp = 0, pv = 0, vp = 0;  // next tile and piece of either product
             bool p_in = false;  // P of tile pv is there, and O free for it
             uint64_t t0 = 0;
+            uint32_t idle = 0;
             while (pv < n_units) {
                 // S of tile qk takes the buffer of tile qk - 2, whose P has been read
                 if (qk < n_units && qk <= pv + 1) {
@@ -685,8 +686,8 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                         continue;
                     }
                 }
+                if (++idle & 63) continue;
                 if (s_abort) break;
-                __nanosleep(20);
                 const uint64_t now = globaltimer_ns();
                 if (t0 == 0) t0 = now;
                 if (now - t0 > p.wait_ns) {
