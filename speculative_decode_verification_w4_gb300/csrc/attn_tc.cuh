@@ -603,6 +603,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         if (elect_one()) {
             constexpr uint32_t iS = tc_idesc(!F8, 128, TK, false);  // bf16, or e4m3
             constexpr uint32_t iO = tc_idesc(!F8, 128, D, true);    // bf16, or f16
+            const uint64_t qd0 = tc_desc<S::kBoxB>(sm, 16, 8 * S::kBoxB);
             int fl[2] = {0, 0}, parts = 0;
             int qk = 0, kp = 0, pv = 0, vp = 0;  // next tile and piece of either product
             bool p_in = false;  // P of tile pv is there, and O free for it
@@ -617,24 +618,23 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                         const int flags = d->flags, seg = d->seg, qs = seg % S::kNQ;
                         if (kp > 0 || !(flags & kUnitFirst) || mbar_test(&b_q[qs], (seg / S::kNQ) & 1)) {
                             tc_fence_after();
-                            const uint32_t k = sm + S::kOffK + st * S::kKPiece;
+                            const uint64_t kd0 = tc_desc<S::kBoxB>(sm + S::kOffK + st * S::kKPiece, 16,
+                                                                   S::kKBlks * S::kAtom);
                             const uint32_t dS = tmem + S::kColS + (qk & 1) * TK;
                             constexpr int KS = S::kKBlks * S::kSteps;  // k steps of the piece
 #pragma unroll
                             for (int t = 0; t < S::kTerms; ++t)
 #pragma unroll
                                 for (int ks = 0; ks < KS; ++ks) {
-                                    const uint64_t kd = tc_desc<S::kBoxB>(
-                                        k + (ks / S::kSteps) * S::kAtom + (ks % S::kSteps) * 32, 16,
-                                        S::kKBlks * S::kAtom);
+                                    const uint64_t kd =
+                                        kd0 + (((ks / S::kSteps) * S::kAtom + (ks % S::kSteps) * 32) >> 4);
                                     const int kq = t * (S::kQRow / 32) + kp * KS + ks;  // k step of Q
                                     const bool add = t > 0 || kp > 0 || ks > 0;
                                     if (S::kQSmem)
-                                        tc_mma_ss<F8>(dS,
-                                                      tc_desc<S::kBoxB>(sm + (kq / S::kSteps) * S::kQBlk +
-                                                                            (kq % S::kSteps) * 32,
-                                                                        16, 8 * S::kBoxB),
-                                                      kd, iS, add);
+                                        tc_mma_ss<F8>(
+                                            dS,
+                                            qd0 + (((kq / S::kSteps) * S::kQBlk + (kq % S::kSteps) * 32) >> 4),
+                                            kd, iS, add);
                                     else
                                         tc_mma_ts<F8>(dS, tmem + S::kColQ + qs * (D / 2) + kq * 8, kd, iS, add);
                                 }
@@ -660,16 +660,15 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                         const int pc = pv * VP + vp;
                         if (!mbar_test(&b_clean[pc & 7], (pc >> 3) & 1)) break;
                         tc_fence_after();
-                        const uint32_t v = sm + (F8 ? S::kOffF + pc % NF * S::kVPiece
-                                                    : S::kOffV + pc % NV * S::kVLoad);
+                        const uint64_t vd =
+                            F8 ? tc_desc<128>(sm + S::kOffF + pc % NF * S::kVPiece, S::kVBlk, 1024)
+                               : tc_desc<128>(sm + S::kOffV + pc % NV * S::kVLoad, S::kAtom,
+                                              S::kVBlks * S::kAtom);
 #pragma unroll
                         for (int ks = 0; ks < S::kVKeys / 16; ++ks)
                             tc_mma_ts<false>(tmem + S::kColO,
                                              tmem + S::kColS + (pv & 1) * TK + (vp * (S::kVKeys / 16) + ks) * 8,
-                                             F8 ? tc_desc<128>(v + ks * 2048, S::kVBlk, 1024)
-                                                : tc_desc<128>(v + ks * (2 * S::kVBlks * S::kAtom), S::kAtom,
-                                                               S::kVBlks * S::kAtom),
-                                             iO, !(first && vp == 0 && ks == 0));
+                                             vd + ((ks * (F8 ? 2048 : 2 * S::kVBlks * S::kAtom)) >> 4), iO, !(first && vp == 0 && ks == 0));
                         tc_commit(F8 ? &b_fe[pc % NF] : &b_ve[pc % NV]);
                         ++vp;
                         went = true;
