@@ -66,14 +66,16 @@ struct AttnTcShape {
     static constexpr int kNV = F8 ? (D == 64 ? 6 : (D == 128 ? 6 : 4))
                                   : (D == 64 ? 4 : (D == 128 || ROWS == 64 ? 3 : 2));
     static constexpr int kNF = !F8 ? 0 : (D == 64 ? 4 : (D == 128 ? 5 : 6));  // f16 pieces
-    static constexpr int kThreads = 16 * 32;         // (warp 4 has no work)
+    static constexpr int kThreads = 16 * 32;
+    static constexpr int kHalves = D == 64 && ROWS == 64 ? 2 : 1;  // threads of a softmax row
+    static constexpr int kLoadV = kHalves > 1 ? 2 : 5, kLoadK = kHalves > 1 ? 3 : 6;  // warps
     static constexpr int kOffK = kQ;
     static constexpr int kOffV = kOffK + kNK * kKPiece;
     static constexpr int kOffF = kOffV + kNV * kVLoad;
     static constexpr int kOffStage = kOffF + kNF * kVPiece;    // 4 KB a softmax warp, for the output
     static constexpr int kUsed = kOffStage + ROWS / 32 * 4096 + 1024;  // and alignment
     static constexpr int kSmem = kUsed < 115 * 1024 ? 115 * 1024 : kUsed;  // one CTA per SM
-    static_assert(kSmem + 3072 <= 227 * 1024, "shared memory");
+    static_assert(kSmem + 5632 <= 227 * 1024, "shared memory");
     // the products read 128 rows of Q whatever ROWS is: what follows must be there
     static_assert(!kQSmem || kOffStage >= (kTerms * kQRow / kBoxB - 1) * kQBlk + 128 * kBoxB, "Q reads");
     // tensor memory columns: O, two S, the queries (two 16-bit values a column)
@@ -95,18 +97,23 @@ struct AttnTcShape {
 
 constexpr float kLazy = 8.f;  // (log2) see above
 
-// Warps: 0 .. 3 softmax, 8 .. 11 queries, 12 .. 15 pass V on.  The loading warps (one each for K and V: a box
-// costs its warp some 60 ns, and a tile of 16-token pages has 32) and the one that
-// issues the products (it polls) share schedulers with the softmax warps that only
-// the largest blocks use.
-constexpr int kTcLoadV = 5, kTcLoadK = 6, kTcMma = 7, kTcQ = 8, kTcPass = 12;
+// Warps: 0 .. 3 softmax, 8 .. 11 queries, 12 .. 15 pass V on.  At head size 64 the softmax
+// of one row a thread is the longest step; blocks of 64 rows leave warps 2 and 3 without
+// rows, and warps 4 and 5, which reach the same lanes of tensor memory as 0 and 1, take
+// half of the columns there (e4m3, 32 sequences of 4000 .. 8000 tokens, 8 key heads, 32
+// rows each: 87 us instead of 98).  At 128 and 256 the products and V's conversion are as
+// long: 115 instead of 114 us, and 62 instead of 57 with a window of 1024.
+// The loading warps (one each for K and V: a box costs its warp some 60 ns, and a tile
+// of 16-token pages has 32) and the one that issues the products (it polls) share
+// schedulers with the softmax warps that only the largest blocks use.
+constexpr int kTcMma = 7, kTcQ = 8, kTcPass = 12;
 
 template <int D, bool F8, int ROWS>
 __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     attn_tc_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps) {
     using S = AttnTcShape<D, F8, ROWS>;
     constexpr int TK = S::kTK, NK = S::kNK, NV = S::kNV, NF = F8 ? S::kNF : 1;
-    constexpr int KP = S::kKP, VP = S::kVP;
+    constexpr int KP = S::kKP, VP = S::kVP, H = S::kHalves;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ uint32_t s_tmem;
@@ -116,7 +123,8 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     __shared__ AttnUnit s_part[8];     // first units of the parts
     __shared__ AttnUnit s_end[2];      // a part's last unit (its start: the first unit's)
     __shared__ int s_end_u[2], s_end_start[2];  // its number, its first key
-    __shared__ float2 s_ml[2][ROWS];   // maximum and sum of a part's rows
+    __shared__ float2 s_ml[2][H][ROWS];  // maximum and sum of a part's rows
+    __shared__ float s_mx[2][H][H > 1 ? ROWS : 1];  // of a tile's columns, for the other half
     __shared__ volatile int s_parts;   // how many parts, once it is known
     // A wait names a phase by its parity: when it begins, the phase before has to be over
     // and the one after not.  So products and scores have two barriers each, taken in
@@ -124,6 +132,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     // Loaded pieces and their release; V pieces passed on (bf16) or as f16 and released.
     __shared__ __align__(8) uint64_t b_k[NK], b_ke[NK], b_v[NV], b_ve[NV], b_clean[8], b_fe[NF];
     __shared__ __align__(8) uint64_t b_s[2], b_p[2], b_pv[2], b_q[2], b_qe[2], b_part[8], b_ml[2], b_o, b_end;
+    __shared__ __align__(8) uint64_t b_x[2][4];  // s_mx of a half's warp is there, S read
     // log2 of the row scales of e4m3 queries, by part: those of part n + 4 are written
     // after the last scores of part n + 2, which wait for the softmax of part n
     __shared__ int8_t s_rs[F8 ? 4 : 1][F8 ? ROWS : 1];
@@ -131,7 +140,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     const int row_warps = (p.tb * p.gb + 31) / 32;     // softmax warps with rows
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (tid == kTcLoadK * 32) {
+    if (tid == S::kLoadK * 32) {
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
     }
@@ -150,8 +159,9 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             for (int k = 0; k < 2; ++k) {
                 mbar_init(&b_s[k], 1);
                 mbar_init(&b_pv[k], 1);
-                mbar_init(&b_ml[k], row_warps);
-                mbar_init(&b_p[k], row_warps);
+                mbar_init(&b_ml[k], H * row_warps);
+                mbar_init(&b_p[k], H * row_warps);
+                for (int j = 0; j < 4; ++j) mbar_init(&b_x[k][j], 1);
                 mbar_init(&b_q[k], S::kQSmem ? 4 : row_warps);
                 mbar_init(&b_qe[k], 1);
             }
@@ -273,6 +283,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             if (reused && !warp_wait(&b_qe[qs], d.seg / S::kNQ - 1)) return false;
             tc_fence_after();
             const uint32_t tq = tmem + (static_cast<uint32_t>(vw * 32) << 16) + S::kColQ + qs * (D / 2);
+            __syncwarp();  // (rows that are not live took another way)
 #pragma unroll
             for (int c = 0; c < D / 8; c += 8) {  // 64 dimensions
                 uint32_t y[32];
@@ -311,7 +322,8 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         const int u = s_end_u[part & 1], h = td.g / p.row_blocks;
         const AttnRow row = attn_row(p, td.g, r);
         const int pr = row.live ? td.p0 + row.i : -1;
-        const float2 ml = s_ml[part & 1][min(r, ROWS - 1)];
+        float2 ml = s_ml[part & 1][0][min(r, ROWS - 1)];
+        if (H > 1) ml.y += s_ml[part & 1][H - 1][min(r, ROWS - 1)].y;
         const float mm = ml.x, l = ml.y;
         // S of tile u was committed after the product of tile u - 2 (see the barriers)
         if (!warp_wait(&b_pv[u & 1], u >> 1)) return false;
@@ -418,9 +430,9 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         return true;
     };
 
-    if (n_units > 0 && (warp == kTcLoadK || warp == kTcLoadV)) {
+    if (n_units > 0 && (warp == S::kLoadK || warp == S::kLoadV)) {
         // -------------------------------------------------------- producers
-        const bool keys = warp == kTcLoadK;
+        const bool keys = warp == S::kLoadK;
         constexpr int ESZ = S::kES, BOXB = S::kBoxB, KB = S::kKBlks, VB = S::kVBlks;
         uint64_t* full = keys ? b_k : b_v;
         uint64_t* empty = keys ? b_ke : b_ve;
@@ -700,10 +712,11 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             mbar_wait_bounded(&b_end, 0, p.wait_ns, nullptr);
         }
         __syncwarp();
-    } else if (n_units > 0 && warp < row_warps) {
+    } else if (n_units > 0 && warp < 4 * H && (warp & 3) < row_warps) {
         // ---------------------------------------------------------- softmax
-        const int r = tid;  // row of the block = lane of tensor memory
-        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+        const int half = warp >> 2, rw = warp & 3;
+        const int r = rw * 32 + lane;  // row of the block = lane of tensor memory
+        const uint32_t lanes = static_cast<uint32_t>(rw * 32) << 16;
         const uint32_t tO = tmem + lanes + S::kColO;
         float m = -INFINITY, l = 0.f, c2 = 1.f;
         int pr = -1, seg_start = 0;
@@ -727,36 +740,53 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 l = 0.f;
             }
             const uint32_t tS = tmem + lanes + S::kColS + (u & 1) * TK;
-            // The row is walked 32 columns at a time, twice, by rolled loops: the roles share
-            // the instruction caches, and unrolled over 128 columns this one alone
-            // overflowed them (a fifth of all warp stalls waited for instructions).
-            uint32_t x[32];
-            float mx = -INFINITY;
-            auto columns = [&](int c) {  // 32 columns of the row from column c
-                tmem_ld32(x, tS + c);
-                if (edge) {
-                    // seen: k <= hi and (k > lo or k < sk), as bits
-                    const int hi = pr - td.start - c;
-                    auto below = [](int n) {  // bits 0 .. n - 1
-                        return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
-                    };
-                    uint32_t seen = below(hi + 1);
-                    if (p.window > 0) seen &= ~below(hi - p.window + 1) | below(p.sinks - td.start - c);
+            // seen: k <= hi and (k > lo or k < sk), as bits of the 32 columns from column c
+            auto mask = [&](uint32_t* x, int c) {
+                const int hi = pr - td.start - c;
+                auto below = [](int n) {  // bits 0 .. n - 1
+                    return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
+                };
+                uint32_t seen = below(hi + 1);
+                if (p.window > 0) seen &= ~below(hi - p.window + 1) | below(p.sinks - td.start - c);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (!((seen >> k) & 1u)) x[k] = 0xff800000u;
+                for (int k = 0; k < 32; ++k)
+                    if (!((seen >> k) & 1u)) x[k] = 0xff800000u;
+            };
+            // A whole row is walked 32 columns at a time, twice, by rolled loops: the roles
+            // share the instruction caches, and unrolled over 128 columns this one alone
+            // overflowed them (a fifth of all warp stalls waited for instructions).  Half a
+            // row is read once: the other half writes P over its scores.
+            constexpr int CW = H > 1 ? TK / H : 32;
+            uint32_t x[CW];
+            float mx = -INFINITY;
+            auto columns = [&](int c) {
+                if constexpr (H > 1) tmem_ld64(x, tS + c);
+                else tmem_ld32(x, tS + c);
+                if (edge) {
+#pragma unroll
+                    for (int k = 0; k < CW; k += 32) mask(x + k, c + k);
                 }
             };
+            const int c0 = H > 1 ? half * CW : 0, c1 = H > 1 ? c0 + CW : TK;
 #pragma unroll 1
-            for (int c = 0; c < TK; c += 32) {
+            for (int c = c0; c < c1; c += CW) {
                 columns(c);
                 float m1 = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
+                for (int k = 0; k < CW; k += 2) {
                     mx = fmaxf(mx, __uint_as_float(x[k]));
                     m1 = fmaxf(m1, __uint_as_float(x[k + 1]));
                 }
                 mx = fmaxf(mx, m1);
+            }
+            if constexpr (H > 1) {
+                s_mx[u & 1][half][r] = mx;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b_x[u & 1][half * 2 + rw]);
+                if (!warp_wait(&b_x[u & 1][(half ^ 1) * 2 + rw], u >> 1)) break;
+                tc_fence_after();
+                mx = fmaxf(mx, s_mx[u & 1][half ^ 1][r]);
             }
             bool grow = false;
             float corr = 1.f;
@@ -775,7 +805,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 if (!warp_wait(&b_pv[(u - 1) & 1], (u - 1) >> 1)) break;
                 tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = half * (D / H); c < (half + 1) * (D / H); c += 32) {
                     uint32_t y[32];
                     tmem_ld32(y, tO + c);
 #pragma unroll
@@ -787,19 +817,20 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             const float mc = m == -INFINITY ? 0.f : m * c2;
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll 1
-            for (int c = 0; c < TK; c += 32) {
-                // (P's columns c / 2 .. + 15 hold scores that have been read)
-                columns(c);
-                uint32_t y[16];
+            for (int c = c0; c < c1; c += CW) {
+                // (P's columns c / 2 .. hold scores that have been read)
+                if (H == 1) columns(c);
+                uint32_t y[CW / 2];
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
+                for (int k = 0; k < CW; k += 2) {
                     const float a = ex2(fmaf(__uint_as_float(x[k]), c2, -mc));
                     const float b = ex2(fmaf(__uint_as_float(x[k + 1]), c2, -mc));
                     s0 += a;
                     s1 += b;
                     y[k / 2] = pack2<F8>(a, b);
                 }
-                tmem_st16(tS + c / 2, y);
+                if constexpr (H > 1) tmem_st32(tS + c / 2, y);
+                else tmem_st16(tS + c / 2, y);
             }
             l += s0 + s1;
             tmem_st_wait();
@@ -809,7 +840,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             if (!(td.flags & kUnitLast)) continue;
 
             // ---- end of the part: its rows are written by the query warps
-            if (r < ROWS) s_ml[td.seg & 1][r] = make_float2(m == -INFINITY ? -INFINITY : mc, l);
+            if (r < ROWS) s_ml[td.seg & 1][half][r] = make_float2(m == -INFINITY ? -INFINITY : mc, l);
             if (tid == 0) {
                 AttnUnit d = td;
                 d.start = seg_start;
