@@ -7,7 +7,8 @@ there is no fallback.  If the library is missing or cannot be loaded, every
 call raises.
 
 Entry points (same names as the C ABI):
-  verify_gemm_w4, verify_moe_w4, accept_greedy, accept_rejection,
+  verify_gemm_w4, verify_gemm_w4_blockmax, verify_greedy_w4, verify_moe_w4,
+  accept_greedy, accept_rejection, accept_rejection_blockmax,
   accept_rejection_topk, verify_rope_append, verify_attn, process_logits,
   vw4_workspace_bytes, vw4_get_device_status, vw4_q4_0_from_blocks,
   vw4_set_wait_limit_ns.

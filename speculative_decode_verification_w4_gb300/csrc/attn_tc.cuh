@@ -8,9 +8,10 @@
 // half of K's dimensions; of V 32, 64 or all 128 keys).  One thread
 // issues S = Q K^T and O += P V piece by piece, whichever has its operands first.
 // The softmax warps own one query row a thread, so the softmax has no shuffles,
-// and S and P never pass through shared memory.  S has two buffers: Q K^T of the
-// next tile runs under the softmax of this one; P overwrites the front of its S.
-// Q lies in tensor memory where O (D columns), two S (256) and two Q fit its 512
+// and S and P never pass through shared memory.  S has two buffers, three at head size
+// 64: Q K^T of the next tiles runs under the softmax of this one; P overwrites the
+// front of its S.
+// Q lies in tensor memory where O (D columns), the S (128 each) and two Q fit its 512
 // columns, else (head size 256) in shared memory: tiles of 64 keys would make
 // room, but the products of 64 columns run at half the rate of those of 128.
 //
@@ -27,6 +28,13 @@
 // the largest below.  For the weights two such terms would not do: a long tail of
 // small weights under one large one lies below their range.  So P is f16 and V
 // becomes f16; converting K as well was bound by that step.
+//
+// What bounds it.  bf16: the bytes (8 key heads of 128, 24 rows each, 32 sequences of
+// 4000 .. 8000 tokens: 130 us, 87 % of the copy rate).  e4m3 halves the bytes but not
+// the work: at head size 256 shared memory's bandwidth (K is read twice for the two
+// terms, V once raw, written and read as f16: about 1.5 us of a tile of 128 keys
+// against 1.4 for its bytes) and the chain of V's conversion; at 128 and 64 the chain
+// scores - softmax - P V over two score buffers, about 1 us a tile.
 //
 // The running maximum that the exponents use follows the true one lazily: O is
 // rescaled only when a row's maximum grew by more than 2^8 (its weights are then
@@ -79,8 +87,9 @@ struct AttnTcShape {
     // the products read 128 rows of Q whatever ROWS is: what follows must be there
     static_assert(!kQSmem || kOffStage >= (kTerms * kQRow / kBoxB - 1) * kQBlk + 128 * kBoxB, "Q reads");
     // tensor memory columns: O, two S, the queries (two 16-bit values a column)
-    static constexpr uint32_t kColO = 0, kColS = D, kColQ = D + 2 * kTK;
-    static_assert(D + 2 * kTK + (kQSmem ? 0 : kNQ * D / 2) <= 512, "tensor memory");
+    static constexpr int kNS = D == 64 ? 3 : 2;      // score buffers
+    static constexpr uint32_t kColO = 0, kColS = D, kColQ = D + kNS * kTK;
+    static_assert(D + kNS * kTK + (kQSmem ? 0 : kNQ * D / 2) <= 512, "tensor memory");
     // 16 bytes of a key of a V piece as it is loaded
     __device__ static __forceinline__ uint32_t v_at(int row, int chunk) {
         return static_cast<uint32_t>((row >> 3) * kVBlks * kAtom) +
@@ -113,7 +122,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     attn_tc_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps) {
     using S = AttnTcShape<D, F8, ROWS>;
     constexpr int TK = S::kTK, NK = S::kNK, NV = S::kNV, NF = F8 ? S::kNF : 1;
-    constexpr int KP = S::kKP, VP = S::kVP, H = S::kHalves;
+    constexpr int KP = S::kKP, VP = S::kVP, H = S::kHalves, NS = S::kNS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ uint32_t s_tmem;
@@ -127,15 +136,16 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     __shared__ float s_mx[2][H][H > 1 ? ROWS : 1];  // of a tile's columns, for the other half
     __shared__ volatile int s_parts;   // how many parts, once it is known
     // A wait names a phase by its parity: when it begins, the phase before has to be over
-    // and the one after not.  So products and scores have two barriers each, taken in
-    // turn: S of tile u is committed after the product of tile u - 2.
+    // and the one after not.  So products and scores have NS barriers each, taken in
+    // turn: S of tile u is committed after the product of tile u - NS.
     // Loaded pieces and their release; V pieces passed on (bf16) or as f16 and released.
     __shared__ __align__(8) uint64_t b_k[NK], b_ke[NK], b_v[NV], b_ve[NV], b_clean[8], b_fe[NF];
-    __shared__ __align__(8) uint64_t b_s[2], b_p[2], b_pv[2], b_q[2], b_qe[2], b_part[8], b_ml[2], b_o, b_end;
+    __shared__ __align__(8) uint64_t b_s[NS], b_p[NS], b_pv[NS], b_q[2], b_qe[2], b_part[8], b_ml[2];
+    __shared__ __align__(8) uint64_t b_o, b_end;
     __shared__ __align__(8) uint64_t b_x[2][4];  // s_mx of a half's warp is there, S read
-    // log2 of the row scales of e4m3 queries, by part: those of part n + 4 are written
-    // after the last scores of part n + 2, which wait for the softmax of part n
-    __shared__ int8_t s_rs[F8 ? 4 : 1][F8 ? ROWS : 1];
+    // log2 of the row scales of e4m3 queries, by part: those of part n + 8 are written
+    // after the last scores of part n + 6, which wait for the softmax of part n + 3
+    __shared__ int8_t s_rs[F8 ? 8 : 1][F8 ? ROWS : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row_warps = (p.tb * p.gb + 31) / 32;     // softmax warps with rows
 
@@ -156,11 +166,13 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 mbar_init(&b_ve[k], 1);
             }
             for (int k = 0; k < NF; ++k) mbar_init(&b_fe[k], 1);
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < NS; ++k) {
                 mbar_init(&b_s[k], 1);
                 mbar_init(&b_pv[k], 1);
-                mbar_init(&b_ml[k], H * row_warps);
                 mbar_init(&b_p[k], H * row_warps);
+            }
+            for (int k = 0; k < 2; ++k) {
+                mbar_init(&b_ml[k], H * row_warps);
                 for (int j = 0; j < 4; ++j) mbar_init(&b_x[k][j], 1);
                 mbar_init(&b_q[k], S::kQSmem ? 4 : row_warps);
                 mbar_init(&b_qe[k], 1);
@@ -201,7 +213,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         const int ex = static_cast<int>(largest >> 7);  // of the largest magnitude, bf16 bits
         int sh = ex == 0 || ex == 255 ? 0 : 127 + 7 - ex;  // to [2^7, 2^8)
         sh = max(-126, min(126, sh));
-        if (keep) s_rs[F8 ? d.seg & 3 : 0][F8 ? r : 0] = static_cast<int8_t>(sh);
+        if (keep) s_rs[F8 ? d.seg & 7 : 0][F8 ? r : 0] = static_cast<int8_t>(sh);
         return ex == 255 ? NAN : __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
     };
     auto largest_of = [](uint32_t mx, const uint4& v) {
@@ -325,8 +337,8 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         float2 ml = s_ml[part & 1][0][min(r, ROWS - 1)];
         if (H > 1) ml.y += s_ml[part & 1][H - 1][min(r, ROWS - 1)].y;
         const float mm = ml.x, l = ml.y;
-        // S of tile u was committed after the product of tile u - 2 (see the barriers)
-        if (!warp_wait(&b_pv[u & 1], u >> 1)) return false;
+        // S of tile u was committed after the product of tile u - NS (see the barriers)
+        if (!warp_wait(&b_pv[u % NS], u / NS)) return false;
         tc_fence_after();
         const int last_key = s_end_start[part & 1] + TK - 1;
         const bool live = row.live, odd = s_odd[part & 7] == part + 1;
@@ -616,14 +628,14 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             constexpr uint32_t iS = tc_idesc(!F8, 128, TK, false);  // bf16, or e4m3
             constexpr uint32_t iO = tc_idesc(!F8, 128, D, true);    // bf16, or f16
             const uint64_t qd0 = tc_desc<S::kBoxB>(sm, 16, 8 * S::kBoxB);
-            int fl[2] = {0, 0}, parts = 0;
+            int fl = 0, parts = 0;  // flags of the tiles qk - 1 (low byte), qk - 2, ..
             int qk = 0, kp = 0, pv = 0, vp = 0;  // next tile and piece of either product
             bool p_in = false;  // P of tile pv is there, and O free for it
             uint64_t t0 = 0;
             uint32_t idle = 0;
             while (pv < n_units) {
-                // S of tile qk takes the buffer of tile qk - 2, whose P has been read
-                if (qk < n_units && qk <= pv + 1) {
+                // S of tile qk takes the buffer of tile qk - NS, whose P has been read
+                if (qk < n_units && qk < pv + NS) {
                     const int pc = qk * KP + kp, st = pc % NK;
                     if (mbar_test(&b_k[st], (pc / NK) & 1)) {
                         const AttnUnit* d = &s_unit[qk % kUnitRing];
@@ -632,7 +644,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                             tc_fence_after();
                             const uint64_t kd0 = tc_desc<S::kBoxB>(sm + S::kOffK + st * S::kKPiece, 16,
                                                                    S::kKBlks * S::kAtom);
-                            const uint32_t dS = tmem + S::kColS + (qk & 1) * TK;
+                            const uint32_t dS = tmem + S::kColS + qk % NS * TK;
                             constexpr int KS = S::kKBlks * S::kSteps;  // k steps of the piece
 #pragma unroll
                             for (int t = 0; t < S::kTerms; ++t)
@@ -652,9 +664,9 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                                 }
                             tc_commit(&b_ke[st]);
                             if (++kp == KP) {
-                                tc_commit(&b_s[qk & 1]);
+                                tc_commit(&b_s[qk % NS]);
                                 if (flags & kUnitLast) tc_commit(&b_qe[qs]);
-                                fl[qk & 1] = flags;
+                                fl = (fl << 8) | flags;
                                 kp = 0;
                                 ++qk;
                             }
@@ -664,8 +676,8 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                     }
                 }
                 if (pv < qk) {
-                    const bool first = fl[pv & 1] & kUnitFirst;
-                    p_in = p_in || (mbar_test(&b_p[pv & 1], (pv >> 1) & 1) &&
+                    const bool first = (fl >> (8 * (qk - 1 - pv))) & kUnitFirst;
+                    p_in = p_in || (mbar_test(&b_p[pv % NS], (pv / NS) & 1) &&
                                     (!first || parts == 0 || mbar_test(&b_o, (parts - 1) & 1)));
                     bool went = false;
                     while (p_in && vp < VP) {
@@ -679,14 +691,14 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
 #pragma unroll
                         for (int ks = 0; ks < S::kVKeys / 16; ++ks)
                             tc_mma_ts<false>(tmem + S::kColO,
-                                             tmem + S::kColS + (pv & 1) * TK + (vp * (S::kVKeys / 16) + ks) * 8,
+                                             tmem + S::kColS + pv % NS * TK + (vp * (S::kVKeys / 16) + ks) * 8,
                                              vd + ((ks * (F8 ? 2048 : 2 * S::kVBlks * S::kAtom)) >> 4), iO, !(first && vp == 0 && ks == 0));
                         tc_commit(F8 ? &b_fe[pc % NF] : &b_ve[pc % NV]);
                         ++vp;
                         went = true;
                     }
                     if (vp == VP) {
-                        tc_commit(&b_pv[pv & 1]);
+                        tc_commit(&b_pv[pv % NS]);
                         parts += first;
                         vp = 0;
                         p_in = false;
@@ -722,7 +734,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         int pr = -1, seg_start = 0;
         AttnRow row{};
         for (int u = 0; u < n_units; ++u) {
-            if (!warp_wait(&b_s[u & 1], u >> 1)) break;
+            if (!warp_wait(&b_s[u % NS], u / NS)) break;
             tc_fence_after();
             const AttnUnit td = s_unit[u % kUnitRing];
             const int h = td.g / p.row_blocks;
@@ -735,11 +747,11 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 if (F8) {
                     if (p.k_scale) c2 *= __ldg(p.k_scale + h);
                     c2 *= __uint_as_float(
-                        static_cast<uint32_t>(127 - s_rs[F8 ? td.seg & 3 : 0][F8 ? min(r, ROWS - 1) : 0]) << 23);
+                        static_cast<uint32_t>(127 - s_rs[F8 ? td.seg & 7 : 0][F8 ? min(r, ROWS - 1) : 0]) << 23);
                 }
                 l = 0.f;
             }
-            const uint32_t tS = tmem + lanes + S::kColS + (u & 1) * TK;
+            const uint32_t tS = tmem + lanes + S::kColS + u % NS * TK;
             // seen: k <= hi and (k > lo or k < sk), as bits of the 32 columns from column c
             auto mask = [&](uint32_t* x, int c) {
                 const int hi = pr - td.start - c;
@@ -802,7 +814,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 m = mx;
             }
             if (__any_sync(0xffffffffu, grow)) {
-                if (!warp_wait(&b_pv[(u - 1) & 1], (u - 1) >> 1)) break;
+                if (!warp_wait(&b_pv[(u - 1) % NS], (u - 1) / NS)) break;
                 tc_fence_after();
 #pragma unroll 1
                 for (int c = half * (D / H); c < (half + 1) * (D / H); c += 32) {
@@ -836,7 +848,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&b_p[u & 1]);
+            if (lane == 0) mbar_arrive(&b_p[u % NS]);
             if (!(td.flags & kUnitLast)) continue;
 
             // ---- end of the part: its rows are written by the query warps
