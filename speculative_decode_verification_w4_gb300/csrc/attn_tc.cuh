@@ -71,9 +71,17 @@ struct AttnTcShape {
     static constexpr int kNQ = kQSmem ? 1 : 2;       // query buffers
     static_assert(!(F8 && D == 256 && ROWS > 64), "blocks of 64 rows");
     static constexpr int kNK = F8 ? (D == 64 ? 6 : (D == 128 ? 4 : 3)) : (D == 64 ? 4 : (D == 128 ? 3 : 2));
-    static constexpr int kNV = F8 ? (D == 64 ? 6 : (D == 128 ? 6 : 4))
-                                  : (D == 64 ? 4 : (D == 128 || ROWS == 64 ? 3 : 2));
-    static constexpr int kNF = !F8 ? 0 : (D == 64 ? 4 : (D == 128 ? 5 : 6));  // f16 pieces
+    static constexpr int kNV = F8 ? (D == 256 ? 4 : 8) : (D == 64 ? 4 : (D == 128 || ROWS == 64 ? 3 : 2));
+    static constexpr int kNF = !F8 ? 0 : (D == 256 ? 6 : 4);  // f16 pieces
+    static constexpr int kPass = 4;                  // warps that pass V on
+    // e4m3: each takes every kPass-th piece, and loads may land out of order.  A place of
+    // the ring has to be one warp's, or a warp could wait for its next piece while the
+    // place still waits for the one before, whose phase has the same parity as the one
+    // two before that: over, it would seem.
+    static_assert(!F8 || kNV % kPass == 0, "a place of the V ring belongs to one warp");
+    // (a place of the f16 ring is waited for in the order of the products, which ends the
+    // phase before: the warp's piece before was free of piece pc - kPass)
+    static_assert(!F8 || kNF >= kPass, "f16 ring");
     static constexpr int kThreads = 16 * 32;
     static constexpr int kHalves = D == 64 && ROWS == 64 ? 2 : 1;  // threads of a softmax row
     static constexpr int kLoadV = kHalves > 1 ? 2 : 5, kLoadK = kHalves > 1 ? 3 : 6;  // warps
@@ -179,7 +187,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             }
             for (int k = 0; k < 8; ++k) {
                 mbar_init(&b_part[k], 1);
-                mbar_init(&b_clean[k], F8 ? 1 : 4);
+                mbar_init(&b_clean[k], F8 ? 1 : S::kPass);
             }
             mbar_init(&b_o, row_warps);
             mbar_init(&b_end, 1);
@@ -512,7 +520,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         // ---------------------------------------------------- V pieces passed on
         const int at = tid - kTcPass * 32;
         constexpr int CH = D * S::kES / 16;
-        for (int pc = F8 ? warp - kTcPass : 0; pc < n_units * VP; pc += F8 ? 4 : 1) {
+        for (int pc = F8 ? warp - kTcPass : 0; pc < n_units * VP; pc += F8 ? S::kPass : 1) {
             const int u = pc / VP, st = pc % NV;
             if (!warp_wait(&b_v[st], pc / NV)) break;
             const AttnUnit d = s_vunit[u % kUnitRing];
@@ -526,7 +534,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
             if (!F8) {
                 if (edge) {
 #pragma unroll 1
-                    for (int c = at; c < S::kVKeys * CH; c += 128) {
+                    for (int c = at; c < S::kVKeys * CH; c += S::kPass * 32) {
                         const int row = c / CH, j = key0 + row;
                         if (key_all(j, d.len, d.p0, p.window, p.sinks)) continue;
                         uint4* q = reinterpret_cast<uint4*>(src + S::v_at(row, c % CH));

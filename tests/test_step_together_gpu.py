@@ -112,3 +112,26 @@ def test_growing_maxima(D, kv, R, Hq):
     o, want, t, tl = attention64(q[0].double(), k, v64[0], n, D ** -0.5, 0, 0, kv)
     check_close(out[0], o, t, "output")
     check_close(lse[0], want, tl, "log-sum-exp")
+
+
+@pytest.mark.parametrize("D,page", [(64, 8), (64, 16), (128, 8), (128, 16), (128, 64), (256, 16)])
+def test_first_call_on_a_cold_cache(D, page):
+    """Pages scattered over memory that was not read before: loads land late and out of
+    order.  The first call gives the bits of the ones after it."""
+    B, Hkv, n = 32, 8, 4000
+    cols = -(-n // page)
+    g = torch.Generator().manual_seed(page + D)
+    total = B * cols * 2
+    table = torch.randperm(total, generator=g)[:B * cols].view(B, cols).to(torch.int32).cuda()
+    k, v = ((torch.randn(total // 64 + 1, 64, page, Hkv, D, device="cuda", dtype=torch.bfloat16) * 20)
+            .to(torch.float8_e4m3fn).view(-1, page, Hkv, D)[:total] for _ in range(2))
+    sc = torch.full((Hkv,), 1 / 20, device="cuda")
+    cache = vw4.KVCache(k, v, table, sc, sc)
+    lens = torch.randint(n // 2, n, (B,), generator=g).to(torch.int32).cuda()
+    q = torch.randn(B, 8, 4 * Hkv, D, generator=g).to(torch.bfloat16).cuda()
+    status()
+    first = vw4.verify_attn(q, cache, lens)
+    for _ in range(3):
+        again = vw4.verify_attn(q, cache, lens)
+        status()
+        assert torch.equal(first.view(torch.int16), again.view(torch.int16))
