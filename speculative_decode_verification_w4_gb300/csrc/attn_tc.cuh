@@ -8,9 +8,9 @@
 // half of K's dimensions; of V 32, 64 or all 128 keys).  One thread
 // issues S = Q K^T and O += P V piece by piece, whichever has its operands first.
 // The softmax warps own one query row a thread, so the softmax has no shuffles,
-// and S and P never pass through shared memory.  S has two buffers, three at head size
-// 64: Q K^T of the next tiles runs under the softmax of this one; P overwrites the
-// front of its S.
+// and S and P never pass through shared memory.  S has two buffers: Q K^T of the
+// next tile runs under the softmax of this one; P overwrites the front of its S.  (A
+// third, for which head size 64 has the room, changed nothing.)
 // Q lies in tensor memory where O (D columns), the S (128 each) and two Q fit its 512
 // columns, else (head size 256) in shared memory: tiles of 64 keys would make
 // room, but the products of 64 columns run at half the rate of those of 128.
@@ -34,7 +34,7 @@
 // the work: at head size 256 shared memory's bandwidth (K is read twice for the two
 // terms, V once raw, written and read as f16: about 1.5 us of a tile of 128 keys
 // against 1.4 for its bytes) and the chain of V's conversion; at 128 and 64 the chain
-// scores - softmax - P V over two score buffers, about 1 us a tile.
+// scores - softmax - P V, about 1 us a tile.
 //
 // The running maximum that the exponents use follows the true one lazily: O is
 // rescaled only when a row's maximum grew by more than 2^8 (its weights are then
@@ -95,7 +95,7 @@ struct AttnTcShape {
     // the products read 128 rows of Q whatever ROWS is: what follows must be there
     static_assert(!kQSmem || kOffStage >= (kTerms * kQRow / kBoxB - 1) * kQBlk + 128 * kBoxB, "Q reads");
     // tensor memory columns: O, two S, the queries (two 16-bit values a column)
-    static constexpr int kNS = D == 64 ? 3 : 2;      // score buffers
+    static constexpr int kNS = 2;                    // score buffers
     static constexpr uint32_t kColO = 0, kColS = D, kColQ = D + kNS * kTK;
     static_assert(D + kNS * kTK + (kQSmem ? 0 : kNQ * D / 2) <= 512, "tensor memory");
     // 16 bytes of a key of a V piece as it is loaded
