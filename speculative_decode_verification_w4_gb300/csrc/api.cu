@@ -212,10 +212,14 @@ int encode_map(CUtensorMap* map, bool bf16, int n, const void* base, const uint6
         b[i] = key.b[i];
         if (i > 0) st[i - 1] = key.s[i];
     }
+    // 64-byte promotion: a head's part of a token may be no longer, and what lies next to it
+    // belongs to other heads' CTAs (e4m3, 8 heads of 128 next to each other, one row a
+    // sequence: 83 us instead of 93 with 256 bytes, of 64 58 instead of 62; bf16 of 64
+    // 73 instead of 100; where the heads lie apart nothing changes)
     const CUresult r =
         g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, n,
                  const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_64B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         char buf[128];
         snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
