@@ -12,9 +12,9 @@
 // batch share one scan of the token history; the few drafts before a row are
 // compared only at the entries that one of them names.  So the rows need no barrier
 // between them.  The bytes bound it (8 a logit; masked logits are not read): 256 x 9
-// rows of 151936 take 469 us, 91 % of the copy rate; 64 x 5 rows with 70 % of the ids
-// masked away 75 us.  The scan re-reads the history once per chunk, from L2.  A small
-// call is the scan's latency: 8 rows of 262144 with 2048 ids of history 7.8 us.
+// rows of 151936 take 438 us, 97 % of the copy rate; 64 x 5 rows with 70 % of the ids
+// masked away 69 us.  The scan re-reads the history once per chunk, from L2.  A small
+// call is the scan's latency: 8 rows of 262144 with 2048 ids of history 8.1 us.
 #include "attn.cuh"
 
 namespace vw4 {
@@ -147,6 +147,23 @@ __global__ void __launch_bounds__(kLogitThreads, VEC == 4 ? 4 : 3)
     const float* bias = p.bias_ids ? p.bias_vals + static_cast<long long>(b) * p.bias_stride : nullptr;
 
     __syncthreads();  // the tables are complete
+    // row i's corrected logit at entry `at`
+    auto correct = [&](int i, int at, float y) {
+        uint32_t c = s_cnt[at];
+        if (c & kDrafted) {
+            c &= ~kDrafted;
+#pragma unroll 1
+            for (int j = 0; j < i; ++j) c += s_draft[j] == c0 + at ? 1u : 0u;
+        }
+        if (c) y = y > 0.f ? __fdiv_rn(y, rep) : y * rep;
+        const float n = static_cast<float>(c & ~kKnown);
+        if (n > 0.f) y = y - fre * n - pre;
+        if (bias) {
+            const uint32_t be = s_bias[at];
+            if (be) y += __ldg(bias + be - 1);
+        }
+        return y;
+    };
     for (int i = row0; i < row1; ++i) {
         if (i + 1 < row1) masks(i + 1);
         const long long row = static_cast<long long>(b) * p.R + i;
@@ -156,30 +173,16 @@ __global__ void __launch_bounds__(kLogitThreads, VEC == 4 ? 4 : 3)
             const int v = place(k), at = v - c0;
             const uint32_t a = (allow >> (k * VEC)) & kFull;
             const uint32_t hits = (s_hit[at >> 5] >> (at & 31)) & a;
+            if (hits) {  // (one branch a step: four, one an element, took 8 % longer)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if ((hits >> e) & 1u) x[k][e] = correct(i, at + e, x[k][e]);
+            }
             float mx = -INFINITY;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                float y = -INFINITY;
-                if ((a >> e) & 1u) {
-                    y = x[k][e];
-                    if ((hits >> e) & 1u) {
-                        uint32_t c = s_cnt[at + e];
-                        if (c & kDrafted) {
-                            c &= ~kDrafted;
-#pragma unroll 1
-                            for (int j = 0; j < i; ++j) c += s_draft[j] == v + e ? 1u : 0u;
-                        }
-                        if (c) y = y > 0.f ? __fdiv_rn(y, rep) : y * rep;
-                        const float n = static_cast<float>(c & ~kKnown);
-                        if (n > 0.f) y = y - fre * n - pre;
-                        if (bias) {
-                            const uint32_t be = s_bias[at + e];
-                            if (be) y += __ldg(bias + be - 1);
-                        }
-                    }
-                }
-                x[k][e] = y;
-                mx = fmaxf(mx, y);
+                if (!((a >> e) & 1u)) x[k][e] = -INFINITY;
+                mx = fmaxf(mx, x[k][e]);
             }
             if (v < p.V) {
                 if (VEC == 4) *reinterpret_cast<float4*>(dst + v) = *reinterpret_cast<float4*>(x[k]);
