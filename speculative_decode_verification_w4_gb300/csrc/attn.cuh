@@ -117,7 +117,6 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t b) {
     return r;
 }
 
-
 // four f16 values (two pairs) as e4m3 bytes hi + lo: hi the nearest, lo the nearest to
 // the rest, which f16 holds exactly
 __device__ __forceinline__ void e4m3_terms(uint32_t ab, uint32_t cd, uint32_t& hi, uint32_t& lo) {

@@ -2,11 +2,13 @@
 // 5th-generation tensor cores: the same units, partials and results as
 // attn_kernel (attn.cuh).
 //
-// One CTA per SM, warps with roles.  A producer warp loads tiles of 128 keys
+// One CTA per SM, warps with roles.  Two producer warps load tiles of 128 keys
 // (TMA) into two rings in the swizzled layout the tensor cores read, one of K
 // pieces and one of V pieces (a piece is the whole tile, or at head size 256
 // half of K's dimensions; of V 32, 64 or all 128 keys).  One thread
 // issues S = Q K^T and O += P V piece by piece, whichever has its operands first.
+// (An elected one: chosen by its lane number it took twice as long over each product,
+// e4m3 of head size 128 136 us against 114.)
 // The softmax warps own one query row a thread, so the softmax has no shuffles,
 // and S and P never pass through shared memory.  S has two buffers: Q K^T of the
 // next tile runs under the softmax of this one; P overwrites the front of its S.  (A
@@ -94,7 +96,7 @@ struct AttnTcShape {
     static_assert(kSmem + 5632 <= 227 * 1024, "shared memory");
     // the products read 128 rows of Q whatever ROWS is: what follows must be there
     static_assert(!kQSmem || kOffStage >= (kTerms * kQRow / kBoxB - 1) * kQBlk + 128 * kBoxB, "Q reads");
-    // tensor memory columns: O, two S, the queries (two 16-bit values a column)
+    // tensor memory columns: O, the S, the queries (two 16-bit values a column)
     static constexpr int kNS = 2;                    // score buffers
     static constexpr uint32_t kColO = 0, kColS = D, kColQ = D + kNS * kTK;
     static_assert(D + kNS * kTK + (kQSmem ? 0 : kNQ * D / 2) <= 512, "tensor memory");
