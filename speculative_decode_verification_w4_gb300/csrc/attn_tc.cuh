@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     if (tid == S::kLoadK * 32) {
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
+        if (S::kQSmem && !F8) tma_prefetch_desc(&maps.q);
     }
     if (warp == kTcMma) {
         tmem_alloc<512>(&s_tmem);
@@ -251,7 +252,19 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                                                   static_cast<long long>(row.hq) * D);
         };
         const bool reused = d.seg >= S::kNQ;
-        if constexpr (S::kQSmem) {
+        if constexpr (S::kQSmem && !F8) {
+            // (every warp arrives, after it has written the part two before)
+            if (reused && !warp_wait(&b_qe[qs], d.seg / S::kNQ - 1)) return false;
+            if (lane == 0) {
+                if (vw == 0) {
+                    mbar_arrive_expect_tx(&b_q[qs], attn_q_bytes(p, D));
+                    attn_load_q<D>(p, &maps.q, sm, S::kQBlk, d, &b_q[qs]);
+                } else {
+                    mbar_arrive(&b_q[qs]);
+                }
+            }
+            __syncwarp();
+        } else if constexpr (S::kQSmem) {
             // a warp a row, a lane 8 dimensions; the first rows are on their way while the
             // last products of the part before are waited for
             constexpr int W = 4, AHEAD = 8;
@@ -269,18 +282,14 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 for (int k = 0; k < AHEAD; ++k) {
                     const int r = r0 + k * W;
                     if (r >= rows) break;
-                    if (F8) {
-                        const uint32_t mx = __reduce_max_sync(0xffffffffu, largest_of(0u, v[k]));
-                        uint32_t hi[2], lo[2];
-                        two_terms(v[k], q_scale(mx, d, r, lane == 0), hi, lo);
+                    const uint32_t mx = __reduce_max_sync(0xffffffffu, largest_of(0u, v[k]));
+                    uint32_t hi[2], lo[2];
+                    two_terms(v[k], q_scale(mx, d, r, lane == 0), hi, lo);
 #pragma unroll
-                        for (int t = 0; t < 2; ++t)
-                            *reinterpret_cast<uint2*>(
-                                smem + S::template at<S::kBoxB>(S::kQBlk, r, t * (D / 16) + lane / 2) +
-                                (lane & 1) * 8) = t ? make_uint2(lo[0], lo[1]) : make_uint2(hi[0], hi[1]);
-                    } else {
-                        *reinterpret_cast<uint4*>(smem + S::template at<S::kBoxB>(S::kQBlk, r, lane)) = v[k];
-                    }
+                    for (int t = 0; t < 2; ++t)
+                        *reinterpret_cast<uint2*>(
+                            smem + S::template at<S::kBoxB>(S::kQBlk, r, t * (D / 16) + lane / 2) +
+                            (lane & 1) * 8) = t ? make_uint2(lo[0], lo[1]) : make_uint2(hi[0], hi[1]);
                 }
             }
             if (vw >= rows && reused && !warp_wait(&b_qe[qs], d.seg / S::kNQ - 1)) return false;
@@ -508,16 +517,20 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     } else if (n_units > 0 && warp >= kTcQ && warp < kTcPass) {
         // ------------------------------------------- queries in, finished rows out
         const int vw = warp - kTcQ;
+        int asked = -1;  // the last part whose queries were asked for
         for (int k = 0;; ++k) {
             if (!warp_wait(&b_part[k & 7], k >> 3)) break;
             const bool more = k < s_parts;
             if (more) {
                 const AttnUnit d = s_part[k & 7];
                 if (!queries(d, vw)) break;
+                asked = k;
             }
             if (k > 0 && vw < row_warps && !finish(k - 1, vw)) break;
             if (!more) break;
         }
+        if (S::kQSmem && !F8 && vw == 0 && asked >= 0)  // a load in flight lands before the end
+            mbar_wait_bounded(&b_q[0], asked & 1, p.wait_ns, nullptr);
     } else if (n_units > 0 && warp >= kTcPass) {
         // ---------------------------------------------------- V pieces passed on
         const int at = tid - kTcPass * 32;
