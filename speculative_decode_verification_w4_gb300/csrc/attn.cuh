@@ -65,6 +65,9 @@ __host__ __device__ inline int attn_ctas(long long T, int grid) {
 }
 __host__ __device__ inline long long attn_unit(long long T, int G, int i) { return T * i / G; }
 __host__ __device__ inline int attn_owner(long long T, int G, long long u) {
+    if (T < (1ll << 32) / (kAttnMaxGrid64 + 1))  // (T (G + 1) in 32 bits: a short division)
+        return static_cast<int>((static_cast<uint32_t>(u + 1) * static_cast<uint32_t>(G) +
+                                 static_cast<uint32_t>(T) - 1u) / static_cast<uint32_t>(T)) - 1;
     return static_cast<int>(((u + 1) * G + T - 1) / T - 1);
 }
 
