@@ -31,11 +31,15 @@ constexpr int kJoinThreads = 128;
 
 // Joins the partials of split items, in the order of their tiles, and writes
 // the rows of sequences without keys.  One block takes `chunk` rows of an
-// item, a warp a row, or 64 columns of one.  The lanes weigh up to 32 partials at
-// once and then own E columns each; the first U partials' values are on their way
-// while the weights are computed (the kernel is a chain of load latencies).  A kernel of its own
-// rather than the last CTA of each item: no ticket to clear and none to wait for.
-template <int D, bool FINE>
+// item, a warp a row (kJoinRows) or 64 columns of one (kJoinColumns); or its warps
+// share the parts of 64 columns of a row (kJoinParts).  The lanes weigh up to 32
+// partials at once and then own E columns each; the first U partials' values are on
+// their way while the weights are computed (the kernel is a chain of load latencies).
+// A kernel of its own rather than the last CTA of each item: no ticket to clear and
+// none to wait for.
+constexpr int kJoinRows = 0, kJoinColumns = 1, kJoinParts = 2;
+
+template <int D, int MODE>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParams p, int rows,
                                                                  int grid, int tk, int chunk) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -52,19 +56,25 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
         c1 = attn_owner(T, G, u + nt - 1);
         if (c0 == c1) return;  // written by the attention kernel
     }
-    constexpr int E = FINE ? 2 : D / 32, U = FINE ? 16 : 8, WR = D / (32 * E);  // (warps of a row)
+    constexpr bool PARTS = MODE == kJoinParts;
+    constexpr int E = MODE == kJoinRows ? D / 32 : 2, U = MODE == kJoinRows ? 8 : 16;
+    constexpr int WR = D / (32 * E), W = kJoinThreads / 32;  // warps of a row, of the block
+    __shared__ float s_m[PARTS ? W : 1], s_l[PARTS ? W : 1];
+    __shared__ float2 s_acc[PARTS ? W : 1][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = (warp % WR) * 64 + lane * 2;
+    const int col = (PARTS ? blockIdx.y % WR : warp % WR) * 64 + lane * 2;
+    const int per = (c1 - c0 + W) / W;  // a warp's parts of kJoinParts
+    const int cs = PARTS ? c0 + warp * per : c0, ce = PARTS ? min(c1, cs + per - 1) : c1;
     const float vs = p.v_scale ? __ldg(p.v_scale + h) : 1.f;
     const size_t slot = static_cast<size_t>(rows) * (D + 2);
     auto part = [&](int c) { return p.partial + static_cast<size_t>(c == c0 ? 2 * c + 1 : 2 * c) * slot; };
-    const int r1 = min((static_cast<int>(blockIdx.y) + 1) * chunk, rows);
-    for (int r = blockIdx.y * chunk + warp / WR; r < r1; r += kJoinThreads / 32 / WR) {
+    const int r0 = PARTS ? blockIdx.y / WR : blockIdx.y * chunk, r1 = min(r0 + chunk, rows);
+    for (int r = PARTS ? r0 : r0 + warp / WR; r < r1; r += PARTS ? 1 : W / WR) {
         const AttnRow row = attn_row(p, g, r);
         if (!row.live) continue;
         float M = -INFINITY, L = 0.f, acc[E] = {};
-        for (int cb = c0; cb <= c1; cb += 32) {
-            const int n = min(32, c1 - cb + 1);
+        for (int cb = cs; cb <= ce; cb += 32) {
+            const int n = min(32, ce - cb + 1);
             float v[U][E];
             auto fetch = [&](int k0) {
 #pragma unroll
@@ -111,6 +121,24 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
                 }
             }
         }
+        if constexpr (PARTS) {  // (one row a block)
+            if (lane == 0) s_m[warp] = M, s_l[warp] = L;
+            s_acc[warp][lane] = make_float2(acc[0], acc[1]);
+            __syncthreads();
+            if (warp > 0) return;
+            float mx = M;
+#pragma unroll
+            for (int k = 1; k < W; ++k) mx = fmaxf(mx, s_m[k]);
+            M = mx;
+            L = acc[0] = acc[1] = 0.f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                const float w = mx == -INFINITY ? 1.f : ex2(s_m[k] - mx);
+                L = fmaf(s_l[k], w, L);
+                acc[0] = fmaf(s_acc[k][lane].x, w, acc[0]);
+                acc[1] = fmaf(s_acc[k][lane].y, w, acc[1]);
+            }
+        }
         const float f = L == 0.f ? 0.f : vs / L;
         const long long orow = static_cast<long long>(b) * p.R + row.i;
         __nv_bfloat16* out = p.out + orow * p.ldo + static_cast<long long>(row.hq) * D;
@@ -120,6 +148,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
         if (col == 0 && p.lse)
             p.lse[orow * p.Hq + row.hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
     }
+}
+
+template <int D>
+static void (*join_of(int mode))(const AttnParams, int, int, int, int) {
+    return mode == kJoinParts     ? attn_join_kernel<D, kJoinParts>
+           : mode == kJoinColumns ? attn_join_kernel<D, kJoinColumns>
+                                  : attn_join_kernel<D, kJoinRows>;
 }
 
 AttnPlan attn_plan(AttnParams& p, int D, bool f8, void* ws) {
@@ -175,16 +210,20 @@ cudaError_t launch_attn(const AttnParams& p, const AttnMaps& maps, AttnPlan plan
     // once (8 x 6 rows of 16 items of 256 in ten parts each: 29.2 us a call instead of
     // 31.0, one token of 4 items in nine parts 11.3 instead of 12.3).  Else a warp a row:
     // 256 items of 4 rows in one or two parts 146 us instead of 149, 128 rows of 32 items
-    // 40.3 instead of 42.5.  About eight blocks an SM.
+    // 40.3 instead of 42.5.  About eight blocks an SM.  From 32 parts on the warps of a
+    // block share them (8 rows of one item of 128 over 65536 tokens, in 304 parts: 23.5 us
+    // instead of 39.4; 32 rows of 4 items in 38: 24.2 instead of 28.8).
     const int items = p.B * p.groups, used = p.tb * p.gb;
     const long long all = static_cast<long long>(items) * used;
     const bool fine = items <= grid / 4 && all <= 8 * sms;
+    const bool parts = fine && items <= grid / 32;
     const int at_once = fine ? kJoinThreads * 2 / D : kJoinThreads / 32;
     int chunk = static_cast<int>((all + 8 * sms - 1) / (8 * sms));
     chunk = chunk < at_once ? at_once : chunk;
     if (chunk > used) chunk = used;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(items, (used + chunk - 1) / chunk);
+    if (parts) chunk = 1;
+    cfg.gridDim = dim3(items, parts ? used * (D / 64) : (used + chunk - 1) / chunk);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -192,9 +231,8 @@ cudaError_t launch_attn(const AttnParams& p, const AttnMaps& maps, AttnPlan plan
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto* join = D == 64    ? (fine ? attn_join_kernel<64, true> : attn_join_kernel<64, false>)
-                 : D == 128 ? (fine ? attn_join_kernel<128, true> : attn_join_kernel<128, false>)
-                            : (fine ? attn_join_kernel<256, true> : attn_join_kernel<256, false>);
+    const int mode = parts ? kJoinParts : (fine ? kJoinColumns : kJoinRows);
+    auto* join = D == 64 ? join_of<64>(mode) : (D == 128 ? join_of<128>(mode) : join_of<256>(mode));
     return cudaLaunchKernelEx(&cfg, join, p, rows, grid, tk, chunk);
 }
 
