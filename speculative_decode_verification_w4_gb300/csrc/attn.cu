@@ -210,13 +210,14 @@ cudaError_t launch_attn(const AttnParams& p, const AttnMaps& maps, AttnPlan plan
     // once (8 x 6 rows of 16 items of 256 in ten parts each: 29.2 us a call instead of
     // 31.0, one token of 4 items in nine parts 11.3 instead of 12.3).  Else a warp a row:
     // 256 items of 4 rows in one or two parts 146 us instead of 149, 128 rows of 32 items
-    // 40.3 instead of 42.5.  About eight blocks an SM.  From 32 parts on the warps of a
+    // 40.3 instead of 42.5.  About eight blocks an SM.  From 16 parts on the warps of a
     // block share them (8 rows of one item of 128 over 65536 tokens, in 304 parts: 23.5 us
-    // instead of 39.4; 32 rows of 4 items in 38: 24.2 instead of 28.8).
+    // instead of 39.4; 32 rows of 8 items in 19: 30.1 instead of 31.8; with ten parts it
+    // took the 48 rows above 33.7 instead of 28.9).
     const int items = p.B * p.groups, used = p.tb * p.gb;
     const long long all = static_cast<long long>(items) * used;
     const bool fine = items <= grid / 4 && all <= 8 * sms;
-    const bool parts = fine && items <= grid / 32;
+    const bool parts = fine && items <= grid / 16;
     const int at_once = fine ? kJoinThreads * 2 / D : kJoinThreads / 32;
     int chunk = static_cast<int>((all + 8 * sms - 1) / (8 * sms));
     chunk = chunk < at_once ? at_once : chunk;
