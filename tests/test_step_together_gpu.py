@@ -135,3 +135,22 @@ def test_first_call_on_a_cold_cache(D, page):
         again = vw4.verify_attn(q, cache, lens)
         status()
         assert torch.equal(first.view(torch.int16), again.view(torch.int16))
+
+
+@pytest.mark.parametrize("R,G", [(1, 3), (4, 6), (16, 8)])
+@pytest.mark.parametrize("B,Hkv,n", [(1, 1, 9000), (1, 8, 3000), (4, 8, 1500), (8, 8, 700), (20, 8, 300)])
+def test_items_in_many_and_few_parts(B, Hkv, n, R, G):
+    """One item over every CTA down to many items each inside one: every way of joining."""
+    D, kv = 128, "e4m3" if R == 4 else "bf16"
+    lens = [n - 7 * b for b in range(B)]
+    c, k64, v64 = make_cache(80 + B, lens, 64, Hkv, D, kv)
+    g = torch.Generator().manual_seed(B)
+    q = (torch.randn(B, R, Hkv * G, D, generator=g) * 2).to(torch.bfloat16)
+    length = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    lse = torch.empty(B, R, Hkv * G, device="cuda")
+    out = vw4.verify_attn(q.cuda(), c, length, lse=lse)
+    status()
+    for b in {0, B // 2, B - 1}:
+        o, want, t, tl = attention64(q[b].double(), k64[b], v64[b], lens[b], D ** -0.5, 0, 0, kv)
+        check_close(out[b], o, t, f"sequence {b} output")
+        check_close(lse[b], want, tl, f"sequence {b} log-sum-exp")
