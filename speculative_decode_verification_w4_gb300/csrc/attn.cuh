@@ -19,7 +19,7 @@
 // What bounds it.  Long caches: the bytes of K and V (32 sequences of 2000 .. 32768
 // tokens, 8 key heads of 128, e4m3, 4 query heads each: 145 us, 77 % of the copy
 // rate).  Short calls: a chain of latencies -- schedule, page id, first tile, softmax,
-// join -- of about 12 us (one token over 517 of head size 256).
+// join -- of about 11 us (one token over 517 of head size 256).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
