@@ -215,30 +215,49 @@ def vw4_workspace_bytes(op: int, a: int, b: int, c: int) -> int:
     return int(load_library().vw4_workspace_bytes(op, a, b, c))
 
 
+def _empty(shape, dtype, device, stream):
+    """An uninitialized tensor for a call on `stream` (None: the current one).  Its memory is
+    that stream's, so nothing that another stream still has to do touches it."""
+    if stream is None or torch.device(device).type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class Workspace:
-    """A growable device scratch buffer (256-byte aligned torch allocation),
-    zero-filled when allocated as the library requires of a fresh workspace
-    (every call leaves it that way)."""
+    """A growable device scratch buffer (256-byte aligned torch allocation, not
+    initialized: no call needs that).  It serves one call after another on one
+    stream; calls that may overlap need a workspace each, and so does a captured
+    call that is replayed (a larger call replaces the buffer)."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = None
+        self._stream = None  # the handle of the stream that the buffer was made on
 
-    def get(self, nbytes: int) -> torch.Tensor:
+    def get(self, nbytes: int, stream=None) -> torch.Tensor:
+        """The buffer, grown to nbytes, for a call on `stream` (None: the current one)."""
+        if stream is None and self.device.type == "cuda":
+            stream = torch.cuda.current_stream(self.device)
+        handle = None if stream is None else stream.cuda_stream
         if self.buf is None or self.buf.numel() < nbytes:
-            self.buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+            self.buf = _empty((max(nbytes, 256),), torch.uint8, self.device, stream)
+            self._stream = handle
+        elif handle != self._stream and self.buf.is_cuda:
+            self.buf.record_stream(stream)
         return self.buf
 
 
-_default_ws = {}
+_default_ws = {}  # one for each device, thread and stream
 
 
-def _workspace(ws, nbytes, device):
+def _workspace(ws, nbytes, device, stream):
     if ws is None:
-        key = (device.index, threading.get_ident())
+        s = stream if stream is not None else torch.cuda.current_stream(device)
+        key = (device.index, threading.get_ident(), s.cuda_stream)
         ws = _default_ws.setdefault(key, Workspace(device))
     if isinstance(ws, Workspace):
-        return ws.get(nbytes)
+        return ws.get(nbytes, stream)
     if ws.numel() * ws.element_size() < nbytes:
         raise VW4Error(6, "workspace", f"need {nbytes} bytes")
     return ws
@@ -265,7 +284,7 @@ def verify_gemm_w4(fmt: int, q: torch.Tensor, scales: torch.Tensor, tensor_scale
         out = torch.empty((M, N), dtype=torch.float32, device=A.device)
     W = make_weight(fmt, q, scales, tensor_scale, N, K)
     need = vw4_workspace_bytes(OP_GEMM, M, N, K)
-    ws = _workspace(workspace, need, A.device)
+    ws = _workspace(workspace, need, A.device, stream)
     code = load_library().verify_gemm_w4(ctypes.byref(W), _ptr(A), M, A.stride(0), _ptr(out),
                                          out.stride(0), _ptr(row_argmax), _ptr(ws),
                                          ws.numel(), _stream(stream))
@@ -290,7 +309,7 @@ def verify_gemm_w4_blockmax(fmt: int, q: torch.Tensor, scales: torch.Tensor,
     if block_max.stride(0) != nb or block_max.stride(1) != 1:
         raise ValueError("block_max must be a contiguous [M, ceil(N/16)] tensor")
     W = make_weight(fmt, q, scales, tensor_scale, N, K)
-    ws = _workspace(workspace, vw4_workspace_bytes(OP_GEMM, M, N, K), A.device)
+    ws = _workspace(workspace, vw4_workspace_bytes(OP_GEMM, M, N, K), A.device, stream)
     code = load_library().verify_gemm_w4_blockmax(ctypes.byref(W), _ptr(A), M, A.stride(0),
                                                   _ptr(out), out.stride(0), _ptr(block_max),
                                                   _ptr(ws), ws.numel(), _stream(stream))
@@ -315,7 +334,7 @@ def verify_greedy_w4(fmt: int, q: torch.Tensor, scales: torch.Tensor, tensor_sca
     if length is None:
         length = torch.empty((B,), dtype=torch.int32, device=A.device)
     W = make_weight(fmt, q, scales, tensor_scale, N, K)
-    ws = _workspace(workspace, vw4_workspace_bytes(OP_GEMM, M, N, K), A.device)
+    ws = _workspace(workspace, vw4_workspace_bytes(OP_GEMM, M, N, K), A.device, stream)
     code = load_library().verify_greedy_w4(
         ctypes.byref(W), _ptr(A), A.stride(0), _ptr(drafts), B, Kd, _ptr(tokens), _ptr(length),
         _ptr(out), out.stride(0) if out is not None else 0, _ptr(ws), ws.numel(), _stream(stream))
@@ -369,7 +388,7 @@ class PreparedGemm:
         self.N, self.K = q.shape[0], q.shape[1] * 2
         self.W = make_weight(fmt, q, scales, tensor_scale, self.N, self.K)
         need = vw4_workspace_bytes(OP_GEMM, M_max, self.N, self.K)
-        self.ws = torch.zeros(max(need, 256), dtype=torch.uint8, device=q.device)
+        self.ws = _empty((max(need, 256),), torch.uint8, q.device, stream)
         self.ws_ptr, self.ws_bytes = self.ws.data_ptr(), self.ws.numel()
         self.stream = (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
         self._fn = load_library().verify_gemm_w4
@@ -417,7 +436,7 @@ def verify_moe_w4(fmt: int, q: torch.Tensor, scales: torch.Tensor, tensor_scale:
         out = torch.empty((rows, N), dtype=torch.float32, device=A.device)
     W = make_weight(fmt, q, scales, tensor_scale, N, K)
     need = vw4_workspace_bytes(OP_MOE, M * topk, N, K)
-    ws = _workspace(workspace, need, A.device)
+    ws = _workspace(workspace, need, A.device, stream)
     code = load_library().verify_moe_w4(ctypes.byref(W), E, _ptr(A), A.stride(0), rows_are_pairs,
                                         _ptr(expert_ids), _ptr(gates), M, topk, combine,
                                         _ptr(out), out.stride(0), _ptr(ws), ws.numel(),
@@ -458,7 +477,7 @@ def accept_rejection(target_logits: torch.Tensor, draft_logits: torch.Tensor | N
         length = torch.empty((B,), dtype=torch.int32, device=dev)
     prm = Sampling(float(temperature), float(top_p), int(top_k), float(min_p))
     need = vw4_workspace_bytes(OP_REJECTION, B, Kd, V)
-    ws = _workspace(workspace, need, dev)
+    ws = _workspace(workspace, need, dev, stream)
     code = load_library().accept_rejection(_ptr(target_logits), _ptr(draft_logits), _ptr(drafts),
                                            B, Kd, V, ctypes.byref(prm), int(seed), int(offset),
                                            _ptr(tokens), _ptr(length), _ptr(ws), ws.numel(),
@@ -485,7 +504,7 @@ def accept_rejection_blockmax(target_logits: torch.Tensor, target_bmax: torch.Te
     if length is None:
         length = torch.empty((B,), dtype=torch.int32, device=dev)
     prm = Sampling(float(temperature), float(top_p), int(top_k), float(min_p))
-    ws = _workspace(workspace, vw4_workspace_bytes(OP_REJECTION, B, Kd, V), dev)
+    ws = _workspace(workspace, vw4_workspace_bytes(OP_REJECTION, B, Kd, V), dev, stream)
     code = load_library().accept_rejection_blockmax(
         _ptr(target_logits), _ptr(target_bmax), _ptr(draft_logits), _ptr(draft_bmax),
         _ptr(drafts), B, Kd, V, ctypes.byref(prm), int(seed), int(offset), _ptr(tokens),
@@ -511,7 +530,7 @@ def accept_rejection_topk(target_ids: torch.Tensor, target_vals: torch.Tensor,
         length = torch.empty((B,), dtype=torch.int32, device=dev)
     prm = Sampling(float(temperature), float(top_p), int(top_k), float(min_p))
     need = vw4_workspace_bytes(OP_REJECTION_TOPK, B, Kd, Kt)
-    ws = _workspace(workspace, need, dev)
+    ws = _workspace(workspace, need, dev, stream)
     code = load_library().accept_rejection_topk(
         _ptr(target_ids), _ptr(target_vals), _ptr(draft_ids), _ptr(draft_vals), _ptr(drafts), B,
         Kd, Kt, int(V), ctypes.byref(prm), int(seed), int(offset), _ptr(tokens), _ptr(length),
@@ -668,7 +687,7 @@ class PreparedAttn(_Prepared):
         need = vw4_workspace_bytes(OP_ATTN, B, R * max(1, Hq // cache.Hkv), D)
         if workspace is None:
             workspace = Workspace(q.device)
-        ws = _workspace(workspace, need, q.device)
+        ws = _workspace(workspace, need, q.device, stream)
         self._bind("verify_attn", args, (q, cache, seq_lens, out, lse), stream, ws)
 
 
@@ -680,7 +699,7 @@ def verify_attn(q, cache, seq_lens, scale=None, window=0, sinks=0, out=None, lse
     need = vw4_workspace_bytes(OP_ATTN, q.shape[0], q.shape[1] * max(1, q.shape[2] // cache.Hkv),
                                q.shape[3])
     p = PreparedAttn(q, cache, seq_lens, scale, window, sinks, out, lse,
-                     _workspace(workspace, need, q.device), stream)
+                     _workspace(workspace, need, q.device, stream), stream)
     p()
     return p.out
 
