@@ -224,6 +224,15 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _result(shape, dtype, device, stream):
+    """A tensor for the results of a call on `stream`, which the caller reads on the current
+    one once that waits for `stream`: neither hands its memory on while the other uses it."""
+    t = _empty(shape, dtype, device, stream)
+    if stream is not None and t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 class Workspace:
     """A growable device scratch buffer (256-byte aligned torch allocation, not
     initialized: no call needs that).  It serves one call after another on one
@@ -281,7 +290,7 @@ def verify_gemm_w4(fmt: int, q: torch.Tensor, scales: torch.Tensor, tensor_scale
     if A.dtype != torch.bfloat16:
         raise ValueError("A must be bfloat16")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=A.device)
+        out = _result((M, N), torch.float32, A.device, stream)
     W = make_weight(fmt, q, scales, tensor_scale, N, K)
     need = vw4_workspace_bytes(OP_GEMM, M, N, K)
     ws = _workspace(workspace, need, A.device, stream)
@@ -302,10 +311,10 @@ def verify_gemm_w4_blockmax(fmt: int, q: torch.Tensor, scales: torch.Tensor,
     if A.dtype != torch.bfloat16:
         raise ValueError("A must be bfloat16")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=A.device)
+        out = _result((M, N), torch.float32, A.device, stream)
     nb = (N + 15) // 16
     if block_max is None:
-        block_max = torch.empty((M, nb), dtype=torch.float32, device=A.device)
+        block_max = _result((M, nb), torch.float32, A.device, stream)
     if block_max.stride(0) != nb or block_max.stride(1) != 1:
         raise ValueError("block_max must be a contiguous [M, ceil(N/16)] tensor")
     W = make_weight(fmt, q, scales, tensor_scale, N, K)
@@ -330,9 +339,9 @@ def verify_greedy_w4(fmt: int, q: torch.Tensor, scales: torch.Tensor, tensor_sca
     if A.dtype != torch.bfloat16 or A.shape[0] != M:
         raise ValueError("A must be bfloat16 [B*(Kd+1), K]")
     if tokens is None:
-        tokens = torch.empty((B, Kd + 1), dtype=torch.int32, device=A.device)
+        tokens = _result((B, Kd + 1), torch.int32, A.device, stream)
     if length is None:
-        length = torch.empty((B,), dtype=torch.int32, device=A.device)
+        length = _result((B,), torch.int32, A.device, stream)
     W = make_weight(fmt, q, scales, tensor_scale, N, K)
     ws = _workspace(workspace, vw4_workspace_bytes(OP_GEMM, M, N, K), A.device, stream)
     code = load_library().verify_greedy_w4(
@@ -414,7 +423,7 @@ def verify_gemm_w4_noalloc(fmt: int, q: torch.Tensor, scales: torch.Tensor, tens
     if A.dtype != torch.bfloat16:
         raise ValueError("A must be bfloat16")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=A.device)
+        out = _result((M, N), torch.float32, A.device, stream)
     W = make_weight(fmt, q, scales, tensor_scale, N, K)
     code = load_library().verify_gemm_w4_noalloc(ctypes.byref(W), _ptr(A), M, A.stride(0),
                                                  _ptr(out), out.stride(0), _ptr(row_argmax),
@@ -433,7 +442,7 @@ def verify_moe_w4(fmt: int, q: torch.Tensor, scales: torch.Tensor, tensor_scale:
     M, topk = expert_ids.shape
     rows = M if combine else M * topk
     if out is None:
-        out = torch.empty((rows, N), dtype=torch.float32, device=A.device)
+        out = _result((rows, N), torch.float32, A.device, stream)
     W = make_weight(fmt, q, scales, tensor_scale, N, K)
     need = vw4_workspace_bytes(OP_MOE, M * topk, N, K)
     ws = _workspace(workspace, need, A.device, stream)
@@ -454,9 +463,9 @@ def accept_greedy(target_logits: torch.Tensor | None, drafts: torch.Tensor,
     Kd = drafts.shape[1]
     dev = drafts.device
     if tokens is None:
-        tokens = torch.empty((B, Kd + 1), dtype=torch.int32, device=dev)
+        tokens = _result((B, Kd + 1), torch.int32, dev, stream)
     if length is None:
-        length = torch.empty((B,), dtype=torch.int32, device=dev)
+        length = _result((B,), torch.int32, dev, stream)
     code = load_library().accept_greedy(_ptr(target_logits), _ptr(drafts), _ptr(target_argmax), B,
                                         Kd, V, _ptr(tokens), _ptr(length), _stream(stream))
     _check(code, "accept_greedy")
@@ -472,9 +481,9 @@ def accept_rejection(target_logits: torch.Tensor, draft_logits: torch.Tensor | N
     Kd = R - 1
     dev = target_logits.device
     if tokens is None:
-        tokens = torch.empty((B, Kd + 1), dtype=torch.int32, device=dev)
+        tokens = _result((B, Kd + 1), torch.int32, dev, stream)
     if length is None:
-        length = torch.empty((B,), dtype=torch.int32, device=dev)
+        length = _result((B,), torch.int32, dev, stream)
     prm = Sampling(float(temperature), float(top_p), int(top_k), float(min_p))
     need = vw4_workspace_bytes(OP_REJECTION, B, Kd, V)
     ws = _workspace(workspace, need, dev, stream)
@@ -500,9 +509,9 @@ def accept_rejection_blockmax(target_logits: torch.Tensor, target_bmax: torch.Te
         raise ValueError("block maxima must be [B, rows, ceil(V/16)]")
     dev = target_logits.device
     if tokens is None:
-        tokens = torch.empty((B, Kd + 1), dtype=torch.int32, device=dev)
+        tokens = _result((B, Kd + 1), torch.int32, dev, stream)
     if length is None:
-        length = torch.empty((B,), dtype=torch.int32, device=dev)
+        length = _result((B,), torch.int32, dev, stream)
     prm = Sampling(float(temperature), float(top_p), int(top_k), float(min_p))
     ws = _workspace(workspace, vw4_workspace_bytes(OP_REJECTION, B, Kd, V), dev, stream)
     code = load_library().accept_rejection_blockmax(
@@ -525,9 +534,9 @@ def accept_rejection_topk(target_ids: torch.Tensor, target_vals: torch.Tensor,
     Kd = R - 1
     dev = target_ids.device
     if tokens is None:
-        tokens = torch.empty((B, Kd + 1), dtype=torch.int32, device=dev)
+        tokens = _result((B, Kd + 1), torch.int32, dev, stream)
     if length is None:
-        length = torch.empty((B,), dtype=torch.int32, device=dev)
+        length = _result((B,), torch.int32, dev, stream)
     prm = Sampling(float(temperature), float(top_p), int(top_k), float(min_p))
     need = vw4_workspace_bytes(OP_REJECTION_TOPK, B, Kd, Kt)
     ws = _workspace(workspace, need, dev, stream)
@@ -635,7 +644,7 @@ class PreparedAppend(_Prepared):
             raise ValueError("x must be float32 or bfloat16 [B*R, (Hq + 2 Hkv) * D] with "
                              "contiguous rows")
         if q_out is None:
-            q_out = torch.empty((B, R, Hq, D), dtype=torch.bfloat16, device=x.device)
+            q_out = _result((B, R, Hq, D), torch.bfloat16, x.device, stream)
         ldq = _rows(q_out, torch.bfloat16, (B, R, Hq, D), "q_out")
         _need(seq_lens, torch.int32, (B,), "seq_lens")
         rot = 0
@@ -677,7 +686,7 @@ class PreparedAttn(_Prepared):
             raise ValueError("q must be [B, R, Hq, D] of the cache's batch and head size")
         ldq = _rows(q, torch.bfloat16, (B, R, Hq, D), "q")
         if out is None:
-            out = torch.empty((B, R, Hq, D), dtype=torch.bfloat16, device=q.device)
+            out = _result((B, R, Hq, D), torch.bfloat16, q.device, stream)
         ldo = _rows(out, torch.bfloat16, (B, R, Hq, D), "out")
         _need(lse, torch.float32, (B, R, Hq), "lse")
         _need(seq_lens, torch.int32, (B,), "seq_lens")
@@ -720,7 +729,7 @@ class PreparedLogits(_Prepared):
         B, R, V = logits.shape
         ldx = _rows(logits, torch.float32, (B, R, V), "logits")
         if out is None:
-            out = torch.empty((B, R, V), dtype=torch.float32, device=logits.device)
+            out = _result((B, R, V), torch.float32, logits.device, stream)
         ldo = _rows(out, torch.float32, (B, R, V), "out")
         _need(block_max, torch.float32, (B, R, (V + 15) // 16), "block_max")
         if R > 1 and drafts is None:

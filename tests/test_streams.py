@@ -72,3 +72,28 @@ def test_workspace_made_while_the_current_stream_is_busy():
             call()
         status()
         assert torch.equal(alone.view(torch.int16), out.view(torch.int16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call", ["attention", "append", "logits"])
+def test_results_made_while_the_current_stream_is_busy(call):
+    """A result is not made of memory that the current stream still has to write to."""
+    B, R, Hq, Hkv, D, V = 3, 8, 12, 2, 128, 50001
+    q, c, n = attn_inputs(4, [9000, 77, 5001])
+    x = torch.randn(B * R, (Hq + 2 * Hkv) * D, device="cuda")
+    logits = torch.randn(B, 1, V, device="cuda")
+    run = {"attention": lambda **kw: vw4.verify_attn(q, c, n, **kw),
+           "append": lambda **kw: vw4.verify_rope_append(x, c, n, R, Hq, **kw),
+           "logits": lambda **kw: vw4.process_logits(logits, **kw)}[call]
+    alone = run()
+    s = torch.cuda.Stream()
+    run(stream=s)  # (its workspace is there)
+    status()
+    for _ in range(3):
+        old = torch.empty_like(alone)
+        torch.cuda._sleep(20_000_000)  # about ten milliseconds
+        old.fill_(7.0)
+        del old
+        out = run(stream=s)
+        status()
+        assert torch.equal(alone.view(torch.int16), out.view(torch.int16))
