@@ -516,9 +516,12 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 mbar_wait_bounded(&full[k % ring], (k / ring) & 1, p.wait_ns, nullptr);
     } else if (n_units > 0 && warp >= kTcQ && warp < kTcPass) {
         // ------------------------------------------- queries in, finished rows out
+        // The walk over the parts is held back by the warps whose queries the products wait
+        // for, all four at head size 256, else those with rows: one that is not waited
+        // for could fall two phases of b_part behind, so it does not walk.
         const int vw = warp - kTcQ;
         int asked = -1;  // the last part whose queries were asked for
-        for (int k = 0;; ++k) {
+        for (int k = 0; S::kQSmem || vw < row_warps; ++k) {
             if (!warp_wait(&b_part[k & 7], k >> 3)) break;
             const bool more = k < s_parts;
             if (more) {
