@@ -469,7 +469,8 @@ VW4_API vw4_status vw4_rejection_row_records(const void* workspace_dev, size_t w
  * k_dev, v_dev  16-byte aligned; every stride a multiple of 16 bytes.
  * block_table_dev  int32 [B][table_stride], table_stride >= max_blocks.
  *             Entries beyond a sequence's length are not read.
- * k_scale_dev, v_scale_dev  fp32 [Hkv], e4m3 only; NULL = 1.
+ * k_scale_dev, v_scale_dev  fp32 [Hkv], e4m3 only, of either sign or zero;
+ *             NULL = 1.
  */
 typedef struct vw4_kv_cache {
     int32_t dtype, page_size, num_pages, Hkv, D, max_blocks;

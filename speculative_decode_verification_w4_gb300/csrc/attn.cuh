@@ -77,6 +77,12 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The factor of an e4m3 cache's scores is |k_scale| (its sign goes to the queries, so that
+// the running maximum is that of the true scores), and at least this: times minus infinity,
+// what is masked, it must not be NaN.  Scores are below 2^32 there, so a smaller factor
+// gives the same weights, all 1.
+constexpr float kMinFactor = 1.17549435e-38f;
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -530,9 +536,10 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
             for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
             const float ks = F8 && p.k_scale ? __ldg(p.k_scale + h) : 1.f;
             if (F8) {
-                // The queries become f16 under a power of two per row that puts the
-                // row's largest magnitude into [2^14, 2^15): exact for every value down
-                // to 2^-31 of it (bf16 has 8 significant bits, f16 11 and subnormals).
+                // The queries become f16 under a power of two per row that puts the row's
+                // largest magnitude into [2^14, 2^15), and the sign of the head's scale: exact
+                // for every value down to 2^-31 of it (bf16 has 8 significant bits, f16 11
+                // and subnormals).
                 // Within 16 dimensions the order is that of the byte loads of K below.
                 for (int r = wk; r < S::kRows; r += S::kWarps) {
                     uint32_t* row = reinterpret_cast<uint32_t*>(smem + S::kOffQ + qslot * S::kQ);
@@ -553,7 +560,8 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
                     const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
                     int sh = ex == 0 || ex == 255 ? 0 : 127 + 14 - ex;  // amax * 2^sh in [2^14, 2^15)
                     sh = max(-126, min(126, sh));
-                    const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+                    const float up = copysignf(
+                        __uint_as_float(static_cast<uint32_t>(127 + sh) << 23), ks);
                     if (lane == 0)
                         s_rs[qslot * S::kRows + r] =
                             __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
@@ -576,8 +584,11 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
                 l[k] = 0.f;
                 ar[k] = attn_row(p, td.g, r0 + 8 * k);
                 pr[k] = ar[k].live ? td.p0 + ar[k].i : -1;
-                c2[k] = p.scale * kLog2e * ks;
-                if (F8) c2[k] *= s_rs[qslot * S::kRows + r0 + 8 * k];
+                c2[k] = p.scale * kLog2e * fabsf(ks);
+                if (F8) {
+                    c2[k] *= s_rs[qslot * S::kRows + r0 + 8 * k];
+                    if (c2[k] < kMinFactor) c2[k] = kMinFactor;  // (NaN stays)
+                }
             }
         }
         const bool edge = td.flags & kUnitEdge;

@@ -220,12 +220,12 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
 
     // An item's queries to their place.  e4m3: as two terms (see above); a row with an
     // infinity or NaN is made NaN, for e4m3 has no infinity.
-    auto q_scale = [&](uint32_t largest, const AttnUnit& d, int r, bool keep) {
+    auto q_scale = [&](uint32_t largest, const AttnUnit& d, int r, bool keep, uint32_t sign) {
         const int ex = static_cast<int>(largest >> 7);  // of the largest magnitude, bf16 bits
         int sh = ex == 0 || ex == 255 ? 0 : 127 + 7 - ex;  // to [2^7, 2^8)
         sh = max(-126, min(126, sh));
         if (keep) s_rs[F8 ? d.seg & 7 : 0][F8 ? r : 0] = static_cast<int8_t>(sh);
-        return ex == 255 ? NAN : __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+        return ex == 255 ? NAN : __uint_as_float((static_cast<uint32_t>(127 + sh) << 23) | sign);
     };
     auto largest_of = [](uint32_t mx, const uint4& v) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -246,6 +246,8 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
     };
     auto queries = [&](const AttnUnit& d, int vw) {
         const int qs = d.seg % S::kNQ;
+        const uint32_t sign =
+            F8 && p.k_scale && __ldg(p.k_scale + d.g / p.row_blocks) < 0.f ? 0x80000000u : 0u;
         auto source = [&](const AttnRow& row) {
             return reinterpret_cast<const uint4*>(p.q +
                                                   (static_cast<long long>(d.b) * p.R + row.i) * p.ldq +
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                     if (r >= rows) break;
                     const uint32_t mx = __reduce_max_sync(0xffffffffu, largest_of(0u, v[k]));
                     uint32_t hi[2], lo[2];
-                    two_terms(v[k], q_scale(mx, d, r, lane == 0), hi, lo);
+                    two_terms(v[k], q_scale(mx, d, r, lane == 0, sign), hi, lo);
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
                         *reinterpret_cast<uint2*>(
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 uint32_t mx = 0;
 #pragma unroll
                 for (int k = 0; k < D / 8; ++k) mx = largest_of(mx, v[k]);
-                up = q_scale(mx, d, r, r < ROWS);
+                up = q_scale(mx, d, r, r < ROWS, sign);
             }
             if (reused && !warp_wait(&b_qe[qs], d.seg / S::kNQ - 1)) return false;
             tc_fence_after();
@@ -771,9 +773,10 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                 pr = row.live ? td.p0 + row.i : -1;
                 c2 = p.scale * kLog2e;
                 if (F8) {
-                    if (p.k_scale) c2 *= __ldg(p.k_scale + h);
+                    if (p.k_scale) c2 *= fabsf(__ldg(p.k_scale + h));
                     c2 *= __uint_as_float(
                         static_cast<uint32_t>(127 - s_rs[F8 ? td.seg & 7 : 0][F8 ? min(r, ROWS - 1) : 0]) << 23);
+                    if (c2 < kMinFactor) c2 = kMinFactor;  // (NaN stays)
                 }
                 l = 0.f;
             }

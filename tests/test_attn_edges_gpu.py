@@ -33,3 +33,30 @@ def test_many_parts_of_one_tile(R, G, D, kv):
     for b in range(0, B, 113):
         o, _, t, _ = attention64(q[b].double(), k64[b], v64[b], lens[b], D ** -0.5, 0, 0, kv)
         check_close(first[b], o, t, f"sequence {b}")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("R,G", [(1, 6), (3, 2), (8, 6), (16, 8)])
+@pytest.mark.parametrize("window", [0, 50])
+def test_scales_of_any_sign(window, R, G, D):
+    """A key head of scale 0 weighs its keys alike; a negative scale turns the scores
+    round; a scale may be as small as fp32 has them."""
+    lens, scales = [1, 200, 3, 5000], [0.03, 0.0, -0.05, 1e-42, -0.0]
+    c, k64, v64 = make_cache(95, lens, 16, len(scales), D, "e4m3")
+    new = torch.tensor(scales)
+    old = c.k_scale.cpu().double()
+    k64 = [k / old[:, None] * new.double()[:, None] for k in k64]
+    c.k_scale.copy_(new)
+    vs = torch.tensor([0.02, -0.04, 0.0, 0.03, 0.01])
+    v64 = [v / c.v_scale.cpu().double()[:, None] * vs.double()[:, None] for v in v64]
+    c.v_scale.copy_(vs)
+    g = torch.Generator().manual_seed(D)
+    q = (torch.randn(len(lens), R, G * len(scales), D, generator=g) * 3).to(torch.bfloat16)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    lse = torch.empty(q.shape[:3], device="cuda")
+    out = vw4.verify_attn(q.cuda(), c, n, window=window, lse=lse)
+    status()
+    for b in range(len(lens)):
+        o, l, t, tl = attention64(q[b].double(), k64[b], v64[b], lens[b], D ** -0.5, window, 0, "e4m3")
+        check_close(out[b], o, t, f"sequence {b} out")
+        check_close(lse[b], l, tl, f"sequence {b} lse")
