@@ -498,7 +498,8 @@ typedef struct vw4_kv_cache {
  *   pos * inv_freq[j] in the planes (j, j + rot/2), or (2j, 2j + 1) when
  *   adjacent = 1:  (a, c) -> (a cos - c sin, c cos + a sin)
  *   queries -> q_dev as bf16; keys and values -> the token's cache slot, as
- *   bf16, or as e4m3 of value / scale (nearest, at most 448 in magnitude).
+ *   bf16, or as e4m3 of value / scale (nearest, at most 448 in magnitude; of
+ *   a finite value 0 where the scale is 0).
  * The angle is computed in 64 bits and reduced before it is rounded.
  *
  * x_dev, ldx  fp32 (x_bf16 = 0) or bf16 (1) [B*R][ldx], ldx >= (Hq+2 Hkv) D.

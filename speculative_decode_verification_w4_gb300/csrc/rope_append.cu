@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
             C* dst = static_cast<C*>(is_k ? p.k : p.v) + slot + static_cast<long long>(hk) * p.head_stride;
             if (F8) {
                 const float* sp = is_k ? p.k_scale : p.v_scale;
-                const float sc = sp ? __ldg(sp + hk) : 1.f;
+                float sc = sp ? __ldg(sp + hk) : 1.f;
+                if (sc == 0.f) sc = INFINITY;  // zeros: what such a head reads back
 #pragma unroll
                 for (int k = 0; k < 2 * U; ++k) v[k] = __fdiv_rn(v[k], sc);
             }
