@@ -565,6 +565,9 @@ class KVCache:
         if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
                 (block_table.shape[1] > 1 and block_table.stride(1) != 1):
             raise ValueError("block_table must be int32 [B, max_blocks] with contiguous rows")
+        if block_table.shape[0] > 1 and block_table.stride(0) < block_table.shape[1]:
+            raise ValueError("block_table: the sequences' rows overlap (an expanded row is one "
+                             "row of memory; make it contiguous)")
         pages, page, hkv, d = k.shape
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None and (t.dtype != torch.float32 or t.shape != (hkv,)

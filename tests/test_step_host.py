@@ -1,0 +1,31 @@
+"""What the Python binding of the calls between the verify GEMMs refuses before it looks at
+the device (host tensors: a later check would refuse those too, with another message)."""
+import pytest
+import torch
+
+import speculative_decode_verification_w4_gb300 as vw4
+
+
+def pages():
+    return torch.zeros(10, 16, 2, 64, dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("table", [
+    torch.zeros(1, 4, dtype=torch.int32).expand(3, 4),
+    torch.zeros(64, dtype=torch.int32).as_strided((3, 4), (2, 1)),
+])
+def test_block_table_of_overlapping_rows(table):
+    """Its rows are not max_blocks apart, and the descriptor's stride is at least that: the
+    kernels would read past them."""
+    with pytest.raises(ValueError, match="overlap"):
+        vw4.KVCache(pages(), pages(), table)
+
+
+@pytest.mark.parametrize("table", [
+    torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, 9, dtype=torch.int32)[:, :4],
+    torch.zeros(4, dtype=torch.int32).as_strided((1, 4), (0, 1)),
+    torch.zeros(3, 1, dtype=torch.int32),
+])
+def test_block_table_rows_that_are_taken(table):
+    with pytest.raises(ValueError, match="CUDA"):
+        vw4.KVCache(pages(), pages(), table)
