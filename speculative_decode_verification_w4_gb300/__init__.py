@@ -267,9 +267,11 @@ def _workspace(ws, nbytes, device, stream):
         ws = _default_ws.setdefault(key, Workspace(device))
     if isinstance(ws, Workspace):
         return ws.get(nbytes, stream)
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
     if ws.numel() * ws.element_size() < nbytes:
         raise VW4Error(6, "workspace", f"need {nbytes} bytes")
-    return ws
+    return ws if ws.dtype == torch.uint8 else ws.view(-1).view(torch.uint8)
 
 
 def make_weight(fmt: int, q: torch.Tensor, scales: torch.Tensor, tensor_scale: float = 1.0,

@@ -29,3 +29,18 @@ def test_block_table_of_overlapping_rows(table):
 def test_block_table_rows_that_are_taken(table):
     with pytest.raises(ValueError, match="CUDA"):
         vw4.KVCache(pages(), pages(), table)
+
+
+def test_workspace_tensors():
+    """A tensor as a workspace: on the call's device, without gaps, counted in bytes
+    (the calls hand its address and size on as they are)."""
+    gpu, cpu = torch.device("cuda", 0), torch.device("cpu")
+    with pytest.raises(ValueError, match="cuda:0"):
+        vw4._workspace(torch.empty(4096, dtype=torch.uint8), 4096, gpu, None)
+    with pytest.raises(ValueError, match="contiguous"):
+        vw4._workspace(torch.empty(8192, dtype=torch.uint8)[::2], 4096, cpu, None)
+    with pytest.raises(vw4.VW4Error):
+        vw4._workspace(torch.empty(1023), 4096, cpu, None)
+    ws = torch.empty(32, 32)
+    got = vw4._workspace(ws, 4096, cpu, None)
+    assert got.data_ptr() == ws.data_ptr() and got.numel() == 4096
