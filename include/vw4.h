@@ -545,7 +545,7 @@ VW4_API vw4_status verify_rope_append(const vw4_append* a, void* stream);
  * (infinities and NaN included).
  *
  * q_dev, ldq  bf16 [B*R][ldq], ldq >= Hq D.
- * out_dev, ldo  bf16 [B*R][ldo].
+ * out_dev, ldo  bf16 [B*R][ldo], Hq D <= ldo <= 2^31.
  * lse_dev     fp32 [B*R][Hq], or NULL.
  * seq_lens_dev  int32 [B]: tokens in the cache, the R rows included.
  * B 1..16384, R 1..16, Hq a multiple of Hkv, at most 256; window >= 0, sinks >= 0 (0 unless

@@ -369,12 +369,15 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
         // The rows leave through 4 KB of shared memory a warp, 128 bytes of each of
         // the 32 rows at a time (fp32 partial: 32 columns, bf16: 64), so that eight
         // lanes write one row's line.
+        // Rows are passed round as offsets in 16 bytes (they start on 16) from the sequence's
+        // first row, or the partial's: 15 strides of at most 2^32 bytes fit 32 bits.
+        uint8_t* dst_base =
+            td.slot >= 0
+                ? reinterpret_cast<uint8_t*>(p.partial + static_cast<long long>(td.slot) * ROWS * (D + 2))
+                : reinterpret_cast<uint8_t*>(p.out + static_cast<long long>(td.b) * p.R * p.ldo);
         const long long dst_row =
-            td.slot >= 0 ? (static_cast<long long>(td.slot) * ROWS * (D + 2) + static_cast<long long>(r) * D) * 4
-                         : (orow * p.ldo + static_cast<long long>(row.hq) * D) * 2;
-        uint8_t* dst_base = td.slot >= 0 ? reinterpret_cast<uint8_t*>(p.partial)
-                                         : reinterpret_cast<uint8_t*>(p.out);
-        // the rows that this lane writes, as offsets in 16 bytes (rows start on 16)
+            td.slot >= 0 ? static_cast<long long>(r) * (D * 4)
+                         : (row.i * p.ldo + static_cast<long long>(row.hq) * D) * 2;
         const uint32_t mine = live ? static_cast<uint32_t>(dst_row >> 4) : 0xffffffffu;
         uint32_t to[8];
 #pragma unroll

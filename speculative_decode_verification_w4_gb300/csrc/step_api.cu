@@ -118,7 +118,7 @@ VW4_API vw4_status verify_attn(const vw4_attn* a, void* workspace_dev, size_t ws
         return VW4_ERR_INVALID_ARG;
     if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return VW4_ERR_INVALID_ARG;
     const int64_t width = static_cast<int64_t>(a->Hq) * c.D;
-    if (a->ldq < width || a->ldo < width) return VW4_ERR_INVALID_ARG;
+    if (a->ldq < width || a->ldo < width || a->ldo > kMaxOutStride) return VW4_ERR_INVALID_ARG;
     if (misaligned(a->q_dev, 16) || misaligned(a->out_dev, 16) || misaligned(a->lse_dev, 4) ||
         misaligned(a->seq_lens_dev, 4) || a->ldq % 8 || a->ldo % 8)
         return VW4_ERR_ALIGN;

@@ -48,6 +48,7 @@ constexpr int kMaxVerifyRows = 16; // dense verify rows per call: two n-tiles
 constexpr int kMaxSeg = 128;       // routed (token, expert) pairs per call: 16 tokens x top-8
 constexpr int kMaxSeqs = 16384;    // sequences of an attention, append or logits call
 constexpr int kMaxHeads = 256;     // query heads of an attention or append call
+constexpr long long kMaxOutStride = 1ll << 31;  // elements between rows of an attention's output
 constexpr int kTileRows = 128;     // weight rows per tile
 constexpr int kStageK = 256;       // k elements per pipeline stage
 constexpr int kMinUnitsPerCta = 4; // tile-aligned split-K: at least this many stages per part

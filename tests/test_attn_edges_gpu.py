@@ -60,3 +60,26 @@ def test_scales_of_any_sign(window, R, G, D):
         o, l, t, tl = attention64(q[b].double(), k64[b], v64[b], lens[b], D ** -0.5, window, 0, "e4m3")
         check_close(out[b], o, t, f"sequence {b} out")
         check_close(lse[b], l, tl, f"sequence {b} lse")
+
+
+@pytest.mark.parametrize("R,G,D,kv", [(2, 16, 64, "e4m3"), (2, 4, 128, "bf16")])
+def test_output_rows_far_apart(R, G, D, kv):
+    """Output rows 2 GiB apart, over more than 64 GiB in all: the bits of a compact output."""
+    B, ldo = 34 // R + 1, 1 << 30
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 76 GiB of device memory")
+    lens = [9000] + [20 + 3 * b for b in range(B - 1)]
+    c, _, _ = make_cache(96, lens, 16, 1, D, kv)
+    g = torch.Generator().manual_seed(D)
+    q = torch.randn(B, R, G, D, generator=g).to(torch.bfloat16).cuda()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want = vw4.verify_attn(q, c, n)
+    flat = torch.empty((B * R - 1) * ldo + G * D, dtype=torch.bfloat16, device="cuda")
+    out = flat.as_strided((B, R, G, D), (R * ldo, ldo, D, 1))
+    out.fill_(7.0)
+    vw4.verify_attn(q, c, n, out=out)
+    status()
+    same = torch.equal(out.view(torch.int16), want.view(torch.int16))
+    del flat, out
+    torch.cuda.empty_cache()
+    assert same

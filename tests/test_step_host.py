@@ -1,5 +1,7 @@
 """What the Python binding of the calls between the verify GEMMs refuses before it looks at
 the device (host tensors: a later check would refuse those too, with another message)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -44,3 +46,17 @@ def test_workspace_tensors():
     ws = torch.empty(32, 32)
     got = vw4._workspace(ws, 4096, cpu, None)
     assert got.data_ptr() == ws.data_ptr() and got.numel() == 4096
+
+
+def test_output_rows_too_far_apart():
+    """verify_attn addresses a sequence's output rows by 32-bit offsets in 16 bytes."""
+    from speculative_decode_verification_w4_gb300 import build
+    build.build()
+    kv = vw4.KVDesc(vw4.KV_BF16, 16, 10, 2, 128, 4, 16 * 256, 256, 128, 4, 0x10000, 0x20000,
+                    0x30000, None, None)
+
+    def call(ldo):  # (a workspace of one byte is refused next)
+        a = vw4.AttnArgs(kv, 0x1000, 0x2000, None, 0x3000, 1024, ldo, 2, 3, 8, 0, 0, 0.1)
+        return vw4.load_library().verify_attn(ctypes.byref(a), 0x100000, 1, None)
+    assert call(1024) == 6 and call(1 << 31) == 6
+    assert call((1 << 31) + 8) == 1
