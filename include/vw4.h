@@ -551,7 +551,8 @@ VW4_API vw4_status verify_rope_append(const vw4_append* a, void* stream);
  * B 1..16384, R 1..16, Hq a multiple of Hkv, at most 256; window >= 0, sinks >= 0 (0 unless
  * window > 0); scale > 0 and finite.
  * Precision: scores, softmax statistics and sums in fp32; the weights enter
- * the value product as bf16 (e4m3 caches: as f16).  The queries of an e4m3
+ * the value product as bf16 (e4m3 caches: as f16, off by at most 2^-11 of
+ * themselves or 2^-31 of the largest).  The queries of an e4m3
  * cache enter the score product under an exact power of two per row: up to
  * 16 rows a key head (R * Hq / Hkv) as f16, exact down to 2^-31 of the row's
  * largest magnitude; with more rows as the sum of two e4m3 values, off by at

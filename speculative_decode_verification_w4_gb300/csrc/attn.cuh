@@ -83,6 +83,13 @@ __device__ __forceinline__ float ex2(float x) {
 // gives the same weights, all 1.
 constexpr float kMinFactor = 1.17549435e-38f;
 
+// The f16 weights of e4m3 caches carry a power of two, and their sum with them: f16 ends at
+// 2^-25, and under one large weight thousands of small ones are a part of the output that
+// shows (a token of weight 1 whose values are zeros over a thousand of 2^-26: all of it).
+// Weights of at most 2^12, or 2^8 times 2^6 where the maximum lags behind (attn_tc.cuh),
+// leave f16 room for what the exponents' rounding adds to very large scores.
+constexpr float kTailBits = 12.f, kTailBitsTc = 6.f;
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -674,7 +681,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
                 corr[k] = mn == m[k] ? 1.f : ex2((m[k] - mn) * c2[k]);
                 grew |= mn != m[k];
                 m[k] = mn;
-                const float mc = mn == -INFINITY ? 0.f : mn * c2[k];
+                const float mc = mn == -INFINITY ? 0.f : mn * c2[k] - (F8 ? kTailBits : 0.f);
                 float sum = 0.f;
 #pragma unroll
                 for (int n = 0; n < S::kKW / 8; ++n) {
@@ -694,8 +701,8 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
                 }
             }
             // P V.  The weights go to the tensor cores in the cache's operand type (bf16,
-            // or f16 for an e4m3 cache): each is off by at most half a step, and the sum l
-            // is of the unrounded ones.
+            // or f16 for an e4m3 cache): each is off by at most half a step, or 2^-37 of the
+            // largest where f16 ends, and the sum l is of the unrounded ones.
             auto load_v = [&](int n, int db, uint32_t* bv) {
                 // bv: operand registers of two 8-column blocks, keys (2t, 2t+1) and + 8 each
                 const int row = k0 + n * 16 + lr + (lm & 1) * 8;
@@ -808,7 +815,8 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kThreads, MINB)
         if (t4 == 0) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                s_m[wk * S::kRows + r0 + 8 * k] = m[k] == -INFINITY ? -INFINITY : m[k] * c2[k];
+                s_m[wk * S::kRows + r0 + 8 * k] =
+                    m[k] == -INFINITY ? -INFINITY : m[k] * c2[k] - (F8 ? kTailBits : 0.f);
                 s_l[wk * S::kRows + r0 + 8 * k] = l[k];
             }
         }

@@ -28,8 +28,8 @@
 // e4m3 terms, its nearest value and that of the rest: 4 + 4 significant bits, so
 // exact for a bf16 value down to 2^-10 of the largest and off by at most 2^-17 of
 // the largest below.  For the weights two such terms would not do: a long tail of
-// small weights under one large one lies below their range.  So P is f16 and V
-// becomes f16; converting K as well was bound by that step.
+// small weights under one large one lies below their range.  So P is f16, times 2^6,
+// and V becomes f16; converting K as well was bound by that step.
 //
 // What bounds it.  bf16: the bytes (8 key heads of 128, 24 rows each, 32 sequences of
 // 4000 .. 8000 tokens: 130 us, 87 % of the copy rate).  e4m3 halves the bytes but not
@@ -40,7 +40,7 @@
 //
 // The running maximum that the exponents use follows the true one lazily: O is
 // rescaled only when a row's maximum grew by more than 2^8 (its weights are then
-// at most 2^8, harmless in bf16, f16 and the fp32 sum).
+// at most 2^8, e4m3 caches 2^14, harmless in bf16, f16 and the fp32 sum).
 #pragma once
 #include "attn.cuh"
 
@@ -858,7 +858,7 @@ __global__ void __launch_bounds__(AttnTcShape<D, F8, ROWS>::kThreads, 1)
                     tmem_st32(tO + c, y);
                 }
             }
-            const float mc = m == -INFINITY ? 0.f : m * c2;
+            const float mc = m == -INFINITY ? 0.f : m * c2 - (F8 ? kTailBitsTc : 0.f);
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll 1
             for (int c = c0; c < c1; c += CW) {

@@ -83,3 +83,40 @@ def test_output_rows_far_apart(R, G, D, kv):
     del flat, out
     torch.cuda.empty_cache()
     assert same
+
+
+@pytest.mark.parametrize("at", [53, 990])
+@pytest.mark.parametrize("R,Hq,D", [(1, 4, 64), (2, 8, 128), (1, 3, 256), (8, 6, 64), (4, 6, 128),
+                                    (16, 8, 128), (8, 6, 256)])
+def test_tail_far_below_one_weight(R, Hq, D, at):
+    """A token of weight near 1 and value zero over a thousand of weight 2^-26: the output is
+    the tail's alone.  e4m3 caches, items inside one thread block (sequences of the same
+    pages).  Off by half a step of bf16, half a step of f16 of every weight and 2^-31 of
+    the largest, and the scores' error (delta of step_util.attention64)."""
+    B, n, page = 640, 1000, 8
+    c, k64, v64 = make_cache(97, [n], page, 1, D, "e4m3")
+    one = torch.ones(1, device="cuda")
+    c.k.copy_(torch.zeros(c.k.shape, device="cuda").to(c.k.dtype))
+    c.v.copy_((torch.rand(c.v.shape, device="cuda") * 100 + 100).to(c.v.dtype))
+    row = c.block_table[0].cpu().tolist()
+    c.k[row[at // page], at % page, 0] = torch.full((D,), 18 / (0.25 * D ** 0.5) / 0.05,
+                                                    device="cuda").to(c.k.dtype)
+    c.v[row[at // page], at % page, 0] = (one * 0).to(c.v.dtype)
+    c.k_scale.copy_(one * 0.05)
+    k = c.k.float().cpu().double()[row].reshape(-1, 1, D)[:n] * float(c.k_scale[0])
+    v = c.v.float().cpu().double()[row].reshape(-1, 1, D)[:n] * float(c.v_scale[0])
+    cache = vw4.KVCache(c.k, c.v, c.block_table.repeat(B, 1), c.k_scale, c.v_scale)
+    q = torch.full((B, R, Hq, D), 0.25, dtype=torch.bfloat16, device="cuda")
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    lse = torch.empty(B, R, Hq, device="cuda")
+    out = vw4.verify_attn(q, cache, lens, lse=lse)
+    status()
+    want, l, _, tl = attention64(q[0].double().cpu(), k, v, n, D ** -0.5, 0, 0, "e4m3")
+    score = float(0.25 * k[at].sum() * D ** -0.5)
+    assert 17 < score < 20 and 0 < float(want[-1].max()) < 1e-3  # (earlier rows may not see it)
+    delta = 2 * D * 2.0 ** -24 * score + 2.0 ** -22 * (2 * score + 1)
+    if R * Hq > 16:
+        delta += 2.0 ** -17 * 0.25 * float(k[at].sum()) * D ** -0.5
+    tol = (2 ** -8 + 2 ** -11 + 2 * delta) * want + n * 2.0 ** -31 * float(v.max())
+    check_close(out, want.expand(B, -1, -1, -1), tol.expand(B, -1, -1, -1), "out")
+    check_close(lse, l.expand(B, -1, -1), tl.expand(B, -1, -1), "lse")
