@@ -120,3 +120,49 @@ def test_tail_far_below_one_weight(R, Hq, D, at):
     tol = (2 ** -8 + 2 ** -11 + 2 * delta) * want + n * 2.0 ** -31 * float(v.max())
     check_close(out, want.expand(B, -1, -1, -1), tol.expand(B, -1, -1, -1), "out")
     check_close(lse, l.expand(B, -1, -1), tl.expand(B, -1, -1), "lse")
+
+
+@pytest.mark.parametrize("kv,D", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("e4m3", 64),
+                                  ("e4m3", 128), ("e4m3", 256)])
+@pytest.mark.parametrize("R,Hq", [(5, 2), (16, 1), (16, 8), (8, 3), (4, 16)])
+@pytest.mark.parametrize("n,window,sinks", [(203, 40, 0), (203, 40, 5), (130, 0, 0), (7000, 3000, 4),
+                                            (9000, 0, 0)])
+def test_infinite_values_where_they_are_seen(n, window, sinks, R, Hq, kv, D):
+    """Infinities and NaN in the values alone: the rows that see one have it, in its
+    dimensions and no others; other rows have none.  Short ones, and ones whose parts
+    are joined."""
+    c, k64, v64 = make_cache(98, [n], 16, 1, D, kv)
+    inf, nan = float("inf"), float("nan")
+    p0 = n - R
+    bad = {n - 1: (1, inf), n - 2: (2, -inf), n - R // 2: (3, nan), n // 2: (4, inf),
+           p0 + 1: (5, -inf)}
+    if window:  # seen by the first row alone, by the rows up to the third, by none
+        bad[p0 - window + 1] = (6, inf)
+        bad[p0 - window + 3] = (7, -inf)
+        bad[p0 - window] = (8, inf)
+    if sinks:
+        bad[sinks - 1], bad[sinks] = (9, inf), (10, inf)
+    clean, dirty = v64[0].clone(), v64[0].clone()
+    for j, (d, x) in bad.items():
+        dims = [d, D // 2 + d, D - 20]
+        x = nan if kv == "e4m3" else x
+        pg = int(c.block_table[0, j // 16])
+        for e in dims:
+            c.v[pg, j % 16, 0, e] = torch.tensor(x, device="cuda").to(c.v.dtype)
+            clean[j, 0, e], dirty[j, 0, e] = 0.0, x
+    g = torch.Generator().manual_seed(n)
+    q = torch.randn(1, R, Hq, D, generator=g).to(torch.bfloat16)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    lse = torch.empty(1, R, Hq, device="cuda")
+    out = vw4.verify_attn(q.cuda(), c, lens, window=window, sinks=sinks, lse=lse)
+    status()
+    args = (n, D ** -0.5, window, sinks, kv)
+    want, l, t, tl = attention64(q[0].double(), k64[0], clean, *args)
+    special = attention64(q[0].double(), k64[0], dirty, *args)[0]
+    fin = torch.isfinite(special)
+    assert not fin[-1].all() and fin.any()
+    got = out[0].double().cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(special))
+    assert torch.equal(got[torch.isinf(special)], special[torch.isinf(special)])
+    check_close(got[fin], want[fin], t[fin], "finite outputs")
+    check_close(lse[0], l, tl, "lse")
