@@ -77,9 +77,9 @@ typedef enum {
 #define VW4_DEV_BOUNDS         0x20u /* checks build only: an index that came from data was
                                         out of range (a library bug): a memory access it
                                         addressed was skipped; a token id is still written */
-#define VW4_DEV_BAD_PAGE       0x40u /* a cache page id outside [0, num_pages), or a length
-                                        beyond the block table: those tokens read as zero
-                                        keys and values, and are not written            */
+#define VW4_DEV_BAD_PAGE       0x40u /* a cache page id outside [0, num_pages): its tokens
+                                        read as zero keys and values, and are not written;
+                                        or a length beyond the block table              */
 
 /* A block-quantized weight matrix [N][K] (see the format notes above). */
 typedef struct vw4_weight {
@@ -547,7 +547,10 @@ VW4_API vw4_status verify_rope_append(const vw4_append* a, void* stream);
  * q_dev, ldq  bf16 [B*R][ldq], ldq >= Hq D.
  * out_dev, ldo  bf16 [B*R][ldo], Hq D <= ldo <= 2^31.
  * lse_dev     fp32 [B*R][Hq], or NULL.
- * seq_lens_dev  int32 [B]: tokens in the cache, the R rows included.
+ * seq_lens_dev  int32 [B]: tokens in the cache, the R rows included.  A length
+ *             beyond the block table sets VW4_DEV_BAD_PAGE and is cut to the
+ *             table, whose last tokens then are the rows' positions (the cache
+ *             append keeps the positions and drops the tokens beyond).
  * B 1..16384, R 1..16, Hq a multiple of Hkv, at most 256; window >= 0, sinks >= 0 (0 unless
  * window > 0); scale > 0 and finite.
  * Precision: scores, softmax statistics and sums in fp32; the weights enter
