@@ -174,43 +174,13 @@ unsigned long long wait_limit_ns() { return g_wait_ns; }
 
 int encode_map(CUtensorMap* map, bool bf16, int n, const void* base, const uint64_t* dims,
                const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw) {
-    struct Key {
-        const void* base;
-        uint64_t d[5], s[5];
-        uint32_t b[5];
-        int n, bf16, sw;
-    };
-    constexpr int kSlots = 64;
-    static Key keys[kSlots];
-    static CUtensorMap maps[kSlots];
-    static int next = 0;
-    static std::mutex mu;
-    Key key;
-    memset(&key, 0, sizeof key);
-    key.base = base;
-    key.n = n;
-    key.bf16 = bf16;
-    key.sw = static_cast<int>(sw);
     const uint64_t es = bf16 ? 2 : 1;
-    for (int i = 0; i < n; ++i) {
-        key.d[i] = dims[i];
-        key.s[i] = i > 0 ? strides[i - 1] * es : es;
-        key.b[i] = box[i];
-    }
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        for (int i = 0; i < kSlots; ++i)
-            if (memcmp(&keys[i], &key, sizeof key) == 0) {
-                *map = maps[i];
-                return VW4_OK;
-            }
-    }
     cuuint64_t d[5], st[4];
     cuuint32_t b[5], one[5] = {1, 1, 1, 1, 1};
     for (int i = 0; i < n; ++i) {
-        d[i] = key.d[i];
-        b[i] = key.b[i];
-        if (i > 0) st[i - 1] = key.s[i];
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i > 0) st[i - 1] = strides[i - 1] * es;
     }
     // 64-byte promotion: a head's part of a token may be no longer, and what lies next to it
     // belongs to other heads' CTAs (e4m3, 8 heads of 128 next to each other, one row a
@@ -226,10 +196,6 @@ int encode_map(CUtensorMap* map, bool bf16, int n, const void* base, const uint6
         g_last_error = buf;
         return VW4_ERR_CUDA;
     }
-    std::lock_guard<std::mutex> lk(mu);
-    keys[next] = key;
-    maps[next] = *map;
-    next = (next + 1) % kSlots;
     return VW4_OK;
 }
 

@@ -266,7 +266,7 @@ cudaError_t launch_attn_d128(const AttnParams& p, const AttnMaps& maps, bool f8,
 cudaError_t launch_attn_d256(const AttnParams& p, const AttnMaps& maps, bool f8, int rows, int* grid,
                              int sms, cudaStream_t s);
 // A tensor map of n dimensions (element type u8 or bf16, sizes and strides in
-// elements of the type, strides of dimensions 1..), cached by its contents.
+// elements of the type, strides of dimensions 1..).
 int encode_map(CUtensorMap* map, bool bf16, int n, const void* base, const uint64_t* dims,
                const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw);
 

@@ -166,3 +166,29 @@ def test_infinite_values_where_they_are_seen(n, window, sinks, R, Hq, kv, D):
     assert torch.equal(got[torch.isinf(special)], special[torch.isinf(special)])
     check_close(got[fin], want[fin], t[fin], "finite outputs")
     check_close(lse[0], l, tl, "lse")
+
+
+def test_many_caches_in_turn():
+    """Ninety layers' caches of one shape, and one that takes another's memory over: every
+    call reads its own."""
+    lens, D = [40], 64
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(1, 2, 2, D, generator=g).to(torch.bfloat16)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    caches = [make_cache(200 + i, lens, 16, 1, D, "bf16") for i in range(90)]
+    calls = [vw4.PreparedAttn(q.cuda(), c, n) for c, _, _ in caches]
+    for _ in range(2):
+        for call in calls:
+            call()
+    status()
+    for call, (_, k64, v64) in zip(calls, caches):
+        o, _, t, _ = attention64(q[0].double(), k64[0], v64[0], lens[0], D ** -0.5, 0, 0, "bf16")
+        check_close(call.out[0], o, t, "out")
+    c, k64, v64 = caches[0]
+    half = vw4.KVCache(c.k[:, :8], c.v[:, :8], c.block_table.repeat_interleave(2, 1))
+    out = vw4.verify_attn(q.cuda(), half, n)  # the same memory as pages of 8, each read twice
+    status()
+    at = torch.tensor([j // 16 * 16 + j % 8 for j in range(lens[0])])
+    k, v = (torch.nan_to_num(x[0][at.clamp(max=lens[0] - 1)]) for x in (k64, v64))
+    o, _, t, _ = attention64(q[0].double(), k, v, lens[0], D ** -0.5, 0, 0, "bf16")
+    check_close(out[0], o, t, "out")
