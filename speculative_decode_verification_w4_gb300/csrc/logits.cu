@@ -24,9 +24,10 @@ constexpr uint32_t kKnown = 0x80000000u;        // count word: in the prompt
 constexpr uint32_t kDrafted = 0x40000000u;      // count word: a draft of the sequence
 constexpr uint32_t kLogitBadDraft = 0x1u;
 
-// VEC consecutive logits a thread and step, kLogitChunk vocabulary entries a block.  A row's logits are on their way while
-// the history is scanned, or while the row before is finished; its mask words a row
-// earlier still, for they decide which logits are read.
+// VEC consecutive logits a thread and step, kLogitChunk vocabulary entries a block.  The
+// first row's logits are on their way while the history is scanned; a later row's are
+// asked for all at once when the row before has been written, by then with the mask words
+// at hand that decide which of them are read.
 template <int VEC, int kLogitChunk>
 __global__ void __launch_bounds__(kLogitThreads, VEC == 4 ? 4 : 3)
     logits_kernel(const LogitsParams p, int row_step) {
