@@ -35,8 +35,9 @@ constexpr int kJoinThreads = 128;
 // share the parts of 64 columns of a row (kJoinParts).  The lanes weigh up to 32
 // partials at once and then own E columns each; the first U partials' values are on
 // their way while the weights are computed (the kernel is a chain of load latencies).
-// A kernel of its own rather than the last CTA of each item: no ticket to clear and
-// none to wait for.
+// A kernel of its own: the CTAs of an item are any run of the grid, however long, so no
+// cluster holds them, and a last arriving CTA would need tickets that the call clears.  Its
+// launch adds 2.6 us to 26.3 for 4 sequences of 8 rows, 24 heads of 256.
 constexpr int kJoinRows = 0, kJoinColumns = 1, kJoinParts = 2;
 
 template <int D, int MODE>
