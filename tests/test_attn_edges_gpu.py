@@ -192,3 +192,59 @@ def test_many_caches_in_turn():
     k, v = (torch.nan_to_num(x[0][at.clamp(max=lens[0] - 1)]) for x in (k64, v64))
     o, _, t, _ = attention64(q[0].double(), k, v, lens[0], D ** -0.5, 0, 0, "bf16")
     check_close(out[0], o, t, "out")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("R,G", [(1, 4), (8, 6)])
+def test_nothing_in_any_cache(R, G, kv):
+    """Every length zero, below zero or shorter than the rows: zeros and minus infinity."""
+    c, _, v64 = make_cache(99, [16, 16, 16], 16, 2, 128, kv)
+    q = torch.randn(3, R, 2 * G, 128, device="cuda").to(torch.bfloat16)
+    for lens in ([0, 0, 0], [-5, 0, -2 ** 31], [0, 1, 0]):
+        lse = torch.zeros(3, R, 2 * G, device="cuda")
+        out = torch.full_like(q, 7.0)
+        vw4.verify_attn(q, c, torch.tensor(lens, dtype=torch.int32, device="cuda"), out=out, lse=lse)
+        status()
+        seen = torch.zeros(3, R, dtype=torch.bool)
+        seen[1, R - 1] = lens[1] == 1  # the last row of the second sequence sees its one token
+        assert (out[~seen] == 0).all() and (lse[~seen] == float("-inf")).all()
+        if lens[1] == 1:
+            want = v64[1][0].repeat_interleave(G, 0)
+            check_close(out[1, -1], want, 2.0 ** -7 * want.abs(), "one token")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("order", ["nhd", "hnd"])
+@pytest.mark.parametrize("R,G", [(2, 4), (8, 3)])
+def test_cache_beyond_32_bits(R, G, order, kv):
+    """Pages of a cache of more than 2^32 elements: the append writes its last ones, and the
+    attention reads them."""
+    page, Hkv, D, B, n = 64, 8, 128, 2, 150
+    pages = (1 << 32) // (page * Hkv * D) + 100
+    dt = torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn
+    shape = (pages, page, Hkv, D) if order == "nhd" else (pages, Hkv, page, D)
+    k, v = (torch.empty(shape, dtype=dt, device="cuda") for _ in range(2))
+    if order == "hnd":
+        k, v = k.transpose(1, 2), v.transpose(1, 2)
+    table = torch.tensor([[pages - 1, pages - 7, 3], [pages - 3, 0, pages - 2]], dtype=torch.int32)
+    scale = None if kv == "bf16" else torch.full((Hkv,), 1 / 32, device="cuda")
+    c = vw4.KVCache(k, v, table.cuda(), scale, scale)
+    g = torch.Generator().manual_seed(R)
+    Hq, keys, values = Hkv * G, [], []
+    for at in range(0, n, 10):  # (no rotation: what is stored is what is given)
+        x = torch.randn(B * 10, (Hq + 2 * Hkv) * D, generator=g).to(torch.bfloat16)
+        vw4.verify_rope_append(x.cuda(), c, torch.full((B,), at + 10, dtype=torch.int32, device="cuda"),
+                               10, Hq)
+        rows = x.view(B, 10, Hq + 2 * Hkv, D)
+        keys.append(rows[:, :, Hq:Hq + Hkv])
+        values.append(rows[:, :, Hq + Hkv:])
+    stored = [torch.cat(t, 1) for t in (keys, values)]
+    if kv == "e4m3":
+        stored = [(t.float() * 32).clamp(-448, 448).to(dt).float() / 32 for t in stored]
+    q = torch.randn(B, R, Hq, D, generator=g).to(torch.bfloat16)
+    out = vw4.verify_attn(q.cuda(), c, torch.full((B,), n, dtype=torch.int32, device="cuda"))
+    status()
+    for b in range(B):
+        o, _, t, _ = attention64(q[b].double(), stored[0][b].double(), stored[1][b].double(), n,
+                                 D ** -0.5, 0, 0, kv)
+        check_close(out[b], o, t, f"sequence {b}")
