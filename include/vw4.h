@@ -596,7 +596,7 @@ VW4_API vw4_status verify_attn(const vw4_attn* a, void* workspace_dev, size_t ws
  * accept_rejection_blockmax takes).
  *
  * x_dev, ldx  fp32 [B*R][ldx]; out_dev, ldo  fp32 [B*R][ldo], may be x_dev
- *             (then ldo = ldx).
+ *             (then ldo = ldx), and must not overlap it otherwise.
  * block_max_dev  fp32 [B*R][ceil(V/16)], or NULL.
  * drafts_dev  int32 [B][R-1] (NULL when R = 1).
  * history_dev int32 [B][hist_stride] (NULL: none), hist_max columns;
