@@ -205,32 +205,38 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _handle(stream, device=None):
+    """The handle of a stream (None: the current one of the device, or of the current device;
+    without the Stream object that torch.cuda.current_stream makes for it, 2 us a call)."""
+    if stream is not None:
+        return stream.cuda_stream
+    index = None if device is None else device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
+
+
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return ctypes.c_void_p(_handle(stream))
 
 
 def vw4_workspace_bytes(op: int, a: int, b: int, c: int) -> int:
     return int(load_library().vw4_workspace_bytes(op, a, b, c))
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(shape, dtype, device, stream, result=False):
     """An uninitialized tensor for a call on `stream` (None: the current one).  Its memory is
-    that stream's, so nothing that another stream still has to do touches it."""
-    if stream is None or torch.device(device).type != "cuda":
+    that stream's, so nothing that another stream still has to do touches it; a result's is
+    not handed on either while the current stream, once it waits for the call's, reads it."""
+    if stream is None or device.type != "cuda" or stream.cuda_stream == _handle(None, device):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _result(shape, dtype, device, stream):
-    """A tensor for the results of a call on `stream`, which the caller reads on the current
-    one once that waits for `stream`: neither hands its memory on while the other uses it."""
-    t = _empty(shape, dtype, device, stream)
-    if stream is not None and t.is_cuda:
-        t.record_stream(torch.cuda.current_stream(t.device))
-    return t
+    return _empty(shape, dtype, device, stream, True)
 
 
 class Workspace:
@@ -246,14 +252,13 @@ class Workspace:
 
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
         """The buffer, grown to nbytes, for a call on `stream` (None: the current one)."""
-        if stream is None and self.device.type == "cuda":
-            stream = torch.cuda.current_stream(self.device)
-        handle = None if stream is None else stream.cuda_stream
+        handle = _handle(stream, self.device) if self.device.type == "cuda" else None
         if self.buf is None or self.buf.numel() < nbytes:
             self.buf = _empty((max(nbytes, 256),), torch.uint8, self.device, stream)
             self._stream = handle
-        elif handle != self._stream and self.buf.is_cuda:
-            self.buf.record_stream(stream)
+        elif handle != self._stream:
+            self.buf.record_stream(stream if stream is not None else
+                                   torch.cuda.current_stream(self.device))
         return self.buf
 
 
@@ -262,9 +267,10 @@ _default_ws = {}  # one for each device, thread and stream
 
 def _workspace(ws, nbytes, device, stream):
     if ws is None:
-        s = stream if stream is not None else torch.cuda.current_stream(device)
-        key = (device.index, threading.get_ident(), s.cuda_stream)
-        ws = _default_ws.setdefault(key, Workspace(device))
+        key = (device.index, threading.get_ident(), _handle(stream, device))
+        ws = _default_ws.get(key)
+        if ws is None:
+            ws = _default_ws.setdefault(key, Workspace(device))
     if isinstance(ws, Workspace):
         return ws.get(nbytes, stream)
     if ws.device != device or not ws.is_contiguous():
@@ -626,7 +632,7 @@ class _Prepared:
     def _bind(self, name, args, keep, stream, workspace=None):
         self._name, self._args, self._keep = name, args, keep
         self._fn, self._ref = getattr(load_library(), name), ctypes.byref(args)
-        s = (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+        s = _handle(stream)
         self._tail = (s,) if workspace is None else (workspace.data_ptr(), workspace.numel(), s)
         self._ws = workspace
 
