@@ -80,6 +80,8 @@ typedef enum {
 #define VW4_DEV_BAD_PAGE       0x40u /* a cache page id outside [0, num_pages): its tokens
                                         read as zero keys and values, and are not written;
                                         or a length beyond the block table              */
+#define VW4_DEV_NO_ROOM        0x80u /* advance_pages ran out of pages, of columns of the
+                                        block table or of slots                         */
 
 /* A block-quantized weight matrix [N][K] (see the format notes above). */
 typedef struct vw4_weight {
@@ -107,6 +109,9 @@ typedef struct vw4_sampling {
 #define VW4_OP_REJECTION  3
 #define VW4_OP_REJECTION_TOPK 4
 #define VW4_OP_ATTN       5
+#define VW4_OP_ATTN_KV4   6
+#define VW4_OP_ADVANCE    7
+#define VW4_OP_LOGPROBS   8
 
 /*
  * verify_gemm_w4 -- the verification pass's skinny matmul.
@@ -634,12 +639,242 @@ typedef struct vw4_logits {
 } vw4_logits;
 VW4_API vw4_status process_logits(const vw4_logits* a, void* stream);
 
+/*
+ * A paged key-value cache in 4 bits: pages, tokens and heads as in vw4_kv_cache,
+ * the values as nvfp4 (see the format notes at the top): value d of a token's
+ * head is e2m1(nibble) * e4m3(block scale of d / 16) * k_scale[h].
+ *
+ * Element d of key head h of the token at place t of a page: byte
+ * k[page * page_stride + t * token_stride + h * head_stride + d / 2] (strides in
+ * bytes, the same for K and V), the even element in the low nibble; its block
+ * scale is byte k_blocks[page * blocks_page_stride + h * blocks_head_stride +
+ * t * (D / 16) + d / 16]: a head's scales of a page lie together, whatever the
+ * order of the values.
+ *
+ * page_size, D, Hkv, max_blocks, block table  as vw4_kv_cache; reserved is 0.
+ * k_dev, v_dev, k_blocks_dev, v_blocks_dev  16-byte aligned; every stride a
+ *             multiple of 16 bytes.
+ * k_scale_dev, v_scale_dev  fp32 [Hkv], of either sign or zero; NULL = 1.
+ */
+typedef struct vw4_kv4_cache {
+    int32_t page_size, num_pages, Hkv, D, max_blocks, reserved;
+    int64_t page_stride, token_stride, head_stride;
+    int64_t blocks_page_stride, blocks_head_stride, table_stride;
+    void* k_dev;
+    void* v_dev;
+    void* k_blocks_dev;
+    void* v_blocks_dev;
+    const int32_t* block_table_dev;
+    const float* k_scale_dev;
+    const float* v_scale_dev;
+} vw4_kv4_cache;
+
+/*
+ * verify_rope_append_kv4 -- verify_rope_append into a 4-bit cache.
+ *
+ * Defined by: the passages of verify_rope_append; the cache's format is the
+ * weights' nvfp4 ("Faster Gemma 4 on MLX with multi-token prediction").
+ *
+ * Queries as verify_rope_append.  A key or value y of a head of scale g is
+ * stored as t = y / g (0 where g is 0), at most 2688 in magnitude; the 16
+ * values of a block get the scale s = e4m3(min(max |t| / 6, 448)) and the codes
+ * e2m1(t / s), at most 6 in magnitude (0 where s is 0), both nearest, ties to
+ * even.  Scale and codes are those of the 64-bit formula: values so near a
+ * border that 32 bits cannot tell are computed again.  A NaN makes its block's
+ * scale, and so the block, NaN.
+ *
+ * Arguments and errors as verify_rope_append.
+ */
+typedef struct vw4_append_kv4 {
+    vw4_kv4_cache kv;
+    const void* x_dev;
+    const double* inv_freq_dev;
+    const float* q_norm_dev;
+    const float* k_norm_dev;
+    void* q_dev;
+    const int32_t* seq_lens_dev;
+    int64_t ldx, ldq;
+    int32_t x_bf16, B, R, Hq, rot, adjacent;
+    float eps;
+} vw4_append_kv4;
+VW4_API vw4_status verify_rope_append_kv4(const vw4_append_kv4* a, void* stream);
+
+/*
+ * verify_attn_kv4 -- verify_attn over a 4-bit cache.
+ *
+ * Defined by: the passages of verify_attn.  Rows, window, first tokens, scale,
+ * lse, rows without keys and keys that a row does not see as there (a NaN block
+ * scale among them).
+ *
+ * Precision: keys and values enter the products exactly (f16), the queries as
+ * f16 under an exact power of two per row (exact down to 2^-31 of the row's
+ * largest magnitude); scores, softmax statistics and sums in fp32; the weights
+ * enter the value product as f16, off by at most 2^-11 of themselves or 2^-34
+ * of the largest.
+ * Errors as verify_attn; the workspace is that of
+ * vw4_workspace_bytes(VW4_OP_ATTN_KV4, B, R * (Hq / Hkv), D).
+ */
+typedef struct vw4_attn_kv4 {
+    vw4_kv4_cache kv;
+    const void* q_dev;
+    void* out_dev;
+    float* lse_dev;
+    const int32_t* seq_lens_dev;
+    int64_t ldq, ldo;
+    int32_t B, R, Hq, window, sinks;
+    float scale;
+} vw4_attn_kv4;
+VW4_API vw4_status verify_attn_kv4(const vw4_attn_kv4* a, void* workspace_dev, size_t ws_bytes,
+                                   void* stream);
+
+/*
+ * read_kv4 -- tokens of a 4-bit cache as contiguous rows.
+ *
+ * Defined by: Ollama's mtp.go commit log, paragraph on snapshot and restore (a
+ * copy is made where a cache's tokens are needed elsewhere): what a pass that
+ * reads whole rows of keys and values (a prompt's chunk, a drafter's cross
+ * attention) takes.
+ *
+ * Row i < n of sequence b is the token at position first[b] + i; positions
+ * below 0 or from seq_lens[b] on give zeros.
+ *
+ * first_dev   int32 [B], or NULL: seq_lens[b] - n (the last n tokens).
+ * k_out_dev, v_out_dev  bf16 (out_f32 = 0: nearest) or fp32 (1) [B][n][Hkv][D].
+ * B 1..16384, 1 <= n <= 2^24.
+ * Errors: VW4_ERR_INVALID_ARG, VW4_ERR_UNSUPPORTED, VW4_ERR_ALIGN (outputs 16
+ * bytes).  A page id outside [0, num_pages), or a position beyond the block
+ * table, sets VW4_DEV_BAD_PAGE and reads as zeros.
+ */
+typedef struct vw4_read_kv4 {
+    vw4_kv4_cache kv;
+    const int32_t* seq_lens_dev;
+    const int32_t* first_dev;
+    void* k_out_dev;
+    void* v_out_dev;
+    int32_t B, n, out_f32;
+} vw4_read_kv4;
+VW4_API vw4_status read_kv4(const vw4_read_kv4* a, void* stream);
+
+/*
+ * advance_pages -- from an accept to the next step's rows: lengths, pages,
+ * block table and slots, on the device.
+ *
+ * Defined by: "Faster Gemma 4 on MLX with multi-token prediction" (no return to
+ * the CPU between passes) and Ollama's mtp.go commit log on caches (a rejected
+ * draft's tokens lie behind the new length, where the next rows go).
+ *
+ * For sequence b, in this order:
+ *   L = ended[b] ? 0 : lens[b] + accepted[b]                    (-> lens_out)
+ *   an ended sequence's held[b] pages (the first columns of its row of the
+ *   table) go to the end of the free list, sequence after sequence
+ *   g = grow[b] (or R); need = max(0, ceil((L + g) / page_size) - held)
+ *   the needed pages are taken from the end of the free list, sequence after
+ *   sequence, into the next columns of the table         (-> held_out, table)
+ *   seq_lens[b] = g > 0 ? L + g : 0: what the calls on R rows at the end of the
+ *   cache take (0: the sequence has no rows in this step)
+ *   row_start[b] = the sum of g before b; row_start[B] = all rows
+ *   slots[row_start[b] + i] = page * page_size + place of position L + i, i < g
+ * A sequence whose need exceeds what is left of the free list (all needs before
+ * it counted) or the table's columns gets no pages and no rows (g = 0), keeps
+ * its tokens, and sets VW4_DEV_NO_ROOM; the sequences behind it that need
+ * pages get none either, unless it was the table that was short.  Pages once
+ * held stay with a sequence until it ends.
+ * Slots behind the last row, and table columns that are not taken, are left as
+ * they are.  Negative lengths and counts read as 0.
+ *
+ * block_table_dev  int32 [B][table_stride], in place; max_blocks columns.
+ * lens_dev, accepted_dev (NULL: 0), ended_dev (NULL: none; not 0 = ended),
+ * grow_dev (NULL: R), held_dev  int32 [B].
+ * free_dev    int32 [num_pages], in place: free_count[0] pages from its start.
+ * lens_out_dev, held_out_dev, free_count_out_dev  may be the inputs.
+ * seq_lens_dev int32 [B], row_start_dev int32 [B + 1].
+ * slots_dev   int64 [rows_max], or NULL.  Rows beyond rows_max get no slot and
+ *             set VW4_DEV_NO_ROOM; a page id in the table outside [0, num_pages)
+ *             gives the slot -1 and sets VW4_DEV_BAD_PAGE.
+ * B 1..16384, R 0..2^20, page_size a power of two 8..65536, max_blocks *
+ * page_size <= 2^30, rows_max <= 2^31 - 1.
+ * Errors: VW4_ERR_INVALID_ARG, VW4_ERR_UNSUPPORTED, VW4_ERR_ALIGN,
+ * VW4_ERR_WORKSPACE (vw4_workspace_bytes(VW4_OP_ADVANCE, B, 0, 0)).
+ */
+typedef struct vw4_advance {
+    int32_t* block_table_dev;
+    const int32_t* lens_dev;
+    const int32_t* accepted_dev;
+    const int32_t* ended_dev;
+    const int32_t* grow_dev;
+    const int32_t* held_dev;
+    int32_t* free_dev;
+    const int32_t* free_count_dev;
+    int32_t* lens_out_dev;
+    int32_t* held_out_dev;
+    int32_t* free_count_out_dev;
+    int32_t* seq_lens_dev;
+    int32_t* row_start_dev;
+    int64_t* slots_dev;
+    int64_t table_stride, rows_max;
+    int32_t B, R, page_size, num_pages, max_blocks;
+} vw4_advance;
+VW4_API vw4_status advance_pages(const vw4_advance* a, void* workspace_dev, size_t ws_bytes,
+                                 void* stream);
+
+/*
+ * token_logprobs -- log probabilities of the committed tokens, the rows'
+ * entropy and their best alternatives.
+ *
+ * Defined by: Ollama's mtp.go commit log, paragraph "rework the MLX sampler"
+ * (the target's distribution stays on the device and is reused after the
+ * accept): what a server returns beside the committed tokens.
+ *
+ * For row i < R of sequence b, over v < V (NaN reads as -infinity):
+ *   y_v = scale * x_v,  lse = log sum_v exp(y_v),  p_v = exp(y_v - lse)
+ *   logprob = y_t - lse for the row's token t
+ *   rank    = 1 + how many entries lie before t in (x descending, index
+ *             ascending) order
+ *   entropy = - sum_v p_v log p_v
+ *   top_ids, top_logprobs = the first `top` entries in that order; entries of
+ *             -infinity are not listed (id -1, log probability -infinity)
+ * A row of -infinity throughout: lse and logprob -infinity, entropy 0.  Where
+ * entries are +infinity, they share the probability and lse is +infinity.
+ * A token of -1 gives logprob -infinity and rank 0; another one outside [0, V)
+ * too, and sets VW4_DEV_BAD_LIST_ID.
+ *
+ * x_dev, ldx  fp32 (x_bf16 = 0) or bf16 (1) [B*R][ldx].
+ * tokens_dev  int32 [B*R] (NULL: no logprob and rank).
+ * len_dev     int32 [B], or NULL: rows i >= len[b] are not read, and their
+ *             outputs are left as they are.
+ * logprob_dev, entropy_dev, lse_dev  fp32 [B*R]; rank_dev int32 [B*R]; each may
+ *             be NULL.
+ * top_ids_dev, top_logprobs_dev  int32 / fp32 [B*R][top] (NULL when top is 0).
+ * B 1..16384, R 1..16, 1 <= V <= 2^24, top 0..32, scale > 0 and finite.
+ * Precision: sums in fp32, over parts of a row and then over the parts.
+ * Errors: VW4_ERR_INVALID_ARG, VW4_ERR_ALIGN (x by its type, 4 bytes else),
+ * VW4_ERR_WORKSPACE (vw4_workspace_bytes(VW4_OP_LOGPROBS, B * R, V, top)).
+ */
+typedef struct vw4_logprobs {
+    const void* x_dev;
+    const int32_t* tokens_dev;
+    const int32_t* len_dev;
+    float* logprob_dev;
+    float* lse_dev;
+    float* entropy_dev;
+    int32_t* rank_dev;
+    int32_t* top_ids_dev;
+    float* top_logprobs_dev;
+    int64_t ldx;
+    int32_t B, R, V, top, x_bf16;
+    float scale;
+} vw4_logprobs;
+VW4_API vw4_status token_logprobs(const vw4_logprobs* a, void* workspace_dev, size_t ws_bytes,
+                                  void* stream);
+
 /* Workspace bytes needed by an operation:
  *   VW4_OP_GEMM:      (M, N, K)
  *   VW4_OP_MOE:       (M*topk, N, K)   -- pass the number of routed pairs first
  *   VW4_OP_REJECTION: (B, Kd, V)
  *   VW4_OP_REJECTION_TOPK: (B, Kd, Kt)
- *   VW4_OP_ATTN:      (B, R * (Hq / Hkv), D)
+ *   VW4_OP_ATTN:      (B, R * (Hq / Hkv), D), VW4_OP_ATTN_KV4 alike
+ *   VW4_OP_ADVANCE:   (B, 0, 0)
+ *   VW4_OP_LOGPROBS:  (B * R, V, top)
  * Returns 0 for an unknown op or invalid sizes. */
 VW4_API size_t vw4_workspace_bytes(int op, int a, int b, int c);
 

@@ -9,8 +9,9 @@ call raises.
 Entry points (same names as the C ABI):
   verify_gemm_w4, verify_gemm_w4_blockmax, verify_greedy_w4, verify_moe_w4,
   accept_greedy, accept_rejection, accept_rejection_blockmax,
-  accept_rejection_topk, verify_rope_append, verify_attn, process_logits,
-  vw4_workspace_bytes, vw4_get_device_status, vw4_q4_0_from_blocks,
+  accept_rejection_topk, verify_rope_append, verify_attn (with a KVCache4: the
+  4-bit cache's verify_rope_append_kv4 and verify_attn_kv4), read_kv4,
+  process_logits, advance_pages, token_logprobs, vw4_workspace_bytes, vw4_get_device_status, vw4_q4_0_from_blocks,
   vw4_set_wait_limit_ns.
 """
 from __future__ import annotations
@@ -18,6 +19,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from collections import namedtuple
 
 import torch
 
@@ -35,6 +37,9 @@ OP_MOE = 2
 OP_REJECTION = 3
 OP_REJECTION_TOPK = 4
 OP_ATTN = 5
+OP_ATTN_KV4 = 6
+OP_ADVANCE = 7
+OP_LOGPROBS = 8
 KV_BF16 = 1
 KV_E4M3 = 2
 
@@ -45,6 +50,7 @@ DEV_ZERO_RESIDUAL = 0x8
 DEV_BAD_LIST_ID = 0x10
 DEV_BOUNDS = 0x20          # checks build only: an in-kernel bounds check failed
 DEV_BAD_PAGE = 0x40
+DEV_NO_ROOM = 0x80
 BUILD_CHECKS = 0x1         # vw4_build_flags(): the checks build
 
 STATUS_NAMES = {0: "VW4_OK", 1: "VW4_ERR_INVALID_ARG", 2: "VW4_ERR_UNSUPPORTED",
@@ -60,7 +66,9 @@ EXPORTS = ("verify_gemm_w4", "verify_moe_w4", "accept_greedy", "accept_rejection
            "vw4_depth_ctl_observe", "vw4_depth_ctl_expected", "vw4_depth_ctl_choose",
            "accept_rejection_topk", "vw4_rejection_row_records",
            "vw4_test_inject_stall", "verify_gemm_w4_blockmax", "accept_rejection_blockmax",
-           "vw4_build_flags", "verify_rope_append", "verify_attn", "process_logits")
+           "vw4_build_flags", "verify_rope_append", "verify_attn", "process_logits",
+           "verify_rope_append_kv4", "verify_attn_kv4", "read_kv4", "advance_pages",
+           "token_logprobs")
 
 
 class VW4Error(RuntimeError):
@@ -116,6 +124,50 @@ class AttnArgs(ctypes.Structure):
     _fields_ = [("kv", KVDesc)] + _fields(
         ("q_dev out_dev lse_dev seq_lens_dev", ctypes.c_void_p), ("ldq ldo", ctypes.c_int64),
         ("B R Hq window sinks", ctypes.c_int32), ("scale", ctypes.c_float))
+
+
+class KV4Desc(ctypes.Structure):
+    """vw4_kv4_cache (see vw4.h)."""
+    _fields_ = _fields(("page_size num_pages Hkv D max_blocks reserved", ctypes.c_int32),
+                       ("page_stride token_stride head_stride blocks_page_stride "
+                        "blocks_head_stride table_stride", ctypes.c_int64),
+                       ("k_dev v_dev k_blocks_dev v_blocks_dev block_table_dev k_scale_dev "
+                        "v_scale_dev", ctypes.c_void_p))
+
+
+class AppendKV4Args(ctypes.Structure):
+    """vw4_append_kv4 (see vw4.h)."""
+    _fields_ = [("kv", KV4Desc)] + AppendArgs._fields_[1:]
+
+
+class AttnKV4Args(ctypes.Structure):
+    """vw4_attn_kv4 (see vw4.h)."""
+    _fields_ = [("kv", KV4Desc)] + AttnArgs._fields_[1:]
+
+
+class ReadKV4Args(ctypes.Structure):
+    """vw4_read_kv4 (see vw4.h)."""
+    _fields_ = [("kv", KV4Desc)] + _fields(
+        ("seq_lens_dev first_dev k_out_dev v_out_dev", ctypes.c_void_p),
+        ("B n out_f32", ctypes.c_int32))
+
+
+class AdvanceArgs(ctypes.Structure):
+    """vw4_advance (see vw4.h)."""
+    _fields_ = _fields(
+        ("block_table_dev lens_dev accepted_dev ended_dev grow_dev held_dev free_dev "
+         "free_count_dev lens_out_dev held_out_dev free_count_out_dev seq_lens_dev row_start_dev "
+         "slots_dev", ctypes.c_void_p),
+        ("table_stride rows_max", ctypes.c_int64),
+        ("B R page_size num_pages max_blocks", ctypes.c_int32))
+
+
+class LogprobsArgs(ctypes.Structure):
+    """vw4_logprobs (see vw4.h)."""
+    _fields_ = _fields(
+        ("x_dev tokens_dev len_dev logprob_dev lse_dev entropy_dev rank_dev top_ids_dev "
+         "top_logprobs_dev", ctypes.c_void_p),
+        ("ldx", ctypes.c_int64), ("B R V top x_bf16", ctypes.c_int32), ("scale", ctypes.c_float))
 
 
 class LogitsArgs(ctypes.Structure):
@@ -180,6 +232,11 @@ def load_library(path: str = LIB_PATH):
             "verify_rope_append": (I, [ctypes.POINTER(AppendArgs), P]),
             "verify_attn": (I, [ctypes.POINTER(AttnArgs), P, ctypes.c_size_t, P]),
             "process_logits": (I, [ctypes.POINTER(LogitsArgs), P]),
+            "verify_rope_append_kv4": (I, [ctypes.POINTER(AppendKV4Args), P]),
+            "verify_attn_kv4": (I, [ctypes.POINTER(AttnKV4Args), P, ctypes.c_size_t, P]),
+            "read_kv4": (I, [ctypes.POINTER(ReadKV4Args), P]),
+            "advance_pages": (I, [ctypes.POINTER(AdvanceArgs), P, ctypes.c_size_t, P]),
+            "token_logprobs": (I, [ctypes.POINTER(LogprobsArgs), P, ctypes.c_size_t, P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
@@ -556,6 +613,15 @@ def accept_rejection_topk(target_ids: torch.Tensor, target_vals: torch.Tensor,
     return tokens, length
 
 
+def _check_table(block_table):
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [B, max_blocks] with contiguous rows")
+    if block_table.shape[0] > 1 and block_table.stride(0) < block_table.shape[1]:
+        raise ValueError("block_table: the sequences' rows overlap (an expanded row is one "
+                         "row of memory; make it contiguous)")
+
+
 class KVCache:
     """A paged cache bound to its vw4_kv_cache descriptor (see vw4.h): k, v are
     [pages, page_size, Hkv, D] tensors (views of any page layout whose last
@@ -570,12 +636,7 @@ class KVCache:
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
             raise ValueError("k and v must be [pages, page_size, Hkv, D] of equal strides, the "
                              "last dimension contiguous")
-        if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
-                (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-            raise ValueError("block_table must be int32 [B, max_blocks] with contiguous rows")
-        if block_table.shape[0] > 1 and block_table.stride(0) < block_table.shape[1]:
-            raise ValueError("block_table: the sequences' rows overlap (an expanded row is one "
-                             "row of memory; make it contiguous)")
+        _check_table(block_table)
         pages, page, hkv, d = k.shape
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None and (t.dtype != torch.float32 or t.shape != (hkv,)
@@ -590,6 +651,62 @@ class KVCache:
                            k.stride(2) if hkv > 1 else 0,
                            max(block_table.stride(0), block_table.shape[1]),
                            *(_addr(t) for t in (k, v, block_table, k_scale, v_scale)))
+
+
+class KVCache4:
+    """A paged cache in 4 bits (nvfp4) bound to its vw4_kv4_cache descriptor (see vw4.h):
+    k, v uint8 [pages, page_size, Hkv, D / 2] (views of any page layout whose last dimension
+    is contiguous), the even element in the low nibble; k_blocks, v_blocks float8_e4m3fn
+    [pages, Hkv, page_size, D / 16], a head's scales of a page together; block_table int32
+    [B, max_blocks]; k_scale, v_scale fp32 [Hkv]."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_blocks: torch.Tensor,
+                 v_blocks: torch.Tensor, block_table: torch.Tensor,
+                 k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None):
+        if k.dtype != torch.uint8 or v.dtype != torch.uint8:
+            raise ValueError("k and v must be uint8 (two values a byte)")
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must be [pages, page_size, Hkv, D / 2] of equal strides, "
+                             "the last dimension contiguous")
+        pages, page, hkv, half = k.shape
+        shape = (pages, hkv, page, half // 8)
+        for name, t in (("k_blocks", k_blocks), ("v_blocks", v_blocks)):
+            if t.dtype != torch.float8_e4m3fn or tuple(t.shape) != shape or half % 8 or \
+                    t.stride() != k_blocks.stride() or t.stride(3) != 1 or \
+                    (page > 1 and t.stride(2) != half // 8):
+                raise ValueError(f"{name} must be float8_e4m3fn [pages, Hkv, page_size, D / 16], "
+                                 "of equal strides, a head's scales of a page contiguous")
+        _check_table(block_table)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _need(t, torch.float32, (hkv,), name)
+        self.k, self.v, self.k_blocks, self.v_blocks = k, v, k_blocks, v_blocks
+        self.block_table, self.k_scale, self.v_scale = block_table, k_scale, v_scale
+        self.B, self.Hkv, self.D, self.page_size = block_table.shape[0], hkv, 2 * half, page
+        # a dimension of one element is never stepped over: its stride may be anything
+        self.desc = KV4Desc(page, pages, hkv, 2 * half, block_table.shape[1], 0,
+                            k.stride(0) if pages > 1 else 0, k.stride(1) if page > 1 else hkv * half,
+                            k.stride(2) if hkv > 1 else 0,
+                            k_blocks.stride(0) if pages > 1 else 0,
+                            k_blocks.stride(1) if hkv > 1 else 0,
+                            max(block_table.stride(0), block_table.shape[1]),
+                            *(_addr(t) for t in self.tensors()))
+
+    def tensors(self):
+        return (self.k, self.v, self.k_blocks, self.v_blocks, self.block_table, self.k_scale,
+                self.v_scale)
+
+
+def _one_device(tensors, what):
+    """The tensors (None among them allowed) lie on one device, the current one, where the
+    call is launched."""
+    on = {t.device for t in tensors if t is not None}
+    if len(on) > 1:
+        raise ValueError(f"{what}: tensors on several devices: {sorted(map(str, on))}")
+    for d in on:
+        if d.type != "cuda":
+            raise ValueError("expected a CUDA tensor")
+        if d.index != torch.cuda.current_device():
+            raise ValueError(f"{what}: tensors on {d}, which is not the current device")
 
 
 def _addr(t):
@@ -643,9 +760,9 @@ class _Prepared:
 
 
 class PreparedAppend(_Prepared):
-    """verify_rope_append bound to its tensors."""
+    """verify_rope_append bound to its tensors (with a KVCache4: verify_rope_append_kv4)."""
 
-    def __init__(self, x: torch.Tensor, cache: KVCache, seq_lens: torch.Tensor, R: int, Hq: int,
+    def __init__(self, x: torch.Tensor, cache: KVCache | KVCache4, seq_lens: torch.Tensor, R: int, Hq: int,
                  inv_freq: torch.Tensor | None = None, adjacent: bool = False,
                  q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None,
                  eps: float = 1e-6, q_out: torch.Tensor | None = None, stream=None):
@@ -666,27 +783,37 @@ class PreparedAppend(_Prepared):
             _need(t, torch.float32, (D,), n)
         self.q_out = q_out
         ldx = x.stride(0) if x.shape[0] > 1 else x.shape[1]
-        args = AppendArgs(cache.desc, _addr(x), _addr(inv_freq) if rot else None, _addr(q_norm),
-                          _addr(k_norm), _addr(q_out), _addr(seq_lens), ldx, ldq,
-                          int(x.dtype == torch.bfloat16), B, R, Hq, rot, int(adjacent), eps)
-        self._bind("verify_rope_append", args,
+        four = isinstance(cache, KVCache4)
+        if four:
+            _one_device((x, seq_lens, inv_freq, q_norm, k_norm, q_out, *cache.tensors()),
+                        "verify_rope_append")
+        kind = AppendKV4Args if four else AppendArgs
+        args = kind(cache.desc, _addr(x), _addr(inv_freq) if rot else None, _addr(q_norm),
+                    _addr(k_norm), _addr(q_out), _addr(seq_lens), ldx, ldq,
+                    int(x.dtype == torch.bfloat16), B, R, Hq, rot, int(adjacent), eps)
+        self._bind("verify_rope_append_kv4" if four else "verify_rope_append", args,
                    (x, cache, seq_lens, inv_freq, q_norm, k_norm, q_out), stream)
 
 
 def verify_rope_append(x, cache, seq_lens, R, Hq, **kw):
     """Packed qkv rows x [B*R, (Hq + 2 Hkv) * D] (fp32 or bf16) -> rotated
     queries bf16 [B, R, Hq, D] (returned), keys and values into the cache slots
-    of positions seq_lens[b] - R + i; see vw4.h.  Keywords: inv_freq fp64
+    of positions seq_lens[b] - R + i of a KVCache or KVCache4; see vw4.h.  Keywords: inv_freq fp64
     [rot/2], adjacent, q_norm, k_norm fp32 [D], eps, q_out, stream."""
     p = PreparedAppend(x, cache, seq_lens, R, Hq, **kw)
     p()
     return p.q_out
 
 
-class PreparedAttn(_Prepared):
-    """verify_attn bound to its tensors and a workspace."""
+def _attn_bytes(cache, B, R, Hq, D):
+    op = OP_ATTN_KV4 if isinstance(cache, KVCache4) else OP_ATTN
+    return vw4_workspace_bytes(op, B, R * max(1, Hq // cache.Hkv), D)
 
-    def __init__(self, q: torch.Tensor, cache: KVCache, seq_lens: torch.Tensor,
+
+class PreparedAttn(_Prepared):
+    """verify_attn bound to its tensors and a workspace (with a KVCache4: verify_attn_kv4)."""
+
+    def __init__(self, q: torch.Tensor, cache: KVCache | KVCache4, seq_lens: torch.Tensor,
                  scale: float | None = None, window: int = 0, sinks: int = 0,
                  out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                  workspace=None, stream=None):
@@ -702,22 +829,26 @@ class PreparedAttn(_Prepared):
         _need(lse, torch.float32, (B, R, Hq), "lse")
         _need(seq_lens, torch.int32, (B,), "seq_lens")
         self.out, self.lse = out, lse
-        args = AttnArgs(cache.desc, _addr(q), _addr(out), _addr(lse), _addr(seq_lens), ldq, ldo, B,
-                        R, Hq, int(window), int(sinks), float(D ** -0.5 if scale is None else scale))
-        need = vw4_workspace_bytes(OP_ATTN, B, R * max(1, Hq // cache.Hkv), D)
+        four = isinstance(cache, KVCache4)
+        if four:
+            _one_device((q, seq_lens, out, lse, *cache.tensors()), "verify_attn")
+        kind = AttnKV4Args if four else AttnArgs
+        args = kind(cache.desc, _addr(q), _addr(out), _addr(lse), _addr(seq_lens), ldq, ldo, B,
+                    R, Hq, int(window), int(sinks), float(D ** -0.5 if scale is None else scale))
+        need = _attn_bytes(cache, B, R, Hq, D)
         if workspace is None:
             workspace = Workspace(q.device)
         ws = _workspace(workspace, need, q.device, stream)
-        self._bind("verify_attn", args, (q, cache, seq_lens, out, lse), stream, ws)
+        self._bind("verify_attn_kv4" if four else "verify_attn", args,
+                   (q, cache, seq_lens, out, lse), stream, ws)
 
 
 def verify_attn(q, cache, seq_lens, scale=None, window=0, sinks=0, out=None, lse=None,
                 workspace=None, stream=None):
     """Attention of the verify rows q bf16 [B, R, Hq, D] (R = 1: plain decoding)
-    over the paged cache -> out bf16 [B, R, Hq, D]; scale defaults to
-    1/sqrt(D); lse: optional fp32 [B, R, Hq]; see vw4.h."""
-    need = vw4_workspace_bytes(OP_ATTN, q.shape[0], q.shape[1] * max(1, q.shape[2] // cache.Hkv),
-                               q.shape[3])
+    over the paged cache (a KVCache or KVCache4) -> out bf16 [B, R, Hq, D]; scale
+    defaults to 1/sqrt(D); lse: optional fp32 [B, R, Hq]; see vw4.h."""
+    need = _attn_bytes(cache, *q.shape)
     p = PreparedAttn(q, cache, seq_lens, scale, window, sinks, out, lse,
                      _workspace(workspace, need, q.device, stream), stream)
     p()
@@ -781,6 +912,163 @@ def process_logits(logits, drafts=None, **kw):
     (a new tensor, or `out`, which may be `logits`); keywords as
     PreparedLogits; see vw4.h."""
     p = PreparedLogits(logits, drafts, **kw)
+    p()
+    return p.out
+
+
+class PreparedRead(_Prepared):
+    """read_kv4 bound to its tensors; k and v are its outputs."""
+
+    def __init__(self, cache: KVCache4, seq_lens: torch.Tensor, n: int,
+                 first: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16,
+                 k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+        if not isinstance(cache, KVCache4):
+            raise ValueError("read_kv4 takes a KVCache4")
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("dtype must be bfloat16 or float32")
+        B, shape = cache.B, (cache.B, n, cache.Hkv, cache.D)
+        _need(seq_lens, torch.int32, (B,), "seq_lens")
+        _need(first, torch.int32, (B,), "first")
+        k = _result(shape, dtype, cache.k.device, stream) if k is None else k
+        v = _result(shape, dtype, cache.k.device, stream) if v is None else v
+        for name, t in (("k", k), ("v", v)):
+            _need(t, dtype, shape, name)
+        _one_device((seq_lens, first, k, v, *cache.tensors()), "read_kv4")
+        self.k, self.v = k, v
+        args = ReadKV4Args(cache.desc, _addr(seq_lens), _addr(first), _addr(k), _addr(v), B, n,
+                           int(dtype == torch.float32))
+        self._bind("read_kv4", args, (cache, seq_lens, first, k, v), stream)
+
+
+def read_kv4(cache, seq_lens, n, first=None, dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """Tokens first[b] .. first[b] + n - 1 of every sequence of a KVCache4 (first None: the last
+    n) -> keys and values [B, n, Hkv, D], zeros outside the sequence; see vw4.h."""
+    p = PreparedRead(cache, seq_lens, n, first, dtype, k, v, stream)
+    p()
+    return p.k, p.v
+
+
+class PreparedAdvance(_Prepared):
+    """advance_pages bound to its tensors and a workspace; lens, held, free_count, seq_lens,
+    row_start and slots are its outputs (new tensors where none is given; lens_out, held_out
+    and free_count_out may be the inputs).  rows_max: how many slots (None: what slots
+    holds; without slots none are made)."""
+
+    def __init__(self, block_table: torch.Tensor, page_size: int, lens: torch.Tensor,
+                 held: torch.Tensor, free: torch.Tensor, free_count: torch.Tensor,
+                 rows_max: int | None = None, R: int = 0, accepted: torch.Tensor | None = None,
+                 ended: torch.Tensor | None = None, grow: torch.Tensor | None = None,
+                 lens_out: torch.Tensor | None = None, held_out: torch.Tensor | None = None,
+                 free_count_out: torch.Tensor | None = None, seq_lens: torch.Tensor | None = None,
+                 row_start: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                 workspace=None, stream=None):
+        _check_table(block_table)
+        B, cols = block_table.shape
+        i32, dev = torch.int32, block_table.device
+        for name, t in (("lens", lens), ("held", held), ("accepted", accepted), ("ended", ended),
+                        ("grow", grow), ("lens_out", lens_out), ("held_out", held_out),
+                        ("seq_lens", seq_lens)):
+            _need(t, i32, (B,), name)
+        for name, t in (("free_count", free_count), ("free_count_out", free_count_out)):
+            _need(t, i32, (1,), name)
+        _need(free, i32, (free.numel(),), "free")
+        _need(row_start, i32, (B + 1,), "row_start")
+        if slots is None and rows_max:
+            slots = _result((rows_max,), torch.int64, dev, stream)
+        if slots is not None:
+            _need(slots, torch.int64, (slots.numel(),), "slots")
+            rows_max = slots.numel() if rows_max is None else rows_max
+            if rows_max > slots.numel():
+                raise ValueError("slots must hold rows_max entries")
+
+        def result(t, n):
+            return _result((n,), i32, dev, stream) if t is None else t
+        self.lens, self.held = result(lens_out, B), result(held_out, B)
+        self.free_count = result(free_count_out, 1)
+        self.seq_lens, self.row_start = result(seq_lens, B), result(row_start, B + 1)
+        self.slots, self.free, self.block_table = slots, free, block_table
+        ptrs = (block_table, lens, accepted, ended, grow, held, free, free_count, self.lens,
+                self.held, self.free_count, self.seq_lens, self.row_start, slots)
+        _one_device(ptrs, "advance_pages")
+        ws = _workspace(Workspace(dev) if workspace is None else workspace,
+                        vw4_workspace_bytes(OP_ADVANCE, B, 0, 0), dev, stream)
+        args = AdvanceArgs(*(_addr(t) for t in ptrs), max(block_table.stride(0), cols),
+                           rows_max if slots is not None else 0, B, R, page_size, free.numel(), cols)
+        self._bind("advance_pages", args, ptrs, stream, ws)
+
+
+def advance_pages(block_table, page_size, lens, held, free, free_count, rows_max=None, R=0,
+                  workspace=None, stream=None, **kw):
+    """After an accept: new lengths, pages from the free list for the next rows (R, or grow[b],
+    a sequence), their places in the block table and their slots -> the call's
+    PreparedAdvance, whose lens, held, free_count, seq_lens, row_start and slots are the
+    results; block_table and free change in place; keywords as there; see vw4.h."""
+    need = vw4_workspace_bytes(OP_ADVANCE, block_table.shape[0], 0, 0)
+    p = PreparedAdvance(block_table, page_size, lens, held, free, free_count, rows_max, R,
+                        workspace=_workspace(workspace, need, block_table.device, stream),
+                        stream=stream, **kw)
+    p()
+    return p
+
+
+TokenLogprobs = namedtuple("TokenLogprobs", "logprob lse entropy rank top_ids top_logprobs")
+
+
+class PreparedLogprobs(_Prepared):
+    """token_logprobs bound to its tensors and a workspace; out is a TokenLogprobs."""
+
+    def __init__(self, logits: torch.Tensor, tokens: torch.Tensor | None = None,
+                 length: torch.Tensor | None = None, top: int = 0, scale: float = 1.0,
+                 logprob: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                 entropy: torch.Tensor | None = None, rank: torch.Tensor | None = None,
+                 top_ids: torch.Tensor | None = None, top_logprobs: torch.Tensor | None = None,
+                 workspace=None, stream=None):
+        if logits.dim() != 3 or logits.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("logits must be float32 or bfloat16 [B, R, V]")
+        B, R, V = logits.shape
+        ldx = _rows(logits, logits.dtype, (B, R, V), "logits")
+        _need(tokens, torch.int32, (B, R), "tokens")
+        _need(length, torch.int32, (B,), "length")
+        f32, i32, dev = torch.float32, torch.int32, logits.device
+        if not 0 <= top <= 32:
+            raise ValueError("top must be 0 .. 32")
+        for name, t in (("logprob", logprob), ("rank", rank)):
+            if t is not None and tokens is None:
+                raise ValueError(f"{name}: tokens int32 [B, R] are needed")
+        for name, t in (("top_ids", top_ids), ("top_logprobs", top_logprobs)):
+            if t is not None and top == 0:
+                raise ValueError(f"{name}: top must be at least 1")
+
+        def result(t, dtype, name, shape=(B, R), want=True):
+            if t is None:
+                return _result(shape, dtype, dev, stream) if want else None
+            return _need(t, dtype, shape, name)
+        given = tokens is not None
+        self.out = TokenLogprobs(
+            result(logprob, f32, "logprob", want=given), result(lse, f32, "lse"),
+            result(entropy, f32, "entropy"), result(rank, i32, "rank", want=given),
+            result(top_ids, i32, "top_ids", (B, R, top), top > 0),
+            result(top_logprobs, f32, "top_logprobs", (B, R, top), top > 0))
+        ptrs = (logits, tokens, length, *self.out)
+        _one_device(ptrs, "token_logprobs")
+        need = vw4_workspace_bytes(OP_LOGPROBS, B * R, V, top)
+        ws = _workspace(Workspace(dev) if workspace is None else workspace, need, dev, stream)
+        args = LogprobsArgs(*(_addr(t) for t in ptrs), ldx, B, R, V, top,
+                            int(logits.dtype == torch.bfloat16), float(scale))
+        self._bind("token_logprobs", args, ptrs, stream, ws)
+
+
+def token_logprobs(logits, tokens=None, length=None, top=0, scale=1.0, workspace=None, stream=None,
+                   **kw):
+    """Log probabilities of tokens int32 [B, R] under softmax(scale * logits), logits fp32 or
+    bf16 [B, R, V], with lse, entropy, the token's rank and the `top` best alternatives -> a
+    TokenLogprobs.  length int32 [B]: rows i >= length[b] are not read, and their outputs left
+    as they are; keywords as PreparedLogprobs; see vw4.h."""
+    need = vw4_workspace_bytes(OP_LOGPROBS, logits.shape[0] * logits.shape[1], logits.shape[2],
+                               top) if logits.dim() == 3 else 0
+    p = PreparedLogprobs(logits, tokens, length, top, scale,
+                         workspace=_workspace(workspace, need, logits.device, stream),
+                         stream=stream, **kw)
     p()
     return p.out
 

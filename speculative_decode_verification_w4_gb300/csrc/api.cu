@@ -258,6 +258,18 @@ VW4_API size_t vw4_workspace_bytes(int op, int a, int b, int c) {
             return 0;
         return attn_workspace_bytes(a, b, c);
     }
+    if (op == VW4_OP_ATTN_KV4) {
+        if (a < 1 || a > kMaxSeqs || b < 1 || b > kMaxVerifyRows * kMaxHeads ||
+            (c != 64 && c != 128 && c != 256))
+            return 0;
+        return attn4_workspace_bytes(a, b, c);
+    }
+    if (op == VW4_OP_ADVANCE) return a < 1 || a > kMaxSeqs ? 0 : advance_workspace_bytes(a);
+    if (op == VW4_OP_LOGPROBS) {
+        if (a < 1 || a > kMaxSeqs * kMaxVerifyRows || b < 1 || b > (1 << 24) || c < 0 || c > kMaxTop)
+            return 0;
+        return logprob_workspace_bytes(a, b, c);
+    }
     return 0;
 }
 

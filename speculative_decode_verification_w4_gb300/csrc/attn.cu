@@ -207,6 +207,11 @@ cudaError_t launch_attn(const AttnParams& p, const AttnMaps& maps, AttnPlan plan
                     : D == 128 ? launch_attn_d128(p, maps, f8, rows, &grid, sms, s)
                                : launch_attn_d256(p, maps, f8, rows, &grid, sms, s);
     if (e != cudaSuccess) return e;
+    return launch_attn_join(p, D, rows, grid, tk, sms, s);
+}
+
+cudaError_t launch_attn_join(const AttnParams& p, int D, int rows, int grid, int tk, int sms,
+                             cudaStream_t s) {
     // Few rows in many parts: a warp 64 columns, for a row's parts are then asked for at
     // once (8 x 6 rows of 16 items of 256 in ten parts each: 29.2 us a call instead of
     // 31.0, one token of 4 items in nine parts 11.3 instead of 12.3).  Else a warp a row:

@@ -132,6 +132,17 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t b) {
         : "=r"(r) : "r"(b));
     return r;
 }
+// four bytes of e2m1 pairs -> four f16x2, the low nibble in the low half; exact
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t* h) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
 
 // four f16 values (two pairs) as e4m3 bytes hi + lo: hi the nearest, lo the nearest to
 // the rest, which f16 holds exactly

@@ -1,0 +1,381 @@
+// logprobs.cu -- log probabilities of given tokens, ranks, entropy and the best
+// alternatives of logits rows, in one pass over the rows.
+//
+// With c = scale log2(e) and a running maximum m of the logits,
+//   Z = sum 2^(c (x - m)),   W = sum 2^(c (x - m)) c (x - m)
+// and when m grows, by d = c (m' - m): W <- (W - d Z) 2^-d, Z <- Z 2^-d.  Then
+//   lse = scale m + ln Z,   entropy = ln 2 (log2 Z - W / Z).
+// (The difference first: c x of the type's lowest value, a usual mask, would overflow.)
+// Each thread keeps its own m, Z and W; they meet in a fixed order.
+//
+// Alternatives: the block keeps the `top` largest entries so far, as 64-bit keys (value,
+// then lower index first), and of a chunk of 4096 entries looks at those above the least
+// of them only.  Where more than kCand are (the first chunk), the threads' own maxima
+// give a better threshold first: of the `top` largest of them the least has that many
+// entries above it, which lie in that many threads.  A candidate's place is the number
+// of candidates above it, so nothing is sorted step by step.
+//
+// The bytes bound it (4 or 2 a logit).  A row is split over blocks where the rows alone
+// would leave SMs idle; a second kernel joins the parts in order.
+#include <cuda_bf16.h>
+
+#include "attn.cuh"
+
+namespace vw4 {
+
+constexpr int kLpThreads = 256;
+constexpr int kLpEach = 16;                          // entries of a thread and chunk
+constexpr int kLpChunk = kLpThreads * kLpEach;
+constexpr int kCand = kMaxTop * kLpEach;             // candidates that are looked at at once
+constexpr int kLpMaxSplit = 64;
+constexpr uint32_t kLpBadId = 0x10u;
+constexpr float kLpFar = 1024.f;                     // 2^-1024 is 0 in fp32
+
+struct LpPart {
+    float m, z, w;
+    int before;   // entries before the token
+};
+
+// Parts of a row: enough blocks to fill the GPU, each of at least a chunk.
+static int lp_split(long long rows, int V) {
+    const long long chunks = (V + kLpChunk - 1) / kLpChunk;
+    long long s = 1;
+    if (rows < 1216) s = (1216 + rows - 1) / rows;
+    if (s > chunks) s = chunks;
+    if (s > kLpMaxSplit) s = kLpMaxSplit;
+    return static_cast<int>(s);
+}
+size_t logprob_workspace_bytes(long long rows, int V, int top) {
+    const size_t parts = static_cast<size_t>(rows) * lp_split(rows, V);
+    return (parts * (sizeof(LpPart) + static_cast<size_t>(top) * 8) + 511) & ~size_t(255);
+}
+
+// Larger keys come first: the value, then the lower index.  0: no entry.
+__device__ __forceinline__ unsigned long long lp_key(float x, int v) {
+    const uint32_t b = __float_as_uint(x + 0.f);  // (+0 for -0)
+    const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
+    return static_cast<unsigned long long>(o) << 32 | static_cast<uint32_t>(~v);
+}
+__device__ __forceinline__ float lp_key_value(unsigned long long k) {
+    const uint32_t o = static_cast<uint32_t>(k >> 32);
+    return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ int lp_key_index(unsigned long long k) {
+    return static_cast<int>(~static_cast<uint32_t>(k));
+}
+
+struct LpSum {
+    float m, z, w;
+};
+// The sum with its maximum moved up to m (of finite values, or -infinity).
+__device__ __forceinline__ LpSum lp_move(LpSum s, float m, float c2) {
+    if (s.m == m || s.z == 0.f) return LpSum{m, s.z, s.w};
+    if (m == INFINITY) return LpSum{m, 0.f, 0.f};
+    const float d = fminf((m - s.m) * c2, kLpFar), f = ex2(-d);
+    return LpSum{m, s.z * f, fmaf(-d, s.z, s.w) * f};
+}
+__device__ __forceinline__ LpSum lp_add(LpSum a, LpSum b, float c2) {
+    const float m = fmaxf(a.m, b.m);
+    a = lp_move(a, m, c2);
+    b = lp_move(b, m, c2);
+    return LpSum{m, a.z + b.z, a.w + b.w};
+}
+
+// log p_v, from x and the row's m and ln Z.
+__device__ __forceinline__ float lp_log(const LogprobParams& p, float x, float m, float lnz) {
+    if (m == INFINITY) return x == INFINITY ? -lnz : -INFINITY;
+    return fmaf(x - m, p.scale, -lnz);
+}
+// The outputs of a row but the alternatives.
+__device__ __forceinline__ void lp_write(const LogprobParams& p, long long row, LpSum s, int before,
+                                         int t, float xt) {
+    const float lnz = logf(s.z);
+    const bool none = s.z == 0.f;  // nothing but -infinity
+    const float lse = none ? -INFINITY : s.m == INFINITY ? INFINITY : fmaf(s.m, p.scale, lnz);
+    if (p.lse) p.lse[row] = lse;
+    if (p.entropy) p.entropy[row] = none ? 0.f : fmaxf(0.f, lnz - s.w / s.z * kLn2);
+    const bool here = t >= 0 && t < p.V;
+    if (p.logprob) p.logprob[row] = !here || none ? -INFINITY : lp_log(p, xt, s.m, lnz);
+    if (p.rank) p.rank[row] = here ? before + 1 : 0;
+}
+__device__ __forceinline__ void lp_write_top(const LogprobParams& p, long long row, int k,
+                                             unsigned long long key, float m, float lnz) {
+    const float x = lp_key_value(key);
+    const bool listed = key != 0 && x > -INFINITY;
+    if (p.top_ids) p.top_ids[row * p.top + k] = listed ? lp_key_index(key) : -1;
+    if (p.top_logprobs)
+        p.top_logprobs[row * p.top + k] = listed ? lp_log(p, x, m, lnz) : -INFINITY;
+}
+
+// How many of n keys in shared memory are above k.
+__device__ __forceinline__ int lp_above(const unsigned long long* keys, int n, unsigned long long k) {
+    int r = 0;
+    for (int j = 0; j < n; ++j) r += keys[j] > k ? 1 : 0;
+    return r;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams p, LpPart* parts,
+                                                             unsigned long long* lists, int split) {
+    constexpr int VEC = BF16 ? 8 : 4, N = kLpEach / VEC;  // entries of a load, loads of a chunk
+    using X = std::conditional_t<BF16, uint16_t, float>;
+    __shared__ unsigned long long s_best[kMaxTop], s_cand[kCand + kMaxTop], s_max[kLpThreads];
+    __shared__ unsigned long long s_tau;
+    __shared__ int s_n;
+    __shared__ LpSum s_sum[kLpThreads / 32];
+    __shared__ int s_before[kLpThreads / 32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long row = blockIdx.x / split;
+    const int part = static_cast<int>(blockIdx.x - row * split);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (p.len && static_cast<int>(row % p.R) >= __ldg(p.len + row / p.R)) return;
+    const X* x = static_cast<const X*>(p.x) + row * p.ldx;
+    // entries counted from the 16 bytes that hold the first one
+    const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(X));
+    const X* base = x - shift;
+    const int chunks = (p.V + shift + kLpChunk - 1) / kLpChunk;
+    const int c0 = chunks * part / split, c1 = chunks * (part + 1) / split;
+    const int t = p.tokens ? __ldg(p.tokens + row) : -1;
+    const bool here = t >= 0 && t < p.V;
+    if (t < -1 || t >= p.V) {
+        if (tid == 0 && part == 0) atomicOr(p.status, kLpBadId);
+    }
+    auto value = [](X raw) {
+        const float f = BF16 ? __uint_as_float(static_cast<uint32_t>(raw) << 16)
+                             : *reinterpret_cast<const float*>(&raw);
+        return fmaxf(f, -INFINITY);  // (a NaN reads as -infinity)
+    };
+    const float xt = here ? value(x[t]) : INFINITY;
+    const float c2 = p.scale * kLog2e;
+
+    uint4 next[N];
+    const int end = shift + p.V;
+    auto fetch = [&](int c) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int at = (c * (kLpChunk / VEC) + k * kLpThreads + tid) * VEC;  // from base
+            if (at >= shift && at + VEC <= end) {
+                next[k] = __ldcs(reinterpret_cast<const uint4*>(base + at));
+            } else {
+                uint32_t w[4] = {};
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    uint32_t raw = BF16 ? 0xFF80u : 0xFF800000u;  // -infinity
+                    if (at + j >= shift && at + j < end) {
+                        const X v = base[at + j];
+                        raw = BF16 ? static_cast<uint32_t>(v) : *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                    w[BF16 ? j / 2 : j & 3] |= BF16 && (j & 1) ? raw << 16 : raw;
+                }
+                next[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    };
+    LpSum s{-INFINITY, 0.f, 0.f};
+    int before = 0;
+    float tau = -INFINITY;  // of the list's last entry: what is larger is a candidate
+    if (tid < kMaxTop) s_best[tid] = 0ull;
+    if (c0 < c1) fetch(c0);
+    for (int c = c0; c < c1; ++c) {
+        float f[kLpEach];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const uint32_t w[4] = {next[k].x, next[k].y, next[k].z, next[k].w};
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const uint32_t raw = BF16 ? (j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16) : w[j & 3];
+                f[k * VEC + j] = fmaxf(__uint_as_float(raw), -INFINITY);
+            }
+        }
+        if (c + 1 < c1) fetch(c + 1);
+        float mx = f[0];
+#pragma unroll
+        for (int k = 1; k < kLpEach; ++k) mx = fmaxf(mx, f[k]);
+        if (mx > s.m) s = lp_move(s, mx, c2);
+        if (s.m == INFINITY) {
+#pragma unroll
+            for (int k = 0; k < kLpEach; ++k) s.z += f[k] == INFINITY ? 1.f : 0.f;
+        } else {
+            const float m = s.m == -INFINITY ? 0.f : s.m;
+            float z = 0.f, w = 0.f;
+#pragma unroll
+            for (int k = 0; k < kLpEach; ++k) {
+                const float d = fmaxf((f[k] - m) * c2, -kLpFar);
+                const float e = ex2(d);
+                z += e;
+                w = fmaf(e, d, w);
+            }
+            s.z += z;
+            s.w += w;
+        }
+        auto index = [&](int k) {
+            return (c * (kLpChunk / VEC) + (k / VEC) * kLpThreads + tid) * VEC + k % VEC - shift;
+        };
+        if (here) {
+#pragma unroll
+            for (int k = 0; k < kLpEach; ++k)
+                before += f[k] > xt || (f[k] == xt && index(k) >= 0 && index(k) < t) ? 1 : 0;
+        }
+        if (p.top == 0) continue;
+        if (!__syncthreads_or(mx > tau)) continue;
+        // ---- some entry may belong to the list
+        unsigned long long thr = s_best[p.top - 1];
+        int mine = 0;
+#pragma unroll
+        for (int k = 0; k < kLpEach; ++k) mine += f[k] > tau ? 1 : 0;
+        if (tid == 0) s_n = 0;
+        __syncthreads();
+        int at = mine ? atomicAdd(&s_n, mine) : 0;
+        __syncthreads();
+        if (s_n > kCand) {
+            unsigned long long best = 0;
+#pragma unroll
+            for (int k = 0; k < kLpEach; ++k)
+                if (f[k] > -INFINITY) best = max(best, lp_key(f[k], index(k)));
+            // (threads without entries: keys of their own below every entry's)
+            if (best == 0) best = static_cast<unsigned long long>(tid);
+            s_max[tid] = best;
+            __syncthreads();
+            if (lp_above(s_max, kLpThreads, best) == p.top - 1) s_tau = best;
+            if (tid == 0) s_n = 0;
+            __syncthreads();
+            thr = max(thr, s_tau - 1);  // (that entry itself is a candidate)
+            mine = 0;
+#pragma unroll
+            for (int k = 0; k < kLpEach; ++k)
+                mine += f[k] > -INFINITY && lp_key(f[k], index(k)) > thr ? 1 : 0;
+            at = mine ? atomicAdd(&s_n, mine) : 0;
+        }
+        if (mine) {
+#pragma unroll
+            for (int k = 0; k < kLpEach; ++k)
+                if (f[k] > -INFINITY && lp_key(f[k], index(k)) > thr) s_cand[at++] = lp_key(f[k], index(k));
+        }
+        __syncthreads();
+        const int n = s_n;
+        if (tid < p.top) s_cand[n + tid] = s_best[tid];
+        __syncthreads();
+        for (int j = tid; j < n + p.top; j += kLpThreads) {
+            const unsigned long long key = s_cand[j];
+            const int r = key ? lp_above(s_cand, n + p.top, key) : p.top;
+            if (r < p.top) s_best[r] = key;
+        }
+        __syncthreads();
+        const unsigned long long last = s_best[p.top - 1];
+        tau = last ? lp_key_value(last) : -INFINITY;
+    }
+
+    // ---- the block's threads
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const LpSum q{__shfl_xor_sync(0xffffffffu, s.m, o), __shfl_xor_sync(0xffffffffu, s.z, o),
+                      __shfl_xor_sync(0xffffffffu, s.w, o)};
+        s = lp_add(s, q, c2);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    if (lane == 0) {
+        s_sum[warp] = s;
+        s_before[warp] = before;
+    }
+    __syncthreads();
+    s = s_sum[0];
+    before = s_before[0];
+#pragma unroll
+    for (int k = 1; k < kLpThreads / 32; ++k) {
+        s = lp_add(s, s_sum[k], c2);
+        before += s_before[k];
+    }
+    const long long slot = row * split + part;
+    if (split > 1) {
+        if (tid == 0) parts[slot] = LpPart{s.m, s.z, s.w, before};
+        if (tid < p.top) lists[slot * p.top + tid] = s_best[tid];
+        return;
+    }
+    if (tid == 0) lp_write(p, row, s, before, t, xt);
+    if (tid < p.top) lp_write_top(p, row, tid, s_best[tid], s.m, logf(s.z));
+}
+
+// Joins the parts of a row, a block a row.
+template <bool BF16>
+__global__ void __launch_bounds__(kLpThreads) logprob_join_kernel(const LogprobParams p,
+                                                                  const LpPart* parts,
+                                                                  const unsigned long long* lists,
+                                                                  int split) {
+    using X = std::conditional_t<BF16, uint16_t, float>;
+    __shared__ unsigned long long s_head[kLpMaxSplit], s_cand[kMaxTop * kMaxTop], s_tau;
+    __shared__ LpPart s_part[kLpMaxSplit];
+    __shared__ int s_n;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x;
+    const long long row = blockIdx.x;
+    if (p.len && static_cast<int>(row % p.R) >= __ldg(p.len + row / p.R)) return;
+    const int t = p.tokens ? __ldg(p.tokens + row) : -1;
+    float xt = INFINITY;
+    if (tid == 0 && t >= 0 && t < p.V) {
+        const X raw = static_cast<const X*>(p.x)[row * p.ldx + t];
+        xt = fmaxf(BF16 ? __uint_as_float(static_cast<uint32_t>(raw) << 16)
+                        : *reinterpret_cast<const float*>(&raw), -INFINITY);
+    }
+    if (tid < split) {
+        s_part[tid] = parts[row * split + tid];
+        s_head[tid] = p.top ? lists[(row * split + tid) * p.top] : 0ull;
+    }
+    if (tid == 0) s_n = 0, s_tau = 0ull;
+    __syncthreads();
+    LpSum s{s_part[0].m, s_part[0].z, s_part[0].w};
+    int before = s_part[0].before;
+    for (int k = 1; k < split; ++k) {
+        s = lp_add(s, LpSum{s_part[k].m, s_part[k].z, s_part[k].w}, p.scale * kLog2e);
+        before += s_part[k].before;
+    }
+    if (tid == 0) lp_write(p, row, s, before, t, xt);
+    if (p.top == 0) return;
+    // of the `top` largest heads the least: the row's `top` largest are not below it, and lie
+    // in those lists (with fewer parts: in any)
+    if (tid < split && s_head[tid] && lp_above(s_head, split, s_head[tid]) == p.top - 1)
+        s_tau = s_head[tid];
+    __syncthreads();
+    const unsigned long long tau = s_tau;
+    for (int j = tid; j < split * p.top; j += kLpThreads) {
+        const unsigned long long key = s_head[j / p.top] < tau || s_head[j / p.top] == 0ull
+                                           ? 0ull
+                                           : lists[row * split * p.top + j];
+        if (key != 0ull && key >= tau) s_cand[atomicAdd(&s_n, 1)] = key;
+    }
+    __syncthreads();
+    const int n = s_n;
+    const float lnz = logf(s.z);
+    for (int j = tid; j < n; j += kLpThreads) {
+        const int r = lp_above(s_cand, n, s_cand[j]);
+        if (r < p.top) lp_write_top(p, row, r, s_cand[j], s.m, lnz);
+    }
+    if (tid >= n && tid < p.top) lp_write_top(p, row, tid, 0ull, s.m, lnz);
+}
+
+cudaError_t launch_logprobs(const LogprobParams& p, void* ws, int sms, cudaStream_t s) {
+    (void)sms;
+    const long long rows = static_cast<long long>(p.B) * p.R;
+    const int split = lp_split(rows, p.V);
+    LpPart* parts = static_cast<LpPart*>(ws);
+    unsigned long long* lists = reinterpret_cast<unsigned long long*>(parts + rows * split);
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * split));
+    cudaError_t e = cudaLaunchKernelEx(&cfg, p.x_bf16 ? logprob_kernel<true> : logprob_kernel<false>,
+                                       p, parts, lists, split);
+    if (e != cudaSuccess || split == 1) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(rows));
+    return cudaLaunchKernelEx(&cfg, p.x_bf16 ? logprob_join_kernel<true> : logprob_join_kernel<false>,
+                              p, static_cast<const LpPart*>(parts),
+                              static_cast<const unsigned long long*>(lists), split);
+}
+
+}  // namespace vw4

@@ -1,7 +1,7 @@
 // rope_append.cu -- from the packed qkv rows of the verify GEMM to rotated
 // queries and cache entries: per head an optional RMS norm, the rotation of
 // its leading dimensions by the token's position, and the rounding to bf16 or
-// (for the cache) to e4m3 of value / scale.
+// (for the cache) to e4m3 of value / scale or to nvfp4.
 //
 // One pass: every value is read once and written once, so the bytes bound it: 2304
 // tokens of 32 heads of 256 (fp32 in, bf16 and e4m3 out) take 23 us, 70 % of the copy
@@ -69,14 +69,192 @@ __device__ __forceinline__ void store_unit(uint8_t* p, const float* v) {
     }
 }
 
-template <int D, bool F8, bool XBF16>
+// ---------------------------------------------------------------- 4-bit caches
+// A head's D values in their order, D / 32 to a lane, so that 512 / D lanes hold the 16
+// values of a block.  t = y / g, block scale s = e4m3(max |t| / 6), codes e2m1(t / s).
+//
+// The codes are to be those of the 64-bit formula, but 64-bit arithmetic has 1/64 of the
+// rate of 32-bit.  So 32 bits give t and how far it may be off, and both ends of that
+// range are rounded: where they agree, so does everything between (rounding is
+// monotone).  Where they do not (about three heads in a thousand), the warp takes that
+// head's norm again in 64 bits, and the lanes with such a value that value.
+//
+// kValueError bounds the error of a key against |a| + |c| of its plane, or |y| of a value
+// that is normed and not turned: the norm's sum of squares 13 roundings of 2^-24,
+// halved by the root, rsqrtf two steps, the two factors and the mean one each: 2^-20.2;
+// angle, sine and cosine 2^-22.2, products and sum 2^-23: below 2^-19.
+constexpr float kValueError = 1.9073486328125e-6f;  // 2^-19
+constexpr float kDivError = 2.384185791015625e-7f;  // 2^-22, of a quotient by a quotient
+
+// Dimension d of a key or value over its head's scale, from the 64-bit formula.
+template <int D, class X>
+__device__ __noinline__ double kv4_exact(const AppendParams& p, const X* x, bool is_k, int d,
+                                         double f, int pos, float g) {
+    const float* w = is_k ? p.k_norm : nullptr;
+    auto at = [&](int k) {
+        double y = static_cast<double>(static_cast<float>(x[k]));
+        if (w) y = y * f * static_cast<double>(w[k]);
+        return y;
+    };
+    double y = at(d);
+    if (is_k && d < p.rot) {
+        const int half = p.rot / 2, j = p.adjacent ? d >> 1 : (d < half ? d : d - half);
+        const bool second = p.adjacent ? d & 1 : d >= half;
+        const double c = at(p.adjacent ? d ^ 1 : (second ? d - half : d + half));
+        double sn, cs;
+        sincos(static_cast<double>(pos) * p.inv_freq[j], &sn, &cs);
+        y = second ? y * cs + c * sn : y * cs - c * sn;
+    }
+    return g == 0.f ? 0.0 : y / static_cast<double>(g);
+}
+
+__device__ __forceinline__ uint32_t e4m3_byte(float v) {
+    return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float e4m3_value(uint32_t b) {
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3)));
+}
+// code of a magnitude, 0 .. 7, and what a code stands for
+__device__ __forceinline__ uint32_t e2m1_code(float v) {
+    uint16_t r;
+    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b16 %0, {t, 0};\n\t}"
+        : "=h"(r) : "f"(0.f), "f"(v));
+    return r & 7u;
+}
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+    return c < 4 ? 0.5f * static_cast<float>(c) : (c & 1 ? 1.5f : 1.f) * (c < 6 ? 2.f : 4.f);
+}
+
+template <int D, class X>
+__device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, const float* head,
+                                          const float* offs, bool is_k, int hk, int pos,
+                                          long long at, long long bat, int lane) {
+    constexpr int N = D / 32, GL = 16 / N;  // values of a lane, lanes of a block
+    const float* sp = is_k ? p.k_scale : p.v_scale;
+    const float g = sp ? __ldg(sp + hk) : 1.f;
+    const float ag = g == 0.f ? INFINITY : fabsf(g);
+    float t[N], e[N];
+    float lo = 0.f, hi = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const float y = head[lane * N + k], off = offs[lane * N + k];
+        t[k] = g == 0.f ? 0.f : __fdiv_rn(y, g);
+        nan |= t[k] != t[k];
+        const float m = fminf(fabsf(t[k]), 2688.f);
+        // Nothing is lost: no rounding before, and the quotient is exact; an infinity, or a
+        // quotient beyond 2^20, is 2688 for sure.  The quotients of such an m by s and by 6
+        // need no margin either: a border times s, or 6, has at most 8 significant bits, so an
+        // m beside it is off by over 2^-24 of itself, and the rounded quotient stays beside.
+        const bool sure = fabsf(t[k]) > 1048576.f || g == 0.f || (off == 0.f && fmaf(t[k], g, -y) == 0.f);
+        e[k] = sure ? 0.f : __fdiv_rn(off, ag) + m * kDivError;
+        lo = fmaxf(lo, m - e[k]);
+        hi = fmaxf(hi, fminf(m + e[k], 2688.f));
+    }
+    unsigned bad = nan;
+#pragma unroll
+    for (int o = 1; o < GL; o <<= 1) {
+        lo = fmaxf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+    }
+    const float wide = lo == hi ? 0.f : kDivError;  // (the quotients are off by half a step)
+    uint32_t sb = e4m3_byte(__fdiv_rn(lo, 6.f) * (1.f - wide));
+    const uint32_t sb1 = e4m3_byte(__fdiv_rn(hi, 6.f) * (1.f + wide));
+    double f = 0.0;
+    bool have_f = false;
+    auto need_norm = [&] {  // all lanes
+        if (have_f) return;
+        have_f = true;
+        if (!is_k || !p.k_norm) return;
+        double ss = 0.0;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const double v = static_cast<double>(static_cast<float>(x[lane * N + k]));
+            ss += v * v;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        f = 1.0 / sqrt(ss / D + static_cast<double>(p.eps));
+    };
+    if (__any_sync(0xffffffffu, sb != sb1 && !bad)) {
+        need_norm();
+        double a = 0.0;
+        if (sb != sb1 && !bad) {
+#pragma unroll 1
+            for (int k = 0; k < N; ++k) {
+                float tk = t[0], ek = e[0];  // (registers: no index at run time)
+#pragma unroll
+                for (int q = 1; q < N; ++q) tk = q == k ? t[q] : tk, ek = q == k ? e[q] : ek;
+                if (fminf(fabsf(tk), 2688.f) + ek >= lo)
+                    a = fmax(a, fmin(fabs(kv4_exact<D, X>(p, x, is_k, lane * N + k, f, pos, g)), 2688.0));
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < GL; o <<= 1) a = fmax(a, __shfl_xor_sync(0xffffffffu, a, o));
+        if (sb != sb1 && !bad) {
+            // the scale of the range that is nearest
+            const double q = a / 6.0;
+            while (sb < sb1) {
+                const double mid = 0.5 * (static_cast<double>(e4m3_value(sb)) + e4m3_value(sb + 1));
+                if (q < mid || (q == mid && !(sb & 1u))) break;
+                ++sb;
+            }
+        }
+    }
+    if (bad) sb = 0x7Fu;
+    const float s = e4m3_value(sb);
+    const bool some = sb != 0u && !bad;
+    uint32_t c[N];
+    uint32_t unsure = 0, minus = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const float m = fminf(fabsf(t[k]), 2688.f);
+        const float q = some ? __fdiv_rn(m, s) : 0.f;
+        const float dq = some && e[k] > 0.f ? __fdiv_rn(e[k], s) + q * kDivError : 0.f;
+        c[k] = e2m1_code(q - dq > 0.f ? q - dq : 0.f);
+        if (c[k] != e2m1_code(q + dq)) unsure |= 1u << k;
+        if (t[k] < 0.f) minus |= 1u << k;
+    }
+    if (__any_sync(0xffffffffu, unsure != 0)) {
+        need_norm();
+#pragma unroll 1
+        for (int k = 0; k < N; ++k) {
+            if (!((unsure >> k) & 1u)) continue;
+            const double v = kv4_exact<D, X>(p, x, is_k, lane * N + k, f, pos, g);
+            const double q = fmin(fabs(v), 2688.0) / static_cast<double>(s);
+            minus = (minus & ~(1u << k)) | (v < 0.0 ? 1u << k : 0u);
+            uint32_t n = 0;
+            while (n < 7) {
+                const double mid = 0.5 * (static_cast<double>(e2m1_value(n)) + e2m1_value(n + 1));
+                if (q < mid || (q == mid && !(n & 1u))) break;
+                ++n;
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) c[j] = j == k ? n : c[j];
+        }
+    }
+    uint32_t w = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) w |= (c[k] | ((minus >> k) & 1u) << 3) << (4 * k);
+    uint8_t* dst = static_cast<uint8_t*>(is_k ? p.k : p.v) + at + lane * (N / 2);
+    if (N == 8) *reinterpret_cast<uint32_t*>(dst) = w;
+    else if (N == 4) *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(w);
+    else *dst = static_cast<uint8_t>(w);
+    uint8_t* bl = is_k ? p.k_blocks : p.v_blocks;
+    if (lane % GL == 0) bl[bat + lane / GL] = static_cast<uint8_t>(sb);
+}
+
+template <int D, int KIND, bool XBF16>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams p,
                                                                    int heads_per_block) {
+    constexpr bool F8 = KIND == kCacheE4m3, KV4 = KIND == kCacheKv4;
     constexpr int U = D / 64;  // dimensions of a unit; a lane has two
     using X = std::conditional_t<XBF16, __nv_bfloat16, float>;
-    using C = std::conditional_t<F8, uint8_t, __nv_bfloat16>;
+    using C = std::conditional_t<KIND == kCacheBf16, __nv_bfloat16, uint8_t>;
     __shared__ __align__(16) float s_cos[kMaxPairs], s_sin[kMaxPairs];
     __shared__ __align__(16) float s_head[kAppendWarps][D];
+    __shared__ __align__(16) float s_off[KV4 ? kAppendWarps : 1][KV4 ? D : 1];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int token = blockIdx.x, b = token / p.R, i = token - b * p.R;
@@ -104,16 +282,19 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
         sincospif(static_cast<float>(2.0 * turns), &s_sin[j], &s_cos[j]);
     }
     // the token's cache slot
-    long long slot = -1;
+    long long slot = -1, bslot = 0;
     if (pos >= 0) {
         const int blk = pos >> p.page_shift;
         const int pg = blk < p.max_blocks
                            ? __ldg(p.table + static_cast<long long>(b) * p.table_stride + blk)
                            : -1;
-        if (pg >= 0 && pg < p.num_pages)
+        if (pg >= 0 && pg < p.num_pages) {
             slot = static_cast<long long>(pg) * p.page_stride +
                    static_cast<long long>(pos & (p.page_size - 1)) * p.token_stride;
-        else if (threadIdx.x == 0)
+            if (KV4)
+                bslot = static_cast<long long>(pg) * p.blocks_page_stride +
+                        static_cast<long long>(pos & (p.page_size - 1)) * (D / 16);
+        } else if (threadIdx.x == 0)
             atomicOr(p.status, kStatusBadPage);
     }
     __syncthreads();
@@ -127,6 +308,11 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
     for (; h < h_end; h += kAppendWarps) {
         if (h + kAppendWarps < h_end) load(h + kAppendWarps, nx);
         const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
+        float off[KV4 ? 2 * U : 1];  // 4-bit keys: what a value may be off by
+        if (KV4) {
+#pragma unroll
+            for (int k = 0; k < 2 * U; ++k) off[KV4 ? k : 0] = 0.f;
+        }
         if (is_q || is_k) {
             const float* w = is_q ? p.q_norm : p.k_norm;
             if (w) {
@@ -141,12 +327,17 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
                 load_unit<U>(w + d1, g + U);
 #pragma unroll
                 for (int k = 0; k < 2 * U; ++k) v[k] = v[k] * f * g[k];
+                if (KV4 && is_k) {
+#pragma unroll
+                    for (int k = 0; k < 2 * U; ++k) off[KV4 ? k : 0] = fabsf(v[k]);
+                }
             }
             if (split) {
                 if (lane < P) {
 #pragma unroll
                     for (int k = 0; k < U; ++k) {
                         const float a = v[k], c = v[U + k];
+                        if (KV4) off[KV4 ? k : 0] = off[KV4 ? U + k : 0] = fabsf(a) + fabsf(c);
                         v[k] = a * cs[k] - c * sn[k];
                         v[U + k] = c * cs[k] + a * sn[k];
                     }
@@ -158,6 +349,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
                     const int j = (d0 + k) / 2;
                     if (j < pairs) {
                         const float a = v[k], c = v[k + 1];
+                        if (KV4) off[KV4 ? k : 0] = off[KV4 ? k + 1 : 0] = fabsf(a) + fabsf(c);
                         v[k] = a * s_cos[j] - c * s_sin[j];
                         v[k + 1] = c * s_cos[j] + a * s_sin[j];
                     }
@@ -171,6 +363,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
 #pragma unroll
                 for (int k = 0; k < 2 * U; ++k) {
                     const int d = d0 + k;
+                    if (KV4 && d < p.rot)
+                        off[KV4 ? k : 0] =
+                            fabsf(v[k]) + fabsf(s_head[warp][d < pairs ? d + pairs : d - pairs]);
                     if (d < pairs) v[k] = v[k] * s_cos[d] - s_head[warp][d + pairs] * s_sin[d];
                     else if (d < p.rot)
                         v[k] = v[k] * s_cos[d - pairs] + s_head[warp][d - pairs] * s_sin[d - pairs];
@@ -181,6 +376,23 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
             __nv_bfloat16* dst = p.q + static_cast<long long>(token) * p.ldq + static_cast<long long>(h) * D;
             store_unit<U>(dst + d0, v);
             store_unit<U>(dst + d1, v + U);
+        } else if (KV4) {
+            if (slot >= 0) {  // (the same for the warp)
+                __syncwarp();  // the last head's reads are done
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    s_head[warp][d0 + k] = v[k];
+                    s_head[warp][d1 + k] = v[U + k];
+                    s_off[KV4 ? warp : 0][KV4 ? d0 + k : 0] = off[KV4 ? k : 0] * kValueError;
+                    s_off[KV4 ? warp : 0][KV4 ? d1 + k : 0] = off[KV4 ? U + k : 0] * kValueError;
+                }
+                __syncwarp();
+                const int hk = is_k ? h - p.Hq : h - p.Hq - p.Hkv;
+                store_kv4<D, X>(p, x + static_cast<long long>(h) * D, s_head[warp],
+                                s_off[KV4 ? warp : 0], is_k, hk, pos,
+                                slot + static_cast<long long>(hk) * p.head_stride,
+                                bslot + static_cast<long long>(hk) * p.blocks_head_stride, lane);
+            }
         } else if (slot >= 0) {
             const int hk = is_k ? h - p.Hq : h - p.Hq - p.Hkv;
             C* dst = static_cast<C*>(is_k ? p.k : p.v) + slot + static_cast<long long>(hk) * p.head_stride;
@@ -200,12 +412,15 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
 }
 
 template <int D>
-static void (*append_of(bool f8, bool bf16))(const AppendParams, int) {
-    if (f8) return bf16 ? append_kernel<D, true, true> : append_kernel<D, true, false>;
-    return bf16 ? append_kernel<D, false, true> : append_kernel<D, false, false>;
+static void (*append_of(int kind, bool bf16))(const AppendParams, int) {
+    if (kind == kCacheKv4)
+        return bf16 ? append_kernel<D, kCacheKv4, true> : append_kernel<D, kCacheKv4, false>;
+    if (kind == kCacheE4m3)
+        return bf16 ? append_kernel<D, kCacheE4m3, true> : append_kernel<D, kCacheE4m3, false>;
+    return bf16 ? append_kernel<D, kCacheBf16, true> : append_kernel<D, kCacheBf16, false>;
 }
 
-cudaError_t launch_append(const AppendParams& p, bool f8, int sms, cudaStream_t s) {
+cudaError_t launch_append(const AppendParams& p, int kind, int sms, cudaStream_t s) {
     const int tokens = p.B * p.R, heads = p.Hq + 2 * p.Hkv;
     // one head a warp while that leaves SMs idle; else more heads share a block's angles
     // (a 64-bit product and a sine and cosine for each of up to 128 planes).  Sixteen
@@ -229,9 +444,9 @@ cudaError_t launch_append(const AppendParams& p, bool f8, int sms, cudaStream_t 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const bool bf16 = p.x_bf16 != 0;
-    void (*k)(const AppendParams, int) = p.D == 64    ? append_of<64>(f8, bf16)
-                                         : p.D == 128 ? append_of<128>(f8, bf16)
-                                                      : append_of<256>(f8, bf16);
+    void (*k)(const AppendParams, int) = p.D == 64    ? append_of<64>(kind, bf16)
+                                         : p.D == 128 ? append_of<128>(kind, bf16)
+                                                      : append_of<256>(kind, bf16);
     return cudaLaunchKernelEx(&cfg, k, p, per);
 }
 

@@ -102,7 +102,8 @@ VW4_API vw4_status verify_rope_append(const vw4_append* a, void* stream) {
     p.max_blocks = c.max_blocks;
     p.num_pages = c.num_pages;
     const cudaError_t e =
-        launch_append(p, c.dtype == VW4_KV_E4M3, sms, static_cast<cudaStream_t>(stream));
+        launch_append(p, c.dtype == VW4_KV_E4M3 ? kCacheE4m3 : kCacheBf16, sms,
+                      static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return static_cast<vw4_status>(report_cuda(e, "verify_rope_append launch"));
     return VW4_OK;

@@ -292,8 +292,13 @@ struct AppendParams {
     long long table_stride, page_stride, token_stride, head_stride;
     int B, R, Hq, Hkv, D;
     int page_size, page_shift, max_blocks, num_pages;
+    // 4-bit caches: block scales (strides of the values are in bytes then)
+    uint8_t* k_blocks;
+    uint8_t* v_blocks;
+    long long blocks_page_stride, blocks_head_stride;
 };
-cudaError_t launch_append(const AppendParams& p, bool f8, int sms, cudaStream_t s);
+constexpr int kCacheBf16 = 0, kCacheE4m3 = 1, kCacheKv4 = 2;
+cudaError_t launch_append(const AppendParams& p, int kind, int sms, cudaStream_t s);
 
 // ---- penalties, biases and masks on the verify logits (logits.cu)
 struct LogitsParams {
@@ -317,6 +322,92 @@ struct LogitsParams {
     int B, R, V, hist_max, bias_max, mask_rows;
 };
 cudaError_t launch_logits(const LogitsParams& p, int sms, cudaStream_t s);
+
+// ---- the 4-bit cache (attn4*.cu, read4.cu)
+struct Kv4Blocks {             // block scales of K and V
+    const uint8_t* k;
+    const uint8_t* v;
+    long long page_stride, head_stride;  // bytes
+};
+size_t attn4_workspace_bytes(int B, int rows, int D);
+struct Attn4Plan {
+    int nt, grid;              // n-tiles of 8 query rows, bound of the grid
+    int box_bytes;
+    CUtensorMapSwizzle swizzle;
+};
+Attn4Plan attn4_plan(AttnParams& p, int D, void* ws);
+cudaError_t launch_attn4(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps,
+                         const Attn4Plan& plan, int D, int sms, cudaStream_t s);
+cudaError_t launch_attn4_d64(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps, int nt,
+                             int* grid, int sms, cudaStream_t s);
+cudaError_t launch_attn4_d128(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps, int nt,
+                              int* grid, int sms, cudaStream_t s);
+cudaError_t launch_attn4_d256(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps, int nt,
+                              int* grid, int sms, cudaStream_t s);
+// The join of an attention call's partials (attn.cu).
+cudaError_t launch_attn_join(const AttnParams& p, int D, int rows, int grid, int tk, int sms,
+                             cudaStream_t s);
+struct Read4Params {
+    const uint8_t* k;
+    const uint8_t* v;
+    Kv4Blocks blocks;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* table;
+    const int32_t* seq_lens;
+    const int32_t* first;      // or null
+    void* k_out;
+    void* v_out;
+    uint32_t* status;
+    long long table_stride, page_stride, token_stride, head_stride;
+    int B, n, Hkv, D, out_f32;
+    int page_size, page_shift, max_blocks, num_pages;
+};
+cudaError_t launch_read4(const Read4Params& p, int sms, cudaStream_t s);
+
+// ---- pages and slots of the next rows (advance.cu)
+constexpr uint32_t kStatusNoRoom = 0x80u;
+struct AdvanceParams {
+    int32_t* table;
+    const int32_t* lens;
+    const int32_t* accepted;   // or null
+    const int32_t* ended;      // or null
+    const int32_t* grow;       // or null: R
+    const int32_t* held;
+    int32_t* free_list;
+    const int32_t* free_count;
+    int32_t* lens_out;
+    int32_t* held_out;
+    int32_t* free_count_out;
+    int32_t* seq_lens;
+    int32_t* row_start;
+    long long* slots;          // or null
+    uint32_t* status;
+    long long table_stride, rows_max;
+    int B, R, page_size, page_shift, num_pages, max_blocks;
+};
+size_t advance_workspace_bytes(int B);
+cudaError_t launch_advance(const AdvanceParams& p, void* ws, int sms, cudaStream_t s);
+
+// ---- log probabilities of committed tokens (logprobs.cu)
+constexpr int kMaxTop = 32;
+struct LogprobParams {
+    const void* x;
+    const int32_t* tokens;     // or null
+    const int32_t* len;        // or null
+    float* logprob;            // the outputs: or null
+    float* lse;
+    float* entropy;
+    int32_t* rank;
+    int32_t* top_ids;
+    float* top_logprobs;
+    uint32_t* status;
+    long long ldx;
+    float scale;
+    int B, R, V, top, x_bf16;
+};
+size_t logprob_workspace_bytes(long long rows, int V, int top);
+cudaError_t launch_logprobs(const LogprobParams& p, void* ws, int sms, cudaStream_t s);
 
 // Copies the first `rows` row records of a rejection workspace (test hook).
 cudaError_t copy_rejection_row_records(const void* ws, long long rows, void* out,
