@@ -7,15 +7,17 @@
 // into the table and the rows' slots.  The second and the third look their sequence up in
 // the prefix sums, so that one long prompt is spread over the whole grid.
 //
-// Small calls (table and slots of at most kOneBlock* entries) are one block's work and one
-// launch: a chain of latencies, as the scans of the others are.  The slots bound large ones.
+// Everything here is a chain of load latencies: the scan keeps its sequences in registers
+// from one load, a warp finds its sequence with 32 probes at a time (three steps for 16384
+// sequences instead of fourteen), and takes few entries.  Small calls (table and slots of
+// at most kOneBlock* entries) are one block's work and one launch.
 #include "vw4_internal.cuh"
 
 namespace vw4 {
 
 constexpr int kAdvThreads = 1024;
 constexpr int kFillThreads = 256;
-constexpr int kWarpSlots = 256;          // consecutive entries that a warp takes at a time
+constexpr int kWarpSlots = 64;           // consecutive entries that a warp takes at a time
 constexpr long long kOneBlockTable = 65536, kOneBlockSlots = 8192;
 
 struct AdvancePlan {
@@ -35,22 +37,23 @@ size_t advance_workspace_bytes(int B) {
     return ((2 * (static_cast<size_t>(B) + 1) + 2) * sizeof(long long) + 255) & ~size_t(255);
 }
 
-// What a call gives of one sequence.
+// What a call finds of one sequence.  Lengths saturate at 2^31 - 1: beyond every table.
 struct AdvSeq {
-    long long len, grow, need;  // need: -1 where the table is too short
-    int held, back;             // pages kept, pages given back
+    int len, grow, need;   // need: -1 where the table is too short
+    int held, back;        // pages kept, pages given back
 };
 __device__ __forceinline__ AdvSeq adv_seq(const AdvanceParams& p, int b) {
     AdvSeq s;
     const bool ended = p.ended && p.ended[b] != 0;
     const int held = max(0, min(p.max_blocks, p.held[b]));
     const long long acc = p.accepted ? max(0, p.accepted[b]) : 0;
-    s.len = ended ? 0 : max(0, p.lens[b]) + acc;
+    const long long len = ended ? 0 : max(0, p.lens[b]) + acc;
+    s.len = static_cast<int>(min(len, 2147483647LL));
     s.held = ended ? 0 : held;
     s.back = ended ? held : 0;
     s.grow = p.grow ? max(0, p.grow[b]) : p.R;
-    const long long cols = (s.len + s.grow + p.page_size - 1) >> p.page_shift;
-    s.need = cols > p.max_blocks ? -1 : max(0LL, cols - s.held);
+    const long long cols = (len + s.grow + p.page_size - 1) >> p.page_shift;
+    s.need = cols > p.max_blocks ? -1 : max(0, static_cast<int>(cols) - s.held);
     return s;
 }
 
@@ -83,57 +86,66 @@ __device__ __forceinline__ Pair block_scan(Pair v, Pair* total, Pair* s_warp) {
     return Pair{in.a - v.a + ba, in.b - v.b + bb};
 }
 
-// Phase 1, by one block of kAdvThreads.
-__device__ void scan_phase(const AdvanceParams& p, const AdvancePlan& w) {
+// Phase 1, by one block of kAdvThreads, PER sequences a thread.
+template <int PER>
+__device__ __forceinline__ void scan_phase(const AdvanceParams& p, const AdvancePlan& w) {
     static_assert(kAdvThreads == 1024, "32 warps");
     __shared__ Pair s_warp[32];
-    const int per = (p.B + kAdvThreads - 1) / kAdvThreads, b0 = threadIdx.x * per;
-    const int b1 = min(p.B, b0 + per);
+    const int b0 = threadIdx.x * PER;
     const long long stock = max(0, min(p.num_pages, p.free_count[0]));
+    AdvSeq s[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        s[k] = AdvSeq{0, 0, 0, 0, 0};
+        if (b0 + k < p.B) s[k] = adv_seq(p, b0 + k);
+    }
     bool short_of = false;
     Pair sum{0, 0}, total;
-    for (int b = b0; b < b1; ++b) {
-        const AdvSeq s = adv_seq(p, b);
-        sum.a += s.back;
-        sum.b += max(0LL, s.need);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        sum.a += s[k].back;
+        sum.b += max(0, s[k].need);
     }
+    // (every input of a sequence has been read before its outputs, which may be the inputs)
     Pair at = block_scan(sum, &total, s_warp);
     const long long count = min(static_cast<long long>(p.num_pages), stock + total.a);
     if (stock + total.a > p.num_pages) short_of = true;
-    // who gets what
-    const Pair first = at;
+    // who gets what: ok[k], and what that adds up to
+    uint32_t ok = 0;
+    long long need = at.b;
     sum = Pair{0, 0};
-    for (int b = b0; b < b1; ++b) {
-        const AdvSeq s = adv_seq(p, b);
-        const bool ok = s.need >= 0 && (s.need == 0 || at.b + s.need <= count);
-        at.b += max(0LL, s.need);
-        if (ok) {
-            sum.a += s.need;
-            sum.b += s.grow;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        if (s[k].need == 0 || (s[k].need > 0 && need + s[k].need <= count)) {
+            ok |= 1u << k;
+            sum.a += s[k].need;
+            sum.b += s[k].grow;
         }
+        need += max(0, s[k].need);
     }
+    const long long back_all = total.a;
     Pair got = block_scan(sum, &total, s_warp);
-    at = first;
-    for (int b = b0; b < b1; ++b) {
-        const AdvSeq s = adv_seq(p, b);  // (before any output, which may be an input)
-        const bool ok = s.need >= 0 && (s.need == 0 || at.b + s.need <= count);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int b = b0 + k;
+        if (b >= p.B) break;
+        const bool mine = (ok >> k) & 1u;
         w.back[b] = at.a;
         w.take[b] = got.a;
         p.row_start[b] = static_cast<int32_t>(min(got.b, 2147483647LL));
-        at.a += s.back;
-        at.b += max(0LL, s.need);
-        if (ok) {
-            got.a += s.need;
-            got.b += s.grow;
+        at.a += s[k].back;
+        if (mine) {
+            got.a += s[k].need;
+            got.b += s[k].grow;
         } else {
             short_of = true;
         }
-        p.lens_out[b] = static_cast<int32_t>(min(s.len, 2147483647LL));
-        p.held_out[b] = s.held + static_cast<int>(ok ? s.need : 0);
-        p.seq_lens[b] = ok && s.grow > 0 ? static_cast<int32_t>(s.len + s.grow) : 0;
+        p.lens_out[b] = s[k].len;
+        p.held_out[b] = s[k].held + (mine ? s[k].need : 0);
+        p.seq_lens[b] = mine && s[k].grow > 0 ? s[k].len + s[k].grow : 0;
     }
-    if (threadIdx.x == kAdvThreads - 1) {  // (its sums end with the last sequence)
-        w.back[p.B] = at.a;
+    if (threadIdx.x == 0) {
+        w.back[p.B] = back_all;
         w.take[p.B] = total.a;
         w.count[0] = stock;
         w.count[1] = count;
@@ -144,14 +156,17 @@ __device__ void scan_phase(const AdvanceParams& p, const AdvancePlan& w) {
     if (short_of) atomicOr(p.status, kStatusNoRoom);
 }
 
-// The sequence of entry i: the last with start[b] <= i.
+// The sequence of entry i, the same in all lanes: the last with start[b] <= i.
 template <class T>
 __device__ __forceinline__ int seq_of(const T* start, int B, long long i) {
-    int lo = 0, hi = B;  // start[lo] <= i < start[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (static_cast<long long>(start[mid]) <= i) lo = mid;
-        else hi = mid;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, span = B;  // start[lo] <= i < start[lo + span]
+    while (span > 1) {
+        const int step = (span + 31) / 32, at = (lane + 1) * step;
+        const bool low = at < span && static_cast<long long>(start[lo + at]) <= i;
+        const int n = __popc(__ballot_sync(0xffffffffu, low)) * step;
+        lo += n;
+        span = min(step, span - n);
     }
     return lo;
 }
@@ -204,11 +219,12 @@ __device__ __forceinline__ void fill_phase(const AdvanceParams& p, const Advance
     if (bad) atomicOr(p.status, kStatusBadPage);
 }
 
+template <int PER>
 __global__ void __launch_bounds__(kAdvThreads) advance_kernel(const AdvanceParams p,
                                                               const AdvancePlan w, int all) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    scan_phase(p, w);
+    scan_phase<PER>(p, w);
     if (!all) return;
     __syncthreads();
     const long long warp = threadIdx.x >> 5;
@@ -241,9 +257,13 @@ cudaError_t launch_advance(const AdvanceParams& p, void* ws, int sms, cudaStream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, advance_kernel, p, w, all);
+    cudaError_t e = p.B <= kAdvThreads       ? cudaLaunchKernelEx(&cfg, advance_kernel<1>, p, w, all)
+                    : p.B <= 4 * kAdvThreads ? cudaLaunchKernelEx(&cfg, advance_kernel<4>, p, w, all)
+                                             : cudaLaunchKernelEx(&cfg, advance_kernel<16>, p, w, all);
     if (e != cudaSuccess || all) return e;
-    cfg.gridDim = dim3(4 * sms);
+    // (a block takes 512 entries at a time; how many pages move only the device knows)
+    const long long blocks = (rows + 511) / 512;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks < sms ? sms : (blocks < 8LL * sms ? blocks : 8LL * sms)));
     cfg.blockDim = dim3(kFillThreads);
     if (p.ended) {
         e = cudaLaunchKernelEx(&cfg, advance_fill_kernel<false>, p, w);

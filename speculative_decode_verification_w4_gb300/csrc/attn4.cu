@@ -11,13 +11,13 @@ static int attn4_tiles(int rows) {
     const int n = (rows + 7) / 8;
     return n <= 4 ? n : (n <= 6 ? 6 : 8);
 }
-static int attn4_grid_cap(int D) { return D == 256 ? kAttnMaxGrid256 : kAttnMaxGrid64; }
+constexpr int kAttn4MaxGrid = kAttnMaxGrid64;  // (three blocks an SM at most)
 static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 size_t attn4_workspace_bytes(int B, int rows, int D) {
     const size_t r = 8 * static_cast<size_t>(attn4_tiles(rows < kAttn4MaxRows ? rows : kAttn4MaxRows));
     return align256((static_cast<size_t>(B) + 1) * sizeof(long long)) +
-           align256(2u * static_cast<size_t>(attn4_grid_cap(D)) * r * (D + 2) * sizeof(float));
+           align256(2u * static_cast<size_t>(kAttn4MaxGrid) * r * (D + 2) * sizeof(float));
 }
 
 Attn4Plan attn4_plan(AttnParams& p, int D, void* ws) {
@@ -37,10 +37,11 @@ Attn4Plan attn4_plan(AttnParams& p, int D, void* ws) {
                                          align256((static_cast<size_t>(p.B) + 1) * sizeof(long long)));
     // at most one CTA per tile that the table could hold
     const long long cap = static_cast<long long>(p.max_blocks) * p.page_size;
-    const long long units = static_cast<long long>(p.B) * p.groups * ((cap + kAttn4Tk - 1) / kAttn4Tk);
-    plan.grid = attn4_grid_cap(D);
+    plan.tk = attn4_tk(D, plan.nt);
+    const long long units = static_cast<long long>(p.B) * p.groups * ((cap + plan.tk - 1) / plan.tk);
+    plan.grid = kAttn4MaxGrid;
     if (units < plan.grid) plan.grid = static_cast<int>(units < 1 ? 1 : units);
-    p.box_rows = p.page_size < kAttn4Tk ? p.page_size : kAttn4Tk;
+    p.box_rows = p.page_size < plan.tk ? p.page_size : plan.tk;
     plan.box_bytes = D / 2;
     const long long group = 8 * p.token_stride;
     if (p.head_stride == D / 2 || p.Hkv == 1) {
@@ -64,7 +65,7 @@ cudaError_t launch_attn4(const AttnParams& p, const Kv4Blocks& kb, const AttnMap
                           : D == 128 ? launch_attn4_d128(p, kb, maps, plan.nt, &grid, sms, s)
                                      : launch_attn4_d256(p, kb, maps, plan.nt, &grid, sms, s);
     if (e != cudaSuccess) return e;
-    return launch_attn_join(p, D, 8 * plan.nt, grid, kAttn4Tk, sms, s);
+    return launch_attn_join(p, D, 8 * plan.nt, grid, plan.tk, sms, s);
 }
 
 }  // namespace vw4

@@ -10,12 +10,12 @@
 // where they are few.  K^T and V become f16 in registers, exactly: e2m1 times its block's
 // e4m3 scale has six significant bits.
 //
-// A tile.  Each of eight warps takes 16 keys for S = K Q^T (32 dimensions of 8 keys are a
-// register of codes a lane), forms P against the block's common reference, and leaves it in
-// shared memory; beside it, the warps leave V's scales as f16, token by token.  After the
-// barrier each warp takes 32 dimensions of V for O = V^T P^T (of all keys at head size 256,
-// of a half or a quarter below), so nothing is converted twice however many query rows there
-// are, and S of the next tile runs in the same phase: one barrier a tile.
+// A tile.  Each warp takes 16 or 32 keys for S = K Q^T (32 dimensions of 8 keys are a register
+// of codes a lane), forms P against the block's common reference, and leaves it in shared
+// memory; beside it, the warps leave V's scales as f16, token by token.  After the barrier
+// each warp takes a slice of V's dimensions for O = V^T P^T, so nothing is converted twice
+// however many query rows there are, and S of the next tile runs in the same phase: one
+// barrier a tile.
 //
 // The reference that the weights use is the running maximum, followed lazily: only where a
 // score exceeds it by 2^5 do the warps meet for the true maximum, rescale and form P again
@@ -28,38 +28,60 @@ namespace vw4 {
 
 constexpr float kTail4 = 9.f;     // weights carry 2^9
 constexpr float kLazy4 = 5.f;     // (log2) of the reference
-constexpr int kAttn4Tk = 128;
+
+// Keys of a tile and warps that compute.  Four warps and about 18 KB a tile put two or three
+// blocks on an SM; with 48 and 64 rows the outputs' registers leave room for fewer keys a
+// warp, and at head size 256 for half of the dimensions.
+__host__ __device__ constexpr int attn4_tk(int D, int nt) {
+    return (D == 256 && nt < 6) || (D == 128 && nt >= 6) ? 64 : 128;
+}
+__host__ __device__ constexpr int attn4_warps(int D, int nt) { return D != 128 && nt >= 6 ? 8 : 4; }
+// Places of the ring of K tiles: what shared memory leaves.
+__host__ __device__ constexpr int attn4_places(int D, int nt) {
+    return D == 64              ? 6
+           : D == 128 && nt > 4 ? (nt == 6 ? 6 : 5)
+           : nt == 1            ? 3
+           : D == 128           ? (nt == 4 ? 3 : 4)
+           : nt > 4             ? (nt == 6 ? 3 : 2)
+                                : (nt >= 3 ? 3 : 4);
+}
 
 #ifdef __CUDACC__
 template <int D, int NT>
 struct Attn4Shape {
-    static constexpr int kWarps = 8;
+    static constexpr int kWarps = attn4_warps(D, NT);
     static constexpr int kThreads = (kWarps + 2) * 32;
-    static constexpr int kTK = kAttn4Tk;
+    static constexpr int kTK = attn4_tk(D, NT);
+    static constexpr int kKM = kTK / kWarps / 16;     // 16-key row tiles of a warp
     static constexpr int kRows = 8 * NT;
     static constexpr int kKB = D / 2;                 // bytes of a key's codes
     static constexpr int kNB = D / 16;                // and of its scales
     static constexpr int kTile = kTK * kKB;
     static constexpr int kSTile = kTK * kNB;
-    static constexpr int kStage = 2 * kTile + 2 * kSTile;  // K, V, scales of K, of V
-    static constexpr int kSlices = D / 32;            // slices of V's dimensions
-    static constexpr int kParts = kWarps / kSlices;   // parts of its keys
+    static constexpr int kStage = kTile + kSTile;     // of K or V: codes, scales
+    static constexpr int kSlices = D / 32;            // slices of 32 of V's dimensions
+    static constexpr int kOwn = kSlices > kWarps ? kSlices / kWarps : 1;    // of a warp
+    static constexpr int kParts = kWarps > kSlices ? kWarps / kSlices : 1;  // parts of V's keys
     static constexpr int kQ = kRows * D * 2;
     static constexpr int kQBlk = kRows * 128;
     static constexpr int kP = NT * kTK * 16;          // weights: f16 [n-tile][key][8]
-    static constexpr int kVRow = (kTK + 16) * 2;      // V's scales: f16 [block][token]
+    static constexpr int kVRow = (kTK + 16) * 2;      // V's scales: f16 [block][v_at(token)]
     static constexpr int kVS = kNB * kVRow;
     static constexpr int kX = (kParts - 1) * kSlices * 1024;  // an n-tile's outputs of the other parts
-    static constexpr int kStages = D == 64 ? 6 : (D == 128 ? 4 : (NT <= 2 ? 2 : 3));
-    static constexpr int kOffQ = kStages * kStage;
+    static constexpr int kMinBlocks = kWarps == 8 ? 1 : (NT == 1 ? 3 : 2);
+    // V of a tile is read a phase after its K: one place more, if it fits
+    static constexpr int kNK = attn4_places(D, NT), kNV = kNK + (NT == 1 && D > 64 ? 0 : 1);
+    static constexpr int kOffVal = kNK * kStage;
+    static constexpr int kOffQ = (kOffVal + kNV * kStage + 1023) / 1024 * 1024;
     static constexpr int kOffP = kOffQ + 2 * kQ;
     static constexpr int kOffV = kOffP + 2 * kP;
     static constexpr int kOffX = kOffV + 2 * kVS;
     static constexpr int kOffML = kOffX + kX;          // float [2][warps][rows]: maxima, sums
-    static constexpr int kOffRow = kOffML + 2 * kWarps * kRows * 4;  // [4][rows], see below
-    static constexpr int kSmem = kOffRow + 4 * kRows * 4 + 1024;
-    static_assert(kStage % 1024 == 0 && kQ % 1024 == 0 && kVS % 16 == 0, "alignment");
+    static constexpr int kOffRow = kOffML + 2 * kWarps * kRows * 4;  // [6][rows], see below
+    static constexpr int kSmem = kOffRow + 6 * kRows * 4 + 1024;
+    static_assert(kStage % (8 * kKB) == 0 && kQ % 1024 == 0 && kVS % 16 == 0, "alignment");
     static_assert(kSmem <= 225 * 1024, "shared memory");
+    static_assert(kTK % (kParts * 32) == 0, "V's keys in steps of 32");
     __device__ static __forceinline__ uint32_t at(int key, int chunk) {  // 16 bytes of a key's codes
         const int x = kKB == 128 ? key & 7 : (kKB == 64 ? (key >> 1) & 3 : (key >> 2) & 1);
         return static_cast<uint32_t>(key * kKB + ((chunk ^ x) << 4));
@@ -67,32 +89,63 @@ struct Attn4Shape {
     __device__ static __forceinline__ uint32_t q_at(int row, int chunk) {  // 16 bytes of a query
         return static_cast<uint32_t>((chunk >> 3) * kQBlk + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
     }
+    // where a token's scale stands: the four pairs of tokens that a lane of O's product
+    // multiplies in a step of 32 keys are 16 bytes
+    __device__ static __forceinline__ int v_at(int token) {
+        return (token & ~31) | ((token >> 1) & 3) << 3 | ((token >> 3) & 3) << 1 | (token & 1);
+    }
 };
 
+// Matrix loads that keep their order to the barriers alone, and products that keep none, so
+// that they are free to overlap.
+__device__ __forceinline__ void ldsm4_free(uint32_t* r, uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t_free(uint32_t* r, uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+// by the low or the high half of s (a broadcast that costs no instruction)
+template <bool HIGH>
+__device__ __forceinline__ uint32_t mul_f16x2_half(uint32_t a, uint32_t s) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&s);
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), HIGH ? __high2half2(h) : __low2half2(h));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 
-template <int D, int NT, int MINB>
-__global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, MINB)
+template <int D, int NT>
+__global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>::kMinBlocks)
     attn4_kernel(const AttnParams p, const Kv4Blocks kb, const __grid_constant__ AttnMaps maps) {
     using S = Attn4Shape<D, NT>;
-    constexpr int TK = S::kTK, NST = S::kStages, NB = S::kNB;
+    constexpr int TK = S::kTK, NK = S::kNK, NV = S::kNV, NB = S::kNB, KM = S::kKM;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ __align__(8) uint64_t b_full[NST], b_empty[NST], b_qe[2];
+    __shared__ __align__(8) uint64_t b_k[NK], b_ke[NK], b_v[NV], b_ve[NV], b_qe[2];
     __shared__ AttnUnit s_unit[kUnitRing];
     __shared__ volatile int s_abort;
+    __shared__ float2 s_scale[2];    // a part's scales of its head of K and V, by seg & 1
     const int tid = threadIdx.x, lane = tid & 31, wk = tid >> 5;
     const uint32_t sm = smem_u32(smem);
     float* s_m = reinterpret_cast<float*>(smem + S::kOffML);
     float* s_l = s_m + S::kWarps * S::kRows;
-    float* s_rs = reinterpret_cast<float*>(smem + S::kOffRow);      // a query row's scale
-    int* s_pos = reinterpret_cast<int*>(s_rs + S::kRows);           // its position (dead: -1)
+    float* s_c2 = reinterpret_cast<float*>(smem + S::kOffRow);      // log2 of a score of a query row
+    int* s_pos = reinterpret_cast<int*>(s_c2 + S::kRows);           // its position (dead: -1)
     int* s_out = s_pos + S::kRows;                                  // verify index << 16 | head (dead: -1)
     uint32_t* s_nan = reinterpret_cast<uint32_t*>(s_out + S::kRows);  // its blocks that a NaN reached
+    float* s_ref = reinterpret_cast<float*>(s_nan + S::kRows);      // [2] its reference (log2), in turn
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == S::kWarps * 32) {
@@ -101,9 +154,13 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, MINB)
         tma_prefetch_desc(&maps.q);
     }
     if (tid == 0) {
-        for (int k = 0; k < NST; ++k) {
-            mbar_init(&b_full[k], 2);
-            mbar_init(&b_empty[k], 1);
+        for (int k = 0; k < NK; ++k) {
+            mbar_init(&b_k[k], 1);
+            mbar_init(&b_ke[k], 1);
+        }
+        for (int k = 0; k < NV; ++k) {
+            mbar_init(&b_v[k], 1);
+            mbar_init(&b_ve[k], 1);
         }
         mbar_init(&b_qe[0], 1);
         mbar_init(&b_qe[1], 1);
@@ -128,20 +185,28 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, MINB)
         // ------------------------------------------------------- producers
         const bool keys = wk == S::kWarps;  // else values
         const uint8_t* blocks = keys ? kb.k : kb.v;
+        uint64_t* full = keys ? b_k : b_v;
+        uint64_t* empty = keys ? b_ke : b_ve;
+        const int places = keys ? NK : NV;
         const uint64_t policy = policy_evict_normal();
         AttnWalk<TK> w;
         w.begin(p, span, cap, lane);
         int u = 0;
-        for (; u < n_units; ++u) {
-            const int st = u % NST;
+        for (int st = 0, round = 0; u < n_units; ++u) {
             const AttnUnit d = w.unit(p);
             const AttnTile t = w.tile(p);
+            float ks = 1.f, vs = 1.f;
+            if (keys && (d.flags & kUnitFirst)) {
+                if (p.k_scale) ks = __ldg(p.k_scale + t.h);
+                if (p.v_scale) vs = __ldg(p.v_scale + t.h);
+            }
             if (u + 1 < n_units) w.next(p, lane);
-            if (u >= NST && !wait(&b_empty[st], u / NST - 1)) break;
+            if (round > 0 && !wait(&empty[st], round - 1)) break;
             const bool q = keys && (d.flags & kUnitFirst);
             if (q && d.seg >= 2 && !wait(&b_qe[d.seg & 1], (d.seg >> 1) - 1)) break;
+            const int off = (keys ? 0 : S::kOffVal) + st * S::kStage;
             const uint32_t box = static_cast<uint32_t>(t.box_rows * NB);  // bytes of a box's scales
-            uint8_t* sdst = smem + st * S::kStage + 2 * S::kTile + (keys ? 0 : S::kSTile) + lane * box;
+            uint8_t* sdst = smem + off + S::kTile + lane * box;
             const bool there = t.page >= 0 && t.page < p.num_pages;
             if (t.page == p.num_pages) {  // no such page: zeros
                 for (uint32_t c = 0; c < box; c += 16)
@@ -153,227 +218,227 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, MINB)
             __syncwarp();
             if (lane == 0) {
                 if (keys) s_unit[u % kUnitRing] = d;
-                mbar_arrive_expect_tx(&b_full[st], bytes + (q ? attn_q_bytes(p, D) : 0u));
+                if (q) s_scale[d.seg & 1] = make_float2(ks, vs);
+                mbar_arrive_expect_tx(&full[st], bytes + (q ? attn_q_bytes(p, D) : 0u));
                 if (q)
-                    attn_load_q<D>(p, &maps.q, sm + S::kOffQ + (d.seg & 1) * S::kQ, S::kQBlk, d,
-                                   &b_full[st]);
+                    attn_load_q<D>(p, &maps.q, sm + S::kOffQ + (d.seg & 1) * S::kQ, S::kQBlk, d, &full[st]);
             }
             __syncwarp();
-            t.template load<TK, 1, 1, S::kKB, 1>(p, keys ? &maps.k : &maps.v,
-                                                 sm + st * S::kStage + (keys ? 0 : S::kTile),
-                                                 &b_full[st], 0, 0, lane);
+            t.template load<TK, 1, 1, S::kKB, 1>(p, keys ? &maps.k : &maps.v, sm + off, &full[st], 0, 0,
+                                                 lane);
             if (there)
                 bulk_load(sdst, blocks + t.page * kb.page_stride + t.h * kb.head_stride +
                                     static_cast<long long>((t.start + lane * t.box_rows) &
                                                            (p.page_size - 1)) * NB,
-                          box, &b_full[st], policy);
+                          box, &full[st], policy);
             __syncwarp();
+            if (++st == places) st = 0, ++round;
         }
         // copies in flight land before the block ends
         if (u < n_units) {
-            for (int k = u > NST ? u - NST : 0; k < u; ++k)
-                mbar_wait_bounded(&b_full[k % NST], (k / NST) & 1, p.wait_ns, nullptr);
+            for (int k = u > places ? u - places : 0; k < u; ++k)
+                mbar_wait_bounded(&full[k % places], (k / places) & 1, p.wait_ns, nullptr);
         }
         return;
     }
 
-    // ---- the eight warps.  Every path between two meetings has the same number of them in
+    // ---- the computing warps.  Every path between two meetings has the same number of them in
     // all warps: a wait that ran out makes a warp skip its work, and the next meeting ends
     // the block's.
     bool dead = false;
-    auto meet = [&](bool flag) {  // the threads of the eight warps; any of the flags
+    auto meet = [&](bool flag) {  // the threads of the computing warps; any of the flags
         uint32_t r;
         asm volatile(
             "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\t"
-            "barrier.cta.red.or.pred b, 1, 256, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
-            : "=r"(r) : "r"(static_cast<uint32_t>(flag)) : "memory");
+            "barrier.cta.red.or.pred b, 1, %2, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+            : "=r"(r) : "r"(static_cast<uint32_t>(flag)), "n"(S::kWarps * 32) : "memory");
         return r != 0;
     };
-    float o[2][NT][4];       // rows: dimensions 4 u + 2 i, + 1 of the slice; columns: query rows
-    float l[NT][2], ref[NT][2], c2[NT][2];
+    // rows: dimensions 4 u + 2 i, + 1 of the slice; columns: query rows
+    float o[S::kOwn][2][NT][4];
+    float l[NT][2];
+    int turn = 0;  // of s_ref
     const int t4 = lane & 3, u8 = lane >> 2, lm = lane >> 3, lr = lane & 7;
-    const int key0 = wk * 16;                          // of the warp's keys
-    const int slice = wk % S::kSlices, part = wk / S::kSlices;
-    const int blk = 2 * slice + (lane >> 4);           // scale block of the lane's dimensions
+    const int key0 = wk * 16 * KM;                     // of the warp's keys
+    const int slice0 = wk % S::kSlices * S::kOwn, part = wk / S::kSlices;
+    const int inv_gb = 65536 / p.gb + 1;               // r / gb = r * inv_gb >> 16 for r < 64
+
+    auto row2 = [&](const float* a, int n, float* v) {  // of the lane's two query rows
+        const float2 f = *reinterpret_cast<const float2*>(a + n * 8 + t4 * 2);
+        v[0] = f.x;
+        v[1] = f.y;
+    };
 
     // O += V^T P^T of unit u
     auto values = [&](int u) {
-        const uint32_t vS = sm + (u % NST) * S::kStage + S::kTile;
+        const uint32_t vS = sm + S::kOffVal + u % NV * S::kStage;
         const uint32_t pS = sm + S::kOffP + (u & 1) * S::kP;
-        const uint8_t* sc = smem + S::kOffV + (u & 1) * S::kVS + blk * S::kVRow;
+        const uint8_t* sc = smem + S::kOffV + (u & 1) * S::kVS + t4 * 16 + (lane >> 4) * S::kVRow;
 #pragma unroll
         for (int k = 0; k < TK / S::kParts; k += 32) {
             const int key = part * (TK / S::kParts) + k;
-            uint32_t x[4], e[4][4];
-            ldsm4t(x, vS + S::at(key + lr + 8 * lm, slice));
-            // a register: two tokens x four dimensions; to pairs of tokens, scaled
+            uint32_t x[S::kOwn][4], b[NT][4];
+            uint4 sv[S::kOwn];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const uint32_t s = *reinterpret_cast<const uint32_t*>(sc + (key + 8 * m + 2 * t4) * 2);
-                uint32_t h[4];
-                e2m1x8_f16(x[m], h);
-                e[m][0] = mul_f16x2(__byte_perm(h[0], h[2], 0x5410), s);
-                e[m][1] = mul_f16x2(__byte_perm(h[0], h[2], 0x7632), s);
-                e[m][2] = mul_f16x2(__byte_perm(h[1], h[3], 0x5410), s);
-                e[m][3] = mul_f16x2(__byte_perm(h[1], h[3], 0x7632), s);
+            for (int q = 0; q < S::kOwn; ++q) {
+                ldsm4t_free(x[q], vS + S::at(key + lr + 8 * lm, slice0 + q));
+                sv[q] = *reinterpret_cast<const uint4*>(sc + (slice0 + q) * 2 * S::kVRow + key * 2);
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                uint32_t b[4];
-                ldsm4t(b, pS + n * (TK * 16) + (key + lr + 8 * lm) * 16);
+            for (int n = 0; n < NT; ++n) ldsm4t_free(b[n], pS + n * (TK * 16) + (key + lr + 8 * lm) * 16);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+            for (int q = 0; q < S::kOwn; ++q) {
+                const uint32_t s[4] = {sv[q].x, sv[q].y, sv[q].z, sv[q].w};
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t a[4] = {e[2 * h][2 * i], e[2 * h][2 * i + 1],
-                                               e[2 * h + 1][2 * i], e[2 * h + 1][2 * i + 1]};
-                        mma16816<true>(o[i][n], a, b[2 * h], b[2 * h + 1]);
+                for (int h = 0; h < 2; ++h) {
+                    // a register: two tokens x four dimensions; to pairs of tokens, scaled
+                    uint32_t e[2][4];
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        uint32_t w[4];
+                        e2m1x8_f16(x[q][2 * h + m], w);
+                        e[m][0] = mul_f16x2(__byte_perm(w[0], w[2], 0x5410), s[2 * h + m]);
+                        e[m][1] = mul_f16x2(__byte_perm(w[0], w[2], 0x7632), s[2 * h + m]);
+                        e[m][2] = mul_f16x2(__byte_perm(w[1], w[3], 0x5410), s[2 * h + m]);
+                        e[m][3] = mul_f16x2(__byte_perm(w[1], w[3], 0x7632), s[2 * h + m]);
                     }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma_f16(o[q][i][n], e[0][2 * i], e[0][2 * i + 1], e[1][2 * i], e[1][2 * i + 1],
+                                    b[n][2 * h], b[n][2 * h + 1]);
+                }
             }
         }
     };
 
     for (int u = 0; u < n_units; ++u) {
         // ---- a part of an item: its queries
-        dead |= !wait(&b_full[u % NST], u / NST);
+        dead |= !wait(&b_k[u % NK], u / NK);
         AttnUnit td = s_unit[u % kUnitRing];
         const int qslot = td.seg & 1;
         const uint32_t qs = sm + S::kOffQ + qslot * S::kQ;
         const int h = td.g / p.row_blocks;
         float ks = 1.f, vs = 1.f;
         if (!dead) {
-            ks = p.k_scale ? __ldg(p.k_scale + h) : 1.f;
-            vs = p.v_scale ? __ldg(p.v_scale + h) : 1.f;
+            ks = s_scale[qslot].x;
+            vs = s_scale[qslot].y;
             // bf16 -> f16 under a power of two per row that puts its largest magnitude into
             // [2^14, 2^15), with the sign of the head's scale: exact for every value down to
             // 2^-31 of it.  Within 32 dimensions the order is that of the codes' registers.
-            for (int r = wk; r < S::kRows; r += S::kWarps) {
-                const AttnRow ar = attn_row(p, td.g, r);
-                uint32_t* row = reinterpret_cast<uint32_t*>(smem + S::kOffQ + qslot * S::kQ);
-                float v[D / 32];
-                float mx = 0.f;
+            // Rows four at a time: a row is a chain of latencies.
+            const int rb = td.g - h * p.row_blocks;
+            const int bt = rb / p.blocks_g, bg = rb - bt * p.blocks_g;
+            uint32_t* rows = reinterpret_cast<uint32_t*>(smem + S::kOffQ + qslot * S::kQ);
+            constexpr int kEach = S::kRows / S::kWarps, kAtOnce = kEach < 4 ? kEach : (kEach % 4 ? kEach / 2 : 4);
+            static_assert(kEach % kAtOnce == 0, "whole steps");
+#pragma unroll 1
+            for (int r0 = wk; r0 < S::kRows; r0 += S::kWarps * kAtOnce) {
+                float v[kAtOnce][D / 32], mx[kAtOnce];
+                int pos[kAtOnce], out[kAtOnce];
 #pragma unroll
-                for (int k = 0; k < D / 64; ++k) {
-                    const int e = lane + 32 * k;  // pair of dimensions 2e, 2e + 1
-                    const uint32_t x = ar.live ? row[(S::q_at(r, e >> 2) >> 2) + (e & 3)] : 0u;
-                    v[2 * k] = __uint_as_float(x << 16);
-                    v[2 * k + 1] = __uint_as_float(x & 0xffff0000u);
-                    mx = fmaxf(mx, fmaxf(fabsf(v[2 * k]), fabsf(v[2 * k + 1])));
+                for (int q = 0; q < kAtOnce; ++q) {
+                    const int r = r0 + q * S::kWarps;
+                    const int t = (r * inv_gb) >> 16, gq = bg * p.gb + r - t * p.gb, i = bt * p.tb + t;
+                    const bool live = t < p.tb && i < p.R && gq < p.G;
+                    pos[q] = live ? td.p0 + i : -1;
+                    out[q] = live ? i << 16 | (h * p.G + gq) : -1;
+                    mx[q] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < D / 64; ++k) {
+                        const int e = lane + 32 * k;  // pair of dimensions 2e, 2e + 1
+                        const uint32_t x = live ? rows[(S::q_at(r, e >> 2) >> 2) + (e & 3)] : 0u;
+                        v[q][2 * k] = __uint_as_float(x << 16);
+                        v[q][2 * k + 1] = __uint_as_float(x & 0xffff0000u);
+                        mx[q] = fmaxf(mx[q], fmaxf(fabsf(v[q][2 * k]), fabsf(v[q][2 * k + 1])));
+                    }
                 }
 #pragma unroll
-                for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-                const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
-                int sh = ex == 0 || ex == 255 ? 0 : 127 + 14 - ex;
-                sh = max(-126, min(126, sh));
-                const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), ks);
-                if (lane == 0) {
-                    s_rs[r] = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-                    s_pos[r] = ar.live ? td.p0 + ar.i : -1;
-                    s_out[r] = ar.live ? ar.i << 16 | ar.hq : -1;
-                    s_nan[r] = 0u;
-                }
-                __syncwarp();
+                for (int s = 16; s > 0; s >>= 1)
 #pragma unroll
-                for (int k = 0; k < D / 64; ++k) {
-                    const int e = lane + 32 * k, s = (e & ~15) | ((e & 3) << 2) | ((e >> 2) & 3);
-                    row[(S::q_at(r, s >> 2) >> 2) + (s & 3)] = pack2<true>(v[2 * k] * up, v[2 * k + 1] * up);
+                    for (int q = 0; q < kAtOnce; ++q)
+                        mx[q] = fmaxf(mx[q], __shfl_xor_sync(0xffffffffu, mx[q], s));
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q) {
+                    const int r = r0 + q * S::kWarps;
+                    const int ex = static_cast<int>(__float_as_uint(mx[q]) >> 23);
+                    int sh = ex == 0 || ex == 255 ? 0 : 127 + 14 - ex;
+                    sh = max(-126, min(126, sh));
+                    const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), ks);
+                    if (lane == 0) {
+                        float c2 = p.scale * kLog2e * fabsf(ks) *
+                                   __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+                        if (c2 < kMinFactor) c2 = kMinFactor;  // (NaN stays)
+                        s_c2[r] = c2;
+                        s_ref[r] = -INFINITY;
+                        s_pos[r] = pos[q];
+                        s_out[r] = out[q];
+                        s_nan[r] = 0u;
+                    }
+#pragma unroll
+                    for (int k = 0; k < D / 64; ++k) {
+                        const int e = lane + 32 * k, s = (e & ~15) | ((e & 3) << 2) | ((e >> 2) & 3);
+                        rows[(S::q_at(r, s >> 2) >> 2) + (s & 3)] =
+                            pack2<true>(v[q][2 * k] * up, v[q][2 * k + 1] * up);
+                    }
                 }
             }
             fence_async_smem();  // (a later load will write there)
         }
         if (meet(dead)) return;
+        turn = 0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                l[n][k] = 0.f;
-                ref[n][k] = -INFINITY;
-                c2[n][k] = p.scale * kLog2e * fabsf(ks) * s_rs[n * 8 + t4 * 2 + k];
-                if (c2[n][k] < kMinFactor) c2[n][k] = kMinFactor;  // (NaN stays)
-                o[0][n][2 * k] = o[0][n][2 * k + 1] = o[1][n][2 * k] = o[1][n][2 * k + 1] = 0.f;
-            }
+            for (int q = 0; q < S::kOwn; ++q)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    o[q][i][n][0] = o[q][i][n][1] = o[q][i][n][2] = o[q][i][n][3] = 0.f;
         }
         for (const int first = u;; ++u) {
             if (u > first) {
-                dead |= !wait(&b_full[u % NST], u / NST);
+                dead |= !wait(&b_k[u % NK], u / NK);
                 if (!dead) td = s_unit[u % kUnitRing];
             }
             const bool edge = td.flags & kUnitEdge;
-            uint8_t* stage = smem + (u % NST) * S::kStage;
-            float s[NT][4];
+            const uint8_t* keys = smem + u % NK * S::kStage;
+            float s[KM][NT][4];
             float sum[NT][2];
-            // weights against the reference, to shared memory; true where a score is too far
-            // above it
-            auto weights = [&] {
-                bool grew = false;
-                uint8_t* dst = smem + S::kOffP + (u & 1) * S::kP + (key0 + u8) * 16 + t4 * 4;
+            // weights of an n-tile against a reference, to shared memory
+            auto weights = [&](int n, const float* c2, const float* ref) {
+                uint8_t* dst = smem + S::kOffP + (u & 1) * S::kP + (key0 + u8) * 16 + t4 * 4 + n * (TK * 16);
+                sum[n][0] = sum[n][1] = 0.f;
+                const float r[2] = {kTail4 - (ref[0] == -INFINITY ? 0.f : ref[0]),
+                                    kTail4 - (ref[1] == -INFINITY ? 0.f : ref[1])};
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int m = 0; m < KM; ++m) {
                     float w[4];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const float r = ref[n][k] == -INFINITY ? 0.f : ref[n][k];
-                        grew |= fmaxf(s[n][k], s[n][k + 2]) * c2[n][k] > ref[n][k] + kLazy4;
-                        w[k] = ex2(fmaf(s[n][k], c2[n][k], kTail4 - r));
-                        w[k + 2] = ex2(fmaf(s[n][k + 2], c2[n][k], kTail4 - r));
-                        sum[n][k] = w[k] + w[k + 2];
+                        w[k] = ex2(fmaf(s[m][n][k], c2[k], r[k]));
+                        w[k + 2] = ex2(fmaf(s[m][n][k + 2], c2[k], r[k]));
+                        sum[n][k] += w[k] + w[k + 2];
                     }
-                    *reinterpret_cast<uint32_t*>(dst + n * (TK * 16)) = pack2<true>(w[0], w[1]);
-                    *reinterpret_cast<uint32_t*>(dst + n * (TK * 16) + 128) = pack2<true>(w[2], w[3]);
+                    *reinterpret_cast<uint32_t*>(dst + m * 256) = pack2<true>(w[0], w[1]);
+                    *reinterpret_cast<uint32_t*>(dst + m * 256 + 128) = pack2<true>(w[2], w[3]);
                 }
-                return grew;
+            };
+            auto largest = [&](int n, int k) {
+                float mx = fmaxf(s[0][n][k], s[0][n][k + 2]);
+#pragma unroll
+                for (int m = 1; m < KM; ++m) mx = fmaxf(mx, fmaxf(s[m][n][k], s[m][n][k + 2]));
+                return mx;
             };
             bool grew = false;
             if (!dead) {
-                // ---- V's scales to f16, token by token
-                {
-                    constexpr int PER = NB / 2;  // bytes of a thread
-                    const int token = tid >> 1, b0 = (tid & 1) * PER;
-                    const uint8_t* src = stage + 2 * S::kTile + S::kSTile + token * NB + b0;
-                    uint32_t w[PER > 4 ? 2 : 1];
-                    if (PER == 2) w[0] = *reinterpret_cast<const uint16_t*>(src);
-                    else if (PER == 4) w[0] = *reinterpret_cast<const uint32_t*>(src);
-                    else {
-                        w[0] = *reinterpret_cast<const uint32_t*>(src);
-                        w[PER > 4 ? 1 : 0] = *reinterpret_cast<const uint32_t*>(src + 4);
-                    }
-                    if (edge) {
-                        const int j = td.start + token;
-                        if (!key_some(j, td.len, td.p0, p.window, p.sinks)) {
-                            // no row sees it: zeros, whatever the cache holds there
-#pragma unroll
-                            for (int k = 0; k < (PER > 4 ? 2 : 1); ++k) w[k] = 0u;
-                        } else if (!key_all(j, td.len, td.p0, p.window, p.sinks)) {
-                            // NaN scales must not reach rows that do not see the key through a
-                            // weight of zero: noted for the others, and taken out
-#pragma unroll 1
-                            for (int k = 0; k < PER; ++k) {
-                                uint32_t& wk4 = w[PER > 4 && k >= 4 ? 1 : 0];
-                                const int at = 8 * (k & 3);
-                                if (((wk4 >> at) & 0x7fu) != 0x7fu) continue;
-                                wk4 &= ~(0xffu << at);
-#pragma unroll 1
-                                for (int r = 0; r < S::kRows; ++r)
-                                    if (s_out[r] >= 0 && key_seen(j, s_pos[r], p.window, p.sinks))
-                                        atomicOr(&s_nan[r], 1u << (b0 + k));
-                            }
-                        }
-                    }
-                    uint8_t* dst = smem + S::kOffV + (u & 1) * S::kVS + b0 * S::kVRow + token * 2;
-#pragma unroll
-                    for (int k = 0; k < PER; k += 2) {
-                        const uint32_t f = e4m3x2_f16x2(w[k / 4] >> (8 * (k & 3)));
-                        *reinterpret_cast<uint16_t*>(dst + k * S::kVRow) = static_cast<uint16_t>(f);
-                        *reinterpret_cast<uint16_t*>(dst + (k + 1) * S::kVRow) =
-                            static_cast<uint16_t>(f >> 16);
-                    }
-                }
                 // ---- S = K Q^T of the warp's keys
-                const uint32_t kS = sm + (u % NST) * S::kStage;
-                uint32_t sk[2][D / 64];  // scales of two 32-dimension chunks, of keys u8 and u8 + 8
+                const uint32_t kS = sm + u % NK * S::kStage;
+                uint32_t sk[2 * KM][D / 64];  // scales of two 32-dimension chunks, of keys u8 + 8 k
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint8_t* src = stage + 2 * S::kTile + (key0 + u8 + 8 * k) * NB;
+                for (int k = 0; k < 2 * KM; ++k) {
+                    const uint8_t* src = keys + S::kTile + (key0 + u8 + 8 * k) * NB;
                     const uint32_t sel = t4 & 2 ? 0x7531u : 0x6420u;
                     if constexpr (NB == 4) {
                         sk[k][0] = e4m3x2_f16x2(
@@ -393,30 +458,36 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, MINB)
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+                for (int m = 0; m < KM; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) s[m][n][0] = s[m][n][1] = s[m][n][2] = s[m][n][3] = 0.f;
 #pragma unroll
                 for (int c = 0; c < D / 32; c += 2) {
-                    uint32_t w[4];
-                    ldsm4(w, kS + S::at(key0 + lr + (lm & 1) * 8, c + (lm >> 1)));
+                    uint32_t w[KM][4];
+#pragma unroll
+                    for (int m = 0; m < KM; ++m)
+                        ldsm4_free(w[m], kS + S::at(key0 + 16 * m + lr + (lm & 1) * 8, c + (lm >> 1)));
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        uint32_t x[4], y[4];
-                        e2m1x8_f16(w[2 * e], x);
-                        e2m1x8_f16(w[2 * e + 1], y);
-                        const uint32_t sx = __byte_perm(sk[0][c / 2], 0, e ? 0x3232 : 0x1010);
-                        const uint32_t sy = __byte_perm(sk[1][c / 2], 0, e ? 0x3232 : 0x1010);
+                        uint32_t b[NT][4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            x[k] = mul_f16x2(x[k], sx);
-                            y[k] = mul_f16x2(y[k], sy);
-                        }
-                        const uint32_t a0[4] = {x[0], y[0], x[1], y[1]}, a1[4] = {x[2], y[2], x[3], y[3]};
+                        for (int n = 0; n < NT; ++n)
+                            ldsm4_free(b[n], qs + S::q_at(n * 8 + lr, (c + e) * 4 + lm));
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            uint32_t b[4];
-                            ldsm4(b, qs + S::q_at(n * 8 + lr, (c + e) * 4 + lm));
-                            mma16816<true>(s[n], a0, b[0], b[1]);
-                            mma16816<true>(s[n], a1, b[2], b[3]);
+                        for (int m = 0; m < KM; ++m) {
+                            uint32_t x[4], y[4];
+                            e2m1x8_f16(w[m][2 * e], x);
+                            e2m1x8_f16(w[m][2 * e + 1], y);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t sx = sk[2 * m][c / 2], sy = sk[2 * m + 1][c / 2];
+                                x[k] = e ? mul_f16x2_half<true>(x[k], sx) : mul_f16x2_half<false>(x[k], sx);
+                                y[k] = e ? mul_f16x2_half<true>(y[k], sy) : mul_f16x2_half<false>(y[k], sy);
+                            }
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma_f16(s[m][n], x[0], y[0], x[1], y[1], b[n][0], b[n][1]);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma_f16(s[m][n], x[2], y[2], x[3], y[3], b[n][2], b[n][3]);
                         }
                     }
                 }
@@ -425,45 +496,124 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, MINB)
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const int pos = s_pos[n * 8 + t4 * 2 + k], j = td.start + key0 + u8;
-                            if (!key_seen(j, pos, p.window, p.sinks)) s[n][k] = -INFINITY;
-                            if (!key_seen(j + 8, pos, p.window, p.sinks)) s[n][k + 2] = -INFINITY;
+                            const int pos = s_pos[n * 8 + t4 * 2 + k];
+#pragma unroll
+                            for (int m = 0; m < KM; ++m) {
+                                const int j = td.start + key0 + 16 * m + u8;
+                                if (!key_seen(j, pos, p.window, p.sinks)) s[m][n][k] = -INFINITY;
+                                if (!key_seen(j + 8, pos, p.window, p.sinks)) s[m][n][k + 2] = -INFINITY;
+                            }
                         }
                 }
-                grew = weights();
-                if (u > first) values(u - 1);
+                // ---- V's scales to f16, token by token: a thread a part of a token's
+                dead |= !wait(&b_v[u % NV], u / NV);
+                if (!dead) {
+                    constexpr int PER = TK * NB / (S::kWarps * 32);  // bytes of a thread
+                    static_assert(PER == 2 || PER == 4 || PER == 8, "up to two words");
+                    constexpr int W = (PER + 3) / 4;
+                    constexpr int TPT = NB / PER;                    // threads of a token
+                    const int token = tid / TPT, b0 = tid % TPT * PER;
+                    const uint8_t* src = smem + S::kOffVal + u % NV * S::kStage + S::kTile + token * NB + b0;
+                    uint32_t w[W];
+                    if (PER == 2) w[0] = *reinterpret_cast<const uint16_t*>(src);
+#pragma unroll
+                    for (int k = 0; k < PER / 4; ++k) w[k] = reinterpret_cast<const uint32_t*>(src)[k];
+                    if (edge) {
+                        const int j = td.start + token;
+                        if (!key_some(j, td.len, td.p0, p.window, p.sinks)) {
+                            // no row sees it: zeros, whatever the cache holds there
+#pragma unroll
+                            for (int k = 0; k < W; ++k) w[k] = 0u;
+                        } else if (!key_all(j, td.len, td.p0, p.window, p.sinks)) {
+                            // NaN scales must not reach rows that do not see the key through a
+                            // weight of zero: noted for the others, and taken out
+#pragma unroll
+                            for (int k = 0; k < PER; ++k) {
+                                if (((w[k / 4] >> (8 * (k & 3))) & 0x7fu) != 0x7fu) continue;
+                                w[k / 4] &= ~(0xffu << (8 * (k & 3)));
+#pragma unroll 1
+                                for (int r = 0; r < S::kRows; ++r)
+                                    if (s_out[r] >= 0 && key_seen(j, s_pos[r], p.window, p.sinks))
+                                        atomicOr(&s_nan[r], 1u << (b0 + k));
+                            }
+                        }
+                    }
+                    uint8_t* dst = smem + S::kOffV + (u & 1) * S::kVS + b0 * S::kVRow + S::v_at(token) * 2;
+#pragma unroll
+                    for (int k = 0; k < PER; k += 2) {
+                        const uint32_t f = e4m3x2_f16x2(w[k / 4] >> (8 * (k & 3)));
+                        *reinterpret_cast<uint16_t*>(dst + k * S::kVRow) = static_cast<uint16_t>(f);
+                        *reinterpret_cast<uint16_t*>(dst + (k + 1) * S::kVRow) =
+                            static_cast<uint16_t>(f >> 16);
+                    }
+                }
+                if (u == first) {
+                    grew = true;  // the first maximum
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float c2[2], ref[2];
+                        row2(s_c2, n, c2);
+                        row2(s_ref + turn * S::kRows, n, ref);
+                        grew |= largest(n, 0) * c2[0] > ref[0] + kLazy4 ||
+                                largest(n, 1) * c2[1] > ref[1] + kLazy4;
+                        weights(n, c2, ref);
+                    }
+                    values(u - 1);
+                }
             }
             if (meet(grew || dead)) {
                 if (meet(dead)) return;
                 // ---- the true maximum of the rows, and the weights again
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
+                    float c2[2], mx[2];
+                    row2(s_c2, n, c2);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        float mx = fmaxf(s[n][k], s[n][k + 2]);
+                        mx[k] = largest(n, k);
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1)
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-                        if (lane < 4) s_m[wk * S::kRows + n * 8 + t4 * 2 + k] = mx * c2[n][k];
+                            mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], x));
+                        mx[k] *= c2[k];
                     }
+                    if (lane < 4)
+                        *reinterpret_cast<float2*>(s_m + wk * S::kRows + n * 8 + t4 * 2) =
+                            make_float2(mx[0], mx[1]);
+                }
                 meet(false);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
+                    float c2[2], ref[2], mx[2];
+                    row2(s_c2, n, c2);
+                    row2(s_ref + turn * S::kRows, n, ref);
+                    mx[0] = ref[0];
+                    mx[1] = ref[1];
+#pragma unroll
+                    for (int w = 0; w < S::kWarps; ++w) {
+                        float m2[2];
+                        row2(s_m + w * S::kRows, n, m2);
+                        mx[0] = fmaxf(mx[0], m2[0]);
+                        mx[1] = fmaxf(mx[1], m2[1]);
+                    }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        float mx = ref[n][k];
-#pragma unroll
-                        for (int w = 0; w < S::kWarps; ++w)
-                            mx = fmaxf(mx, s_m[w * S::kRows + n * 8 + t4 * 2 + k]);
-                        const float f = mx == ref[n][k] ? 1.f : ex2(ref[n][k] - mx);
-                        ref[n][k] = mx;
+                        const float f = mx[k] == ref[k] ? 1.f : ex2(ref[k] - mx[k]);
                         l[n][k] *= f;
-                        o[0][n][k] *= f;
-                        o[0][n][k + 2] *= f;
-                        o[1][n][k] *= f;
-                        o[1][n][k + 2] *= f;
+#pragma unroll
+                        for (int q = 0; q < S::kOwn; ++q)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                o[q][i][n][k] *= f;
+                                o[q][i][n][k + 2] *= f;
+                            }
                     }
-                weights();
+                    if (wk == 0 && lane < 4)
+                        *reinterpret_cast<float2*>(s_ref + (turn ^ 1) * S::kRows + n * 8 + t4 * 2) =
+                            make_float2(mx[0], mx[1]);
+                    weights(n, c2, mx);
+                }
+                turn ^= 1;
                 meet(false);
             }
 #pragma unroll
@@ -471,7 +621,10 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, MINB)
                 l[n][0] += sum[n][0];
                 l[n][1] += sum[n][1];
             }
-            if (u > first && tid == 0) mbar_arrive(&b_empty[(u - 1) % NST]);
+            if (tid == 0) {
+                mbar_arrive(&b_ke[u % NK]);
+                if (u > first) mbar_arrive(&b_ve[(u - 1) % NV]);
+            }
             if (td.flags & kUnitLast) break;
         }
         values(u);
@@ -488,56 +641,79 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, MINB)
         float* po = nullptr;  // partial rows [rows][D], then m [rows], l [rows]
         if (td.slot >= 0) po = p.partial + static_cast<long long>(td.slot) * S::kRows * (D + 2);
         float4* xb = reinterpret_cast<float4*>(smem + S::kOffX);
+        meet(false);
+        if (tid < S::kRows) {  // a row's sum, its factor and the row's own outputs
+            const int r = tid, to = s_out[r];
+            float L = 0.f;
+#pragma unroll
+            for (int w = 0; w < S::kWarps; ++w) L += s_l[w * S::kRows + r];
+            const float ref = s_ref[turn * S::kRows + r];
+            const float M = ref == -INFINITY ? -INFINITY : ref - kTail4;
+            s_m[r] = L == 0.f ? 0.f : vs / L;
+            if (td.slot >= 0) {
+                po[S::kRows * D + r] = M;
+                po[S::kRows * (D + 1) + r] = L;
+            } else if (p.lse && to >= 0) {
+                p.lse[(static_cast<long long>(td.b) * p.R + (to >> 16)) * p.Hq + (to & 0xffff)] =
+                    L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+            }
+        }
+        meet(false);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float4 v[2] = {make_float4(o[0][n][0], o[0][n][2], o[1][n][0], o[1][n][2]),
-                           make_float4(o[0][n][1], o[0][n][3], o[1][n][1], o[1][n][3])};
-            if (S::kParts > 1 && part > 0) {
-                xb[(wk - S::kSlices) * 64 + lane] = v[0];
-                xb[(wk - S::kSlices) * 64 + 32 + lane] = v[1];
+            float4 v[S::kOwn][2];
+#pragma unroll
+            for (int q = 0; q < S::kOwn; ++q)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    v[q][k] = make_float4(o[q][0][n][k], o[q][0][n][k + 2], o[q][1][n][k], o[q][1][n][k + 2]);
+            if (S::kParts > 1) {
+                if (part > 0) {
+                    xb[(wk - S::kSlices) * 64 + lane] = v[0][0];
+                    xb[(wk - S::kSlices) * 64 + 32 + lane] = v[0][1];
+                }
+                meet(false);
             }
-            if (S::kParts > 1 || n == 0) meet(false);  // (n = 0: s_l too)
             if (part == 0) {
+                const int r = n * 8 + t4 * 2;
+                const int2 to2 = *reinterpret_cast<const int2*>(s_out + r);
+                const uint2 nan2 = *reinterpret_cast<const uint2*>(s_nan + r);
+                float f2[2];
+                row2(s_m, n, f2);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
 #pragma unroll
                     for (int q = 1; q < S::kParts; ++q) {
-                        const float4 a = xb[(slice + (q - 1) * S::kSlices) * 64 + 32 * k + lane];
-                        v[k].x += a.x;
-                        v[k].y += a.y;
-                        v[k].z += a.z;
-                        v[k].w += a.w;
+                        const float4 a = xb[(slice0 + (q - 1) * S::kSlices) * 64 + 32 * k + lane];
+                        v[0][k].x += a.x;
+                        v[0][k].y += a.y;
+                        v[0][k].z += a.z;
+                        v[0][k].w += a.w;
                     }
-                    const int r = n * 8 + t4 * 2 + k, to = s_out[r];
-                    if (to < 0) continue;
-                    if ((s_nan[r] >> blk) & 1u) v[k] = make_float4(NAN, NAN, NAN, NAN);
-                    float L = 0.f;
+                    const int to = k ? to2.y : to2.x;
+                    const uint32_t nan = k ? nan2.y : nan2.x;
+                    const float f = f2[k];
+                    __nv_bfloat16* out = p.out + (static_cast<long long>(td.b) * p.R + (to >> 16)) * p.ldo +
+                                         static_cast<long long>(to & 0xffff) * D;
 #pragma unroll
-                    for (int w = 0; w < S::kWarps; ++w) L += s_l[w * S::kRows + r];
-                    const float M = ref[n][k] == -INFINITY ? -INFINITY : ref[n][k] - kTail4;
-                    const int col = slice * 32 + u8 * 4;
-                    if (td.slot >= 0) {
-                        *reinterpret_cast<float4*>(po + r * D + col) = v[k];
-                        if (col == 0) {
-                            po[S::kRows * D + r] = M;
-                            po[S::kRows * (D + 1) + r] = L;
+                    for (int q = 0; q < S::kOwn; ++q) {
+                        const int col = (slice0 + q) * 32 + u8 * 4;
+                        if ((nan >> (col / 16)) & 1u) v[q][k] = make_float4(NAN, NAN, NAN, NAN);
+                        if (to < 0) {
+                        } else if (td.slot >= 0) {
+                            *reinterpret_cast<float4*>(po + (r + k) * D + col) = v[q][k];
+                        } else {
+                            *reinterpret_cast<uint2*>(out + col) =
+                                make_uint2(pack2<false>(v[q][k].x * f, v[q][k].y * f),
+                                           pack2<false>(v[q][k].z * f, v[q][k].w * f));
                         }
-                    } else {
-                        const long long orow = static_cast<long long>(td.b) * p.R + (to >> 16);
-                        const int hq = to & 0xffff;
-                        const float f = L == 0.f ? 0.f : vs / L;
-                        *reinterpret_cast<uint2*>(p.out + orow * p.ldo + static_cast<long long>(hq) * D + col) =
-                            make_uint2(pack2<false>(v[k].x * f, v[k].y * f),
-                                       pack2<false>(v[k].z * f, v[k].w * f));
-                        if (col == 0 && p.lse)
-                            p.lse[orow * p.Hq + hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
                     }
                 }
             }
             if (S::kParts > 1 || n == NT - 1) meet(false);
         }
         if (tid == 0) {
-            mbar_arrive(&b_empty[u % NST]);
+            mbar_arrive(&b_ve[u % NV]);
             mbar_arrive(&b_qe[qslot]);
         }
     }
@@ -547,10 +723,9 @@ template <int D, int NT>
 cudaError_t attn4_launch(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps, int* grid,
                          int sms, cudaStream_t s) {
     using S = Attn4Shape<D, NT>;
-    constexpr int kMinBlocks = S::kSmem <= 113 * 1024 && NT <= 3 ? 2 : 1;
     static std::atomic<unsigned long long> once;
     static std::atomic<int> occ;
-    auto* kernel = attn4_kernel<D, NT, kMinBlocks>;
+    auto* kernel = attn4_kernel<D, NT>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

@@ -18,6 +18,7 @@
 // The bytes bound it (4 or 2 a logit).  A row is split over blocks where the rows alone
 // would leave SMs idle; a second kernel joins the parts in order.
 #include <cuda_bf16.h>
+#include <algorithm>
 
 #include "attn.cuh"
 
@@ -28,6 +29,7 @@ constexpr int kLpEach = 16;                          // entries of a thread and 
 constexpr int kLpChunk = kLpThreads * kLpEach;
 constexpr int kCand = kMaxTop * kLpEach;             // candidates that are looked at at once
 constexpr int kLpMaxSplit = 64;
+constexpr long long kLpFill = 608;                   // blocks that fill the GPU
 constexpr uint32_t kLpBadId = 0x10u;
 constexpr float kLpFar = 1024.f;                     // 2^-1024 is 0 in fp32
 
@@ -36,14 +38,15 @@ struct LpPart {
     int before;   // entries before the token
 };
 
-// Parts of a row: enough blocks to fill the GPU, each of at least a chunk.
+// Parts of a row: a chunk at least where the blocks would not fill the GPU, else eight chunks
+// at least, for eight times the blocks that fill it (rows that are not read and rows of
+// equal length leave no SM with a whole row alone at the end).
 static int lp_split(long long rows, int V) {
     const long long chunks = (V + kLpChunk - 1) / kLpChunk;
-    long long s = 1;
-    if (rows < 1216) s = (1216 + rows - 1) / rows;
-    if (s > chunks) s = chunks;
-    if (s > kLpMaxSplit) s = kLpMaxSplit;
-    return static_cast<int>(s);
+    const long long fill = std::min(chunks, (kLpFill + rows - 1) / rows);
+    const long long even = std::min(chunks / 8, (8 * kLpFill + rows - 1) / rows);
+    const long long s = std::max(fill, even);
+    return static_cast<int>(s < kLpMaxSplit ? s : kLpMaxSplit);
 }
 size_t logprob_workspace_bytes(long long rows, int V, int top) {
     const size_t parts = static_cast<size_t>(rows) * lp_split(rows, V);
@@ -110,18 +113,20 @@ __device__ __forceinline__ void lp_write_top(const LogprobParams& p, long long r
 // How many of n keys in shared memory are above k.
 __device__ __forceinline__ int lp_above(const unsigned long long* keys, int n, unsigned long long k) {
     int r = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) r += keys[j] > k ? 1 : 0;
     return r;
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams p, LpPart* parts,
+__global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobParams p, LpPart* parts,
                                                              unsigned long long* lists, int split) {
     constexpr int VEC = BF16 ? 8 : 4, N = kLpEach / VEC;  // entries of a load, loads of a chunk
     using X = std::conditional_t<BF16, uint16_t, float>;
     __shared__ unsigned long long s_best[kMaxTop], s_cand[kCand + kMaxTop], s_max[kLpThreads];
     __shared__ unsigned long long s_tau;
     __shared__ int s_n;
+    __shared__ uint32_t s_warp[kLpThreads / 32];
     __shared__ LpSum s_sum[kLpThreads / 32];
     __shared__ int s_before[kLpThreads / 32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 const uint32_t raw = BF16 ? (j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16) : w[j & 3];
-                f[k * VEC + j] = fmaxf(__uint_as_float(raw), -INFINITY);
+                f[k * VEC + j] = __uint_as_float(raw);  // (a NaN loses every comparison below)
             }
         }
         if (c + 1 < c1) fetch(c + 1);
@@ -197,14 +202,22 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
 #pragma unroll
             for (int k = 0; k < kLpEach; ++k) s.z += f[k] == INFINITY ? 1.f : 0.f;
         } else {
-            const float m = s.m == -INFINITY ? 0.f : s.m;
+            const float m = s.m == -INFINITY ? 0.f : s.m, mc = m * c2;
             float z = 0.f, w = 0.f;
+            if (fabsf(mc) < 1e30f) {  // (c x of the type's lowest value overflows to 2^-infinity)
 #pragma unroll
-            for (int k = 0; k < kLpEach; ++k) {
-                const float d = fmaxf((f[k] - m) * c2, -kLpFar);
-                const float e = ex2(d);
-                z += e;
-                w = fmaf(e, d, w);
+                for (int k = 0; k < kLpEach; ++k) {
+                    const float d = fmaxf(fmaf(f[k], c2, -mc), -kLpFar), e = ex2(d);
+                    z += e;
+                    w = fmaf(e, d, w);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kLpEach; ++k) {
+                    const float d = fmaxf((f[k] - m) * c2, -kLpFar), e = ex2(d);
+                    z += e;
+                    w = fmaf(e, d, w);
+                }
             }
             s.z += z;
             s.w += w;
@@ -213,9 +226,21 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
             return (c * (kLpChunk / VEC) + (k / VEC) * kLpThreads + tid) * VEC + k % VEC - shift;
         };
         if (here) {
+            // equal entries count where they stand before the token
+            const int at0 = c * kLpChunk - shift;
+            if (c > 0 && at0 + kLpChunk <= t && xt > -INFINITY) {
 #pragma unroll
-            for (int k = 0; k < kLpEach; ++k)
-                before += f[k] > xt || (f[k] == xt && index(k) >= 0 && index(k) < t) ? 1 : 0;
+                for (int k = 0; k < kLpEach; ++k) before += f[k] >= xt ? 1 : 0;
+            } else if (at0 > t && xt > -INFINITY) {
+#pragma unroll
+                for (int k = 0; k < kLpEach; ++k) before += f[k] > xt ? 1 : 0;
+            } else {
+#pragma unroll
+                for (int k = 0; k < kLpEach; ++k) {
+                    const float v = fmaxf(f[k], -INFINITY);  // (a NaN reads as -infinity)
+                    before += v > xt || (v == xt && index(k) >= 0 && index(k) < t) ? 1 : 0;
+                }
+            }
         }
         if (p.top == 0) continue;
         if (!__syncthreads_or(mx > tau)) continue;
@@ -228,6 +253,28 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
         __syncthreads();
         int at = mine ? atomicAdd(&s_n, mine) : 0;
         __syncthreads();
+        float least = tau;   // candidates: above thr, and not below this value
+        if (s_n > kCand) {
+            // the ceil(top / 8)-th largest of each warp's maxima
+            uint32_t o = mx > -INFINITY ? static_cast<uint32_t>(lp_key(mx, 0) >> 32) : 0u, v = 0u;
+            for (int k = 0; k < p.top; k += kLpThreads / 32) {
+                v = __reduce_max_sync(0xffffffffu, o);
+                const unsigned who = __ballot_sync(0xffffffffu, o == v);
+                if (lane == __ffs(who) - 1) o = 0u;
+            }
+            if (lane == 0) s_warp[warp] = v;
+            __syncthreads();
+            if (tid == 0) s_n = 0;
+#pragma unroll
+            for (int k = 0; k < kLpThreads / 32; ++k) v = min(v, s_warp[k]);
+            if (v) least = lp_key_value(static_cast<unsigned long long>(v) << 32);
+            mine = 0;
+#pragma unroll
+            for (int k = 0; k < kLpEach; ++k) mine += f[k] > tau && f[k] >= least ? 1 : 0;
+            __syncthreads();
+            at = mine ? atomicAdd(&s_n, mine) : 0;
+            __syncthreads();
+        }
         if (s_n > kCand) {
             unsigned long long best = 0;
 #pragma unroll
@@ -241,6 +288,7 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
             if (tid == 0) s_n = 0;
             __syncthreads();
             thr = max(thr, s_tau - 1);  // (that entry itself is a candidate)
+            least = -INFINITY;
             mine = 0;
 #pragma unroll
             for (int k = 0; k < kLpEach; ++k)
@@ -250,7 +298,8 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
         if (mine) {
 #pragma unroll
             for (int k = 0; k < kLpEach; ++k)
-                if (f[k] > -INFINITY && lp_key(f[k], index(k)) > thr) s_cand[at++] = lp_key(f[k], index(k));
+                if (f[k] > -INFINITY && f[k] >= least && lp_key(f[k], index(k)) > thr)
+                    s_cand[at++] = lp_key(f[k], index(k));
         }
         __syncthreads();
         const int n = s_n;
@@ -324,11 +373,20 @@ __global__ void __launch_bounds__(kLpThreads) logprob_join_kernel(const LogprobP
     }
     if (tid == 0) s_n = 0, s_tau = 0ull;
     __syncthreads();
-    LpSum s{s_part[0].m, s_part[0].z, s_part[0].w};
-    int before = s_part[0].before;
-    for (int k = 1; k < split; ++k) {
-        s = lp_add(s, LpSum{s_part[k].m, s_part[k].z, s_part[k].w}, p.scale * kLog2e);
-        before += s_part[k].before;
+    // every warp sums the parts, two a lane
+    const float c2 = p.scale * kLog2e;
+    const int lane = tid & 31;
+    auto part = [&](int k) {
+        return k < split ? LpSum{s_part[k].m, s_part[k].z, s_part[k].w} : LpSum{-INFINITY, 0.f, 0.f};
+    };
+    static_assert(kLpMaxSplit == 64, "two parts a lane");
+    LpSum s = lp_add(part(lane), part(lane + 32), c2);
+    int before = (lane < split ? s_part[lane].before : 0) + (lane + 32 < split ? s_part[lane + 32].before : 0);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s = lp_add(s, LpSum{__shfl_xor_sync(0xffffffffu, s.m, o), __shfl_xor_sync(0xffffffffu, s.z, o),
+                            __shfl_xor_sync(0xffffffffu, s.w, o)}, c2);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
     }
     if (tid == 0) lp_write(p, row, s, before, t, xt);
     if (p.top == 0) return;

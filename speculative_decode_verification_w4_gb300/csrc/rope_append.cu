@@ -76,8 +76,8 @@ __device__ __forceinline__ void store_unit(uint8_t* p, const float* v) {
 // The codes are to be those of the 64-bit formula, but 64-bit arithmetic has 1/64 of the
 // rate of 32-bit.  So 32 bits give t and how far it may be off, and both ends of that
 // range are rounded: where they agree, so does everything between (rounding is
-// monotone).  Where they do not (about three heads in a thousand), the warp takes that
-// head's norm again in 64 bits, and the lanes with such a value that value.
+// monotone).  Where they do not (about three heads in a thousand), the warp does the head
+// again: its norm in 64 bits, and the values near a border.
 //
 // kValueError bounds the error of a key against |a| + |c| of its plane, or |y| of a value
 // that is normed and not turned: the norm's sum of squares 13 roundings of 2^-24,
@@ -121,17 +121,22 @@ __device__ __forceinline__ uint32_t e2m1_code(float v) {
         : "=h"(r) : "f"(0.f), "f"(v));
     return r & 7u;
 }
+__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {  // signed, two nibbles
+    uint16_t r;
+    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b16 %0, {t, 0};\n\t}"
+        : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ float e2m1_value(uint32_t c) {
     return c < 4 ? 0.5f * static_cast<float>(c) : (c & 1 ? 1.5f : 1.f) * (c < 6 ? 2.f : 4.f);
 }
 
+// The lane's codes and block scale (low byte of the result's second word), by the whole warp.
 template <int D, class X>
-__device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, const float* head,
-                                          const float* offs, bool is_k, int hk, int pos,
-                                          long long at, long long bat, int lane) {
+__device__ __noinline__ uint2 kv4_near_border(const AppendParams& p, const X* x, const float* head,
+                                              const float* offs, bool is_k, int pos, float g) {
     constexpr int N = D / 32, GL = 16 / N;  // values of a lane, lanes of a block
-    const float* sp = is_k ? p.k_scale : p.v_scale;
-    const float g = sp ? __ldg(sp + hk) : 1.f;
+    const int lane = threadIdx.x & 31;
     const float ag = g == 0.f ? INFINITY : fabsf(g);
     float t[N], e[N];
     float lo = 0.f, hi = 0.f;
@@ -237,6 +242,82 @@ __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, con
     uint32_t w = 0;
 #pragma unroll
     for (int k = 0; k < N; ++k) w |= (c[k] | ((minus >> k) & 1u) << 3) << (4 * k);
+    return make_uint2(w, sb);
+}
+
+// The head's values from shared memory to the cache.  Quotients by products with reciprocals
+// here, off by 2^-23 at most; the margins count that.
+template <int D, class X>
+__device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, const float* head,
+                                          const float* offs, bool is_k, int hk, int pos,
+                                          long long at, long long bat, int lane) {
+    constexpr int N = D / 32, GL = 16 / N;  // values of a lane, lanes of a block
+    const float* sp = is_k ? p.k_scale : p.v_scale;
+    const float g = sp ? __ldg(sp + hk) : 1.f;
+    const float rg = __fdiv_rn(1.f, g), ar = fabsf(rg);
+    const bool usual = ar > 0.f && ar < 1e37f;  // (a scale of 0, or whose reciprocal overflows)
+    float m[N], e[N];
+    float lo = 0.f, hi = 0.f;
+    unsigned minus = 0;
+    bool odd = !usual;  // to be done again, or not a number
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const float y = head[lane * N + k], off = offs[lane * N + k], t = y * rg;
+        minus |= (t < 0.f ? 8u : 0u) << (4 * k);
+        m[k] = fminf(fabsf(t), 2688.f);
+        // Exact: nothing was rounded before, and the quotient is one.
+        e[k] = off == 0.f && fmaf(t, g, -y) == 0.f ? 0.f : fmaf(off, ar, m[k] * kDivError);
+        odd |= !(fabsf(t) < 1048576.f);
+        lo = fmaxf(lo, m[k] - e[k]);
+        hi = fmaxf(hi, fminf(m[k] + e[k], 2688.f));
+    }
+#pragma unroll
+    for (int o = 1; o < GL; o <<= 1) {
+        lo = fmaxf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    uint32_t sb = e4m3_byte(lo * (1.f / 6.f) * (1.f - kDivError));
+    const uint32_t sb1 = e4m3_byte(hi * (1.f / 6.f) * (1.f + kDivError));
+    if (sb != sb1) {
+        // the maximum itself against six times the border, which has few bits: exact
+        const float mid = 3.f * (e4m3_value(sb) + e4m3_value(sb1));
+        if (lo != hi || sb1 != sb + 1) odd = true;
+        else if (lo > mid || (lo == mid && (sb & 1u))) sb = sb1;
+    }
+    const float s = e4m3_value(sb), rs = sb ? __fdiv_rn(1.f, s) : 0.f;
+    uint32_t w = 0;
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+        float q[2], d[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            q[j] = m[k + j] * rs;
+            d[j] = fmaf(e[k + j], rs, q[j]) * kDivError;
+            d[j] = fmaf(e[k + j], rs, d[j]);
+        }
+        uint32_t a = e2m1_pair(q[0] - d[0], q[1] - d[1]) & 0x77u;
+        const uint32_t c = e2m1_pair(q[0] + d[0], q[1] + d[1]);
+        // (a value that may be 0 may come out below it: code 0 like 0)
+        if (q[0] < d[0]) a &= 0x70u;
+        if (q[1] < d[1]) a &= 0x07u;
+        if (a != c) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t ca = (a >> (4 * j)) & 7u, cc = (c >> (4 * j)) & 7u;
+                if (ca == cc) continue;
+                const float mid = 0.5f * (e2m1_value(ca) + e2m1_value(cc)) * s;  // exact
+                if (e[k + j] != 0.f || cc != ca + 1) odd = true;
+                else if (m[k + j] > mid || (m[k + j] == mid && (ca & 1u))) a += 1u << (4 * j);
+            }
+        }
+        w |= a << (4 * k);
+    }
+    w |= minus;
+    if (__any_sync(0xffffffffu, odd)) {
+        const uint2 r = kv4_near_border<D, X>(p, x, head, offs, is_k, pos, g);
+        w = r.x;
+        sb = r.y;
+    }
     uint8_t* dst = static_cast<uint8_t*>(is_k ? p.k : p.v) + at + lane * (N / 2);
     if (N == 8) *reinterpret_cast<uint32_t*>(dst) = w;
     else if (N == 4) *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(w);
@@ -246,7 +327,7 @@ __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, con
 }
 
 template <int D, int KIND, bool XBF16>
-__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams p,
+__global__ void __launch_bounds__(kAppendWarps * 32, KIND == kCacheKv4 ? 7 : 1) append_kernel(const AppendParams p,
                                                                    int heads_per_block) {
     constexpr bool F8 = KIND == kCacheE4m3, KV4 = KIND == kCacheKv4;
     constexpr int U = D / 64;  // dimensions of a unit; a lane has two

@@ -331,7 +331,7 @@ struct Kv4Blocks {             // block scales of K and V
 };
 size_t attn4_workspace_bytes(int B, int rows, int D);
 struct Attn4Plan {
-    int nt, grid;              // n-tiles of 8 query rows, bound of the grid
+    int nt, tk, grid;          // n-tiles of 8 query rows, keys of a tile, bound of the grid
     int box_bytes;
     CUtensorMapSwizzle swizzle;
 };
