@@ -195,21 +195,27 @@ __device__ __forceinline__ void push_phase(const AdvanceParams& p, const Advance
     });
 }
 
-__device__ __forceinline__ void fill_phase(const AdvanceParams& p, const AdvancePlan& w,
+// columns of sequence b that held pages before
+__device__ __forceinline__ int adv_kept(const AdvanceParams& p, const AdvancePlan& w, int b) {
+    return p.held_out[b] - static_cast<int>(w.take[b + 1] - w.take[b]);
+}
+__device__ __forceinline__ void take_phase(const AdvanceParams& p, const AdvancePlan& w,
                                            long long warp, long long warps) {
     const long long top = w.count[1] - 1;
-    auto kept = [&](int b) {  // columns that held pages before
-        return p.held_out[b] - static_cast<int>(w.take[b + 1] - w.take[b]);
-    };
     each_entry(w.take, p.B, w.take[p.B], warp, warps, [&](int b, long long i) {
-        p.table[b * p.table_stride + kept(b) + (i - w.take[b])] = p.free_list[top - i];
+        p.table[b * p.table_stride + adv_kept(p, w, b) + (i - w.take[b])] = p.free_list[top - i];
     });
+}
+// (reads no table column that take_phase writes)
+__device__ __forceinline__ void slot_phase(const AdvanceParams& p, const AdvancePlan& w,
+                                           long long warp, long long warps) {
     if (!p.slots) return;
+    const long long top = w.count[1] - 1;
     const long long rows = min(static_cast<long long>(p.row_start[p.B]), p.rows_max);
     bool bad = false;
     each_entry(p.row_start, p.B, rows, warp, warps, [&](int b, long long i) {
         const long long pos = p.lens_out[b] + (i - p.row_start[b]);
-        const int col = static_cast<int>(pos >> p.page_shift), k = kept(b);
+        const int col = static_cast<int>(pos >> p.page_shift), k = adv_kept(p, w, b);
         const int page = col < k ? p.table[b * p.table_stride + col]
                                  : p.free_list[top - (w.take[b] + col - k)];
         const bool ok = page >= 0 && page < p.num_pages;
@@ -230,18 +236,22 @@ __global__ void __launch_bounds__(kAdvThreads) advance_kernel(const AdvanceParam
     const long long warp = threadIdx.x >> 5;
     push_phase(p, w, warp, kAdvThreads / 32);
     __syncthreads();
-    fill_phase(p, w, warp, kAdvThreads / 32);
+    take_phase(p, w, warp, kAdvThreads / 32);
+    slot_phase(p, w, warp, kAdvThreads / 32);
 }
 
+// FILL: the first `takers` blocks fill the table, the others the slots.
 template <bool FILL>
 __global__ void __launch_bounds__(kFillThreads) advance_fill_kernel(const AdvanceParams p,
-                                                                    const AdvancePlan w) {
+                                                                    const AdvancePlan w, int takers) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long warps = static_cast<long long>(gridDim.x) * (kFillThreads / 32);
-    const long long warp = static_cast<long long>(blockIdx.x) * (kFillThreads / 32) + (threadIdx.x >> 5);
-    if (FILL) fill_phase(p, w, warp, warps);
-    else push_phase(p, w, warp, warps);
+    const int blocks = static_cast<int>(gridDim.x), block = static_cast<int>(blockIdx.x);
+    const int in = threadIdx.x >> 5;
+    constexpr int W = kFillThreads / 32;
+    if (!FILL) push_phase(p, w, block * W + in, blocks * W);
+    else if (block < takers) take_phase(p, w, block * W + in, takers * W);
+    else slot_phase(p, w, (block - takers) * W + in, (blocks - takers) * W);
 }
 
 cudaError_t launch_advance(const AdvanceParams& p, void* ws, int sms, cudaStream_t s) {
@@ -261,15 +271,16 @@ cudaError_t launch_advance(const AdvanceParams& p, void* ws, int sms, cudaStream
                     : p.B <= 4 * kAdvThreads ? cudaLaunchKernelEx(&cfg, advance_kernel<4>, p, w, all)
                                              : cudaLaunchKernelEx(&cfg, advance_kernel<16>, p, w, all);
     if (e != cudaSuccess || all) return e;
-    // (a block takes 512 entries at a time; how many pages move only the device knows)
-    const long long blocks = (rows + 511) / 512;
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks < sms ? sms : (blocks < 8LL * sms ? blocks : 8LL * sms)));
     cfg.blockDim = dim3(kFillThreads);
     if (p.ended) {
-        e = cudaLaunchKernelEx(&cfg, advance_fill_kernel<false>, p, w);
+        cfg.gridDim = dim3(2 * sms);
+        e = cudaLaunchKernelEx(&cfg, advance_fill_kernel<false>, p, w, 0);
         if (e != cudaSuccess) return e;
     }
-    return cudaLaunchKernelEx(&cfg, advance_fill_kernel<true>, p, w);
+    // a block takes 512 slots at a time; how many pages move only the device knows
+    const long long blocks = (rows + 511) / 512;
+    cfg.gridDim = dim3(static_cast<unsigned>(sms + (blocks < 6LL * sms ? blocks : 6LL * sms)));
+    return cudaLaunchKernelEx(&cfg, advance_fill_kernel<true>, p, w, sms);
 }
 
 }  // namespace vw4

@@ -8,12 +8,15 @@
 // (The difference first: c x of the type's lowest value, a usual mask, would overflow.)
 // Each thread keeps its own m, Z and W; they meet in a fixed order.
 //
-// Alternatives: the block keeps the `top` largest entries so far, as 64-bit keys (value,
-// then lower index first), and of a chunk of 4096 entries looks at those above the least
-// of them only.  Where more than kCand are (the first chunk), the threads' own maxima
-// give a better threshold first: of the `top` largest of them the least has that many
-// entries above it, which lie in that many threads.  A candidate's place is the number
-// of candidates above it, so nothing is sorted step by step.
+// Alternatives: the block keeps the `top` largest entries as 64-bit keys (value, then lower
+// index first) and lists those above the least of them; every few chunks of 4096 entries
+// its threads meet and choose from the list: a candidate's place is the number of
+// candidates above it, so nothing is sorted step by step.  The first chunk, where all are
+// above, gets a threshold first: the ceil(top / 8)-th largest of each warp's maxima, of
+// which the least has `top` entries that are not below it; and where that leaves too many
+// (equal entries, warps without any), the exact one: of the `top` largest maxima of a thread
+// the least has that many entries above it, which lie in that many threads.  Chunks that
+// overfill the list (rows in ascending order) are read again that way.
 //
 // The bytes bound it (4 or 2 a logit).  A row is split over blocks where the rows alone
 // would leave SMs idle; a second kernel joins the parts in order.
@@ -27,7 +30,10 @@ namespace vw4 {
 constexpr int kLpThreads = 256;
 constexpr int kLpEach = 16;                          // entries of a thread and chunk
 constexpr int kLpChunk = kLpThreads * kLpEach;
-constexpr int kCand = kMaxTop * kLpEach;             // candidates that are looked at at once
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kCand = kMaxTop * kLpEach;             // candidates of the list
+constexpr int kCandFull = 16;                        // so many are worth choosing from
+constexpr int kLpGroup = 8;                          // chunks between the block's meetings
 constexpr int kLpMaxSplit = 64;
 constexpr long long kLpFill = 608;                   // blocks that fill the GPU
 constexpr uint32_t kLpBadId = 0x10u;
@@ -38,13 +44,13 @@ struct LpPart {
     int before;   // entries before the token
 };
 
-// Parts of a row: a chunk at least where the blocks would not fill the GPU, else eight chunks
-// at least, for eight times the blocks that fill it (rows that are not read and rows of
-// equal length leave no SM with a whole row alone at the end).
+// Parts of a row: a chunk at least where the blocks would not fill the GPU, else sixteen
+// chunks at least (each part begins with the search for a threshold), for eight times the
+// blocks that fill it (no SM is left with a whole row alone at the end).
 static int lp_split(long long rows, int V) {
     const long long chunks = (V + kLpChunk - 1) / kLpChunk;
     const long long fill = std::min(chunks, (kLpFill + rows - 1) / rows);
-    const long long even = std::min(chunks / 8, (8 * kLpFill + rows - 1) / rows);
+    const long long even = std::min(chunks / 16, (8 * kLpFill + rows - 1) / rows);
     const long long s = std::max(fill, even);
     return static_cast<int>(s < kLpMaxSplit ? s : kLpMaxSplit);
 }
@@ -120,15 +126,15 @@ __device__ __forceinline__ int lp_above(const unsigned long long* keys, int n, u
 
 template <bool BF16>
 __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobParams p, LpPart* parts,
-                                                             unsigned long long* lists, int split) {
+                                                                unsigned long long* lists, int split) {
     constexpr int VEC = BF16 ? 8 : 4, N = kLpEach / VEC;  // entries of a load, loads of a chunk
     using X = std::conditional_t<BF16, uint16_t, float>;
     __shared__ unsigned long long s_best[kMaxTop], s_cand[kCand + kMaxTop], s_max[kLpThreads];
     __shared__ unsigned long long s_tau;
+    __shared__ uint32_t s_first[kLpWarps];
     __shared__ int s_n;
-    __shared__ uint32_t s_warp[kLpThreads / 32];
-    __shared__ LpSum s_sum[kLpThreads / 32];
-    __shared__ int s_before[kLpThreads / 32];
+    __shared__ LpSum s_sum[kLpWarps];
+    __shared__ int s_before[kLpWarps];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row = blockIdx.x / split;
@@ -179,10 +185,37 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
     };
     LpSum s{-INFINITY, 0.f, 0.f};
     int before = 0;
-    float tau = -INFINITY;  // of the list's last entry: what is larger is a candidate
     if (tid < kMaxTop) s_best[tid] = 0ull;
+    if (tid == 0) s_n = 0;
     if (c0 < c1) fetch(c0);
-    for (int c = c0; c < c1; ++c) {
+    if (p.top > 0) __syncthreads();
+    float tau = -INFINITY;  // of the last of s_best: what is larger is a candidate
+    int listed = 0;         // candidates at the last meeting
+    // the `top` largest of n candidates and of those before (all threads)
+    auto choose = [&](int n) {
+        if (tid < p.top) s_cand[n + tid] = s_best[tid];
+        __syncthreads();
+        // four threads a candidate
+        for (int j0 = 0; j0 < n + p.top; j0 += kLpThreads / 4) {
+            const int j = j0 + (tid >> 2);
+            const unsigned long long key = j < n + p.top ? s_cand[j] : 0ull;
+            int r = 0;
+#pragma unroll 4
+            for (int i = tid & 3; i < n + p.top; i += 4) r += s_cand[i] > key ? 1 : 0;
+            r += __shfl_xor_sync(0xffffffffu, r, 1);
+            r += __shfl_xor_sync(0xffffffffu, r, 2);
+            if (key && r < p.top && (tid & 3) == 0) s_best[r] = key;
+        }
+        if (tid == 0) s_n = 0;
+        __syncthreads();
+        listed = 0;
+        const unsigned long long last = s_best[p.top - 1];
+        tau = last ? lp_key_value(last) : -INFINITY;
+    };
+    int group = c0 + 1;     // first chunk since the last meeting
+    int careful = c0 + 1;   // chunks before it get a threshold of their own
+    bool again = false;     // of a second reading
+    for (int c = c0; c < c1;) {
         float f[kLpEach];
 #pragma unroll
         for (int k = 0; k < N; ++k) {
@@ -197,8 +230,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
         float mx = f[0];
 #pragma unroll
         for (int k = 1; k < kLpEach; ++k) mx = fmaxf(mx, f[k]);
-        if (mx > s.m) s = lp_move(s, mx, c2);
-        if (s.m == INFINITY) {
+        if (!again && mx > s.m) s = lp_move(s, mx, c2);
+        if (again) {
+        } else if (s.m == INFINITY) {
 #pragma unroll
             for (int k = 0; k < kLpEach; ++k) s.z += f[k] == INFINITY ? 1.f : 0.f;
         } else {
@@ -225,7 +259,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
         auto index = [&](int k) {
             return (c * (kLpChunk / VEC) + (k / VEC) * kLpThreads + tid) * VEC + k % VEC - shift;
         };
-        if (here) {
+        if (here && !again) {
             // equal entries count where they stand before the token
             const int at0 = c * kLpChunk - shift;
             if (c > 0 && at0 + kLpChunk <= t && xt > -INFINITY) {
@@ -242,77 +276,100 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
                 }
             }
         }
-        if (p.top == 0) continue;
-        if (!__syncthreads_or(mx > tau)) continue;
-        // ---- some entry may belong to the list
-        unsigned long long thr = s_best[p.top - 1];
-        int mine = 0;
+        if (p.top == 0) {
+            ++c;
+            continue;
+        }
+        // ---- alternatives
+        if (c < careful) {
+            float least = tau;   // candidates: above tau, and not below this value
+            {
+                // the ceil(top / 8)-th largest of each warp's maxima
+                uint32_t o = mx > -INFINITY ? static_cast<uint32_t>(lp_key(mx, 0) >> 32) : 0u, v = 0u;
+                for (int k = 0; k < p.top; k += kLpWarps) {
+                    v = __reduce_max_sync(0xffffffffu, o);
+                    const unsigned who = __ballot_sync(0xffffffffu, o == v);
+                    if (lane == __ffs(who) - 1) o = 0u;
+                }
+                if (lane == 0) s_first[warp] = v;
+                __syncthreads();
 #pragma unroll
-        for (int k = 0; k < kLpEach; ++k) mine += f[k] > tau ? 1 : 0;
-        if (tid == 0) s_n = 0;
-        __syncthreads();
-        int at = mine ? atomicAdd(&s_n, mine) : 0;
-        __syncthreads();
-        float least = tau;   // candidates: above thr, and not below this value
-        if (s_n > kCand) {
-            // the ceil(top / 8)-th largest of each warp's maxima
-            uint32_t o = mx > -INFINITY ? static_cast<uint32_t>(lp_key(mx, 0) >> 32) : 0u, v = 0u;
-            for (int k = 0; k < p.top; k += kLpThreads / 32) {
-                v = __reduce_max_sync(0xffffffffu, o);
-                const unsigned who = __ballot_sync(0xffffffffu, o == v);
-                if (lane == __ffs(who) - 1) o = 0u;
+                for (int k = 0; k < kLpWarps; ++k) v = min(v, s_first[k]);
+                if (v) least = lp_key_value(static_cast<unsigned long long>(v) << 32);
             }
-            if (lane == 0) s_warp[warp] = v;
-            __syncthreads();
-            if (tid == 0) s_n = 0;
+            unsigned long long thr = s_best[p.top - 1];
+            int mine = 0, at = 0;
+            if (mx > tau && mx >= least) {
 #pragma unroll
-            for (int k = 0; k < kLpThreads / 32; ++k) v = min(v, s_warp[k]);
-            if (v) least = lp_key_value(static_cast<unsigned long long>(v) << 32);
-            mine = 0;
+                for (int k = 0; k < kLpEach; ++k) mine += f[k] > tau && f[k] >= least ? 1 : 0;
+                at = atomicAdd(&s_n, mine);
+            }
+            __syncthreads();
+            if (s_n > kCand) {
+                unsigned long long best = 0;
 #pragma unroll
-            for (int k = 0; k < kLpEach; ++k) mine += f[k] > tau && f[k] >= least ? 1 : 0;
+                for (int k = 0; k < kLpEach; ++k)
+                    if (f[k] > -INFINITY) best = max(best, lp_key(f[k], index(k)));
+                // (threads without entries: keys of their own below every entry's)
+                if (best == 0) best = static_cast<unsigned long long>(tid);
+                s_max[tid] = best;
+                __syncthreads();
+                if (lp_above(s_max, kLpThreads, best) == p.top - 1) s_tau = best;
+                if (tid == 0) s_n = 0;
+                __syncthreads();
+                thr = max(thr, s_tau - 1);  // (that entry itself is a candidate)
+                least = -INFINITY;
+                mine = 0;
+#pragma unroll
+                for (int k = 0; k < kLpEach; ++k)
+                    mine += f[k] > -INFINITY && lp_key(f[k], index(k)) > thr ? 1 : 0;
+                at = mine ? atomicAdd(&s_n, mine) : 0;
+            }
+            if (mine) {
+#pragma unroll
+                for (int k = 0; k < kLpEach; ++k)
+                    if (f[k] > -INFINITY && f[k] >= least && lp_key(f[k], index(k)) > thr)
+                        s_cand[at++] = lp_key(f[k], index(k));
+            }
             __syncthreads();
-            at = mine ? atomicAdd(&s_n, mine) : 0;
-            __syncthreads();
+            choose(s_n);
+            if (++c == careful) {
+                again = false;
+                group = c;
+            }
+            continue;
         }
-        if (s_n > kCand) {
-            unsigned long long best = 0;
+        if (mx > tau) {
+            int mine = 0;
 #pragma unroll
-            for (int k = 0; k < kLpEach; ++k)
-                if (f[k] > -INFINITY) best = max(best, lp_key(f[k], index(k)));
-            // (threads without entries: keys of their own below every entry's)
-            if (best == 0) best = static_cast<unsigned long long>(tid);
-            s_max[tid] = best;
-            __syncthreads();
-            if (lp_above(s_max, kLpThreads, best) == p.top - 1) s_tau = best;
-            if (tid == 0) s_n = 0;
-            __syncthreads();
-            thr = max(thr, s_tau - 1);  // (that entry itself is a candidate)
-            least = -INFINITY;
-            mine = 0;
+            for (int k = 0; k < kLpEach; ++k) mine += f[k] > tau ? 1 : 0;
+            int at = atomicAdd(&s_n, mine);
+            if (at + mine <= kCand) {
 #pragma unroll
-            for (int k = 0; k < kLpEach; ++k)
-                mine += f[k] > -INFINITY && lp_key(f[k], index(k)) > thr ? 1 : 0;
-            at = mine ? atomicAdd(&s_n, mine) : 0;
+                for (int k = 0; k < kLpEach; ++k)
+                    if (f[k] > tau) s_cand[at++] = lp_key(f[k], index(k));
+            }
         }
-        if (mine) {
-#pragma unroll
-            for (int k = 0; k < kLpEach; ++k)
-                if (f[k] > -INFINITY && f[k] >= least && lp_key(f[k], index(k)) > thr)
-                    s_cand[at++] = lp_key(f[k], index(k));
-        }
+        if (++c < c1 && c - group < kLpGroup) continue;
+        // ---- the threads meet
         __syncthreads();
-        const int n = s_n;
-        if (tid < p.top) s_cand[n + tid] = s_best[tid];
-        __syncthreads();
-        for (int j = tid; j < n + p.top; j += kLpThreads) {
-            const unsigned long long key = s_cand[j];
-            const int r = key ? lp_above(s_cand, n + p.top, key) : p.top;
-            if (r < p.top) s_best[r] = key;
+        const int now = s_n;
+        if (now > kCand) {
+            // more than the list holds: without this group's, which is read again
+            choose(listed);
+            careful = c;
+            again = true;
+            c = group;
+            fetch(c);
+        } else {
+            if (now >= kCandFull || c == c1) {
+                choose(now);
+            } else {
+                listed = now;
+                __syncthreads();  // (all have read s_n)
+            }
+            group = c;
         }
-        __syncthreads();
-        const unsigned long long last = s_best[p.top - 1];
-        tau = last ? lp_key_value(last) : -INFINITY;
     }
 
     // ---- the block's threads
@@ -336,13 +393,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
         before += s_before[k];
     }
     const long long slot = row * split + part;
-    if (split > 1) {
-        if (tid == 0) parts[slot] = LpPart{s.m, s.z, s.w, before};
-        if (tid < p.top) lists[slot * p.top + tid] = s_best[tid];
-        return;
+    if (tid == 0) {
+        if (split > 1) parts[slot] = LpPart{s.m, s.z, s.w, before};
+        else lp_write(p, row, s, before, t, xt);
     }
-    if (tid == 0) lp_write(p, row, s, before, t, xt);
-    if (tid < p.top) lp_write_top(p, row, tid, s_best[tid], s.m, logf(s.z));
+    if (tid < p.top) {
+        if (split > 1) lists[slot * p.top + tid] = s_best[tid];
+        else lp_write_top(p, row, tid, s_best[tid], s.m, logf(s.z));
+    }
 }
 
 // Joins the parts of a row, a block a row.
@@ -367,9 +425,16 @@ __global__ void __launch_bounds__(kLpThreads) logprob_join_kernel(const LogprobP
         xt = fmaxf(BF16 ? __uint_as_float(static_cast<uint32_t>(raw) << 16)
                         : *reinterpret_cast<const float*>(&raw), -INFINITY);
     }
+    constexpr int kKeys = kLpMaxSplit * kMaxTop / kLpThreads;  // of a thread
+    unsigned long long key[kKeys];  // on their way before the heads say which count
+#pragma unroll
+    for (int q = 0; q < kKeys; ++q) {
+        const int j = tid + q * kLpThreads;
+        key[q] = j < split * p.top ? __ldcg(lists + row * split * p.top + j) : 0ull;
+    }
     if (tid < split) {
         s_part[tid] = parts[row * split + tid];
-        s_head[tid] = p.top ? lists[(row * split + tid) * p.top] : 0ull;
+        s_head[tid] = p.top ? __ldcg(lists + (row * split + tid) * p.top) : 0ull;
     }
     if (tid == 0) s_n = 0, s_tau = 0ull;
     __syncthreads();
@@ -396,18 +461,21 @@ __global__ void __launch_bounds__(kLpThreads) logprob_join_kernel(const LogprobP
         s_tau = s_head[tid];
     __syncthreads();
     const unsigned long long tau = s_tau;
-    for (int j = tid; j < split * p.top; j += kLpThreads) {
-        const unsigned long long key = s_head[j / p.top] < tau || s_head[j / p.top] == 0ull
-                                           ? 0ull
-                                           : lists[row * split * p.top + j];
-        if (key != 0ull && key >= tau) s_cand[atomicAdd(&s_n, 1)] = key;
-    }
+#pragma unroll
+    for (int q = 0; q < kKeys; ++q)
+        if (key[q] != 0ull && key[q] >= tau) s_cand[atomicAdd(&s_n, 1)] = key[q];
     __syncthreads();
     const int n = s_n;
     const float lnz = logf(s.z);
-    for (int j = tid; j < n; j += kLpThreads) {
-        const int r = lp_above(s_cand, n, s_cand[j]);
-        if (r < p.top) lp_write_top(p, row, r, s_cand[j], s.m, lnz);
+    for (int j0 = 0; j0 < n; j0 += kLpThreads / 4) {  // four threads a candidate
+        const int j = j0 + (tid >> 2);
+        const unsigned long long mine = j < n ? s_cand[j] : 0ull;
+        int r = 0;
+#pragma unroll 4
+        for (int i = tid & 3; i < n; i += 4) r += s_cand[i] > mine ? 1 : 0;
+        r += __shfl_xor_sync(0xffffffffu, r, 1);
+        r += __shfl_xor_sync(0xffffffffu, r, 2);
+        if (mine && r < p.top && (tid & 3) == 0) lp_write_top(p, row, r, mine, s.m, lnz);
     }
     if (tid >= n && tid < p.top) lp_write_top(p, row, tid, 0ull, s.m, lnz);
 }

@@ -25,6 +25,12 @@ constexpr int kAppendWarps = 4;
 constexpr int kMaxPairs = 128;
 
 template <int U>
+__device__ __forceinline__ void put_unit(float* p, const float* v) {  // (p aligned to the unit)
+    if (U == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else if (U == 2) *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    else p[0] = v[0];
+}
+template <int U>
 __device__ __forceinline__ void load_unit(const float* p, float* v) {
     if (U == 4) *reinterpret_cast<float4*>(v) = __ldg(reinterpret_cast<const float4*>(p));
     else if (U == 2) *reinterpret_cast<float2*>(v) = __ldg(reinterpret_cast<const float2*>(p));
@@ -143,7 +149,7 @@ __device__ __noinline__ uint2 kv4_near_border(const AppendParams& p, const X* x,
     bool nan = false;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const float y = head[lane * N + k], off = offs[lane * N + k];
+        const float y = head[lane * N + k], off = offs ? offs[lane * N + k] : 0.f;
         t[k] = g == 0.f ? 0.f : __fdiv_rn(y, g);
         nan |= t[k] != t[k];
         const float m = fminf(fabsf(t[k]), 2688.f);
@@ -260,9 +266,16 @@ __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, con
     float lo = 0.f, hi = 0.f;
     unsigned minus = 0;
     bool odd = !usual;  // to be done again, or not a number
+    __align__(16) float ys[N], of[N];
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+        *reinterpret_cast<float2*>(ys + k) = *reinterpret_cast<const float2*>(head + lane * N + k);
+        *reinterpret_cast<float2*>(of + k) =
+            offs ? *reinterpret_cast<const float2*>(offs + lane * N + k) : make_float2(0.f, 0.f);
+    }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const float y = head[lane * N + k], off = offs[lane * N + k], t = y * rg;
+        const float y = ys[k], off = of[k], t = y * rg;
         minus |= (t < 0.f ? 8u : 0u) << (4 * k);
         m[k] = fminf(fabsf(t), 2688.f);
         // Exact: nothing was rounded before, and the quotient is one.
@@ -326,23 +339,26 @@ __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, con
     if (lane % GL == 0) bl[bat + lane / GL] = static_cast<uint8_t>(sb);
 }
 
-template <int D, int KIND, bool XBF16>
-__global__ void __launch_bounds__(kAppendWarps * 32, KIND == kCacheKv4 ? 7 : 1) append_kernel(const AppendParams p,
-                                                                   int heads_per_block) {
+// A block's heads: all of them (kHeadsAll), queries or keys and values, from first on.
+constexpr int kHeadsAll = 0, kHeadsQ = 1, kHeadsKv = 2;
+
+template <int D, int KIND, bool XBF16, int PART>
+__device__ __forceinline__ void append_block(const AppendParams& p, int first, int heads_per_block) {
     constexpr bool F8 = KIND == kCacheE4m3, KV4 = KIND == kCacheKv4;
     constexpr int U = D / 64;  // dimensions of a unit; a lane has two
     using X = std::conditional_t<XBF16, __nv_bfloat16, float>;
     using C = std::conditional_t<KIND == kCacheBf16, __nv_bfloat16, uint8_t>;
     __shared__ __align__(16) float s_cos[kMaxPairs], s_sin[kMaxPairs];
     __shared__ __align__(16) float s_head[kAppendWarps][D];
-    __shared__ __align__(16) float s_off[KV4 ? kAppendWarps : 1][KV4 ? D : 1];
+    constexpr bool OFF = KV4 && PART != kHeadsQ;
+    __shared__ __align__(16) float s_off[OFF ? kAppendWarps : 1][OFF ? D : 1];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int token = blockIdx.x, b = token / p.R, i = token - b * p.R;
     const int pairs = p.rot / 2;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int heads = p.Hq + 2 * p.Hkv;
-    const int h_end = min(heads, (static_cast<int>(blockIdx.y) + 1) * heads_per_block);
+    const int heads = PART == kHeadsQ ? p.Hq : p.Hq + 2 * p.Hkv;
+    const int h_end = min(heads, first + heads_per_block);
     // the lane's units: lanes below P hold a pair of units that turn together, the others
     // two neighbouring units of the rest
     const bool split = pairs > 0 && !p.adjacent && pairs % U == 0;
@@ -353,7 +369,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, KIND == kCacheKv4 ? 7 : 1) 
         load_unit<U>(x + static_cast<long long>(h) * D + d0, v);
         load_unit<U>(x + static_cast<long long>(h) * D + d1, v + U);
     };
-    int h = blockIdx.y * heads_per_block + warp;
+    int h = first + warp;
     __align__(16) float v[2 * U], nx[2 * U];
     if (h < h_end) load(h, v);  // on its way while the angles are computed
     const int pos = p.seq_lens[b] - p.R + i;
@@ -364,7 +380,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, KIND == kCacheKv4 ? 7 : 1) 
     }
     // the token's cache slot
     long long slot = -1, bslot = 0;
-    if (pos >= 0) {
+    if (PART != kHeadsQ && pos >= 0) {
         const int blk = pos >> p.page_shift;
         const int pg = blk < p.max_blocks
                            ? __ldg(p.table + static_cast<long long>(b) * p.table_stride + blk)
@@ -388,7 +404,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32, KIND == kCacheKv4 ? 7 : 1) 
 
     for (; h < h_end; h += kAppendWarps) {
         if (h + kAppendWarps < h_end) load(h + kAppendWarps, nx);
-        const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
+        const bool is_q = PART == kHeadsQ || (PART == kHeadsAll && h < p.Hq);
+        const bool is_k = !is_q && h < p.Hq + p.Hkv;
         float off[KV4 ? 2 * U : 1];  // 4-bit keys: what a value may be off by
         if (KV4) {
 #pragma unroll
@@ -457,20 +474,22 @@ __global__ void __launch_bounds__(kAppendWarps * 32, KIND == kCacheKv4 ? 7 : 1) 
             __nv_bfloat16* dst = p.q + static_cast<long long>(token) * p.ldq + static_cast<long long>(h) * D;
             store_unit<U>(dst + d0, v);
             store_unit<U>(dst + d1, v + U);
-        } else if (KV4) {
+        } else if (OFF) {
             if (slot >= 0) {  // (the same for the warp)
                 __syncwarp();  // the last head's reads are done
+                float* offs = s_off[OFF ? warp : 0];
 #pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    s_head[warp][d0 + k] = v[k];
-                    s_head[warp][d1 + k] = v[U + k];
-                    s_off[KV4 ? warp : 0][KV4 ? d0 + k : 0] = off[KV4 ? k : 0] * kValueError;
-                    s_off[KV4 ? warp : 0][KV4 ? d1 + k : 0] = off[KV4 ? U + k : 0] * kValueError;
+                for (int k = 0; k < 2 * U; ++k) off[KV4 ? k : 0] *= kValueError;
+                put_unit<U>(s_head[warp] + d0, v);
+                put_unit<U>(s_head[warp] + d1, v + U);
+                if (is_k) {
+                    put_unit<U>(offs + d0, off);
+                    put_unit<U>(offs + d1, off + (KV4 ? U : 0));
                 }
                 __syncwarp();
                 const int hk = is_k ? h - p.Hq : h - p.Hq - p.Hkv;
                 store_kv4<D, X>(p, x + static_cast<long long>(h) * D, s_head[warp],
-                                s_off[KV4 ? warp : 0], is_k, hk, pos,
+                                is_k ? offs : nullptr, is_k, hk, pos,
                                 slot + static_cast<long long>(hk) * p.head_stride,
                                 bslot + static_cast<long long>(hk) * p.blocks_head_stride, lane);
             }
@@ -492,10 +511,27 @@ __global__ void __launch_bounds__(kAppendWarps * 32, KIND == kCacheKv4 ? 7 : 1) 
     }
 }
 
+template <int D, int KIND, bool XBF16>
+__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams p,
+                                                                   int heads_per_block) {
+    append_block<D, KIND, XBF16, kHeadsAll>(p, blockIdx.y * heads_per_block, heads_per_block);
+}
+// Queries and the others in blocks of their own: the registers that rounding to 4 bits takes
+// would be spilled in the queries' loop (2304 tokens of 32 heads of 256: 54 us together).
+template <int D, bool XBF16>
+__global__ void __launch_bounds__(kAppendWarps * 32, 7) append_kv4_kernel(const AppendParams p,
+                                                                          int heads_per_block) {
+    const int q_blocks = (p.Hq + heads_per_block - 1) / heads_per_block, y = blockIdx.y;
+    if (y < q_blocks)
+        append_block<D, kCacheKv4, XBF16, kHeadsQ>(p, y * heads_per_block, heads_per_block);
+    else
+        append_block<D, kCacheKv4, XBF16, kHeadsKv>(p, p.Hq + (y - q_blocks) * heads_per_block, heads_per_block);
+}
+
 template <int D>
 static void (*append_of(int kind, bool bf16))(const AppendParams, int) {
     if (kind == kCacheKv4)
-        return bf16 ? append_kernel<D, kCacheKv4, true> : append_kernel<D, kCacheKv4, false>;
+        return bf16 ? append_kv4_kernel<D, true> : append_kv4_kernel<D, false>;
     if (kind == kCacheE4m3)
         return bf16 ? append_kernel<D, kCacheE4m3, true> : append_kernel<D, kCacheE4m3, false>;
     return bf16 ? append_kernel<D, kCacheBf16, true> : append_kernel<D, kCacheBf16, false>;
@@ -516,7 +552,8 @@ cudaError_t launch_append(const AppendParams& p, int kind, int sms, cudaStream_t
     const int shares = (heads + per - 1) / per;
     per = ((heads + shares - 1) / shares + kAppendWarps - 1) / kAppendWarps * kAppendWarps;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(tokens, (heads + per - 1) / per);
+    cfg.gridDim = dim3(tokens, kind == kCacheKv4 ? (p.Hq + per - 1) / per + (2 * p.Hkv + per - 1) / per
+                                                 : (heads + per - 1) / per);
     cfg.blockDim = dim3(kAppendWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
