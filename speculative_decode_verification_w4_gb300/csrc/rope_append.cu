@@ -251,8 +251,9 @@ __device__ __noinline__ uint2 kv4_near_border(const AppendParams& p, const X* x,
     return make_uint2(w, sb);
 }
 
-// The head's values from shared memory to the cache.  Quotients by products with reciprocals
-// here, off by 2^-23 at most; the margins count that.
+// The head's values from shared memory to the cache.  Quotients are products with reciprocals
+// here: t is off by 2^-23 of itself (exact under a scale that is a power of two, where nothing
+// was rounded before), t / s by 2^-21 with it.
 template <int D, class X>
 __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, const float* head,
                                           const float* offs, bool is_k, int hk, int pos,
@@ -261,71 +262,67 @@ __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, con
     const float* sp = is_k ? p.k_scale : p.v_scale;
     const float g = sp ? __ldg(sp + hk) : 1.f;
     const float rg = __fdiv_rn(1.f, g), ar = fabsf(rg);
-    const bool usual = ar > 0.f && ar < 1e37f;  // (a scale of 0, or whose reciprocal overflows)
-    float m[N], e[N];
-    float lo = 0.f, hi = 0.f;
-    unsigned minus = 0;
-    bool odd = !usual;  // to be done again, or not a number
-    __align__(16) float ys[N], of[N];
+    bool odd = !(ar > 0.f && ar < 1e37f);  // to be done again (a scale of 0, or too small)
+    const bool exact = !offs && (__float_as_uint(g) & 0x7fffffu) == 0u;
+    __align__(16) float t[N], of[N];
 #pragma unroll
     for (int k = 0; k < N; k += 2) {
-        *reinterpret_cast<float2*>(ys + k) = *reinterpret_cast<const float2*>(head + lane * N + k);
+        *reinterpret_cast<float2*>(t + k) = *reinterpret_cast<const float2*>(head + lane * N + k);
         *reinterpret_cast<float2*>(of + k) =
             offs ? *reinterpret_cast<const float2*>(offs + lane * N + k) : make_float2(0.f, 0.f);
     }
+    uint32_t largest = 0u;  // bits of the largest magnitude: a NaN's are above all
+    float off = 0.f;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const float y = ys[k], off = of[k], t = y * rg;
-        minus |= (t < 0.f ? 8u : 0u) << (4 * k);
-        m[k] = fminf(fabsf(t), 2688.f);
-        // Exact: nothing was rounded before, and the quotient is one.
-        e[k] = off == 0.f && fmaf(t, g, -y) == 0.f ? 0.f : fmaf(off, ar, m[k] * kDivError);
-        odd |= !(fabsf(t) < 1048576.f);
-        lo = fmaxf(lo, m[k] - e[k]);
-        hi = fmaxf(hi, fminf(m[k] + e[k], 2688.f));
+        t[k] *= rg;
+        largest = max(largest, __float_as_uint(t[k]) & 0x7fffffffu);
+        off = fmaxf(off, of[k]);
     }
 #pragma unroll
     for (int o = 1; o < GL; o <<= 1) {
-        lo = fmaxf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+        if (offs) off = fmaxf(off, __shfl_xor_sync(0xffffffffu, off, o));
     }
+    const float m = __uint_as_float(largest);
+    odd |= !(m < 1048576.f);
+    const float e = exact ? 0.f : fmaf(off, ar, m * kDivError);
+    const float lo = fminf(m - e, 2688.f), hi = fminf(m + e, 2688.f);
     uint32_t sb = e4m3_byte(lo * (1.f / 6.f) * (1.f - kDivError));
     const uint32_t sb1 = e4m3_byte(hi * (1.f / 6.f) * (1.f + kDivError));
     if (sb != sb1) {
-        // the maximum itself against six times the border, which has few bits: exact
+        // an exact maximum against six times the border, which has few bits
         const float mid = 3.f * (e4m3_value(sb) + e4m3_value(sb1));
-        if (lo != hi || sb1 != sb + 1) odd = true;
+        if (!exact || sb1 != sb + 1) odd = true;
         else if (lo > mid || (lo == mid && (sb & 1u))) sb = sb1;
     }
-    const float s = e4m3_value(sb), rs = sb ? __fdiv_rn(1.f, s) : 0.f;
+    const float s = e4m3_value(sb), rs = sb ? __frcp_rn(s) : 0.f, ors = ar * rs;
     uint32_t w = 0;
 #pragma unroll
     for (int k = 0; k < N; k += 2) {
         float q[2], d[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            q[j] = m[k + j] * rs;
-            d[j] = fmaf(e[k + j], rs, q[j]) * kDivError;
-            d[j] = fmaf(e[k + j], rs, d[j]);
+            q[j] = t[k + j] * rs;
+            d[j] = fmaf(of[k + j], ors, fabsf(q[j]) * (2.f * kDivError));
         }
-        uint32_t a = e2m1_pair(q[0] - d[0], q[1] - d[1]) & 0x77u;
+        uint32_t a = e2m1_pair(q[0] - d[0], q[1] - d[1]);
         const uint32_t c = e2m1_pair(q[0] + d[0], q[1] + d[1]);
-        // (a value that may be 0 may come out below it: code 0 like 0)
-        if (q[0] < d[0]) a &= 0x70u;
-        if (q[1] < d[1]) a &= 0x07u;
         if (a != c) {
+            // a border between (or 0, of either sign): decided where t is exact
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const uint32_t ca = (a >> (4 * j)) & 7u, cc = (c >> (4 * j)) & 7u;
-                if (ca == cc) continue;
-                const float mid = 0.5f * (e2m1_value(ca) + e2m1_value(cc)) * s;  // exact
-                if (e[k + j] != 0.f || cc != ca + 1) odd = true;
-                else if (m[k + j] > mid || (m[k + j] == mid && (ca & 1u))) a += 1u << (4 * j);
+                const uint32_t ca = (a >> (4 * j)) & 15u, cc = (c >> (4 * j)) & 15u;
+                if (ca == cc || ((ca | cc) & 7u) == 0u) continue;
+                const uint32_t low = min(ca & 7u, cc & 7u), high = max(ca & 7u, cc & 7u);
+                const float mid = 0.5f * (e2m1_value(low) + e2m1_value(high)) * s, y = fabsf(t[k + j]);
+                if (!exact || ((ca ^ cc) & 8u) || high != low + 1) odd = true;
+                const uint32_t code = (y > mid || (y == mid && (low & 1u)) ? high : low) | (ca & 8u);
+                a = (a & ~(15u << (4 * j))) | code << (4 * j);
             }
         }
         w |= a << (4 * k);
     }
-    w |= minus;
     if (__any_sync(0xffffffffu, odd)) {
         const uint2 r = kv4_near_border<D, X>(p, x, head, offs, is_k, pos, g);
         w = r.x;
@@ -339,10 +336,11 @@ __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, con
     if (lane % GL == 0) bl[bat + lane / GL] = static_cast<uint8_t>(sb);
 }
 
-// A block's heads: all of them (kHeadsAll), queries or keys and values, from first on.
-constexpr int kHeadsAll = 0, kHeadsQ = 1, kHeadsKv = 2;
+// A block's heads, from first on: any (kHeadsAny), queries, or keys and values.
+constexpr int kHeadsAny = 0, kHeadsQ = 1, kHeadsKv = 2;
 
-template <int D, int KIND, bool XBF16, int PART>
+// AHEAD: how many heads of a warp are on their way while one is turned.
+template <int D, int KIND, bool XBF16, int PART, int AHEAD>
 __device__ __forceinline__ void append_block(const AppendParams& p, int first, int heads_per_block) {
     constexpr bool F8 = KIND == kCacheE4m3, KV4 = KIND == kCacheKv4;
     constexpr int U = D / 64;  // dimensions of a unit; a lane has two
@@ -370,8 +368,11 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int first, i
         load_unit<U>(x + static_cast<long long>(h) * D + d1, v + U);
     };
     int h = first + warp;
-    __align__(16) float v[2 * U], nx[2 * U];
+    __align__(16) float v[2 * U], nx[AHEAD][2 * U];
     if (h < h_end) load(h, v);  // on its way while the angles are computed
+#pragma unroll
+    for (int q = 0; q + 1 < AHEAD; ++q)
+        if (h + (q + 1) * kAppendWarps < h_end) load(h + (q + 1) * kAppendWarps, nx[q]);
     const int pos = p.seq_lens[b] - p.R + i;
     for (int j = threadIdx.x; j < pairs; j += kAppendWarps * 32) {
         double turns = static_cast<double>(pos) * p.inv_freq[j] * 0.15915494309189535;
@@ -403,8 +404,8 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int first, i
     }
 
     for (; h < h_end; h += kAppendWarps) {
-        if (h + kAppendWarps < h_end) load(h + kAppendWarps, nx);
-        const bool is_q = PART == kHeadsQ || (PART == kHeadsAll && h < p.Hq);
+        if (h + AHEAD * kAppendWarps < h_end) load(h + AHEAD * kAppendWarps, nx[AHEAD - 1]);
+        const bool is_q = PART == kHeadsQ || (PART == kHeadsAny && h < p.Hq);
         const bool is_k = !is_q && h < p.Hq + p.Hkv;
         float off[KV4 ? 2 * U : 1];  // 4-bit keys: what a value may be off by
         if (KV4) {
@@ -474,7 +475,7 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int first, i
             __nv_bfloat16* dst = p.q + static_cast<long long>(token) * p.ldq + static_cast<long long>(h) * D;
             store_unit<U>(dst + d0, v);
             store_unit<U>(dst + d1, v + U);
-        } else if (OFF) {
+        } else if (KV4 && PART != kHeadsQ) {
             if (slot >= 0) {  // (the same for the warp)
                 __syncwarp();  // the last head's reads are done
                 float* offs = s_off[OFF ? warp : 0];
@@ -507,25 +508,31 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int first, i
             store_unit<U>(dst + d1, v + U);
         }
 #pragma unroll
-        for (int k = 0; k < 2 * U; ++k) v[k] = nx[k];
+        for (int k = 0; k < 2 * U; ++k) {
+            v[k] = nx[0][k];
+#pragma unroll
+            for (int q = 0; q + 1 < AHEAD; ++q) nx[q][k] = nx[q + 1][k];
+        }
     }
 }
 
 template <int D, int KIND, bool XBF16>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams p,
                                                                    int heads_per_block) {
-    append_block<D, KIND, XBF16, kHeadsAll>(p, blockIdx.y * heads_per_block, heads_per_block);
+    append_block<D, KIND, XBF16, kHeadsAny, 1>(p, blockIdx.y * heads_per_block, heads_per_block);
 }
 // Queries and the others in blocks of their own: the registers that rounding to 4 bits takes
-// would be spilled in the queries' loop (2304 tokens of 32 heads of 256: 54 us together).
+// would be spilled in the queries' loop (2304 tokens of 32 heads of 256, with the rows read
+// back: 54 us together, 40 apart).  Keys and values first: a head that is done again has the
+// queries to hide behind (47 us last).
 template <int D, bool XBF16>
 __global__ void __launch_bounds__(kAppendWarps * 32, 7) append_kv4_kernel(const AppendParams p,
                                                                           int heads_per_block) {
-    const int q_blocks = (p.Hq + heads_per_block - 1) / heads_per_block, y = blockIdx.y;
-    if (y < q_blocks)
-        append_block<D, kCacheKv4, XBF16, kHeadsQ>(p, y * heads_per_block, heads_per_block);
+    const int kv_blocks = (2 * p.Hkv + heads_per_block - 1) / heads_per_block, y = blockIdx.y;
+    if (y < kv_blocks)
+        append_block<D, kCacheKv4, XBF16, kHeadsKv, 1>(p, p.Hq + y * heads_per_block, heads_per_block);
     else
-        append_block<D, kCacheKv4, XBF16, kHeadsKv>(p, p.Hq + (y - q_blocks) * heads_per_block, heads_per_block);
+        append_block<D, kCacheKv4, XBF16, kHeadsQ, 2>(p, (y - kv_blocks) * heads_per_block, heads_per_block);
 }
 
 template <int D>
