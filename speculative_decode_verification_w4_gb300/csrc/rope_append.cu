@@ -80,38 +80,50 @@ __device__ __forceinline__ void store_unit(uint8_t* p, const float* v) {
 // values of a block.  t = y / g, block scale s = e4m3(max |t| / 6), codes e2m1(t / s).
 //
 // The codes are to be those of the 64-bit formula, but 64-bit arithmetic has 1/64 of the
-// rate of 32-bit.  So 32 bits give t and how far it may be off, and both ends of that
+// rate of 32-bit.  So 32 bits give t / s and how far it may be off, and both ends of that
 // range are rounded: where they agree, so does everything between (rounding is
-// monotone).  Where they do not (about three heads in a thousand), the warp does the head
-// again: its norm in 64 bits, and the values near a border.
+// monotone).  Where they do not, |y| is compared with border * s * |g|: a fused product
+// and sum of 32 bits has the exact sign where y itself is exact; else (about six heads of
+// keys in a thousand) y is taken again in 64 bits, the head's norm by the warp, the value
+// by its lane.
 //
 // kValueError bounds the error of a key against |a| + |c| of its plane, or |y| of a value
 // that is normed and not turned: the norm's sum of squares 13 roundings of 2^-24,
 // halved by the root, rsqrtf two steps, the two factors and the mean one each: 2^-20.2;
 // angle, sine and cosine 2^-22.2, products and sum 2^-23: below 2^-19.
 constexpr float kValueError = 1.9073486328125e-6f;  // 2^-19
-constexpr float kDivError = 2.384185791015625e-7f;  // 2^-22, of a quotient by a quotient
+constexpr float kDivError = 2.384185791015625e-7f;  // 2^-22, of a product with a reciprocal
 
-// Dimension d of a key or value over its head's scale, from the 64-bit formula.
+// The norm's factor of a key head in 64 bits (the whole warp; 1 without a norm).
 template <int D, class X>
-__device__ __noinline__ double kv4_exact(const AppendParams& p, const X* x, bool is_k, int d,
-                                         double f, int pos, float g) {
-    const float* w = is_k ? p.k_norm : nullptr;
-    auto at = [&](int k) {
-        double y = static_cast<double>(static_cast<float>(x[k]));
-        if (w) y = y * f * static_cast<double>(w[k]);
-        return y;
-    };
-    double y = at(d);
-    if (is_k && d < p.rot) {
-        const int half = p.rot / 2, j = p.adjacent ? d >> 1 : (d < half ? d : d - half);
-        const bool second = p.adjacent ? d & 1 : d >= half;
-        const double c = at(p.adjacent ? d ^ 1 : (second ? d - half : d + half));
-        double sn, cs;
-        sincos(static_cast<double>(pos) * p.inv_freq[j], &sn, &cs);
-        y = second ? y * cs + c * sn : y * cs - c * sn;
+__device__ __noinline__ double kv4_norm(const AppendParams& p, const X* x) {
+    if (!p.k_norm) return 1.0;
+    double ss = 0.0;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+        const double v = static_cast<double>(static_cast<float>(x[(threadIdx.x & 31) * (D / 32) + k]));
+        ss = fma(v, v, ss);
     }
-    return g == 0.f ? 0.0 : y / static_cast<double>(g);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    return rsqrt(ss / D + static_cast<double>(p.eps));
+}
+// Dimension d of a key in 64 bits.
+template <int D, class X>
+__device__ __noinline__ double kv4_key(const AppendParams& p, const X* x, int d, double f, int pos) {
+    auto at = [&](int k) {
+        const double y = static_cast<double>(static_cast<float>(x[k]));
+        return p.k_norm ? y * f * static_cast<double>(p.k_norm[k]) : y;
+    };
+    const double y = at(d);
+    if (d >= p.rot) return y;
+    const int half = p.rot / 2, j = p.adjacent ? d >> 1 : (d < half ? d : d - half);
+    const bool second = p.adjacent ? d & 1 : d >= half;
+    const double c = at(p.adjacent ? d ^ 1 : (second ? d - half : d + half));
+    double turns = static_cast<double>(pos) * p.inv_freq[j] * 0.15915494309189535, sn, cs;
+    turns -= rint(turns);
+    sincospi(2.0 * turns, &sn, &cs);
+    return second ? y * cs + c * sn : y * cs - c * sn;
 }
 
 __device__ __forceinline__ uint32_t e4m3_byte(float v) {
@@ -120,14 +132,8 @@ __device__ __forceinline__ uint32_t e4m3_byte(float v) {
 __device__ __forceinline__ float e4m3_value(uint32_t b) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3)));
 }
-// code of a magnitude, 0 .. 7, and what a code stands for
-__device__ __forceinline__ uint32_t e2m1_code(float v) {
-    uint16_t r;
-    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b16 %0, {t, 0};\n\t}"
-        : "=h"(r) : "f"(0.f), "f"(v));
-    return r & 7u;
-}
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {  // signed, two nibbles
+// two codes, sign and magnitude, and what a magnitude stands for
+__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
     uint16_t r;
     asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b16 %0, {t, 0};\n\t}"
         : "=h"(r) : "f"(hi), "f"(lo));
@@ -137,123 +143,54 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
     return c < 4 ? 0.5f * static_cast<float>(c) : (c & 1 ? 1.5f : 1.f) * (c < 6 ? 2.f : 4.f);
 }
 
-// The lane's codes and block scale (low byte of the result's second word), by the whole warp.
+// What the quick way below does not take, all of it by quotients: infinities, NaN, head scales
+// of 0 or so small that their reciprocal overflows.  (Codes, block scale) of the lane.
 template <int D, class X>
-__device__ __noinline__ uint2 kv4_near_border(const AppendParams& p, const X* x, const float* head,
-                                              const float* offs, bool is_k, int pos, float g) {
-    constexpr int N = D / 32, GL = 16 / N;  // values of a lane, lanes of a block
+__device__ __noinline__ uint2 kv4_special(const AppendParams& p, const X* x, const float* head,
+                                          bool is_k, int pos, float g) {
+    constexpr int N = D / 32, GL = 16 / N;
     const int lane = threadIdx.x & 31;
-    const float ag = g == 0.f ? INFINITY : fabsf(g);
-    float t[N], e[N];
-    float lo = 0.f, hi = 0.f;
+    const double f = is_k ? kv4_norm<D, X>(p, x) : 1.0;
+    double t[N], m = 0.0;
     bool nan = false;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const float y = head[lane * N + k], off = offs ? offs[lane * N + k] : 0.f;
-        t[k] = g == 0.f ? 0.f : __fdiv_rn(y, g);
-        nan |= t[k] != t[k];
-        const float m = fminf(fabsf(t[k]), 2688.f);
-        // Nothing is lost: no rounding before, and the quotient is exact; an infinity, or a
-        // quotient beyond 2^20, is 2688 for sure.  The quotients of such an m by s and by 6
-        // need no margin either: a border times s, or 6, has at most 8 significant bits, so an
-        // m beside it is off by over 2^-24 of itself, and the rounded quotient stays beside.
-        const bool sure = fabsf(t[k]) > 1048576.f || g == 0.f || (off == 0.f && fmaf(t[k], g, -y) == 0.f);
-        e[k] = sure ? 0.f : __fdiv_rn(off, ag) + m * kDivError;
-        lo = fmaxf(lo, m - e[k]);
-        hi = fmaxf(hi, fminf(m + e[k], 2688.f));
+        const int d = lane * N + k;
+        const double y = is_k && isfinite(head[d]) ? kv4_key<D, X>(p, x, d, f, pos) : head[d];
+        t[k] = g == 0.f ? (isnan(y) ? y : 0.0) : y / static_cast<double>(g);
+        nan |= isnan(t[k]);
+        t[k] = fmin(fmax(t[k], -2688.0), 2688.0);
+        m = fmax(m, fabs(t[k]));
     }
     unsigned bad = nan;
 #pragma unroll
     for (int o = 1; o < GL; o <<= 1) {
-        lo = fmaxf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
         bad |= __shfl_xor_sync(0xffffffffu, bad, o);
     }
-    const float wide = lo == hi ? 0.f : kDivError;  // (the quotients are off by half a step)
-    uint32_t sb = e4m3_byte(__fdiv_rn(lo, 6.f) * (1.f - wide));
-    const uint32_t sb1 = e4m3_byte(__fdiv_rn(hi, 6.f) * (1.f + wide));
-    double f = 0.0;
-    bool have_f = false;
-    auto need_norm = [&] {  // all lanes
-        if (have_f) return;
-        have_f = true;
-        if (!is_k || !p.k_norm) return;
-        double ss = 0.0;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const double v = static_cast<double>(static_cast<float>(x[lane * N + k]));
-            ss += v * v;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        f = 1.0 / sqrt(ss / D + static_cast<double>(p.eps));
-    };
-    if (__any_sync(0xffffffffu, sb != sb1 && !bad)) {
-        need_norm();
-        double a = 0.0;
-        if (sb != sb1 && !bad) {
-#pragma unroll 1
-            for (int k = 0; k < N; ++k) {
-                float tk = t[0], ek = e[0];  // (registers: no index at run time)
-#pragma unroll
-                for (int q = 1; q < N; ++q) tk = q == k ? t[q] : tk, ek = q == k ? e[q] : ek;
-                if (fminf(fabsf(tk), 2688.f) + ek >= lo)
-                    a = fmax(a, fmin(fabs(kv4_exact<D, X>(p, x, is_k, lane * N + k, f, pos, g)), 2688.0));
-            }
-        }
-#pragma unroll
-        for (int o = 1; o < GL; o <<= 1) a = fmax(a, __shfl_xor_sync(0xffffffffu, a, o));
-        if (sb != sb1 && !bad) {
-            // the scale of the range that is nearest
-            const double q = a / 6.0;
-            while (sb < sb1) {
-                const double mid = 0.5 * (static_cast<double>(e4m3_value(sb)) + e4m3_value(sb + 1));
-                if (q < mid || (q == mid && !(sb & 1u))) break;
-                ++sb;
-            }
-        }
+    uint32_t sb = 0u;
+    while (sb < 0x7Eu) {
+        const double mid = 3.0 * (static_cast<double>(e4m3_value(sb)) + e4m3_value(sb + 1));
+        if (m < mid || (m == mid && !(sb & 1u))) break;
+        ++sb;
     }
-    if (bad) sb = 0x7Fu;
-    const float s = e4m3_value(sb);
-    const bool some = sb != 0u && !bad;
-    uint32_t c[N];
-    uint32_t unsure = 0, minus = 0;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const float m = fminf(fabsf(t[k]), 2688.f);
-        const float q = some ? __fdiv_rn(m, s) : 0.f;
-        const float dq = some && e[k] > 0.f ? __fdiv_rn(e[k], s) + q * kDivError : 0.f;
-        c[k] = e2m1_code(q - dq > 0.f ? q - dq : 0.f);
-        if (c[k] != e2m1_code(q + dq)) unsure |= 1u << k;
-        if (t[k] < 0.f) minus |= 1u << k;
-    }
-    if (__any_sync(0xffffffffu, unsure != 0)) {
-        need_norm();
-#pragma unroll 1
-        for (int k = 0; k < N; ++k) {
-            if (!((unsure >> k) & 1u)) continue;
-            const double v = kv4_exact<D, X>(p, x, is_k, lane * N + k, f, pos, g);
-            const double q = fmin(fabs(v), 2688.0) / static_cast<double>(s);
-            minus = (minus & ~(1u << k)) | (v < 0.0 ? 1u << k : 0u);
-            uint32_t n = 0;
-            while (n < 7) {
-                const double mid = 0.5 * (static_cast<double>(e2m1_value(n)) + e2m1_value(n + 1));
-                if (q < mid || (q == mid && !(n & 1u))) break;
-                ++n;
-            }
-#pragma unroll
-            for (int j = 0; j < N; ++j) c[j] = j == k ? n : c[j];
-        }
-    }
+    const double s = e4m3_value(sb);
     uint32_t w = 0;
 #pragma unroll
-    for (int k = 0; k < N; ++k) w |= (c[k] | ((minus >> k) & 1u) << 3) << (4 * k);
-    return make_uint2(w, sb);
+    for (int k = 0; k < N; ++k) {
+        uint32_t c = 0;
+        while (sb && c < 7u) {
+            const double mid = 0.5 * (static_cast<double>(e2m1_value(c)) + e2m1_value(c + 1)) * s;
+            if (fabs(t[k]) < mid || (fabs(t[k]) == mid && !(c & 1u))) break;
+            ++c;
+        }
+        w |= (c | (t[k] < 0.0 ? 8u : 0u)) << (4 * k);
+    }
+    return make_uint2(w, bad ? 0x7Fu : sb);
 }
 
-// The head's values from shared memory to the cache.  Quotients are products with reciprocals
-// here: t is off by 2^-23 of itself (exact under a scale that is a power of two, where nothing
-// was rounded before), t / s by 2^-21 with it.
+// The head's values from shared memory to the cache.  offs: what they may be off by (keys), or
+// null: exact.  t / s is y times a product of reciprocals: off by less than 2^-21 of itself.
 template <int D, class X>
 __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, const float* head,
                                           const float* offs, bool is_k, int hk, int pos,
@@ -261,13 +198,11 @@ __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, con
     constexpr int N = D / 32, GL = 16 / N;  // values of a lane, lanes of a block
     const float* sp = is_k ? p.k_scale : p.v_scale;
     const float g = sp ? __ldg(sp + hk) : 1.f;
-    const float rg = __fdiv_rn(1.f, g), ar = fabsf(rg);
-    bool odd = !(ar > 0.f && ar < 1e37f);  // to be done again (a scale of 0, or too small)
-    const bool exact = !offs && (__float_as_uint(g) & 0x7fffffu) == 0u;
-    __align__(16) float t[N], of[N];
+    const float rg = __fdiv_rn(1.f, g), ag = fabsf(g), ar = fabsf(rg);
+    __align__(16) float y[N], of[N];
 #pragma unroll
     for (int k = 0; k < N; k += 2) {
-        *reinterpret_cast<float2*>(t + k) = *reinterpret_cast<const float2*>(head + lane * N + k);
+        *reinterpret_cast<float2*>(y + k) = *reinterpret_cast<const float2*>(head + lane * N + k);
         *reinterpret_cast<float2*>(of + k) =
             offs ? *reinterpret_cast<const float2*>(offs + lane * N + k) : make_float2(0.f, 0.f);
     }
@@ -275,8 +210,7 @@ __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, con
     float off = 0.f;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        t[k] *= rg;
-        largest = max(largest, __float_as_uint(t[k]) & 0x7fffffffu);
+        largest = max(largest, __float_as_uint(y[k]) & 0x7fffffffu);
         off = fmaxf(off, of[k]);
     }
 #pragma unroll
@@ -285,48 +219,74 @@ __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, con
         if (offs) off = fmaxf(off, __shfl_xor_sync(0xffffffffu, off, o));
     }
     const float m = __uint_as_float(largest);
-    odd |= !(m < 1048576.f);
-    const float e = exact ? 0.f : fmaf(off, ar, m * kDivError);
-    const float lo = fminf(m - e, 2688.f), hi = fminf(m + e, 2688.f);
-    uint32_t sb = e4m3_byte(lo * (1.f / 6.f) * (1.f - kDivError));
-    const uint32_t sb1 = e4m3_byte(hi * (1.f / 6.f) * (1.f + kDivError));
-    if (sb != sb1) {
-        // an exact maximum against six times the border, which has few bits
-        const float mid = 3.f * (e4m3_value(sb) + e4m3_value(sb1));
-        if (!exact || sb1 != sb + 1) odd = true;
-        else if (lo > mid || (lo == mid && (sb & 1u))) sb = sb1;
-    }
-    const float s = e4m3_value(sb), rs = sb ? __frcp_rn(s) : 0.f, ors = ar * rs;
-    uint32_t w = 0;
-#pragma unroll
-    for (int k = 0; k < N; k += 2) {
-        float q[2], d[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            q[j] = t[k + j] * rs;
-            d[j] = fmaf(of[k + j], ors, fabsf(q[j]) * (2.f * kDivError));
-        }
-        uint32_t a = e2m1_pair(q[0] - d[0], q[1] - d[1]);
-        const uint32_t c = e2m1_pair(q[0] + d[0], q[1] + d[1]);
-        if (a != c) {
-            // a border between (or 0, of either sign): decided where t is exact
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t ca = (a >> (4 * j)) & 15u, cc = (c >> (4 * j)) & 15u;
-                if (ca == cc || ((ca | cc) & 7u) == 0u) continue;
-                const uint32_t low = min(ca & 7u, cc & 7u), high = max(ca & 7u, cc & 7u);
-                const float mid = 0.5f * (e2m1_value(low) + e2m1_value(high)) * s, y = fabsf(t[k + j]);
-                if (!exact || ((ca ^ cc) & 8u) || high != low + 1) odd = true;
-                const uint32_t code = (y > mid || (y == mid && (low & 1u)) ? high : low) | (ca & 8u);
-                a = (a & ~(15u << (4 * j))) | code << (4 * j);
-            }
-        }
-        w |= a << (4 * k);
-    }
-    if (__any_sync(0xffffffffu, odd)) {
-        const uint2 r = kv4_near_border<D, X>(p, x, head, offs, is_k, pos, g);
+    uint32_t w = 0, sb;
+    if (__any_sync(0xffffffffu, !(ar > 1e-30f && ar < 1e30f && m < 1e30f))) {
+        const uint2 r = kv4_special<D, X>(p, x, head, is_k, pos, g);
         w = r.x;
         sb = r.y;
+    } else {
+        const float e = fmaf(off, ar, m * ar * kDivError);
+        sb = e4m3_byte((m * ar - e) * (1.f / 6.f) * (1.f - kDivError));
+        const uint32_t sb1 = e4m3_byte((m * ar + e) * (1.f / 6.f) * (1.f + kDivError));
+        double f = 0.0;
+        bool have_f = false;
+        if (__any_sync(0xffffffffu, sb != sb1)) {
+            double top = m;
+            if (offs) {
+                f = kv4_norm<D, X>(p, x);
+                have_f = true;
+                top = 0.0;
+#pragma unroll 1
+                for (int k = 0; k < N; ++k) {
+                    const float v = head[lane * N + k];
+                    if (sb != sb1 && fabsf(v) + 2.f * off >= m)
+                        top = fmax(top, fabs(kv4_key<D, X>(p, x, lane * N + k, f, pos)));
+                }
+#pragma unroll
+                for (int o = 1; o < GL; o <<= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+            }
+            while (sb < sb1) {
+                const double mid = 3.0 * (static_cast<double>(e4m3_value(sb)) + e4m3_value(sb + 1)) * ag;
+                if (top < mid || (top == mid && !(sb & 1u))) break;
+                ++sb;
+            }
+        }
+        const float s = e4m3_value(sb), rs = sb ? __frcp_rn(s) : 0.f, c1 = rg * rs, c2 = ar * rs;
+        uint32_t unsure = 0;
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
+            float q[2], d[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                q[j] = y[k + j] * c1;
+                d[j] = fmaf(of[k + j], c2, fabsf(q[j]) * (2.f * kDivError));
+            }
+            const uint32_t a = e2m1_pair(q[0] - d[0], q[1] - d[1]);
+            const uint32_t c = e2m1_pair(q[0] + d[0], q[1] + d[1]);
+            unsure |= (a ^ c) << (4 * k);
+            w |= a << (4 * k);
+        }
+        if (__any_sync(0xffffffffu, unsure != 0u)) {
+            if (offs && !have_f) f = kv4_norm<D, X>(p, x);
+#pragma unroll 1
+            for (int k = 0; k < N; ++k) {
+                if (((unsure >> (4 * k)) & 15u) == 0u) continue;
+                // the codes that the range reaches, from the least magnitude on
+                const float v = head[lane * N + k], mag = fabsf(v), o = offs ? offs[lane * N + k] : 0.f;
+                const double v64 = offs ? kv4_key<D, X>(p, x, lane * N + k, f, pos) : 0.0;
+                const float least = mag * c2 - fmaf(o, c2, mag * c2 * (2.f * kDivError));
+                uint32_t c = least > 0.f ? e2m1_pair(least, 0.f) & 7u : 0u;
+                while (sb && c < 7u) {
+                    const float mid = 0.5f * (e2m1_value(c) + e2m1_value(c + 1)) * s;  // few bits
+                    const bool low = offs ? fabs(v64) < static_cast<double>(mid) * ag : fmaf(mid, ag, -mag) > 0.f;
+                    const bool tie = offs ? fabs(v64) == static_cast<double>(mid) * ag : fmaf(mid, ag, -mag) == 0.f;
+                    if (low || (tie && !(c & 1u))) break;
+                    ++c;
+                }
+                const bool minus = offs ? (v64 < 0.0) != (g < 0.f) : (v < 0.f) != (g < 0.f);
+                w = (w & ~(15u << (4 * k))) | (c | (minus ? 8u : 0u)) << (4 * k);
+            }
+        }
     }
     uint8_t* dst = static_cast<uint8_t*>(is_k ? p.k : p.v) + at + lane * (N / 2);
     if (N == 8) *reinterpret_cast<uint32_t*>(dst) = w;
@@ -490,7 +450,7 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int first, i
                 __syncwarp();
                 const int hk = is_k ? h - p.Hq : h - p.Hq - p.Hkv;
                 store_kv4<D, X>(p, x + static_cast<long long>(h) * D, s_head[warp],
-                                is_k ? offs : nullptr, is_k, hk, pos,
+                                is_k && (p.k_norm || p.rot > 0) ? offs : nullptr, is_k, hk, pos,
                                 slot + static_cast<long long>(hk) * p.head_stride,
                                 bslot + static_cast<long long>(hk) * p.blocks_head_stride, lane);
             }
