@@ -134,7 +134,8 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ __align__(8) uint64_t b_k[NK], b_ke[NK], b_v[NV], b_ve[NV], b_qe[2];
-    __shared__ AttnUnit s_unit[kUnitRing];
+    __shared__ AttnUnit s_unit[kUnitRing];  // a part's first unit, by its number
+    __shared__ int4 s_tile[kUnitRing];      // a unit's first key, flags, partial slot
     __shared__ volatile int s_abort;
     __shared__ float2 s_scale[2];    // a part's scales of its head of K and V, by seg & 1
     const int tid = threadIdx.x, lane = tid & 31, wk = tid >> 5;
@@ -182,55 +183,58 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
     };
 
     if (wk >= S::kWarps) {
-        // ------------------------------------------------------- producers
-        const bool keys = wk == S::kWarps;  // else values
+        // ------------------------------------------------------- a loading warp for K, one for V
+        const bool keys = wk == S::kWarps;
+        const CUtensorMap* map = keys ? &maps.k : &maps.v;
         const uint8_t* blocks = keys ? kb.k : kb.v;
         uint64_t* full = keys ? b_k : b_v;
         uint64_t* empty = keys ? b_ke : b_ve;
-        const int places = keys ? NK : NV;
+        const int places = keys ? NK : NV, base = keys ? 0 : S::kOffVal;
         const uint64_t policy = policy_evict_normal();
+        const uint32_t box = static_cast<uint32_t>(p.box_rows * NB);  // bytes of a box's scales
         AttnWalk<TK> w;
         w.begin(p, span, cap, lane);
-        int u = 0;
-        for (int st = 0, round = 0; u < n_units; ++u) {
+        int u = 0, st = 0, round = 0;
+        for (; u < n_units; ++u) {
             const AttnUnit d = w.unit(p);
             const AttnTile t = w.tile(p);
+            const bool q = keys && (d.flags & kUnitFirst);
             float ks = 1.f, vs = 1.f;
-            if (keys && (d.flags & kUnitFirst)) {
+            if (q) {
                 if (p.k_scale) ks = __ldg(p.k_scale + t.h);
                 if (p.v_scale) vs = __ldg(p.v_scale + t.h);
             }
             if (u + 1 < n_units) w.next(p, lane);
-            if (round > 0 && !wait(&empty[st], round - 1)) break;
-            const bool q = keys && (d.flags & kUnitFirst);
-            if (q && d.seg >= 2 && !wait(&b_qe[d.seg & 1], (d.seg >> 1) - 1)) break;
-            const int off = (keys ? 0 : S::kOffVal) + st * S::kStage;
-            const uint32_t box = static_cast<uint32_t>(t.box_rows * NB);  // bytes of a box's scales
-            uint8_t* sdst = smem + off + S::kTile + lane * box;
             const bool there = t.page >= 0 && t.page < p.num_pages;
+            const uint32_t bytes = t.template bytes<TK, 1, S::kKB>(0, lane) +
+                                   __popc(__ballot_sync(0xffffffffu, there)) * box;
+            const uint8_t* from = blocks;
+            if (there)
+                from += t.page * kb.page_stride + t.h * kb.head_stride +
+                        ((t.start + lane * p.box_rows) & (p.page_size - 1)) * NB;
+            const int off = base + st * S::kStage;
+            uint8_t* sdst = smem + off + S::kTile + lane * box;
+            if (round > 0 && !wait(&empty[st], round - 1)) break;
+            if (q && d.seg >= 2 && !wait(&b_qe[d.seg & 1], (d.seg >> 1) - 1)) break;
             if (t.page == p.num_pages) {  // no such page: zeros
                 for (uint32_t c = 0; c < box; c += 16)
                     *reinterpret_cast<uint4*>(sdst + c) = make_uint4(0, 0, 0, 0);
                 fence_async_smem();
             }
-            const uint32_t bytes = t.template bytes<TK, 1, S::kKB>(0, lane) +
-                                   __popc(__ballot_sync(0xffffffffu, there)) * box;
             __syncwarp();
             if (lane == 0) {
-                if (keys) s_unit[u % kUnitRing] = d;
-                if (q) s_scale[d.seg & 1] = make_float2(ks, vs);
+                if (keys) s_tile[u % kUnitRing] = make_int4(d.start, d.flags, d.slot, 0);
+                if (q) {
+                    s_unit[d.seg % kUnitRing] = d;
+                    s_scale[d.seg & 1] = make_float2(ks, vs);
+                }
                 mbar_arrive_expect_tx(&full[st], bytes + (q ? attn_q_bytes(p, D) : 0u));
                 if (q)
                     attn_load_q<D>(p, &maps.q, sm + S::kOffQ + (d.seg & 1) * S::kQ, S::kQBlk, d, &full[st]);
             }
             __syncwarp();
-            t.template load<TK, 1, 1, S::kKB, 1>(p, keys ? &maps.k : &maps.v, sm + off, &full[st], 0, 0,
-                                                 lane);
-            if (there)
-                bulk_load(sdst, blocks + t.page * kb.page_stride + t.h * kb.head_stride +
-                                    static_cast<long long>((t.start + lane * t.box_rows) &
-                                                           (p.page_size - 1)) * NB,
-                          box, &full[st], policy);
+            t.template load<TK, 1, 1, S::kKB, 1>(p, map, sm + off, &full[st], 0, 0, lane);
+            if (there) bulk_load(sdst, from, box, &full[st], policy);
             __syncwarp();
             if (++st == places) st = 0, ++round;
         }
@@ -262,6 +266,16 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
     const int key0 = wk * 16 * KM;                     // of the warp's keys
     const int slice0 = wk % S::kSlices * S::kOwn, part = wk / S::kSlices;
     const int inv_gb = 65536 / p.gb + 1;               // r / gb = r * inv_gb >> 16 for r < 64
+    // Matrix loads: the lane's part of the address, in which a further 32-dimension chunk of K
+    // (even), slice of V or half of 64 query dimensions is an exclusive or.
+    const uint32_t k_lane = S::at(key0 + lr + (lm & 1) * 8, lm >> 1);
+    const uint32_t v_lane = S::at(part * (TK / S::kParts) + lr + 8 * lm, slice0);
+    const uint32_t q_lane = S::q_at(lr, lm);
+    const uint32_t p_lane = (part * (TK / S::kParts) + lr + 8 * lm) * 16;
+    const uint32_t sc_lane = S::kOffV + t4 * 16 + (slice0 * 2 + (lane >> 4)) * S::kVRow +
+                             part * (TK / S::kParts) * 2;
+    int kst = 0, vst = 0, vlast = 0;                   // places of the unit's K and V, of the last V
+    int kround = 0, vround = 0;
 
     auto row2 = [&](const float* a, int n, float* v) {  // of the lane's two query rows
         const float2 f = *reinterpret_cast<const float2*>(a + n * 8 + t4 * 2);
@@ -269,23 +283,22 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
         v[1] = f.y;
     };
 
-    // O += V^T P^T of unit u
-    auto values = [&](int u) {
-        const uint32_t vS = sm + S::kOffVal + u % NV * S::kStage;
-        const uint32_t pS = sm + S::kOffP + (u & 1) * S::kP;
-        const uint8_t* sc = smem + S::kOffV + (u & 1) * S::kVS + t4 * 16 + (lane >> 4) * S::kVRow;
+    // O += V^T P^T of unit u, whose V is in place st
+    auto values = [&](int u, int st) {
+        const uint32_t vS = sm + S::kOffVal + st * S::kStage + v_lane;
+        const uint32_t pS = sm + S::kOffP + (u & 1) * S::kP + p_lane;
+        const uint8_t* sc = smem + (u & 1) * S::kVS + sc_lane;
 #pragma unroll
         for (int k = 0; k < TK / S::kParts; k += 32) {
-            const int key = part * (TK / S::kParts) + k;
             uint32_t x[S::kOwn][4], b[NT][4];
             uint4 sv[S::kOwn];
 #pragma unroll
             for (int q = 0; q < S::kOwn; ++q) {
-                ldsm4t_free(x[q], vS + S::at(key + lr + 8 * lm, slice0 + q));
-                sv[q] = *reinterpret_cast<const uint4*>(sc + (slice0 + q) * 2 * S::kVRow + key * 2);
+                ldsm4t_free(x[q], (vS ^ (q << 4)) + k * S::kKB);
+                sv[q] = *reinterpret_cast<const uint4*>(sc + q * 2 * S::kVRow + k * 2);
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) ldsm4t_free(b[n], pS + n * (TK * 16) + (key + lr + 8 * lm) * 16);
+            for (int n = 0; n < NT; ++n) ldsm4t_free(b[n], pS + n * (TK * 16) + k * 16);
 #pragma unroll
             for (int q = 0; q < S::kOwn; ++q) {
                 const uint32_t s[4] = {sv[q].x, sv[q].y, sv[q].z, sv[q].w};
@@ -313,11 +326,11 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
         }
     };
 
-    for (int u = 0; u < n_units; ++u) {
+    for (int u = 0, seg = 0; u < n_units; ++u) {
         // ---- a part of an item: its queries
-        dead |= !wait(&b_k[u % NK], u / NK);
-        AttnUnit td = s_unit[u % kUnitRing];
-        const int qslot = td.seg & 1;
+        dead |= !wait(&b_k[kst], kround);
+        const AttnUnit td = s_unit[seg % kUnitRing];
+        const int qslot = seg++ & 1;
         const uint32_t qs = sm + S::kOffQ + qslot * S::kQ;
         const int h = td.g / p.row_blocks;
         float ks = 1.f, vs = 1.f;
@@ -397,13 +410,13 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
                 for (int i = 0; i < 2; ++i)
                     o[q][i][n][0] = o[q][i][n][1] = o[q][i][n][2] = o[q][i][n][3] = 0.f;
         }
+        int4 tile;
         for (const int first = u;; ++u) {
-            if (u > first) {
-                dead |= !wait(&b_k[u % NK], u / NK);
-                if (!dead) td = s_unit[u % kUnitRing];
-            }
-            const bool edge = td.flags & kUnitEdge;
-            const uint8_t* keys = smem + u % NK * S::kStage;
+            if (u > first) dead |= !wait(&b_k[kst], kround);
+            tile = s_tile[u % kUnitRing];
+            const int start = tile.x;
+            const bool edge = tile.y & kUnitEdge;
+            const uint8_t* keys = smem + kst * S::kStage;
             float s[KM][NT][4];
             float sum[NT][2];
             // weights of an n-tile against a reference, to shared memory
@@ -434,7 +447,7 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
             bool grew = false;
             if (!dead) {
                 // ---- S = K Q^T of the warp's keys
-                const uint32_t kS = sm + u % NK * S::kStage;
+                const uint32_t kS = sm + kst * S::kStage + k_lane, qS = qs + q_lane;
                 uint32_t sk[2 * KM][D / 64];  // scales of two 32-dimension chunks, of keys u8 + 8 k
 #pragma unroll
                 for (int k = 0; k < 2 * KM; ++k) {
@@ -466,13 +479,13 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
                     uint32_t w[KM][4];
 #pragma unroll
                     for (int m = 0; m < KM; ++m)
-                        ldsm4_free(w[m], kS + S::at(key0 + 16 * m + lr + (lm & 1) * 8, c + (lm >> 1)));
+                        ldsm4_free(w[m], (kS ^ (c << 4)) + m * 16 * S::kKB);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         uint32_t b[NT][4];
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-                            ldsm4_free(b[n], qs + S::q_at(n * 8 + lr, (c + e) * 4 + lm));
+                            ldsm4_free(b[n], (qS ^ (e << 6)) + c / 2 * S::kQBlk + n * 1024);
 #pragma unroll
                         for (int m = 0; m < KM; ++m) {
                             uint32_t x[4], y[4];
@@ -499,27 +512,27 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
                             const int pos = s_pos[n * 8 + t4 * 2 + k];
 #pragma unroll
                             for (int m = 0; m < KM; ++m) {
-                                const int j = td.start + key0 + 16 * m + u8;
+                                const int j = start + key0 + 16 * m + u8;
                                 if (!key_seen(j, pos, p.window, p.sinks)) s[m][n][k] = -INFINITY;
                                 if (!key_seen(j + 8, pos, p.window, p.sinks)) s[m][n][k + 2] = -INFINITY;
                             }
                         }
                 }
                 // ---- V's scales to f16, token by token: a thread a part of a token's
-                dead |= !wait(&b_v[u % NV], u / NV);
+                dead |= !wait(&b_v[vst], vround);
                 if (!dead) {
                     constexpr int PER = TK * NB / (S::kWarps * 32);  // bytes of a thread
                     static_assert(PER == 2 || PER == 4 || PER == 8, "up to two words");
                     constexpr int W = (PER + 3) / 4;
                     constexpr int TPT = NB / PER;                    // threads of a token
                     const int token = tid / TPT, b0 = tid % TPT * PER;
-                    const uint8_t* src = smem + S::kOffVal + u % NV * S::kStage + S::kTile + token * NB + b0;
+                    const uint8_t* src = smem + S::kOffVal + vst * S::kStage + S::kTile + token * NB + b0;
                     uint32_t w[W];
                     if (PER == 2) w[0] = *reinterpret_cast<const uint16_t*>(src);
 #pragma unroll
                     for (int k = 0; k < PER / 4; ++k) w[k] = reinterpret_cast<const uint32_t*>(src)[k];
                     if (edge) {
-                        const int j = td.start + token;
+                        const int j = start + token;
                         if (!key_some(j, td.len, td.p0, p.window, p.sinks)) {
                             // no row sees it: zeros, whatever the cache holds there
 #pragma unroll
@@ -559,7 +572,7 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
                                 largest(n, 1) * c2[1] > ref[1] + kLazy4;
                         weights(n, c2, ref);
                     }
-                    values(u - 1);
+                    values(u - 1, vlast);
                 }
             }
             if (meet(grew || dead)) {
@@ -622,12 +635,15 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
                 l[n][1] += sum[n][1];
             }
             if (tid == 0) {
-                mbar_arrive(&b_ke[u % NK]);
-                if (u > first) mbar_arrive(&b_ve[(u - 1) % NV]);
+                mbar_arrive(&b_ke[kst]);
+                if (u > first) mbar_arrive(&b_ve[vlast]);
             }
-            if (td.flags & kUnitLast) break;
+            vlast = vst;
+            if (++kst == NK) kst = 0, ++kround;
+            if (++vst == NV) vst = 0, ++vround;
+            if (tile.y & kUnitLast) break;
         }
-        values(u);
+        values(u, vlast);
         // ---- end of the part: join the warps, write out
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -638,8 +654,9 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
                 for (int q = 4; q < 32; q <<= 1) x += __shfl_xor_sync(0xffffffffu, x, q);
                 if (lane < 4) s_l[wk * S::kRows + n * 8 + t4 * 2 + k] = x;
             }
+        const int slot = tile.z;
         float* po = nullptr;  // partial rows [rows][D], then m [rows], l [rows]
-        if (td.slot >= 0) po = p.partial + static_cast<long long>(td.slot) * S::kRows * (D + 2);
+        if (slot >= 0) po = p.partial + static_cast<long long>(slot) * S::kRows * (D + 2);
         float4* xb = reinterpret_cast<float4*>(smem + S::kOffX);
         meet(false);
         if (tid < S::kRows) {  // a row's sum, its factor and the row's own outputs
@@ -650,7 +667,7 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
             const float ref = s_ref[turn * S::kRows + r];
             const float M = ref == -INFINITY ? -INFINITY : ref - kTail4;
             s_m[r] = L == 0.f ? 0.f : vs / L;
-            if (td.slot >= 0) {
+            if (slot >= 0) {
                 po[S::kRows * D + r] = M;
                 po[S::kRows * (D + 1) + r] = L;
             } else if (p.lse && to >= 0) {
@@ -700,7 +717,7 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
                         const int col = (slice0 + q) * 32 + u8 * 4;
                         if ((nan >> (col / 16)) & 1u) v[q][k] = make_float4(NAN, NAN, NAN, NAN);
                         if (to < 0) {
-                        } else if (td.slot >= 0) {
+                        } else if (slot >= 0) {
                             *reinterpret_cast<float4*>(po + (r + k) * D + col) = v[q][k];
                         } else {
                             *reinterpret_cast<uint2*>(out + col) =
@@ -713,7 +730,7 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
             if (S::kParts > 1 || n == NT - 1) meet(false);
         }
         if (tid == 0) {
-            mbar_arrive(&b_ve[u % NV]);
+            mbar_arrive(&b_ve[vlast]);
             mbar_arrive(&b_qe[qslot]);
         }
     }
