@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
     attn4_kernel(const AttnParams p, const Kv4Blocks kb, const __grid_constant__ AttnMaps maps) {
     using S = Attn4Shape<D, NT>;
     constexpr int TK = S::kTK, NK = S::kNK, NV = S::kNV, NB = S::kNB, KM = S::kKM;
+    constexpr bool kValuesFirst = NT <= 3;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ __align__(8) uint64_t b_k[NK], b_ke[NK], b_v[NV], b_ve[NV], b_qe[2];
@@ -504,6 +505,8 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
                         }
                     }
                 }
+                // (the products of S are on their way meanwhile, where the registers last for both)
+                if (kValuesFirst && u > first) values(u - 1, vlast);
                 if (edge) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -572,7 +575,7 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
                                 largest(n, 1) * c2[1] > ref[1] + kLazy4;
                         weights(n, c2, ref);
                     }
-                    values(u - 1, vlast);
+                    if (!kValuesFirst) values(u - 1, vlast);
                 }
             }
             if (meet(grew || dead)) {
