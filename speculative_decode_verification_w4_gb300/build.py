@@ -23,7 +23,7 @@ BUILD_CHECKS = os.path.join(HERE, "_build_checks")
 LIB_CHECKS = os.path.join(HERE, "libvw4_checks.so")
 SOURCES = ["api.cu", "gemm_w4.cu", "accept.cu", "rejection.cu", "controller.cpp", "step_api.cu",
            "attn.cu", "attn_d64.cu", "attn_d128.cu", "attn_d256.cu", "rope_append.cu", "logits.cu",
-           "kv4_api.cu", "attn4.cu", "attn4_d64.cu", "attn4_d128.cu", "attn4_d256.cu", "read4.cu",
+           "kv4_api.cu", "attn4.cu", "attn4_d64.cu", "attn4_d128.cu", "attn4_d256.cu", "attn4_tc.cu", "read4.cu",
            "advance.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler",

@@ -29,29 +29,19 @@ namespace vw4 {
 constexpr float kTail4 = 9.f;     // weights carry 2^9
 constexpr float kLazy4 = 5.f;     // (log2) of the reference
 
-// Keys of a tile and warps that compute.  Four warps and about 18 KB a tile put two or three
-// blocks on an SM; with 48 and 64 rows the outputs' registers leave room for fewer keys a
-// warp, and at head size 256 for half of the dimensions.
-__host__ __device__ constexpr int attn4_tk(int D, int nt) {
-    return (D == 256 && nt < 6) || (D == 128 && nt >= 6) ? 64 : 128;
-}
-__host__ __device__ constexpr int attn4_warps(int D, int nt) { return D != 128 && nt >= 6 ? 8 : 4; }
+// Keys of a tile.  Four warps and about 18 KB a tile put two or three blocks on an SM.
+__host__ __device__ constexpr int attn4_tk(int D) { return D == 256 ? 64 : 128; }
 // Places of the ring of K tiles: what shared memory leaves.
 __host__ __device__ constexpr int attn4_places(int D, int nt) {
-    return D == 64              ? 6
-           : D == 128 && nt > 4 ? (nt == 6 ? 6 : 5)
-           : nt == 1            ? 3
-           : D == 128           ? (nt == 4 ? 3 : 4)
-           : nt > 4             ? (nt == 6 ? 3 : 2)
-                                : (nt >= 3 ? 3 : 4);
+    return D == 64 ? 6 : (nt == 1 ? 3 : (D == 128 ? (nt == 4 ? 3 : 4) : (nt >= 3 ? 3 : 4)));
 }
 
 #ifdef __CUDACC__
 template <int D, int NT>
 struct Attn4Shape {
-    static constexpr int kWarps = attn4_warps(D, NT);
+    static constexpr int kWarps = 4;
     static constexpr int kThreads = (kWarps + 2) * 32;
-    static constexpr int kTK = attn4_tk(D, NT);
+    static constexpr int kTK = attn4_tk(D);
     static constexpr int kKM = kTK / kWarps / 16;     // 16-key row tiles of a warp
     static constexpr int kRows = 8 * NT;
     static constexpr int kKB = D / 2;                 // bytes of a key's codes
@@ -68,7 +58,7 @@ struct Attn4Shape {
     static constexpr int kVRow = (kTK + 16) * 2;      // V's scales: f16 [block][v_at(token)]
     static constexpr int kVS = kNB * kVRow;
     static constexpr int kX = (kParts - 1) * kSlices * 1024;  // an n-tile's outputs of the other parts
-    static constexpr int kMinBlocks = kWarps == 8 ? 1 : (NT == 1 ? 3 : 2);
+    static constexpr int kMinBlocks = NT == 1 ? 3 : 2;
     // V of a tile is read a phase after its K: one place more, if it fits
     static constexpr int kNK = attn4_places(D, NT), kNV = kNK + (NT == 1 && D > 64 ? 0 : 1);
     static constexpr int kOffVal = kNK * kStage;
@@ -266,7 +256,7 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
     const int t4 = lane & 3, u8 = lane >> 2, lm = lane >> 3, lr = lane & 7;
     const int key0 = wk * 16 * KM;                     // of the warp's keys
     const int slice0 = wk % S::kSlices * S::kOwn, part = wk / S::kSlices;
-    const int inv_gb = 65536 / p.gb + 1;               // r / gb = r * inv_gb >> 16 for r < 64
+    const int inv_gb = 65536 / p.gb + 1;               // r / gb = r * inv_gb >> 16 for r < 32
     // Matrix loads: the lane's part of the address, in which a further 32-dimension chunk of K
     // (even), slice of V or half of 64 query dimensions is an exclusive or.
     const uint32_t k_lane = S::at(key0 + lr + (lm & 1) * 8, lm >> 1);
@@ -782,8 +772,6 @@ cudaError_t attn4_dispatch(const AttnParams& p, const Kv4Blocks& kb, const AttnM
         case 2: return attn4_launch<D, 2>(p, kb, maps, grid, sms, s);
         case 3: return attn4_launch<D, 3>(p, kb, maps, grid, sms, s);
         case 4: return attn4_launch<D, 4>(p, kb, maps, grid, sms, s);
-        case 6: return attn4_launch<D, 6>(p, kb, maps, grid, sms, s);
-        case 8: return attn4_launch<D, 8>(p, kb, maps, grid, sms, s);
     }
     return cudaErrorInvalidValue;
 }

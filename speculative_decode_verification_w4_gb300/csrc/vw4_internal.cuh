@@ -331,7 +331,8 @@ struct Kv4Blocks {             // block scales of K and V
 };
 size_t attn4_workspace_bytes(int B, int rows, int D);
 struct Attn4Plan {
-    int nt, tk, grid;          // n-tiles of 8 query rows, keys of a tile, bound of the grid
+    bool tc;                   // on the 5th-generation tensor cores
+    int rows, tk, grid;        // query rows of a block, keys of a tile, bound of the grid
     int box_bytes;
     CUtensorMapSwizzle swizzle;
 };
@@ -344,6 +345,8 @@ cudaError_t launch_attn4_d128(const AttnParams& p, const Kv4Blocks& kb, const At
                               int* grid, int sms, cudaStream_t s);
 cudaError_t launch_attn4_d256(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps, int nt,
                               int* grid, int sms, cudaStream_t s);
+cudaError_t launch_attn4_tc(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps, int D, int rows,
+                            int* grid, int sms, cudaStream_t s);
 // The join of an attention call's partials (attn.cu).
 cudaError_t launch_attn_join(const AttnParams& p, int D, int rows, int grid, int tk, int sms,
                              cudaStream_t s);

@@ -48,6 +48,17 @@ def test_shapes(R, Hq, Hkv, D):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("R,G", [(16, 2), (3, 11), (16, 4), (5, 13), (16, 8), (3, 43), (1, 129),
+                                 (10, 13), (4, 33), (3, 48), (2, 200)])
+def test_numbers_of_rows(R, G, D):
+    """32 and 33, 64 and 65, 128 and 129 rows of a key head, and cuts of more into blocks by
+    verify indexes and by heads; beside full tiles, with a window that ends inside some."""
+    Hkv = 2 if G <= 128 else 1
+    run_case(40 + R, [R, 150, 600, 1111], R, Hkv * G, Hkv, D, 16)
+    run_case(41 + R, [333, 901], R, G, 1, D, 8, window=200, sinks=17)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("order", ["nhd", "hnd"])
 @pytest.mark.parametrize("page", [8, 32, 128, 512])
 def test_pages(page, order, D):
