@@ -8,11 +8,15 @@ library follow one another in a step.
     verify_gemm_w4_blockmax(x)        -> logits of the LM head and their block maxima
     process_logits(logits)            -> penalties, biases and the grammar's mask
     accept_rejection_blockmax(logits) -> committed tokens
+    token_logprobs(logits, tokens)    -> their log probabilities, and the best alternatives
+    advance_pages(accepted)           -> lengths, and pages for the next step's rows
 
 A step verifies the token committed last and Kd drafts of every sequence: R = Kd
 + 1 rows at the end of the cache.  Rejected drafts leave their keys and values
 behind the new length, where the next step's rows overwrite them.  The drafts
 come from a table of logits by the token before (a stand-in for a draft model).
+Pages come from one pool, as the sequences grow; the caches hold bf16, e4m3 or
+(kv="nvfp4") 4 bits a value.
 
 Run it on a GPU:  python examples/verify_step.py
 """
@@ -58,13 +62,24 @@ class VerifyLoop:
         self.draft_table = torch.randn(V, V, device="cuda", generator=g)
         self.inv_freq = 1e4 ** (-torch.arange(0, D, 2, dtype=torch.float64, device="cuda") / D)
         self.head_norm = torch.ones(D, device="cuda")
-        # every sequence owns its pages; the table maps positions to them in any order
+        # the pages of one pool, in any order, go to the sequences as they grow
         cols = -(-max_len // page)
-        table = torch.randperm(B * cols, device="cuda", generator=g).to(torch.int32).view(B, cols)
-        scale = torch.full((Hkv,), 1 / 32, device="cuda") if kv == torch.float8_e4m3fn else None
-        self.caches = [vw4.KVCache(torch.zeros(B * cols, page, Hkv, D, device="cuda").to(kv),
-                                   torch.zeros(B * cols, page, Hkv, D, device="cuda").to(kv),
-                                   table, scale, scale) for _ in range(layers)]
+        self.page, pages = page, B * cols
+        self.free = torch.randperm(pages, device="cuda", generator=g).to(torch.int32)
+        self.free_count = torch.full((1,), pages, dtype=torch.int32, device="cuda")
+        self.table = torch.full((B, cols), -1, dtype=torch.int32, device="cuda")
+        self.held = torch.zeros(B, dtype=torch.int32, device="cuda")
+        if kv == "nvfp4":
+            scale = torch.full((Hkv,), 1 / 64, device="cuda")
+            self.caches = [vw4.KVCache4(
+                *(torch.zeros(pages, page, Hkv, D // 2, dtype=torch.uint8, device="cuda") for _ in range(2)),
+                *(torch.zeros(pages, Hkv, page, D // 16, device="cuda").to(torch.float8_e4m3fn)
+                  for _ in range(2)), self.table, scale, scale) for _ in range(layers)]
+        else:
+            scale = torch.full((Hkv,), 1 / 32, device="cuda") if kv == torch.float8_e4m3fn else None
+            self.caches = [vw4.KVCache(torch.zeros(pages, page, Hkv, D, device="cuda").to(kv),
+                                       torch.zeros(pages, page, Hkv, D, device="cuda").to(kv),
+                                       self.table, scale, scale) for _ in range(layers)]
         # all tokens so far: the prompt, then what was committed
         self.history = torch.zeros((B, max_len), dtype=torch.int32, device="cuda")
         self.length = torch.tensor([len(p) for p in prompts], dtype=torch.int32, device="cuda")
@@ -83,10 +98,22 @@ class VerifyLoop:
             self.mask = (words - ((words >> 31) << 32)).to(torch.int32).view(1, -1).cuda()
             self.mask_row = torch.zeros((B, self.R), dtype=torch.int32, device="cuda")
         self.steps = 0
+        self.logprobs = None  # of the last step's tokens
         # the prompts, but for their last tokens, which the first step verifies
+        self.cached = torch.zeros(B, dtype=torch.int32, device="cuda")
+        self.seq_lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        self.advance(grow=self.length + self.Kd)
         for i in range(0, int(self.length.max()) - 1):
             n = torch.minimum(self.length - 1, torch.tensor(i + 1, device="cuda")).to(torch.int32)
             self.layers(self.history.gather(1, (n - 1).clamp(min=0).long()[:, None]), n)
+
+        self.cached.copy_(self.length - 1)
+
+    def advance(self, accepted=None, grow=None):
+        """Lengths of the caches after accepted more tokens, pages for R (or grow) more rows."""
+        vw4.advance_pages(self.table, self.page, self.cached, self.held, self.free, self.free_count,
+                          R=self.R, accepted=accepted, grow=grow, lens_out=self.cached,
+                          held_out=self.held, free_count_out=self.free_count, seq_lens=self.seq_lens)
 
     def layers(self, tokens, seq_lens):
         """The rows of tokens [B, R] at the end of caches of seq_lens tokens -> [B * R, hidden]."""
@@ -117,7 +144,7 @@ class VerifyLoop:
         B, R, V = self.B, self.R, self.V
         last = self.history.gather(1, self.length.long()[:, None] - 1)
         rows = torch.cat([last, drafts], 1)
-        x = self.layers(rows, self.length + self.Kd)
+        x = self.layers(rows, self.seq_lens)
         logits, bmax = vw4.verify_gemm_w4_blockmax(*self.head.args, rms_norm(x))
         logits, bmax = logits.view(B, R, V), bmax.view(B, R, -1)
         vw4.process_logits(logits, drafts, history=self.history, hist_len=self.length,
@@ -128,7 +155,12 @@ class VerifyLoop:
 
     def step(self):
         """-> tokens [B, Kd + 1] and how many of them are committed [B]."""
-        drafts, draft_logits = self.draft()
+        out = self.commit(*self.draft())
+        self.steps += 1
+        return out
+
+    def commit(self, drafts, draft_logits):
+        """The step after its drafts, all of it on the device and in place: it can be captured."""
         logits, bmax = self.verify(drafts)
         draft_bmax = None
         if self.Kd:  # the draft's logits as they are; the call fills in their block maxima
@@ -138,21 +170,23 @@ class VerifyLoop:
         tokens, n = vw4.accept_rejection_blockmax(logits, bmax, draft_logits, draft_bmax, drafts,
                                                   temperature=1.0, top_p=1.0, seed=7,
                                                   offset=self.steps)
+        self.logprobs = vw4.token_logprobs(logits, tokens, length=n, top=4)
         at = self.length.long()[:, None] + torch.arange(self.R, device="cuda")
         keep = torch.arange(self.R, device="cuda") < n[:, None]
         old = self.history.gather(1, at)
         self.history.scatter_(1, at, torch.where(keep, tokens, old))
-        self.length = self.length + n
-        self.steps += 1
+        self.length += n
+        self.advance(accepted=n)
         return tokens, n
 
 
 def main():
-    loop = VerifyLoop([[5, 17, 300, 42], [9, 9, 1234]], kv=torch.float8_e4m3fn,
+    loop = VerifyLoop([[5, 17, 300, 42], [9, 9, 1234]], kv="nvfp4",
                       allowed=torch.arange(0, 4000, 2))
     for _ in range(8):
         tokens, n = loop.step()
-        print("committed", [tokens[b, :n[b]].tolist() for b in range(loop.B)])
+        print("committed", [tokens[b, :n[b]].tolist() for b in range(loop.B)], "of log probability",
+              [[round(x, 2) for x in loop.logprobs.logprob[b, :n[b]].tolist()] for b in range(loop.B)])
     if vw4.vw4_get_device_status():
         raise SystemExit("the device reported an error")
 
