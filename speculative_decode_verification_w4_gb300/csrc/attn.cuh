@@ -63,9 +63,15 @@ __host__ __device__ inline AttnSeq attn_seq(int len_raw, int cap, int R, int win
 __host__ __device__ inline int attn_ctas(long long T, int grid) {
     return T < grid ? static_cast<int>(T) : grid;
 }
-__host__ __device__ inline long long attn_unit(long long T, int G, int i) { return T * i / G; }
+__host__ __device__ inline bool attn_short(long long T) {  // T (G + 1) in 32 bits: short divisions
+    return T < (1ll << 32) / (kAttnMaxGrid64 + 1);
+}
+__host__ __device__ inline long long attn_unit(long long T, int G, int i) {
+    if (attn_short(T)) return static_cast<uint32_t>(T) * static_cast<uint32_t>(i) / static_cast<uint32_t>(G);
+    return T * i / G;
+}
 __host__ __device__ inline int attn_owner(long long T, int G, long long u) {
-    if (T < (1ll << 32) / (kAttnMaxGrid64 + 1))  // (T (G + 1) in 32 bits: a short division)
+    if (attn_short(T))
         return static_cast<int>((static_cast<uint32_t>(u + 1) * static_cast<uint32_t>(G) +
                                  static_cast<uint32_t>(T) - 1u) / static_cast<uint32_t>(T)) - 1;
     return static_cast<int>(((u + 1) * G + T - 1) / T - 1);
@@ -335,7 +341,7 @@ struct AttnWalk {
         boxes = TK / box_rows;
         enter(p, lane);
         const long long r = w.u0 - w.base;
-        g = static_cast<int>(r / s.nt);
+        g = r < (1ll << 31) ? static_cast<int>(r) / s.nt : static_cast<int>(r / s.nt);
         t = static_cast<int>(r - static_cast<long long>(g) * s.nt);
         fetch(p, lane);
     }

@@ -4,11 +4,11 @@
 namespace vw4 {
 
 // The 5th-generation tensor cores take their time from the softmax's latency, not from the
-// rows: from 33 rows on they are ahead at every head size and length, up to 32 behind
-// or even (16 / 32 / 40 / 64 rows, us, mma.sync against tcgen05: 32 sequences of up to
-// 32768 tokens, head size 128, 4 key heads 75 / 106 / 177 / 262 against 111 / 114 / 115 /
-// 121; head size 256 135 / 198 / 280 / 426 against 184 / 194 / 200 / 210; windows of 1024,
-// 64 sequences, head size 128, 16 / 32 / 64 rows 30 / 44 / 87 against 49 / 53 / 62).
+// rows: from 33 rows on they are ahead at every head size and length, up to 32 behind or
+// even (16 / 32 / 40 / 64 rows, us, mma.sync against tcgen05: 32 sequences of up to 32768
+// tokens, 4 key heads of size 128 75 / 106 / 177 / 262 against 109 / 112 / 112 / 117; of size
+// 256 135 / 198 / 280 / 426 against 176 / 181 / 182 / 192; 64 windows of 1024, head size 128,
+// 24 / 32 / 64 rows 37 / 44 / 87 against 53 / 54 / 57).
 constexpr int kAttn4TcFrom = 33;
 
 constexpr int kAttn4MaxGrid = kAttnMaxGrid64;  // (three blocks an SM at most)

@@ -14,11 +14,16 @@
 // chain of latencies of about 1 us under the load of the other warps (16384 keys' and as many
 // values' elements; their conversion takes 0.5 us beside it, the products 0.5, the bytes from
 // HBM 0.4).  Without conversions and exponentials a tile still takes 1.1 us of its 1.4.  So
-// the time hardly grows with the rows: 32 sequences of up to 32768 tokens, 8 key heads of
-// size 128, are 220 us at 48 rows, 235 at 64 and 310 at 128, of 424 MB.  Tried and slower:
-// weights formed at once against the lagging reference (252 at 64 rows), the rows' copies in
-// the other lanes so that every sub-core has softmax warps (332), keys as the rows of the
-// instructions and eight warps of weights through shared memory (541).
+// the time hardly grows with the rows: 32 sequences of up to 32768 tokens, 4 key heads of
+// size 128 (219 MB), are 112 us at 36 rows, 117 at 64 and 150 at 128; head size 256 182 / 192 /
+// 260.  Tried and slower: weights formed at once against the lagging reference (252 us
+// against 235 at 64 rows of 8 heads), the rows' copies in the other lanes so that every
+// sub-core has softmax warps (332), keys as the rows of the instructions and eight warps of
+// weights through shared memory (541).
+//
+// What happens once a part of an item, its queries and its rows, is code that no instruction
+// cache holds yet: divisions once a row, rows handed on by shuffles and maxima of pairs took
+// 8 rows of 6 heads of 4 sequences from 33 to 28.5 us, windows of 1024 from 92 to 70.
 //
 // The reference of the weights follows the running maximum lazily, as in attn4.cuh.
 #pragma once
@@ -46,7 +51,8 @@ struct Attn4TcShape {
     static constexpr int kOffV = kNF * kF;
     static constexpr int kOffRawK = 2 * kNF * kF;
     static constexpr int kOffRawV = kOffRawK + kNR * kRaw;
-    static constexpr int kUsed = kOffRawV + kNR * kRaw + 1024;
+    static constexpr int kOffX = kOffRawV + kNR * kRaw;  // 4 KB a softmax warp
+    static constexpr int kUsed = kOffX + 4 * 4096 + 1024;
     static constexpr int kSmem = kUsed < 115 * 1024 ? 115 * 1024 : kUsed;  // one CTA an SM
     static_assert(kSmem <= 221 * 1024, "shared memory");
     static_assert(kRaw % (8 * kKB) == 0 && kF % 1024 == 0, "alignment");
@@ -66,24 +72,336 @@ struct Attn4TcShape {
 };
 constexpr int kTc4Mma = 6, kTc4K = 8, kTc4V = 12;  // first warps of the roles
 
+__device__ __forceinline__ void tmem_ld16(uint32_t* r, uint32_t a) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+          "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+          "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a)
+        : "memory");
+}
+
+struct Attn4TcRow {
+    float c2, vs;
+    int at;  // verify index << 16 | head (dead: -1)
+};
+
+// What the warps of a CTA share beside the tiles.
+template <int D, int ROWS>
+struct Attn4TcShared {
+    using S = Attn4TcShape<D, ROWS>;
+    static constexpr int NR = S::kNR, NF = S::kNF, H = S::kHalves;
+    uint32_t s_tmem;
+    volatile int s_abort;
+    volatile int s_odd[8];            // seg + 1: the part's values lost NaN
+    AttnUnit s_unit[kUnitRing], s_vunit[kUnitRing], s_part[16];
+    float s_mx[2][2][H > 1 ? ROWS : 1];  // of a tile's columns, for the other half
+    Attn4TcRow s_row[2][H][ROWS];        // of a part, by seg & 1: each thread its own
+    float s_sum[H > 1 ? ROWS : 1];       // of a part's weights
+    uint32_t s_top[2][H > 1 ? ROWS : 1]; // of the queries' halves: largest magnitudes
+    uint64_t b_rk[NR], b_rke[NR], b_rv[NR], b_rve[NR];
+    uint64_t b_k[NF], b_ke[NF], b_v[NF], b_ve[NF];
+    uint64_t b_s[2], b_p[2], b_pv[2], b_q[2], b_qe[2], b_part[16], b_o, b_end;
+    uint64_t b_x[2][4];     // s_mx of a half's warp is there
+    uint64_t b_l[4], b_t[4];  // s_sum and s_top of a half's warp are there
+};
+
+struct Attn4TcWarp {
+    int half, rw, r, lane;
+    uint32_t tmem;
+    uint8_t* stage;  // 16 bytes of 32 rows of 128: eight lanes take a row, or a lane its own
+};
+
+// (the same answer in every lane: what follows is executed by whole warps)
+template <class Shared>
+__device__ __forceinline__ bool attn4_tc_wait(const AttnParams& p, Shared& sh, uint64_t* bar, int phase) {
+    bool ok = mbar_wait_bounded(bar, phase & 1, p.wait_ns, &sh.s_abort);
+    if (!ok) {
+        sh.s_abort = 1;
+        atomicOr(p.status, kStatusWaitTimeout);
+    }
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+
+// An item's queries into tensor memory: f16 under a power of two per row that puts its
+// largest magnitude into [2^14, 2^15), with the sign of the head's scale.  Eight lanes
+// read 64 dimensions of a row.  The halves take every other 64, all read at once, and
+// exchange their magnitudes; a thread of a whole row reads it twice.
+template <int D, int ROWS>
+__device__ __forceinline__ bool attn4_tc_queries(const AttnParams& p, Attn4TcShared<D, ROWS>& sh, const Attn4TcWarp& w,
+                                              int seg) {
+    using S = Attn4TcShape<D, ROWS>;
+    constexpr int NQ = S::kNQ, H = S::kHalves;
+    const int half = w.half, rw = w.rw, r = w.r, lane = w.lane;
+    const uint32_t lanes = static_cast<uint32_t>(rw * 32) << 16, tmem = w.tmem;
+    auto& s_part = sh.s_part;
+    auto& s_row = sh.s_row;
+    auto& s_top = sh.s_top;
+    auto& b_q = sh.b_q;
+    auto& b_qe = sh.b_qe;
+    auto& b_part = sh.b_part;
+    auto& b_t = sh.b_t;
+    uint4* stage = reinterpret_cast<uint4*>(w.stage);
+    auto x_at = [](int row, int chunk) { return row * 8 + (chunk ^ (row & 7)); };
+    auto warp_wait = [&](uint64_t* bar, int phase) { return attn4_tc_wait(p, sh, bar, phase); };
+    if (!warp_wait(&b_part[seg & 15], seg >> 4)) return false;
+    const AttnUnit d = s_part[seg & 15];
+    const int h = d.g / p.row_blocks;
+    const float ks = p.k_scale ? __ldg(p.k_scale + h) : 1.f;
+    const float vs = p.v_scale ? __ldg(p.v_scale + h) : 1.f;
+    const AttnRow own = attn_row(p, d.g, r);
+    const int at = own.live ? own.i << 16 | own.hq : -1;
+    const uint4* src[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int a = __shfl_sync(0xffffffffu, at, 4 * j + (lane >> 3));
+        src[j] = a >= 0 ? reinterpret_cast<const uint4*>(
+                              p.q + (static_cast<long long>(d.b) * p.R + (a >> 16)) * p.ldq +
+                              static_cast<long long>(a & 0xffff) * D) + (lane & 7)
+                        : nullptr;
+    }
+    auto read = [&](uint4* v, int c) {  // 64 dimensions
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = src[j] ? __ldg(src[j] + c * 8) : make_uint4(0, 0, 0, 0);
+    };
+    constexpr int NC = (D / 64 + H - 1) / H;  // of a half
+    uint4 all[H > 1 ? NC : 1][8];
+    uint32_t mx[8] = {};
+    auto largest = [&](const uint4* v) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[j] = __vmaxu2(mx[j], w[e] & 0x7fff7fffu);
+        }
+    };
+    if constexpr (H > 1) {
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+            if (half + k * H < D / 64) read(all[k], half + k * H);
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+            if (half + k * H < D / 64) largest(all[k]);
+    } else {
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+            read(all[0], c);
+            largest(all[0]);
+        }
+    }
+    uint32_t top = 0;  // of the lane's own row
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int s = 4; s > 0; s >>= 1) mx[j] = __vmaxu2(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], s));
+        const uint32_t t = __shfl_sync(0xffffffffu, mx[j], (lane & 3) * 8);
+        if (lane >> 2 == j) top = t;
+    }
+    if constexpr (H > 1) {
+        s_top[half][r] = top;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_t[half * 2 + rw]);
+        if (!warp_wait(&b_t[(half ^ 1) * 2 + rw], seg)) return false;
+        top = __vmaxu2(top, s_top[half ^ 1][r]);
+    }
+    top = max(top & 0xffffu, top >> 16);
+    const int ex = static_cast<int>(top >> 7);
+    int shift = ex == 0 || ex == 255 ? 0 : 127 + 14 - ex;
+    shift = max(-126, min(126, shift));
+    const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + shift) << 23), ks);
+    float c = p.scale * kLog2e * fabsf(ks) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+    if (c < kMinFactor) c = kMinFactor;  // (NaN stays)
+    s_row[seg & 1][half][r] = {c, vs, at};
+    if (seg >= NQ && !warp_wait(&b_qe[seg % NQ], seg / NQ - 1)) return false;
+    tc_fence_after();
+    const uint32_t tq = tmem + lanes + S::kColQ + seg % NQ * (D / 2);
+    auto bring = [&](const uint4* v, int c) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) stage[x_at(4 * j + (lane >> 3), lane & 7)] = v[j];
+        __syncwarp();
+        uint32_t y[32];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint4 x = stage[x_at(lane, k)];
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y[4 * k + e] = pack2<true>(__uint_as_float(w[e] << 16) * up,
+                                           __uint_as_float(w[e] & 0xffff0000u) * up);
+        }
+        tmem_st32(tq + c * 32, y);
+    };
+    if constexpr (H > 1) {
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+            if (half + k * H < D / 64) bring(all[k], half + k * H);
+    } else {
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+            read(all[0], c);
+            bring(all[0], c);
+        }
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b_q[seg % NQ]);
+    return true;
+}
+
+// A part's rows from tensor memory to the output, or to its partial.
+template <int D, int ROWS>
+__device__ __forceinline__ bool attn4_tc_finish(const AttnParams& p, const Kv4Blocks& kb, Attn4TcShared<D, ROWS>& sh,
+                                             const Attn4TcWarp& w, const AttnUnit& td, int u, int seg_start,
+                                             int pr, bool live, float m, float l, float c2) {
+    using S = Attn4TcShape<D, ROWS>;
+    constexpr int H = S::kHalves, NB = S::kNB, TK = S::kTK;
+    const int half = w.half, rw = w.rw, r = w.r, lane = w.lane;
+    const uint32_t tO = w.tmem + (static_cast<uint32_t>(rw * 32) << 16);
+    auto& s_odd = sh.s_odd;
+    auto& s_row = sh.s_row;
+    auto& s_sum = sh.s_sum;
+    auto& b_pv = sh.b_pv;
+    auto& b_o = sh.b_o;
+    auto& b_l = sh.b_l;
+    uint4* stage = reinterpret_cast<uint4*>(w.stage);
+    auto x_at = [](int row, int chunk) { return row * 8 + (chunk ^ (row & 7)); };
+    auto warp_wait = [&](uint64_t* bar, int phase) { return attn4_tc_wait(p, sh, bar, phase); };
+    const float vs = s_row[td.seg & 1][half][r].vs;
+    const int row_at = s_row[td.seg & 1][half][r].at;
+    if constexpr (H > 1) {
+        // the sums of both halves
+        if (half == 1) {
+            s_sum[r] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b_l[2 + rw]);
+        }
+        if (!warp_wait(&b_l[half ? rw : 2 + rw], td.seg)) return false;
+        if (half == 0) {
+            l += s_sum[r];
+            s_sum[r] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b_l[rw]);
+        } else {
+            l = s_sum[r];
+        }
+    }
+    if (!warp_wait(&b_pv[u & 1], u >> 1)) return false;
+    tc_fence_after();
+    const int h = td.g / p.row_blocks;
+    const float M = m == -INFINITY ? -INFINITY : m * c2 - kTail4;
+    const float f = l == 0.f ? 0.f : vs / l;
+    uint32_t nan = 0;  // blocks of 16 dimensions that a NaN reached
+    if (s_odd[td.seg & 7] == td.seg + 1 && live) {
+        auto look = [&](int j0, int j1) {
+            for (int j = max(j0, seg_start); j <= min(j1, td.start + TK - 1); ++j) {
+                const int pg = p.table[static_cast<long long>(td.b) * p.table_stride + (j >> p.page_shift)];
+                if (pg < 0 || pg >= p.num_pages || !key_seen(j, pr, p.window, p.sinks)) continue;
+                const uint8_t* s = kb.v + pg * kb.page_stride + h * kb.head_stride +
+                                   static_cast<long long>(j & (p.page_size - 1)) * NB;
+                for (int k = 0; k < NB; ++k)
+                    if ((s[k] & 0x7fu) == 0x7fu) nan |= 1u << k;
+            }
+        };
+        // the ends of the rows' windows, then the verify rows themselves
+        if (p.window > 0) look(max(0, td.p0 - p.window + 1), min(td.p0, td.len - 1 - p.window));
+        look(max(0, td.p0 + 1), td.len - 1);
+    }
+    int at[8];  // verify index << 16 | head of the rows that this lane writes (dead: -1)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) at[j] = __shfl_sync(0xffffffffu, row_at, 4 * j + (lane >> 3));
+    float* po = p.partial + static_cast<long long>(td.slot < 0 ? 0 : td.slot) * ROWS * (D + 2);
+    __syncwarp();
+#pragma unroll 1
+    for (int c = half * (D / H); c < (half + 1) * (D / H); c += 32) {
+        uint32_t y[32];
+        tmem_ld32(y, tO + c);
+        if (nan & (3u << (c / 16))) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                if ((nan >> (c / 16 + k / 16)) & 1u) y[k] = 0x7fffffffu;
+        }
+        // through shared memory, so that eight lanes write a row's 32 columns
+        const float to = td.slot >= 0 ? 1.f : f;
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            stage[x_at(lane, k)] = make_uint4(__float_as_uint(__uint_as_float(y[4 * k]) * to),
+                                              __float_as_uint(__uint_as_float(y[4 * k + 1]) * to),
+                                              __float_as_uint(__uint_as_float(y[4 * k + 2]) * to),
+                                              __float_as_uint(__uint_as_float(y[4 * k + 3]) * to));
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int q = 4 * j + (lane >> 3), col = c + (lane & 7) * 4;
+            const uint4 x = stage[x_at(q, lane & 7)];
+            if (at[j] < 0) {
+            } else if (td.slot >= 0) {
+                *reinterpret_cast<uint4*>(po + (rw * 32 + q) * D + col) = x;
+            } else {
+                *reinterpret_cast<uint2*>(
+                    p.out + (static_cast<long long>(td.b) * p.R + (at[j] >> 16)) * p.ldo +
+                    static_cast<long long>(at[j] & 0xffff) * D + col) =
+                    make_uint2(pack2<false>(__uint_as_float(x.x), __uint_as_float(x.y)),
+                               pack2<false>(__uint_as_float(x.z), __uint_as_float(x.w)));
+            }
+        }
+    }
+    if (live && half == 0) {
+        if (td.slot >= 0) {
+            po[ROWS * D + r] = M;
+            po[ROWS * (D + 1) + r] = l;
+        } else if (p.lse) {
+            p.lse[(static_cast<long long>(td.b) * p.R + (row_at >> 16)) * p.Hq + (row_at & 0xffff)] =
+                l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b_o);
+    return true;
+}
+
 template <int D, int ROWS>
 __global__ void __launch_bounds__(Attn4TcShape<D, ROWS>::kThreads, 1)
-    attn4_tc_kernel(const AttnParams p, const Kv4Blocks kb, const __grid_constant__ AttnMaps maps) {
+    attn4_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ Kv4Blocks kb,
+                    const __grid_constant__ AttnMaps maps) {
     using S = Attn4TcShape<D, ROWS>;
     constexpr int TK = S::kTK, NR = S::kNR, NF = S::kNF, NQ = S::kNQ, H = S::kHalves, NB = S::kNB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_abort;
-    __shared__ volatile int s_odd[8];            // seg + 1: the part's values lost NaN
-    __shared__ AttnUnit s_unit[kUnitRing], s_vunit[kUnitRing], s_part[16];
-    __shared__ float s_mx[2][2][H > 1 ? ROWS : 1];  // of a tile's columns, for the other half
-    __shared__ float s_sum[H > 1 ? ROWS : 1];       // of a part's weights
-    __shared__ __align__(8) uint64_t b_rk[NR], b_rke[NR], b_rv[NR], b_rve[NR];
-    __shared__ __align__(8) uint64_t b_k[NF], b_ke[NF], b_v[NF], b_ve[NF];
-    __shared__ __align__(8) uint64_t b_s[2], b_p[2], b_pv[2], b_q[2], b_qe[2], b_part[16], b_o, b_end;
-    __shared__ __align__(8) uint64_t b_x[2][4];     // s_mx of a half's warp is there
-    __shared__ __align__(8) uint64_t b_l[4];        // s_sum of the other half's warp is there
+    __shared__ Attn4TcShared<D, ROWS> sh;
+    auto& s_tmem = sh.s_tmem;
+    auto& s_abort = sh.s_abort;
+    auto& s_odd = sh.s_odd;
+    auto& s_unit = sh.s_unit;
+    auto& s_vunit = sh.s_vunit;
+    auto& s_part = sh.s_part;
+    auto& s_mx = sh.s_mx;
+    auto& s_row = sh.s_row;
+    auto& b_rk = sh.b_rk;
+    auto& b_rke = sh.b_rke;
+    auto& b_rv = sh.b_rv;
+    auto& b_rve = sh.b_rve;
+    auto& b_k = sh.b_k;
+    auto& b_ke = sh.b_ke;
+    auto& b_v = sh.b_v;
+    auto& b_ve = sh.b_ve;
+    auto& b_s = sh.b_s;
+    auto& b_p = sh.b_p;
+    auto& b_pv = sh.b_pv;
+    auto& b_q = sh.b_q;
+    auto& b_qe = sh.b_qe;
+    auto& b_part = sh.b_part;
+    auto& b_o = sh.b_o;
+    auto& b_end = sh.b_end;
+    auto& b_x = sh.b_x;
+    auto& b_l = sh.b_l;
+    auto& b_t = sh.b_t;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row_warps = (p.tb * p.gb + 31) / 32;
 
@@ -116,7 +434,10 @@ __global__ void __launch_bounds__(Attn4TcShape<D, ROWS>::kThreads, 1)
                 for (int j = 0; j < 4; ++j) mbar_init(&b_x[k][j], 1);
             }
             for (int k = 0; k < 16; ++k) mbar_init(&b_part[k], 1);
-            for (int k = 0; k < 4; ++k) mbar_init(&b_l[k], 1);
+            for (int k = 0; k < 4; ++k) {
+                mbar_init(&b_l[k], 1);
+                mbar_init(&b_t[k], 1);
+            }
             mbar_init(&b_o, H * row_warps);
             mbar_init(&b_end, 1);
             fence_barrier_init();
@@ -137,10 +458,7 @@ __global__ void __launch_bounds__(Attn4TcShape<D, ROWS>::kThreads, 1)
         atomicOr(p.status, kStatusWaitTimeout);
         return false;
     };
-    // (the same answer in every lane: what follows is executed by whole warps)
-    auto warp_wait = [&](uint64_t* bar, int phase) {
-        return __all_sync(0xffffffffu, wait(bar, phase)) != 0;
-    };
+    auto warp_wait = [&](uint64_t* bar, int phase) { return attn4_tc_wait(p, sh, bar, phase); };
 
     if (n_units > 0 && (warp == S::kLoadK || warp == S::kLoadV)) {
         // -------------------------------------------------------- loading warps
@@ -315,269 +633,132 @@ __global__ void __launch_bounds__(Attn4TcShape<D, ROWS>::kThreads, 1)
         const int r = rw * 32 + lane;  // row of the block = lane of tensor memory
         const uint32_t lanes = static_cast<uint32_t>(rw * 32) << 16;
         const uint32_t tO = tmem + lanes;
-        float m = -INFINITY, l = 0.f, c2 = 1.f, c2_next = 1.f;
-        AttnRow row{}, row_next{};
+        float m = -INFINITY, l = 0.f, c2 = 1.f;
+        bool live = false;
         int pr = -1, seg_start = 0;
 
-        // An item's queries into tensor memory: f16 under a power of two per row that puts its
-        // largest magnitude into [2^14, 2^15), with the sign of the head's scale.  A half of
-        // a row's threads reads all of it and brings its half.
-        auto queries = [&](int seg) {
-            if (!warp_wait(&b_part[seg & 15], seg >> 4)) return false;
-            const AttnUnit d = s_part[seg & 15];
-            const int h = d.g / p.row_blocks;
-            const float ks = p.k_scale ? __ldg(p.k_scale + h) : 1.f;
-            row_next = attn_row(p, d.g, r);
-            const uint4* src = reinterpret_cast<const uint4*>(
-                p.q + (static_cast<long long>(d.b) * p.R + row_next.i) * p.ldq +
-                static_cast<long long>(row_next.hq) * D);
-            uint32_t mx = 0;
-#pragma unroll 1
-            for (int c = 0; c < D / 8; c += 8) {
-                uint4 v[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = row_next.live ? __ldg(src + c + k) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mx = max(mx, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        const Attn4TcWarp w{half, rw, r, lane, tmem, smem + S::kOffX + (half * (4 / H) + rw) * 4096};
+        bool ok = true;
+        AttnUnit td{};
+        for (int u = -1; ok;) {
+            // ---- between parts: the next one's queries first, for its scores wait for them,
+            // not for these rows
+            if (u + 1 < n_units) ok = attn4_tc_queries<D, ROWS>(p, sh, w, u < 0 ? 0 : td.seg + 1);
+            if (ok && u >= 0)
+                ok = attn4_tc_finish<D, ROWS>(p, kb, sh, w, td, u, seg_start, pr, live, m, l, c2);
+            if (!ok || u + 1 >= n_units) break;
+            do {
+                ++u;
+                ok = warp_wait(&b_s[u & 1], u >> 1);
+                if (!ok) break;
+                tc_fence_after();
+                td = s_unit[u % kUnitRing];
+                const bool first = td.flags & kUnitFirst, edge = td.flags & kUnitEdge;
+                if (first) {
+                    seg_start = td.start;
+                    const Attn4TcRow& a = s_row[td.seg & 1][half][r];
+                    c2 = a.c2;
+                    live = a.at >= 0;
+                    pr = live ? td.p0 + (a.at >> 16) : -1;
+                    l = 0.f;
                 }
-            }
-            const int ex = static_cast<int>(mx >> 7);
-            int sh = ex == 0 || ex == 255 ? 0 : 127 + 14 - ex;
-            sh = max(-126, min(126, sh));
-            const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), ks);
-            c2_next = p.scale * kLog2e * fabsf(ks) * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-            if (c2_next < kMinFactor) c2_next = kMinFactor;  // (NaN stays)
-            if (seg >= NQ && !warp_wait(&b_qe[seg % NQ], seg / NQ - 1)) return false;
-            tc_fence_after();
-            __syncwarp();
-            const uint32_t tq = tmem + lanes + S::kColQ + seg % NQ * (D / 2);
-#pragma unroll 1
-            for (int c = half * (D / 8 / H); c < (half + 1) * (D / 8 / H); c += 4) {  // 32 dimensions
-                uint32_t y[16];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint4 v = row_next.live ? __ldg(src + c + k) : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        y[4 * k + e] = pack2<true>(__uint_as_float(w[e] << 16) * up,
-                                                   __uint_as_float(w[e] & 0xffff0000u) * up);
-                }
-                __syncwarp();
-                tmem_st16(tq + c * 4, y);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&b_q[seg % NQ]);
-            return true;
-        };
-
-        // A part's rows from tensor memory to the output, or to its partial.
-        auto finish = [&](const AttnUnit& td, int u) {
-            if constexpr (H > 1) {
-                // the sums of both halves
-                if (half == 1) {
-                    s_sum[r] = l;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&b_l[2 + rw]);
-                }
-                if (!warp_wait(&b_l[half ? rw : 2 + rw], td.seg)) return false;
-                if (half == 0) {
-                    l += s_sum[r];
-                    s_sum[r] = l;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&b_l[rw]);
-                } else {
-                    l = s_sum[r];
-                }
-            }
-            if (!warp_wait(&b_pv[u & 1], u >> 1)) return false;
-            tc_fence_after();
-            const int h = td.g / p.row_blocks;
-            const float M = m == -INFINITY ? -INFINITY : m * c2 - kTail4;
-            const float vs = p.v_scale ? __ldg(p.v_scale + h) : 1.f;
-            const float f = l == 0.f ? 0.f : vs / l;
-            uint32_t nan = 0;  // blocks of 16 dimensions that a NaN reached
-            if (s_odd[td.seg & 7] == td.seg + 1 && row.live) {
-                auto look = [&](int j0, int j1) {
-                    for (int j = max(j0, seg_start); j <= min(j1, td.start + TK - 1); ++j) {
-                        const int pg = p.table[static_cast<long long>(td.b) * p.table_stride + (j >> p.page_shift)];
-                        if (pg < 0 || pg >= p.num_pages || !key_seen(j, pr, p.window, p.sinks)) continue;
-                        const uint8_t* s = kb.v + pg * kb.page_stride + h * kb.head_stride +
-                                           static_cast<long long>(j & (p.page_size - 1)) * NB;
-                        for (int k = 0; k < NB; ++k)
-                            if ((s[k] & 0x7fu) == 0x7fu) nan |= 1u << k;
-                    }
-                };
-                // the ends of the rows' windows, then the verify rows themselves
-                if (p.window > 0) look(max(0, td.p0 - p.window + 1), min(td.p0, td.len - 1 - p.window));
-                look(max(0, td.p0 + 1), td.len - 1);
-            }
-            const long long orow = static_cast<long long>(td.b) * p.R + row.i;
-            __nv_bfloat16* out = p.out + orow * p.ldo + static_cast<long long>(row.hq) * D;
-            float* po = p.partial + static_cast<long long>(td.slot < 0 ? 0 : td.slot) * ROWS * (D + 2);
-            __syncwarp();
-#pragma unroll 1
-            for (int c = half * (D / H); c < (half + 1) * (D / H); c += 32) {
-                uint32_t y[32];
-                tmem_ld32(y, tO + c);
-                if (nan & (3u << (c / 16))) {
+                const uint32_t tS = tmem + lanes + S::kColS + (u & 1) * TK;
+                // seen: k <= hi and (k > lo or k < sk), as bits of the 32 columns from column c
+                auto mask = [&](uint32_t* x, int c) {
+                    const int hi = pr - td.start - c;
+                    auto below = [](int n) {  // bits 0 .. n - 1
+                        return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
+                    };
+                    uint32_t seen = below(hi + 1);
+                    if (p.window > 0) seen &= ~below(hi - p.window + 1) | below(p.sinks - td.start - c);
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        if ((nan >> (c / 16 + k / 16)) & 1u) y[k] = 0x7fffffffu;
+                        if (!((seen >> k) & 1u)) x[k] = 0xff800000u;
+                };
+                // half a row is read once, a whole one twice, 32 columns at a time
+                constexpr int CW = H > 1 ? TK / H : 32;
+                uint32_t x[CW];
+                auto columns = [&](int c) {
+                    if constexpr (CW == 64) tmem_ld64(x, tS + c);
+                    else tmem_ld32(x, tS + c);
+                    if (edge) {
+#pragma unroll
+                        for (int k = 0; k < CW; k += 32) mask(x + k, c + k);
+                    }
+                };
+                const int c0 = half * CW, c1 = H > 1 ? c0 + CW : TK;
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c = c0; c < c1; c += CW) {
+                    columns(c);
+                    float m1 = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < CW; k += 2) {
+                        mx = fmaxf(mx, __uint_as_float(x[k]));
+                        m1 = fmaxf(m1, __uint_as_float(x[k + 1]));
+                    }
+                    mx = fmaxf(mx, m1);
                 }
-                if (row.live) {
-                    if (td.slot >= 0) {
+                if constexpr (H > 1) {
+                    s_mx[u & 1][half][r] = mx;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b_x[u & 1][half * 2 + rw]);
+                    ok = warp_wait(&b_x[u & 1][(half ^ 1) * 2 + rw], u >> 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    mx = fmaxf(mx, s_mx[u & 1][half ^ 1][r]);
+                }
+                bool grow = false;
+                float corr = 1.f;
+                if (first) {
+                    m = mx;
+                } else if (live && (mx - m) * c2 > kLazy4) {  // (the other rows hold anything)
+                    // (m = -infinity: O and l are zeros still)
+                    if (m != -INFINITY) {
+                        corr = ex2((m - mx) * c2);
+                        grow = true;
+                    }
+                    l *= corr;
+                    m = mx;
+                }
+                if (__any_sync(0xffffffffu, grow)) {
+                    ok = warp_wait(&b_pv[(u - 1) & 1], (u - 1) >> 1);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = half * (D / H); c < (half + 1) * (D / H); c += 16) {  // (beside the scores)
+                        uint32_t y[16];
+                        tmem_ld16(y, tO + c);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            *reinterpret_cast<uint4*>(po + r * D + c + 4 * k) =
-                                make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = pack2<false>(__uint_as_float(y[8 * k + 2 * e]) * f,
-                                                    __uint_as_float(y[8 * k + 2 * e + 1]) * f);
-                            *reinterpret_cast<uint4*>(out + c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                        for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * corr);
+                        tmem_st16(tO + c, y);
                     }
                 }
-                __syncwarp();
-            }
-            if (row.live && half == 0) {
-                if (td.slot >= 0) {
-                    po[ROWS * D + r] = M;
-                    po[ROWS * (D + 1) + r] = l;
-                } else if (p.lse) {
-                    p.lse[orow * p.Hq + row.hq] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&b_o);
-            return true;
-        };
-
-        bool ok = queries(0);
-        for (int u = 0; u < n_units && ok; ++u) {
-            ok = warp_wait(&b_s[u & 1], u >> 1);
-            if (!ok) break;
-            tc_fence_after();
-            const AttnUnit td = s_unit[u % kUnitRing];
-            const bool first = td.flags & kUnitFirst, edge = td.flags & kUnitEdge;
-            if (first) {
-                seg_start = td.start;
-                row = row_next;
-                pr = row.live ? td.p0 + row.i : -1;
-                c2 = c2_next;
-                l = 0.f;
-            }
-            const uint32_t tS = tmem + lanes + S::kColS + (u & 1) * TK;
-            // seen: k <= hi and (k > lo or k < sk), as bits of the 32 columns from column c
-            auto mask = [&](uint32_t* x, int c) {
-                const int hi = pr - td.start - c;
-                auto below = [](int n) {  // bits 0 .. n - 1
-                    return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
-                };
-                uint32_t seen = below(hi + 1);
-                if (p.window > 0) seen &= ~below(hi - p.window + 1) | below(p.sinks - td.start - c);
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    if (!((seen >> k) & 1u)) x[k] = 0xff800000u;
-            };
-            // half a row is read once, a whole one twice, 32 columns at a time
-            constexpr int CW = H > 1 ? TK / H : 32;
-            uint32_t x[CW];
-            auto columns = [&](int c) {
-                if constexpr (CW == 64) tmem_ld64(x, tS + c);
-                else tmem_ld32(x, tS + c);
-                if (edge) {
-#pragma unroll
-                    for (int k = 0; k < CW; k += 32) mask(x + k, c + k);
-                }
-            };
-            const int c0 = half * CW, c1 = H > 1 ? c0 + CW : TK;
-            float mx = -INFINITY;
+                const float mc = m == -INFINITY ? 0.f : m * c2 - kTail4;
+                float s0 = 0.f, s1 = 0.f;
 #pragma unroll 1
-            for (int c = c0; c < c1; c += CW) {
-                columns(c);
-                float m1 = -INFINITY;
+                for (int c = c0; c < c1; c += CW) {
+                    // (P's columns c / 2 .. hold scores that have been read)
+                    if (H == 1) columns(c);
+                    uint32_t y[CW / 2];
 #pragma unroll
-                for (int k = 0; k < CW; k += 2) {
-                    mx = fmaxf(mx, __uint_as_float(x[k]));
-                    m1 = fmaxf(m1, __uint_as_float(x[k + 1]));
+                    for (int k = 0; k < CW; k += 2) {
+                        const float a = ex2(fmaf(__uint_as_float(x[k]), c2, -mc));
+                        const float b = ex2(fmaf(__uint_as_float(x[k + 1]), c2, -mc));
+                        s0 += a;
+                        s1 += b;
+                        y[k / 2] = pack2<true>(a, b);
+                    }
+                    if constexpr (CW == 64) tmem_st32(tS + c / 2, y);
+                    else tmem_st16(tS + c / 2, y);
                 }
-                mx = fmaxf(mx, m1);
-            }
-            if constexpr (H > 1) {
-                s_mx[u & 1][half][r] = mx;
+                l += s0 + s1;
+                tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&b_x[u & 1][half * 2 + rw]);
-                ok = warp_wait(&b_x[u & 1][(half ^ 1) * 2 + rw], u >> 1);
-                if (!ok) break;
-                tc_fence_after();
-                mx = fmaxf(mx, s_mx[u & 1][half ^ 1][r]);
-            }
-            bool grow = false;
-            float corr = 1.f;
-            if (first) {
-                m = mx;
-            } else if (row.live && (mx - m) * c2 > kLazy4) {  // (the other rows hold anything)
-                // (m = -infinity: O and l are zeros still)
-                if (m != -INFINITY) {
-                    corr = ex2((m - mx) * c2);
-                    grow = true;
-                }
-                l *= corr;
-                m = mx;
-            }
-            if (__any_sync(0xffffffffu, grow)) {
-                ok = warp_wait(&b_pv[(u - 1) & 1], (u - 1) >> 1);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = half * (D / H); c < (half + 1) * (D / H); c += 32) {
-                    uint32_t y[32];
-                    tmem_ld32(y, tO + c);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * corr);
-                    tmem_st32(tO + c, y);
-                }
-            }
-            const float mc = m == -INFINITY ? 0.f : m * c2 - kTail4;
-            float s0 = 0.f, s1 = 0.f;
-#pragma unroll 1
-            for (int c = c0; c < c1; c += CW) {
-                // (P's columns c / 2 .. hold scores that have been read)
-                if (H == 1) columns(c);
-                uint32_t y[CW / 2];
-#pragma unroll
-                for (int k = 0; k < CW; k += 2) {
-                    const float a = ex2(fmaf(__uint_as_float(x[k]), c2, -mc));
-                    const float b = ex2(fmaf(__uint_as_float(x[k + 1]), c2, -mc));
-                    s0 += a;
-                    s1 += b;
-                    y[k / 2] = pack2<true>(a, b);
-                }
-                if constexpr (CW == 64) tmem_st32(tS + c / 2, y);
-                else tmem_st16(tS + c / 2, y);
-            }
-            l += s0 + s1;
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&b_p[u & 1]);
-            if (!(td.flags & kUnitLast)) continue;
-            // the next part's queries first: its scores wait for them, not for these rows
-            if (u + 1 < n_units) ok = queries(td.seg + 1);
-            if (ok) ok = finish(td, u);
+                if (lane == 0) mbar_arrive(&b_p[u & 1]);
+            } while (!(td.flags & kUnitLast));
         }
     }
     tc_fence_before();
