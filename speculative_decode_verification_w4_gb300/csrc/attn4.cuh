@@ -18,8 +18,8 @@
 // barrier a tile.
 //
 // The reference that the weights use is the running maximum, followed lazily: only where a
-// score exceeds it by 2^5 do the warps meet for the true maximum, rescale and form P again
-// (the first tile of an item; rarely later).  Weights are at most 2^14 in f16, and reach
+// score exceeds it by 2^6 do the warps meet for the true maximum, rescale and form P again
+// (the first tile of an item; rarely later).  Weights are at most 2^15 in f16, and reach
 // down to 2^-33 of the largest (f16 ends at 2^-24).
 #pragma once
 #include "attn.cuh"
@@ -27,7 +27,7 @@
 namespace vw4 {
 
 constexpr float kTail4 = 9.f;     // weights carry 2^9
-constexpr float kLazy4 = 5.f;     // (log2) of the reference
+constexpr float kLazy4 = 6.f;     // (log2) of the reference
 
 // Keys of a tile.  Four warps and about 18 KB a tile put two or three blocks on an SM.
 __host__ __device__ constexpr int attn4_tk(int D) { return D == 256 ? 64 : 128; }
@@ -331,61 +331,56 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
             // bf16 -> f16 under a power of two per row that puts its largest magnitude into
             // [2^14, 2^15), with the sign of the head's scale: exact for every value down to
             // 2^-31 of it.  Within 32 dimensions the order is that of the codes' registers.
-            // Rows four at a time: a row is a chain of latencies.
+            // Up to eight rows at once: a row is a chain of latencies.
             const int rb = td.g - h * p.row_blocks;
             const int bt = rb / p.blocks_g, bg = rb - bt * p.blocks_g;
             uint32_t* rows = reinterpret_cast<uint32_t*>(smem + S::kOffQ + qslot * S::kQ);
-            constexpr int kEach = S::kRows / S::kWarps, kAtOnce = kEach < 4 ? kEach : (kEach % 4 ? kEach / 2 : 4);
-            static_assert(kEach % kAtOnce == 0, "whole steps");
-#pragma unroll 1
-            for (int r0 = wk; r0 < S::kRows; r0 += S::kWarps * kAtOnce) {
-                float v[kAtOnce][D / 32], mx[kAtOnce];
-                int pos[kAtOnce], out[kAtOnce];
+            constexpr int kAtOnce = S::kRows / S::kWarps;
+            uint32_t v[kAtOnce][D / 64], mx[kAtOnce];
+            int pos[kAtOnce], out[kAtOnce];
 #pragma unroll
-                for (int q = 0; q < kAtOnce; ++q) {
-                    const int r = r0 + q * S::kWarps;
-                    const int t = (r * inv_gb) >> 16, gq = bg * p.gb + r - t * p.gb, i = bt * p.tb + t;
-                    const bool live = t < p.tb && i < p.R && gq < p.G;
-                    pos[q] = live ? td.p0 + i : -1;
-                    out[q] = live ? i << 16 | (h * p.G + gq) : -1;
-                    mx[q] = 0.f;
+            for (int q = 0; q < kAtOnce; ++q) {
+                const int r = wk + q * S::kWarps;
+                const int t = (r * inv_gb) >> 16, gq = bg * p.gb + r - t * p.gb, i = bt * p.tb + t;
+                const bool live = t < p.tb && i < p.R && gq < p.G;
+                pos[q] = live ? td.p0 + i : -1;
+                out[q] = live ? i << 16 | (h * p.G + gq) : -1;
+                mx[q] = 0u;
 #pragma unroll
-                    for (int k = 0; k < D / 64; ++k) {
-                        const int e = lane + 32 * k;  // pair of dimensions 2e, 2e + 1
-                        const uint32_t x = live ? rows[(S::q_at(r, e >> 2) >> 2) + (e & 3)] : 0u;
-                        v[q][2 * k] = __uint_as_float(x << 16);
-                        v[q][2 * k + 1] = __uint_as_float(x & 0xffff0000u);
-                        mx[q] = fmaxf(mx[q], fmaxf(fabsf(v[q][2 * k]), fabsf(v[q][2 * k + 1])));
-                    }
+                for (int k = 0; k < D / 64; ++k) {
+                    const int e = lane + 32 * k;  // pair of dimensions 2e, 2e + 1
+                    v[q][k] = live ? rows[(S::q_at(r, e >> 2) >> 2) + (e & 3)] : 0u;
+                    mx[q] = __vmaxu2(mx[q], v[q][k] & 0x7fff7fffu);
+                }
+            }
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1)
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q)
+                    mx[q] = __vmaxu2(mx[q], __shfl_xor_sync(0xffffffffu, mx[q], s));
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+                const int r = wk + q * S::kWarps;
+                const int ex = static_cast<int>(max(mx[q] & 0xffffu, mx[q] >> 16) >> 7);
+                int sh = ex == 0 || ex == 255 ? 0 : 127 + 14 - ex;
+                sh = max(-126, min(126, sh));
+                const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), ks);
+                if (lane == 0) {
+                    float c2 = p.scale * kLog2e * fabsf(ks) *
+                               __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+                    if (c2 < kMinFactor) c2 = kMinFactor;  // (NaN stays)
+                    s_c2[r] = c2;
+                    s_ref[r] = -INFINITY;
+                    s_pos[r] = pos[q];
+                    s_out[r] = out[q];
+                    s_nan[r] = 0u;
                 }
 #pragma unroll
-                for (int s = 16; s > 0; s >>= 1)
-#pragma unroll
-                    for (int q = 0; q < kAtOnce; ++q)
-                        mx[q] = fmaxf(mx[q], __shfl_xor_sync(0xffffffffu, mx[q], s));
-#pragma unroll
-                for (int q = 0; q < kAtOnce; ++q) {
-                    const int r = r0 + q * S::kWarps;
-                    const int ex = static_cast<int>(__float_as_uint(mx[q]) >> 23);
-                    int sh = ex == 0 || ex == 255 ? 0 : 127 + 14 - ex;
-                    sh = max(-126, min(126, sh));
-                    const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), ks);
-                    if (lane == 0) {
-                        float c2 = p.scale * kLog2e * fabsf(ks) *
-                                   __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-                        if (c2 < kMinFactor) c2 = kMinFactor;  // (NaN stays)
-                        s_c2[r] = c2;
-                        s_ref[r] = -INFINITY;
-                        s_pos[r] = pos[q];
-                        s_out[r] = out[q];
-                        s_nan[r] = 0u;
-                    }
-#pragma unroll
-                    for (int k = 0; k < D / 64; ++k) {
-                        const int e = lane + 32 * k, s = (e & ~15) | ((e & 3) << 2) | ((e >> 2) & 3);
-                        rows[(S::q_at(r, s >> 2) >> 2) + (s & 3)] =
-                            pack2<true>(v[q][2 * k] * up, v[q][2 * k + 1] * up);
-                    }
+                for (int k = 0; k < D / 64; ++k) {
+                    const int e = lane + 32 * k, s = (e & ~15) | ((e & 3) << 2) | ((e >> 2) & 3);
+                    rows[(S::q_at(r, s >> 2) >> 2) + (s & 3)] =
+                        pack2<true>(__uint_as_float(v[q][k] << 16) * up,
+                                    __uint_as_float(v[q][k] & 0xffff0000u) * up);
                 }
             }
             fence_async_smem();  // (a later load will write there)
