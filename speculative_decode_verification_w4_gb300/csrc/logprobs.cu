@@ -1,12 +1,13 @@
 // logprobs.cu -- log probabilities of given tokens, ranks, entropy and the best
 // alternatives of logits rows, in one pass over the rows.
 //
-// With c = scale log2(e) and a running maximum m of the logits,
+// With c = scale log2(e) and a reference m that follows the running maximum of the logits,
 //   Z = sum 2^(c (x - m)),   W = sum 2^(c (x - m)) c (x - m)
 // and when m grows, by d = c (m' - m): W <- (W - d Z) 2^-d, Z <- Z 2^-d.  Then
 //   lse = scale m + ln Z,   entropy = ln 2 (log2 Z - W / Z).
 // (The difference first: c x of the type's lowest value, a usual mask, would overflow.)
-// Each thread keeps its own m, Z and W; they meet in a fixed order.
+// Each thread keeps its own m (moved where an entry exceeds it by 2^8), Z and W; they meet
+// in a fixed order.
 //
 // Alternatives: the block keeps the `top` largest entries as 64-bit keys (value, then lower
 // index first) and lists those above the least of them; every few chunks of 4096 entries
@@ -33,10 +34,11 @@ constexpr int kLpChunk = kLpThreads * kLpEach;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kCand = kMaxTop * kLpEach;             // candidates of the list
 constexpr int kCandFull = 16;                        // so many are worth choosing from
-constexpr int kLpGroup = 8;                          // chunks between the block's meetings
+constexpr int kLpGroup = 16;                         // chunks between the block's meetings, at most
 constexpr int kLpMaxSplit = 64;
 constexpr long long kLpFill = 608;                   // blocks that fill the GPU
 constexpr uint32_t kLpBadId = 0x10u;
+constexpr float kLpLazy = 8.f;                       // log2 of an entry over its thread's reference
 constexpr float kLpFar = 1024.f;                     // 2^-1024 is 0 in fp32
 
 struct LpPart {
@@ -44,13 +46,13 @@ struct LpPart {
     int before;   // entries before the token
 };
 
-// Parts of a row: a chunk at least where the blocks would not fill the GPU, else sixteen
+// Parts of a row: a chunk at least where the blocks would not fill the GPU, else thirty-two
 // chunks at least (each part begins with the search for a threshold), for eight times the
 // blocks that fill it (no SM is left with a whole row alone at the end).
 static int lp_split(long long rows, int V) {
     const long long chunks = (V + kLpChunk - 1) / kLpChunk;
     const long long fill = std::min(chunks, (kLpFill + rows - 1) / rows);
-    const long long even = std::min(chunks / 16, (8 * kLpFill + rows - 1) / rows);
+    const long long even = std::min(chunks / 32, (8 * kLpFill + rows - 1) / rows);
     const long long s = std::max(fill, even);
     return static_cast<int>(s < kLpMaxSplit ? s : kLpMaxSplit);
 }
@@ -88,6 +90,12 @@ __device__ __forceinline__ LpSum lp_add(LpSum a, LpSum b, float c2) {
     a = lp_move(a, m, c2);
     b = lp_move(b, m, c2);
     return LpSum{m, a.z + b.z, a.w + b.w};
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // log p_v, from x and the row's m and ln Z.
@@ -163,6 +171,13 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
     uint4 next[N];
     const int end = shift + p.V;
     auto fetch = [&](int c) {
+        if (c * kLpChunk >= shift && (c + 1) * kLpChunk <= end) {
+            const uint4* from = reinterpret_cast<const uint4*>(base) +
+                                static_cast<long long>(c) * (kLpChunk / VEC) + tid;
+#pragma unroll
+            for (int k = 0; k < N; ++k) next[k] = __ldcs(from + k * kLpThreads);
+            return;
+        }
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const int at = (c * (kLpChunk / VEC) + k * kLpThreads + tid) * VEC;  // from base
@@ -229,8 +244,10 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
         if (c + 1 < c1) fetch(c + 1);
         float mx = f[0];
 #pragma unroll
-        for (int k = 1; k < kLpEach; ++k) mx = fmaxf(mx, f[k]);
-        if (!again && mx > s.m) s = lp_move(s, mx, c2);
+        for (int k = 1; k + 1 < kLpEach; k += 2) mx = max3(mx, f[k], f[k + 1]);
+        mx = fmaxf(mx, f[kLpEach - 1]);
+        // (the reference follows lazily: exponents of up to kLpLazy cost their rounding alone)
+        if (!again && (mx - s.m) * c2 > kLpLazy) s = lp_move(s, mx, c2);
         if (again) {
         } else if (s.m == INFINITY) {
 #pragma unroll
@@ -259,15 +276,19 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
         auto index = [&](int k) {
             return (c * (kLpChunk / VEC) + (k / VEC) * kLpThreads + tid) * VEC + k % VEC - shift;
         };
-        if (here && !again) {
+        // (a chunk's entries are seldom before a likely token: one look at their maximum)
+        if (here && !again && !(mx < xt)) {
             // equal entries count where they stand before the token
             const int at0 = c * kLpChunk - shift;
+            float n = 0.f;
             if (c > 0 && at0 + kLpChunk <= t && xt > -INFINITY) {
 #pragma unroll
-                for (int k = 0; k < kLpEach; ++k) before += f[k] >= xt ? 1 : 0;
+                for (int k = 0; k < kLpEach; ++k) n += f[k] >= xt ? 1.f : 0.f;
+                before += static_cast<int>(n);
             } else if (at0 > t && xt > -INFINITY) {
 #pragma unroll
-                for (int k = 0; k < kLpEach; ++k) before += f[k] > xt ? 1 : 0;
+                for (int k = 0; k < kLpEach; ++k) n += f[k] > xt ? 1.f : 0.f;
+                before += static_cast<int>(n);
             } else {
 #pragma unroll
                 for (int k = 0; k < kLpEach; ++k) {
@@ -340,17 +361,16 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LogprobPar
             continue;
         }
         if (mx > tau) {
-            int mine = 0;
+            // (one of a thread's entries, as a rule)
 #pragma unroll
-            for (int k = 0; k < kLpEach; ++k) mine += f[k] > tau ? 1 : 0;
-            int at = atomicAdd(&s_n, mine);
-            if (at + mine <= kCand) {
-#pragma unroll
-                for (int k = 0; k < kLpEach; ++k)
-                    if (f[k] > tau) s_cand[at++] = lp_key(f[k], index(k));
+            for (int k = 0; k < kLpEach; ++k) {
+                if (f[k] > tau) {
+                    const int at = atomicAdd(&s_n, 1);
+                    if (at < kCand) s_cand[at] = lp_key(f[k], index(k));
+                }
             }
         }
-        if (++c < c1 && c - group < kLpGroup) continue;
+        if (++c < c1 && c - group < min(kLpGroup, 2 * (group - c0))) continue;
         // ---- the threads meet
         __syncthreads();
         const int now = s_n;
