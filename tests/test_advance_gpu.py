@@ -71,7 +71,7 @@ def make(seed, B, page, cols, spare, hi, used=None):
 
 
 def check(seed, B, page, cols, spare, hi, R=8, accepted=True, ended=0.2, grow=None, rows_max=None,
-          in_place=False, break_input=None):
+          in_place=False, break_input=None, shift=0):
     lens, held, table, free, count, total, g = make(seed, B, page, cols, spare, hi)
     acc = torch.randint(0, 3, (B,), generator=g).int() if accepted else torch.zeros(B, dtype=torch.int32)
     end = (torch.rand(B, generator=g) < ended).int()
@@ -82,13 +82,16 @@ def check(seed, B, page, cols, spare, hi, R=8, accepted=True, ended=0.2, grow=No
     rows = rows_max if rows_max is not None else int(gr.clamp(min=0).sum())
     want = reference(t, page, lens.tolist(), held.tolist(), f, count, rows, R, acc.tolist(),
                      end.tolist(), gr.tolist(), total)
-    dl, dh, dc = lens.cuda(), held.cuda(), torch.tensor([count], dtype=torch.int32, device="cuda")
+    def put(x):  # on the device, `shift` elements behind an allocation's start
+        d = torch.empty(x.numel() + shift, dtype=x.dtype, device="cuda")[shift:]
+        return d.copy_(x)
+    dl, dh, dc = put(lens), put(held), torch.tensor([count], dtype=torch.int32, device="cuda")
     dt, df = table.cuda(), free.cuda()
     kw = dict(lens_out=dl, held_out=dh, free_count_out=dc) if in_place else {}
     slots = torch.full((rows + 7,), -9, dtype=torch.int64, device="cuda")
-    p = vw4.advance_pages(dt, page, dl, dh, df, dc, rows, R, accepted=acc.cuda() if accepted else None,
-                          ended=end.cuda() if ended else None,
-                          grow=None if grow is None and not break_input else gr.cuda(), slots=slots, **kw)
+    p = vw4.advance_pages(dt, page, dl, dh, df, dc, rows, R, accepted=put(acc) if accepted else None,
+                          ended=put(end) if ended else None,
+                          grow=None if grow is None and not break_input else put(gr), slots=slots, **kw)
     status(want[6])
     assert p.lens.tolist() == want[0]
     assert p.held.tolist() == want[1]
@@ -102,6 +105,15 @@ def check(seed, B, page, cols, spare, hi, R=8, accepted=True, ended=0.2, grow=No
     assert df.tolist() == f
     if not in_place:
         assert dl.tolist() == lens.tolist() and dh.tolist() == held.tolist() and int(dc) == count
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("B,spare", [(4096, 9000), (4097, 50), (9001, 3000), (16384, 30000), (16383, 400)])
+def test_many_sequences(B, spare, shift, in_place):
+    """One and several groups of sequences a thread, with pages for all of them and for some,
+    arrays that lie on 16 bytes or not."""
+    check(B, B, 8, 6, spare, 24, 3, grow=9, in_place=in_place, shift=shift)
 
 
 @pytest.mark.parametrize("in_place", [False, True])
