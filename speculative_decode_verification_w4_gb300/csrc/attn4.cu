@@ -57,7 +57,7 @@ Attn4Plan attn4_plan(AttnParams& p, int D, void* ws) {
                                          align256((static_cast<size_t>(p.B) + 1) * sizeof(long long)));
     // at most one CTA per tile that the table could hold
     const long long cap = static_cast<long long>(p.max_blocks) * p.page_size;
-    plan.tk = k.tc ? attn4_tc_tk(D) : attn4_tk(D);
+    plan.tk = k.tc ? attn4_tc_tk(D) : attn4_tk(D, k.rows / 8);
     const long long units = static_cast<long long>(p.B) * p.groups * ((cap + plan.tk - 1) / plan.tk);
     plan.grid = k.grid;
     if (units < plan.grid) plan.grid = static_cast<int>(units < 1 ? 1 : units);

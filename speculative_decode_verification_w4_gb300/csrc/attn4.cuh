@@ -4,18 +4,24 @@
 // the other cache types (attn.cuh).
 //
 // Mathematics.  S = Q K^T, P = exp(S - max), O = P V with a running maximum and sum over
-// tiles of 128 keys, all transposed: keys, then dimensions are the rows of the matrix
+// tiles of 64 to 256 keys, all transposed: keys, then dimensions are the rows of the matrix
 // instructions and the query rows their columns, eight to an instruction, so that the
 // converted cache values are the operand that is made once and the query rows cost little
 // where they are few.  K^T and V become f16 in registers, exactly: e2m1 times its block's
 // e4m3 scale has six significant bits.
 //
-// A tile.  Each warp takes 16 or 32 keys for S = K Q^T (32 dimensions of 8 keys are a register
+// A tile.  Each warp takes 16 to 64 keys for S = K Q^T (32 dimensions of 8 keys are a register
 // of codes a lane), forms P against the block's common reference, and leaves it in shared
 // memory; beside it, the warps leave V's scales as f16, token by token.  After the barrier
 // each warp takes a slice of V's dimensions for O = V^T P^T, so nothing is converted twice
 // however many query rows there are, and S of the next tile runs in the same phase: one
 // barrier a tile.
+//
+// What bounds it: with few rows the conversions (a cvt for two codes, a multiply by the scale:
+// the ALU is 54 % busy, the issue slots 60 %) and the chain of a tile, from 16 rows on the
+// products too.  32 sequences of up to 32768 tokens, 8 key heads of size 128, four rows each:
+// 105 us of 424 MB, 62.5 at the copy rate; 24 rows of size 256 over 64 windows of 1024: 54 us.
+// Without conversions and products the loads alone take 78 and 39.
 //
 // The reference that the weights use is the running maximum, followed lazily: only where a
 // score exceeds it by 2^6 do the warps meet for the true maximum, rescale and form P again
@@ -29,11 +35,22 @@ namespace vw4 {
 constexpr float kTail4 = 9.f;     // weights carry 2^9
 constexpr float kLazy4 = 6.f;     // (log2) of the reference
 
-// Keys of a tile.  Four warps and about 18 KB a tile put two or three blocks on an SM.
-__host__ __device__ constexpr int attn4_tk(int D) { return D == 256 ? 64 : 128; }
+// Keys of a tile: four warps and about 18 KB of K and V put two blocks on an SM (three with 9 KB,
+// at head size 64).  One n-tile of query rows, and two at head size 64, leave the registers for
+// twice as many: fewer meetings, rings and edges for the same bytes (32 sequences of up to 32768
+// tokens, one row of four heads: head size 64 71.5 us instead of 118.6, 128 105 instead of 109
+// with three blocks, 256 98 instead of 108; 16 rows at head size 64 85 instead of 105).  16 rows of
+// larger heads are faster so over long sequences (128: 126 instead of 138) and slower over short
+// ones and windows (30 us instead of 38 there), for want of room for the rings.
+__host__ __device__ constexpr int attn4_tk(int D, int nt) {
+    return (D == 256 ? 64 : 128) * (nt == 1 || (D == 64 && nt == 2) ? 2 : 1);
+}
 // Places of the ring of K tiles: what shared memory leaves.
 __host__ __device__ constexpr int attn4_places(int D, int nt) {
-    return D == 64 ? 6 : (nt == 1 ? 3 : (D == 128 ? (nt == 4 ? 3 : 4) : (nt >= 3 ? 3 : 4)));
+    return nt == 1    ? (D == 64 ? 3 : 2)
+           : D == 64  ? (nt == 2 ? 4 : 6)
+           : D == 128 ? (nt == 4 ? 3 : 4)
+                      : (nt >= 3 ? 3 : 4);
 }
 
 #ifdef __CUDACC__
@@ -41,7 +58,7 @@ template <int D, int NT>
 struct Attn4Shape {
     static constexpr int kWarps = 4;
     static constexpr int kThreads = (kWarps + 2) * 32;
-    static constexpr int kTK = attn4_tk(D);
+    static constexpr int kTK = attn4_tk(D, NT);
     static constexpr int kKM = kTK / kWarps / 16;     // 16-key row tiles of a warp
     static constexpr int kRows = 8 * NT;
     static constexpr int kKB = D / 2;                 // bytes of a key's codes
@@ -58,9 +75,9 @@ struct Attn4Shape {
     static constexpr int kVRow = (kTK + 16) * 2;      // V's scales: f16 [block][v_at(token)]
     static constexpr int kVS = kNB * kVRow;
     static constexpr int kX = (kParts - 1) * kSlices * 1024;  // an n-tile's outputs of the other parts
-    static constexpr int kMinBlocks = NT == 1 ? 3 : 2;
+    static constexpr int kMinBlocks = NT == 1 && D == 64 ? 3 : 2;
     // V of a tile is read a phase after its K: one place more, if it fits
-    static constexpr int kNK = attn4_places(D, NT), kNV = kNK + (NT == 1 && D > 64 ? 0 : 1);
+    static constexpr int kNK = attn4_places(D, NT), kNV = kNK + (NT == 1 ? 0 : 1);
     static constexpr int kOffVal = kNK * kStage;
     static constexpr int kOffQ = (kOffVal + kNV * kStage + 1023) / 1024 * 1024;
     static constexpr int kOffP = kOffQ + 2 * kQ;
@@ -509,43 +526,47 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
                 // ---- V's scales to f16, token by token: a thread a part of a token's
                 dead |= !wait(&b_v[vst], vround);
                 if (!dead) {
-                    constexpr int PER = TK * NB / (S::kWarps * 32);  // bytes of a thread
+                    constexpr int ALL = TK * NB / (S::kWarps * 32);  // bytes of a thread
+                    constexpr int PER = ALL < NB ? ALL : (NB < 8 ? NB : 8);  // of them one token's
                     static_assert(PER == 2 || PER == 4 || PER == 8, "up to two words");
                     constexpr int W = (PER + 3) / 4;
                     constexpr int TPT = NB / PER;                    // threads of a token
-                    const int token = tid / TPT, b0 = tid % TPT * PER;
-                    const uint8_t* src = smem + S::kOffVal + vst * S::kStage + S::kTile + token * NB + b0;
-                    uint32_t w[W];
-                    if (PER == 2) w[0] = *reinterpret_cast<const uint16_t*>(src);
 #pragma unroll
-                    for (int k = 0; k < PER / 4; ++k) w[k] = reinterpret_cast<const uint32_t*>(src)[k];
-                    if (edge) {
-                        const int j = start + token;
-                        if (!key_some(j, td.len, td.p0, p.window, p.sinks)) {
-                            // no row sees it: zeros, whatever the cache holds there
+                    for (int round = 0; round < ALL / PER; ++round) {
+                        const int token = tid / TPT + round * (S::kWarps * 32 / TPT), b0 = tid % TPT * PER;
+                        const uint8_t* src = smem + S::kOffVal + vst * S::kStage + S::kTile + token * NB + b0;
+                        uint32_t w[W];
+                        if (PER == 2) w[0] = *reinterpret_cast<const uint16_t*>(src);
 #pragma unroll
-                            for (int k = 0; k < W; ++k) w[k] = 0u;
-                        } else if (!key_all(j, td.len, td.p0, p.window, p.sinks)) {
-                            // NaN scales must not reach rows that do not see the key through a
-                            // weight of zero: noted for the others, and taken out
+                        for (int k = 0; k < PER / 4; ++k) w[k] = reinterpret_cast<const uint32_t*>(src)[k];
+                        if (edge) {
+                            const int j = start + token;
+                            if (!key_some(j, td.len, td.p0, p.window, p.sinks)) {
+                                // no row sees it: zeros, whatever the cache holds there
 #pragma unroll
-                            for (int k = 0; k < PER; ++k) {
-                                if (((w[k / 4] >> (8 * (k & 3))) & 0x7fu) != 0x7fu) continue;
-                                w[k / 4] &= ~(0xffu << (8 * (k & 3)));
+                                for (int k = 0; k < W; ++k) w[k] = 0u;
+                            } else if (!key_all(j, td.len, td.p0, p.window, p.sinks)) {
+                                // NaN scales must not reach rows that do not see the key through a
+                                // weight of zero: noted for the others, and taken out
+#pragma unroll
+                                for (int k = 0; k < PER; ++k) {
+                                    if (((w[k / 4] >> (8 * (k & 3))) & 0x7fu) != 0x7fu) continue;
+                                    w[k / 4] &= ~(0xffu << (8 * (k & 3)));
 #pragma unroll 1
-                                for (int r = 0; r < S::kRows; ++r)
-                                    if (s_out[r] >= 0 && key_seen(j, s_pos[r], p.window, p.sinks))
-                                        atomicOr(&s_nan[r], 1u << (b0 + k));
+                                    for (int r = 0; r < S::kRows; ++r)
+                                        if (s_out[r] >= 0 && key_seen(j, s_pos[r], p.window, p.sinks))
+                                            atomicOr(&s_nan[r], 1u << (b0 + k));
+                                }
                             }
                         }
-                    }
-                    uint8_t* dst = smem + S::kOffV + (u & 1) * S::kVS + b0 * S::kVRow + S::v_at(token) * 2;
+                        uint8_t* dst = smem + S::kOffV + (u & 1) * S::kVS + b0 * S::kVRow + S::v_at(token) * 2;
 #pragma unroll
-                    for (int k = 0; k < PER; k += 2) {
-                        const uint32_t f = e4m3x2_f16x2(w[k / 4] >> (8 * (k & 3)));
-                        *reinterpret_cast<uint16_t*>(dst + k * S::kVRow) = static_cast<uint16_t>(f);
-                        *reinterpret_cast<uint16_t*>(dst + (k + 1) * S::kVRow) =
-                            static_cast<uint16_t>(f >> 16);
+                        for (int k = 0; k < PER; k += 2) {
+                            const uint32_t f = e4m3x2_f16x2(w[k / 4] >> (8 * (k & 3)));
+                            *reinterpret_cast<uint16_t*>(dst + k * S::kVRow) = static_cast<uint16_t>(f);
+                            *reinterpret_cast<uint16_t*>(dst + (k + 1) * S::kVRow) =
+                                static_cast<uint16_t>(f >> 16);
+                        }
                     }
                 }
                 if (u == first) {

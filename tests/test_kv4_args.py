@@ -143,7 +143,7 @@ def test_workspace_sizes(lib):
     for D in (64, 128, 256):
         assert 0 < size(vw4.OP_ATTN_KV4, 1, 1, D) <= size(vw4.OP_ATTN_KV4, 1, 64, D)
         # a key head with more rows is cut into blocks: no more room
-        assert size(vw4.OP_ATTN_KV4, 1, 64, D) == size(vw4.OP_ATTN_KV4, 1, 4096, D)
+        assert size(vw4.OP_ATTN_KV4, 1, 128, D) == size(vw4.OP_ATTN_KV4, 1, 4096, D)
     assert size(vw4.OP_ATTN_KV4, 1, 0, 64) == size(vw4.OP_ATTN_KV4, 1, 1, 96) == 0
     assert size(vw4.OP_ADVANCE, 16384, 0, 0) >= 2 * 8 * 16385
     assert size(vw4.OP_ADVANCE, 0, 0, 0) == size(vw4.OP_ADVANCE, 16385, 0, 0) == 0
