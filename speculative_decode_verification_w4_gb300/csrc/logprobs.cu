@@ -20,8 +20,8 @@
 // overfill the list (rows in ascending order) are read again that way.
 //
 // The bytes bound it (4 or 2 a logit) and, at 16 instructions a logit, the issue slots: 256 x 9
-// rows of 151936, of which 60 % are read, with five alternatives, take 153 us in fp32 (124 at the
-// copy rate; without alternatives 135) and 135 in bf16.  A row is split over blocks where the rows
+// rows of 151936, of which 60 % are read, with five alternatives, take 154 us in fp32 (124 at the
+// copy rate; without alternatives 147) and 135 in bf16.  A row is split over blocks where the rows
 // alone would leave SMs idle (one sequence's 8 rows of 262144 with 20 alternatives: 14 us, of
 // which the join of 64 parts a row is 3), and a second kernel joins the parts in order.
 #include <cuda_bf16.h>
@@ -136,7 +136,7 @@ __device__ __forceinline__ int lp_above(const unsigned long long* keys, int n, u
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kLpThreads, BF16 ? 4 : 5)
+__global__ void __launch_bounds__(kLpThreads, 4)
     logprob_kernel(const LogprobParams p, LpPart* parts, unsigned long long* lists, int split) {
     constexpr int VEC = BF16 ? 8 : 4, N = kLpEach / VEC;  // entries of a load, loads of a chunk
     using X = std::conditional_t<BF16, uint16_t, float>;
@@ -171,9 +171,9 @@ __global__ void __launch_bounds__(kLpThreads, BF16 ? 4 : 5)
     const float xt = here ? value(x[t]) : INFINITY;
     const float c2 = p.scale * kLog2e;
 
-    // fp32: five blocks an SM cover each other's loads; bf16: the next chunk is on its way while
-    // this one is worked on (the other way round 158 instead of 155 us, and 143 instead of 137,
-    // for 256 x 9 rows of 151936)
+    // The next chunk is on its way while this one is worked on.  (Without that, five blocks an SM
+    // cover each other's loads: 80 to 87 us instead of 70 to 93 for 80 x 9 rows of 151936, and
+    // 153 or 166 from run to run for 256 x 9; bf16 143 instead of 137.)
     uint4 next[N];
     const int end = shift + p.V;
     auto fetch = [&](int c) {
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kLpThreads, BF16 ? 4 : 5)
     int before = 0;
     if (tid < kMaxTop) s_best[tid] = 0ull;
     if (tid == 0) s_n = 0;
-    if (BF16 && c0 < c1) fetch(c0);
+    if (c0 < c1) fetch(c0);
     if (p.top > 0) __syncthreads();
     float tau = -INFINITY;  // of the last of s_best: what is larger is a candidate
     int listed = 0;         // candidates at the last meeting
@@ -238,7 +238,6 @@ __global__ void __launch_bounds__(kLpThreads, BF16 ? 4 : 5)
     int careful = c0 + 1;   // chunks before it get a threshold of their own
     bool again = false;     // of a second reading
     for (int c = c0; c < c1;) {
-        if (!BF16) fetch(c);
         float f[kLpEach];
 #pragma unroll
         for (int k = 0; k < N; ++k) {
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(kLpThreads, BF16 ? 4 : 5)
                 f[k * VEC + j] = __uint_as_float(raw);  // (a NaN loses every comparison below)
             }
         }
-        if (BF16 && c + 1 < c1) fetch(c + 1);
+        if (c + 1 < c1) fetch(c + 1);
         float mx = f[0];
 #pragma unroll
         for (int k = 1; k + 1 < kLpEach; k += 2) mx = max3(mx, f[k], f[k + 1]);
@@ -388,7 +387,7 @@ __global__ void __launch_bounds__(kLpThreads, BF16 ? 4 : 5)
             careful = c;
             again = true;
             c = group;
-            if (BF16) fetch(c);
+            fetch(c);
         } else {
             if (now >= kCandFull || c == c1) {
                 choose(now);
