@@ -11,6 +11,7 @@ namespace vw4 {
 // 24 / 32 / 64 rows 37 / 44 / 87 against 53 / 54 / 57).
 constexpr int kAttn4TcFrom = 33;
 
+constexpr int kAttn4Sms = 152;
 constexpr int kAttn4MaxGrid = kAttnMaxGrid64;  // (three blocks an SM at most)
 static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
@@ -57,10 +58,15 @@ Attn4Plan attn4_plan(AttnParams& p, int D, void* ws) {
                                          align256((static_cast<size_t>(p.B) + 1) * sizeof(long long)));
     // at most one CTA per tile that the table could hold
     const long long cap = static_cast<long long>(p.max_blocks) * p.page_size;
-    plan.tk = k.tc ? attn4_tc_tk(D) : attn4_tk(D, k.rows / 8);
-    const long long units = static_cast<long long>(p.B) * p.groups * ((cap + plan.tk - 1) / plan.tk);
+    const auto units = [&](int tk) {
+        return static_cast<long long>(p.B) * p.groups * ((cap + tk - 1) / tk);
+    };
+    const int nt = k.rows / 8;
+    plan.large = !k.tc && (nt == 1 ? units(attn4_tk(D, true)) >= kAttn4Sms : D == 64 && nt == 2);
+    plan.tk = k.tc ? attn4_tc_tk(D) : attn4_tk(D, plan.large);
     plan.grid = k.grid;
-    if (units < plan.grid) plan.grid = static_cast<int>(units < 1 ? 1 : units);
+    const long long most_units = units(plan.tk);
+    if (most_units < plan.grid) plan.grid = static_cast<int>(most_units < 1 ? 1 : most_units);
     p.box_rows = p.page_size < plan.tk ? p.page_size : plan.tk;
     plan.box_bytes = D / 2;
     const long long group = 8 * p.token_stride;
@@ -82,9 +88,9 @@ cudaError_t launch_attn4(const AttnParams& p, const Kv4Blocks& kb, const AttnMap
                          const Attn4Plan& plan, int D, int sms, cudaStream_t s) {
     int grid = plan.grid;
     const cudaError_t e = plan.tc   ? launch_attn4_tc(p, kb, maps, D, plan.rows, &grid, sms, s)
-                          : D == 64  ? launch_attn4_d64(p, kb, maps, plan.rows / 8, &grid, sms, s)
-                          : D == 128 ? launch_attn4_d128(p, kb, maps, plan.rows / 8, &grid, sms, s)
-                                     : launch_attn4_d256(p, kb, maps, plan.rows / 8, &grid, sms, s);
+                          : D == 64  ? launch_attn4_d64(p, kb, maps, plan.rows / 8, plan.large, &grid, sms, s)
+                          : D == 128 ? launch_attn4_d128(p, kb, maps, plan.rows / 8, plan.large, &grid, sms, s)
+                                     : launch_attn4_d256(p, kb, maps, plan.rows / 8, plan.large, &grid, sms, s);
     if (e != cudaSuccess) return e;
     return launch_attn_join(p, D, plan.rows, grid, plan.tk, sms, s);
 }

@@ -41,24 +41,27 @@ constexpr float kLazy4 = 6.f;     // (log2) of the reference
 // tokens, one row of four heads: head size 64 71.5 us instead of 118.6, 128 105 instead of 109
 // with three blocks, 256 98 instead of 108; 16 rows at head size 64 85 instead of 105).  16 rows of
 // larger heads are faster so over long sequences (128: 126 instead of 138) and slower over short
-// ones and windows (30 us instead of 38 there), for want of room for the rings.
-__host__ __device__ constexpr int attn4_tk(int D, int nt) {
-    return (D == 256 ? 64 : 128) * (nt == 1 || (D == 64 && nt == 2) ? 2 : 1);
+// ones and windows (30 us instead of 38 there), for want of room for the rings.  One n-tile keeps
+// the small tiles too, for tables that do not hold a large one for every SM (one sequence of 517
+// tokens, 4 key heads of size 256: 9.7 us instead of 10.2).
+__host__ __device__ constexpr int attn4_tk(int D, bool large) {
+    return (D == 256 ? 64 : 128) * (large ? 2 : 1);
 }
 // Places of the ring of K tiles: what shared memory leaves.
-__host__ __device__ constexpr int attn4_places(int D, int nt) {
-    return nt == 1    ? (D == 64 ? 3 : 2)
-           : D == 64  ? (nt == 2 ? 4 : 6)
+__host__ __device__ constexpr int attn4_places(int D, int nt, bool large) {
+    return large      ? (D > 64 ? 2 : (nt == 1 ? 3 : 4))
+           : D == 64  ? 6
+           : nt == 1  ? 3
            : D == 128 ? (nt == 4 ? 3 : 4)
                       : (nt >= 3 ? 3 : 4);
 }
 
 #ifdef __CUDACC__
-template <int D, int NT>
+template <int D, int NT, bool LARGE>
 struct Attn4Shape {
     static constexpr int kWarps = 4;
     static constexpr int kThreads = (kWarps + 2) * 32;
-    static constexpr int kTK = attn4_tk(D, NT);
+    static constexpr int kTK = attn4_tk(D, LARGE);
     static constexpr int kKM = kTK / kWarps / 16;     // 16-key row tiles of a warp
     static constexpr int kRows = 8 * NT;
     static constexpr int kKB = D / 2;                 // bytes of a key's codes
@@ -75,9 +78,9 @@ struct Attn4Shape {
     static constexpr int kVRow = (kTK + 16) * 2;      // V's scales: f16 [block][v_at(token)]
     static constexpr int kVS = kNB * kVRow;
     static constexpr int kX = (kParts - 1) * kSlices * 1024;  // an n-tile's outputs of the other parts
-    static constexpr int kMinBlocks = NT == 1 && D == 64 ? 3 : 2;
+    static constexpr int kMinBlocks = NT == 1 && (D == 64 || !LARGE) ? 3 : 2;
     // V of a tile is read a phase after its K: one place more, if it fits
-    static constexpr int kNK = attn4_places(D, NT), kNV = kNK + (NT == 1 ? 0 : 1);
+    static constexpr int kNK = attn4_places(D, NT, LARGE), kNV = kNK + (NT == 1 && (D > 64 || LARGE) ? 0 : 1);
     static constexpr int kOffVal = kNK * kStage;
     static constexpr int kOffQ = (kOffVal + kNV * kStage + 1023) / 1024 * 1024;
     static constexpr int kOffP = kOffQ + 2 * kQ;
@@ -133,10 +136,10 @@ __device__ __forceinline__ uint32_t mul_f16x2_half(uint32_t a, uint32_t s) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>::kMinBlocks)
+template <int D, int NT, bool LARGE>
+__global__ void __launch_bounds__(Attn4Shape<D, NT, LARGE>::kThreads, Attn4Shape<D, NT, LARGE>::kMinBlocks)
     attn4_kernel(const AttnParams p, const Kv4Blocks kb, const __grid_constant__ AttnMaps maps) {
-    using S = Attn4Shape<D, NT>;
+    using S = Attn4Shape<D, NT, LARGE>;
     constexpr int TK = S::kTK, NK = S::kNK, NV = S::kNV, NB = S::kNB, KM = S::kKM;
     constexpr bool kValuesFirst = NT <= 3;
     extern __shared__ uint8_t smem_raw[];
@@ -745,13 +748,13 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT>::kThreads, Attn4Shape<D, NT>
     }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool LARGE>
 cudaError_t attn4_launch(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps, int* grid,
                          int sms, cudaStream_t s) {
-    using S = Attn4Shape<D, NT>;
+    using S = Attn4Shape<D, NT, LARGE>;
     static std::atomic<unsigned long long> once;
     static std::atomic<int> occ;
-    auto* kernel = attn4_kernel<D, NT>;
+    auto* kernel = attn4_kernel<D, NT, LARGE>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -782,12 +785,14 @@ cudaError_t attn4_launch(const AttnParams& p, const Kv4Blocks& kb, const AttnMap
 
 template <int D>
 cudaError_t attn4_dispatch(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps, int nt,
-                           int* grid, int sms, cudaStream_t s) {
+                           bool large, int* grid, int sms, cudaStream_t s) {
     switch (nt) {
-        case 1: return attn4_launch<D, 1>(p, kb, maps, grid, sms, s);
-        case 2: return attn4_launch<D, 2>(p, kb, maps, grid, sms, s);
-        case 3: return attn4_launch<D, 3>(p, kb, maps, grid, sms, s);
-        case 4: return attn4_launch<D, 4>(p, kb, maps, grid, sms, s);
+        case 1:
+            return large ? attn4_launch<D, 1, true>(p, kb, maps, grid, sms, s)
+                         : attn4_launch<D, 1, false>(p, kb, maps, grid, sms, s);
+        case 2: return attn4_launch<D, 2, D == 64>(p, kb, maps, grid, sms, s);
+        case 3: return attn4_launch<D, 3, false>(p, kb, maps, grid, sms, s);
+        case 4: return attn4_launch<D, 4, false>(p, kb, maps, grid, sms, s);
     }
     return cudaErrorInvalidValue;
 }

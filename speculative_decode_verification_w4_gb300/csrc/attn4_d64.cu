@@ -3,7 +3,7 @@
 
 namespace vw4 {
 cudaError_t launch_attn4_d64(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps, int nt,
-                            int* grid, int sms, cudaStream_t s) {
-    return attn4_dispatch<64>(p, kb, maps, nt, grid, sms, s);
+                            bool large, int* grid, int sms, cudaStream_t s) {
+    return attn4_dispatch<64>(p, kb, maps, nt, large, grid, sms, s);
 }
 }  // namespace vw4

@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(kLpThreads, 4)
     const float c2 = p.scale * kLog2e;
 
     // The next chunk is on its way while this one is worked on.  (Without that, five blocks an SM
-    // cover each other's loads: 80 to 87 us instead of 70 to 93 for 80 x 9 rows of 151936, and
-    // 153 or 166 from run to run for 256 x 9; bf16 143 instead of 137.)
+    // cover each other's loads: 79 us instead of 93 for 80 x 9 rows of 151936, but 153 or 166 from
+    // run to run for 256 x 9 instead of 154, and 143 instead of 137 in bf16.)
     uint4 next[N];
     const int end = shift + p.V;
     auto fetch = [&](int c) {

@@ -331,7 +331,7 @@ struct Kv4Blocks {             // block scales of K and V
 };
 size_t attn4_workspace_bytes(int B, int rows, int D);
 struct Attn4Plan {
-    bool tc;                   // on the 5th-generation tensor cores
+    bool tc, large;            // on the 5th-generation tensor cores; large tiles on the others
     int rows, tk, grid;        // query rows of a block, keys of a tile, bound of the grid
     int box_bytes;
     CUtensorMapSwizzle swizzle;
@@ -340,11 +340,11 @@ Attn4Plan attn4_plan(AttnParams& p, int D, void* ws);
 cudaError_t launch_attn4(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps,
                          const Attn4Plan& plan, int D, int sms, cudaStream_t s);
 cudaError_t launch_attn4_d64(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps, int nt,
-                             int* grid, int sms, cudaStream_t s);
+                             bool large, int* grid, int sms, cudaStream_t s);
 cudaError_t launch_attn4_d128(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps, int nt,
-                              int* grid, int sms, cudaStream_t s);
+                              bool large, int* grid, int sms, cudaStream_t s);
 cudaError_t launch_attn4_d256(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps, int nt,
-                              int* grid, int sms, cudaStream_t s);
+                              bool large, int* grid, int sms, cudaStream_t s);
 cudaError_t launch_attn4_tc(const AttnParams& p, const Kv4Blocks& kb, const AttnMaps& maps, int D, int rows,
                             int* grid, int sms, cudaStream_t s);
 // The join of an attention call's partials (attn.cu).

@@ -108,6 +108,16 @@ def test_many_tiles_per_block(R, G, D, page):
     run_case(61, [300 + 37 * b for b in range(40)], R, 2 * G, 2, D, page, only=range(0, 40, 7))
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("R,G,page,order,window,sinks", [(1, 4, 8, "nhd", 0, 0), (1, 8, 64, "hnd", 0, 0),
+                                                         (2, 3, 512, "nhd", 700, 9), (1, 1, 16, "hnd", 257, 300),
+                                                         (4, 2, 32, "nhd", 64, 1)])
+def test_tables_for_every_sm(R, G, page, order, window, sinks, D):
+    """Few rows over tables that hold a large tile for every SM; lengths on both sides of one."""
+    lens = [0, 1, 63, 128, 129, 255, 256, 257, 511, 513, 1000, 4099] + [300 + 71 * b for b in range(28)]
+    run_case(80 + R, lens, R, 2 * G, 2, D, page, order, window=window, sinks=sinks)
+
+
 @pytest.mark.parametrize("R,G,D", [(5, 4, 64), (9, 4, 128), (16, 7, 256), (1, 3, 128)])
 def test_many_parts_of_one_tile(R, G, D):
     B, Hkv = 1500, 4
