@@ -1,11 +1,13 @@
 // advance.cu -- lengths, pages, block table and slots of the next step's rows, from the
 // lengths that an accept left on the device.
 //
-// Three phases, each over what the one before has written: scans over the sequences (what
-// each gives back, needs and gets: prefix sums in the sequences' order make the outcome
-// independent of the schedule); the returned pages onto the free list; the taken pages
-// into the table and the rows' slots.  The second and the third look their sequence up in
-// the prefix sums, so that one long prompt is spread over the whole grid.
+// Three phases: scans over the sequences (what each gives back, needs and gets: prefix sums
+// in the sequences' order make the outcome independent of the schedule); the returned pages
+// onto the free list; the taken pages into the table and the rows' slots.  The second needs
+// little of the first and runs beside it, in blocks that sum up the returned pages by
+// themselves (as a launch of its own it took a call on 4096 sequences from 22 to 27 us); the
+// third looks its sequence up in the prefix sums, so that one long prompt is spread over the
+// whole grid.
 //
 // Everything here is a chain of load latencies: the scan keeps its sequences in registers
 // from one load, a warp finds its sequence with 32 probes at a time (three steps for 16384
@@ -24,17 +26,27 @@ struct AdvancePlan {
     long long* back;   // [B + 1] pages given back before each sequence
     long long* take;   // [B + 1] pages taken before each sequence
     long long* count;  // [0] pages of the free list before, [1] with the returned ones
+    // the outputs that may be inputs: themselves, or a copy until all have read the inputs
+    int32_t* lens;
+    int32_t* held;
+    int32_t* free_count;
 };
 
-static AdvancePlan plan_of(void* ws, int B) {
+static AdvancePlan plan_of(const AdvanceParams& p, void* ws, bool direct) {
+    const int B = p.B;
     AdvancePlan w;
     w.back = static_cast<long long*>(ws);
     w.take = w.back + (B + 2) / 2 * 2;  // (16-byte boundaries)
     w.count = w.take + (B + 2) / 2 * 2;
+    int32_t* copies = reinterpret_cast<int32_t*>(w.count + 2);
+    w.lens = direct ? p.lens_out : copies;
+    w.held = direct ? p.held_out : copies + (B + 3) / 4 * 4;
+    w.free_count = direct ? p.free_count_out : copies + 2 * ((B + 3) / 4 * 4);
     return w;
 }
 size_t advance_workspace_bytes(int B) {
-    return ((2 * (static_cast<size_t>(B) + 2) + 2) * sizeof(long long) + 255) & ~size_t(255);
+    return ((2 * (static_cast<size_t>(B) + 2) + 2) * sizeof(long long) +
+            (2 * (static_cast<size_t>(B) + 3) + 4) * sizeof(int32_t) + 255) & ~size_t(255);
 }
 
 // What a call finds of one sequence.  Lengths saturate at 2^31 - 1: beyond every table.
@@ -87,7 +99,7 @@ __device__ __forceinline__ Pair block_scan(Pair v, Pair* total, Pair* s_warp) {
 
 // N entries from b on of an array of n, four at a time where the arrays allow it (one at a
 // time each of a warp's stores writes parts of 16 sectors: a call on 4096 sequences took 31.3 us
-// instead of 27.8).
+// instead of 27.8, then).
 template <int N>
 __device__ __forceinline__ void adv_load(int (&v)[N], const int32_t* a, int b, int n, bool vec, int none) {
     if (N % 4 == 0 && vec && b + N <= n) {
@@ -137,7 +149,7 @@ __device__ __forceinline__ void scan_phase(const AdvanceParams& p, const Advance
     const bool vec = ((reinterpret_cast<uintptr_t>(p.ended) | reinterpret_cast<uintptr_t>(p.held) |
                        reinterpret_cast<uintptr_t>(p.accepted) | reinterpret_cast<uintptr_t>(p.lens) |
                        reinterpret_cast<uintptr_t>(p.grow) | reinterpret_cast<uintptr_t>(p.row_start) |
-                       reinterpret_cast<uintptr_t>(p.lens_out) | reinterpret_cast<uintptr_t>(p.held_out) |
+                       reinterpret_cast<uintptr_t>(w.lens) | reinterpret_cast<uintptr_t>(w.held) |
                        reinterpret_cast<uintptr_t>(p.seq_lens)) & 15u) == 0;
     AdvSeq s[N];
     auto group = [&](int g) {
@@ -215,8 +227,8 @@ __device__ __forceinline__ void scan_phase(const AdvanceParams& p, const Advance
         adv_store(w.back, back, b, p.B);
         adv_store(w.take, take, b, p.B);
         adv_store(p.row_start, start, b, p.B, vec);
-        adv_store(p.lens_out, lens, b, p.B, vec);
-        adv_store(p.held_out, held, b, p.B, vec);
+        adv_store(w.lens, lens, b, p.B, vec);
+        adv_store(w.held, held, b, p.B, vec);
         adv_store(p.seq_lens, seq_lens, b, p.B, vec);
     }
     if (threadIdx.x == 0) {
@@ -225,10 +237,56 @@ __device__ __forceinline__ void scan_phase(const AdvanceParams& p, const Advance
         w.count[0] = stock;
         w.count[1] = count;
         p.row_start[p.B] = static_cast<int32_t>(min(total.b, 2147483647LL));
-        p.free_count_out[0] = static_cast<int32_t>(count - total.a);
+        w.free_count[0] = static_cast<int32_t>(count - total.a);
         if (p.slots && total.b > p.rows_max) short_of = true;
     }
     if (short_of) atomicOr(p.status, kStatusNoRoom);
+}
+
+// The returned pages onto the free list, by `blocks` blocks of kAdvThreads next to the one that
+// scans: each sums up what comes before its sequences by itself, and takes every blocks-th
+// eight of them, a warp a sequence.
+template <int N, int G>
+__device__ __forceinline__ void push_beside(const AdvanceParams& p, int block, int blocks) {
+    __shared__ Pair s_warp[32];
+    const int b0 = threadIdx.x * (N * G), lane = threadIdx.x & 31;
+    const long long stock = max(0, min(p.num_pages, p.free_count[0]));
+    const bool vec = ((reinterpret_cast<uintptr_t>(p.ended) | reinterpret_cast<uintptr_t>(p.held)) & 15u) == 0;
+    int back[N];
+    auto group = [&](int g) {
+        int ended[N];
+        adv_load(ended, p.ended, b0 + g * N, p.B, vec, 0);
+        adv_load(back, p.held, b0 + g * N, p.B, vec, 0);
+#pragma unroll
+        for (int k = 0; k < N; ++k) back[k] = ended[k] != 0 ? max(0, min(p.max_blocks, back[k])) : 0;
+    };
+    Pair sum{0, 0}, total;
+#pragma unroll 1
+    for (int g = 0; g < G; ++g) {
+        group(g);
+#pragma unroll
+        for (int k = 0; k < N; ++k) sum.a += back[k];
+    }
+    Pair at = block_scan(sum, &total, s_warp);
+#pragma unroll 1
+    for (int g = 0; g < G; ++g) {
+        if (G > 1) group(g);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int b = b0 + g * N + k;
+            unsigned who = __ballot_sync(0xffffffffu, back[k] > 0 && (b >> 3) % blocks == block);
+            while (who) {
+                const int l = __ffs(who) - 1;
+                who &= who - 1;
+                const int n = __shfl_sync(0xffffffffu, back[k], l), bl = __shfl_sync(0xffffffffu, b, l);
+                const long long to = stock + __shfl_sync(0xffffffffu, at.a, l);
+                const int32_t* row = p.table + bl * p.table_stride;
+                for (int i = lane; i < n; i += 32)
+                    if (to + i < p.num_pages) p.free_list[to + i] = row[i];
+            }
+            at.a += back[k];
+        }
+    }
 }
 
 // The sequence of entry i, the same in all lanes: the last with start[b] <= i.
@@ -272,7 +330,7 @@ __device__ __forceinline__ void push_phase(const AdvanceParams& p, const Advance
 
 // columns of sequence b that held pages before
 __device__ __forceinline__ int adv_kept(const AdvanceParams& p, const AdvancePlan& w, int b) {
-    return p.held_out[b] - static_cast<int>(w.take[b + 1] - w.take[b]);
+    return w.held[b] - static_cast<int>(w.take[b + 1] - w.take[b]);
 }
 __device__ __forceinline__ void take_phase(const AdvanceParams& p, const AdvancePlan& w,
                                            long long warp, long long warps) {
@@ -289,7 +347,7 @@ __device__ __forceinline__ void slot_phase(const AdvanceParams& p, const Advance
     const long long rows = min(static_cast<long long>(p.row_start[p.B]), p.rows_max);
     bool bad = false;
     each_entry(p.row_start, p.B, rows, warp, warps, [&](int b, long long i) {
-        const long long pos = p.lens_out[b] + (i - p.row_start[b]);
+        const long long pos = w.lens[b] + (i - p.row_start[b]);
         const int col = static_cast<int>(pos >> p.page_shift), k = adv_kept(p, w, b);
         const int page = col < k ? p.table[b * p.table_stride + col]
                                  : p.free_list[top - (w.take[b] + col - k)];
@@ -305,6 +363,7 @@ __global__ void __launch_bounds__(kAdvThreads) advance_kernel(const AdvanceParam
                                                               const AdvancePlan w, int all) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x > 0) return push_beside<N, G>(p, blockIdx.x - 1, gridDim.x - 1);
     scan_phase<N, G>(p, w);
     if (!all) return;
     __syncthreads();
@@ -315,8 +374,8 @@ __global__ void __launch_bounds__(kAdvThreads) advance_kernel(const AdvanceParam
     slot_phase(p, w, warp, kAdvThreads / 32);
 }
 
-// FILL: the first `takers` blocks fill the table, the others the slots.
-template <bool FILL>
+// The first `takers` blocks fill the table and leave the outputs that may be inputs, the others
+// fill the slots.
 __global__ void __launch_bounds__(kFillThreads) advance_fill_kernel(const AdvanceParams p,
                                                                     const AdvancePlan w, int takers) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -324,17 +383,21 @@ __global__ void __launch_bounds__(kFillThreads) advance_fill_kernel(const Advanc
     const int blocks = static_cast<int>(gridDim.x), block = static_cast<int>(blockIdx.x);
     const int in = threadIdx.x >> 5;
     constexpr int W = kFillThreads / 32;
-    if (!FILL) push_phase(p, w, block * W + in, blocks * W);
-    else if (block < takers) take_phase(p, w, block * W + in, takers * W);
-    else slot_phase(p, w, (block - takers) * W + in, (blocks - takers) * W);
+    if (block >= takers) return slot_phase(p, w, (block - takers) * W + in, (blocks - takers) * W);
+    for (int i = block * kFillThreads + threadIdx.x; i < p.B; i += takers * kFillThreads) {
+        p.lens_out[i] = w.lens[i];
+        p.held_out[i] = w.held[i];
+    }
+    if (block == 0 && threadIdx.x == 0) p.free_count_out[0] = w.free_count[0];
+    take_phase(p, w, block * W + in, takers * W);
 }
 
 cudaError_t launch_advance(const AdvanceParams& p, void* ws, int sms, cudaStream_t s) {
-    const AdvancePlan w = plan_of(ws, p.B);
     const long long rows = p.slots ? p.rows_max : 0;
     const int all = static_cast<long long>(p.B) * p.max_blocks <= kOneBlockTable && rows <= kOneBlockSlots;
+    const AdvancePlan w = plan_of(p, ws, all);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(1);
+    cfg.gridDim = dim3(all || !p.ended ? 1 : sms);
     cfg.blockDim = dim3(kAdvThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -347,15 +410,10 @@ cudaError_t launch_advance(const AdvanceParams& p, void* ws, int sms, cudaStream
                                              : cudaLaunchKernelEx(&cfg, advance_kernel<4, 4>, p, w, all);
     if (e != cudaSuccess || all) return e;
     cfg.blockDim = dim3(kFillThreads);
-    if (p.ended) {
-        cfg.gridDim = dim3(2 * sms);
-        e = cudaLaunchKernelEx(&cfg, advance_fill_kernel<false>, p, w, 0);
-        if (e != cudaSuccess) return e;
-    }
     // a block takes 512 slots at a time; how many pages move only the device knows
     const long long blocks = (rows + 511) / 512;
     cfg.gridDim = dim3(static_cast<unsigned>(sms + (blocks < 6LL * sms ? blocks : 6LL * sms)));
-    return cudaLaunchKernelEx(&cfg, advance_fill_kernel<true>, p, w, sms);
+    return cudaLaunchKernelEx(&cfg, advance_fill_kernel, p, w, sms);
 }
 
 }  // namespace vw4
