@@ -5,7 +5,7 @@
 // in the sequences' order make the outcome independent of the schedule); the returned pages
 // onto the free list; the taken pages into the table and the rows' slots.  The second needs
 // little of the first and runs beside it, in blocks that sum up the returned pages by
-// themselves (as a launch of its own it took a call on 4096 sequences from 22 to 27 us); the
+// themselves (as a launch of its own it took a call on 4096 sequences from 18 to 27 us); the
 // third looks its sequence up in the prefix sums, so that one long prompt is spread over the
 // whole grid.
 //

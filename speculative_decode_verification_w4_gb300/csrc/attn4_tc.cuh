@@ -13,7 +13,9 @@
 // What bounds it: the way of a tile from its scores to its weights in the softmax warps, a
 // chain of latencies of about 1 us under the load of the other warps (16384 keys' and as many
 // values' elements; their conversion takes 0.5 us beside it, the products 0.5, the bytes from
-// HBM 0.4).  Without conversions and exponentials a tile still takes 1.1 us of its 1.4.  So
+// HBM 0.4).  The exponentials are 0.5 of it: tensor memory's lanes bind a block of up to 64 rows
+// to two of the four sub-cores.  Without conversions and exponentials a tile still takes 1.1 us
+// of its 1.4; a second issuing thread, for the other product, changes nothing.  So
 // the time hardly grows with the rows: 32 sequences of up to 32768 tokens, 4 key heads of
 // size 128 (219 MB), are 112 us at 36 rows, 117 at 64 and 150 at 128; head size 256 182 / 192 /
 // 260.  Tried and slower: weights formed at once against the lagging reference (252 us

@@ -20,8 +20,8 @@
 // overfill the list (rows in ascending order) are read again that way.
 //
 // The bytes bound it (4 or 2 a logit) and, at 16 instructions a logit, the issue slots: 256 x 9
-// rows of 151936, of which 60 % are read, with five alternatives, take 154 us in fp32 (124 at the
-// copy rate; without alternatives 147) and 135 in bf16.  A row is split over blocks where the rows
+// rows of 151936, of which 60 % are read, with five alternatives, take 156 us in fp32 (124 at the
+// copy rate; without alternatives 146) and 137 in bf16.  A row is split over blocks where the rows
 // alone would leave SMs idle (one sequence's 8 rows of 262144 with 20 alternatives: 14 us, of
 // which the join of 64 parts a row is 3), and a second kernel joins the parts in order.
 #include <cuda_bf16.h>
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kLpThreads, 4)
 
     // The next chunk is on its way while this one is worked on.  (Without that, five blocks an SM
     // cover each other's loads: 79 us instead of 93 for 80 x 9 rows of 151936, but 153 or 166 from
-    // run to run for 256 x 9 instead of 154, and 143 instead of 137 in bf16.)
+    // run to run for 256 x 9 instead of 156, and 143 instead of 137 in bf16.)
     uint4 next[N];
     const int end = shift + p.V;
     auto fetch = [&](int c) {
