@@ -5,9 +5,13 @@
 //   Z = sum 2^(c (x - m)),   W = sum 2^(c (x - m)) c (x - m)
 // and when m grows, by d = c (m' - m): W <- (W - d Z) 2^-d, Z <- Z 2^-d.  Then
 //   lse = scale m + ln Z,   entropy = ln 2 (log2 Z - W / Z).
-// (The difference first: c x of the type's lowest value, a usual mask, would overflow.)
+// The difference first: it is exact next to m, so that the error of an exponent goes with
+// the entry's distance from m and not with the logits' size.  (A fused c x - c m is off by the
+// rounding of c m, the same for all of a thread's entries and another for the next thread's:
+// 4e-4 of ln Z at a logit of 10000, 12.7 where a row is masked with -1e9.)
 // Each thread keeps its own m (moved where an entry exceeds it by 2^8), Z and W; they meet
-// in a fixed order.
+// in a fixed order.  Z holds an entry of weight 1, and one of 2^-8 of any that exceeds m: no log
+// probability comes out above 0.
 //
 // Alternatives: the block keeps the `top` largest entries as 64-bit keys (value, then lower
 // index first) and lists those above the least of them; every few chunks of 4096 entries
@@ -260,22 +264,13 @@ __global__ void __launch_bounds__(kLpThreads, 4)
 #pragma unroll
             for (int k = 0; k < kLpEach; ++k) s.z += f[k] == INFINITY ? 1.f : 0.f;
         } else {
-            const float m = s.m == -INFINITY ? 0.f : s.m, mc = m * c2;
+            const float m = s.m == -INFINITY ? 0.f : s.m;
             float z = 0.f, w = 0.f;
-            if (fabsf(mc) < 1e30f) {  // (c x of the type's lowest value overflows to 2^-infinity)
 #pragma unroll
-                for (int k = 0; k < kLpEach; ++k) {
-                    const float d = fmaxf(fmaf(f[k], c2, -mc), -kLpFar), e = ex2(d);
-                    z += e;
-                    w = fmaf(e, d, w);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < kLpEach; ++k) {
-                    const float d = fmaxf((f[k] - m) * c2, -kLpFar), e = ex2(d);
-                    z += e;
-                    w = fmaf(e, d, w);
-                }
+            for (int k = 0; k < kLpEach; ++k) {
+                const float d = fmaxf((f[k] - m) * c2, -kLpFar), e = ex2(d);
+                z += e;
+                w = fmaf(e, d, w);
             }
             s.z += z;
             s.w += w;
