@@ -845,7 +845,7 @@ VW4_API vw4_status advance_pages(const vw4_advance* a, void* workspace_dev, size
  * logprob_dev, entropy_dev, lse_dev  fp32 [B*R]; rank_dev int32 [B*R]; each may
  *             be NULL.
  * top_ids_dev, top_logprobs_dev  int32 / fp32 [B*R][top] (NULL when top is 0).
- * B 1..16384, R 1..16, 1 <= V <= 2^24, top 0..32, scale > 0 and finite.
+ * B 1..16384, R 1..16, 1 <= V <= 2^24, top 0..32, 0 < scale <= 2^126.
  * Precision: sums in fp32, over parts of a row and then over the parts, of
  * exponentials of differences x_v - m, whatever the logits' size: lse and the log
  * probabilities are off by at most 2^-16 and 2^-23 of themselves for rows of up to

@@ -321,7 +321,8 @@ VW4_API vw4_status token_logprobs(const vw4_logprobs* a, void* workspace_dev, si
         a->V > (1 << 24) || a->ldx < a->V)
         return VW4_ERR_INVALID_ARG;
     if (a->top < 0 || a->top > kMaxTop || (a->x_bf16 != 0 && a->x_bf16 != 1)) return VW4_ERR_INVALID_ARG;
-    if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return VW4_ERR_INVALID_ARG;
+    // (beyond 2^126, scale log2(e) is infinite)
+    if (!(a->scale > 0.f && a->scale <= 0x1p126f)) return VW4_ERR_INVALID_ARG;
     if ((a->logprob_dev || a->rank_dev) && !a->tokens_dev) return VW4_ERR_INVALID_ARG;
     if (a->top > 0 ? !a->top_ids_dev || !a->top_logprobs_dev : a->top_ids_dev || a->top_logprobs_dev)
         return VW4_ERR_INVALID_ARG;
