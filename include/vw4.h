@@ -678,10 +678,10 @@ typedef struct vw4_kv4_cache {
  * Queries as verify_rope_append.  A key or value y of a head of scale g is
  * stored as t = y / g (0 where g is 0), at most 2688 in magnitude; the 16
  * values of a block get the scale s = e4m3(min(max |t| / 6, 448)) and the codes
- * e2m1(t / s), at most 6 in magnitude (0 where s is 0), both nearest, ties to
- * even.  Scale and codes are those of the 64-bit formula: values so near a
- * border that 32 bits cannot tell are computed again.  A NaN makes its block's
- * scale, and so the block, NaN.
+ * e2m1(t / s), at most 6 in magnitude (0 where s or t is 0, else of t's sign),
+ * both nearest, ties to even.  Scale and codes are those of the 64-bit formula:
+ * values so near a border that 32 bits cannot tell are computed again.  A NaN
+ * makes its block's scale, and so the block, NaN.
  *
  * Arguments and errors as verify_rope_append.
  */

@@ -184,7 +184,7 @@ __device__ __noinline__ uint2 kv4_special(const AppendParams& p, const X* x, con
             if (fabs(t[k]) < mid || (fabs(t[k]) == mid && !(c & 1u))) break;
             ++c;
         }
-        w |= (c | (t[k] < 0.0 ? 8u : 0u)) << (4 * k);
+        w |= (c | (sb && t[k] < 0.0 ? 8u : 0u)) << (4 * k);
     }
     return make_uint2(w, bad ? 0x7Fu : sb);
 }
@@ -266,6 +266,7 @@ __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, con
             unsure |= (a ^ c) << (4 * k);
             w |= a << (4 * k);
         }
+        if (sb == 0u) w = unsure = 0u;
         if (__any_sync(0xffffffffu, unsure != 0u)) {
             if (offs && !have_f) f = kv4_norm<D, X>(p, x);
 #pragma unroll 1
@@ -283,7 +284,9 @@ __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, con
                     if (low || (tie && !(c & 1u))) break;
                     ++c;
                 }
-                const bool minus = offs ? (v64 < 0.0) != (g < 0.f) : (v < 0.f) != (g < 0.f);
+                // (a zero has no sign)
+                const bool minus = offs ? v64 != 0.0 && (v64 < 0.0) != (g < 0.f)
+                                        : v != 0.f && (v < 0.f) != (g < 0.f);
                 w = (w & ~(15u << (4 * k))) | (c | (minus ? 8u : 0u)) << (4 * k);
             }
         }
