@@ -226,7 +226,8 @@ __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, con
         sb = r.y;
     } else {
         const float e = fmaf(off, ar, m * ar * kDivError);
-        sb = e4m3_byte((m * ar - e) * (1.f / 6.f) * (1.f - kDivError));
+        // (the bound may be above the block's values: those of a key's partners go into it)
+        sb = e4m3_byte(fmaxf(0.f, m * ar - e) * (1.f / 6.f) * (1.f - kDivError));
         const uint32_t sb1 = e4m3_byte((m * ar + e) * (1.f / 6.f) * (1.f + kDivError));
         double f = 0.0;
         bool have_f = false;

@@ -71,6 +71,24 @@ def heads(B, R, Hkv, D, seed=0, gain=1.0):
     return torch.randn(B * R, 3 * Hkv, D, generator=g) * gain
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("small,partner", [(0.0, 1.0), (0.0, 200.0), (1e-4, 200.0), (-1e-4, 200.0), (1e-7, 1.0),
+                                           (0.0, 1e6)])
+def test_blocks_far_below_their_partners(small, partner, adjacent, D):
+    """At position 0, where nothing turns, and behind it: a block of zeros or next to them whose
+    partners in the rotation are large, so that the bound of a key's error exceeds the block."""
+    Hkv, R = 2, 3
+    x = heads(2, R, Hkv, D, gain=1e-3)
+    k = x[:, Hkv:2 * Hkv]
+    if adjacent:
+        k[..., 0::2], k[..., 1::2] = small, partner
+    else:
+        k[..., :D // 2], k[..., D // 2:] = small, partner
+    x[:, Hkv + 1] = x[:, Hkv + 1].flip(-1)
+    run(x.flatten(1), [R, 40], R, Hkv, D, [1 / 32, -1 / 32], rot=D, adjacent=adjacent)
+
+
 @pytest.mark.parametrize("rot,norm", [(0, False), (64, False), (64, True), (6, False)])
 @pytest.mark.parametrize("scales", [[1.0, -1.0], [0.03, -0.07], [0.0, -0.0]])
 def test_zeros_of_either_sign(scales, rot, norm):
