@@ -143,8 +143,9 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
     return c < 4 ? 0.5f * static_cast<float>(c) : (c & 1 ? 1.5f : 1.f) * (c < 6 ? 2.f : 4.f);
 }
 
-// What the quick way below does not take, all of it by quotients: infinities, NaN, head scales
-// of 0 or so small that their reciprocal overflows.  (Codes, block scale) of the lane.
+// What the quick way below does not take, all of it by quotients: infinities, NaN, heads whose
+// squares overflow or vanish, head scales of 0 or so small that their reciprocal overflows.
+// (Codes, block scale) of the lane.
 template <int D, class X>
 __device__ __noinline__ uint2 kv4_special(const AppendParams& p, const X* x, const float* head,
                                           bool is_k, int pos, float g) {
@@ -156,7 +157,7 @@ __device__ __noinline__ uint2 kv4_special(const AppendParams& p, const X* x, con
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         const int d = lane * N + k;
-        const double y = is_k && isfinite(head[d]) ? kv4_key<D, X>(p, x, d, f, pos) : head[d];
+        const double y = is_k ? kv4_key<D, X>(p, x, d, f, pos) : head[d];
         t[k] = g == 0.f ? (isnan(y) ? y : 0.0) : y / static_cast<double>(g);
         nan |= isnan(t[k]);
         t[k] = fmin(fmax(t[k], -2688.0), 2688.0);
@@ -220,7 +221,7 @@ __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, con
     }
     const float m = __uint_as_float(largest);
     uint32_t w = 0, sb;
-    if (__any_sync(0xffffffffu, !(ar > 1e-30f && ar < 1e30f && m < 1e30f))) {
+    if (__any_sync(0xffffffffu, !(ar > 1e-30f && ar < 1e30f && m < 1e30f && off < 1e30f))) {
         const uint2 r = kv4_special<D, X>(p, x, head, is_k, pos, g);
         w = r.x;
         sb = r.y;
@@ -372,6 +373,7 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int first, i
         const bool is_q = PART == kHeadsQ || (PART == kHeadsAny && h < p.Hq);
         const bool is_k = !is_q && h < p.Hq + p.Hkv;
         float off[KV4 ? 2 * U : 1];  // 4-bit keys: what a value may be off by
+        bool wide = false;           // and whether 32 bits say nothing of it
         if (KV4) {
 #pragma unroll
             for (int k = 0; k < 2 * U; ++k) off[KV4 ? k : 0] = 0.f;
@@ -384,7 +386,7 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int first, i
                 for (int k = 0; k < 2 * U; ++k) ss = fmaf(v[k], v[k], ss);
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const float f = rsqrtf(ss * (1.f / D) + p.eps);
+                const float mean = ss * (1.f / D) + p.eps, f = rsqrtf(mean);
                 __align__(16) float g[2 * U];
                 load_unit<U>(w + d0, g);
                 load_unit<U>(w + d1, g + U);
@@ -393,6 +395,8 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int first, i
                 if (KV4 && is_k) {
 #pragma unroll
                     for (int k = 0; k < 2 * U; ++k) off[KV4 ? k : 0] = fabsf(v[k]);
+                    // squares that leave the range of 32 bits: the head is taken in 64
+                    wide = !(mean > 1e-30f && mean < 1e30f);
                 }
             }
             if (split) {
@@ -444,7 +448,7 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int first, i
                 __syncwarp();  // the last head's reads are done
                 float* offs = s_off[OFF ? warp : 0];
 #pragma unroll
-                for (int k = 0; k < 2 * U; ++k) off[KV4 ? k : 0] *= kValueError;
+                for (int k = 0; k < 2 * U; ++k) off[KV4 ? k : 0] = wide ? INFINITY : off[KV4 ? k : 0] * kValueError;
                 put_unit<U>(s_head[warp] + d0, v);
                 put_unit<U>(s_head[warp] + d1, v + U);
                 if (is_k) {

@@ -101,3 +101,28 @@ def test_zeros_of_either_sign(scales, rot, norm):
     x[3] *= 1e-8
     w = torch.linspace(0.5, 2.0, D) if norm else None
     run(x.flatten(1), [R], R, Hkv, D, scales, rot=rot, k_norm=w)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rot,adjacent", [(0, False), (64, False), (64, True), (10, False)])
+@pytest.mark.parametrize("gain,eps", [(3e18, 1e-6), (1e19, 1e-6), (1e24, 1e-6), (1e37, 1e-6), (1e-19, 0.0),
+                                      (1e-22, 0.0), (1e-30, 0.0), (1e-19, 1e-38), (0.0, 0.0)])
+def test_sums_of_squares_beyond_32_bits(gain, eps, rot, adjacent, D):
+    """Heads whose norm is an ordinary number in 64 bits alone."""
+    Hkv, R = 2, 2
+    x = heads(2, R, Hkv, D, 2)
+    x[:, Hkv:2 * Hkv] *= gain
+    run(x.flatten(1), [R, 1000], R, Hkv, D, [0.02, -0.02], rot=rot, adjacent=adjacent,
+        k_norm=torch.linspace(-1.0, 2.0, D), eps=eps)
+
+
+@pytest.mark.parametrize("rot,norm", [(0, False), (64, False), (64, True), (32, True)])
+def test_not_finite(rot, norm):
+    """NaN and infinities in keys and values, beside partners and heads that are finite."""
+    D, Hkv, R = 128, 2, 6
+    x = heads(1, R, Hkv, D, 3)
+    for r, v in enumerate((float("nan"), float("inf"), float("-inf"))):
+        x[2 * r, :, 3] = v
+        x[2 * r + 1, :, 100] = v
+    w = torch.linspace(0.5, 2.0, D) if norm else None
+    run(x.flatten(1), [40], R, Hkv, D, [0.5, -0.25], rot=rot, k_norm=w)
