@@ -144,7 +144,8 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
 }
 
 // What the quick way below does not take, all of it by quotients: infinities, NaN, heads whose
-// squares overflow or vanish, head scales of 0 or so small that their reciprocal overflows.
+// squares overflow or vanish, head scales of 0 or so small that their reciprocal or a quotient
+// overflows.
 // (Codes, block scale) of the lane.
 template <int D, class X>
 __device__ __noinline__ uint2 kv4_special(const AppendParams& p, const X* x, const float* head,
@@ -221,7 +222,8 @@ __device__ __forceinline__ void store_kv4(const AppendParams& p, const X* x, con
     }
     const float m = __uint_as_float(largest);
     uint32_t w = 0, sb;
-    if (__any_sync(0xffffffffu, !(ar > 1e-30f && ar < 1e30f && m < 1e30f && off < 1e30f))) {
+    // (quotients as well: what follows has no room for an infinity)
+    if (__any_sync(0xffffffffu, !(ar > 1e-30f && ar < 1e30f && m + off < 1e30f && (m + off) * ar < 1e30f))) {
         const uint2 r = kv4_special<D, X>(p, x, head, is_k, pos, g);
         w = r.x;
         sb = r.y;

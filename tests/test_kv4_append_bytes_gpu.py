@@ -103,6 +103,19 @@ def test_zeros_of_either_sign(scales, rot, norm):
     run(x.flatten(1), [R], R, Hkv, D, scales, rot=rot, k_norm=w)
 
 
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("rot,norm", [(0, False), (64, False), (64, True)])
+@pytest.mark.parametrize("gain,g", [(1e19, 1e-20), (1e10, 1e-29), (1.0, 3e-30), (1e25, 1e-10), (1e29, 1e-29),
+                                    (1e-20, 1e-25), (1e-25, 1e20)])
+def test_quotients_beyond_32_bits(gain, g, rot, norm, D):
+    """Values and head scales that are ordinary numbers, and quotients that are not."""
+    Hkv, R = 2, 2
+    x = heads(2, R, Hkv, D, 1, gain)
+    x[0, Hkv, :16] = 0.0
+    w = torch.linspace(0.5, 2.0, D) if norm else None
+    run(x.flatten(1), [R, 77], R, Hkv, D, [g, -g], rot=rot, k_norm=w)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("rot,adjacent", [(0, False), (64, False), (64, True), (10, False)])
 @pytest.mark.parametrize("gain,eps", [(3e18, 1e-6), (1e19, 1e-6), (1e24, 1e-6), (1e37, 1e-6), (1e-19, 0.0),
