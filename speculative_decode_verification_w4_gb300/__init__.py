@@ -300,7 +300,8 @@ class Workspace:
     """A growable device scratch buffer (256-byte aligned torch allocation, not
     initialized: no call needs that).  It serves one call after another on one
     stream; calls that may overlap need a workspace each, and so does a captured
-    call that is replayed (a larger call replaces the buffer)."""
+    call that is replayed (a larger call replaces the buffer).  A captured call
+    without a workspace has scratch of its graph's memory."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
@@ -319,10 +320,24 @@ class Workspace:
         return self.buf
 
 
-_default_ws = {}  # one for each device, thread and stream
+_default_ws = {}  # one for each device, thread and stream; calls that are captured use none
+
+
+def _capturing(device, stream):
+    """Whether a call on `stream` (None: the current one) is being captured into a graph."""
+    if device.type != "cuda":
+        return False
+    if stream is None or stream.cuda_stream == _handle(None, device):
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def _workspace(ws, nbytes, device, stream):
+    if ws is None and _capturing(device, stream):
+        # scratch of the graph's own memory: a cached buffer would be replaced by a larger call's,
+        # and freed, while the graph still names it
+        return _empty((max(nbytes, 256),), torch.uint8, device, stream)
     if ws is None:
         key = (device.index, threading.get_ident(), _handle(stream, device))
         ws = _default_ws.get(key)
