@@ -99,6 +99,7 @@ class VerifyLoop:
             self.mask_row = torch.zeros((B, self.R), dtype=torch.int32, device="cuda")
         self.steps = 0
         self.logprobs = None  # of the last step's tokens
+        self.graphs = None
         # the prompts, but for their last tokens, which the first step verifies
         self.cached = torch.zeros(B, dtype=torch.int32, device="cuda")
         self.seq_lens = torch.zeros(B, dtype=torch.int32, device="cuda")
@@ -154,37 +155,82 @@ class VerifyLoop:
         return logits, bmax
 
     def step(self):
-        """-> tokens [B, Kd + 1] and how many of them are committed [B]."""
-        out = self.commit(*self.draft())
+        """-> tokens [B, Kd + 1] and how many of them are committed [B].  After capture(): the
+        same from two graphs, in tensors that the next step overwrites."""
+        drafts, draft_logits = self.draft()
+        if self.graphs is None:
+            out = self.commit(drafts, draft_logits)
+        else:
+            before, after, rows, scored, kept, logprobs = self.graphs
+            rows[0].copy_(drafts)
+            if draft_logits is not None:
+                rows[1].copy_(draft_logits)
+            before.replay()
+            # the accept itself is launched: a graph would hold the offset of its random numbers
+            for to, made in zip(kept, self.accept(*rows, *scored)):
+                to.copy_(made)
+            after.replay()
+            out, self.logprobs = kept, logprobs
         self.steps += 1
         return out
 
     def commit(self, drafts, draft_logits):
-        """The step after its drafts, all of it on the device and in place: it can be captured."""
+        """The step after its drafts, on the device and in place.  (Captured whole, every replay
+        would draw the random numbers of the captured step's offset: see capture.)"""
+        scored = self.score(drafts, draft_logits)
+        tokens, n = self.accept(drafts, draft_logits, *scored)
+        self.logprobs = self.keep(scored[0], tokens, n)
+        return tokens, n
+
+    def score(self, drafts, draft_logits):
+        """-> the verify rows' logits and block maxima, and the drafts' block maxima."""
         logits, bmax = self.verify(drafts)
         draft_bmax = None
         if self.Kd:  # the draft's logits as they are; the call fills in their block maxima
             draft_bmax = torch.empty(self.B, self.Kd, bmax.shape[2], device="cuda")
             vw4.process_logits(draft_logits, drafts[:, 1:].contiguous(), out=draft_logits,
                                block_max=draft_bmax)
-        tokens, n = vw4.accept_rejection_blockmax(logits, bmax, draft_logits, draft_bmax, drafts,
-                                                  temperature=1.0, top_p=1.0, seed=7,
-                                                  offset=self.steps)
-        self.logprobs = vw4.token_logprobs(logits, tokens, length=n, top=4)
+        return logits, bmax, draft_bmax
+
+    def accept(self, drafts, draft_logits, logits, bmax, draft_bmax):
+        return vw4.accept_rejection_blockmax(logits, bmax, draft_logits, draft_bmax, drafts,
+                                             temperature=1.0, top_p=1.0, seed=7, offset=self.steps)
+
+    def keep(self, logits, tokens, n):
+        """The committed tokens into the history, pages for what follows -> their log probabilities."""
+        logprobs = vw4.token_logprobs(logits, tokens, length=n, top=4)
         at = self.length.long()[:, None] + torch.arange(self.R, device="cuda")
         keep = torch.arange(self.R, device="cuda") < n[:, None]
         old = self.history.gather(1, at)
         self.history.scatter_(1, at, torch.where(keep, tokens, old))
         self.length += n
         self.advance(accepted=n)
-        return tokens, n
+        return logprobs
+
+    def capture(self):
+        """From now on (after a first step) a step replays what lies before and behind its accept
+        from graphs.  The accept takes its random numbers' offset from the host, so that it stays
+        a launch of its own."""
+        drafts, draft_logits = self.draft()
+        rows = drafts.clone(), None if draft_logits is None else draft_logits.clone()
+        kept = (torch.zeros(self.B, self.R, dtype=torch.int32, device="cuda"),
+                torch.zeros(self.B, dtype=torch.int32, device="cuda"))
+        torch.cuda.synchronize()
+        before, after = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(before):
+            scored = self.score(*rows)
+        with torch.cuda.graph(after):
+            logprobs = self.keep(scored[0], *kept)
+        self.graphs = before, after, rows, scored, kept, logprobs
 
 
 def main():
     loop = VerifyLoop([[5, 17, 300, 42], [9, 9, 1234]], kv="nvfp4",
                       allowed=torch.arange(0, 4000, 2))
-    for _ in range(8):
+    for k in range(8):
         tokens, n = loop.step()
+        if k == 0:
+            loop.capture()
         print("committed", [tokens[b, :n[b]].tolist() for b in range(loop.B)], "of log probability",
               [[round(x, 2) for x in loop.logprobs.logprob[b, :n[b]].tolist()] for b in range(loop.B)])
     if vw4.vw4_get_device_status():
