@@ -710,7 +710,8 @@ VW4_API vw4_status verify_rope_append_kv4(const vw4_append_kv4* a, void* stream)
  * f16 under an exact power of two per row (exact down to 2^-31 of the row's
  * largest magnitude); scores, softmax statistics and sums in fp32; the weights
  * enter the value product as f16, off by at most 2^-11 of themselves or 2^-34
- * of the largest.
+ * of the largest (2^-25 where scores are near the largest that are allowed:
+ * 2^26 in magnitude).
  * Errors as verify_attn; the workspace is that of
  * vw4_workspace_bytes(VW4_OP_ATTN_KV4, B, R * (Hq / Hkv), D).
  */

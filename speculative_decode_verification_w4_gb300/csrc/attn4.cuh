@@ -26,7 +26,9 @@
 // The reference that the weights use is the running maximum, followed lazily: only where a
 // score exceeds it by 2^6 do the warps meet for the true maximum, rescale and form P again
 // (the first tile of an item; rarely later).  Weights are at most 2^15 in f16, and reach
-// down to 2^-33 of the largest (f16 ends at 2^-24).
+// down to 2^-33 of the largest (f16 ends at 2^-24).  What a weight's exponent takes from its score
+// is the reference less 9, rounded up once; rescaling and the join take the same number, so that
+// its rounding is a common factor of a row and no weight leaves f16, however large the scores.
 #pragma once
 #include "attn.cuh"
 
@@ -57,6 +59,11 @@ __host__ __device__ constexpr int attn4_places(int D, int nt, bool large) {
 }
 
 #ifdef __CUDACC__
+// What the exponents take from scores whose largest is m under the factor c2 (-infinity: none).
+__device__ __forceinline__ float attn4_ref(float m, float c2) {
+    return m == -INFINITY ? -INFINITY : __fmaf_ru(m, c2, -kTail4);
+}
+
 template <int D, int NT, bool LARGE>
 struct Attn4Shape {
     static constexpr int kWarps = 4;
@@ -157,7 +164,7 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT, LARGE>::kThreads, Attn4Shape
     int* s_pos = reinterpret_cast<int*>(s_c2 + S::kRows);           // its position (dead: -1)
     int* s_out = s_pos + S::kRows;                                  // verify index << 16 | head (dead: -1)
     uint32_t* s_nan = reinterpret_cast<uint32_t*>(s_out + S::kRows);  // its blocks that a NaN reached
-    float* s_ref = reinterpret_cast<float*>(s_nan + S::kRows);      // [2] its reference (log2), in turn
+    float* s_ref = reinterpret_cast<float*>(s_nan + S::kRows);      // [2] its attn4_ref, in turn
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == S::kWarps * 32) {
@@ -429,8 +436,7 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT, LARGE>::kThreads, Attn4Shape
             auto weights = [&](int n, const float* c2, const float* ref) {
                 uint8_t* dst = smem + S::kOffP + (u & 1) * S::kP + (key0 + u8) * 16 + t4 * 4 + n * (TK * 16);
                 sum[n][0] = sum[n][1] = 0.f;
-                const float r[2] = {kTail4 - (ref[0] == -INFINITY ? 0.f : ref[0]),
-                                    kTail4 - (ref[1] == -INFINITY ? 0.f : ref[1])};
+                const float r[2] = {ref[0] == -INFINITY ? 0.f : -ref[0], ref[1] == -INFINITY ? 0.f : -ref[1]};
 #pragma unroll
                 for (int m = 0; m < KM; ++m) {
                     float w[4];
@@ -580,8 +586,8 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT, LARGE>::kThreads, Attn4Shape
                         float c2[2], ref[2];
                         row2(s_c2, n, c2);
                         row2(s_ref + turn * S::kRows, n, ref);
-                        grew |= largest(n, 0) * c2[0] > ref[0] + kLazy4 ||
-                                largest(n, 1) * c2[1] > ref[1] + kLazy4;
+                        grew |= __fmul_ru(largest(n, 0), c2[0]) > __fadd_rd(ref[0], kTail4 + kLazy4) ||
+                                __fmul_ru(largest(n, 1), c2[1]) > __fadd_rd(ref[1], kTail4 + kLazy4);
                         weights(n, c2, ref);
                     }
                     if (!kValuesFirst) values(u - 1, vlast);
@@ -600,7 +606,7 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT, LARGE>::kThreads, Attn4Shape
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1)
                             mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], x));
-                        mx[k] *= c2[k];
+                        mx[k] = attn4_ref(mx[k], c2[k]);
                     }
                     if (lane < 4)
                         *reinterpret_cast<float2*>(s_m + wk * S::kRows + n * 8 + t4 * 2) =
@@ -676,8 +682,7 @@ __global__ void __launch_bounds__(Attn4Shape<D, NT, LARGE>::kThreads, Attn4Shape
             float L = 0.f;
 #pragma unroll
             for (int w = 0; w < S::kWarps; ++w) L += s_l[w * S::kRows + r];
-            const float ref = s_ref[turn * S::kRows + r];
-            const float M = ref == -INFINITY ? -INFINITY : ref - kTail4;
+            const float M = s_ref[turn * S::kRows + r];
             s_m[r] = L == 0.f ? 0.f : vs / L;
             if (slot >= 0) {
                 po[S::kRows * D + r] = M;

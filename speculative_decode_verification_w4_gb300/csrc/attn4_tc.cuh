@@ -295,7 +295,7 @@ __device__ __forceinline__ bool attn4_tc_finish(const AttnParams& p, const Kv4Bl
     if (!warp_wait(&b_pv[u & 1], u >> 1)) return false;
     tc_fence_after();
     const int h = td.g / p.row_blocks;
-    const float M = m == -INFINITY ? -INFINITY : m * c2 - kTail4;
+    const float M = attn4_ref(m, c2);
     const float f = l == 0.f ? 0.f : vs / l;
     uint32_t nan = 0;  // blocks of 16 dimensions that a NaN reached
     if (s_odd[td.seg & 7] == td.seg + 1 && live) {
@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(Attn4TcShape<D, ROWS>::kThreads, 1)
                 } else if (live && (mx - m) * c2 > kLazy4) {  // (the other rows hold anything)
                     // (m = -infinity: O and l are zeros still)
                     if (m != -INFINITY) {
-                        corr = ex2((m - mx) * c2);
+                        corr = ex2(attn4_ref(m, c2) - attn4_ref(mx, c2));
                         grow = true;
                     }
                     l *= corr;
@@ -737,7 +737,7 @@ __global__ void __launch_bounds__(Attn4TcShape<D, ROWS>::kThreads, 1)
                         tmem_st16(tO + c, y);
                     }
                 }
-                const float mc = m == -INFINITY ? 0.f : m * c2 - kTail4;
+                const float mc = m == -INFINITY ? 0.f : attn4_ref(m, c2);
                 float s0 = 0.f, s1 = 0.f;
 #pragma unroll 1
                 for (int c = c0; c < c1; c += CW) {
