@@ -5,7 +5,7 @@
 // in the sequences' order make the outcome independent of the schedule); the returned pages
 // onto the free list; the taken pages into the table and the rows' slots.  The second needs
 // little of the first and runs beside it, in blocks that sum up the returned pages by
-// themselves (as a launch of its own it took a call on 4096 sequences from 18 to 27 us); the
+// themselves (as a launch of its own 28 us instead of 22 for 4096 sequences); the
 // third looks its sequence up in the prefix sums, so that one long prompt is spread over the
 // whole grid.
 //
@@ -14,7 +14,9 @@
 // sequences instead of fourteen), and takes few entries.  Small calls (table and slots of
 // at most kOneBlock* entries) are one block's work and one launch: 16 sequences of 8 rows 6.3 us
 // instead of 7.1; one prompt of 2000 rows among them is 8.5 so, 7.0 in two, 256 sequences of 8
-// with new ones 20.1 and 15.1.
+// with new ones 20.1 and 15.1.  A call without slots goes by its table alone: 2048 sequences of 32
+// columns are 12.9 us in one block and 14.4 in two launches where no page moves, 21.4 and 13.7
+// where an eighth of them ends and an eighth is new; which of them it is only the device knows.
 #include "vw4_internal.cuh"
 
 namespace vw4 {

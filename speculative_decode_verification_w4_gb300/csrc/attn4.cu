@@ -11,7 +11,7 @@ namespace vw4 {
 // 24 / 32 / 64 rows 37 / 44 / 87 against 53 / 54 / 57).
 constexpr int kAttn4TcFrom = 33;
 
-constexpr int kAttn4Sms = 152;
+constexpr int kAttn4Sms = 152;  // (of this GPU)
 constexpr int kAttn4MaxGrid = kAttnMaxGrid64;  // (three blocks an SM at most)
 static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 

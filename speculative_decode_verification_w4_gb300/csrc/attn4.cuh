@@ -17,11 +17,12 @@
 // however many query rows there are, and S of the next tile runs in the same phase: one
 // barrier a tile.
 //
-// What bounds it: with few rows the conversions (a cvt for two codes, a multiply by the scale:
-// the ALU is 54 % busy, the issue slots 60 %) and the chain of a tile, from 16 rows on the
-// products too.  32 sequences of up to 32768 tokens, 8 key heads of size 128, four rows each:
-// 105 us of 424 MB, 62.5 at the copy rate; 24 rows of size 256 over 64 windows of 1024: 54 us.
-// Without conversions and products the loads alone take 78 and 39.
+// What bounds it: the chain of a tile, which eight computing warps an SM hide in part: with few
+// rows no unit is a limit (the ALU, whose work is mostly conversions, a cvt for two codes and a
+// multiply by the scale, is 50 % busy, the issue slots 53 %, HBM 53 %); from 16 rows on the
+// products are in the chain too.  32 sequences of up to 32768 tokens, 8 key heads of size 128,
+// four rows each: 104 us of 424 MB, 62.5 at the copy rate; 24 rows of size 256 over 64 windows of
+// 1024: 53 us.  Without conversions and products the loads alone take 78 and 39.
 //
 // The reference that the weights use is the running maximum, followed lazily: only where a
 // score exceeds it by 2^6 do the warps meet for the true maximum, rescale and form P again
@@ -45,7 +46,10 @@ constexpr float kLazy4 = 6.f;     // (log2) of the reference
 // larger heads are faster so over long sequences (128: 126 instead of 138) and slower over short
 // ones and windows (30 us instead of 38 there), for want of room for the rings.  One n-tile keeps
 // the small tiles too, for tables that do not hold a large one for every SM (one sequence of 517
-// tokens, 4 key heads of size 256: 9.7 us instead of 10.2).
+// tokens, 4 key heads of size 256, one row of six heads: 9.5 us instead of 10.2).  The lengths are
+// the device's: the rule, and the grid, go by the table, and a wide one costs a short sequence
+// what the grid costs: 517 tokens under tables of 4608 (small tiles), 5000 (large) and 131072
+// tokens 10.4, 10.5 and 11.6 us, with 8 heads of size 128 10.5, 11.4 and 12.0 (9.6 under their own).
 __host__ __device__ constexpr int attn4_tk(int D, bool large) {
     return (D == 256 ? 64 : 128) * (large ? 2 : 1);
 }

@@ -23,11 +23,11 @@
 // the least has that many entries above it, which lie in that many threads.  Chunks that
 // overfill the list (rows in ascending order) are read again that way.
 //
-// The bytes bound it (4 or 2 a logit) and, at 16 instructions a logit, the issue slots: 256 x 9
-// rows of 151936, of which 60 % are read, with five alternatives, take 156 us in fp32 (124 at the
-// copy rate; without alternatives 146) and 137 in bf16.  A row is split over blocks where the rows
-// alone would leave SMs idle (one sequence's 8 rows of 262144 with 20 alternatives: 14 us, of
-// which the join of 64 parts a row is 3), and a second kernel joins the parts in order.
+// The bytes bound it (4 or 2 a logit) and, at 17 instructions a logit, the issue slots (71 % busy):
+// 256 x 9 rows of 151936, of which 60 % are read, with five alternatives, take 157 us in fp32
+// (124 at the copy rate; without alternatives 147) and 139 in bf16 (62; 113).  A row is split
+// over blocks where the rows alone would leave SMs idle (one sequence's 8 rows of 262144: 9.2 us,
+// 14.4 with 20 alternatives), and a second kernel joins the parts in order.
 #include <cuda_bf16.h>
 #include <algorithm>
 
@@ -43,7 +43,7 @@ constexpr int kCand = kMaxTop * kLpEach;             // candidates of the list
 constexpr int kCandFull = 8;                         // so many are worth choosing from
 constexpr int kLpGroup = 16;                         // chunks between the block's meetings, at most
 constexpr int kLpMaxSplit = 64;
-constexpr long long kLpFill = 608;                   // blocks that fill the GPU
+constexpr long long kLpFill = 608;                   // blocks that fill the GPU (four on each of 152 SMs)
 constexpr uint32_t kLpBadId = 0x10u;
 constexpr float kLpLazy = 8.f;                       // log2 of an entry over its thread's reference
 constexpr float kLpFar = 1024.f;                     // 2^-1024 is 0 in fp32
@@ -176,8 +176,10 @@ __global__ void __launch_bounds__(kLpThreads, 4)
     const float c2 = p.scale * kLog2e;
 
     // The next chunk is on its way while this one is worked on.  (Without that, five blocks an SM
-    // cover each other's loads: 79 us instead of 93 for 80 x 9 rows of 151936, but 153 or 166 from
-    // run to run for 256 x 9 instead of 156, and 143 instead of 137 in bf16.)
+    // cover each other's loads, in fp32 for better and worse, by how many rows are read, which the
+    // host does not know: 80 x 9 rows of 151936 80 us instead of 93 where all are, 76 instead of
+    // 60 where 60 % are; 256 x 9, 60 %, 154 or, on some runs, 166 instead of 157, without
+    // alternatives 136 instead of 147.  bf16 143 instead of 137.)
     uint4 next[N];
     const int end = shift + p.V;
     auto fetch = [&](int c) {

@@ -3,7 +3,9 @@
 // value = e2m1(nibble) * e4m3(block scale) * head scale: the product of the first two is
 // exact, that with the head's scale rounds to fp32, and to bf16 once more.
 //
-// One pass: 9/16 of a byte in and 2 bytes out a value, so the writes bound it.  A block
+// One pass: 9/16 of a byte in and 2 bytes out a value, so the writes bound it: 8192 tokens of 16
+// sequences, 8 heads of size 128, 108 us in bf16 (96 at the copy rate) and 282 in fp32 (174; a
+// thread's 32 bytes are two stores there).  A block
 // takes kReadTokens tokens of a sequence at a time, whose places in the cache it looks up at
 // once; a thread takes 8 values (4 bytes of codes, a scale) of the same place of several
 // tokens, neighbouring threads neighbouring pieces, so that a warp writes 512 bytes in a

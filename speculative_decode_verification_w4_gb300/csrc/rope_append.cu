@@ -494,7 +494,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
 // Queries and the others in blocks of their own: the registers that rounding to 4 bits takes
 // would be spilled in the queries' loop (2304 tokens of 32 heads of 256, with the rows read
 // back: 54 us together, 40 apart).  Keys and values first: a head that is done again has the
-// queries to hide behind (47 us last).
+// queries to hide behind (47 us last).  Alone the kernel takes 31 us of fp32 rows (15.7 at the copy
+// rate) and 32 of bf16 (10.1), 28 and 29 without a rotation: both blocks of a token compute its
+// angles.  No unit is above 59 % (issue slots); its warps wait for rows and for shared memory.
 template <int D, bool XBF16>
 __global__ void __launch_bounds__(kAppendWarps * 32, 7) append_kv4_kernel(const AppendParams p,
                                                                           int heads_per_block) {
