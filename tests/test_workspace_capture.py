@@ -60,3 +60,29 @@ def test_graphs_outlive_larger_calls(D, R, G):
         status()
         for a, b in zip(outs, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_captured_on_another_stream_than_the_current():
+    """A call whose stream is captured while another one is current, and the other way round."""
+    c, _, _ = make_cache4(3, [300], 16, 1, 128)
+    q = torch.randn(1, 2, 4, 128, device="cuda").to(torch.bfloat16)
+    n = torch.tensor([300], dtype=torch.int32, device="cuda")
+    want = vw4.verify_attn(q, c, n)
+    side, current = torch.cuda.Stream(), torch.cuda.current_stream()
+    torch.cuda.synchronize()
+    assert not vw4._capturing(q.device, None) and not vw4._capturing(q.device, side)
+    kept, graph = dict(vw4._default_ws), torch.cuda.CUDAGraph()
+    out = torch.empty_like(want)
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        assert vw4._capturing(q.device, None) and vw4._capturing(q.device, main)
+        assert not vw4._capturing(q.device, side)
+        side.wait_stream(main)
+        assert vw4._capturing(q.device, side) and torch.cuda.current_stream() == main
+        vw4.verify_attn(q, c, n, out=out, stream=side)
+        main.wait_stream(side)
+    assert vw4._default_ws == kept and torch.cuda.current_stream() == current
+    graph.replay()
+    status()
+    assert torch.equal(out, want)
